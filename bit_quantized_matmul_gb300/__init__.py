@@ -7,7 +7,9 @@ is missing, importing this package raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 
 import torch  # device memory and streams; loads the CUDA runtime first
@@ -38,6 +40,9 @@ Q4MM_PATH_SIMT = 1
 Q4MM_PATH_TC = 2
 Q4MM_PATH_ROW_BY_ROW = 3
 Q4MM_PATH_MMA = 4
+Q4_DTYPE_F32 = 0
+Q4_DTYPE_F16 = 1
+Q4_DTYPE_BF16 = 2
 
 BLOCK = 32
 BLOCK_BYTES = 18
@@ -51,6 +56,8 @@ EXPORTS = (
     "q4mm_get_group_m_threshold", "q4_device_status", "q4mm_set_wait_limit_ns", "q4mm_set_stall_for_test",
     "q4_status_string", "q4_scratch_bytes",
     "q4_kv_append",
+    "q4_kvq_cache_bytes", "q4_kvq_append", "q4_kvq_read", "q4_kvq_attention", "q4_kvq_evict",
+    "q4_prompt_attention",
 )
 
 if not os.path.exists(LIB_PATH):
@@ -61,6 +68,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 _p = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _u32 = ctypes.c_uint32
+_int = ctypes.c_int
 _sig = {
     "q4_quantize": [_p, _i64, _i64, ctypes.POINTER(_p), _p],
     "q4_import_blocks": [_p, _i64, _i64, ctypes.POINTER(_p), _p],
@@ -79,6 +87,13 @@ _sig = {
     "q4_verify_greedy": [_p, _p, _i64, _p, _i64, _p, _p],
     "q4_kv_append": [_p, _p, _p, _p, _i64, _i64, _i64, _i64, _i64, ctypes.c_int, ctypes.POINTER(_i64),
                      ctypes.POINTER(_i64), _p, _p, _p, _i64, _i64, _p],
+    "q4_kvq_cache_bytes": [_i64] * 4 + [ctypes.POINTER(ctypes.c_size_t)],
+    "q4_kvq_append": [_p, _p, _p, _int] + [_i64] * 4 + [_p] * 5 + [_i64, _i64, _p],
+    "q4_kvq_read": [_p, _p, _p, _int] + [_i64] * 4 + [_p] * 3 + [_i64, _i64, _p],
+    "q4_kvq_attention": [_p, _p, _p, _p, _int] + [_i64] * 5 + [_p, ctypes.c_float] + [_p] * 3 + [_i64, _i64, _p],
+    "q4_kvq_evict": [_p, _p] + [_i64] * 4 + [_p] * 3 + [_i64] * 3 + [_p] * 3,
+    "q4_prompt_attention": [_p] * 4 + [_int] + [_i64] * 3 + [_p] * 3 + [ctypes.c_float, _int, _p, _p] + [_i64] * 3 +
+                           [_p],
     "q4mm_select_path": [_p, _i64, _u32],
     "q4mm_plan_info": [_p, _i64, _u32, ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int),
                        ctypes.POINTER(ctypes.c_int)],
@@ -373,6 +388,210 @@ def q4_kv_append(k_cache: torch.Tensor, v_cache: torch.Tensor, k_new: torch.Tens
                                  L, slots, H, D, cap, k_cache.element_size(), ks, vs, offsets.data_ptr(),
                                  slot.data_ptr(), pos.data_ptr(), S, k_new.shape[1], _stream(stream)),
                "q4_kv_append")
+
+
+_DTYPES = {torch.float32: Q4_DTYPE_F32, torch.float16: Q4_DTYPE_F16, torch.bfloat16: Q4_DTYPE_BF16}
+_I64x2 = _i64 * 2
+_HERE_CTX = contextlib.nullcontext()
+
+
+def _on(device: torch.device):
+    """Context in which `device` is current (nothing to do when it already is)."""
+    return _HERE_CTX if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _dtype_code(dtype, name: str) -> int:
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise ValueError("%s must be float32, float16 or bfloat16" % name)
+    return code
+
+
+def _rows3(t: torch.Tensor, name: str, heads: int, head_dim: int, dtype, device) -> torch.Tensor:
+    """A [rows, heads, head_dim] view with contiguous head_dim (any other strides)."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim or (t.stride(2) != 1 and t.numel()):
+        raise ValueError("%s must be a [rows, %d, %d] view with contiguous rows" % (name, heads, head_dim))
+    if t.dtype != dtype or t.device != device:
+        raise ValueError("%s must be %s on %s" % (name, dtype, device))
+    return t
+
+
+def _ints(device, **tensors):
+    for name, t in tensors.items():
+        if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
+            raise ValueError("%s must be a contiguous int32 tensor on the cache's device" % name)
+
+
+def _out3(t, shape, dtype, device, name: str) -> torch.Tensor:
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s" % (name, dtype, shape, device))
+    return t
+
+
+class Q4KVCache:
+    """A 4-bit KV cache of one decoder layer: slots x heads x capacity positions of head_dim values.
+
+    Owns the device buffer (``data``) that the ``q4_kvq_*`` calls work on; its layout is the library's.
+    """
+
+    def __init__(self, slots: int, heads: int, head_dim: int, capacity: int, device=None):
+        self.slots, self.heads, self.head_dim, self.capacity = int(slots), int(heads), int(head_dim), int(capacity)
+        n = ctypes.c_size_t(0)
+        _check(_lib.q4_kvq_cache_bytes(self.slots, self.heads, self.head_dim, self.capacity, ctypes.byref(n)),
+               "q4_kvq_cache_bytes")
+        device = torch.device("cuda" if device is None else device)
+        self.data = torch.zeros(n.value, dtype=torch.uint8, device=device)
+        self.device = self.data.device
+        self._dims = (self.slots, self.heads, self.head_dim, self.capacity)
+
+    @property
+    def nbytes(self) -> int:
+        return self.data.numel()
+
+    def new_mass(self) -> torch.Tensor:
+        """Zeroed attention weights, fp32 [slots, heads, capacity]."""
+        return torch.zeros((self.slots, self.heads, self.capacity), dtype=torch.float32, device=self.device)
+
+
+def _step(cache: Q4KVCache, offsets, slot, pos) -> int:
+    _ints(cache.device, offsets=offsets, slot=slot, pos=pos)
+    S = slot.numel()
+    if offsets.numel() != S + 1 or pos.numel() != S:
+        raise ValueError("offsets must have S + 1 entries and pos S")
+    return S
+
+
+def _mass(cache: Q4KVCache, mass: torch.Tensor):
+    if tuple(mass.shape) != (cache.slots, cache.heads, cache.capacity) or mass.dtype != torch.float32 or \
+            mass.device != cache.device or not mass.is_contiguous():
+        raise ValueError("mass must be a contiguous float32 [slots, heads, capacity] tensor on the cache's device")
+
+
+def q4_kvq_append(cache: Q4KVCache, k_new: torch.Tensor, v_new: torch.Tensor, offsets: torch.Tensor,
+                  slot: torch.Tensor, pos: torch.Tensor, stream=None):
+    """Quantize the step's new K/V rows ([total, heads, head_dim] views) into the cache.
+
+    offsets int32 [S + 1], slot and pos int32 [S]: row offsets[s] + j of the packed
+    step becomes position pos[s] + j of slot[s].
+    """
+    S = _step(cache, offsets, slot, pos)
+    code = _dtype_code(k_new.dtype, "k_new")
+    _rows3(k_new, "k_new", cache.heads, cache.head_dim, k_new.dtype, cache.device)
+    _rows3(v_new, "v_new", cache.heads, cache.head_dim, k_new.dtype, cache.device)
+    total = k_new.shape[0]
+    if v_new.shape[0] != total:
+        raise ValueError("k_new and v_new differ in rows")
+    with _on(cache.device):
+        _check(_lib.q4_kvq_append(cache.data.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), code, *cache._dims,
+                                  _I64x2(k_new.stride(0), k_new.stride(1)), _I64x2(v_new.stride(0), v_new.stride(1)),
+                                  offsets.data_ptr(), slot.data_ptr(), pos.data_ptr(), S, total, _stream(stream)),
+               "q4_kvq_append")
+
+
+def q4_kvq_read(cache: Q4KVCache, offsets: torch.Tensor, slot: torch.Tensor, pos: torch.Tensor, total: int,
+                dtype=torch.float32, k: torch.Tensor | None = None, v: torch.Tensor | None = None, stream=None):
+    """(k, v), each [total, heads, head_dim]: the rows that the cache holds for a step's requests."""
+    S = _step(cache, offsets, slot, pos)
+    code = _dtype_code(dtype, "dtype")
+    shape = (int(total), cache.heads, cache.head_dim)
+    k = _out3(k, shape, dtype, cache.device, "k")
+    v = _out3(v, shape, dtype, cache.device, "v")
+    with _on(cache.device):
+        _check(_lib.q4_kvq_read(cache.data.data_ptr(), k.data_ptr(), v.data_ptr(), code, *cache._dims,
+                                offsets.data_ptr(), slot.data_ptr(), pos.data_ptr(), S, total, _stream(stream)),
+               "q4_kvq_read")
+    return k, v
+
+
+def q4_kvq_attention(cache: Q4KVCache, q: torch.Tensor, offsets: torch.Tensor, slot: torch.Tensor,
+                     pos: torch.Tensor, scale: float | None = None, mass: torch.Tensor | None = None,
+                     out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of the step's query rows over the cache, [total, q_heads, head_dim] of q's dtype.
+
+    Row j of request s sees positions 0 .. pos[s] + j of its slot (append the
+    step's rows first).  scale defaults to 1 / sqrt(head_dim).  mass, fp32
+    [slots, heads, capacity], collects the weight that each position got.
+    """
+    S = _step(cache, offsets, slot, pos)
+    code = _dtype_code(q.dtype, "q")
+    if q.dim() != 3 or q.shape[1] == 0 or q.shape[1] % cache.heads:
+        raise ValueError("q must be [total, q_heads, head_dim] with q_heads a multiple of %d" % cache.heads)
+    total, hq = q.shape[0], q.shape[1]
+    _rows3(q, "q", hq, cache.head_dim, q.dtype, cache.device)
+    out = _out3(out, (total, hq, cache.head_dim), q.dtype, cache.device, "out")
+    if mass is not None:
+        _mass(cache, mass)
+    if scale is None:
+        scale = 1.0 / math.sqrt(cache.head_dim)
+    slots, heads, d, cap = cache._dims
+    with _on(cache.device):
+        _check(_lib.q4_kvq_attention(cache.data.data_ptr(), q.data_ptr(), out.data_ptr(),
+                                     None if mass is None else mass.data_ptr(), code, slots, heads, hq, d, cap,
+                                     _I64x2(q.stride(0), q.stride(1)), scale, offsets.data_ptr(), slot.data_ptr(),
+                                     pos.data_ptr(), S, total, _stream(stream)), "q4_kvq_attention")
+    return out
+
+
+def q4_kvq_evict(cache: Q4KVCache, mass: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, length: torch.Tensor,
+                 keep: int, recent: int = 0, stream=None):
+    """Thin out slots by attention weight: (new_length int32 [S], kept int32 [S, heads, keep]).
+
+    Each head of slot src[s] (length[s] positions) keeps its last `recent`
+    positions and the others of largest mass, `keep` in all, moved in order
+    to the front of slot dst[s] (the same slot: in place), mass alike.
+    """
+    _ints(cache.device, src=src, dst=dst, length=length)
+    _mass(cache, mass)
+    S = src.numel()
+    if dst.numel() != S or length.numel() != S:
+        raise ValueError("src, dst and length differ in length")
+    new_length = torch.empty((S,), dtype=torch.int32, device=cache.device)
+    kept = torch.empty((S, cache.heads, max(int(keep), 0)), dtype=torch.int32, device=cache.device)
+    with _on(cache.device):
+        _check(_lib.q4_kvq_evict(cache.data.data_ptr(), mass.data_ptr(), *cache._dims, src.data_ptr(), dst.data_ptr(),
+                                 length.data_ptr(), S, int(keep), int(recent), new_length.data_ptr(), kept.data_ptr(),
+                                 _stream(stream)), "q4_kvq_evict")
+    return new_length, kept
+
+
+def q4_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_offsets: torch.Tensor,
+                        k_offsets: torch.Tensor | None = None, causal: bool = True, scale: float | None = None,
+                        out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention over packed prompts: q [q_total, q_heads, D], k and v [k_total, kv_heads, D] views
+    (float16 or bfloat16), sequence s being rows offsets[s] .. offsets[s + 1].
+
+    Causal rows are the last of their sequence's keys; k_offsets defaults to
+    q_offsets and scale to 1 / sqrt(D).
+    """
+    if q.dim() != 3 or k.dim() != 3 or k.shape[1] == 0 or q.shape[1] == 0 or q.shape[1] % k.shape[1]:
+        raise ValueError("q must be [rows, q_heads, D] with q_heads a multiple of k's heads")
+    if q.dtype not in (torch.float16, torch.bfloat16) or not q.is_cuda:
+        raise ValueError("q must be a float16 or bfloat16 CUDA tensor")
+    if k_offsets is None:
+        k_offsets = q_offsets
+    tq, hq, d = q.shape
+    tk, hk, _ = k.shape
+    _rows3(q, "q", hq, d, q.dtype, q.device)
+    _rows3(k, "k", hk, d, q.dtype, q.device)
+    _rows3(v, "v", hk, d, q.dtype, q.device)
+    if v.shape[0] != tk:
+        raise ValueError("k and v differ in rows")
+    _ints(q.device, q_offsets=q_offsets, k_offsets=k_offsets)
+    S = q_offsets.numel() - 1
+    if k_offsets.numel() != S + 1:
+        raise ValueError("q_offsets and k_offsets differ in length")
+    out = _out3(out, (tq, hq, d), q.dtype, q.device, "out")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    with _on(q.device):
+        _check(_lib.q4_prompt_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _DTYPES[q.dtype], hq,
+                                        hk, d, _I64x2(q.stride(0), q.stride(1)), _I64x2(k.stride(0), k.stride(1)),
+                                        _I64x2(v.stride(0), v.stride(1)), scale, 1 if causal else 0,
+                                        q_offsets.data_ptr(), k_offsets.data_ptr(), S, tq, tk, _stream(stream)),
+               "q4_prompt_attention")
+    return out
 
 
 def q4mm_argmax_ex(W: Q4Weight, x: torch.Tensor, flags: int = 0, want_max: bool = True, stream=None):

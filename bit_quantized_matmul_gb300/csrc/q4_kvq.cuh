@@ -1,0 +1,138 @@
+// q4_kvq.cuh — device layout of the 4-bit KV cache and the small helpers its
+// kernels share (not part of the public ABI).
+//
+// Layout.  A (slot, head) plane is a run of tiles of KVQ_TILE = 16 positions;
+// a tile holds, one after another,
+//   K codes   16 rows of D/2 bytes      K scales  16 rows of D/32 binary16
+//   V codes   16 rows of D/2 bytes      V scales  16 rows of D/32 binary16
+// so a warp fetches one tile with one bulk copy (2,304 bytes at D = 128, 1,152
+// at D = 64), and the K half alone is one copy too.  Codes are the nibbles
+// q = 0..15 of the Q4_0 rule; block b of a row (32 values) is four words,
+// word j holding values 8j .. 8j+7 from the low nibble up.
+//
+// K row: word j of block b sits at byte j*4*NB + 4b (NB = D/32).  In an
+// m16n8k16 product with keys along n, lane 4g + tq feeds key g with the words
+// j = tq, which are then contiguous (16 bytes at D = 128).  Which value sits
+// at which k index does not matter as long as the query fragment agrees.
+// V row: half-word g (values 4g .. 4g+3 of a block) of block b sits at byte
+// (g*NB + b)*2, so lane (g, tq) of the P V product, with values along n and
+// keys along k, reads contiguous bytes too.  With D = 128 the 16-byte vectors
+// of rows with bit 2 set are stored with index ^ 2: the four rows that a
+// half-warp reads together then fall into different shared-memory banks.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "q4mm_internal.h"
+
+namespace q4 {
+
+template <int D>
+struct Kvq {
+  static constexpr int NB = D / 32;                       // blocks (scales) per row
+  static constexpr int ROW = D / 2;                       // code bytes per row
+  static constexpr int SCL = 2 * NB;                      // scale bytes per row
+  static constexpr int KS_OFF = KVQ_TILE * ROW;           // K scales
+  static constexpr int V_OFF = KS_OFF + KVQ_TILE * SCL;   // V codes (= bytes of the K half)
+  static constexpr int VS_OFF = V_OFF + KVQ_TILE * ROW;   // V scales
+  static constexpr int BYTES = VS_OFF + KVQ_TILE * SCL;   // one tile
+};
+
+// Byte offset in a V row of 16-byte vector v, for row r of a tile.
+template <int D>
+__device__ __forceinline__ int kvq_v_vec(int r, int v) {
+  return (D == 128 ? (v ^ ((r & 4) >> 1)) : v) * 16;
+}
+
+// Byte offset in a tile of word j (values 8j .. 8j+7) of block b of K row r.
+template <int D>
+__device__ __forceinline__ int kvq_k_word(int r, int b, int j) {
+  return r * Kvq<D>::ROW + (j * Kvq<D>::NB + b) * 4;
+}
+
+// Byte offset in a tile of half-word g (values 4g .. 4g+3) of block b of V row r.
+template <int D>
+__device__ __forceinline__ int kvq_v_half(int r, int b, int g) {
+  const int o = (g * Kvq<D>::NB + b) * 2;
+  return Kvq<D>::V_OFF + r * Kvq<D>::ROW + kvq_v_vec<D>(r, o >> 4) + (o & 15);
+}
+
+// The request whose packed rows contain row t: the last s with offsets[s] <= t
+// (offsets are expected to be non-decreasing; callers check the result).
+__device__ __forceinline__ int kvq_find_request(const int32_t* __restrict__ offsets, int S, int64_t t) {
+  int lo = 0, hi = S;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if ((int64_t)__ldg(offsets + mid) <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Request s of a step: its packed rows [b, e), slot and first position.
+struct KvqRequest {
+  int64_t b, e, slot, pos;
+  // rows that fit the packed step, the cache and a slot of it
+  __device__ __forceinline__ bool ok(int64_t total, int64_t slots, int64_t capacity) const {
+    return b >= 0 && e >= b && e <= total && slot >= 0 && slot < slots && pos >= 0 && pos + (e - b) <= capacity;
+  }
+};
+
+__device__ __forceinline__ KvqRequest kvq_request(const int32_t* __restrict__ offsets,
+                                                  const int32_t* __restrict__ slot,
+                                                  const int32_t* __restrict__ pos, int s) {
+  return {__ldg(offsets + s), __ldg(offsets + s + 1), __ldg(slot + s), __ldg(pos + s)};
+}
+
+// Eight consecutive elements as fp32 (16-byte aligned).
+__device__ __forceinline__ void kvq_load8(const float* p, float (&v)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void kvq_load8(const __half* p, float (&v)[8]) {
+  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void kvq_load8(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+// Eight consecutive elements from fp32, rounded once (16-byte aligned).
+__device__ __forceinline__ void kvq_store8(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void kvq_store8(__half* p, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void kvq_store8(__nv_bfloat16* p, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+}  // namespace q4

@@ -1,0 +1,836 @@
+// q4_kvq_attention.cu — attention of a step's query rows over the 4-bit cache.
+//
+//   o[r] = sum_p w[r,p] v[p],  w[r,p] = exp(s[r,p]) / sum_p' exp(s[r,p']),
+//   s[r,p] = scale * q[r] . k[p],  p = 0 .. pos + j for row j of a request,
+//
+// for every (row, query head) r; the G query heads of a key/value head share
+// its cache rows.  One pass over the cache with a running maximum and sum per
+// row; the cache is read once per eight virtual rows (row j, head h of the
+// group: j*G + h), which is once for a decode row of up to eight heads a group.
+//
+// Accuracy.  Codes are exact in binary16 and the other operand is a pair
+// hi + lo / 2048 of binary16 terms (22 bits), so products carry fp32 accuracy
+// for fp32 queries.  An m16n8k16 product has 16 rows: rows 0-7 take the hi and
+// rows 8-15 the lo terms of eight virtual rows, so the pair costs no extra
+// instruction and both halves of a sum meet in one thread.
+//
+// Codes as matrix operands.  A nibble masked in place is the binary16 number
+// q * 2^-24 (low nibble of a byte) or 16 q * 2^-24 (high nibble), a subnormal
+// that the tensor core takes as it is: five integer instructions give four
+// operand registers.  The factor 16 is taken out of the query fragment, or
+// out of the accumulator for V; the offset -8 enters as the initial
+// accumulator -8 sum(q) of each block for K, and for V as 8 sum(w d) at the
+// end.  Scales: K's multiply each block's partial score, V's are folded into
+// the weights of that block.
+//
+// Work.  A unit is one cache tile (16 positions) of one item (request, head,
+// eight virtual rows).  The launch's CTAs take equal, contiguous ranges of
+// units whatever the lengths are (each CTA sums the lengths itself, so the
+// host needs none of them); the four warps of a CTA take the tiles of a range
+// in turn, each through its own ring of bulk copies, and merge their sums when
+// an item's range ends.  Items cut between CTAs leave (maximum, sum, o) in
+// scratch and a second launch joins them.
+#include <atomic>
+
+#include "q4_kvq.cuh"
+#include "q4_ptx.cuh"
+
+namespace q4 {
+namespace {
+
+constexpr int WARPS = 4;
+constexpr int THREADS = 32 * WARPS;
+constexpr int ROWS = 8;               // virtual rows of an item
+constexpr int CTAS_PER_SM = 3;
+constexpr int STAGES = 6;             // tiles in flight per warp
+constexpr int MIN_UNITS = WARPS;      // units a CTA takes at least: one tile per warp
+constexpr float LO_SCALE = 2048.0f;   // 2^11: the lo term's factor
+constexpr float NEG_INF = -INFINITY;
+
+template <typename T>
+struct Args {
+  const uint8_t* cache;
+  const T* q;
+  int64_t q_token, q_head;  // strides in elements
+  T* out;                   // [total, q_heads, D]
+  float scale_log2;         // scale * log2(e)
+  int64_t slots, capacity, plane_bytes, total;
+  int heads, group, S;
+  const int32_t *offsets, *slot, *pos;
+  unsigned* status;
+  unsigned long long wait_ns;
+  float* partial;           // [2 * CTAs][ROWS][D]
+  float2* partial_ml;       // [2 * CTAs][ROWS] (maximum, sum)
+  int64_t* unit_start;      // [S + 1]
+  int workers;              // CTAs of the main launch
+  float* lse;               // [total, q_heads] log2 of the sum of exponentials, or null
+  float* mass;              // [slots, heads, capacity], or null
+};
+
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// hi and lo terms of two values: x = hi + lo / 2048
+__device__ __forceinline__ void split(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x0, x1);
+  const float2 f = __half22float2(h);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = pack((x0 - f.x) * LO_SCALE, (x1 - f.y) * LO_SCALE);
+}
+
+// The operand registers of a word of codes: nibbles (0, 4), 16 * (1, 5),
+// (2, 6) and 16 * (3, 7) as binary16 pairs scaled by 2^-24.
+__device__ __forceinline__ void unpack(uint32_t w, uint32_t (&r)[4]) {
+  r[0] = w & 0x000F000Fu;
+  r[1] = w & 0x00F000F0u;
+  r[2] = (w >> 8) & 0x000F000Fu;
+  r[3] = (w >> 8) & 0x00F000F0u;
+}
+
+// ---------------------------------------------------------------- work ranges
+struct Request {
+  int64_t b, pos, slot;
+  int n, tiles, items;  // rows, cache tiles, items (heads x row groups); 0 tiles: nothing to do
+};
+
+template <typename T>
+__device__ __forceinline__ Request load_request(const Args<T>& a, int s, bool by_rows, bool* bad = nullptr) {
+  const KvqRequest q = kvq_request(a.offsets, a.slot, a.pos, s);
+  Request r{q.b, q.pos, q.slot, 0, 0, 0};
+  if (!q.ok(a.total, a.slots, a.capacity)) {
+    if (bad) *bad = q.e > q.b;
+    return r;
+  }
+  r.n = (int)(q.e - q.b);
+  if (r.n == 0) return r;
+  r.tiles = (int)((q.pos + r.n + KVQ_TILE - 1) / KVQ_TILE);
+  r.items = a.heads * (by_rows ? (r.n * a.group + ROWS - 1) / ROWS : 1);
+  return r;
+}
+
+// The CTA's range of units: sums every request's units, takes an equal share
+// and finds where it starts.  by_rows: an item per eight virtual rows (else
+// one per head).
+struct Range {
+  int64_t left;  // units to do
+  int s, item, tile;
+};
+
+template <typename T>
+__device__ Range plan_range(const Args<T>& a, bool by_rows, int64_t* unit_start) {
+  __shared__ int64_t warp_sum[WARPS];
+  __shared__ Range found;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int chunk = (a.S + THREADS - 1) / THREADS;
+  const int s0 = min(a.S, tid * chunk), s1 = min(a.S, s0 + chunk);
+  int64_t mine = 0;
+  bool any_bad = false;
+  for (int s = s0; s < s1; ++s) {
+    bool bad = false;
+    const Request r = load_request(a, s, by_rows, &bad);
+    any_bad |= bad;
+    mine += (int64_t)r.tiles * r.items;
+  }
+  if (any_bad && blockIdx.x == 0) atomicOr(a.status, STATUS_KV_RANGE);
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  if (tid == 0) found = Range{0, 0, 0, 0};
+  __syncthreads();
+  int64_t base = 0, all = 0;
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < warp) base += warp_sum[w];
+    all += warp_sum[w];
+  }
+  int64_t start = base + incl - mine;
+  const int64_t need = (all + MIN_UNITS - 1) / MIN_UNITS;
+  const int64_t workers = need < gridDim.x ? need : gridDim.x;
+  int64_t u0 = 0, u1 = 0;
+  if ((int64_t)blockIdx.x < workers) {
+    u0 = blockIdx.x * all / workers;
+    u1 = (blockIdx.x + 1) * all / workers;
+  }
+  const bool here = u0 < u1 && u0 >= start && u0 < start + mine;
+  const bool note = unit_start && blockIdx.x == 0;
+  if (here || note) {
+    for (int s = s0; s < s1; ++s) {
+      const Request r = load_request(a, s, by_rows);
+      const int64_t units = (int64_t)r.tiles * r.items;
+      if (here && u0 >= start && u0 < start + units) {
+        const int64_t in = u0 - start;
+        found = Range{u1 - u0, s, (int)(in / r.tiles), (int)(in % r.tiles)};
+      }
+      if (note) unit_start[s] = start;
+      start += units;
+    }
+    if (note && tid == THREADS - 1) unit_start[a.S] = all;
+  }
+  __syncthreads();
+  return found;
+}
+
+// Walks a range segment by segment: a run of tiles of one item.
+template <typename T>
+struct Walk {
+  int64_t left;
+  int s, item, t0, t1;  // the segment: tiles [t0, t1) of the item
+  Request r;
+  __device__ __forceinline__ void begin(const Args<T>& a, const Range& g, bool by_rows) {
+    left = g.left;
+    s = g.s;
+    item = g.item;
+    t0 = t1 = g.tile;
+    if (left > 0) {
+      r = load_request(a, s, by_rows);
+      cut();
+    }
+  }
+  __device__ __forceinline__ void cut() {
+    const int64_t end = t0 + left;
+    t1 = end < r.tiles ? (int)end : r.tiles;
+    left -= t1 - t0;
+  }
+  // the next segment; t0 == t1 when none is left
+  __device__ __forceinline__ void next(const Args<T>& a, bool by_rows) {
+    t0 = 0;
+    t1 = 0;
+    if (left <= 0) return;
+    if (++item >= r.items) {
+      item = 0;
+      do {
+        if (++s >= a.S) {
+          left = 0;
+          return;
+        }
+        r = load_request(a, s, by_rows);
+      } while (r.tiles == 0);
+    }
+    cut();
+  }
+};
+
+// ---------------------------------------------------------------- queries
+// The query fragment of eight virtual rows: A registers per block and k-step,
+// the initial accumulators of each block, and the factor of the scores.
+template <int D>
+struct Query {
+  uint32_t a[Kvq<D>::NB][2][4];
+  float c_hi[Kvq<D>::NB], c_lo[Kvq<D>::NB];
+  float factor;
+};
+
+template <int D, typename T>
+__device__ __forceinline__ void load_query(Query<D>& f, const Args<T>& a, const Request& r, int head, int row0,
+                                           int lane) {
+  constexpr int NB = Kvq<D>::NB;
+  const int g = lane >> 2, tq = lane & 3;
+  const int vr = row0 + g;
+  float x[NB][8];
+  float top = 0.0f;
+  if (vr < r.n * a.group) {
+    const int j = vr / a.group, hg = vr - j * a.group;
+    const T* p = a.q + (r.b + j) * a.q_token + (int64_t)(head * a.group + hg) * a.q_head + 8 * tq;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      kvq_load8(p + 32 * b, x[b]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[b][i] *= a.scale_log2;
+        top = fmaxf(top, fabsf(x[b][i]));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[b][i] = 0.0f;
+  }
+  top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+  top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+  // the row's largest value goes to [2^11, 2^12): binary16 keeps 37 binades
+  // below it, and the partial scores of 24 fewer stay normal in fp32
+  int e = 0;
+  if (top > 0.0f && top < INFINITY) e = ilogbf(top) - 11;
+  f.factor = scalbnf(1.0f, 24 + e);
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    float h = 0.0f, l = 0.0f;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {  // values (2s + k) and (2s + k) + 4; the second pair meets codes of factor 16
+        const float up = k ? 0.0625f : 1.0f;
+        const float x0 = scalbnf(x[b][2 * s + k], -e) * up, x1 = scalbnf(x[b][2 * s + k + 4], -e) * up;
+        uint32_t hi, lo;
+        split(x0, x1, hi, lo);
+        f.a[b][s][2 * k] = hi;
+        f.a[b][s][2 * k + 1] = lo;
+        const float2 fh = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+        const float2 fl = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+        const float back = k ? 16.0f : 1.0f;
+        h += (fh.x + fh.y) * back;
+        l += (fl.x + fl.y) * back;
+      }
+    }
+    h += __shfl_xor_sync(0xFFFFFFFFu, h, 1);
+    l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
+    h += __shfl_xor_sync(0xFFFFFFFFu, h, 2);
+    l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
+    f.c_hi[b] = h * (-8.0f * 0x1p-24f);
+    f.c_lo[b] = l * (-8.0f * 0x1p-24f);
+  }
+}
+
+// Scales of the two cache rows e, e ^ 1 (e < 8, row group t of the tile).
+template <int D>
+__device__ __forceinline__ void load_scales(const uint8_t* scl, int t, int e, float (&d0)[Kvq<D>::NB],
+                                            float (&d1)[Kvq<D>::NB]) {
+  constexpr int NB = Kvq<D>::NB;
+  const uint8_t* p = scl + (8 * t + (e & ~1)) * Kvq<D>::SCL;
+  uint32_t w[NB];
+  if constexpr (D == 128) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    const bool odd = e & 1;
+    w[0] = odd ? v.z : v.x;
+    w[1] = odd ? v.w : v.y;
+    w[2] = odd ? v.x : v.z;
+    w[3] = odd ? v.y : v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    const bool odd = e & 1;
+    w[0] = odd ? v.y : v.x;
+    w[1] = odd ? v.x : v.y;
+  }
+#pragma unroll
+  for (int i = 0; i < NB / 2; ++i) {
+    const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&w[NB / 2 + i]));
+    d0[2 * i] = f0.x;
+    d0[2 * i + 1] = f0.y;
+    d1[2 * i] = f1.x;
+    d1[2 * i + 1] = f1.y;
+  }
+}
+
+// Words of K row r that lane tq of an MMA group reads.
+template <int D>
+__device__ __forceinline__ void load_k(const uint8_t* tile, int r, int tq, uint32_t (&w)[Kvq<D>::NB]) {
+  if constexpr (D == 128) {
+    const uint4 v = *reinterpret_cast<const uint4*>(tile + r * Kvq<D>::ROW + tq * 16);
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(tile + r * Kvq<D>::ROW + tq * 8);
+    w[0] = v.x;
+    w[1] = v.y;
+  }
+}
+
+// Scores (log2 units) of a tile: sc[t][c] for this thread's row and the keys
+// key_of(t, 2 tq + c).  Column n of a product stands for cache row
+// 8t + (n ^ n >> 1): with this order the rows that a group of lanes reads
+// together lie in different shared-memory banks.
+__device__ __forceinline__ int gray(int n) { return n ^ (n >> 1); }
+
+template <int D>
+__device__ __forceinline__ void tile_scores(const uint8_t* tile, const Query<D>& q, int lane, float (&sc)[2][2]) {
+  constexpr int NB = Kvq<D>::NB;
+  const int g = lane >> 2, tq = lane & 3;
+  const int e = gray(2 * tq);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    uint32_t w[NB];
+    load_k<D>(tile, 8 * t + gray(g), tq, w);
+    float d0[NB], d1[NB];
+    load_scales<D>(tile + Kvq<D>::KS_OFF, t, e, d0, d1);
+    float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      float c[4] = {q.c_hi[b], q.c_hi[b], q.c_lo[b], q.c_lo[b]};
+      uint32_t r[4];
+      unpack(w[b], r);
+      mma(c, q.a[b][0], r[0], r[1]);
+      mma(c, q.a[b][1], r[2], r[3]);
+      s0 = fmaf(d0[b], fmaf(c[2], 1.0f / LO_SCALE, c[0]), s0);
+      s1 = fmaf(d1[b], fmaf(c[3], 1.0f / LO_SCALE, c[1]), s1);
+    }
+    sc[t][0] = s0 * q.factor;
+    sc[t][1] = s1 * q.factor;
+  }
+}
+
+// ---------------------------------------------------------------- main kernel
+template <int D>
+struct Smem {
+  static constexpr int RING = WARPS * STAGES * Kvq<D>::BYTES;
+  static constexpr int MERGE = WARPS * ROWS * D * 4;
+  static constexpr int ML = WARPS * ROWS * 8;
+  static constexpr int BYTES = RING + MERGE + ML + WARPS * STAGES * 8;
+};
+
+template <int D, typename T>
+__global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kvq_attention_kernel(const Args<T> a) {
+  using L = Kvq<D>;
+  constexpr int NB = L::NB;
+  extern __shared__ __align__(128) uint8_t smem[];
+  float* merge = reinterpret_cast<float*>(smem + Smem<D>::RING);                      // [WARPS][ROWS][D]
+  float2* merge_ml = reinterpret_cast<float2*>(smem + Smem<D>::RING + Smem<D>::MERGE);  // [WARPS][ROWS]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Smem<D>::RING + Smem<D>::MERGE + Smem<D>::ML);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, tq = lane & 3;
+  uint8_t* ring = smem + warp * STAGES * L::BYTES;
+  const uint32_t ring_u32 = smem_u32(ring), bar_u32 = smem_u32(bars + warp * STAGES);
+  if (lane < STAGES) mbar_init(bar_u32 + 8 * lane, 1);
+  mbar_init_fence();
+  __syncwarp();
+  asm volatile("griddepcontrol.launch_dependents;");
+  const Range range = plan_range(a, true, a.unit_start);
+
+  // the issue cursor runs ahead of the consuming one by up to STAGES tiles
+  Walk<T> in, out;
+  in.begin(a, range, true);
+  out.begin(a, range, true);
+  int in_tile = in.t0 + warp;
+  unsigned issued = 0, taken = 0;
+  auto issue = [&]() {  // the warp's next tile, if any, into the ring
+    while (in.t0 < in.t1 && in_tile >= in.t1) {
+      in.next(a, true);
+      in_tile = in.t0 + warp;
+    }
+    if (in.t0 >= in.t1) return;
+    const int head = in.item / (in.r.items / a.heads);
+    if (lane == 0) {
+      const unsigned st = issued % STAGES;
+      mbar_expect_tx(bar_u32 + 8 * st, L::BYTES);
+      bulk_load(ring_u32 + st * L::BYTES,
+                a.cache + (in.r.slot * a.heads + head) * a.plane_bytes + (int64_t)in_tile * L::BYTES, L::BYTES,
+                bar_u32 + 8 * st);
+    }
+    ++issued;
+    in_tile += WARPS;
+  };
+#pragma unroll 1
+  for (int i = 0; i < STAGES; ++i) issue();
+
+  bool dead = false;  // a wait ran out: nothing more is read
+  while (out.t0 < out.t1) {
+    const Request& r = out.r;
+    const int groups = r.items / a.heads;  // row groups of a head
+    const int head = out.item / groups, row0 = (out.item - head * groups) * ROWS;
+    Query<D> q;
+    load_query<D, T>(q, a, r, head, row0, lane);
+    float o[4 * NB][4];
+    float vb[NB];
+#pragma unroll
+    for (int i = 0; i < 4 * NB; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[i][k] = 0.0f;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) vb[b] = 0.0f;
+    float m = NEG_INF, l = 0.0f;
+    const int64_t last = r.pos + (row0 + g) / a.group;  // the row's last visible position
+    const int64_t clear = r.pos + row0 / a.group;       // positions up to here are visible to every row
+
+    for (int t = out.t0 + warp; t < out.t1; t += WARPS) {
+      const unsigned st = taken % STAGES;
+      if (!dead && !mbar_wait_warp(bar_u32 + 8 * st, (taken / STAGES) & 1, a.wait_ns)) {
+        dead = true;
+        if (lane == 0) atomicOr(a.status, STATUS_TIMEOUT);
+      }
+      if (dead) continue;
+      ++taken;
+      const uint8_t* tile = ring + st * L::BYTES;
+      float sc[2][2];
+      tile_scores<D>(tile, q, lane, sc);
+      const int e = gray(2 * tq);
+      const bool masked = (int64_t)(t + 1) * KVQ_TILE - 1 > clear;
+      bool vis[2][2] = {{true, true}, {true, true}};
+      if (masked) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            vis[u][c] = (int64_t)t * KVQ_TILE + 8 * u + (e ^ c) <= last;
+            sc[u][c] = vis[u][c] ? sc[u][c] : NEG_INF;
+          }
+      }
+      const float top = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
+      if (__any_sync(0xFFFFFFFFu, top > m)) {
+        float mn = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        mn = fmaxf(m, fmaxf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, 2)));
+        const float f = mn == m ? 1.0f : ex2(m - mn);  // 0 on the first tile (m = -inf)
+        m = mn;
+        l *= f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) vb[b] *= f;
+#pragma unroll
+        for (int i = 0; i < 4 * NB; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[i][k] *= f;
+      }
+      const float mm = m == NEG_INF ? 0.0f : m;  // no position visible yet: every weight is 0
+      float p[2][2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          p[u][c] = ex2(sc[u][c] - mm);
+          l += p[u][c];
+        }
+      // weights times V's scale of each block, as hi and lo terms
+      uint32_t pa[NB][4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float d0[NB], d1[NB];
+        load_scales<D>(tile + L::VS_OFF, u, e, d0, d1);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          float x0 = p[u][0] * d0[b], x1 = p[u][1] * d1[b];
+          if (masked) {  // scales of rows past the end may be anything
+            x0 = vis[u][0] ? x0 : 0.0f;
+            x1 = vis[u][1] ? x1 : 0.0f;
+          }
+          vb[b] += x0 + x1;
+          split(x0, x1, pa[b][2 * u], pa[b][2 * u + 1]);
+        }
+      }
+      // V words of the rows of columns 2 tq and 2 tq + 1, both row groups
+      uint32_t vw[2][2][NB / 2];  // [row group][row][word: blocks 2i, 2i + 1]
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int row = 8 * u + (e ^ c);
+          const uint8_t* v = tile + kvq_v_half<D>(row, 0, g);
+          if constexpr (D == 128) {
+            const uint2 x = *reinterpret_cast<const uint2*>(v);
+            vw[u][c][0] = x.x;
+            vw[u][c][1] = x.y;
+          } else {
+            vw[u][c][0] = *reinterpret_cast<const uint32_t*>(v);
+          }
+        }
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        uint32_t r0[4], r1[4];
+        const uint32_t sel = (b & 1) ? 0x7632u : 0x5410u;
+        unpack(__byte_perm(vw[0][0][b / 2], vw[0][1][b / 2], sel), r0);
+        unpack(__byte_perm(vw[1][0][b / 2], vw[1][1][b / 2], sel), r1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mma(o[4 * b + i], pa[b], r0[i], r1[i]);
+      }
+      __syncwarp();  // every lane has read the stage before it is written again
+      issue();
+    }
+
+    // ---- merge the warps' sums of the segment ----
+    l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
+    l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
+    __syncthreads();  // the previous segment's sums have been read
+    if (tq == 0) merge_ml[warp * ROWS + g] = make_float2(m, l);
+    float* mo = merge + (warp * ROWS + g) * D;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      vb[b] += __shfl_xor_sync(0xFFFFFFFFu, vb[b], 1);
+      vb[b] += __shfl_xor_sync(0xFFFFFFFFu, vb[b], 2);
+      float x[2][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float up = (i & 1) ? 0x1p20f : 0x1p24f;  // codes 2^-24, or 16 times that
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          x[c][i] = fmaf(fmaf(o[4 * b + i][2 + c], 1.0f / LO_SCALE, o[4 * b + i][c]), up, -8.0f * vb[b]);
+      }
+      // column 2 tq + c of product i is value 32 b + 4 (2 tq + c) + i
+      *reinterpret_cast<float4*>(mo + 32 * b + 8 * tq) = make_float4(x[0][0], x[0][1], x[0][2], x[0][3]);
+      *reinterpret_cast<float4*>(mo + 32 * b + 8 * tq + 4) = make_float4(x[1][0], x[1][1], x[1][2], x[1][3]);
+    }
+    __syncthreads();
+    const bool whole = out.t0 == 0 && out.t1 == r.tiles;
+    const int slot = 2 * blockIdx.x + (out.t0 == 0 ? 1 : 0);
+    constexpr int PER = ROWS * D / THREADS;  // consecutive values of one row
+    {
+      const int row = tid * PER / D, d = tid * PER % D;
+      float2 ml[WARPS];
+      float top = NEG_INF;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        ml[w] = merge_ml[w * ROWS + row];
+        top = fmaxf(top, ml[w].x);
+      }
+      float sum = 0.0f;
+      float acc[PER] = {};
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        const float f = ml[w].x == NEG_INF ? 0.0f : ex2(ml[w].x - top);  // a NaN sum stays one
+        sum = fmaf(ml[w].y, f, sum);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) acc[i] = fmaf(merge[(w * ROWS + row) * D + d + i], f, acc[i]);
+      }
+      const int vr = row0 + row;
+      if (vr < r.n * a.group) {
+        if (whole) {
+          const int j = vr / a.group, hq = head * a.group + vr - j * a.group;
+          const int64_t at = (r.b + j) * (int64_t)(a.heads * a.group) + hq;
+          const float inv = 1.0f / sum;
+          T* dst = a.out + at * D + d;
+#pragma unroll
+          for (int i = 0; i < PER; ++i) acc[i] *= inv;
+          if constexpr (PER == 8) {
+            kvq_store8(dst, acc);
+          } else {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) dst[i] = (T)acc[i];
+          }
+          if (a.lse && d == 0) a.lse[at] = top + log2f(sum);
+        } else {
+          float* dst = a.partial + ((int64_t)slot * ROWS + row) * D + d;
+#pragma unroll
+          for (int i = 0; i < PER; i += 4)
+            *reinterpret_cast<float4*>(dst + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+          if (d == 0) a.partial_ml[(int64_t)slot * ROWS + row] = make_float2(top, sum);
+        }
+      }
+    }
+    out.next(a, true);
+  }
+  // a warp that gave up waits (again with a limit) for its copies in flight
+  if (dead)
+    for (; taken < issued; ++taken) mbar_wait_warp(bar_u32 + 8 * (taken % STAGES), (taken / STAGES) & 1, a.wait_ns);
+}
+
+// ---------------------------------------------------------------- join
+// One CTA per (packed row, query head): joins the partial sums of an item cut
+// between CTAs; rows of no request, or of one that is out of range, get zeros.
+template <int D, typename T>
+__global__ void __launch_bounds__(THREADS) kvq_join_kernel(const Args<T> a) {
+  constexpr int PER = D / 32;
+  __shared__ float s_sum[WARPS], s_top[WARPS];
+  __shared__ float s_acc[WARPS][D];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t t = blockIdx.x;
+  const int hq = blockIdx.y;
+  const int hq_all = a.heads * a.group;
+  const int64_t at = t * hq_all + hq;
+  const int s = kvq_find_request(a.offsets, a.S, t);
+  const Request r = load_request(a, s, true);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (r.tiles == 0 || t < r.b || t >= r.b + r.n) {
+    for (int d = tid; d < D; d += THREADS) a.out[at * D + d] = (T)0.0f;
+    if (a.lse && tid == 0) a.lse[at] = NEG_INF;
+    return;
+  }
+  const int64_t all = a.unit_start[a.S];
+  const int64_t need = (all + MIN_UNITS - 1) / MIN_UNITS;
+  const int64_t workers = need < a.workers ? need : a.workers;
+  const int head = hq / a.group;
+  const int vr = (int)(t - r.b) * a.group + (hq - head * a.group);
+  const int item = head * (r.items / a.heads) + vr / ROWS, row = vr % ROWS;
+  const int64_t u0 = a.unit_start[s] + (int64_t)item * r.tiles, u1 = u0 + r.tiles - 1;
+  // the CTA whose range holds unit u: the last w with w * all / workers <= u
+  const int wa = (int)(((u0 + 1) * workers - 1) / all), wb = (int)(((u1 + 1) * workers - 1) / all);
+  if (wa == wb) return;  // written by the main launch
+  float top = NEG_INF;
+  for (int w = wa + tid; w <= wb; w += THREADS)
+    top = fmaxf(top, a.partial_ml[(int64_t)(2 * w + (w == wa)) * ROWS + row].x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  if (lane == 0) s_top[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) top = fmaxf(top, s_top[w]);
+  float sum = 0.0f, acc[PER] = {};
+#pragma unroll 4
+  for (int w = wa + warp; w <= wb; w += WARPS) {
+    const int64_t p = (int64_t)(2 * w + (w == wa)) * ROWS + row;
+    const float2 ml = a.partial_ml[p];
+    float v[PER];
+    if constexpr (PER == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(a.partial + p * D + lane * 4);
+      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(a.partial + p * D + lane * 2);
+      v[0] = x.x; v[1] = x.y;
+    }
+    const float f = ml.x == NEG_INF ? 0.0f : ex2(ml.x - top);
+    sum = fmaf(ml.y, f, sum);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) acc[i] = fmaf(v[i], f, acc[i]);
+  }
+  if (lane == 0) s_sum[warp] = sum;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) s_acc[warp][lane * PER + i] = acc[i];
+  __syncthreads();
+  sum = 0.0f;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) sum += s_sum[w];
+  const float inv = 1.0f / sum;
+  if (tid < D) {
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) v += s_acc[w][tid];
+    a.out[at * D + tid] = (T)(v * inv);
+  }
+  if (a.lse && tid == 0) a.lse[at] = top + log2f(sum);
+}
+
+// ---------------------------------------------------------------- weights
+// mass[slot, head, p] += sum over the request's rows and the group's heads of
+// exp2(s - lse); a position that this step appended starts from 0.  Reads the
+// K half of the cache again: keeping the scores instead would write and read
+// as many bytes for a group of seven heads.  Every position belongs to one
+// thread, so the sums have a fixed order.
+template <int D, typename T>
+__global__ void __launch_bounds__(THREADS) kvq_mass_kernel(const Args<T> a) {
+  using L = Kvq<D>;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, tq = lane & 3;
+  const Range range = plan_range(a, false, nullptr);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  Walk<T> it;
+  for (it.begin(a, range, false); it.t0 < it.t1; it.next(a, false)) {
+    const Request& r = it.r;
+    const int head = it.item;
+    const uint8_t* plane = a.cache + (r.slot * a.heads + head) * a.plane_bytes;
+    float* mass = a.mass + (r.slot * a.heads + head) * a.capacity;
+    const int rows = r.n * a.group;
+    for (int row0 = 0; row0 < rows; row0 += ROWS) {
+      Query<D> q;
+      load_query<D, T>(q, a, r, head, row0, lane);
+      const int vr = row0 + g;
+      const bool live = vr < rows;
+      const int j = live ? vr / a.group : 0;
+      const float lse = live ? a.lse[(r.b + j) * (int64_t)(a.heads * a.group) + head * a.group + vr - j * a.group] : 0.0f;
+      const int64_t last = live ? r.pos + j : -1;
+      for (int t = it.t0 + warp; t < it.t1; t += WARPS) {
+        float sc[2][2];
+        tile_scores<D>(plane + (int64_t)t * L::BYTES, q, lane, sc);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int64_t p = (int64_t)t * KVQ_TILE + 8 * u + (gray(2 * tq) ^ c);
+            float w = p <= last ? ex2(sc[u][c] - lse) : 0.0f;
+            w += __shfl_xor_sync(0xFFFFFFFFu, w, 4);
+            w += __shfl_xor_sync(0xFFFFFFFFu, w, 8);
+            w += __shfl_xor_sync(0xFFFFFFFFu, w, 16);
+            if (g == 0 && p < r.pos + r.n) {
+              const float old = (row0 == 0 && p >= r.pos) ? 0.0f : mass[p];
+              mass[p] = old + w;
+            }
+          }
+      }
+    }
+  }
+}
+
+template <int D, typename T>
+int launch_as(const KvqStep& c, const uint8_t* cache, const void* q, const int64_t* qs, int q_heads, float scale,
+              void* out, float* mass, const KvqAttnScratch& ws, cudaStream_t s) {
+  Args<T> a;
+  a.cache = cache;
+  a.q = static_cast<const T*>(q);
+  a.q_token = qs[0];
+  a.q_head = qs[1];
+  a.out = static_cast<T*>(out);
+  a.scale_log2 = scale * 1.44269504088896340736f;
+  a.slots = c.slots;
+  a.capacity = c.capacity;
+  a.plane_bytes = kvq_plane_bytes(D, c.capacity);
+  a.total = c.total;
+  a.heads = (int)c.heads;
+  a.group = q_heads / (int)c.heads;
+  a.S = c.S;
+  a.offsets = c.offsets;
+  a.slot = c.slot;
+  a.pos = c.pos;
+  a.status = c.status;
+  a.wait_ns = wait_limit_ns();
+  a.workers = c.num_sms * CTAS_PER_SM;
+  a.partial = ws.partial;
+  a.partial_ml = ws.partial_ml;
+  a.unit_start = ws.unit_start;
+  a.lse = mass ? ws.lse : nullptr;
+  a.mass = mass;
+  static std::atomic<bool> sized[64];  // per device: the kernel's shared memory limit is set
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return Q4_ERR_CUDA;
+  if (!sized[dev].load()) {
+    if (cudaFuncSetAttribute(kvq_attention_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Smem<D>::BYTES) != cudaSuccess)
+      return Q4_ERR_CUDA;
+    sized[dev].store(true);
+  }
+  kvq_attention_kernel<D, T><<<a.workers, THREADS, Smem<D>::BYTES, s>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return Q4_ERR_CUDA;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)c.total, (unsigned)q_heads);
+  cfg.blockDim = dim3(THREADS);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kvq_join_kernel<D, T>, a) != cudaSuccess) return Q4_ERR_CUDA;
+  if (mass) {
+    cfg.gridDim = dim3(c.num_sms * 4);
+    cfg.numAttrs = 0;
+    if (cudaLaunchKernelEx(&cfg, kvq_mass_kernel<D, T>, a) != cudaSuccess) return Q4_ERR_CUDA;
+  }
+  return Q4_OK;
+}
+
+template <typename T>
+int launch_d(const KvqStep& c, const uint8_t* cache, const void* q, const int64_t* qs, int q_heads, float scale,
+             void* out, float* mass, const KvqAttnScratch& ws, cudaStream_t s) {
+  return c.head_dim == 128 ? launch_as<128, T>(c, cache, q, qs, q_heads, scale, out, mass, ws, s)
+                           : launch_as<64, T>(c, cache, q, qs, q_heads, scale, out, mass, ws, s);
+}
+
+}  // namespace
+
+size_t kvq_attn_scratch_bytes(int64_t S, int64_t total, int q_heads, bool mass, int num_sms, KvqAttnScratch* out,
+                              uint8_t* base) {
+  // sized for D = 128, so one area serves both head sizes
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += (bytes + 255) / 256 * 256;
+    return o;
+  };
+  const size_t segs = (size_t)2 * num_sms * CTAS_PER_SM * ROWS;
+  const size_t p = take(segs * 128 * sizeof(float)), ml = take(segs * sizeof(float2));
+  const size_t us = take((size_t)(S + 1) * sizeof(int64_t)), ls = take(mass ? (size_t)total * q_heads * 4 : 0);
+  if (out) {
+    out->partial = reinterpret_cast<float*>(base + p);
+    out->partial_ml = reinterpret_cast<float2*>(base + ml);
+    out->unit_start = reinterpret_cast<int64_t*>(base + us);
+    out->lse = reinterpret_cast<float*>(base + ls);
+  }
+  return at;
+}
+
+int launch_kvq_attention(const KvqStep& c, const uint8_t* cache, const void* q, const int64_t* qs, int q_heads,
+                         float scale, void* out, float* mass, int dtype, const KvqAttnScratch& ws, cudaStream_t s) {
+  if (dtype == Q4_DTYPE_F32) return launch_d<float>(c, cache, q, qs, q_heads, scale, out, mass, ws, s);
+  if (dtype == Q4_DTYPE_F16) return launch_d<__half>(c, cache, q, qs, q_heads, scale, out, mass, ws, s);
+  return launch_d<__nv_bfloat16>(c, cache, q, qs, q_heads, scale, out, mass, ws, s);
+}
+
+}  // namespace q4

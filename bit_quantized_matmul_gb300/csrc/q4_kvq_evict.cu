@@ -1,0 +1,244 @@
+// q4_kvq_evict.cu — a 4-bit cache thinned out to the positions that collected
+// most attention weight.
+//
+// Of a head's n positions the last `recent` stay, and of the others the
+// keep - recent of largest weight (the lowest position among equals); their
+// order is kept.  Select: a radix select over the weights' order-preserving
+// 32-bit keys (four passes of 8 bits) gives the smallest weight that stays and
+// how many positions of exactly that weight do; one more pass in position
+// order numbers the positions that stay.  Move: row i of the result is row
+// kept[i] >= i, so a copy within one slot runs chunk by chunk, each chunk read
+// whole before it is written; a copy to another slot has no order.
+//
+// Both are short: select reads 4 bytes a position from the caches a few times,
+// move reads and writes the kept rows once.
+#include "q4_kvq.cuh"
+
+namespace q4 {
+namespace {
+
+constexpr int SEL_THREADS = 512;
+constexpr int SEL_WARPS = SEL_THREADS / 32;
+constexpr int MOVE_THREADS = 256;
+constexpr int MOVE_VEC = 4;  // 16-byte vectors per thread and step
+
+// A request whose slots, length and neighbours allow it.
+__device__ bool evict_ok(const KvqEvict& a, int s) {
+  const int64_t src = a.src[s], dst = a.dst[s], n = a.len[s];
+  return src >= 0 && src < a.slots && dst >= 0 && dst < a.slots && n >= 0 && n <= a.capacity;
+}
+
+// No other request of the call writes this one's slots or reads its target.
+__device__ bool evict_apart(const KvqEvict& a, int s) {
+  const int src = a.src[s], dst = a.dst[s];
+  bool clash = false;
+  for (int i = threadIdx.x; i < a.S; i += blockDim.x)
+    if (i != s) clash |= a.dst[i] == dst || a.dst[i] == src || a.src[i] == dst;
+  return !__syncthreads_or(clash);
+}
+
+// Weights in ascending order as unsigned keys; NaN below everything.
+__device__ __forceinline__ uint32_t order_key(float f) {
+  if (isnan(f)) return 0u;
+  f += 0.0f;  // -0 and 0 are equal
+  const uint32_t u = __float_as_uint(f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+__global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const KvqEvict a) {
+  __shared__ unsigned hist[256];
+  __shared__ unsigned warp_sum[2][SEL_WARPS];
+  __shared__ uint32_t s_prefix;
+  __shared__ unsigned s_want;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int s = blockIdx.x / (int)a.heads, h = blockIdx.x % (int)a.heads;
+  const bool ok = evict_ok(a, s);
+  const bool apart = evict_apart(a, s);
+  int32_t* kept = a.kept + (int64_t)blockIdx.x * a.keep;
+  if (!ok || !apart) {
+    if (tid == 0) {
+      atomicOr(a.status, STATUS_KV_RANGE);
+      if (h == 0) a.new_len[s] = -1;
+    }
+    for (int i = tid; i < a.keep; i += SEL_THREADS) kept[i] = -1;
+    return;
+  }
+  const int n = a.len[s];
+  const int out_n = min(n, a.keep);
+  const int first = n - min(n, min(a.recent, a.keep));  // positions below compete
+  const int want = out_n - (n - first);                 // of which so many stay
+  const float* mass = a.mass + ((int64_t)a.src[s] * a.heads + h) * a.capacity;
+  float* mass_out = a.mass + ((int64_t)a.dst[s] * a.heads + h) * a.capacity;
+  if (tid == 0 && h == 0) a.new_len[s] = out_n;
+  for (int i = out_n + tid; i < a.keep; i += SEL_THREADS) kept[i] = -1;
+
+  // the key of rank `want` from the top, 8 bits at a time
+  uint32_t prefix = 0;
+  unsigned left = (unsigned)want;  // of the positions that match the prefix, so many stay
+  if (want > 0 && want < first) {
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      if (tid < 256) hist[tid] = 0;
+      __syncthreads();
+      for (int p = tid; p < first; p += SEL_THREADS) {
+        const uint32_t k = order_key(mass[p]);
+        if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+      }
+      __syncthreads();
+      if (warp == 0) {  // lane i sums the bins 8i .. 8i+7; the first lane from the top that reaches `left` looks closer
+        unsigned mine = 0;
+        for (int b = 0; b < 8; ++b) mine += hist[lane * 8 + b];
+        unsigned above = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned v = __shfl_down_sync(0xFFFFFFFFu, above, o);
+          if (lane + o < 32) above += v;
+        }
+        above -= mine;  // in the bins above this lane's
+        if (above < left && above + mine >= left) {
+          unsigned c = above;
+          for (int b = 7; b >= 0; --b) {
+            const unsigned v = hist[lane * 8 + b];
+            if (c + v >= left) {
+              s_prefix = prefix | (uint32_t)(lane * 8 + b) << shift;
+              s_want = left - c;
+              break;
+            }
+            c += v;
+          }
+        }
+      }
+      __syncthreads();
+      prefix = s_prefix;
+      left = s_want;
+    }
+  }
+  const bool all_stay = want >= first, none_stays = want <= 0;
+
+  // number the positions that stay, in position order
+  int done = 0;           // written so far
+  unsigned ties = 0;      // positions of exactly the smallest weight met so far
+  for (int p0 = 0; p0 < n; p0 += SEL_THREADS) {
+    const int p = p0 + tid;
+    const bool in = p < n;
+    const float w = in ? mass[p] : 0.0f;
+    const uint32_t k = order_key(w);
+    const bool competes = in && p < first;
+    const bool tie = competes && !all_stay && !none_stays && k == prefix;
+    bool stay = in && (p >= first || all_stay || (!none_stays && k > prefix));
+    const unsigned tb = __ballot_sync(0xFFFFFFFFu, tie);
+    if (lane == 0) warp_sum[0][warp] = __popc(tb);
+    __syncthreads();
+    unsigned before = ties, all_ties = 0;
+    for (int i = 0; i < SEL_WARPS; ++i) {
+      if (i < warp) before += warp_sum[0][i];
+      all_ties += warp_sum[0][i];
+    }
+    const unsigned below = (1u << lane) - 1u;
+    if (tie) stay = before + __popc(tb & below) < left;
+    ties += all_ties;
+    const unsigned sb = __ballot_sync(0xFFFFFFFFu, stay);
+    if (lane == 0) warp_sum[1][warp] = __popc(sb);
+    __syncthreads();  // every thread has read its weight, and the weights written below lie at or before them
+    int at = done, all = 0;
+    for (int i = 0; i < SEL_WARPS; ++i) {
+      if (i < warp) at += warp_sum[1][i];
+      all += warp_sum[1][i];
+    }
+    if (stay) {
+      at += __popc(sb & below);
+      kept[at] = p;
+      mass_out[at] = w;
+    }
+    done += all;
+  }
+}
+
+// Vectors of a row: codes of K and V (D/32 each of 16 bytes) and the scales.
+// The V vectors of a row depend on its place in the tile (kvq_v_vec).
+template <int D>
+struct RowCopy {
+  using L = Kvq<D>;
+  static constexpr int CV = D / 32;       // code vectors per K or V row
+  static constexpr int VECS = 2 * CV;     // 16-byte vectors; then two scale words
+  __device__ static const uint8_t* at(const uint8_t* plane, int64_t p, int v) {
+    const int row = (int)(p % KVQ_TILE);
+    const uint8_t* tile = plane + p / KVQ_TILE * L::BYTES;
+    if (v < CV) return tile + row * L::ROW + v * 16;
+    return tile + L::V_OFF + row * L::ROW + kvq_v_vec<D>(row, v - CV);
+  }
+  __device__ static const uint8_t* scale(const uint8_t* plane, int64_t p, int kv) {
+    return plane + p / KVQ_TILE * L::BYTES + (kv ? L::VS_OFF : L::KS_OFF) + (p % KVQ_TILE) * L::SCL;
+  }
+};
+
+// Scales of a row: 8 bytes at D = 128, 4 at D = 64.
+template <int D>
+using ScaleWord = typename std::conditional<D == 128, uint2, uint32_t>::type;
+
+template <int D>
+__global__ void __launch_bounds__(MOVE_THREADS) evict_move_kernel(const KvqEvict a, int64_t plane_bytes) {
+  using R = RowCopy<D>;
+  constexpr int ITEMS = R::VECS + 2;  // per row: vectors, then the K and the V scales
+  const int s = blockIdx.y / (int)a.heads, h = blockIdx.y % (int)a.heads;
+  const int n = a.new_len[s];
+  if (n <= 0) return;
+  const int64_t src_slot = a.src[s], dst_slot = a.dst[s];
+  const bool in_place = src_slot == dst_slot;
+  if (in_place && (blockIdx.x != 0 || n == a.len[s])) return;
+  const uint8_t* src = a.cache + (src_slot * a.heads + h) * plane_bytes;
+  uint8_t* dst = a.cache + (dst_slot * a.heads + h) * plane_bytes;
+  const int32_t* kept = a.kept + (int64_t)blockIdx.y * a.keep;
+  const int items = n * ITEMS;  // below 2^31: checked on the host
+  constexpr int STEP = MOVE_THREADS * MOVE_VEC;
+  const int first = in_place ? 0 : blockIdx.x * STEP, stride = in_place ? STEP : gridDim.x * STEP;
+  for (int i0 = first; i0 < items; i0 += stride) {
+    uint4 v[MOVE_VEC];
+#pragma unroll
+    for (int u = 0; u < MOVE_VEC; ++u) {
+      const int it = i0 + u * MOVE_THREADS + threadIdx.x;
+      if (it < items) {
+        const int row = it / ITEMS, e = it - row * ITEMS;
+        const int64_t p = kept[row];
+        if (e < R::VECS) {
+          v[u] = *reinterpret_cast<const uint4*>(R::at(src, p, e));
+        } else {
+          *reinterpret_cast<ScaleWord<D>*>(&v[u]) =
+              *reinterpret_cast<const ScaleWord<D>*>(R::scale(src, p, e - R::VECS));
+        }
+      }
+    }
+    if (in_place) __syncthreads();  // the step is read before it is written; later steps read from further on
+#pragma unroll
+    for (int u = 0; u < MOVE_VEC; ++u) {
+      const int it = i0 + u * MOVE_THREADS + threadIdx.x;
+      if (it < items) {
+        const int row = it / ITEMS, e = it - row * ITEMS;
+        if (e < R::VECS) {
+          *reinterpret_cast<uint4*>(const_cast<uint8_t*>(R::at(dst, row, e))) = v[u];
+        } else {
+          *reinterpret_cast<ScaleWord<D>*>(const_cast<uint8_t*>(R::scale(dst, row, e - R::VECS))) =
+              *reinterpret_cast<ScaleWord<D>*>(&v[u]);
+        }
+      }
+    }
+  }
+}
+
+}  // namespace
+
+int launch_kvq_evict(const KvqEvict& c, cudaStream_t s) {
+  const int64_t planes = (int64_t)c.S * c.heads;
+  evict_select_kernel<<<(unsigned)planes, SEL_THREADS, 0, s>>>(c);
+  if (cudaGetLastError() != cudaSuccess) return Q4_ERR_CUDA;
+  const int64_t items = (int64_t)c.keep * (2 * (c.head_dim / 32) + 2);
+  const int64_t steps = (items + MOVE_THREADS * MOVE_VEC - 1) / (MOVE_THREADS * MOVE_VEC);
+  int64_t gx = ((int64_t)c.num_sms * 8 + planes - 1) / planes;
+  if (gx > steps) gx = steps;
+  const dim3 grid((unsigned)gx, (unsigned)planes);
+  const int64_t pb = kvq_plane_bytes(c.head_dim, c.capacity);
+  if (c.head_dim == 128) evict_move_kernel<128><<<grid, MOVE_THREADS, 0, s>>>(c, pb);
+  else evict_move_kernel<64><<<grid, MOVE_THREADS, 0, s>>>(c, pb);
+  return cudaGetLastError() == cudaSuccess ? Q4_OK : Q4_ERR_CUDA;
+}
+
+}  // namespace q4

@@ -198,8 +198,19 @@ int run(const q4_weight* Wh, const float* x, float* y, int32_t* idx, float* maxv
 
 // Caller holds g_dev[device].mu.
 int workspace_get(int device, size_t partial_bytes, size_t xop_bytes, Workspace* out, size_t gu_bytes,
-                  size_t xpre_bytes) {
+                  size_t xpre_bytes, size_t attn_bytes) {
   DeviceScratch& ds = g_dev[device];
+  if (attn_bytes > ds.ws.attn_bytes) {
+    size_t want = attn_bytes + attn_bytes / 2;
+    if (ds.ws.attn) cudaFree(ds.ws.attn);
+    ds.ws.attn = nullptr;
+    ds.ws.attn_bytes = 0;
+    if (cudaMalloc(&ds.ws.attn, want) != cudaSuccess) {
+      cudaGetLastError();
+      return Q4_ERR_NOMEM;
+    }
+    ds.ws.attn_bytes = want;
+  }
   if (xpre_bytes > ds.ws.xpre_bytes) {
     size_t want = xpre_bytes + xpre_bytes / 2;
     if (ds.ws.xpre) cudaFree(ds.ws.xpre);
@@ -273,6 +284,21 @@ int workspace_reserve_for(int device, const Weight* W) {
   }
   Workspace ws;
   return workspace_get(device, partial, xop, &ws, 0, mma_xpre_bytes(W->KBP, mma_plan(W, ds.num_sms)));
+}
+
+int scratch_acquire(size_t attn_bytes, ScratchLock* out) {
+  int dev;
+  int st = current_device(&dev);
+  if (st) return st;
+  DeviceScratch& ds = g_dev[dev];
+  out->lock = std::unique_lock<std::mutex>(ds.mu);
+  st = init_device_locked(dev, ds);
+  if (st) return st;
+  st = workspace_get(dev, 0, 0, &out->ws, 0, 0, attn_bytes);
+  if (st) return st;
+  out->num_sms = ds.num_sms;
+  out->sm103 = ds.cc_major == 10 && ds.cc_minor == 3;
+  return Q4_OK;
 }
 
 int device_num_sms(int device) { return g_dev[device].num_sms; }
@@ -759,7 +785,9 @@ int q4_device_status(void) {
   st = noalloc_status_take(dev, &na);
   if (st) return st;
   v |= na;
-  if (v) return (v & STATUS_TIMEOUT) ? Q4_ERR_TIMEOUT : Q4_ERR_INVALID_ARG;
+  if (v & STATUS_TIMEOUT) return Q4_ERR_TIMEOUT;
+  if (v & ~(STATUS_KV_NONFINITE | STATUS_KV_SCALE)) return Q4_ERR_INVALID_ARG;
+  if (v) return (v & STATUS_KV_NONFINITE) ? Q4_ERR_NONFINITE : Q4_ERR_RANGE;
   return Q4_OK;
 }
 

@@ -4,6 +4,8 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <mutex>
+
 #include <cuda_runtime.h>
 
 #include "q4mm.h"
@@ -75,17 +77,21 @@ struct Workspace {
   size_t gu_bytes = 0;
   uint8_t* xpre = nullptr;             // chunk-slot image of the pre-conversion pass
   size_t xpre_bytes = 0;
+  uint8_t* attn = nullptr;             // cache attention: partial sums of items cut between CTAs
+  size_t attn_bytes = 0;
 };
 constexpr int MAX_COUNTERS = 1 << 16;
 
 // Bits of the device status word (read and cleared by q4_device_status).
 constexpr unsigned STATUS_TIMEOUT = 1u;   // a bounded wait ran out
 constexpr unsigned STATUS_BAD_ROW = 2u;   // a row index of q4mm_argmax_rows was out of range
-constexpr unsigned STATUS_KV_RANGE = 4u;  // a q4_kv_append request was out of range (not written)
+constexpr unsigned STATUS_KV_RANGE = 4u;  // a cache or prompt request was out of range (not written)
+constexpr unsigned STATUS_KV_NONFINITE = 8u;  // q4_kvq_append met a NaN or an infinity (stored as NaN)
+constexpr unsigned STATUS_KV_SCALE = 16u;     // a block's scale passed binary16 (stored as NaN)
 
 // Returns Q4_OK and fills *ws with at least the requested capacities.
 int workspace_get(int device, size_t partial_bytes, size_t xop_bytes, Workspace* ws, size_t gu_bytes = 0,
-                  size_t xpre_bytes = 0);
+                  size_t xpre_bytes = 0, size_t attn_bytes = 0);
 
 // ---- launchers (return a Q4 status; launch errors map to Q4_ERR_CUDA) ----
 // Quantize fp32 W (device) into canonical blocks in canon_dev, then repack.
@@ -155,6 +161,70 @@ int launch_kv_append(uint8_t* k_cache, uint8_t* v_cache, const uint8_t* k_new, c
                      const int64_t (&stride)[6], const int32_t* offsets,
                      const int32_t* slot, const int32_t* pos, int S, int64_t total, unsigned* status,
                      int num_sms, cudaStream_t s);
+
+// ---- 4-bit KV cache (layout in q4_kvq.cuh) ----
+constexpr int KVQ_TILE = 16;  // positions per tile
+inline int64_t kvq_tile_bytes(int64_t head_dim) { return KVQ_TILE * (head_dim + head_dim / 8); }
+inline int64_t kvq_plane_bytes(int64_t head_dim, int64_t capacity) {
+  return (capacity + KVQ_TILE - 1) / KVQ_TILE * kvq_tile_bytes(head_dim);
+}
+// One step's packed rows over a cache: what its calls have in common.
+struct KvqStep {
+  int64_t slots, heads, capacity, total;
+  int head_dim, S;
+  const int32_t *offsets, *slot, *pos;
+  unsigned* status;
+  int num_sms;
+};
+int launch_kvq_append(const KvqStep& c, uint8_t* cache, const void* k_new, const void* v_new, const int64_t* ks,
+                      const int64_t* vs, int dtype, cudaStream_t s);
+int launch_kvq_read(const KvqStep& c, const uint8_t* cache, void* k_out, void* v_out, int dtype, cudaStream_t s);
+struct KvqAttnScratch {
+  float* partial;
+  float2* partial_ml;
+  int64_t* unit_start;
+  float* lse;
+};
+// Bytes of the attention scratch of a call; with `out`, its parts at `base`.
+size_t kvq_attn_scratch_bytes(int64_t S, int64_t total, int q_heads, bool mass, int num_sms, KvqAttnScratch* out,
+                              uint8_t* base);
+int launch_kvq_attention(const KvqStep& c, const uint8_t* cache, const void* q, const int64_t* qs, int q_heads,
+                         float scale, void* out, float* mass, int dtype, const KvqAttnScratch& ws, cudaStream_t s);
+struct KvqEvict {
+  uint8_t* cache;
+  float* mass;
+  int64_t slots, heads, capacity;
+  int head_dim, S, keep, recent;
+  const int32_t *src, *dst, *len;
+  int32_t *new_len, *kept;
+  unsigned* status;
+  int num_sms;
+};
+int launch_kvq_evict(const KvqEvict& c, cudaStream_t s);
+
+// ---- prompt attention ----
+struct PromptAttn {
+  const void *q, *k, *v;
+  void* out;
+  int64_t q_strides[2], k_strides[2], v_strides[2];  // row, head; in elements
+  int64_t q_total, k_total;
+  int dtype, q_heads, kv_heads, head_dim, S, causal;
+  float scale;
+  const int32_t *q_offsets, *k_offsets;
+  unsigned* status;
+  int num_sms;
+};
+int launch_prompt_attention(const PromptAttn& c, cudaStream_t s);
+
+// The scratch of the current device, locked: other calls' launches wait until
+// it goes out of scope, so the pointers stay valid while this call launches.
+struct ScratchLock {
+  std::unique_lock<std::mutex> lock;
+  Workspace ws;
+  int num_sms = 0;
+  bool sm103 = false;
+};
+int scratch_acquire(size_t attn_bytes, ScratchLock* out);
 
 // Greedy verification of draft tokens per request (see q4_verify_greedy).
 int launch_verify(const int32_t* idx, const int32_t* draft, int64_t total, const int32_t* offsets,

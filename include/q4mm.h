@@ -322,6 +322,126 @@ Q4_API int q4_kv_append(void* k_cache, void* v_cache, const void* k_new, const v
                         const int64_t* v_strides, const int32_t* offsets, const int32_t* slot,
                         const int32_t* pos, int64_t S, int64_t total, cudaStream_t stream);
 
+/* ---- 4-bit KV cache -------------------------------------------------------
+ *
+ * A cache of K and V rows in the Q4_0 blocks of this library: 4.5 bits a value
+ * where q4_kv_append's cache holds 16 or 32.  The cache is one device buffer
+ * of q4_kvq_cache_bytes bytes, caller-owned, 16-byte aligned, for one decoder
+ * layer: `slots` requests x `heads` key/value heads x `capacity` positions of
+ * head_dim (64 or 128) values.  Its layout is private; it needs no
+ * initialization, and positions that nothing was appended to are never used.
+ *
+ * The calls of a step share its ragged description, as in q4_kv_append:
+ *   offsets   device, int32 [S + 1], non-decreasing: request s owns packed rows
+ *             [offsets[s], offsets[s+1]) of the step's `total` rows.
+ *   slot,pos  device, int32 [S]: request s's slot and the position of its first
+ *             row in the cache; row offsets[s] + j is position pos[s] + j.
+ * Host-checked for all of them: sizes >= 1, total * heads below 2^31, pointers
+ * given (INVALID_ARG); head_dim 64 or 128 (SHAPE); base addresses and
+ * strides multiples of 16 bytes (ALIGN).  On the device a request whose slot
+ * is outside [0, slots), or whose rows pass capacity or total, is left out (its
+ * rows are not written; rows that a call puts out for it are zero) and
+ * q4_device_status then reports Q4_ERR_INVALID_ARG. */
+
+/* Element types of rows that are passed in or out. */
+#define Q4_DTYPE_F32 0
+#define Q4_DTYPE_F16 1
+#define Q4_DTYPE_BF16 2
+
+/* Bytes of a cache buffer. */
+Q4_API int q4_kvq_cache_bytes(int64_t slots, int64_t heads, int64_t head_dim, int64_t capacity,
+                              size_t* bytes);
+
+/* Quantize the step's new K and V rows into the cache (the block rule in the
+ * file header, 32 values of one row a block).
+ *   k_new, v_new  device, dtype: element (t, h, d) at t*strides[0] +
+ *                 h*strides[1] + d (host arrays of 2 strides, in elements).
+ * A block that holds a NaN or an infinity, or whose scale passes binary16, is
+ * stored as NaN; q4_device_status then reports Q4_ERR_NONFINITE or
+ * Q4_ERR_RANGE.  S = 0 or total = 0: a no-op.  Asynchronous on stream. */
+Q4_API int q4_kvq_append(void* cache, const void* k_new, const void* v_new, int dtype, int64_t slots,
+                         int64_t heads, int64_t head_dim, int64_t capacity, const int64_t* k_strides,
+                         const int64_t* v_strides, const int32_t* offsets, const int32_t* slot,
+                         const int32_t* pos, int64_t S, int64_t total, cudaStream_t stream);
+
+/* The rows that the cache holds, as (q - 8) * d rounded once to dtype.
+ *   k_out, v_out  device, dtype [total, heads, head_dim], fully overwritten
+ *                 (rows of no request get zeros). */
+Q4_API int q4_kvq_read(const void* cache, void* k_out, void* v_out, int dtype, int64_t slots,
+                       int64_t heads, int64_t head_dim, int64_t capacity, const int32_t* offsets,
+                       const int32_t* slot, const int32_t* pos, int64_t S, int64_t total,
+                       cudaStream_t stream);
+
+/* Attention of the step's query rows over the cache (its own new rows already
+ * appended): row j of request s sees positions 0 .. pos[s] + j of its slot,
+ *   out[t, hq] = sum_p softmax_p(scale * q[t, hq] . K[p]) V[p]
+ * with key/value head hq / (q_heads / heads); scale is positive.
+ *   q     device, dtype, strides as in append; q_heads a multiple of heads.
+ *   out   device, dtype [total, q_heads, head_dim], fully overwritten; rows of
+ *         no request get zeros.
+ *   mass  device, fp32 [slots, heads, capacity], or NULL: adds to each position
+ *         the attention weight that it got from the request's rows and from
+ *         the query heads of its head (they sum to rows * q_heads / heads per
+ *         request and head).  Positions pos[s] .. of this step start from 0, so
+ *         only a prompt's positions have to be set before.  Each slot in at
+ *         most one request of the call.
+ * Products carry fp32 accuracy for fp32 queries; sums are held in fp32.  The
+ * lengths are read on the device only: a launch of a fixed number of CTAs
+ * divides them evenly, and the result does not depend on anything but the
+ * arguments.  Uses the library's scratch (grown on the first call of a larger
+ * S, or of larger total * q_heads with mass): order calls on one stream. */
+Q4_API int q4_kvq_attention(const void* cache, const void* q, void* out, float* mass, int dtype,
+                            int64_t slots, int64_t heads, int64_t q_heads, int64_t head_dim,
+                            int64_t capacity, const int64_t* q_strides, float scale,
+                            const int32_t* offsets, const int32_t* slot, const int32_t* pos,
+                            int64_t S, int64_t total, cudaStream_t stream);
+
+/* Thin out the cache of S slots by accumulated attention weight: of the len[s]
+ * positions of slot src[s], each head keeps the last `recent` and, of the
+ * others, the keep - recent of largest mass (the lowest position among
+ * equals; NaN counts as the smallest).  The kept rows are written to
+ * positions 0 .. new_len[s] - 1 of slot dst[s] in their old order, and so is
+ * their mass; dst[s] == src[s] works in place.
+ *   src, dst, len   device, int32 [S]; no dst in two requests, none that another
+ *                   request reads.  len <= capacity.
+ *   keep, recent    1 <= keep <= capacity, 0 <= recent <= keep (INVALID_ARG).
+ *   mass            device, fp32 [slots, heads, capacity].
+ *   new_len         device, int32 [S] out: min(len, keep); not an alias of len.
+ *   kept            device, int32 [S, heads, keep] out: the old position of each
+ *                   kept row, then -1.
+ * S * heads at most 65535 (SHAPE).  A request that breaks these rules on the
+ * device is left as it is (new_len and kept -1), and q4_device_status reports
+ * Q4_ERR_INVALID_ARG. */
+Q4_API int q4_kvq_evict(void* cache, float* mass, int64_t slots, int64_t heads, int64_t head_dim,
+                        int64_t capacity, const int32_t* src, const int32_t* dst, const int32_t* len,
+                        int64_t S, int64_t keep, int64_t recent, int32_t* new_len, int32_t* kept,
+                        cudaStream_t stream);
+
+/* Attention over whole prompts, packed one after another, on the tensor cores.
+ *   q, k, v    device, F16 or BF16: element (t, h, d) at t*strides[0] +
+ *              h*strides[1] + d (2 strides each, in elements).  q has q_total
+ *              rows of q_heads, k and v k_total rows of kv_heads; key/value head
+ *              of query head hq: hq / (q_heads / kv_heads).
+ *   out        device, dtype [q_total, q_heads, head_dim], fully overwritten.
+ *   q_offsets, k_offsets  device, int32 [S + 1], non-decreasing: sequence s has
+ *              query rows [q_offsets[s], q_offsets[s+1]) and key rows likewise.
+ *   scale      positive.
+ *   causal     nonzero: row i of a sequence sees its keys j <= i + klen - qlen
+ *              (the rows are the sequence's last); else all of its keys.
+ * Rows that see no key, and rows of no sequence, get zeros.  Weights are
+ * rounded to dtype before the product with v; sums are held in fp32.  What
+ * lies outside a sequence's rows, NaN included, does not reach its results.
+ * head_dim 64 or 128, at most 128 query heads per key/value head (SHAPE);
+ * addresses and strides multiples of 16 bytes (ALIGN).  A sequence whose
+ * offsets are out of range gets zeros and q4_device_status reports
+ * Q4_ERR_INVALID_ARG.  Needs sm_103 (UNSUPPORTED). */
+Q4_API int q4_prompt_attention(const void* q, const void* k, const void* v, void* out, int dtype,
+                               int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                               const int64_t* q_strides, const int64_t* k_strides,
+                               const int64_t* v_strides, float scale, int causal,
+                               const int32_t* q_offsets, const int32_t* k_offsets, int64_t S,
+                               int64_t q_total, int64_t k_total, cudaStream_t stream);
+
 /* The kernel path (Q4MM_PATH_*) a call with these arguments would take, or a
  * negative status. */
 Q4_API int q4mm_select_path(const q4_weight* W, int64_t M, uint32_t flags);
@@ -375,7 +495,8 @@ Q4_API int q4mm_set_stall_for_test(int on);
  * words (the library's scratch and, once q4mm_forward_noalloc has run on the
  * device, its fixed array): Q4_OK; Q4_ERR_TIMEOUT if a bounded wait in a kernel ran out
  * (the library's scratch words are then reset for the calls that follow);
- * Q4_ERR_INVALID_ARG if q4mm_argmax_rows met a row index out of range; or
+ * Q4_ERR_INVALID_ARG if a call met a row index or a request out of range;
+ * Q4_ERR_NONFINITE or Q4_ERR_RANGE if q4_kvq_append stored a block as NaN; or
  * Q4_ERR_CUDA if the device reports an error. */
 Q4_API int q4_device_status(void);
 
