@@ -32,7 +32,7 @@ bool strides_aligned(const int64_t* st, int eb, int64_t rows, int64_t heads) {
 bool scale_ok(float scale) { return scale > 0.0f && std::isfinite(scale * 1.4427f); }
 
 int check_cache(int64_t slots, int64_t heads, int64_t head_dim, int64_t capacity) {
-  if (slots < 1 || heads < 1 || capacity < 1 || slots >= LIM || heads >= LIM || capacity >= LIM - 2 * KVQ_TILE)
+  if (slots < 1 || heads < 1 || capacity < 1 || slots >= LIM || heads >= LIM || capacity >= LIM - 64)
     return Q4_ERR_INVALID_ARG;
   if (head_dim != 64 && head_dim != 128) return Q4_ERR_SHAPE;
   // bytes and plane indexes stay far below 2^63

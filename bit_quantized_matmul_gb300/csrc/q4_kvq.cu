@@ -84,16 +84,15 @@ __global__ void __launch_bounds__(256) kvq_append_kernel(const AppendArgs<T> a) 
       }
     }
     const int64_t p = q.pos + (t - q.b);
-    const int row = (int)(p % KVQ_TILE);
-    uint8_t* tile = a.cache + (q.slot * a.heads + h) * a.plane_bytes + p / KVQ_TILE * L::BYTES;
+    const int row = (int)(p % L::POS);
+    uint8_t* tile = a.cache + (q.slot * a.heads + h) * a.plane_bytes + p / L::POS * L::BYTES;
     if (kv == 0) {
       *reinterpret_cast<uint32_t*>(tile + kvq_k_word<D>(row, b, j)) = codes;
-      if (j == 0) *reinterpret_cast<uint16_t*>(tile + L::KS_OFF + row * L::SCL + 2 * b) = d16;
     } else {
       *reinterpret_cast<uint16_t*>(tile + kvq_v_half<D>(row, b, 2 * j)) = (uint16_t)codes;
       *reinterpret_cast<uint16_t*>(tile + kvq_v_half<D>(row, b, 2 * j + 1)) = (uint16_t)(codes >> 16);
-      if (j == 0) *reinterpret_cast<uint16_t*>(tile + L::VS_OFF + row * L::SCL + 2 * b) = d16;
     }
+    if (j == 0) *reinterpret_cast<uint16_t*>(tile + kvq_scale<D>(kv, row, b)) = d16;
   }
 }
 
@@ -126,8 +125,8 @@ __global__ void __launch_bounds__(256) kvq_read_kernel(const ReadArgs<T> a) {
         if (kv == 0 && w == 0 && h == 0) atomicOr(a.status, STATUS_KV_RANGE);
       } else {
         const int64_t p = q.pos + (t - q.b);
-        const int row = (int)(p % KVQ_TILE);
-        const uint8_t* tile = a.cache + (q.slot * a.heads + h) * a.plane_bytes + p / KVQ_TILE * L::BYTES;
+        const int row = (int)(p % L::POS);
+        const uint8_t* tile = a.cache + (q.slot * a.heads + h) * a.plane_bytes + p / L::POS * L::BYTES;
         uint32_t codes;
         if (kv == 0) {
           codes = *reinterpret_cast<const uint32_t*>(tile + kvq_k_word<D>(row, b, j));
@@ -135,8 +134,8 @@ __global__ void __launch_bounds__(256) kvq_read_kernel(const ReadArgs<T> a) {
           codes = *reinterpret_cast<const uint16_t*>(tile + kvq_v_half<D>(row, b, 2 * j)) |
                   (uint32_t)*reinterpret_cast<const uint16_t*>(tile + kvq_v_half<D>(row, b, 2 * j + 1)) << 16;
         }
-        const float d = __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t*>(
-            tile + (kv ? L::VS_OFF : L::KS_OFF) + row * L::SCL + 2 * b)));
+        const float d =
+            __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t*>(tile + kvq_scale<D>(kv, row, b))));
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = (float)((int)((codes >> (4 * i)) & 15u) - 8) * d;
       }

@@ -1,24 +1,28 @@
 // q4_kvq.cuh — device layout of the 4-bit KV cache and the small helpers its
 // kernels share (not part of the public ABI).
 //
-// Layout.  A (slot, head) plane is a run of tiles of KVQ_TILE = 16 positions;
-// a tile holds, one after another,
-//   K codes   16 rows of D/2 bytes      K scales  16 rows of D/32 binary16
-//   V codes   16 rows of D/2 bytes      V scales  16 rows of D/32 binary16
-// so a warp fetches one tile with one bulk copy (2,304 bytes at D = 128, 1,152
-// at D = 64), and the K half alone is one copy too.  Codes are the nibbles
-// q = 0..15 of the Q4_0 rule; block b of a row (32 values) is four words,
-// word j holding values 8j .. 8j+7 from the low nibble up.
+// Layout.  A (slot, head) plane is a run of 2,304-byte tiles of POS positions
+// (16 at D = 128, 32 at D = 64); a tile holds, one after another,
+//   K codes   POS rows of D/2 bytes      K scales  POS x D/32 binary16
+//   V codes   POS rows of D/2 bytes      V scales  POS x D/32 binary16
+// so a warp fetches one tile with one bulk copy, and the K half alone is one
+// copy too.  Codes are the nibbles q = 0..15 of the Q4_0 rule; block b of a
+// row (32 values) is four words, word j holding values 8j .. 8j+7 from the low
+// nibble up.
 //
 // K row: word j of block b sits at byte j*4*NB + 4b (NB = D/32).  In an
 // m16n8k16 product with keys along n, lane 4g + tq feeds key g with the words
 // j = tq, which are then contiguous (16 bytes at D = 128).  Which value sits
 // at which k index does not matter as long as the query fragment agrees.
 // V row: half-word g (values 4g .. 4g+3 of a block) of block b sits at byte
-// (g*NB + b)*2, so lane (g, tq) of the P V product, with values along n and
-// keys along k, reads contiguous bytes too.  With D = 128 the 16-byte vectors
-// of rows with bit 2 set are stored with index ^ 2: the four rows that a
-// half-warp reads together then fall into different shared-memory banks.
+// (g*NB + b)*2, so lane (g, tq) of the P V product, with values along m and
+// keys along k, reads contiguous bytes too.
+// Position r is stored as code row r with its low three bits in Gray code, and
+// at D = 128 the 16-byte vectors of V rows with bit 2 set have index ^ 2: the
+// rows that a group of lanes reads together (consecutive ones for K, every
+// second one for V) then fall into different shared-memory banks.
+// Scales are stored by pairs of positions: [r / 2][block][r % 2], so one word
+// is the pair that a lane's two columns need.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -31,31 +35,42 @@ namespace q4 {
 template <int D>
 struct Kvq {
   static constexpr int NB = D / 32;                       // blocks (scales) per row
+  static constexpr int POS = kvq_tile_positions(D);       // positions per tile
   static constexpr int ROW = D / 2;                       // code bytes per row
   static constexpr int SCL = 2 * NB;                      // scale bytes per row
-  static constexpr int KS_OFF = KVQ_TILE * ROW;           // K scales
-  static constexpr int V_OFF = KS_OFF + KVQ_TILE * SCL;   // V codes (= bytes of the K half)
-  static constexpr int VS_OFF = V_OFF + KVQ_TILE * ROW;   // V scales
-  static constexpr int BYTES = VS_OFF + KVQ_TILE * SCL;   // one tile
+  static constexpr int KS_OFF = POS * ROW;                // K scales
+  static constexpr int V_OFF = KS_OFF + POS * SCL;        // V codes (= bytes of the K half)
+  static constexpr int VS_OFF = V_OFF + POS * ROW;        // V scales
+  static constexpr int BYTES = VS_OFF + POS * SCL;        // one tile
+  static_assert(BYTES == KVQ_TILE_BYTES, "tile size");
 };
 
-// Byte offset in a V row of 16-byte vector v, for row r of a tile.
+// The code row of position r of a tile.
+__host__ __device__ constexpr int kvq_row(int r) { return (r & ~7) | ((r & 7) ^ ((r & 7) >> 1)); }
+
+// Byte offset in a V row of 16-byte vector v, for code row cr.
 template <int D>
-__device__ __forceinline__ int kvq_v_vec(int r, int v) {
-  return (D == 128 ? (v ^ ((r & 4) >> 1)) : v) * 16;
+__device__ __forceinline__ int kvq_v_vec(int cr, int v) {
+  return (D == 128 ? (v ^ ((cr & 4) >> 1)) : v) * 16;
 }
 
-// Byte offset in a tile of word j (values 8j .. 8j+7) of block b of K row r.
+// Byte offset in a tile of word j (values 8j .. 8j+7) of block b of position r's K.
 template <int D>
 __device__ __forceinline__ int kvq_k_word(int r, int b, int j) {
-  return r * Kvq<D>::ROW + (j * Kvq<D>::NB + b) * 4;
+  return kvq_row(r) * Kvq<D>::ROW + (j * Kvq<D>::NB + b) * 4;
 }
 
-// Byte offset in a tile of half-word g (values 4g .. 4g+3) of block b of V row r.
+// Byte offset in a tile of half-word g (values 4g .. 4g+3) of block b of position r's V.
 template <int D>
 __device__ __forceinline__ int kvq_v_half(int r, int b, int g) {
-  const int o = (g * Kvq<D>::NB + b) * 2;
-  return Kvq<D>::V_OFF + r * Kvq<D>::ROW + kvq_v_vec<D>(r, o >> 4) + (o & 15);
+  const int o = (g * Kvq<D>::NB + b) * 2, cr = kvq_row(r);
+  return Kvq<D>::V_OFF + cr * Kvq<D>::ROW + kvq_v_vec<D>(cr, o >> 4) + (o & 15);
+}
+
+// Byte offset in a tile of the scale of block b of position r.
+template <int D>
+__device__ __forceinline__ int kvq_scale(int kv, int r, int b) {
+  return (kv ? Kvq<D>::VS_OFF : Kvq<D>::KS_OFF) + (((r >> 1) * Kvq<D>::NB + b) * 2 + (r & 1)) * 2;
 }
 
 // The request whose packed rows contain row t: the last s with offsets[s] <= t

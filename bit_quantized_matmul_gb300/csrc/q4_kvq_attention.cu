@@ -8,22 +8,30 @@
 // row; the cache is read once per eight virtual rows (row j, head h of the
 // group: j*G + h), which is once for a decode row of up to eight heads a group.
 //
-// Accuracy.  Codes are exact in binary16 and the other operand is a pair
-// hi + lo / 2048 of binary16 terms (22 bits), so products carry fp32 accuracy
-// for fp32 queries.  An m16n8k16 product has 16 rows: rows 0-7 take the hi and
-// rows 8-15 the lo terms of eight virtual rows, so the pair costs no extra
-// instruction and both halves of a sum meet in one thread.
+// Accuracy.  Codes are exact in binary16 and the other operand x is a pair of
+// binary16 terms, x = hi + lo, so products carry the accuracy of fp32.
 //
-// Codes as matrix operands.  A nibble masked in place is the binary16 number
-// q * 2^-24 (low nibble of a byte) or 16 q * 2^-24 (high nibble), a subnormal
-// that the tensor core takes as it is: five integer instructions give four
-// operand registers.  The factor 16 is taken out of the query fragment, or
-// out of the accumulator for V; the offset -8 enters as the initial
-// accumulator -8 sum(q) of each block for K, and for V as 8 sum(w d) at the
-// end.  Scales: K's multiply each block's partial score, V's are folded into
-// the weights of that block.
+// Scores.  A nibble masked in place is the binary16 number q * 2^-24 (low
+// nibble of a byte) or 16 q * 2^-24 (high nibble), a subnormal that the tensor
+// core takes as it is: five integer instructions give four operand registers.
+// The factor 16 is taken out of the query fragment, and the offset -8 enters
+// as the initial accumulator -8 sum(x) of each block.  The tensor core aligns
+// products by their operands' exponents, of which a subnormal has the
+// largest that it can have, and drops what lies below: the query's hi terms
+// are therefore integers (the row scaled to |x| <= 2048), of whose sums
+// nothing is dropped, and lo is the rest.  One m16n8k16 product takes the hi
+// terms of eight virtual rows in its rows 0-7 and their lo terms in rows 8-15,
+// and a thread holds both.  K's scales multiply each block's partial score.
 //
-// Work.  A unit is one cache tile (16 positions) of one item (request, head,
+// Output.  Weights differ by many binades within a row, so here hi is x
+// rounded to binary16 and the codes are made q - 8 exactly (one more
+// instruction a register, none for the offset).  V's scales are folded into
+// the weights of their block; the weights' power-of-two scale follows the
+// largest V scale met so far as their exponent follows the largest score, so
+// that they fit binary16.  Values lie along m and virtual rows along n, and hi
+// and lo go into one accumulator.
+//
+// Work.  A unit is one cache tile (2,304 bytes) of one item (request, head,
 // eight virtual rows).  The launch's CTAs take equal, contiguous ranges of
 // units whatever the lengths are (each CTA sums the lengths itself, so the
 // host needs none of them); the four warps of a CTA take the tiles of a range
@@ -42,9 +50,8 @@ constexpr int WARPS = 4;
 constexpr int THREADS = 32 * WARPS;
 constexpr int ROWS = 8;               // virtual rows of an item
 constexpr int CTAS_PER_SM = 3;
-constexpr int STAGES = 6;             // tiles in flight per warp
+constexpr int STAGES = 4;             // tiles in flight per warp
 constexpr int MIN_UNITS = WARPS;      // units a CTA takes at least: one tile per warp
-constexpr float LO_SCALE = 2048.0f;   // 2^11: the lo term's factor
 constexpr float NEG_INF = -INFINITY;
 
 template <typename T>
@@ -56,6 +63,7 @@ struct Args {
   float scale_log2;         // scale * log2(e)
   int64_t slots, capacity, plane_bytes, total;
   int heads, group, S;
+  int tile;                 // positions per cache tile
   const int32_t *offsets, *slot, *pos;
   unsigned* status;
   unsigned long long wait_ns;
@@ -67,11 +75,45 @@ struct Args {
   float* mass;              // [slots, heads, capacity], or null
 };
 
-__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+// D = A B + C, m16n8k16, binary16 operands, fp32 sums
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                    const float (&c)[4]) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+
+// Two fp32 values in one 64-bit register: one instruction for both.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unf2(F2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 half2_f2(uint32_t w) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return f2(f.x, f.y);
 }
 
 __device__ __forceinline__ uint32_t pack(float a, float b) {
@@ -79,12 +121,12 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// hi and lo terms of two values: x = hi + lo / 2048
-__device__ __forceinline__ void split(float x0, float x1, uint32_t& hi, uint32_t& lo) {
-  const __half2 h = __floats2half2_rn(x0, x1);
-  const float2 f = __half22float2(h);
-  hi = *reinterpret_cast<const uint32_t*>(&h);
-  lo = pack((x0 - f.x) * LO_SCALE, (x1 - f.y) * LO_SCALE);
+// hi and lo terms of two values
+__device__ __forceinline__ void split(F2 x, uint32_t& hi, uint32_t& lo) {
+  const float2 v = unf2(x);
+  hi = pack(v.x, v.y);
+  const float2 l = unf2(fma2(half2_f2(hi), f2(-1.0f, -1.0f), x));
+  lo = pack(l.x, l.y);
 }
 
 // The operand registers of a word of codes: nibbles (0, 4), 16 * (1, 5),
@@ -94,6 +136,20 @@ __device__ __forceinline__ void unpack(uint32_t w, uint32_t (&r)[4]) {
   r[1] = w & 0x00F000F0u;
   r[2] = (w >> 8) & 0x000F000Fu;
   r[3] = (w >> 8) & 0x00F000F0u;
+}
+
+// The same as exact binary16 pairs q - 8: 1024 + q less 1032, or (1024 + 16 q) / 16 less 72.
+__device__ __forceinline__ void unpack_centred(uint32_t w, uint32_t (&r)[4]) {
+  const __half2 k1032 = __float2half2_rn(-1032.0f), k72 = __float2half2_rn(-72.0f),
+                k16 = __float2half2_rn(0.0625f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t v = i < 2 ? w : w >> 8;
+    const uint32_t x = (v & ((i & 1) ? 0x00F000F0u : 0x000F000Fu)) | 0x64006400u;
+    const __half2 h = *reinterpret_cast<const __half2*>(&x);
+    const __half2 y = (i & 1) ? __hfma2(h, k16, k72) : __hadd2(h, k1032);
+    r[i] = *reinterpret_cast<const uint32_t*>(&y);
+  }
 }
 
 // ---------------------------------------------------------------- work ranges
@@ -112,7 +168,7 @@ __device__ __forceinline__ Request load_request(const Args<T>& a, int s, bool by
   }
   r.n = (int)(q.e - q.b);
   if (r.n == 0) return r;
-  r.tiles = (int)((q.pos + r.n + KVQ_TILE - 1) / KVQ_TILE);
+  r.tiles = (int)((q.pos + r.n + a.tile - 1) / a.tile);
   r.items = a.heads * (by_rows ? (r.n * a.group + ROWS - 1) / ROWS : 1);
   return r;
 }
@@ -223,14 +279,18 @@ struct Walk {
 };
 
 // ---------------------------------------------------------------- queries
-// The query fragment of eight virtual rows: A registers per block and k-step,
-// the initial accumulators of each block, and the factor of the scores.
+// The query fragment of eight virtual rows: A registers per block and k-step
+// (rows 0-7 hi, rows 8-15 lo), the initial accumulators of each block, and the
+// factor of the scores.
 template <int D>
 struct Query {
   uint32_t a[Kvq<D>::NB][2][4];
-  float c_hi[Kvq<D>::NB], c_lo[Kvq<D>::NB];
+  float c[Kvq<D>::NB][4];
   float factor;
 };
+
+// 2^e for -126 <= e <= 127
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 
 template <int D, typename T>
 __device__ __forceinline__ void load_query(Query<D>& f, const Args<T>& a, const Request& r, int head, int row0,
@@ -260,10 +320,10 @@ __device__ __forceinline__ void load_query(Query<D>& f, const Args<T>& a, const 
   }
   top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
   top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-  // the row's largest value goes to [2^11, 2^12): binary16 keeps 37 binades
-  // below it, and the partial scores of 24 fewer stay normal in fp32
+  // the row's largest value goes to [1024, 2048); two factors, as 2^-e may not be a normal number
   int e = 0;
-  if (top > 0.0f && top < INFINITY) e = ilogbf(top) - 11;
+  if (top > 0.0f && top < INFINITY) e = max(((__float_as_int(top) >> 23) & 255) - 127, -126) - 10;
+  const float up1 = pow2((-e) / 2), up2 = pow2(-e - (-e) / 2);
   f.factor = scalbnf(1.0f, 24 + e);
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
@@ -272,16 +332,14 @@ __device__ __forceinline__ void load_query(Query<D>& f, const Args<T>& a, const 
     for (int s = 0; s < 2; ++s) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {  // values (2s + k) and (2s + k) + 4; the second pair meets codes of factor 16
-        const float up = k ? 0.0625f : 1.0f;
-        const float x0 = scalbnf(x[b][2 * s + k], -e) * up, x1 = scalbnf(x[b][2 * s + k + 4], -e) * up;
-        uint32_t hi, lo;
-        split(x0, x1, hi, lo);
-        f.a[b][s][2 * k] = hi;
+        const float x0 = x[b][2 * s + k] * up1 * up2, x1 = x[b][2 * s + k + 4] * up1 * up2;
+        const float h0 = rintf(x0), h1 = rintf(x1);
+        const float down = k ? 0.0625f : 1.0f, back = k ? 16.0f : 1.0f;
+        f.a[b][s][2 * k] = pack(h0 * down, h1 * down);
+        const uint32_t lo = pack((x0 - h0) * down, (x1 - h1) * down);
         f.a[b][s][2 * k + 1] = lo;
-        const float2 fh = __half22float2(*reinterpret_cast<const __half2*>(&hi));
         const float2 fl = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-        const float back = k ? 16.0f : 1.0f;
-        h += (fh.x + fh.y) * back;
+        h += h0 + h1;
         l += (fl.x + fl.y) * back;
       }
     }
@@ -289,88 +347,193 @@ __device__ __forceinline__ void load_query(Query<D>& f, const Args<T>& a, const 
     l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
     h += __shfl_xor_sync(0xFFFFFFFFu, h, 2);
     l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
-    f.c_hi[b] = h * (-8.0f * 0x1p-24f);
-    f.c_lo[b] = l * (-8.0f * 0x1p-24f);
+    f.c[b][0] = f.c[b][1] = h * (-8.0f * 0x1p-24f);
+    f.c[b][2] = f.c[b][3] = l * (-8.0f * 0x1p-24f);
   }
 }
 
-// Scales of the two cache rows e, e ^ 1 (e < 8, row group t of the tile).
+// The scale words of a lane's two columns, positions 8t + 2 tq and the next.
 template <int D>
-__device__ __forceinline__ void load_scales(const uint8_t* scl, int t, int e, float (&d0)[Kvq<D>::NB],
-                                            float (&d1)[Kvq<D>::NB]) {
-  constexpr int NB = Kvq<D>::NB;
-  const uint8_t* p = scl + (8 * t + (e & ~1)) * Kvq<D>::SCL;
-  uint32_t w[NB];
+__device__ __forceinline__ void load_scales(const uint8_t* scl, int t, int tq, uint32_t (&w)[Kvq<D>::NB]) {
+  const uint8_t* p = scl + (4 * t + tq) * 4 * Kvq<D>::NB;
   if constexpr (D == 128) {
     const uint4 v = *reinterpret_cast<const uint4*>(p);
-    const bool odd = e & 1;
-    w[0] = odd ? v.z : v.x;
-    w[1] = odd ? v.w : v.y;
-    w[2] = odd ? v.x : v.z;
-    w[3] = odd ? v.y : v.w;
-  } else {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    const bool odd = e & 1;
-    w[0] = odd ? v.y : v.x;
-    w[1] = odd ? v.x : v.y;
-  }
-#pragma unroll
-  for (int i = 0; i < NB / 2; ++i) {
-    const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-    const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&w[NB / 2 + i]));
-    d0[2 * i] = f0.x;
-    d0[2 * i + 1] = f0.y;
-    d1[2 * i] = f1.x;
-    d1[2 * i + 1] = f1.y;
-  }
-}
-
-// Words of K row r that lane tq of an MMA group reads.
-template <int D>
-__device__ __forceinline__ void load_k(const uint8_t* tile, int r, int tq, uint32_t (&w)[Kvq<D>::NB]) {
-  if constexpr (D == 128) {
-    const uint4 v = *reinterpret_cast<const uint4*>(tile + r * Kvq<D>::ROW + tq * 16);
     w[0] = v.x;
     w[1] = v.y;
     w[2] = v.z;
     w[3] = v.w;
   } else {
-    const uint2 v = *reinterpret_cast<const uint2*>(tile + r * Kvq<D>::ROW + tq * 8);
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
     w[0] = v.x;
     w[1] = v.y;
   }
 }
 
-// Scores (log2 units) of a tile: sc[t][c] for this thread's row and the keys
-// key_of(t, 2 tq + c).  Column n of a product stands for cache row
-// 8t + (n ^ n >> 1): with this order the rows that a group of lanes reads
-// together lie in different shared-memory banks.
-__device__ __forceinline__ int gray(int n) { return n ^ (n >> 1); }
-
+// Scores (log2 units) of eight positions: sc for this lane's row g and the
+// positions 8t + 2 tq, + 1 of the tile.
 template <int D>
-__device__ __forceinline__ void tile_scores(const uint8_t* tile, const Query<D>& q, int lane, float (&sc)[2][2]) {
+__device__ __forceinline__ float2 scores8(const uint8_t* tile, const Query<D>& q, int t, int g, int tq) {
   constexpr int NB = Kvq<D>::NB;
-  const int g = lane >> 2, tq = lane & 3;
-  const int e = gray(2 * tq);
+  uint32_t w[NB], d[NB];
+  const uint8_t* row = tile + (8 * t + kvq_row(g)) * Kvq<D>::ROW + tq * 4 * NB;
+  if constexpr (D == 128) {
+    const uint4 v = *reinterpret_cast<const uint4*>(row);
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(row);
+    w[0] = v.x;
+    w[1] = v.y;
+  }
+  load_scales<D>(tile + Kvq<D>::KS_OFF, t, tq, d);
+  F2 s = f2(0.0f, 0.0f);
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    uint32_t w[NB];
-    load_k<D>(tile, 8 * t + gray(g), tq, w);
-    float d0[NB], d1[NB];
-    load_scales<D>(tile + Kvq<D>::KS_OFF, t, e, d0, d1);
-    float s0 = 0.0f, s1 = 0.0f;
+  for (int b = 0; b < NB; ++b) {
+    float c[4];
+    uint32_t r[4];
+    unpack(w[b], r);
+    mma(c, q.a[b][0], r[0], r[1], q.c[b]);
+    mma(c, q.a[b][1], r[2], r[3], c);
+    s = fma2(half2_f2(d[b]), add2(f2(c[0], c[1]), f2(c[2], c[3])), s);
+  }
+  return unf2(mul2(s, f2(q.factor, q.factor)));
+}
+
+// ---------------------------------------------------------------- sums
+// A warp's running sums over the positions it has taken.  Weights are
+// 2^(score - m + up), with up such that weight times V scale is at most 2^14.
+template <int D>
+struct Sums {
+  float o[Kvq<D>::NB][2][4];  // [block][values 4g + 2i, + 1][rows 2 tq, 2 tq + 1, twice]
+  F2 l;                       // row g
+  float m, off;               // row g: the largest score, and m - up (0 while m is -inf)
+  uint32_t dtop;              // the largest V scale so far, as a power of two, in both halves
+  int up;
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      float c[4] = {q.c_hi[b], q.c_hi[b], q.c_lo[b], q.c_lo[b]};
-      uint32_t r[4];
-      unpack(w[b], r);
-      mma(c, q.a[b][0], r[0], r[1]);
-      mma(c, q.a[b][1], r[2], r[3]);
-      s0 = fmaf(d0[b], fmaf(c[2], 1.0f / LO_SCALE, c[0]), s0);
-      s1 = fmaf(d1[b], fmaf(c[3], 1.0f / LO_SCALE, c[1]), s1);
+    for (int b = 0; b < Kvq<D>::NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[b][i][k] = 0.0f;
+    l = f2(0.0f, 0.0f);
+    m = NEG_INF;
+    off = 0.0f;
+    dtop = 0;
+    up = 0;
+  }
+};
+
+// Takes the positions p0 .. p0 + 15, the `half`th sixteen of a tile.  MASKED:
+// some row does not see them all; row g sees those up to `last`, and what lies
+// at `end` and after may be anything.
+template <int D, bool MASKED>
+__device__ __forceinline__ void step16(const uint8_t* tile, int half, int p0, const Query<D>& q, Sums<D>& a, int g,
+                                       int tq, int last, int end) {
+  using L = Kvq<D>;
+  constexpr int NB = L::NB;
+  float sc[2][2];
+  uint32_t vd[2][NB];  // V scale pairs
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const float2 x = scores8<D>(tile, q, 2 * half + u, g, tq);
+    sc[u][0] = x.x;
+    sc[u][1] = x.y;
+    load_scales<D>(tile + L::VS_OFF, 2 * half + u, tq, vd[u]);
+  }
+  if constexpr (MASKED) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int p = p0 + 8 * u + 2 * tq + c;
+        sc[u][c] = p <= last ? sc[u][c] : NEG_INF;
+        if (p >= end) {
+#pragma unroll
+          for (int b = 0; b < NB; ++b) vd[u][b] &= c ? 0x0000FFFFu : 0xFFFF0000u;
+        }
+      }
+  }
+  const float top = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
+  __half2 dm = *reinterpret_cast<const __half2*>(&a.dtop);
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+#pragma unroll
+    for (int b = 0; b < NB; ++b) dm = __hmax2(dm, __habs2(*reinterpret_cast<const __half2*>(&vd[u][b])));
+  const uint32_t dmw = *reinterpret_cast<const uint32_t*>(&dm);
+  if (__any_sync(0xFFFFFFFFu, top > a.m || dmw != a.dtop)) {
+    float mn = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    mn = fmaxf(a.m, fmaxf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, 2)));
+    uint32_t h = max(dmw & 0xFFFFu, dmw >> 16);  // magnitudes order as integers
+    h = max(h, __shfl_xor_sync(0xFFFFFFFFu, h, 1));
+    h = max(h, __shfl_xor_sync(0xFFFFFFFFu, h, 2));
+    h = min((max(h, 1u << 10) + 0x3FFu) & 0x7C00u, 0x7800u);  // up to a power of two, 2^-14 .. 2^15
+    a.dtop = h | h << 16;
+    a.up = 14 + 15 - (int)(h >> 10);
+    const float no = mn == NEG_INF ? 0.0f : mn - (float)a.up;
+    const float f = a.m == NEG_INF ? 1.0f : ex2(a.off - no);  // nothing summed yet while m is -inf
+    a.m = mn;
+    a.off = no;
+    a.l = mul2(a.l, f2(f, f));
+    const float f0 = __shfl_sync(0xFFFFFFFFu, f, 8 * tq), f1 = __shfl_sync(0xFFFFFFFFu, f, 8 * tq + 4);
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        a.o[b][i][0] *= f0;
+        a.o[b][i][1] *= f1;
+        a.o[b][i][2] *= f0;
+        a.o[b][i][3] *= f1;
+      }
+  }
+  F2 p[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    p[u] = f2(ex2(sc[u][0] - a.off), ex2(sc[u][1] - a.off));
+    a.l = add2(a.l, p[u]);
+  }
+  // V words of this lane's keys 2 tq, 2 tq + 1 (u = 0) and + 8 (u = 1)
+  uint32_t vw[2][2][NB / 2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const uint8_t* v = tile + kvq_v_half<D>(16 * half + 8 * u + 2 * tq + c, 0, g);
+      if constexpr (D == 128) {
+        const uint2 x = *reinterpret_cast<const uint2*>(v);
+        vw[u][c][0] = x.x;
+        vw[u][c][1] = x.y;
+      } else {
+        vw[u][c][0] = *reinterpret_cast<const uint32_t*>(v);
+      }
     }
-    sc[t][0] = s0 * q.factor;
-    sc[t][1] = s1 * q.factor;
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    // weights times the block's V scales, as hi and lo terms: B operand with keys along k
+    uint32_t hi[2], lo[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      F2 x = mul2(p[u], half2_f2(vd[u][b]));
+      if constexpr (MASKED) {  // a weight of 0 keeps a NaN scale out
+        float2 y = unf2(x);
+        if (sc[u][0] == NEG_INF) y.x = 0.0f;
+        if (sc[u][1] == NEG_INF) y.y = 0.0f;
+        x = f2(y.x, y.y);
+      }
+      split(x, hi[u], lo[u]);
+    }
+    uint32_t r0[4], r1[4];
+    const uint32_t sel = (b & 1) ? 0x7632u : 0x5410u;
+    unpack_centred(__byte_perm(vw[0][0][b / 2], vw[0][1][b / 2], sel), r0);
+    unpack_centred(__byte_perm(vw[1][0][b / 2], vw[1][1][b / 2], sel), r1);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {  // values 4g + 2i and 4g + 2i + 1 of the block as rows g and g + 8
+      const uint32_t av[4] = {r0[2 * i], r0[2 * i + 1], r1[2 * i], r1[2 * i + 1]};
+      mma(a.o[b][i], av, hi[0], hi[1], a.o[b][i]);
+      mma(a.o[b][i], av, lo[0], lo[1], a.o[b][i]);
+    }
   }
 }
 
@@ -405,24 +568,30 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kvq_attention_kernel(con
   Walk<T> in, out;
   in.begin(a, range, true);
   out.begin(a, range, true);
-  int in_tile = in.t0 + warp;
+  const uint8_t* in_ptr = nullptr;  // the warp's next tile of the issue cursor's segment
+  int in_left = 0;                  // and how many it has
+  auto enter = [&]() {
+    const int head = in.item / (in.r.items / a.heads);
+    in_ptr = a.cache + (in.r.slot * a.heads + head) * a.plane_bytes + (int64_t)(in.t0 + warp) * L::BYTES;
+    in_left = (in.t1 - in.t0 - warp + WARPS - 1) / WARPS;  // rounds towards zero: none when the segment is short
+  };
+  if (in.t0 < in.t1) enter();
   unsigned issued = 0, taken = 0;
   auto issue = [&]() {  // the warp's next tile, if any, into the ring
-    while (in.t0 < in.t1 && in_tile >= in.t1) {
+    while (in_left <= 0) {
+      if (in.t0 >= in.t1) return;
       in.next(a, true);
-      in_tile = in.t0 + warp;
+      if (in.t0 >= in.t1) return;
+      enter();
     }
-    if (in.t0 >= in.t1) return;
-    const int head = in.item / (in.r.items / a.heads);
     if (lane == 0) {
       const unsigned st = issued % STAGES;
       mbar_expect_tx(bar_u32 + 8 * st, L::BYTES);
-      bulk_load(ring_u32 + st * L::BYTES,
-                a.cache + (in.r.slot * a.heads + head) * a.plane_bytes + (int64_t)in_tile * L::BYTES, L::BYTES,
-                bar_u32 + 8 * st);
+      bulk_load(ring_u32 + st * L::BYTES, in_ptr, L::BYTES, bar_u32 + 8 * st);
     }
     ++issued;
-    in_tile += WARPS;
+    --in_left;
+    in_ptr += WARPS * L::BYTES;
   };
 #pragma unroll 1
   for (int i = 0; i < STAGES; ++i) issue();
@@ -434,17 +603,11 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kvq_attention_kernel(con
     const int head = out.item / groups, row0 = (out.item - head * groups) * ROWS;
     Query<D> q;
     load_query<D, T>(q, a, r, head, row0, lane);
-    float o[4 * NB][4];
-    float vb[NB];
-#pragma unroll
-    for (int i = 0; i < 4 * NB; ++i)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) o[i][k] = 0.0f;
-#pragma unroll
-    for (int b = 0; b < NB; ++b) vb[b] = 0.0f;
-    float m = NEG_INF, l = 0.0f;
-    const int64_t last = r.pos + (row0 + g) / a.group;  // the row's last visible position
-    const int64_t clear = r.pos + row0 / a.group;       // positions up to here are visible to every row
+    Sums<D> sums;
+    sums.clear();
+    const int last = (int)r.pos + (row0 + g) / a.group;  // the row's last visible position
+    const int clear = (int)r.pos + row0 / a.group + 1;   // positions below are visible to every row
+    const int end = (int)r.pos + r.n;                    // positions from here on hold anything
 
     for (int t = out.t0 + warp; t < out.t1; t += WARPS) {
       const unsigned st = taken % STAGES;
@@ -455,111 +618,31 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kvq_attention_kernel(con
       if (dead) continue;
       ++taken;
       const uint8_t* tile = ring + st * L::BYTES;
-      float sc[2][2];
-      tile_scores<D>(tile, q, lane, sc);
-      const int e = gray(2 * tq);
-      const bool masked = (int64_t)(t + 1) * KVQ_TILE - 1 > clear;
-      bool vis[2][2] = {{true, true}, {true, true}};
-      if (masked) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            vis[u][c] = (int64_t)t * KVQ_TILE + 8 * u + (e ^ c) <= last;
-            sc[u][c] = vis[u][c] ? sc[u][c] : NEG_INF;
-          }
-      }
-      const float top = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
-      if (__any_sync(0xFFFFFFFFu, top > m)) {
-        float mn = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-        mn = fmaxf(m, fmaxf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, 2)));
-        const float f = mn == m ? 1.0f : ex2(m - mn);  // 0 on the first tile (m = -inf)
-        m = mn;
-        l *= f;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) vb[b] *= f;
-#pragma unroll
-        for (int i = 0; i < 4 * NB; ++i)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) o[i][k] *= f;
-      }
-      const float mm = m == NEG_INF ? 0.0f : m;  // no position visible yet: every weight is 0
-      float p[2][2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          p[u][c] = ex2(sc[u][c] - mm);
-          l += p[u][c];
-        }
-      // weights times V's scale of each block, as hi and lo terms
-      uint32_t pa[NB][4];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        float d0[NB], d1[NB];
-        load_scales<D>(tile + L::VS_OFF, u, e, d0, d1);
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          float x0 = p[u][0] * d0[b], x1 = p[u][1] * d1[b];
-          if (masked) {  // scales of rows past the end may be anything
-            x0 = vis[u][0] ? x0 : 0.0f;
-            x1 = vis[u][1] ? x1 : 0.0f;
-          }
-          vb[b] += x0 + x1;
-          split(x0, x1, pa[b][2 * u], pa[b][2 * u + 1]);
-        }
-      }
-      // V words of the rows of columns 2 tq and 2 tq + 1, both row groups
-      uint32_t vw[2][2][NB / 2];  // [row group][row][word: blocks 2i, 2i + 1]
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int row = 8 * u + (e ^ c);
-          const uint8_t* v = tile + kvq_v_half<D>(row, 0, g);
-          if constexpr (D == 128) {
-            const uint2 x = *reinterpret_cast<const uint2*>(v);
-            vw[u][c][0] = x.x;
-            vw[u][c][1] = x.y;
-          } else {
-            vw[u][c][0] = *reinterpret_cast<const uint32_t*>(v);
-          }
-        }
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        uint32_t r0[4], r1[4];
-        const uint32_t sel = (b & 1) ? 0x7632u : 0x5410u;
-        unpack(__byte_perm(vw[0][0][b / 2], vw[0][1][b / 2], sel), r0);
-        unpack(__byte_perm(vw[1][0][b / 2], vw[1][1][b / 2], sel), r1);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mma(o[4 * b + i], pa[b], r0[i], r1[i]);
+      for (int half = 0; half < L::POS / 16; ++half) {
+        const int p0 = t * L::POS + 16 * half;
+        if (p0 + 16 <= clear) step16<D, false>(tile, half, p0, q, sums, g, tq, last, end);
+        else step16<D, true>(tile, half, p0, q, sums, g, tq, last, end);
       }
       __syncwarp();  // every lane has read the stage before it is written again
       issue();
     }
 
     // ---- merge the warps' sums of the segment ----
+    const float down = pow2(-sums.up);
+    const float2 lp = unf2(sums.l);
+    float l = lp.x + lp.y;
     l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
     l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
     __syncthreads();  // the previous segment's sums have been read
-    if (tq == 0) merge_ml[warp * ROWS + g] = make_float2(m, l);
-    float* mo = merge + (warp * ROWS + g) * D;
+    if (tq == 0) merge_ml[warp * ROWS + g] = make_float2(sums.m, l * down);
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      vb[b] += __shfl_xor_sync(0xFFFFFFFFu, vb[b], 1);
-      vb[b] += __shfl_xor_sync(0xFFFFFFFFu, vb[b], 2);
-      float x[2][4];
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float up = (i & 1) ? 0x1p20f : 0x1p24f;  // codes 2^-24, or 16 times that
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          x[c][i] = fmaf(fmaf(o[4 * b + i][2 + c], 1.0f / LO_SCALE, o[4 * b + i][c]), up, -8.0f * vb[b]);
-      }
-      // column 2 tq + c of product i is value 32 b + 4 (2 tq + c) + i
-      *reinterpret_cast<float4*>(mo + 32 * b + 8 * tq) = make_float4(x[0][0], x[0][1], x[0][2], x[0][3]);
-      *reinterpret_cast<float4*>(mo + 32 * b + 8 * tq + 4) = make_float4(x[1][0], x[1][1], x[1][2], x[1][3]);
-    }
+      for (int k = 0; k < 2; ++k)  // row 2 tq + k: values 32 b + 4 g ..
+        *reinterpret_cast<float4*>(merge + (warp * ROWS + 2 * tq + k) * D + 32 * b + 4 * g) =
+            make_float4(sums.o[b][0][k] * down, sums.o[b][0][2 + k] * down, sums.o[b][1][k] * down,
+                        sums.o[b][1][2 + k] * down);
     __syncthreads();
     const bool whole = out.t0 == 0 && out.t1 == r.tiles;
     const int slot = 2 * blockIdx.x + (out.t0 == 0 ? 1 : 0);
@@ -718,22 +801,22 @@ __global__ void __launch_bounds__(THREADS) kvq_mass_kernel(const Args<T> a) {
       const float lse = live ? a.lse[(r.b + j) * (int64_t)(a.heads * a.group) + head * a.group + vr - j * a.group] : 0.0f;
       const int64_t last = live ? r.pos + j : -1;
       for (int t = it.t0 + warp; t < it.t1; t += WARPS) {
-        float sc[2][2];
-        tile_scores<D>(plane + (int64_t)t * L::BYTES, q, lane, sc);
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < L::POS / 8; ++u) {
+          const float2 sc = scores8<D>(plane + (int64_t)t * L::BYTES, q, u, g, tq);
+          const int64_t p = (int64_t)t * L::POS + 8 * u + 2 * tq;
+          float w[2] = {p <= last ? ex2(sc.x - lse) : 0.0f, p + 1 <= last ? ex2(sc.y - lse) : 0.0f};
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const int64_t p = (int64_t)t * KVQ_TILE + 8 * u + (gray(2 * tq) ^ c);
-            float w = p <= last ? ex2(sc[u][c] - lse) : 0.0f;
-            w += __shfl_xor_sync(0xFFFFFFFFu, w, 4);
-            w += __shfl_xor_sync(0xFFFFFFFFu, w, 8);
-            w += __shfl_xor_sync(0xFFFFFFFFu, w, 16);
-            if (g == 0 && p < r.pos + r.n) {
-              const float old = (row0 == 0 && p >= r.pos) ? 0.0f : mass[p];
-              mass[p] = old + w;
+            w[c] += __shfl_xor_sync(0xFFFFFFFFu, w[c], 4);
+            w[c] += __shfl_xor_sync(0xFFFFFFFFu, w[c], 8);
+            w[c] += __shfl_xor_sync(0xFFFFFFFFu, w[c], 16);
+            if (g == 0 && p + c < r.pos + r.n) {
+              const float old = (row0 == 0 && p + c >= r.pos) ? 0.0f : mass[p + c];
+              mass[p + c] = old + w[c];
             }
           }
+        }
       }
     }
   }
@@ -756,6 +839,7 @@ int launch_as(const KvqStep& c, const uint8_t* cache, const void* q, const int64
   a.heads = (int)c.heads;
   a.group = q_heads / (int)c.heads;
   a.S = c.S;
+  a.tile = Kvq<D>::POS;
   a.offsets = c.offsets;
   a.slot = c.slot;
   a.pos = c.pos;

@@ -153,42 +153,38 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const KvqEvic
   }
 }
 
-// Vectors of a row: codes of K and V (D/32 each of 16 bytes) and the scales.
-// The V vectors of a row depend on its place in the tile (kvq_v_vec).
+// A row as pieces: 16-byte vectors of K and V codes, then the binary16 scales
+// of K and V.  Where a piece lies depends on the row's place in its tile.
 template <int D>
-struct RowCopy {
+struct RowPieces {
   using L = Kvq<D>;
-  static constexpr int CV = D / 32;       // code vectors per K or V row
-  static constexpr int VECS = 2 * CV;     // 16-byte vectors; then two scale words
-  __device__ static const uint8_t* at(const uint8_t* plane, int64_t p, int v) {
-    const int row = (int)(p % KVQ_TILE);
-    const uint8_t* tile = plane + p / KVQ_TILE * L::BYTES;
-    if (v < CV) return tile + row * L::ROW + v * 16;
-    return tile + L::V_OFF + row * L::ROW + kvq_v_vec<D>(row, v - CV);
+  static constexpr int CV = D / 32;          // code vectors per K or V row
+  static constexpr int VECS = 2 * CV;
+  static constexpr int PIECES = VECS + 2 * L::NB;
+  __device__ static uint8_t* vec(uint8_t* plane, int64_t p, int v) {
+    const int cr = kvq_row((int)(p % L::POS));
+    uint8_t* tile = plane + p / L::POS * L::BYTES;
+    return v < CV ? tile + cr * L::ROW + v * 16 : tile + L::V_OFF + cr * L::ROW + kvq_v_vec<D>(cr, v - CV);
   }
-  __device__ static const uint8_t* scale(const uint8_t* plane, int64_t p, int kv) {
-    return plane + p / KVQ_TILE * L::BYTES + (kv ? L::VS_OFF : L::KS_OFF) + (p % KVQ_TILE) * L::SCL;
+  __device__ static uint16_t* scale(uint8_t* plane, int64_t p, int i) {
+    return reinterpret_cast<uint16_t*>(plane + p / L::POS * L::BYTES +
+                                       kvq_scale<D>(i / L::NB, (int)(p % L::POS), i % L::NB));
   }
 };
 
-// Scales of a row: 8 bytes at D = 128, 4 at D = 64.
-template <int D>
-using ScaleWord = typename std::conditional<D == 128, uint2, uint32_t>::type;
-
 template <int D>
 __global__ void __launch_bounds__(MOVE_THREADS) evict_move_kernel(const KvqEvict a, int64_t plane_bytes) {
-  using R = RowCopy<D>;
-  constexpr int ITEMS = R::VECS + 2;  // per row: vectors, then the K and the V scales
+  using R = RowPieces<D>;
   const int s = blockIdx.y / (int)a.heads, h = blockIdx.y % (int)a.heads;
   const int n = a.new_len[s];
   if (n <= 0) return;
   const int64_t src_slot = a.src[s], dst_slot = a.dst[s];
   const bool in_place = src_slot == dst_slot;
   if (in_place && (blockIdx.x != 0 || n == a.len[s])) return;
-  const uint8_t* src = a.cache + (src_slot * a.heads + h) * plane_bytes;
+  uint8_t* src = a.cache + (src_slot * a.heads + h) * plane_bytes;
   uint8_t* dst = a.cache + (dst_slot * a.heads + h) * plane_bytes;
   const int32_t* kept = a.kept + (int64_t)blockIdx.y * a.keep;
-  const int items = n * ITEMS;  // below 2^31: checked on the host
+  const int items = n * R::PIECES;  // below 2^31: checked on the host
   constexpr int STEP = MOVE_THREADS * MOVE_VEC;
   const int first = in_place ? 0 : blockIdx.x * STEP, stride = in_place ? STEP : gridDim.x * STEP;
   for (int i0 = first; i0 < items; i0 += stride) {
@@ -197,14 +193,10 @@ __global__ void __launch_bounds__(MOVE_THREADS) evict_move_kernel(const KvqEvict
     for (int u = 0; u < MOVE_VEC; ++u) {
       const int it = i0 + u * MOVE_THREADS + threadIdx.x;
       if (it < items) {
-        const int row = it / ITEMS, e = it - row * ITEMS;
+        const int row = it / R::PIECES, e = it - row * R::PIECES;
         const int64_t p = kept[row];
-        if (e < R::VECS) {
-          v[u] = *reinterpret_cast<const uint4*>(R::at(src, p, e));
-        } else {
-          *reinterpret_cast<ScaleWord<D>*>(&v[u]) =
-              *reinterpret_cast<const ScaleWord<D>*>(R::scale(src, p, e - R::VECS));
-        }
+        if (e < R::VECS) v[u] = *reinterpret_cast<const uint4*>(R::vec(src, p, e));
+        else v[u].x = *R::scale(src, p, e - R::VECS);
       }
     }
     if (in_place) __syncthreads();  // the step is read before it is written; later steps read from further on
@@ -212,13 +204,9 @@ __global__ void __launch_bounds__(MOVE_THREADS) evict_move_kernel(const KvqEvict
     for (int u = 0; u < MOVE_VEC; ++u) {
       const int it = i0 + u * MOVE_THREADS + threadIdx.x;
       if (it < items) {
-        const int row = it / ITEMS, e = it - row * ITEMS;
-        if (e < R::VECS) {
-          *reinterpret_cast<uint4*>(const_cast<uint8_t*>(R::at(dst, row, e))) = v[u];
-        } else {
-          *reinterpret_cast<ScaleWord<D>*>(const_cast<uint8_t*>(R::scale(dst, row, e - R::VECS))) =
-              *reinterpret_cast<ScaleWord<D>*>(&v[u]);
-        }
+        const int row = it / R::PIECES, e = it - row * R::PIECES;
+        if (e < R::VECS) *reinterpret_cast<uint4*>(R::vec(dst, row, e)) = v[u];
+        else *R::scale(dst, row, e - R::VECS) = (uint16_t)v[u].x;
       }
     }
   }
@@ -230,7 +218,7 @@ int launch_kvq_evict(const KvqEvict& c, cudaStream_t s) {
   const int64_t planes = (int64_t)c.S * c.heads;
   evict_select_kernel<<<(unsigned)planes, SEL_THREADS, 0, s>>>(c);
   if (cudaGetLastError() != cudaSuccess) return Q4_ERR_CUDA;
-  const int64_t items = (int64_t)c.keep * (2 * (c.head_dim / 32) + 2);
+  const int64_t items = (int64_t)c.keep * (4 * (c.head_dim / 32));
   const int64_t steps = (items + MOVE_THREADS * MOVE_VEC - 1) / (MOVE_THREADS * MOVE_VEC);
   int64_t gx = ((int64_t)c.num_sms * 8 + planes - 1) / planes;
   if (gx > steps) gx = steps;

@@ -163,10 +163,11 @@ int launch_kv_append(uint8_t* k_cache, uint8_t* v_cache, const uint8_t* k_new, c
                      int num_sms, cudaStream_t s);
 
 // ---- 4-bit KV cache (layout in q4_kvq.cuh) ----
-constexpr int KVQ_TILE = 16;  // positions per tile
-inline int64_t kvq_tile_bytes(int64_t head_dim) { return KVQ_TILE * (head_dim + head_dim / 8); }
+constexpr int KVQ_TILE_BYTES = 2304;
+__host__ __device__ constexpr int kvq_tile_positions(int64_t head_dim) { return (int)(2048 / head_dim); }
 inline int64_t kvq_plane_bytes(int64_t head_dim, int64_t capacity) {
-  return (capacity + KVQ_TILE - 1) / KVQ_TILE * kvq_tile_bytes(head_dim);
+  const int64_t n = kvq_tile_positions(head_dim);
+  return (capacity + n - 1) / n * KVQ_TILE_BYTES;
 }
 // One step's packed rows over a cache: what its calls have in common.
 struct KvqStep {
