@@ -14,15 +14,16 @@
 // m16n8k16 product with keys along n, lane 4g + tq feeds key g with the words
 // j = tq, which are then contiguous (16 bytes at D = 128).  Which value sits
 // at which k index does not matter as long as the query fragment agrees.
-// V row: half-word g (values 4g .. 4g+3 of a block) of block b sits at byte
-// (g*NB + b)*2, so lane (g, tq) of the P V product, with values along m and
-// keys along k, reads contiguous bytes too.
-// Position r is stored as code row r with its low three bits in Gray code, and
-// at D = 128 the 16-byte vectors of V rows with bit 2 set have index ^ 2: the
-// rows that a group of lanes reads together (consecutive ones for K, every
-// second one for V) then fall into different shared-memory banks.
-// Scales are stored by pairs of positions: [r / 2][block][r % 2], so one word
-// is the pair that a lane's two columns need.
+// Position r is stored as K row r with its low three bits in Gray code: the rows
+// that a group of lanes reads together then fall into different shared-memory
+// banks.
+// V: positions 2i and 2i + 1 share a pair row of D bytes.  Half-word g (values
+// 4g .. 4g+3 of a block) of block b is word g*NB + b of the pair row, the even
+// position in its low and the odd one in its high half, so lane (g, tq) of the
+// P V product, with values along m and keys along k, reads the two keys of a
+// register as contiguous words (16 bytes at D = 128); these groups of NB words
+// are stored with index ^ 2 (i % 4), again for the banks.
+// Scales are stored by pairs of positions too: [r / 2][block][r % 2].
 #pragma once
 
 #include <cuda_bf16.h>
@@ -48,23 +49,22 @@ struct Kvq {
 // The code row of position r of a tile.
 __host__ __device__ constexpr int kvq_row(int r) { return (r & ~7) | ((r & 7) ^ ((r & 7) >> 1)); }
 
-// Byte offset in a V row of 16-byte vector v, for code row cr.
-template <int D>
-__device__ __forceinline__ int kvq_v_vec(int cr, int v) {
-  return (D == 128 ? (v ^ ((cr & 4) >> 1)) : v) * 16;
-}
-
 // Byte offset in a tile of word j (values 8j .. 8j+7) of block b of position r's K.
 template <int D>
 __device__ __forceinline__ int kvq_k_word(int r, int b, int j) {
   return kvq_row(r) * Kvq<D>::ROW + (j * Kvq<D>::NB + b) * 4;
 }
 
+// Byte offset in a tile of the words of group g of the pair row of positions r and r ^ 1.
+template <int D>
+__host__ __device__ constexpr int kvq_v_group(int r, int g) {
+  return Kvq<D>::V_OFF + (r >> 1) * D + (g ^ (r & 6)) * Kvq<D>::NB * 4;
+}
+
 // Byte offset in a tile of half-word g (values 4g .. 4g+3) of block b of position r's V.
 template <int D>
 __device__ __forceinline__ int kvq_v_half(int r, int b, int g) {
-  const int o = (g * Kvq<D>::NB + b) * 2, cr = kvq_row(r);
-  return Kvq<D>::V_OFF + cr * Kvq<D>::ROW + kvq_v_vec<D>(cr, o >> 4) + (o & 15);
+  return kvq_v_group<D>(r, g) + b * 4 + (r & 1) * 2;
 }
 
 // Byte offset in a tile of the scale of block b of position r.

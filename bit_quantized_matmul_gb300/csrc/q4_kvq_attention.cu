@@ -32,14 +32,11 @@
 // and lo go into one accumulator.
 //
 // Work.  A unit is one cache tile (2,304 bytes) of one item (request, head,
-// eight virtual rows).  The launch's CTAs take equal, contiguous ranges of
+// eight virtual rows).  The launch's warps take equal, contiguous ranges of
 // units whatever the lengths are (each CTA sums the lengths itself, so the
-// host needs none of them); the four warps of a CTA take the tiles of a range
-// in turn, each through its own ring of bulk copies, and merge their sums when
-// an item's range ends.  Items cut between CTAs leave (maximum, sum, o) in
-// scratch and a second launch joins them.
-#include <atomic>
-
+// host needs none of them), each through its own ring of bulk copies; after
+// the plan no warp waits for another.  Items cut between warps leave
+// (reference score, sum, o) in scratch and a second launch joins them.
 #include "q4_kvq.cuh"
 #include "q4_ptx.cuh"
 
@@ -51,8 +48,8 @@ constexpr int THREADS = 32 * WARPS;
 constexpr int ROWS = 8;               // virtual rows of an item
 constexpr int CTAS_PER_SM = 3;
 constexpr int STAGES = 4;             // tiles in flight per warp
-constexpr int MIN_UNITS = WARPS;      // units a CTA takes at least: one tile per warp
 constexpr float NEG_INF = -INFINITY;
+constexpr float SLACK = 5.0f;         // log2 of how far a weight may pass 1 before the sums are rescaled
 
 template <typename T>
 struct Args {
@@ -67,10 +64,10 @@ struct Args {
   const int32_t *offsets, *slot, *pos;
   unsigned* status;
   unsigned long long wait_ns;
-  float* partial;           // [2 * CTAs][ROWS][D]
-  float2* partial_ml;       // [2 * CTAs][ROWS] (maximum, sum)
+  float* partial;           // [2 * workers][ROWS][D]
+  float2* partial_ml;       // [2 * workers][ROWS] (reference score, sum)
   int64_t* unit_start;      // [S + 1]
-  int workers;              // CTAs of the main launch
+  int workers;              // warps of the main launch
   float* lse;               // [total, q_heads] log2 of the sum of exponentials, or null
   float* mass;              // [slots, heads, capacity], or null
 };
@@ -173,26 +170,54 @@ __device__ __forceinline__ Request load_request(const Args<T>& a, int s, bool by
   return r;
 }
 
-// The CTA's range of units: sums every request's units, takes an equal share
-// and finds where it starts.  by_rows: an item per eight virtual rows (else
-// one per head).
+// How `all` units are shared out: the first `more` of `workers` get size + 1,
+// the others size.  A worker is a warp; worker w is warp w / CTAs of CTA
+// w % CTAs, so that few units spread over all SMs.
+struct Shares {
+  int64_t size;
+  int more, workers;
+  __device__ __forceinline__ Shares(int64_t all, int most) {
+    workers = (int)min(all, (int64_t)most);
+    if (all < (int64_t)1 << 31) {
+      size = workers ? (int)all / workers : 0;
+    } else {
+      size = all / workers;
+    }
+    more = (int)(all - size * workers);
+  }
+  __device__ __forceinline__ int64_t start(int w) const { return w * size + min(w, more); }
+  // the worker that has unit u
+  __device__ __forceinline__ int of(int64_t u) const {
+    const int64_t big = more * (size + 1);
+    if (u < big) return big < (int64_t)1 << 31 ? (int)u / ((int)size + 1) : (int)(u / (size + 1));
+    u -= big;
+    return more + (u < (int64_t)1 << 31 && size < (int64_t)1 << 31 ? (int)u / (int)size : (int)(u / size));
+  }
+};
+
+// A worker's range of units.
 struct Range {
   int64_t left;  // units to do
   int s, item, tile;
+  Request r;
 };
 
+// Sums every request's units and finds where this warp's share starts.
+// by_rows: an item per eight virtual rows (else one per head).  CTA 0 writes
+// down the requests' first units.
 template <typename T>
-__device__ Range plan_range(const Args<T>& a, bool by_rows, int64_t* unit_start) {
+__device__ __forceinline__ Range plan_range(const Args<T>& a, bool by_rows, int64_t* unit_start) {
   __shared__ int64_t warp_sum[WARPS];
-  __shared__ Range found;
+  __shared__ Range found[WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int chunk = (a.S + THREADS - 1) / THREADS;
   const int s0 = min(a.S, tid * chunk), s1 = min(a.S, s0 + chunk);
   int64_t mine = 0;
   bool any_bad = false;
+  Request r{};
   for (int s = s0; s < s1; ++s) {
     bool bad = false;
-    const Request r = load_request(a, s, by_rows, &bad);
+    r = load_request(a, s, by_rows, &bad);
     any_bad |= bad;
     mine += (int64_t)r.tiles * r.items;
   }
@@ -204,38 +229,37 @@ __device__ Range plan_range(const Args<T>& a, bool by_rows, int64_t* unit_start)
     if (lane >= o) incl += v;
   }
   if (lane == 31) warp_sum[warp] = incl;
-  if (tid == 0) found = Range{0, 0, 0, 0};
+  if (tid < WARPS) found[tid].left = 0;
   __syncthreads();
   int64_t base = 0, all = 0;
+#pragma unroll
   for (int w = 0; w < WARPS; ++w) {
     if (w < warp) base += warp_sum[w];
     all += warp_sum[w];
   }
   int64_t start = base + incl - mine;
-  const int64_t need = (all + MIN_UNITS - 1) / MIN_UNITS;
-  const int64_t workers = need < gridDim.x ? need : gridDim.x;
-  int64_t u0 = 0, u1 = 0;
-  if ((int64_t)blockIdx.x < workers) {
-    u0 = blockIdx.x * all / workers;
-    u1 = (blockIdx.x + 1) * all / workers;
-  }
-  const bool here = u0 < u1 && u0 >= start && u0 < start + mine;
+  const Shares share(all, gridDim.x * WARPS);
   const bool note = unit_start && blockIdx.x == 0;
-  if (here || note) {
-    for (int s = s0; s < s1; ++s) {
-      const Request r = load_request(a, s, by_rows);
-      const int64_t units = (int64_t)r.tiles * r.items;
-      if (here && u0 >= start && u0 < start + units) {
-        const int64_t in = u0 - start;
-        found = Range{u1 - u0, s, (int)(in / r.tiles), (int)(in % r.tiles)};
-      }
-      if (note) unit_start[s] = start;
-      start += units;
+#pragma unroll 1
+  for (int s = s0; s < s1; ++s) {
+    if (chunk > 1) r = load_request(a, s, by_rows);
+    const int64_t units = (int64_t)r.tiles * r.items;
+    if (note) unit_start[s] = start;
+#pragma unroll 1
+    for (int w = 0; w < WARPS; ++w) {
+      const int worker = w * gridDim.x + blockIdx.x;
+      if (worker >= share.workers) break;
+      const int64_t u0 = share.start(worker);
+      if (u0 < start || u0 >= start + units) continue;
+      const int64_t in = u0 - start;
+      const int item = in < (int64_t)1 << 31 ? (int)in / r.tiles : (int)(in / r.tiles);
+      found[w] = Range{share.start(worker + 1) - u0, s, item, (int)(in - (int64_t)item * r.tiles), r};
     }
-    if (note && tid == THREADS - 1) unit_start[a.S] = all;
+    start += units;
   }
+  if (note && tid == THREADS - 1) unit_start[a.S] = all;
   __syncthreads();
-  return found;
+  return found[warp];
 }
 
 // Walks a range segment by segment: a run of tiles of one item.
@@ -244,15 +268,13 @@ struct Walk {
   int64_t left;
   int s, item, t0, t1;  // the segment: tiles [t0, t1) of the item
   Request r;
-  __device__ __forceinline__ void begin(const Args<T>& a, const Range& g, bool by_rows) {
+  __device__ __forceinline__ void begin(const Range& g) {
     left = g.left;
     s = g.s;
     item = g.item;
     t0 = t1 = g.tile;
-    if (left > 0) {
-      r = load_request(a, s, by_rows);
-      cut();
-    }
+    r = g.r;
+    if (left > 0) cut();
   }
   __device__ __forceinline__ void cut() {
     const int64_t end = t0 + left;
@@ -352,11 +374,9 @@ __device__ __forceinline__ void load_query(Query<D>& f, const Args<T>& a, const 
   }
 }
 
-// The scale words of a lane's two columns, positions 8t + 2 tq and the next.
-template <int D>
-__device__ __forceinline__ void load_scales(const uint8_t* scl, int t, int tq, uint32_t (&w)[Kvq<D>::NB]) {
-  const uint8_t* p = scl + (4 * t + tq) * 4 * Kvq<D>::NB;
-  if constexpr (D == 128) {
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N == 4) {
     const uint4 v = *reinterpret_cast<const uint4*>(p);
     w[0] = v.x;
     w[1] = v.y;
@@ -369,24 +389,19 @@ __device__ __forceinline__ void load_scales(const uint8_t* scl, int t, int tq, u
   }
 }
 
+// The scale pairs of a lane's two columns, positions 8t + 2 tq and the next.
+template <int D>
+__device__ __forceinline__ void load_scales(const uint8_t* scl, int t, int tq, uint32_t (&w)[Kvq<D>::NB]) {
+  load_words<Kvq<D>::NB>(scl + (4 * t + tq) * 4 * Kvq<D>::NB, w);
+}
+
 // Scores (log2 units) of eight positions: sc for this lane's row g and the
 // positions 8t + 2 tq, + 1 of the tile.
 template <int D>
 __device__ __forceinline__ float2 scores8(const uint8_t* tile, const Query<D>& q, int t, int g, int tq) {
   constexpr int NB = Kvq<D>::NB;
   uint32_t w[NB], d[NB];
-  const uint8_t* row = tile + (8 * t + kvq_row(g)) * Kvq<D>::ROW + tq * 4 * NB;
-  if constexpr (D == 128) {
-    const uint4 v = *reinterpret_cast<const uint4*>(row);
-    w[0] = v.x;
-    w[1] = v.y;
-    w[2] = v.z;
-    w[3] = v.w;
-  } else {
-    const uint2 v = *reinterpret_cast<const uint2*>(row);
-    w[0] = v.x;
-    w[1] = v.y;
-  }
+  load_words<NB>(tile + (8 * t + kvq_row(g)) * Kvq<D>::ROW + tq * 4 * NB, w);
   load_scales<D>(tile + Kvq<D>::KS_OFF, t, tq, d);
   F2 s = f2(0.0f, 0.0f);
 #pragma unroll
@@ -403,12 +418,13 @@ __device__ __forceinline__ float2 scores8(const uint8_t* tile, const Query<D>& q
 
 // ---------------------------------------------------------------- sums
 // A warp's running sums over the positions it has taken.  Weights are
-// 2^(score - m + up), with up such that weight times V scale is at most 2^14.
+// 2^(score - m + up), where m is at most SLACK below the largest score and up is
+// such that weight times V scale is at most 2^14 (2^15 for scales above 2^15).
 template <int D>
 struct Sums {
   float o[Kvq<D>::NB][2][4];  // [block][values 4g + 2i, + 1][rows 2 tq, 2 tq + 1, twice]
   F2 l;                       // row g
-  float m, off;               // row g: the largest score, and m - up (0 while m is -inf)
+  float m, off;               // row g: the reference score, and m - up (0 while m is -inf)
   uint32_t dtop;              // the largest V scale so far, as a power of two, in both halves
   int up;
   __device__ __forceinline__ void clear() {
@@ -463,7 +479,7 @@ __device__ __forceinline__ void step16(const uint8_t* tile, int half, int p0, co
 #pragma unroll
     for (int b = 0; b < NB; ++b) dm = __hmax2(dm, __habs2(*reinterpret_cast<const __half2*>(&vd[u][b])));
   const uint32_t dmw = *reinterpret_cast<const uint32_t*>(&dm);
-  if (__any_sync(0xFFFFFFFFu, top > a.m || dmw != a.dtop)) {
+  if (__any_sync(0xFFFFFFFFu, top > a.m + SLACK || dmw != a.dtop)) {
     float mn = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
     mn = fmaxf(a.m, fmaxf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, 2)));
     uint32_t h = max(dmw & 0xFFFFu, dmw >> 16);  // magnitudes order as integers
@@ -471,7 +487,7 @@ __device__ __forceinline__ void step16(const uint8_t* tile, int half, int p0, co
     h = max(h, __shfl_xor_sync(0xFFFFFFFFu, h, 2));
     h = min((max(h, 1u << 10) + 0x3FFu) & 0x7C00u, 0x7800u);  // up to a power of two, 2^-14 .. 2^15
     a.dtop = h | h << 16;
-    a.up = 14 + 15 - (int)(h >> 10);
+    a.up = 9 + 15 - (int)(h >> 10);
     const float no = mn == NEG_INF ? 0.0f : mn - (float)a.up;
     const float f = a.m == NEG_INF ? 1.0f : ex2(a.off - no);  // nothing summed yet while m is -inf
     a.m = mn;
@@ -495,20 +511,9 @@ __device__ __forceinline__ void step16(const uint8_t* tile, int half, int p0, co
     a.l = add2(a.l, p[u]);
   }
   // V words of this lane's keys 2 tq, 2 tq + 1 (u = 0) and + 8 (u = 1)
-  uint32_t vw[2][2][NB / 2];
+  uint32_t vw[2][NB];
 #pragma unroll
-  for (int u = 0; u < 2; ++u)
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const uint8_t* v = tile + kvq_v_half<D>(16 * half + 8 * u + 2 * tq + c, 0, g);
-      if constexpr (D == 128) {
-        const uint2 x = *reinterpret_cast<const uint2*>(v);
-        vw[u][c][0] = x.x;
-        vw[u][c][1] = x.y;
-      } else {
-        vw[u][c][0] = *reinterpret_cast<const uint32_t*>(v);
-      }
-    }
+  for (int u = 0; u < 2; ++u) load_words<NB>(tile + kvq_v_group<D>(16 * half + 8 * u + 2 * tq, g), vw[u]);
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     // weights times the block's V scales, as hi and lo terms: B operand with keys along k
@@ -525,9 +530,8 @@ __device__ __forceinline__ void step16(const uint8_t* tile, int half, int p0, co
       split(x, hi[u], lo[u]);
     }
     uint32_t r0[4], r1[4];
-    const uint32_t sel = (b & 1) ? 0x7632u : 0x5410u;
-    unpack_centred(__byte_perm(vw[0][0][b / 2], vw[0][1][b / 2], sel), r0);
-    unpack_centred(__byte_perm(vw[1][0][b / 2], vw[1][1][b / 2], sel), r1);
+    unpack_centred(vw[0][b], r0);
+    unpack_centred(vw[1][b], r1);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {  // values 4g + 2i and 4g + 2i + 1 of the block as rows g and g + 8
       const uint32_t av[4] = {r0[2 * i], r0[2 * i + 1], r1[2 * i], r1[2 * i + 1]};
@@ -538,47 +542,49 @@ __device__ __forceinline__ void step16(const uint8_t* tile, int half, int p0, co
 }
 
 // ---------------------------------------------------------------- main kernel
-template <int D>
-struct Smem {
-  static constexpr int RING = WARPS * STAGES * Kvq<D>::BYTES;
-  static constexpr int MERGE = WARPS * ROWS * D * 4;
-  static constexpr int ML = WARPS * ROWS * 8;
-  static constexpr int BYTES = RING + MERGE + ML + WARPS * STAGES * 8;
-};
+template <int D, typename T>
+__device__ __forceinline__ void store4(T* p, const float (&v)[4]) {
+  if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+    T h[4] = {(T)v[0], (T)v[1], (T)v[2], (T)v[3]};
+    *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(h);
+  }
+}
 
 template <int D, typename T>
 __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kvq_attention_kernel(const Args<T> a) {
   using L = Kvq<D>;
   constexpr int NB = L::NB;
-  extern __shared__ __align__(128) uint8_t smem[];
-  float* merge = reinterpret_cast<float*>(smem + Smem<D>::RING);                      // [WARPS][ROWS][D]
-  float2* merge_ml = reinterpret_cast<float2*>(smem + Smem<D>::RING + Smem<D>::MERGE);  // [WARPS][ROWS]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Smem<D>::RING + Smem<D>::MERGE + Smem<D>::ML);
+  __shared__ __align__(128) uint8_t rings[WARPS][STAGES][L::BYTES];
+  __shared__ uint64_t bars[WARPS][STAGES];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, tq = lane & 3;
-  uint8_t* ring = smem + warp * STAGES * L::BYTES;
-  const uint32_t ring_u32 = smem_u32(ring), bar_u32 = smem_u32(bars + warp * STAGES);
+  const uint32_t ring_u32 = smem_u32(rings[warp]), bar_u32 = smem_u32(bars[warp]);
   if (lane < STAGES) mbar_init(bar_u32 + 8 * lane, 1);
   mbar_init_fence();
   __syncwarp();
   asm volatile("griddepcontrol.launch_dependents;");
-  const Range range = plan_range(a, true, a.unit_start);
+  const int worker = warp * gridDim.x + blockIdx.x;
 
   // the issue cursor runs ahead of the consuming one by up to STAGES tiles
   Walk<T> in, out;
-  in.begin(a, range, true);
-  out.begin(a, range, true);
-  const uint8_t* in_ptr = nullptr;  // the warp's next tile of the issue cursor's segment
-  int in_left = 0;                  // and how many it has
+  {
+    const Range range = plan_range(a, true, a.unit_start);
+    in.begin(range);
+    out.begin(range);
+  }
+  const uint8_t* in_ptr = nullptr;  // the next tile of the issue cursor's segment
+  int in_left = 0;                  // and how many are left of it
   auto enter = [&]() {
     const int head = in.item / (in.r.items / a.heads);
-    in_ptr = a.cache + (in.r.slot * a.heads + head) * a.plane_bytes + (int64_t)(in.t0 + warp) * L::BYTES;
-    in_left = (in.t1 - in.t0 - warp + WARPS - 1) / WARPS;  // rounds towards zero: none when the segment is short
+    in_ptr = a.cache + (in.r.slot * a.heads + head) * a.plane_bytes + (int64_t)in.t0 * L::BYTES;
+    in_left = in.t1 - in.t0;
   };
   if (in.t0 < in.t1) enter();
   unsigned issued = 0, taken = 0;
-  auto issue = [&]() {  // the warp's next tile, if any, into the ring
-    while (in_left <= 0) {
+  auto issue = [&]() {  // the next tile, if any, into the ring
+    if (in_left == 0) {
       if (in.t0 >= in.t1) return;
       in.next(a, true);
       if (in.t0 >= in.t1) return;
@@ -591,12 +597,11 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kvq_attention_kernel(con
     }
     ++issued;
     --in_left;
-    in_ptr += WARPS * L::BYTES;
+    in_ptr += L::BYTES;
   };
 #pragma unroll 1
   for (int i = 0; i < STAGES; ++i) issue();
 
-  bool dead = false;  // a wait ran out: nothing more is read
   while (out.t0 < out.t1) {
     const Request& r = out.r;
     const int groups = r.items / a.heads;  // row groups of a head
@@ -609,15 +614,17 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kvq_attention_kernel(con
     const int clear = (int)r.pos + row0 / a.group + 1;   // positions below are visible to every row
     const int end = (int)r.pos + r.n;                    // positions from here on hold anything
 
-    for (int t = out.t0 + warp; t < out.t1; t += WARPS) {
+    for (int t = out.t0; t < out.t1; ++t) {
       const unsigned st = taken % STAGES;
-      if (!dead && !mbar_wait_warp(bar_u32 + 8 * st, (taken / STAGES) & 1, a.wait_ns)) {
-        dead = true;
+      if (!mbar_wait_warp(bar_u32 + 8 * st, (taken / STAGES) & 1, a.wait_ns)) {
+        // a copy never landed: wait (again with a limit) for the others in flight and give up
         if (lane == 0) atomicOr(a.status, STATUS_TIMEOUT);
+        for (; taken < issued; ++taken)
+          mbar_wait_warp(bar_u32 + 8 * (taken % STAGES), (taken / STAGES) & 1, a.wait_ns);
+        return;
       }
-      if (dead) continue;
       ++taken;
-      const uint8_t* tile = ring + st * L::BYTES;
+      const uint8_t* tile = rings[warp][st];
 #pragma unroll
       for (int half = 0; half < L::POS / 16; ++half) {
         const int p0 = t * L::POS + 16 * half;
@@ -628,78 +635,46 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kvq_attention_kernel(con
       issue();
     }
 
-    // ---- merge the warps' sums of the segment ----
-    const float down = pow2(-sums.up);
+    // ---- the segment's sums: the result, or a part for the join ----
     const float2 lp = unf2(sums.l);
     float l = lp.x + lp.y;
     l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
     l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
-    __syncthreads();  // the previous segment's sums have been read
-    if (tq == 0) merge_ml[warp * ROWS + g] = make_float2(sums.m, l * down);
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int k = 0; k < 2; ++k)  // row 2 tq + k: values 32 b + 4 g ..
-        *reinterpret_cast<float4*>(merge + (warp * ROWS + 2 * tq + k) * D + 32 * b + 4 * g) =
-            make_float4(sums.o[b][0][k] * down, sums.o[b][0][2 + k] * down, sums.o[b][1][k] * down,
-                        sums.o[b][1][2 + k] * down);
-    __syncthreads();
+    const float down = pow2(-sums.up);
     const bool whole = out.t0 == 0 && out.t1 == r.tiles;
-    const int slot = 2 * blockIdx.x + (out.t0 == 0 ? 1 : 0);
-    constexpr int PER = ROWS * D / THREADS;  // consecutive values of one row
-    {
-      const int row = tid * PER / D, d = tid * PER % D;
-      float2 ml[WARPS];
-      float top = NEG_INF;
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        ml[w] = merge_ml[w * ROWS + row];
-        top = fmaxf(top, ml[w].x);
+    const int rows = r.n * a.group;
+    // the row of this lane's l is g, those of its values 2 tq and 2 tq + 1
+    const int64_t slot = ((int64_t)2 * worker + (out.t0 == 0 ? 1 : 0)) * ROWS;
+    const float f = whole ? 1.0f / l : down;
+    if (whole) {
+      if (a.lse && tq == 0 && row0 + g < rows) {
+        const int j = (row0 + g) / a.group;
+        a.lse[(r.b + j) * (int64_t)(a.heads * a.group) + head * a.group + row0 + g - j * a.group] = sums.off + log2f(l);
       }
-      float sum = 0.0f;
-      float acc[PER] = {};
+    } else if (tq == 0) {
+      a.partial_ml[slot + g] = make_float2(sums.m, l * down);
+    }
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        const float f = ml[w].x == NEG_INF ? 0.0f : ex2(ml[w].x - top);  // a NaN sum stays one
-        sum = fmaf(ml[w].y, f, sum);
+    for (int k = 0; k < 2; ++k) {
+      const int row = 2 * tq + k;
+      const float fr = __shfl_sync(0xFFFFFFFFu, f, 4 * row);
+      const int j = (row0 + row) / a.group;
+      const int64_t at = (r.b + j) * (int64_t)(a.heads * a.group) + head * a.group + row0 + row - j * a.group;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) acc[i] = fmaf(merge[(w * ROWS + row) * D + d + i], f, acc[i]);
-      }
-      const int vr = row0 + row;
-      if (vr < r.n * a.group) {
-        if (whole) {
-          const int j = vr / a.group, hq = head * a.group + vr - j * a.group;
-          const int64_t at = (r.b + j) * (int64_t)(a.heads * a.group) + hq;
-          const float inv = 1.0f / sum;
-          T* dst = a.out + at * D + d;
-#pragma unroll
-          for (int i = 0; i < PER; ++i) acc[i] *= inv;
-          if constexpr (PER == 8) {
-            kvq_store8(dst, acc);
-          } else {
-#pragma unroll
-            for (int i = 0; i < PER; ++i) dst[i] = (T)acc[i];
-          }
-          if (a.lse && d == 0) a.lse[at] = top + log2f(sum);
-        } else {
-          float* dst = a.partial + ((int64_t)slot * ROWS + row) * D + d;
-#pragma unroll
-          for (int i = 0; i < PER; i += 4)
-            *reinterpret_cast<float4*>(dst + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
-          if (d == 0) a.partial_ml[(int64_t)slot * ROWS + row] = make_float2(top, sum);
-        }
+      for (int b = 0; b < NB; ++b) {
+        const float v[4] = {sums.o[b][0][k] * fr, sums.o[b][0][2 + k] * fr, sums.o[b][1][k] * fr,
+                            sums.o[b][1][2 + k] * fr};
+        if (!whole) store4<D>(a.partial + (slot + row) * D + 32 * b + 4 * g, v);
+        else if (row0 + row < rows) store4<D>(a.out + at * D + 32 * b + 4 * g, v);
       }
     }
     out.next(a, true);
   }
-  // a warp that gave up waits (again with a limit) for its copies in flight
-  if (dead)
-    for (; taken < issued; ++taken) mbar_wait_warp(bar_u32 + 8 * (taken % STAGES), (taken / STAGES) & 1, a.wait_ns);
 }
 
 // ---------------------------------------------------------------- join
 // One CTA per (packed row, query head): joins the partial sums of an item cut
-// between CTAs; rows of no request, or of one that is out of range, get zeros.
+// between workers; rows of no request, or of one that is out of range, get zeros.
 template <int D, typename T>
 __global__ void __launch_bounds__(THREADS) kvq_join_kernel(const Args<T> a) {
   constexpr int PER = D / 32;
@@ -718,15 +693,12 @@ __global__ void __launch_bounds__(THREADS) kvq_join_kernel(const Args<T> a) {
     if (a.lse && tid == 0) a.lse[at] = NEG_INF;
     return;
   }
-  const int64_t all = a.unit_start[a.S];
-  const int64_t need = (all + MIN_UNITS - 1) / MIN_UNITS;
-  const int64_t workers = need < a.workers ? need : a.workers;
+  const Shares share(a.unit_start[a.S], a.workers);
   const int head = hq / a.group;
   const int vr = (int)(t - r.b) * a.group + (hq - head * a.group);
   const int item = head * (r.items / a.heads) + vr / ROWS, row = vr % ROWS;
-  const int64_t u0 = a.unit_start[s] + (int64_t)item * r.tiles, u1 = u0 + r.tiles - 1;
-  // the CTA whose range holds unit u: the last w with w * all / workers <= u
-  const int wa = (int)(((u0 + 1) * workers - 1) / all), wb = (int)(((u1 + 1) * workers - 1) / all);
+  const int64_t u0 = a.unit_start[s] + (int64_t)item * r.tiles;
+  const int wa = share.of(u0), wb = share.of(u0 + r.tiles - 1);
   if (wa == wb) return;  // written by the main launch
   float top = NEG_INF;
   for (int w = wa + tid; w <= wb; w += THREADS)
@@ -781,12 +753,12 @@ __global__ void __launch_bounds__(THREADS) kvq_join_kernel(const Args<T> a) {
 template <int D, typename T>
 __global__ void __launch_bounds__(THREADS) kvq_mass_kernel(const Args<T> a) {
   using L = Kvq<D>;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int lane = threadIdx.x & 31;
   const int g = lane >> 2, tq = lane & 3;
   const Range range = plan_range(a, false, nullptr);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   Walk<T> it;
-  for (it.begin(a, range, false); it.t0 < it.t1; it.next(a, false)) {
+  for (it.begin(range); it.t0 < it.t1; it.next(a, false)) {
     const Request& r = it.r;
     const int head = it.item;
     const uint8_t* plane = a.cache + (r.slot * a.heads + head) * a.plane_bytes;
@@ -800,7 +772,7 @@ __global__ void __launch_bounds__(THREADS) kvq_mass_kernel(const Args<T> a) {
       const int j = live ? vr / a.group : 0;
       const float lse = live ? a.lse[(r.b + j) * (int64_t)(a.heads * a.group) + head * a.group + vr - j * a.group] : 0.0f;
       const int64_t last = live ? r.pos + j : -1;
-      for (int t = it.t0 + warp; t < it.t1; t += WARPS) {
+      for (int t = it.t0; t < it.t1; ++t) {
 #pragma unroll
         for (int u = 0; u < L::POS / 8; ++u) {
           const float2 sc = scores8<D>(plane + (int64_t)t * L::BYTES, q, u, g, tq);
@@ -845,22 +817,13 @@ int launch_as(const KvqStep& c, const uint8_t* cache, const void* q, const int64
   a.pos = c.pos;
   a.status = c.status;
   a.wait_ns = wait_limit_ns();
-  a.workers = c.num_sms * CTAS_PER_SM;
+  a.workers = c.num_sms * CTAS_PER_SM * WARPS;
   a.partial = ws.partial;
   a.partial_ml = ws.partial_ml;
   a.unit_start = ws.unit_start;
   a.lse = mass ? ws.lse : nullptr;
   a.mass = mass;
-  static std::atomic<bool> sized[64];  // per device: the kernel's shared memory limit is set
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return Q4_ERR_CUDA;
-  if (!sized[dev].load()) {
-    if (cudaFuncSetAttribute(kvq_attention_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Smem<D>::BYTES) != cudaSuccess)
-      return Q4_ERR_CUDA;
-    sized[dev].store(true);
-  }
-  kvq_attention_kernel<D, T><<<a.workers, THREADS, Smem<D>::BYTES, s>>>(a);
+  kvq_attention_kernel<D, T><<<c.num_sms * CTAS_PER_SM, THREADS, 0, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return Q4_ERR_CUDA;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -898,7 +861,7 @@ size_t kvq_attn_scratch_bytes(int64_t S, int64_t total, int q_heads, bool mass, 
     at += (bytes + 255) / 256 * 256;
     return o;
   };
-  const size_t segs = (size_t)2 * num_sms * CTAS_PER_SM * ROWS;
+  const size_t segs = (size_t)2 * num_sms * CTAS_PER_SM * WARPS * ROWS;
   const size_t p = take(segs * 128 * sizeof(float)), ml = take(segs * sizeof(float2));
   const size_t us = take((size_t)(S + 1) * sizeof(int64_t)), ls = take(mass ? (size_t)total * q_heads * 4 : 0);
   if (out) {

@@ -153,28 +153,61 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const KvqEvic
   }
 }
 
-// A row as pieces: 16-byte vectors of K and V codes, then the binary16 scales
-// of K and V.  Where a piece lies depends on the row's place in its tile.
+// A pair of result rows as pieces: 16-byte vectors of K codes (of either row),
+// of V codes (both rows interleaved) and the scale words of K and V (likewise).
 template <int D>
-struct RowPieces {
+struct PairPieces {
   using L = Kvq<D>;
-  static constexpr int CV = D / 32;          // code vectors per K or V row
-  static constexpr int VECS = 2 * CV;
-  static constexpr int PIECES = VECS + 2 * L::NB;
-  __device__ static uint8_t* vec(uint8_t* plane, int64_t p, int v) {
-    const int cr = kvq_row((int)(p % L::POS));
-    uint8_t* tile = plane + p / L::POS * L::BYTES;
-    return v < CV ? tile + cr * L::ROW + v * 16 : tile + L::V_OFF + cr * L::ROW + kvq_v_vec<D>(cr, v - CV);
+  static constexpr int CV = D / 32;          // K code vectors per row
+  static constexpr int VV = D / 16;          // V code vectors per pair
+  static constexpr int PIECES = 2 * CV + VV + 2 * L::NB;
+  __device__ static uint8_t* tile(uint8_t* plane, int64_t p) { return plane + p / L::POS * L::BYTES; }
+  // halves (two binary16s' worth) of a and b that positions p0 and p1 own, as one word
+  __device__ static uint32_t join(uint32_t a, int64_t p0, uint32_t b, int64_t p1) {
+    return __byte_perm(a, b, ((p0 & 1) ? 0x32 : 0x10) | ((p1 & 1) ? 0x7600 : 0x5400));
   }
-  __device__ static uint16_t* scale(uint8_t* plane, int64_t p, int i) {
-    return reinterpret_cast<uint16_t*>(plane + p / L::POS * L::BYTES +
-                                       kvq_scale<D>(i / L::NB, (int)(p % L::POS), i % L::NB));
+  // piece e of the pair whose rows are positions p0 and p1 of `src`
+  __device__ static uint4 read(uint8_t* src, int64_t p0, int64_t p1, int e) {
+    if (e < 2 * CV) {
+      const int64_t p = e < CV ? p0 : p1;
+      return *reinterpret_cast<const uint4*>(tile(src, p) + kvq_row((int)(p % L::POS)) * L::ROW + (e % CV) * 16);
+    }
+    e -= 2 * CV;
+    if (e < VV) {
+      uint4 a = *vec(src, p0, e);
+      const uint4 b = *vec(src, p1, e);
+      a.x = join(a.x, p0, b.x, p1);
+      a.y = join(a.y, p0, b.y, p1);
+      a.z = join(a.z, p0, b.z, p1);
+      a.w = join(a.w, p0, b.w, p1);
+      return a;
+    }
+    e -= VV;
+    return make_uint4(join(*scale(src, p0, e), p0, *scale(src, p1, e), p1), 0u, 0u, 0u);
+  }
+  __device__ static void write(uint8_t* dst, int64_t p, int e, const uint4& v) {  // p even
+    if (e < 2 * CV) {
+      p += e < CV ? 0 : 1;
+      *reinterpret_cast<uint4*>(tile(dst, p) + kvq_row((int)(p % L::POS)) * L::ROW + (e % CV) * 16) = v;
+      return;
+    }
+    e -= 2 * CV;
+    if (e < VV) *vec(dst, p, e) = v;
+    else *scale(dst, p, e - VV) = v.x;
+  }
+  // vector e of a pair row: groups of NB words, in the order that the row's swizzle gives them
+  __device__ static uint4* vec(uint8_t* plane, int64_t p, int e) {
+    constexpr int PER = 4 / L::NB;  // groups per vector
+    return reinterpret_cast<uint4*>(tile(plane, p) + kvq_v_group<D>((int)(p % L::POS), e * PER));
+  }
+  __device__ static uint32_t* scale(uint8_t* plane, int64_t p, int i) {
+    return reinterpret_cast<uint32_t*>(tile(plane, p) + kvq_scale<D>(i / L::NB, (int)(p % L::POS) & ~1, i % L::NB));
   }
 };
 
 template <int D>
 __global__ void __launch_bounds__(MOVE_THREADS) evict_move_kernel(const KvqEvict a, int64_t plane_bytes) {
-  using R = RowPieces<D>;
+  using R = PairPieces<D>;
   const int s = blockIdx.y / (int)a.heads, h = blockIdx.y % (int)a.heads;
   const int n = a.new_len[s];
   if (n <= 0) return;
@@ -184,7 +217,7 @@ __global__ void __launch_bounds__(MOVE_THREADS) evict_move_kernel(const KvqEvict
   uint8_t* src = a.cache + (src_slot * a.heads + h) * plane_bytes;
   uint8_t* dst = a.cache + (dst_slot * a.heads + h) * plane_bytes;
   const int32_t* kept = a.kept + (int64_t)blockIdx.y * a.keep;
-  const int items = n * R::PIECES;  // below 2^31: checked on the host
+  const int items = (n + 1) / 2 * R::PIECES;  // below 2^31: checked on the host
   constexpr int STEP = MOVE_THREADS * MOVE_VEC;
   const int first = in_place ? 0 : blockIdx.x * STEP, stride = in_place ? STEP : gridDim.x * STEP;
   for (int i0 = first; i0 < items; i0 += stride) {
@@ -193,10 +226,10 @@ __global__ void __launch_bounds__(MOVE_THREADS) evict_move_kernel(const KvqEvict
     for (int u = 0; u < MOVE_VEC; ++u) {
       const int it = i0 + u * MOVE_THREADS + threadIdx.x;
       if (it < items) {
-        const int row = it / R::PIECES, e = it - row * R::PIECES;
-        const int64_t p = kept[row];
-        if (e < R::VECS) v[u] = *reinterpret_cast<const uint4*>(R::vec(src, p, e));
-        else v[u].x = *R::scale(src, p, e - R::VECS);
+        const int pair = it / R::PIECES, e = it - pair * R::PIECES;
+        const int p0 = kept[2 * pair];
+        const int p1 = 2 * pair + 1 < n ? kept[2 * pair + 1] : p0;  // a last odd row: its neighbour is never used
+        v[u] = R::read(src, p0, p1, e);
       }
     }
     if (in_place) __syncthreads();  // the step is read before it is written; later steps read from further on
@@ -204,9 +237,8 @@ __global__ void __launch_bounds__(MOVE_THREADS) evict_move_kernel(const KvqEvict
     for (int u = 0; u < MOVE_VEC; ++u) {
       const int it = i0 + u * MOVE_THREADS + threadIdx.x;
       if (it < items) {
-        const int row = it / R::PIECES, e = it - row * R::PIECES;
-        if (e < R::VECS) *reinterpret_cast<uint4*>(R::vec(dst, row, e)) = v[u];
-        else *R::scale(dst, row, e - R::VECS) = (uint16_t)v[u].x;
+        const int pair = it / R::PIECES;
+        R::write(dst, 2 * (int64_t)pair, it - pair * R::PIECES, v[u]);
       }
     }
   }
@@ -218,7 +250,7 @@ int launch_kvq_evict(const KvqEvict& c, cudaStream_t s) {
   const int64_t planes = (int64_t)c.S * c.heads;
   evict_select_kernel<<<(unsigned)planes, SEL_THREADS, 0, s>>>(c);
   if (cudaGetLastError() != cudaSuccess) return Q4_ERR_CUDA;
-  const int64_t items = (int64_t)c.keep * (4 * (c.head_dim / 32));
+  const int64_t items = (int64_t)((c.keep + 1) / 2) * (6 * (c.head_dim / 32));
   const int64_t steps = (items + MOVE_THREADS * MOVE_VEC - 1) / (MOVE_THREADS * MOVE_VEC);
   int64_t gx = ((int64_t)c.num_sms * 8 + planes - 1) / planes;
   if (gx > steps) gx = steps;
