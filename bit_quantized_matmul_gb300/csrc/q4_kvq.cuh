@@ -1,10 +1,10 @@
 // q4_kvq.cuh — device layout of the 4-bit KV cache and the small helpers its
 // kernels share (not part of the public ABI).
 //
-// Layout.  A (slot, head) plane is a run of 2,304-byte tiles of POS positions
-// (16 at D = 128, 32 at D = 64); a tile holds, one after another,
-//   K codes   POS rows of D/2 bytes      K scales  POS x D/32 binary16
-//   V codes   POS rows of D/2 bytes      V scales  POS x D/32 binary16
+// Layout.  A (slot, head) plane is a run of tiles of 32 positions (4,608 bytes
+// at D = 128, 2,304 at D = 64); a tile holds, one after another,
+//   K codes   32 rows of D/2 bytes      K scales  32 x D/32 binary16
+//   V codes   32 rows of D/2 bytes      V scales  32 x D/32 binary16
 // so a warp fetches one tile with one bulk copy, and the K half alone is one
 // copy too.  Codes are the nibbles q = 0..15 of the Q4_0 rule; block b of a
 // row (32 values) is four words, word j holding values 8j .. 8j+7 from the low
@@ -12,17 +12,14 @@
 //
 // K row: word j of block b sits at byte j*4*NB + 4b (NB = D/32).  In an
 // m16n8k16 product with keys along n, lane 4g + tq feeds key g with the words
-// j = tq, which are then contiguous (16 bytes at D = 128).  Which value sits
-// at which k index does not matter as long as the query fragment agrees.
-// Position r is stored as K row r with its low three bits in Gray code: the rows
-// that a group of lanes reads together then fall into different shared-memory
-// banks.
-// V: positions 2i and 2i + 1 share a pair row of D bytes.  Half-word g (values
-// 4g .. 4g+3 of a block) of block b is word g*NB + b of the pair row, the even
-// position in its low and the odd one in its high half, so lane (g, tq) of the
-// P V product, with values along m and keys along k, reads the two keys of a
-// register as contiguous words (16 bytes at D = 128); these groups of NB words
-// are stored with index ^ 2 (i % 4), again for the banks.
+// j = tq, which are then contiguous; the lanes of a warp read the rows of
+// eight keys in address order.  Which value sits at which k index does not
+// matter as long as the query fragment agrees.
+// V: half-word g (values 4g .. 4g+3 of a block) of block b of two neighbouring
+// positions is one word, the even position in its low half, and the words of
+// eight positions are stored as [g][pair][b]: lane (g, tq) of the P V product,
+// with values along m and keys along k, reads the two keys 2 tq, 2 tq + 1 of
+// each register ready made, and the warp again reads in address order.
 // Scales are stored by pairs of positions too: [r / 2][block][r % 2].
 #pragma once
 
@@ -36,29 +33,25 @@ namespace q4 {
 template <int D>
 struct Kvq {
   static constexpr int NB = D / 32;                       // blocks (scales) per row
-  static constexpr int POS = kvq_tile_positions(D);       // positions per tile
+  static constexpr int POS = KVQ_POS;                     // positions per tile
   static constexpr int ROW = D / 2;                       // code bytes per row
   static constexpr int SCL = 2 * NB;                      // scale bytes per row
   static constexpr int KS_OFF = POS * ROW;                // K scales
   static constexpr int V_OFF = KS_OFF + POS * SCL;        // V codes (= bytes of the K half)
   static constexpr int VS_OFF = V_OFF + POS * ROW;        // V scales
   static constexpr int BYTES = VS_OFF + POS * SCL;        // one tile
-  static_assert(BYTES == KVQ_TILE_BYTES, "tile size");
 };
-
-// The code row of position r of a tile.
-__host__ __device__ constexpr int kvq_row(int r) { return (r & ~7) | ((r & 7) ^ ((r & 7) >> 1)); }
 
 // Byte offset in a tile of word j (values 8j .. 8j+7) of block b of position r's K.
 template <int D>
 __device__ __forceinline__ int kvq_k_word(int r, int b, int j) {
-  return kvq_row(r) * Kvq<D>::ROW + (j * Kvq<D>::NB + b) * 4;
+  return r * Kvq<D>::ROW + (j * Kvq<D>::NB + b) * 4;
 }
 
-// Byte offset in a tile of the words of group g of the pair row of positions r and r ^ 1.
+// Byte offset in a tile of the words of group g of positions r and r ^ 1.
 template <int D>
-__host__ __device__ constexpr int kvq_v_group(int r, int g) {
-  return Kvq<D>::V_OFF + (r >> 1) * D + (g ^ (r & 6)) * Kvq<D>::NB * 4;
+__device__ __forceinline__ int kvq_v_group(int r, int g) {
+  return Kvq<D>::V_OFF + (r >> 3) * 8 * Kvq<D>::ROW + (4 * g + ((r >> 1) & 3)) * Kvq<D>::NB * 4;
 }
 
 // Byte offset in a tile of half-word g (values 4g .. 4g+3) of block b of position r's V.

@@ -31,12 +31,14 @@
 // that they fit binary16.  Values lie along m and virtual rows along n, and hi
 // and lo go into one accumulator.
 //
-// Work.  A unit is one cache tile (2,304 bytes) of one item (request, head,
+// Work.  A unit is one cache tile (32 positions) of one item (request, head,
 // eight virtual rows).  The launch's warps take equal, contiguous ranges of
 // units whatever the lengths are (each CTA sums the lengths itself, so the
 // host needs none of them), each through its own ring of bulk copies; after
 // the plan no warp waits for another.  Items cut between warps leave
 // (reference score, sum, o) in scratch and a second launch joins them.
+#include <atomic>
+
 #include "q4_kvq.cuh"
 #include "q4_ptx.cuh"
 
@@ -47,7 +49,8 @@ constexpr int WARPS = 4;
 constexpr int THREADS = 32 * WARPS;
 constexpr int ROWS = 8;               // virtual rows of an item
 constexpr int CTAS_PER_SM = 3;
-constexpr int STAGES = 4;             // tiles in flight per warp
+constexpr int STAGES = 3;             // tiles in flight per warp
+constexpr int ITEM_UNITS = 2;         // what beginning an item costs, in tiles: its queries, its sums' end
 constexpr float NEG_INF = -INFINITY;
 constexpr float SLACK = 5.0f;         // log2 of how far a weight may pass 1 before the sums are rescaled
 
@@ -60,7 +63,6 @@ struct Args {
   float scale_log2;         // scale * log2(e)
   int64_t slots, capacity, plane_bytes, total;
   int heads, group, S;
-  int tile;                 // positions per cache tile
   const int32_t *offsets, *slot, *pos;
   unsigned* status;
   unsigned long long wait_ns;
@@ -151,21 +153,24 @@ __device__ __forceinline__ void unpack_centred(uint32_t w, uint32_t (&r)[4]) {
 
 // ---------------------------------------------------------------- work ranges
 struct Request {
-  int64_t b, pos, slot;
+  int b, pos, slot;
   int n, tiles, items;  // rows, cache tiles, items (heads x row groups); 0 tiles: nothing to do
+  // an item counts as some units more than its tiles: the first ones stand for its beginning
+  __device__ __forceinline__ int span() const { return tiles ? tiles + ITEM_UNITS : 0; }
+  __device__ __forceinline__ int64_t units() const { return (int64_t)span() * items; }
 };
 
 template <typename T>
 __device__ __forceinline__ Request load_request(const Args<T>& a, int s, bool by_rows, bool* bad = nullptr) {
   const KvqRequest q = kvq_request(a.offsets, a.slot, a.pos, s);
-  Request r{q.b, q.pos, q.slot, 0, 0, 0};
+  Request r{(int)q.b, (int)q.pos, (int)q.slot, 0, 0, 0};
   if (!q.ok(a.total, a.slots, a.capacity)) {
     if (bad) *bad = q.e > q.b;
     return r;
   }
   r.n = (int)(q.e - q.b);
   if (r.n == 0) return r;
-  r.tiles = (int)((q.pos + r.n + a.tile - 1) / a.tile);
+  r.tiles = (r.pos + r.n + KVQ_POS - 1) / KVQ_POS;
   r.items = a.heads * (by_rows ? (r.n * a.group + ROWS - 1) / ROWS : 1);
   return r;
 }
@@ -197,8 +202,8 @@ struct Shares {
 
 // A worker's range of units.
 struct Range {
-  int64_t left;  // units to do
-  int s, item, tile;
+  int64_t left;       // units to do
+  int s, item, unit;  // from this unit of the item on
   Request r;
 };
 
@@ -219,7 +224,7 @@ __device__ __forceinline__ Range plan_range(const Args<T>& a, bool by_rows, int6
     bool bad = false;
     r = load_request(a, s, by_rows, &bad);
     any_bad |= bad;
-    mine += (int64_t)r.tiles * r.items;
+    mine += r.units();
   }
   if (any_bad && blockIdx.x == 0) atomicOr(a.status, STATUS_KV_RANGE);
   int64_t incl = mine;
@@ -243,7 +248,7 @@ __device__ __forceinline__ Range plan_range(const Args<T>& a, bool by_rows, int6
 #pragma unroll 1
   for (int s = s0; s < s1; ++s) {
     if (chunk > 1) r = load_request(a, s, by_rows);
-    const int64_t units = (int64_t)r.tiles * r.items;
+    const int64_t units = r.units();
     if (note) unit_start[s] = start;
 #pragma unroll 1
     for (int w = 0; w < WARPS; ++w) {
@@ -252,8 +257,8 @@ __device__ __forceinline__ Range plan_range(const Args<T>& a, bool by_rows, int6
       const int64_t u0 = share.start(worker);
       if (u0 < start || u0 >= start + units) continue;
       const int64_t in = u0 - start;
-      const int item = in < (int64_t)1 << 31 ? (int)in / r.tiles : (int)(in / r.tiles);
-      found[w] = Range{share.start(worker + 1) - u0, s, item, (int)(in - (int64_t)item * r.tiles), r};
+      const int item = in < (int64_t)1 << 31 ? (int)in / r.span() : (int)(in / r.span());
+      found[w] = Range{share.start(worker + 1) - u0, s, item, (int)(in - (int64_t)item * r.span()), r};
     }
     start += units;
   }
@@ -266,37 +271,39 @@ __device__ __forceinline__ Range plan_range(const Args<T>& a, bool by_rows, int6
 template <typename T>
 struct Walk {
   int64_t left;
-  int s, item, t0, t1;  // the segment: tiles [t0, t1) of the item
+  int s, item, t0, t1;  // the segment: tiles [t0, t1) of the item; t0 == t1 when none is left
   Request r;
-  __device__ __forceinline__ void begin(const Range& g) {
+  __device__ __forceinline__ void begin(const Args<T>& a, const Range& g, bool by_rows) {
     left = g.left;
     s = g.s;
     item = g.item;
-    t0 = t1 = g.tile;
     r = g.r;
-    if (left > 0) cut();
+    t0 = t1 = 0;
+    if (left > 0 && !cut(g.unit)) next(a, by_rows);
   }
-  __device__ __forceinline__ void cut() {
-    const int64_t end = t0 + left;
-    t1 = end < r.tiles ? (int)end : r.tiles;
-    left -= t1 - t0;
+  // the segment from unit u of the item on; false when no tile is in it
+  __device__ __forceinline__ bool cut(int u) {
+    const int end = (int)min(u + left, (int64_t)r.span());
+    left -= end - u;
+    t0 = max(u - ITEM_UNITS, 0);
+    t1 = max(end - ITEM_UNITS, 0);
+    return t0 < t1;
   }
-  // the next segment; t0 == t1 when none is left
   __device__ __forceinline__ void next(const Args<T>& a, bool by_rows) {
-    t0 = 0;
-    t1 = 0;
-    if (left <= 0) return;
-    if (++item >= r.items) {
-      item = 0;
-      do {
-        if (++s >= a.S) {
-          left = 0;
-          return;
-        }
-        r = load_request(a, s, by_rows);
-      } while (r.tiles == 0);
-    }
-    cut();
+    do {
+      t0 = t1 = 0;
+      if (left <= 0) return;
+      if (++item >= r.items) {
+        item = 0;
+        do {
+          if (++s >= a.S) {
+            left = 0;
+            return;
+          }
+          r = load_request(a, s, by_rows);
+        } while (r.tiles == 0);
+      }
+    } while (!cut(0));
   }
 };
 
@@ -324,7 +331,7 @@ __device__ __forceinline__ void load_query(Query<D>& f, const Args<T>& a, const 
   float top = 0.0f;
   if (vr < r.n * a.group) {
     const int j = vr / a.group, hg = vr - j * a.group;
-    const T* p = a.q + (r.b + j) * a.q_token + (int64_t)(head * a.group + hg) * a.q_head + 8 * tq;
+    const T* p = a.q + (int64_t)(r.b + j) * a.q_token + (int64_t)(head * a.group + hg) * a.q_head + 8 * tq;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       kvq_load8(p + 32 * b, x[b]);
@@ -401,7 +408,7 @@ template <int D>
 __device__ __forceinline__ float2 scores8(const uint8_t* tile, const Query<D>& q, int t, int g, int tq) {
   constexpr int NB = Kvq<D>::NB;
   uint32_t w[NB], d[NB];
-  load_words<NB>(tile + (8 * t + kvq_row(g)) * Kvq<D>::ROW + tq * 4 * NB, w);
+  load_words<NB>(tile + 8 * t * Kvq<D>::ROW + (4 * g + tq) * 4 * NB, w);
   load_scales<D>(tile + Kvq<D>::KS_OFF, t, tq, d);
   F2 s = f2(0.0f, 0.0f);
 #pragma unroll
@@ -513,7 +520,7 @@ __device__ __forceinline__ void step16(const uint8_t* tile, int half, int p0, co
   // V words of this lane's keys 2 tq, 2 tq + 1 (u = 0) and + 8 (u = 1)
   uint32_t vw[2][NB];
 #pragma unroll
-  for (int u = 0; u < 2; ++u) load_words<NB>(tile + kvq_v_group<D>(16 * half + 8 * u + 2 * tq, g), vw[u]);
+  for (int u = 0; u < 2; ++u) load_words<NB>(tile + L::V_OFF + (16 * half + 8 * u) * L::ROW + (4 * g + tq) * 4 * NB, vw[u]);
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     // weights times the block's V scales, as hi and lo terms: B operand with keys along k
@@ -556,11 +563,12 @@ template <int D, typename T>
 __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kvq_attention_kernel(const Args<T> a) {
   using L = Kvq<D>;
   constexpr int NB = L::NB;
-  __shared__ __align__(128) uint8_t rings[WARPS][STAGES][L::BYTES];
+  extern __shared__ __align__(128) uint8_t smem[];  // a ring per warp
   __shared__ uint64_t bars[WARPS][STAGES];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, tq = lane & 3;
-  const uint32_t ring_u32 = smem_u32(rings[warp]), bar_u32 = smem_u32(bars[warp]);
+  const uint8_t* ring = smem + warp * STAGES * L::BYTES;
+  const uint32_t ring_u32 = smem_u32(ring), bar_u32 = smem_u32(bars[warp]);
   if (lane < STAGES) mbar_init(bar_u32 + 8 * lane, 1);
   mbar_init_fence();
   __syncwarp();
@@ -571,14 +579,14 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kvq_attention_kernel(con
   Walk<T> in, out;
   {
     const Range range = plan_range(a, true, a.unit_start);
-    in.begin(range);
-    out.begin(range);
+    in.begin(a, range, true);
+    out.begin(a, range, true);
   }
   const uint8_t* in_ptr = nullptr;  // the next tile of the issue cursor's segment
   int in_left = 0;                  // and how many are left of it
   auto enter = [&]() {
     const int head = in.item / (in.r.items / a.heads);
-    in_ptr = a.cache + (in.r.slot * a.heads + head) * a.plane_bytes + (int64_t)in.t0 * L::BYTES;
+    in_ptr = a.cache + ((int64_t)in.r.slot * a.heads + head) * a.plane_bytes + (int64_t)in.t0 * L::BYTES;
     in_left = in.t1 - in.t0;
   };
   if (in.t0 < in.t1) enter();
@@ -610,9 +618,9 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kvq_attention_kernel(con
     load_query<D, T>(q, a, r, head, row0, lane);
     Sums<D> sums;
     sums.clear();
-    const int last = (int)r.pos + (row0 + g) / a.group;  // the row's last visible position
-    const int clear = (int)r.pos + row0 / a.group + 1;   // positions below are visible to every row
-    const int end = (int)r.pos + r.n;                    // positions from here on hold anything
+    const int last = r.pos + (row0 + g) / a.group;  // the row's last visible position
+    const int clear = r.pos + row0 / a.group + 1;   // positions below are visible to every row
+    const int end = r.pos + r.n;                    // positions from here on hold anything
 
     for (int t = out.t0; t < out.t1; ++t) {
       const unsigned st = taken % STAGES;
@@ -624,7 +632,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kvq_attention_kernel(con
         return;
       }
       ++taken;
-      const uint8_t* tile = rings[warp][st];
+      const uint8_t* tile = ring + st * L::BYTES;
 #pragma unroll
       for (int half = 0; half < L::POS / 16; ++half) {
         const int p0 = t * L::POS + 16 * half;
@@ -649,7 +657,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kvq_attention_kernel(con
     if (whole) {
       if (a.lse && tq == 0 && row0 + g < rows) {
         const int j = (row0 + g) / a.group;
-        a.lse[(r.b + j) * (int64_t)(a.heads * a.group) + head * a.group + row0 + g - j * a.group] = sums.off + log2f(l);
+        a.lse[(int64_t)(r.b + j) * (a.heads * a.group) + head * a.group + row0 + g - j * a.group] = sums.off + log2f(l);
       }
     } else if (tq == 0) {
       a.partial_ml[slot + g] = make_float2(sums.m, l * down);
@@ -659,7 +667,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kvq_attention_kernel(con
       const int row = 2 * tq + k;
       const float fr = __shfl_sync(0xFFFFFFFFu, f, 4 * row);
       const int j = (row0 + row) / a.group;
-      const int64_t at = (r.b + j) * (int64_t)(a.heads * a.group) + head * a.group + row0 + row - j * a.group;
+      const int64_t at = (int64_t)(r.b + j) * (a.heads * a.group) + head * a.group + row0 + row - j * a.group;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const float v[4] = {sums.o[b][0][k] * fr, sums.o[b][0][2 + k] * fr, sums.o[b][1][k] * fr,
@@ -681,10 +689,9 @@ __global__ void __launch_bounds__(THREADS) kvq_join_kernel(const Args<T> a) {
   __shared__ float s_sum[WARPS], s_top[WARPS];
   __shared__ float s_acc[WARPS][D];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t t = blockIdx.x;
-  const int hq = blockIdx.y;
+  const int t = blockIdx.x, hq = blockIdx.y;
   const int hq_all = a.heads * a.group;
-  const int64_t at = t * hq_all + hq;
+  const int64_t at = (int64_t)t * hq_all + hq;
   const int s = kvq_find_request(a.offsets, a.S, t);
   const Request r = load_request(a, s, true);
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -695,9 +702,9 @@ __global__ void __launch_bounds__(THREADS) kvq_join_kernel(const Args<T> a) {
   }
   const Shares share(a.unit_start[a.S], a.workers);
   const int head = hq / a.group;
-  const int vr = (int)(t - r.b) * a.group + (hq - head * a.group);
+  const int vr = (t - r.b) * a.group + (hq - head * a.group);
   const int item = head * (r.items / a.heads) + vr / ROWS, row = vr % ROWS;
-  const int64_t u0 = a.unit_start[s] + (int64_t)item * r.tiles;
+  const int64_t u0 = a.unit_start[s] + (int64_t)item * r.span() + ITEM_UNITS;  // the first tile
   const int wa = share.of(u0), wb = share.of(u0 + r.tiles - 1);
   if (wa == wb) return;  // written by the main launch
   float top = NEG_INF;
@@ -758,11 +765,11 @@ __global__ void __launch_bounds__(THREADS) kvq_mass_kernel(const Args<T> a) {
   const Range range = plan_range(a, false, nullptr);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   Walk<T> it;
-  for (it.begin(range); it.t0 < it.t1; it.next(a, false)) {
+  for (it.begin(a, range, false); it.t0 < it.t1; it.next(a, false)) {
     const Request& r = it.r;
     const int head = it.item;
-    const uint8_t* plane = a.cache + (r.slot * a.heads + head) * a.plane_bytes;
-    float* mass = a.mass + (r.slot * a.heads + head) * a.capacity;
+    const uint8_t* plane = a.cache + ((int64_t)r.slot * a.heads + head) * a.plane_bytes;
+    float* mass = a.mass + ((int64_t)r.slot * a.heads + head) * a.capacity;
     const int rows = r.n * a.group;
     for (int row0 = 0; row0 < rows; row0 += ROWS) {
       Query<D> q;
@@ -770,7 +777,7 @@ __global__ void __launch_bounds__(THREADS) kvq_mass_kernel(const Args<T> a) {
       const int vr = row0 + g;
       const bool live = vr < rows;
       const int j = live ? vr / a.group : 0;
-      const float lse = live ? a.lse[(r.b + j) * (int64_t)(a.heads * a.group) + head * a.group + vr - j * a.group] : 0.0f;
+      const float lse = live ? a.lse[(int64_t)(r.b + j) * (a.heads * a.group) + head * a.group + vr - j * a.group] : 0.0f;
       const int64_t last = live ? r.pos + j : -1;
       for (int t = it.t0; t < it.t1; ++t) {
 #pragma unroll
@@ -811,7 +818,6 @@ int launch_as(const KvqStep& c, const uint8_t* cache, const void* q, const int64
   a.heads = (int)c.heads;
   a.group = q_heads / (int)c.heads;
   a.S = c.S;
-  a.tile = Kvq<D>::POS;
   a.offsets = c.offsets;
   a.slot = c.slot;
   a.pos = c.pos;
@@ -823,7 +829,17 @@ int launch_as(const KvqStep& c, const uint8_t* cache, const void* q, const int64
   a.unit_start = ws.unit_start;
   a.lse = mass ? ws.lse : nullptr;
   a.mass = mass;
-  kvq_attention_kernel<D, T><<<c.num_sms * CTAS_PER_SM, THREADS, 0, s>>>(a);
+  constexpr int SMEM = WARPS * STAGES * Kvq<D>::BYTES;
+  static std::atomic<bool> sized[64];  // per device: the kernel's shared memory limit is set
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return Q4_ERR_CUDA;
+  if (!sized[dev].load()) {
+    if (cudaFuncSetAttribute(kvq_attention_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) !=
+        cudaSuccess)
+      return Q4_ERR_CUDA;
+    sized[dev].store(true);
+  }
+  kvq_attention_kernel<D, T><<<c.num_sms * CTAS_PER_SM, THREADS, SMEM, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return Q4_ERR_CUDA;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

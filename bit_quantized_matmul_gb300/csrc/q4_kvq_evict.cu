@@ -20,7 +20,7 @@ namespace {
 constexpr int SEL_THREADS = 512;
 constexpr int SEL_WARPS = SEL_THREADS / 32;
 constexpr int MOVE_THREADS = 256;
-constexpr int MOVE_VEC = 4;  // 16-byte vectors per thread and step
+constexpr int MOVE_VEC = 4;  // pieces per thread and step
 
 // A request whose slots, length and neighbours allow it.
 __device__ bool evict_ok(const KvqEvict& a, int s) {
@@ -154,54 +154,56 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const KvqEvic
 }
 
 // A pair of result rows as pieces: 16-byte vectors of K codes (of either row),
-// of V codes (both rows interleaved) and the scale words of K and V (likewise).
+// the V word groups (both rows interleaved) and the scale words of K and V
+// (likewise).
 template <int D>
 struct PairPieces {
   using L = Kvq<D>;
+  static constexpr int NB = L::NB;
   static constexpr int CV = D / 32;          // K code vectors per row
-  static constexpr int VV = D / 16;          // V code vectors per pair
-  static constexpr int PIECES = 2 * CV + VV + 2 * L::NB;
+  static constexpr int PIECES = 2 * CV + 8 + 2;
+  struct Piece {
+    uint32_t w[4];
+  };
   __device__ static uint8_t* tile(uint8_t* plane, int64_t p) { return plane + p / L::POS * L::BYTES; }
-  // halves (two binary16s' worth) of a and b that positions p0 and p1 own, as one word
-  __device__ static uint32_t join(uint32_t a, int64_t p0, uint32_t b, int64_t p1) {
-    return __byte_perm(a, b, ((p0 & 1) ? 0x32 : 0x10) | ((p1 & 1) ? 0x7600 : 0x5400));
+  __device__ static uint4* k_vec(uint8_t* plane, int64_t p, int e) {
+    return reinterpret_cast<uint4*>(tile(plane, p) + (int)(p % L::POS) * L::ROW + e * 16);
+  }
+  // NB words of positions p and p ^ 1: V's group e, or the scales of K (8) or V (9)
+  __device__ static uint32_t* words(uint8_t* plane, int64_t p, int e) {
+    const int r = (int)(p % L::POS);
+    return reinterpret_cast<uint32_t*>(tile(plane, p) +
+                                       (e < 8 ? kvq_v_group<D>(r, e) : kvq_scale<D>(e - 8, r & ~1, 0)));
+  }
+  __device__ static Piece load(const uint32_t* p) {
+    Piece v;
+    if constexpr (NB == 4) *reinterpret_cast<uint4*>(v.w) = *reinterpret_cast<const uint4*>(p);
+    else *reinterpret_cast<uint2*>(v.w) = *reinterpret_cast<const uint2*>(p);
+    return v;
   }
   // piece e of the pair whose rows are positions p0 and p1 of `src`
-  __device__ static uint4 read(uint8_t* src, int64_t p0, int64_t p1, int e) {
+  __device__ static Piece read(uint8_t* src, int64_t p0, int64_t p1, int e) {
+    Piece v;
     if (e < 2 * CV) {
-      const int64_t p = e < CV ? p0 : p1;
-      return *reinterpret_cast<const uint4*>(tile(src, p) + kvq_row((int)(p % L::POS)) * L::ROW + (e % CV) * 16);
+      *reinterpret_cast<uint4*>(v.w) = *k_vec(src, e < CV ? p0 : p1, e % CV);
+      return v;
     }
-    e -= 2 * CV;
-    if (e < VV) {
-      uint4 a = *vec(src, p0, e);
-      const uint4 b = *vec(src, p1, e);
-      a.x = join(a.x, p0, b.x, p1);
-      a.y = join(a.y, p0, b.y, p1);
-      a.z = join(a.z, p0, b.z, p1);
-      a.w = join(a.w, p0, b.w, p1);
-      return a;
-    }
-    e -= VV;
-    return make_uint4(join(*scale(src, p0, e), p0, *scale(src, p1, e), p1), 0u, 0u, 0u);
+    v = load(words(src, p0, e - 2 * CV));
+    const Piece b = load(words(src, p1, e - 2 * CV));
+    // the half of each word that the position owns
+    const unsigned sel = ((p0 & 1) ? 0x32u : 0x10u) | ((p1 & 1) ? 0x7600u : 0x5400u);
+#pragma unroll
+    for (int i = 0; i < NB; ++i) v.w[i] = __byte_perm(v.w[i], b.w[i], sel);
+    return v;
   }
-  __device__ static void write(uint8_t* dst, int64_t p, int e, const uint4& v) {  // p even
+  __device__ static void write(uint8_t* dst, int64_t p, int e, const Piece& v) {  // p even
     if (e < 2 * CV) {
-      p += e < CV ? 0 : 1;
-      *reinterpret_cast<uint4*>(tile(dst, p) + kvq_row((int)(p % L::POS)) * L::ROW + (e % CV) * 16) = v;
+      *k_vec(dst, p + (e < CV ? 0 : 1), e % CV) = *reinterpret_cast<const uint4*>(v.w);
       return;
     }
-    e -= 2 * CV;
-    if (e < VV) *vec(dst, p, e) = v;
-    else *scale(dst, p, e - VV) = v.x;
-  }
-  // vector e of a pair row: groups of NB words, in the order that the row's swizzle gives them
-  __device__ static uint4* vec(uint8_t* plane, int64_t p, int e) {
-    constexpr int PER = 4 / L::NB;  // groups per vector
-    return reinterpret_cast<uint4*>(tile(plane, p) + kvq_v_group<D>((int)(p % L::POS), e * PER));
-  }
-  __device__ static uint32_t* scale(uint8_t* plane, int64_t p, int i) {
-    return reinterpret_cast<uint32_t*>(tile(plane, p) + kvq_scale<D>(i / L::NB, (int)(p % L::POS) & ~1, i % L::NB));
+    uint32_t* q = words(dst, p, e - 2 * CV);
+    if constexpr (NB == 4) *reinterpret_cast<uint4*>(q) = *reinterpret_cast<const uint4*>(v.w);
+    else *reinterpret_cast<uint2*>(q) = *reinterpret_cast<const uint2*>(v.w);
   }
 };
 
@@ -221,7 +223,7 @@ __global__ void __launch_bounds__(MOVE_THREADS) evict_move_kernel(const KvqEvict
   constexpr int STEP = MOVE_THREADS * MOVE_VEC;
   const int first = in_place ? 0 : blockIdx.x * STEP, stride = in_place ? STEP : gridDim.x * STEP;
   for (int i0 = first; i0 < items; i0 += stride) {
-    uint4 v[MOVE_VEC];
+    typename R::Piece v[MOVE_VEC];
 #pragma unroll
     for (int u = 0; u < MOVE_VEC; ++u) {
       const int it = i0 + u * MOVE_THREADS + threadIdx.x;
@@ -250,7 +252,7 @@ int launch_kvq_evict(const KvqEvict& c, cudaStream_t s) {
   const int64_t planes = (int64_t)c.S * c.heads;
   evict_select_kernel<<<(unsigned)planes, SEL_THREADS, 0, s>>>(c);
   if (cudaGetLastError() != cudaSuccess) return Q4_ERR_CUDA;
-  const int64_t items = (int64_t)((c.keep + 1) / 2) * (6 * (c.head_dim / 32));
+  const int64_t items = (int64_t)((c.keep + 1) / 2) * (2 * (c.head_dim / 32) + 10);
   const int64_t steps = (items + MOVE_THREADS * MOVE_VEC - 1) / (MOVE_THREADS * MOVE_VEC);
   int64_t gx = ((int64_t)c.num_sms * 8 + planes - 1) / planes;
   if (gx > steps) gx = steps;

@@ -163,11 +163,9 @@ int launch_kv_append(uint8_t* k_cache, uint8_t* v_cache, const uint8_t* k_new, c
                      int num_sms, cudaStream_t s);
 
 // ---- 4-bit KV cache (layout in q4_kvq.cuh) ----
-constexpr int KVQ_TILE_BYTES = 2304;
-__host__ __device__ constexpr int kvq_tile_positions(int64_t head_dim) { return (int)(2048 / head_dim); }
+constexpr int KVQ_POS = 32;  // positions per tile
 inline int64_t kvq_plane_bytes(int64_t head_dim, int64_t capacity) {
-  const int64_t n = kvq_tile_positions(head_dim);
-  return (capacity + n - 1) / n * KVQ_TILE_BYTES;
+  return (capacity + KVQ_POS - 1) / KVQ_POS * (KVQ_POS * (head_dim + head_dim / 8));
 }
 // One step's packed rows over a cache: what its calls have in common.
 struct KvqStep {
