@@ -15,7 +15,7 @@
 // nibble of a byte) or 16 q * 2^-24 (high nibble), a subnormal that the tensor
 // core takes as it is: five integer instructions give four operand registers.
 // The factor 16 is taken out of the query fragment, and the offset -8 enters
-// as the initial accumulator -8 sum(x) of each block.  The tensor core aligns
+// as -8 sum(x), added to each block's sum.  The tensor core aligns
 // products by their operands' exponents, of which a subnormal has the
 // largest that it can have, and drops what lies below: the query's hi terms
 // are therefore integers (the row scaled to |x| <= 2048), of whose sums
@@ -308,22 +308,25 @@ struct Walk {
 };
 
 // ---------------------------------------------------------------- queries
-// The query fragment of eight virtual rows: A registers per block and k-step
-// (rows 0-7 hi, rows 8-15 lo), the initial accumulators of each block, and the
-// factor of the scores.
+// The query of eight virtual rows.  Its fragments (A registers of each block and
+// k-step, rows 0-7 hi and rows 8-15 lo) are kept in shared memory, a 16-byte
+// vector per lane: they serve four products each time they are loaded, and the
+// registers that they would hold keep three CTAs per SM free of spills.
 template <int D>
 struct Query {
-  uint32_t a[Kvq<D>::NB][2][4];
-  float c[Kvq<D>::NB][4];
-  float factor;
+  const uint4* frag;        // [block][k-step][lane]
+  float bias[Kvq<D>::NB];   // row g: what a block's partial score has too much, negative
+  float factor;             // row g: from partial scores to scores
 };
+template <int D>
+constexpr int QUERY_BYTES = Kvq<D>::NB * 2 * 32 * 16;
 
 // 2^e for -126 <= e <= 127
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 
 template <int D, typename T>
-__device__ __forceinline__ void load_query(Query<D>& f, const Args<T>& a, const Request& r, int head, int row0,
-                                           int lane) {
+__device__ __forceinline__ void load_query(Query<D>& f, uint4* frag, const Args<T>& a, const Request& r, int head,
+                                           int row0, int lane) {
   constexpr int NB = Kvq<D>::NB;
   const int g = lane >> 2, tq = lane & 3;
   const int vr = row0 + g;
@@ -354,31 +357,31 @@ __device__ __forceinline__ void load_query(Query<D>& f, const Args<T>& a, const 
   if (top > 0.0f && top < INFINITY) e = max(((__float_as_int(top) >> 23) & 255) - 127, -126) - 10;
   const float up1 = pow2((-e) / 2), up2 = pow2(-e - (-e) / 2);
   f.factor = scalbnf(1.0f, 24 + e);
+  f.frag = frag + lane;
+  __syncwarp();  // the last query's fragments have been read
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
-    float h = 0.0f, l = 0.0f;
+    float sum = 0.0f;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
+      uint32_t w[4];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {  // values (2s + k) and (2s + k) + 4; the second pair meets codes of factor 16
         const float x0 = x[b][2 * s + k] * up1 * up2, x1 = x[b][2 * s + k + 4] * up1 * up2;
         const float h0 = rintf(x0), h1 = rintf(x1);
         const float down = k ? 0.0625f : 1.0f, back = k ? 16.0f : 1.0f;
-        f.a[b][s][2 * k] = pack(h0 * down, h1 * down);
-        const uint32_t lo = pack((x0 - h0) * down, (x1 - h1) * down);
-        f.a[b][s][2 * k + 1] = lo;
-        const float2 fl = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-        h += h0 + h1;
-        l += (fl.x + fl.y) * back;
+        w[2 * k] = pack(h0 * down, h1 * down);
+        w[2 * k + 1] = pack((x0 - h0) * down, (x1 - h1) * down);
+        const float2 fl = __half22float2(*reinterpret_cast<const __half2*>(&w[2 * k + 1]));
+        sum += (h0 + fl.x * back) + (h1 + fl.y * back);
       }
+      frag[(2 * b + s) * 32 + lane] = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    h += __shfl_xor_sync(0xFFFFFFFFu, h, 1);
-    l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
-    h += __shfl_xor_sync(0xFFFFFFFFu, h, 2);
-    l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
-    f.c[b][0] = f.c[b][1] = h * (-8.0f * 0x1p-24f);
-    f.c[b][2] = f.c[b][3] = l * (-8.0f * 0x1p-24f);
+    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+    f.bias[b] = sum * (-8.0f * 0x1p-24f);
   }
+  __syncwarp();
 }
 
 template <int N>
@@ -402,25 +405,42 @@ __device__ __forceinline__ void load_scales(const uint8_t* scl, int t, int tq, u
   load_words<Kvq<D>::NB>(scl + (4 * t + tq) * 4 * Kvq<D>::NB, w);
 }
 
-// Scores (log2 units) of eight positions: sc for this lane's row g and the
-// positions 8t + 2 tq, + 1 of the tile.
+// Scores (log2 units) of a tile: sc[u] for this lane's row g and the positions
+// 8u + 2 tq, + 1.
 template <int D>
-__device__ __forceinline__ float2 scores8(const uint8_t* tile, const Query<D>& q, int t, int g, int tq) {
-  constexpr int NB = Kvq<D>::NB;
-  uint32_t w[NB], d[NB];
-  load_words<NB>(tile + 8 * t * Kvq<D>::ROW + (4 * g + tq) * 4 * NB, w);
-  load_scales<D>(tile + Kvq<D>::KS_OFF, t, tq, d);
-  F2 s = f2(0.0f, 0.0f);
+__device__ __forceinline__ void scores(const uint8_t* tile, const Query<D>& q, int g, int tq,
+                                       float (&sc)[KVQ_POS / 8][2]) {
+  constexpr int NB = Kvq<D>::NB, N = KVQ_POS / 8;
+  uint32_t w[N][NB], d[N][NB];
+  F2 s[N];
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    load_words<NB>(tile + 8 * u * Kvq<D>::ROW + (4 * g + tq) * 4 * NB, w[u]);
+    load_scales<D>(tile + Kvq<D>::KS_OFF, u, tq, d[u]);
+    s[u] = f2(0.0f, 0.0f);
+  }
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
-    float c[4];
-    uint32_t r[4];
-    unpack(w[b], r);
-    mma(c, q.a[b][0], r[0], r[1], q.c[b]);
-    mma(c, q.a[b][1], r[2], r[3], c);
-    s = fma2(half2_f2(d[b]), add2(f2(c[0], c[1]), f2(c[2], c[3])), s);
+    const uint4 x = q.frag[2 * b * 32], y = q.frag[(2 * b + 1) * 32];
+    const uint32_t a0[4] = {x.x, x.y, x.z, x.w}, a1[4] = {y.x, y.y, y.z, y.w};
+    const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      float c[4];
+      uint32_t r[4];
+      unpack(w[u][b], r);
+      mma(c, a0, r[0], r[1], zero);
+      mma(c, a1, r[2], r[3], c);
+      const F2 t = add2(add2(f2(c[0], c[1]), f2(q.bias[b], q.bias[b])), f2(c[2], c[3]));
+      s[u] = fma2(half2_f2(d[u][b]), t, s[u]);
+    }
   }
-  return unf2(mul2(s, f2(q.factor, q.factor)));
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    const float2 x = unf2(mul2(s[u], f2(q.factor, q.factor)));
+    sc[u][0] = x.x;
+    sc[u][1] = x.y;
+  }
 }
 
 // ---------------------------------------------------------------- sums
@@ -449,42 +469,41 @@ struct Sums {
   }
 };
 
-// Takes the positions p0 .. p0 + 15, the `half`th sixteen of a tile.  MASKED:
-// some row does not see them all; row g sees those up to `last`, and what lies
-// at `end` and after may be anything.
+// Takes the positions p0 .. p0 + 31 of a tile.  MASKED: some row does not see
+// them all; row g sees those up to `last`, and what lies at `end` and after
+// may be anything.
 template <int D, bool MASKED>
-__device__ __forceinline__ void step16(const uint8_t* tile, int half, int p0, const Query<D>& q, Sums<D>& a, int g,
-                                       int tq, int last, int end) {
+__device__ __forceinline__ void take_tile(const uint8_t* tile, int p0, const Query<D>& q, Sums<D>& a, int g, int tq,
+                                          int last, int end) {
   using L = Kvq<D>;
-  constexpr int NB = L::NB;
-  float sc[2][2];
-  uint32_t vd[2][NB];  // V scale pairs
+  constexpr int NB = L::NB, N = L::POS / 8;
+  // V scale pairs of eight positions; those of positions past the end are zero
+  auto v_scales = [&](int u, uint32_t (&vd)[NB]) {
+    load_scales<D>(tile + L::VS_OFF, u, tq, vd);
+    if constexpr (MASKED) {
+      const int p = p0 + 8 * u + 2 * tq;
+      const uint32_t keep = (p < end ? 0x0000FFFFu : 0u) | (p + 1 < end ? 0xFFFF0000u : 0u);
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const float2 x = scores8<D>(tile, q, 2 * half + u, g, tq);
-    sc[u][0] = x.x;
-    sc[u][1] = x.y;
-    load_scales<D>(tile + L::VS_OFF, 2 * half + u, tq, vd[u]);
-  }
-  if constexpr (MASKED) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int p = p0 + 8 * u + 2 * tq + c;
-        sc[u][c] = p <= last ? sc[u][c] : NEG_INF;
-        if (p >= end) {
-#pragma unroll
-          for (int b = 0; b < NB; ++b) vd[u][b] &= c ? 0x0000FFFFu : 0xFFFF0000u;
-        }
-      }
-  }
-  const float top = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
+      for (int b = 0; b < NB; ++b) vd[b] &= keep;
+    }
+  };
+  float sc[N][2];
+  scores<D>(tile, q, g, tq, sc);
+  float top = NEG_INF;
   __half2 dm = *reinterpret_cast<const __half2*>(&a.dtop);
 #pragma unroll
-  for (int u = 0; u < 2; ++u)
+  for (int u = 0; u < N; ++u) {
+    if constexpr (MASKED) {
+      const int p = p0 + 8 * u + 2 * tq;
+      if (p > last) sc[u][0] = NEG_INF;
+      if (p + 1 > last) sc[u][1] = NEG_INF;
+    }
+    top = fmaxf(top, fmaxf(sc[u][0], sc[u][1]));
+    uint32_t vd[NB];
+    v_scales(u, vd);
 #pragma unroll
-    for (int b = 0; b < NB; ++b) dm = __hmax2(dm, __habs2(*reinterpret_cast<const __half2*>(&vd[u][b])));
+    for (int b = 0; b < NB; ++b) dm = __hmax2(dm, __habs2(*reinterpret_cast<const __half2*>(&vd[b])));
+  }
   const uint32_t dmw = *reinterpret_cast<const uint32_t*>(&dm);
   if (__any_sync(0xFFFFFFFFu, top > a.m + SLACK || dmw != a.dtop)) {
     float mn = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
@@ -511,39 +530,42 @@ __device__ __forceinline__ void step16(const uint8_t* tile, int half, int p0, co
         a.o[b][i][3] *= f1;
       }
   }
-  F2 p[2];
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    p[u] = f2(ex2(sc[u][0] - a.off), ex2(sc[u][1] - a.off));
-    a.l = add2(a.l, p[u]);
-  }
-  // V words of this lane's keys 2 tq, 2 tq + 1 (u = 0) and + 8 (u = 1)
-  uint32_t vw[2][NB];
-#pragma unroll
-  for (int u = 0; u < 2; ++u) load_words<NB>(tile + L::V_OFF + (16 * half + 8 * u) * L::ROW + (4 * g + tq) * 4 * NB, vw[u]);
-#pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    // weights times the block's V scales, as hi and lo terms: B operand with keys along k
-    uint32_t hi[2], lo[2];
+  for (int k = 0; k < N / 2; ++k) {  // sixteen keys a product: eight positions 2k, eight positions 2k + 1
+    F2 p[2];
+    uint32_t vd[2][NB], vw[2][NB];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      F2 x = mul2(p[u], half2_f2(vd[u][b]));
-      if constexpr (MASKED) {  // a weight of 0 keeps a NaN scale out
-        float2 y = unf2(x);
-        if (sc[u][0] == NEG_INF) y.x = 0.0f;
-        if (sc[u][1] == NEG_INF) y.y = 0.0f;
-        x = f2(y.x, y.y);
-      }
-      split(x, hi[u], lo[u]);
+      const int e = 2 * k + u;
+      p[u] = f2(ex2(sc[e][0] - a.off), ex2(sc[e][1] - a.off));
+      a.l = add2(a.l, p[u]);
+      v_scales(e, vd[u]);
+      load_words<NB>(tile + L::V_OFF + 8 * e * L::ROW + (4 * g + tq) * 4 * NB, vw[u]);
     }
-    uint32_t r0[4], r1[4];
-    unpack_centred(vw[0][b], r0);
-    unpack_centred(vw[1][b], r1);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {  // values 4g + 2i and 4g + 2i + 1 of the block as rows g and g + 8
-      const uint32_t av[4] = {r0[2 * i], r0[2 * i + 1], r1[2 * i], r1[2 * i + 1]};
-      mma(a.o[b][i], av, hi[0], hi[1], a.o[b][i]);
-      mma(a.o[b][i], av, lo[0], lo[1], a.o[b][i]);
+    for (int b = 0; b < NB; ++b) {
+      // weights times the block's V scales, as hi and lo terms: B operand with keys along k
+      uint32_t hi[2], lo[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        F2 x = mul2(p[u], half2_f2(vd[u][b]));
+        if constexpr (MASKED) {  // a weight of 0 keeps a NaN scale out
+          float2 y = unf2(x);
+          if (sc[2 * k + u][0] == NEG_INF) y.x = 0.0f;
+          if (sc[2 * k + u][1] == NEG_INF) y.y = 0.0f;
+          x = f2(y.x, y.y);
+        }
+        split(x, hi[u], lo[u]);
+      }
+      uint32_t r0[4], r1[4];
+      unpack_centred(vw[0][b], r0);
+      unpack_centred(vw[1][b], r1);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {  // values 4g + 2i and 4g + 2i + 1 of the block as rows g and g + 8
+        const uint32_t av[4] = {r0[2 * i], r0[2 * i + 1], r1[2 * i], r1[2 * i + 1]};
+        mma(a.o[b][i], av, hi[0], hi[1], a.o[b][i]);
+        mma(a.o[b][i], av, lo[0], lo[1], a.o[b][i]);
+      }
     }
   }
 }
@@ -563,7 +585,7 @@ template <int D, typename T>
 __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kvq_attention_kernel(const Args<T> a) {
   using L = Kvq<D>;
   constexpr int NB = L::NB;
-  extern __shared__ __align__(128) uint8_t smem[];  // a ring per warp
+  extern __shared__ __align__(128) uint8_t smem[];  // a ring per warp, then a query per warp
   __shared__ uint64_t bars[WARPS][STAGES];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, tq = lane & 3;
@@ -615,7 +637,8 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kvq_attention_kernel(con
     const int groups = r.items / a.heads;  // row groups of a head
     const int head = out.item / groups, row0 = (out.item - head * groups) * ROWS;
     Query<D> q;
-    load_query<D, T>(q, a, r, head, row0, lane);
+    load_query<D, T>(q, reinterpret_cast<uint4*>(smem + WARPS * STAGES * L::BYTES + warp * QUERY_BYTES<D>), a, r, head,
+                     row0, lane);
     Sums<D> sums;
     sums.clear();
     const int last = r.pos + (row0 + g) / a.group;  // the row's last visible position
@@ -633,12 +656,8 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kvq_attention_kernel(con
       }
       ++taken;
       const uint8_t* tile = ring + st * L::BYTES;
-#pragma unroll
-      for (int half = 0; half < L::POS / 16; ++half) {
-        const int p0 = t * L::POS + 16 * half;
-        if (p0 + 16 <= clear) step16<D, false>(tile, half, p0, q, sums, g, tq, last, end);
-        else step16<D, true>(tile, half, p0, q, sums, g, tq, last, end);
-      }
+      if ((t + 1) * L::POS <= clear) take_tile<D, false>(tile, t * L::POS, q, sums, g, tq, last, end);
+      else take_tile<D, true>(tile, t * L::POS, q, sums, g, tq, last, end);
       __syncwarp();  // every lane has read the stage before it is written again
       issue();
     }
@@ -760,6 +779,7 @@ __global__ void __launch_bounds__(THREADS) kvq_join_kernel(const Args<T> a) {
 template <int D, typename T>
 __global__ void __launch_bounds__(THREADS) kvq_mass_kernel(const Args<T> a) {
   using L = Kvq<D>;
+  __shared__ uint4 frags[WARPS][QUERY_BYTES<D> / 16];
   const int lane = threadIdx.x & 31;
   const int g = lane >> 2, tq = lane & 3;
   const Range range = plan_range(a, false, nullptr);
@@ -773,18 +793,19 @@ __global__ void __launch_bounds__(THREADS) kvq_mass_kernel(const Args<T> a) {
     const int rows = r.n * a.group;
     for (int row0 = 0; row0 < rows; row0 += ROWS) {
       Query<D> q;
-      load_query<D, T>(q, a, r, head, row0, lane);
+      load_query<D, T>(q, frags[threadIdx.x >> 5], a, r, head, row0, lane);
       const int vr = row0 + g;
       const bool live = vr < rows;
       const int j = live ? vr / a.group : 0;
       const float lse = live ? a.lse[(int64_t)(r.b + j) * (a.heads * a.group) + head * a.group + vr - j * a.group] : 0.0f;
       const int64_t last = live ? r.pos + j : -1;
       for (int t = it.t0; t < it.t1; ++t) {
+        float sc[L::POS / 8][2];
+        scores<D>(plane + (int64_t)t * L::BYTES, q, g, tq, sc);
 #pragma unroll
         for (int u = 0; u < L::POS / 8; ++u) {
-          const float2 sc = scores8<D>(plane + (int64_t)t * L::BYTES, q, u, g, tq);
           const int64_t p = (int64_t)t * L::POS + 8 * u + 2 * tq;
-          float w[2] = {p <= last ? ex2(sc.x - lse) : 0.0f, p + 1 <= last ? ex2(sc.y - lse) : 0.0f};
+          float w[2] = {p <= last ? ex2(sc[u][0] - lse) : 0.0f, p + 1 <= last ? ex2(sc[u][1] - lse) : 0.0f};
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             w[c] += __shfl_xor_sync(0xFFFFFFFFu, w[c], 4);
@@ -829,7 +850,7 @@ int launch_as(const KvqStep& c, const uint8_t* cache, const void* q, const int64
   a.unit_start = ws.unit_start;
   a.lse = mass ? ws.lse : nullptr;
   a.mass = mass;
-  constexpr int SMEM = WARPS * STAGES * Kvq<D>::BYTES;
+  constexpr int SMEM = WARPS * (STAGES * Kvq<D>::BYTES + QUERY_BYTES<D>);
   static std::atomic<bool> sized[64];  // per device: the kernel's shared memory limit is set
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return Q4_ERR_CUDA;
