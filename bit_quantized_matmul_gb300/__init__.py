@@ -7,9 +7,7 @@ is missing, importing this package raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
-import math
 import os
 
 import torch  # device memory and streams; loads the CUDA runtime first
@@ -390,14 +388,27 @@ def q4_kv_append(k_cache: torch.Tensor, v_cache: torch.Tensor, k_new: torch.Tens
                "q4_kv_append")
 
 
+# The calls of a decode step are a few microseconds of GPU work each, so what
+# their bindings cost on the host is kept small: one pass over each tensor's
+# attributes, and PyTorch's raw stream and device getters.
 _DTYPES = {torch.float32: Q4_DTYPE_F32, torch.float16: Q4_DTYPE_F16, torch.bfloat16: Q4_DTYPE_BF16}
 _I64x2 = _i64 * 2
-_HERE_CTX = contextlib.nullcontext()
+_f32, _i32 = torch.float32, torch.int32
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _on(device: torch.device):
-    """Context in which `device` is current (nothing to do when it already is)."""
-    return _HERE_CTX if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+def _call(fn, what: str, device: torch.device, stream, *args):
+    """fn(*args, stream) with `device` current; raises on a status that is not Q4_OK."""
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return _call(fn, what, device, stream, *args)
+    if stream is None and _raw_stream is not None:
+        stream = _raw_stream(device.index)
+    else:
+        stream = _stream(stream)
+    status = fn(*args, stream)
+    if status != Q4_OK:
+        raise Q4Error(status, what)
 
 
 def _dtype_code(dtype, name: str) -> int:
@@ -407,19 +418,24 @@ def _dtype_code(dtype, name: str) -> int:
     return code
 
 
-def _rows3(t: torch.Tensor, name: str, heads: int, head_dim: int, dtype, device) -> torch.Tensor:
-    """A [rows, heads, head_dim] view with contiguous head_dim (any other strides)."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim or (t.stride(2) != 1 and t.numel()):
-        raise ValueError("%s must be a [rows, %d, %d] view with contiguous rows" % (name, heads, head_dim))
+def _rows3(t: torch.Tensor, name: str, heads: int, head_dim: int, dtype, device):
+    """(rows, the two outer strides) of a [rows, heads, head_dim] view with contiguous head_dim."""
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != head_dim:
+        raise ValueError("%s must be a [rows, %d, %d] view" % (name, heads, head_dim))
+    s0, s1, s2 = t.stride()
+    if s2 != 1 and t.numel():
+        raise ValueError("%s must have contiguous rows of head_dim values" % name)
     if t.dtype != dtype or t.device != device:
         raise ValueError("%s must be %s on %s" % (name, dtype, device))
-    return t
+    return shape[0], _I64x2(s0, s1)
 
 
-def _ints(device, **tensors):
-    for name, t in tensors.items():
-        if t.dtype != torch.int32 or t.device != device or not t.is_contiguous():
-            raise ValueError("%s must be a contiguous int32 tensor on the cache's device" % name)
+def _ints(device, t: torch.Tensor, name: str) -> int:
+    """Length of a contiguous int32 tensor on `device`."""
+    if t.dtype != _i32 or t.device != device or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 tensor on %s" % (name, device))
+    return t.numel()
 
 
 def _out3(t, shape, dtype, device, name: str) -> torch.Tensor:
@@ -445,6 +461,7 @@ class Q4KVCache:
         self.data = torch.zeros(n.value, dtype=torch.uint8, device=device)
         self.device = self.data.device
         self._dims = (self.slots, self.heads, self.head_dim, self.capacity)
+        self._ptr = self.data.data_ptr()
 
     @property
     def nbytes(self) -> int:
@@ -456,17 +473,18 @@ class Q4KVCache:
 
 
 def _step(cache: Q4KVCache, offsets, slot, pos) -> int:
-    _ints(cache.device, offsets=offsets, slot=slot, pos=pos)
-    S = slot.numel()
-    if offsets.numel() != S + 1 or pos.numel() != S:
+    device = cache.device
+    S = _ints(device, slot, "slot")
+    if _ints(device, offsets, "offsets") != S + 1 or _ints(device, pos, "pos") != S:
         raise ValueError("offsets must have S + 1 entries and pos S")
     return S
 
 
-def _mass(cache: Q4KVCache, mass: torch.Tensor):
-    if tuple(mass.shape) != (cache.slots, cache.heads, cache.capacity) or mass.dtype != torch.float32 or \
+def _mass(cache: Q4KVCache, mass: torch.Tensor) -> int:
+    if tuple(mass.shape) != (cache.slots, cache.heads, cache.capacity) or mass.dtype != _f32 or \
             mass.device != cache.device or not mass.is_contiguous():
         raise ValueError("mass must be a contiguous float32 [slots, heads, capacity] tensor on the cache's device")
+    return mass.data_ptr()
 
 
 def q4_kvq_append(cache: Q4KVCache, k_new: torch.Tensor, v_new: torch.Tensor, offsets: torch.Tensor,
@@ -477,17 +495,15 @@ def q4_kvq_append(cache: Q4KVCache, k_new: torch.Tensor, v_new: torch.Tensor, of
     step becomes position pos[s] + j of slot[s].
     """
     S = _step(cache, offsets, slot, pos)
-    code = _dtype_code(k_new.dtype, "k_new")
-    _rows3(k_new, "k_new", cache.heads, cache.head_dim, k_new.dtype, cache.device)
-    _rows3(v_new, "v_new", cache.heads, cache.head_dim, k_new.dtype, cache.device)
-    total = k_new.shape[0]
-    if v_new.shape[0] != total:
+    dtype, device = k_new.dtype, cache.device
+    code = _dtype_code(dtype, "k_new")
+    slots, heads, d, cap = cache._dims
+    total, ks = _rows3(k_new, "k_new", heads, d, dtype, device)
+    total_v, vs = _rows3(v_new, "v_new", heads, d, dtype, device)
+    if total_v != total:
         raise ValueError("k_new and v_new differ in rows")
-    with _on(cache.device):
-        _check(_lib.q4_kvq_append(cache.data.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), code, *cache._dims,
-                                  _I64x2(k_new.stride(0), k_new.stride(1)), _I64x2(v_new.stride(0), v_new.stride(1)),
-                                  offsets.data_ptr(), slot.data_ptr(), pos.data_ptr(), S, total, _stream(stream)),
-               "q4_kvq_append")
+    _call(_lib.q4_kvq_append, "q4_kvq_append", device, stream, cache._ptr, k_new.data_ptr(), v_new.data_ptr(), code,
+          slots, heads, d, cap, ks, vs, offsets.data_ptr(), slot.data_ptr(), pos.data_ptr(), S, total)
 
 
 def q4_kvq_read(cache: Q4KVCache, offsets: torch.Tensor, slot: torch.Tensor, pos: torch.Tensor, total: int,
@@ -495,13 +511,13 @@ def q4_kvq_read(cache: Q4KVCache, offsets: torch.Tensor, slot: torch.Tensor, pos
     """(k, v), each [total, heads, head_dim]: the rows that the cache holds for a step's requests."""
     S = _step(cache, offsets, slot, pos)
     code = _dtype_code(dtype, "dtype")
-    shape = (int(total), cache.heads, cache.head_dim)
-    k = _out3(k, shape, dtype, cache.device, "k")
-    v = _out3(v, shape, dtype, cache.device, "v")
-    with _on(cache.device):
-        _check(_lib.q4_kvq_read(cache.data.data_ptr(), k.data_ptr(), v.data_ptr(), code, *cache._dims,
-                                offsets.data_ptr(), slot.data_ptr(), pos.data_ptr(), S, total, _stream(stream)),
-               "q4_kvq_read")
+    slots, heads, d, cap = cache._dims
+    device = cache.device
+    shape = (int(total), heads, d)
+    k = _out3(k, shape, dtype, device, "k")
+    v = _out3(v, shape, dtype, device, "v")
+    _call(_lib.q4_kvq_read, "q4_kvq_read", device, stream, cache._ptr, k.data_ptr(), v.data_ptr(), code, slots, heads,
+          d, cap, offsets.data_ptr(), slot.data_ptr(), pos.data_ptr(), S, shape[0])
     return k, v
 
 
@@ -515,22 +531,17 @@ def q4_kvq_attention(cache: Q4KVCache, q: torch.Tensor, offsets: torch.Tensor, s
     [slots, heads, capacity], collects the weight that each position got.
     """
     S = _step(cache, offsets, slot, pos)
-    code = _dtype_code(q.dtype, "q")
-    if q.dim() != 3 or q.shape[1] == 0 or q.shape[1] % cache.heads:
-        raise ValueError("q must be [total, q_heads, head_dim] with q_heads a multiple of %d" % cache.heads)
-    total, hq = q.shape[0], q.shape[1]
-    _rows3(q, "q", hq, cache.head_dim, q.dtype, cache.device)
-    out = _out3(out, (total, hq, cache.head_dim), q.dtype, cache.device, "out")
-    if mass is not None:
-        _mass(cache, mass)
-    if scale is None:
-        scale = 1.0 / math.sqrt(cache.head_dim)
+    dtype, device = q.dtype, cache.device
+    code = _dtype_code(dtype, "q")
     slots, heads, d, cap = cache._dims
-    with _on(cache.device):
-        _check(_lib.q4_kvq_attention(cache.data.data_ptr(), q.data_ptr(), out.data_ptr(),
-                                     None if mass is None else mass.data_ptr(), code, slots, heads, hq, d, cap,
-                                     _I64x2(q.stride(0), q.stride(1)), scale, offsets.data_ptr(), slot.data_ptr(),
-                                     pos.data_ptr(), S, total, _stream(stream)), "q4_kvq_attention")
+    hq = q.shape[1] if q.dim() == 3 else 0
+    if hq == 0 or hq % heads:
+        raise ValueError("q must be [total, q_heads, head_dim] with q_heads a multiple of %d" % heads)
+    total, qs = _rows3(q, "q", hq, d, dtype, device)
+    out = _out3(out, (total, hq, d), dtype, device, "out")
+    _call(_lib.q4_kvq_attention, "q4_kvq_attention", device, stream, cache._ptr, q.data_ptr(), out.data_ptr(),
+          None if mass is None else _mass(cache, mass), code, slots, heads, hq, d, cap, qs,
+          d ** -0.5 if scale is None else scale, offsets.data_ptr(), slot.data_ptr(), pos.data_ptr(), S, total)
     return out
 
 
@@ -542,17 +553,17 @@ def q4_kvq_evict(cache: Q4KVCache, mass: torch.Tensor, src: torch.Tensor, dst: t
     positions and the others of largest mass, `keep` in all, moved in order
     to the front of slot dst[s] (the same slot: in place), mass alike.
     """
-    _ints(cache.device, src=src, dst=dst, length=length)
-    _mass(cache, mass)
-    S = src.numel()
-    if dst.numel() != S or length.numel() != S:
+    device, keep = cache.device, int(keep)
+    S = _ints(device, src, "src")
+    if _ints(device, dst, "dst") != S or _ints(device, length, "length") != S:
         raise ValueError("src, dst and length differ in length")
-    new_length = torch.empty((S,), dtype=torch.int32, device=cache.device)
-    kept = torch.empty((S, cache.heads, max(int(keep), 0)), dtype=torch.int32, device=cache.device)
-    with _on(cache.device):
-        _check(_lib.q4_kvq_evict(cache.data.data_ptr(), mass.data_ptr(), *cache._dims, src.data_ptr(), dst.data_ptr(),
-                                 length.data_ptr(), S, int(keep), int(recent), new_length.data_ptr(), kept.data_ptr(),
-                                 _stream(stream)), "q4_kvq_evict")
+    mass_ptr = _mass(cache, mass)
+    slots, heads, d, cap = cache._dims
+    new_length = torch.empty((S,), dtype=_i32, device=device)
+    kept = torch.empty((S, heads, max(keep, 0)), dtype=_i32, device=device)
+    _call(_lib.q4_kvq_evict, "q4_kvq_evict", device, stream, cache._ptr, mass_ptr, slots, heads, d, cap,
+          src.data_ptr(), dst.data_ptr(), length.data_ptr(), S, keep, int(recent), new_length.data_ptr(),
+          kept.data_ptr())
     return new_length, kept
 
 
@@ -567,30 +578,24 @@ def q4_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_off
     """
     if q.dim() != 3 or k.dim() != 3 or k.shape[1] == 0 or q.shape[1] == 0 or q.shape[1] % k.shape[1]:
         raise ValueError("q must be [rows, q_heads, D] with q_heads a multiple of k's heads")
-    if q.dtype not in (torch.float16, torch.bfloat16) or not q.is_cuda:
+    dtype, device = q.dtype, q.device
+    if dtype not in (torch.float16, torch.bfloat16) or not q.is_cuda:
         raise ValueError("q must be a float16 or bfloat16 CUDA tensor")
     if k_offsets is None:
         k_offsets = q_offsets
-    tq, hq, d = q.shape
-    tk, hk, _ = k.shape
-    _rows3(q, "q", hq, d, q.dtype, q.device)
-    _rows3(k, "k", hk, d, q.dtype, q.device)
-    _rows3(v, "v", hk, d, q.dtype, q.device)
-    if v.shape[0] != tk:
+    hq, hk, d = q.shape[1], k.shape[1], q.shape[2]
+    tq, qs = _rows3(q, "q", hq, d, dtype, device)
+    tk, ks = _rows3(k, "k", hk, d, dtype, device)
+    tv, vs = _rows3(v, "v", hk, d, dtype, device)
+    if tv != tk:
         raise ValueError("k and v differ in rows")
-    _ints(q.device, q_offsets=q_offsets, k_offsets=k_offsets)
-    S = q_offsets.numel() - 1
-    if k_offsets.numel() != S + 1:
+    S = _ints(device, q_offsets, "q_offsets") - 1
+    if _ints(device, k_offsets, "k_offsets") != S + 1:
         raise ValueError("q_offsets and k_offsets differ in length")
-    out = _out3(out, (tq, hq, d), q.dtype, q.device, "out")
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    with _on(q.device):
-        _check(_lib.q4_prompt_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _DTYPES[q.dtype], hq,
-                                        hk, d, _I64x2(q.stride(0), q.stride(1)), _I64x2(k.stride(0), k.stride(1)),
-                                        _I64x2(v.stride(0), v.stride(1)), scale, 1 if causal else 0,
-                                        q_offsets.data_ptr(), k_offsets.data_ptr(), S, tq, tk, _stream(stream)),
-               "q4_prompt_attention")
+    out = _out3(out, (tq, hq, d), dtype, device, "out")
+    _call(_lib.q4_prompt_attention, "q4_prompt_attention", device, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          out.data_ptr(), _DTYPES[dtype], hq, hk, d, qs, ks, vs, d ** -0.5 if scale is None else scale,
+          1 if causal else 0, q_offsets.data_ptr(), k_offsets.data_ptr(), S, tq, tk)
     return out
 
 
