@@ -12,7 +12,7 @@
 // positions wide.
 //
 // A CTA takes two such tiles, one after another in a sequence, against key
-// blocks of 128.  Roles (320 threads):
+// blocks of 128.  Roles (384 threads, three warpgroups):
 //   warps 0-3, 4-7  softmax of tile 0 / tile 1: a thread owns one row, so its
 //                   maximum and sum need no exchange.  S comes from tensor
 //                   memory, the weights go back over it as 16-bit values (the A
@@ -25,6 +25,10 @@
 //                   tensor maps with the 128-byte swizzle
 //   warp 9          issues the products: S of one tile while the other tile's
 //                   softmax runs
+// The launch gives each thread 168 registers; the softmax warpgroups take 224
+// and leave the third 56 (2 * 224 + 56 = 3 * 168), so a row of scores stays in
+// registers.  Weights are handed over in two halves, so the second product
+// starts while the second half is computed.
 // The products of a CTA run in order, so when S of block i + 1 is there, the
 // accumulation of block i is done and O may be rescaled without a wait.
 //
@@ -49,7 +53,7 @@ namespace {
 constexpr int BM = 128;                 // packed rows per tile
 constexpr int BN = 128;                 // keys per block
 constexpr int TMA_WARP = 8, MMA_WARP = 9;
-constexpr int THREADS = 320;
+constexpr int THREADS = 384;
 constexpr int TMEM_COLS = 512;
 constexpr float NEG_INF = -INFINITY;
 constexpr float RESCALE = 8.0f;         // log2 of the growth that triggers a rescale
@@ -161,6 +165,12 @@ __device__ void clear_rows(const Args& a) {
   }
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   if constexpr (std::is_same<T, __half>::value) {
@@ -229,7 +239,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint8_t* smem_p = smem_raw + (smem - smem_u32(smem_raw));
   const uint32_t q_smem = smem, ring = smem + 2 * C::TILE, bars = smem + C::BAR_OFF;
   const uint32_t q_full = bars, full = bars + 8, empty = full + 8 * NST, fixed = empty + 8 * NST;
-  const uint32_t s_full = fixed + 8 * NST, p_full = s_full + 16, o_full = p_full + 16, drain = o_full + 16;
+  const uint32_t s_full = fixed + 8 * NST, p_full = s_full + 16, o_full = p_full + 32, drain = o_full + 16;
   volatile int* err = &s_err;
   if (tid == 0) {
     mbar_init(q_full, 1);
@@ -241,7 +251,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(s_full + 8 * t, 1);
-      mbar_init(p_full + 8 * t, 4);
+      mbar_init(p_full + 16 * t, 4);
+      mbar_init(p_full + 16 * t + 8, 4);
       mbar_init(o_full + 8 * t, 1);
     }
     s_err = 0;
@@ -254,6 +265,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = s_tmem;
 
+  if (warp >= TMA_WARP) {
+  fewer_registers<56>();
   if (warp == TMA_WARP) {
     // ---------------- copies ----------------
     int issued = 0;
@@ -341,13 +354,17 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (ok && i + 1 < nblocks) ok = mbar_wait(full + 8 * sk, (nk / NST) & 1, err, a.wait_ns);
         for (int t = 0; t < 2 && ok; ++t) {
           if (i >= blocks[t]) continue;
-          ok = mbar_wait(p_full + 8 * t, i & 1, err, a.wait_ns);
-          if (!ok) break;
-          tc_fence_after();
 #pragma unroll
-          for (int k = 0; k < BN / 16; ++k)  // O_t += P_t V
-            mma_ts(tmem + C::O_COL + t * D, tmem + t * BN + k * 8,
-                   desc_sw128(ring + sv * C::TILE + k * 2048, C::CHUNK, 1024), ID_O, i > 0 || k > 0);
+          for (int h = 0; h < 2 && ok; ++h) {  // O_t += P_t V, a half of the keys at a time
+            ok = mbar_wait(p_full + 16 * t + 8 * h, i & 1, err, a.wait_ns);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = h * BN / 32; k < (h + 1) * BN / 32; ++k)
+              mma_ts(tmem + C::O_COL + t * D, tmem + t * BN + k * 8,
+                     desc_sw128(ring + sv * C::TILE + k * 2048, C::CHUNK, 1024), ID_O, i > 0 || k > 0);
+          }
+          if (!ok) break;
           if (i + 1 < blocks[t]) qk(t, sk);
           else mma_commit(o_full + 8 * t);
         }
@@ -363,7 +380,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
     __syncwarp();
+  }
   } else {
+    more_registers<224>();
     // ---------------- softmax ----------------
     const int t = warp >> 2;
     const int r = tid & 127;
@@ -394,8 +413,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       float top[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
 #pragma unroll
-      for (int c = 0; c < BN; ++c) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(s[c]));
-      float mn = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+      for (int c = 0; c < BN; c += 2)
+        top[(c >> 1) & 3] = max3(top[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+      float mn = max3(fmaxf(top[0], top[1]), top[2], top[3]);
       mn *= a.scale_log2;  // positive: checked on the host
       if (i == 0) {
         m = mn;
@@ -415,21 +435,26 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       const float mm = m == NEG_INF ? 0.0f : m;
-      float sum[4] = {};
+      const F2 sc2 = f2(a.scale_log2, a.scale_log2), mm2 = f2(-mm, -mm);
+      F2 sum[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};
 #pragma unroll
-      for (int c = 0; c < BN; c += 2) {
-        const float p0 = ex2(fmaf(__uint_as_float(s[c]), a.scale_log2, -mm));
-        const float p1 = ex2(fmaf(__uint_as_float(s[c + 1]), a.scale_log2, -mm));
-        sum[(c >> 1) & 3] += p0 + p1;
-        s[c / 2] = pack2<T>(p0, p1);
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int c = h * BN / 2; c < (h + 1) * BN / 2; c += 2) {
+          const float2 x = unf2(fma2(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, mm2));
+          const float p0 = ex2(x.x), p1 = ex2(x.y);
+          sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], f2(p0, p1));
+          s[c / 2] = pack2<T>(p0, p1);
+        }
+        if (h == 0) tmem_st32<0>(s_addr, s);
+        else tmem_st32<32>(s_addr + 32, s);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + 16 * t + 8 * h);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tmem_st32<0>(s_addr, s);
-      tmem_st32<32>(s_addr + 32, s);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full + 8 * t);
+      const float2 l2 = unf2(add2(sum[0], sum[1]));
+      l += l2.x + l2.y;
     }
     // ---- O / l to memory ----
     const int hq = head * G + r % G;
