@@ -12,7 +12,10 @@
 // positions wide.
 //
 // A CTA takes two such tiles, one after another in a sequence, against key
-// blocks of 128.  Roles (384 threads, three warpgroups):
+// blocks of 128; when it is done with them it takes over a pair of tiles that
+// another CTA of the launch was to do and has not begun (the longest come
+// first), so that the copies and first products of one pair run under the end
+// of the last one.  Roles (384 threads, three warpgroups):
 //   warps 0-3, 4-7  softmax of tile 0 / tile 1: a thread owns one row, so its
 //                   maximum and sum need no exchange.  S comes from tensor
 //                   memory, the weights go back over it as 16-bit values (the A
@@ -25,8 +28,9 @@
 //                   tensor maps with the 128-byte swizzle
 //   warp 9          issues the products: S of one tile while the other tile's
 //                   softmax runs
-// The launch gives each thread 168 registers; the softmax warpgroups take 224
-// and leave the third 56 (2 * 224 + 56 = 3 * 168), so a row of scores stays in
+//   warp 10         finds the work
+// The launch gives each thread 168 registers; the softmax warpgroups take 208
+// and leave the third 88 (2 * 208 + 88 = 3 * 168), so a row of scores stays in
 // registers.  Weights are handed over in two halves, so the second product
 // starts while the second half is computed.
 // The products of a CTA run in order, so when S of block i + 1 is there, the
@@ -52,7 +56,8 @@ namespace {
 
 constexpr int BM = 128;                 // packed rows per tile
 constexpr int BN = 128;                 // keys per block
-constexpr int TMA_WARP = 8, MMA_WARP = 9;
+constexpr int TMA_WARP = 8, MMA_WARP = 9, WORK_WARP = 10;
+constexpr int WORKS = 2;                // the pair under way and the next one
 constexpr int THREADS = 384;
 constexpr int TMEM_COLS = 512;
 constexpr float NEG_INF = -INFINITY;
@@ -75,7 +80,7 @@ struct Args {
   int64_t v_row, v_head;  // strides of v in elements
   int64_t q_total, k_total;
   int q_heads, kv_heads, group, positions;  // positions per tile
-  int S, causal, ctas;
+  int S, causal;
   float scale_log2;
   const int32_t *q_offsets, *k_offsets;
   unsigned* status;
@@ -93,69 +98,111 @@ __device__ __forceinline__ bool load_seq(const Args& a, int s, Seq* q) {
   return qb >= 0 && qe >= qb && qe <= a.q_total && kb >= 0 && ke >= kb && ke <= a.k_total;
 }
 
-// What a CTA works on.
+// A pair of tiles.
 struct Work {
-  int ok;       // 0: nothing
+  int ok;       // 0: there is no more
+  int head;
   int pos0;     // first position of tile 0 in the sequence
   Seq q;
 };
 
-// The CTA's pair of tiles: pair `index` of all sequences' pairs, counted from
-// the last one back (the longest causal rows first).
-__device__ void find_work(const Args& a, int index, Work* out) {
-  __shared__ int warp_sum[THREADS / 32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int step = 2 * a.positions;
-  const int chunk = (a.S + THREADS - 1) / THREADS;
-  const int s0 = min(a.S, tid * chunk), s1 = min(a.S, s0 + chunk);
-  int mine = 0;
-  bool bad = false;
-  for (int s = s0; s < s1; ++s) {
-    Seq q;
-    if (load_seq(a, s, &q)) mine += (q.qlen + step - 1) / step;
-    else bad = true;
+// Finds pairs for the CTA, run by one warp.  Pairs are counted from the last
+// one back (the longest causal rows of a sequence first).
+struct Finder {
+  Seq q;        // with at most 32 sequences: the lane's own
+  int n, upto;  // its pairs, and all up to and with it
+  int all;
+  bool gaps;    // some rows belong to no sequence, or to one that is out of range
+  __device__ __forceinline__ static int pairs(const Args& a, int s, Seq* q, bool* bad) {
+    const int step = 2 * a.positions;
+    *q = Seq{0, 0, 0, 0};
+    if (s >= a.S) return 0;
+    if (load_seq(a, s, q)) return (q->qlen + step - 1) / step;
+    *bad = true;
+    return 0;
   }
-  if (bad && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(a.status, STATUS_KV_RANGE);
-  int incl = mine;
+  __device__ __forceinline__ static int scan(int v, int lane) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-    if (lane >= o) incl += v;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xFFFFFFFFu, v, o);
+      if (lane >= o) v += x;
+    }
+    return v;
   }
-  if (lane == 31) warp_sum[warp] = incl;
-  if (tid == 0) out->ok = 0;
-  __syncthreads();
-  int base = 0, all = 0;
-  for (int w = 0; w < THREADS / 32; ++w) {
-    if (w < warp) base += warp_sum[w];
-    all += warp_sum[w];
+  __device__ __forceinline__ void begin(const Args& a, int lane) {
+    bool bad = false;
+    all = 0;
+    for (int s = 0; s < a.S; s += 32) {
+      n = pairs(a, s + lane, &q, &bad);
+      upto = scan(n, lane);
+      all += __shfl_sync(0xFFFFFFFFu, upto, 31);
+    }
+    bad = __any_sync(0xFFFFFFFFu, bad);
+    if (bad && lane == 0) atomicOr(a.status, STATUS_KV_RANGE);
+    gaps = bad || (a.S > 0 && (__ldg(a.q_offsets) > 0 || __ldg(a.q_offsets + a.S) < a.q_total));
   }
-  const int want = all - 1 - index;
-  int start = base + incl - mine;
-  if (want >= start && want < start + mine) {
-    for (int s = s0; s < s1; ++s) {
-      Seq q;
-      if (!load_seq(a, s, &q)) continue;
-      const int n = (q.qlen + step - 1) / step;
-      if (want < start + n) {
-        *out = Work{1, (want - start) * step, q};
-        break;
+  // pair `index` of one head; false when there is none.  Every lane gets it.
+  __device__ __forceinline__ bool find(const Args& a, int index, int lane, Work* w) {
+    const int want = all - 1 - index;
+    if (want < 0) return false;
+    int base = 0;
+    for (int s = 0;; s += 32) {
+      if (a.S > 32) {
+        bool bad = false;
+        n = pairs(a, s + lane, &q, &bad);
+        upto = scan(n, lane);
       }
-      start += n;
+      const unsigned hit = __ballot_sync(0xFFFFFFFFu, want < base + upto);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        const int first = base + __shfl_sync(0xFFFFFFFFu, upto - n, l);
+        w->q.qb = __shfl_sync(0xFFFFFFFFu, q.qb, l);
+        w->q.qlen = __shfl_sync(0xFFFFFFFFu, q.qlen, l);
+        w->q.kb = __shfl_sync(0xFFFFFFFFu, q.kb, l);
+        w->q.klen = __shfl_sync(0xFFFFFFFFu, q.klen, l);
+        w->pos0 = (want - first) * 2 * a.positions;
+        w->ok = 1;
+        return true;
+      }
+      base += __shfl_sync(0xFFFFFFFFu, upto, 31);
     }
   }
-  __syncthreads();
-}
+};
 
-// Rows that belong to no sequence, or to one that is out of range, are zero.
+// What the roles derive from a pair.
+struct Plan {
+  int blocks[2];     // key blocks of each tile
+  int nblocks;       // of the pair
+  int first_hidden;  // the first key that some row does not see, klen when all are seen
+  int zone;          // blocks from here on hold such keys, or end past the sequence
+  int shift;
+  __device__ __forceinline__ int limit(const Args& a, const Work& w, int pos) const {
+    return a.causal ? pos + shift : w.q.klen - 1;
+  }
+  __device__ __forceinline__ Plan(const Args& a, const Work& w) {
+    shift = w.q.klen - w.q.qlen;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int p0 = w.pos0 + t * a.positions;
+      const int last = limit(a, w, min(p0 + a.positions, w.q.qlen) - 1);
+      blocks[t] = p0 < w.q.qlen && last >= 0 ? last / BN + 1 : 0;
+    }
+    nblocks = max(blocks[0], blocks[1]);
+    first_hidden = max(0, min(limit(a, w, w.pos0) + 1, w.q.klen));
+    zone = first_hidden / BN;  // past the last block when nothing is hidden
+  }
+};
+
+// Rows that belong to no sequence, or to one that is out of range, are zero:
+// the share of one of `threads` threads.
 template <int D, typename T>
-__device__ void clear_rows(const Args& a) {
+__device__ void clear_rows(const Args& a, int64_t thread, int64_t threads) {
   const int64_t row = (int64_t)a.q_heads * D * sizeof(T) / 16;  // 16-byte vectors of a packed row
   auto clear = [&](int64_t r0, int64_t r1) {
     uint4* p = static_cast<uint4*>(a.out);
     r0 = r0 < 0 ? 0 : r0;
     r1 = r1 > a.q_total ? a.q_total : r1;
-    for (int64_t i = r0 * row + threadIdx.x; i < r1 * row; i += blockDim.x) p[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int64_t i = r0 * row + thread; i < r1 * row; i += threads) p[i] = make_uint4(0u, 0u, 0u, 0u);
   };
   clear(0, a.q_offsets[0]);
   clear(a.q_offsets[a.S], a.q_total);
@@ -204,46 +251,28 @@ __global__ void __launch_bounds__(THREADS, 1)
                   const __grid_constant__ CUtensorMap map_v) {
   using C = Cfg<D>;
   constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
-  constexpr int NST = C::STAGES, NV = NST / 2;
+  constexpr int NST = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ Work work;
-  __shared__ int s_err, s_nonfinite;
+  __shared__ Work work[WORKS];
+  __shared__ __align__(16) uint4 taken;
+  __shared__ int s_err, s_nonfinite[WORKS];
   __shared__ uint32_t s_tmem;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-
-  if ((int)blockIdx.x == a.ctas) {
-    if (blockIdx.y == 0) clear_rows<D, T>(a);
-    return;
-  }
-  find_work(a, blockIdx.x, &work);
-  if (!work.ok) return;
-  const Seq sq = work.q;
-  const int head = blockIdx.y;
   const int G = a.group, P = a.positions;
-  // the last key that a position sees, and the key blocks of each tile
-  const int shift = a.causal ? sq.klen - sq.qlen : 0;
-  auto limit = [&](int pos) { return a.causal ? pos + shift : sq.klen - 1; };
-  int blocks[2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int p0 = work.pos0 + t * P;
-    const int last = limit(min(p0 + P, sq.qlen) - 1);
-    blocks[t] = p0 < sq.qlen && last >= 0 ? last / BN + 1 : 0;
-  }
-  const int nblocks = max(blocks[0], blocks[1]);
-  // blocks from here on hold keys that some row of the CTA does not see
-  const int first_hidden = max(0, min(limit(work.pos0) + 1, sq.klen));
-  const int zone = first_hidden / BN;  // beyond the last block when nothing is hidden
 
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* smem_p = smem_raw + (smem - smem_u32(smem_raw));
   const uint32_t q_smem = smem, ring = smem + 2 * C::TILE, bars = smem + C::BAR_OFF;
-  const uint32_t q_full = bars, full = bars + 8, empty = full + 8 * NST, fixed = empty + 8 * NST;
-  const uint32_t s_full = fixed + 8 * NST, p_full = s_full + 16, o_full = p_full + 32, drain = o_full + 16;
+  const uint32_t q_full = bars, q_empty = q_full + 8, drain = q_empty + 8, answer = drain + 8;
+  const uint32_t full = answer + 8, empty = full + 8 * NST, fixed = empty + 8 * NST;
+  const uint32_t s_full = fixed + 8 * NST, p_full = s_full + 16, o_full = p_full + 32, o_empty = o_full + 16;
+  const uint32_t work_full = o_empty + 16, work_empty = work_full + 8 * WORKS;
   volatile int* err = &s_err;
   if (tid == 0) {
     mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
     mbar_init(drain, 1);
+    mbar_init(answer, 1);
     for (int i = 0; i < NST; ++i) {
       mbar_init(full + 8 * i, 1);
       mbar_init(empty + 8 * i, 1);
@@ -254,9 +283,14 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(p_full + 16 * t, 4);
       mbar_init(p_full + 16 * t + 8, 4);
       mbar_init(o_full + 8 * t, 1);
+      mbar_init(o_empty + 8 * t, 4);
+    }
+    for (int i = 0; i < WORKS; ++i) {
+      mbar_init(work_full + 8 * i, 1);
+      mbar_init(work_empty + 8 * i, 10);  // the copies', the products' and eight softmax warps
+      s_nonfinite[i] = 0;
     }
     s_err = 0;
-    s_nonfinite = 0;
     mbar_init_fence();
   }
   if (warp == MMA_WARP) tmem_alloc(smem_u32(&s_tmem), TMEM_COLS);
@@ -264,235 +298,336 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
+  // The roles go through the same pairs in the same order, each with its own
+  // count of what it has waited for.  The next pair, false when there is none.
+  auto next_work = [&](int nth, Work* w) {
+    const bool ok = mbar_wait(work_full + 8 * (nth % WORKS), (nth / WORKS) & 1, err, a.wait_ns);
+    if (!ok) return false;
+    *w = work[nth % WORKS];
+    return w->ok != 0;
+  };
 
   if (warp >= TMA_WARP) {
-  fewer_registers<56>();
-  if (warp == TMA_WARP) {
-    // ---------------- copies ----------------
-    int issued = 0;
-    if (lane == 0 && nblocks > 0) {
-      uint32_t bytes = 0;
-      for (int t = 0; t < 2; ++t)
-        if (blocks[t]) bytes += (uint32_t)(C::CHUNKS * P * G * 128);
-      mbar_expect_tx(q_full, bytes);
-      for (int t = 0; t < 2; ++t)
-        if (blocks[t])
-          for (int c = 0; c < C::CHUNKS; ++c)
-            tensor_load(q_smem + t * C::TILE + c * C::CHUNK, &map_q, 64 * c, head * G, sq.qb + work.pos0 + t * P,
-                        q_full);
-    }
-    bool ok = true;
-    for (int i = 0; i < nblocks && ok; ++i) {
-      for (int kv = 0; kv < 2 && ok; ++kv) {
-        const int n = 2 * i + kv, st = n % NST;
+    fewer_registers<88>();
+    if (warp == WORK_WARP) {
+      // ---------------- work ----------------
+      Finder f;
+      f.begin(a, lane);
+      uint32_t index = blockIdx.x;
+      bool more = true;
+      int nth = 0;
+      for (int asked = 0; more; ++asked) {
+        Work w;
+        if (f.find(a, (int)(index / a.kv_heads), lane, &w)) {
+          if (lane == 0) {
+            w.head = (int)(index % a.kv_heads);
+            work[nth % WORKS] = w;
+            s_nonfinite[nth % WORKS] = 0;
+            mbar_arrive(work_full + 8 * (nth % WORKS));
+          }
+          __syncwarp();
+          ++nth;
+        }
+        if (f.gaps) clear_rows<D, T>(a, (int64_t)index * 32 + lane, (int64_t)gridDim.x * 32);
+        // one pair is under way and one waits: take another only when the first is done
+        if (nth >= WORKS) {
+          const int v = nth - WORKS;
+          if (!__all_sync(0xFFFFFFFFu, mbar_wait(work_empty + 8 * (v % WORKS), (v / WORKS) & 1, err, a.wait_ns))) break;
+        }
         if (lane == 0) {
-          if (n >= NST) ok = mbar_wait(empty + 8 * st, ((n / NST) - 1) & 1, err, a.wait_ns);
-          if (ok) {
-            mbar_expect_tx(full + 8 * st, C::TILE);
-            for (int c = 0; c < C::CHUNKS; ++c)
-              tensor_load(ring + st * C::TILE + c * C::CHUNK, kv ? (const void*)&map_v : (const void*)&map_k, 64 * c,
-                          head, sq.kb + i * BN, full + 8 * st);
-          }
+          mbar_expect_tx(answer, 16);
+          take_cta(smem_u32(&taken), answer);
         }
-        ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0) != 0;
-        if (ok) issued = n + 1;
-      }
-      if (ok && i >= zone) {  // make V safe to multiply with weights of 0
-        const int n = 2 * i + 1, st = n % NST;
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(full + 8 * st, (n / NST) & 1, err, a.wait_ns));
-        if (!ok) break;
-        const int r0 = max(0, first_hidden - i * BN), end = min(BN, sq.klen - i * BN);
-        uint8_t* vb = smem_p + (ring - smem) + st * C::TILE;
-        bool found = false;
-        for (int it = lane; it < (BN - r0) * C::CHUNKS * 8; it += 32) {
-          const int row = r0 + it / (C::CHUNKS * 8), e = it % (C::CHUNKS * 8);
-          uint4* p = reinterpret_cast<uint4*>(vb + (e >> 3) * C::CHUNK + row * 128 + ((e & 7) ^ (row & 7)) * 16);
-          if (row >= end) {
-            *p = make_uint4(0u, 0u, 0u, 0u);
-          } else {
-            const uint4 v = *p;
-            if (nonfinite2<T>(v.x) || nonfinite2<T>(v.y) || nonfinite2<T>(v.z) || nonfinite2<T>(v.w)) {
-              found = true;
-              *p = make_uint4(finite2<T>(v.x), finite2<T>(v.y), finite2<T>(v.z), finite2<T>(v.w));
-            }
-          }
+        __syncwarp();
+        if (!mbar_wait_warp(answer, asked & 1, a.wait_ns)) {
+          *err = 1;
+          break;
         }
-        if (found) atomicExch(&s_nonfinite, 1);
+        more = taken_cta(smem_u32(&taken), &index);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(fixed + 8 * st);
       }
-    }
-    // the copies in flight land before the CTA ends, also when another role has given up
-    if (nblocks > 0) mbar_wait_warp(q_full, 0, a.wait_ns);
-    for (int n = max(0, issued - NST); n < issued; ++n)
-      mbar_wait_warp(full + 8 * (n % NST), (n / NST) & 1, a.wait_ns);
-  } else if (warp == MMA_WARP) {
-    // ---------------- products ----------------
-    if (lane == 0 && nblocks > 0) {
-      constexpr uint32_t ID_S = idesc_f16(BF16, BN, false), ID_O = idesc_f16(BF16, D, true);
-      auto qk = [&](int t, int st) {  // S_t = Q_t K^T
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (uint32_t)((k >> 2) * C::CHUNK + (k & 3) * 32);
-          mma_ss(tmem + t * BN, desc_sw128(q_smem + t * C::TILE + off, 16, 1024),
-                 desc_sw128(ring + st * C::TILE + off, 16, 1024), ID_S, k > 0);
+      if (!more && lane == 0) {  // its slot is free: waited for above, or never used
+        work[nth % WORKS].ok = 0;
+        mbar_arrive(work_full + 8 * (nth % WORKS));
+      }
+    } else if (warp == TMA_WARP) {
+      // ---------------- copies ----------------
+      int n = 0, nq = 0;        // blocks and Q pairs so far
+      bool ok = true;
+      Work w;
+      for (int nth = 0; ok; ++nth) {
+        if (!__all_sync(0xFFFFFFFFu, next_work(nth, &w))) break;
+        const Plan p(a, w);
+        const Seq sq = w.q;
+        if (p.nblocks > 0) {
+          if (lane == 0) {
+            if (nq > 0) ok = mbar_wait(q_empty, (nq - 1) & 1, err, a.wait_ns);
+            if (ok) {
+              uint32_t bytes = 0;
+              for (int t = 0; t < 2; ++t)
+                if (p.blocks[t]) bytes += (uint32_t)(C::CHUNKS * P * G * 128);
+              mbar_expect_tx(q_full, bytes);
+              for (int t = 0; t < 2; ++t)
+                if (p.blocks[t])
+                  for (int c = 0; c < C::CHUNKS; ++c)
+                    tensor_load(q_smem + t * C::TILE + c * C::CHUNK, &map_q, 64 * c, w.head * G,
+                                sq.qb + w.pos0 + t * P, q_full);
+            }
+          }
+          ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0) != 0;
+          if (ok) ++nq;
         }
-        mma_commit(s_full + 8 * t);
-      };
-      bool ok = mbar_wait(q_full, 0, err, a.wait_ns) && mbar_wait(full, 0, err, a.wait_ns);
-      tc_fence_after();
-      if (ok) {
-        for (int t = 0; t < 2; ++t)
-          if (blocks[t]) qk(t, 0);
-        mma_commit(empty);
-      }
-      for (int i = 0; i < nblocks && ok; ++i) {
-        const int nv = 2 * i + 1, sv = nv % NST, nk = nv + 1, sk = nk % NST;
-        ok = mbar_wait(full + 8 * sv, (nv / NST) & 1, err, a.wait_ns);
-        if (ok && i >= zone) ok = mbar_wait(fixed + 8 * sv, ((i - zone) / NV) & 1, err, a.wait_ns);
-        if (ok && i + 1 < nblocks) ok = mbar_wait(full + 8 * sk, (nk / NST) & 1, err, a.wait_ns);
-        for (int t = 0; t < 2 && ok; ++t) {
-          if (i >= blocks[t]) continue;
-#pragma unroll
-          for (int h = 0; h < 2 && ok; ++h) {  // O_t += P_t V, a half of the keys at a time
-            ok = mbar_wait(p_full + 16 * t + 8 * h, i & 1, err, a.wait_ns);
+        for (int i = 0; i < p.nblocks && ok; ++i) {
+          for (int kv = 0; kv < 2 && ok; ++kv) {
+            const int st = n % NST;
+            if (lane == 0) {
+              if (n >= NST) ok = mbar_wait(empty + 8 * st, ((n / NST) - 1) & 1, err, a.wait_ns);
+              if (ok) {
+                mbar_expect_tx(full + 8 * st, C::TILE);
+                for (int c = 0; c < C::CHUNKS; ++c)
+                  tensor_load(ring + st * C::TILE + c * C::CHUNK, kv ? (const void*)&map_v : (const void*)&map_k,
+                              64 * c, w.head, sq.kb + i * BN, full + 8 * st);
+              }
+            }
+            ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0) != 0;
+            if (ok) ++n;
+          }
+          if (ok && i >= p.zone) {  // make V safe to multiply with weights of 0
+            const int st = (n - 1) % NST;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(full + 8 * st, ((n - 1) / NST) & 1, err, a.wait_ns));
             if (!ok) break;
+            const int r0 = max(0, p.first_hidden - i * BN), end = min(BN, sq.klen - i * BN);
+            uint8_t* vb = smem_p + (ring - smem) + st * C::TILE;
+            bool found = false;
+            for (int it = lane; it < (BN - r0) * C::CHUNKS * 8; it += 32) {
+              const int row = r0 + it / (C::CHUNKS * 8), e = it % (C::CHUNKS * 8);
+              uint4* x = reinterpret_cast<uint4*>(vb + (e >> 3) * C::CHUNK + row * 128 + ((e & 7) ^ (row & 7)) * 16);
+              if (row >= end) {
+                *x = make_uint4(0u, 0u, 0u, 0u);
+              } else {
+                const uint4 v = *x;
+                if (nonfinite2<T>(v.x) || nonfinite2<T>(v.y) || nonfinite2<T>(v.z) || nonfinite2<T>(v.w)) {
+                  found = true;
+                  *x = make_uint4(finite2<T>(v.x), finite2<T>(v.y), finite2<T>(v.z), finite2<T>(v.w));
+                }
+              }
+            }
+            if (found) atomicExch(&s_nonfinite[nth % WORKS], 1);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(fixed + 8 * st);
+          }
+        }
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(work_empty + 8 * (nth % WORKS));
+      }
+      // the copies in flight land before the CTA ends, also when another role has given up
+      if (nq > 0) mbar_wait_warp(q_full, (nq - 1) & 1, a.wait_ns);
+      for (int v = max(0, n - NST); v < n; ++v) mbar_wait_warp(full + 8 * (v % NST), (v / NST) & 1, a.wait_ns);
+    } else if (warp == MMA_WARP) {
+      // ---------------- products ----------------
+      if (lane == 0) {
+        constexpr uint32_t ID_S = idesc_f16(BF16, BN, false), ID_O = idesc_f16(BF16, D, true);
+        int n = 0, nq = 0;
+        int np[2] = {0, 0}, no[2] = {0, 0};  // weights taken and outputs begun, per tile
+        uint32_t fixed_once = 0;             // parity of each stage's `fixed`
+        auto qk = [&](int t, int st) {  // S_t = Q_t K^T
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (uint32_t)((k >> 2) * C::CHUNK + (k & 3) * 32);
+            mma_ss(tmem + t * BN, desc_sw128(q_smem + t * C::TILE + off, 16, 1024),
+                   desc_sw128(ring + st * C::TILE + off, 16, 1024), ID_S, k > 0);
+          }
+          mma_commit(s_full + 8 * t);
+        };
+        bool ok = true;
+        Work w;
+        for (int nth = 0; ok && next_work(nth, &w); ++nth) {
+          const Plan p(a, w);
+          if (p.nblocks > 0) {
+            ok = mbar_wait(q_full, nq & 1, err, a.wait_ns) &&
+                 mbar_wait(full + 8 * (n % NST), (n / NST) & 1, err, a.wait_ns);
+            if (!ok) break;
+            ++nq;
             tc_fence_after();
 #pragma unroll
-            for (int k = h * BN / 32; k < (h + 1) * BN / 32; ++k)
-              mma_ts(tmem + C::O_COL + t * D, tmem + t * BN + k * 8,
-                     desc_sw128(ring + sv * C::TILE + k * 2048, C::CHUNK, 1024), ID_O, i > 0 || k > 0);
+            for (int t = 0; t < 2; ++t)
+              if (p.blocks[t]) qk(t, n % NST);
+            mma_commit(empty + 8 * (n % NST));
+            if (p.nblocks == 1) mma_commit(q_empty);
           }
-          if (!ok) break;
-          if (i + 1 < blocks[t]) qk(t, sk);
-          else mma_commit(o_full + 8 * t);
+          for (int i = 0; i < p.nblocks && ok; ++i, n += 2) {
+            const int sv = (n + 1) % NST, sk = (n + 2) % NST;
+            ok = mbar_wait(full + 8 * sv, ((n + 1) / NST) & 1, err, a.wait_ns);
+            if (ok && i >= p.zone) {
+              ok = mbar_wait(fixed + 8 * sv, (fixed_once >> sv) & 1, err, a.wait_ns);
+              fixed_once ^= 1u << sv;
+            }
+            if (ok && i + 1 < p.nblocks) ok = mbar_wait(full + 8 * sk, ((n + 2) / NST) & 1, err, a.wait_ns);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (!ok || i >= p.blocks[t]) continue;
+              if (i == 0) {  // the last output of this tile has been read
+                if (no[t] > 0) ok = mbar_wait(o_empty + 8 * t, (no[t] - 1) & 1, err, a.wait_ns);
+                ++no[t];
+              }
+#pragma unroll
+              for (int h = 0; h < 2 && ok; ++h) {  // O_t += P_t V, a half of the keys at a time
+                ok = mbar_wait(p_full + 16 * t + 8 * h, np[t] & 1, err, a.wait_ns);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = h * BN / 32; k < (h + 1) * BN / 32; ++k)
+                  mma_ts(tmem + C::O_COL + t * D, tmem + t * BN + k * 8,
+                         desc_sw128(ring + sv * C::TILE + k * 2048, C::CHUNK, 1024), ID_O, i > 0 || k > 0);
+              }
+              if (!ok) continue;
+              ++np[t];
+              if (i + 1 < p.blocks[t]) qk(t, sk);
+              else mma_commit(o_full + 8 * t);
+            }
+            if (ok) {
+              mma_commit(empty + 8 * sv);
+              if (i + 1 < p.nblocks) mma_commit(empty + 8 * sk);
+              if (i + 2 == p.nblocks) mma_commit(q_empty);  // the pair's last scores
+            }
+          }
+          if (ok) mbar_arrive(work_empty + 8 * (nth % WORKS));
         }
-        if (ok) {
-          mma_commit(empty + 8 * sv);
-          if (i + 1 < nblocks) mma_commit(empty + 8 * sk);
-        }
-      }
-      if (!ok) {  // every product issued is done before tensor memory is freed
+        // every product issued is done before tensor memory is freed
         mma_commit(drain);
         const unsigned long long t0 = globaltimer();
         while (!mbar_try(drain, 0) && globaltimer() - t0 < a.wait_ns) {}
       }
+      __syncwarp();
     }
-    __syncwarp();
-  }
   } else {
-    more_registers<224>();
+    more_registers<208>();
     // ---------------- softmax ----------------
     const int t = warp >> 2;
     const int r = tid & 127;
-    const int pos = work.pos0 + t * P + r / G;
-    const bool live = r < P * G && pos < sq.qlen;
-    const int lim = live ? limit(pos) : -1;
-    // keys up to here are seen by every live row of the warp (rows are in position order)
-    const int first_row = (warp & 3) * 32;
-    const int clear = limit(min(work.pos0 + t * P + first_row / G, sq.qlen - 1));
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_addr = tmem + lanes + t * BN, o_addr = tmem + lanes + C::O_COL + t * D;
-    float m = NEG_INF, l = 0.0f;  // in units of log2, scaled
+    const int row_pos = r / G, row_head = r - row_pos * G;
+    const int first_pos = ((warp & 3) * 32) / G;  // of the warp's rows, which are in position order
+    int ns = 0, no = 0;                           // scores and outputs so far
     bool ok = true;
-    for (int i = 0; i < blocks[t]; ++i) {
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait(s_full + 8 * t, i & 1, err, a.wait_ns));
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t s[128];
-      tmem_ld32<0>(s_addr, s);
-      tmem_ld32<32>(s_addr + 32, s);
-      tmem_ld32<64>(s_addr + 64, s);
-      tmem_ld32<96>(s_addr + 96, s);
-      tmem_wait_ld();
-      if ((i + 1) * BN - 1 > clear) {
-        const int seen = lim - i * BN;  // columns up to here
+    Work w;
+    for (int nth = 0; ok; ++nth) {
+      if (!__all_sync(0xFFFFFFFFu, next_work(nth, &w))) break;
+      const Plan p(a, w);
+      const int blocks = t ? p.blocks[1] : p.blocks[0];
+      const int pos = w.pos0 + t * P + row_pos;
+      const bool live = r < P * G && pos < w.q.qlen;
+      const int lim = live ? p.limit(a, w, pos) : -1;
+      // keys up to here are seen by every live row of the warp
+      const int clear = p.limit(a, w, min(w.pos0 + t * P + first_pos, w.q.qlen - 1));
+      float m = NEG_INF, l = 0.0f;  // in units of log2, scaled
+      for (int i = 0; i < blocks; ++i, ++ns) {
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(s_full + 8 * t, ns & 1, err, a.wait_ns));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[128];
+        tmem_ld32<0>(s_addr, s);
+        tmem_ld32<32>(s_addr + 32, s);
+        tmem_ld32<64>(s_addr + 64, s);
+        tmem_ld32<96>(s_addr + 96, s);
+        tmem_wait_ld();
+        if ((i + 1) * BN - 1 > clear) {
+          const int seen = lim - i * BN;  // columns up to here
 #pragma unroll
-        for (int c = 0; c < BN; ++c) s[c] = c <= seen ? s[c] : __float_as_uint(NEG_INF);
-      }
-      float top[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
-#pragma unroll
-      for (int c = 0; c < BN; c += 2)
-        top[(c >> 1) & 3] = max3(top[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-      float mn = max3(fmaxf(top[0], top[1]), top[2], top[3]);
-      mn *= a.scale_log2;  // positive: checked on the host
-      if (i == 0) {
-        m = mn;
-      } else if (__any_sync(0xFFFFFFFFu, mn > m + RESCALE)) {
-        const float nm = fmaxf(m, mn);
-        const float f = m == NEG_INF ? 0.0f : ex2(m - nm);
-        m = nm;
-        l *= f;
-#pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          tmem_ld32<0>(o_addr + c, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-          tmem_st32<0>(o_addr + c, o);
+          for (int c = 0; c < BN; ++c) s[c] = c <= seen ? s[c] : __float_as_uint(NEG_INF);
         }
-      }
-      const float mm = m == NEG_INF ? 0.0f : m;
-      const F2 sc2 = f2(a.scale_log2, a.scale_log2), mm2 = f2(-mm, -mm);
-      F2 sum[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};
+        float top[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+        for (int c = 0; c < BN; c += 2)
+          top[(c >> 1) & 3] = max3(top[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+        float mn = max3(fmaxf(top[0], top[1]), top[2], top[3]);
+        mn *= a.scale_log2;  // positive: checked on the host
+        if (i == 0) {
+          m = mn;
+        } else if (__any_sync(0xFFFFFFFFu, mn > m + RESCALE)) {
+          const float nm = fmaxf(m, mn);
+          const float f = m == NEG_INF ? 0.0f : ex2(m - nm);
+          m = nm;
+          l *= f;
 #pragma unroll
-        for (int c = h * BN / 2; c < (h + 1) * BN / 2; c += 2) {
-          const float2 x = unf2(fma2(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, mm2));
-          const float p0 = ex2(x.x), p1 = ex2(x.y);
-          sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], f2(p0, p1));
-          s[c / 2] = pack2<T>(p0, p1);
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32<0>(o_addr + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st32<0>(o_addr + c, o);
+          }
         }
-        if (h == 0) tmem_st32<0>(s_addr, s);
-        else tmem_st32<32>(s_addr + 32, s);
-        tmem_wait_st();
+        const float mm = m == NEG_INF ? 0.0f : m;
+        const F2 sc2 = f2(a.scale_log2, a.scale_log2), mm2 = f2(-mm, -mm);
+        F2 sum[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int c = h * BN / 2; c < (h + 1) * BN / 2; c += 2) {
+            const float2 x = unf2(fma2(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, mm2));
+            const float p0 = ex2(x.x), p1 = ex2(x.y);
+            sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], f2(p0, p1));
+            s[c / 2] = pack2<T>(p0, p1);
+          }
+          if (h == 0) tmem_st32<0>(s_addr, s);
+          else tmem_st32<32>(s_addr + 32, s);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full + 16 * t + 8 * h);
+        }
+        const float2 l2 = unf2(add2(sum[0], sum[1]));
+        l += l2.x + l2.y;
+      }
+      // ---- O / l to memory ----
+      T* dst = static_cast<T*>(a.out) + ((int64_t)(w.q.qb + pos) * a.q_heads + w.head * G + row_head) * D;
+      if (blocks == 0) {
+        if (live)
+          for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(dst + c) = make_uint4(0u, 0u, 0u, 0u);
+      } else if (ok) {
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(o_full + 8 * t, no & 1, err, a.wait_ns));
+        if (!ok) break;
+        ++no;
+        tc_fence_after();
+        uint32_t o[D];
+        tmem_ld32<0>(o_addr, o);
+        tmem_ld32<32>(o_addr + 32, o);
+        if constexpr (D == 128) {
+          tmem_ld32<64>(o_addr + 64, o);
+          tmem_ld32<96>(o_addr + 96, o);
+        }
+        tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + 16 * t + 8 * h);
-      }
-      const float2 l2 = unf2(add2(sum[0], sum[1]));
-      l += l2.x + l2.y;
-    }
-    // ---- O / l to memory ----
-    const int hq = head * G + r % G;
-    T* dst = static_cast<T*>(a.out) + ((int64_t)(sq.qb + pos) * a.q_heads + hq) * D;
-    if (blocks[t] == 0) {
-      if (live)
-        for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(dst + c) = make_uint4(0u, 0u, 0u, 0u);
-    } else if (ok) {
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait(o_full + 8 * t, 0, err, a.wait_ns));
-      if (ok) {
-        tc_fence_after();
-        const float inv = lim < 0 ? 0.0f : 1.0f / l;
-        const bool extra = s_nonfinite != 0;
+        if (lane == 0) mbar_arrive(o_empty + 8 * t);
+        const float inv = 1.0f / l;
+        const bool extra = s_nonfinite[nth % WORKS] != 0;
+        if (live) {
 #pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          tmem_ld32<0>(o_addr + c, o);
-          tmem_wait_ld();
-          float x[32];
+          for (int c = 0; c < D; c += 8) {
+            float x[8];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = lim < 0 ? 0.0f : __uint_as_float(o[e]) * inv;
-          if (live) {
+            for (int e = 0; e < 8; ++e) x[e] = lim < 0 ? 0.0f : __uint_as_float(o[c + e]) * inv;
             if (extra) {  // what was set aside: keys that this row sees
-              const T* v = static_cast<const T*>(a.v) + (int64_t)head * a.v_head + c;
-              for (int j = first_hidden; j <= lim; ++j)
-                for (int e = 0; e < 32; ++e) {
-                  const float f = (float)v[(int64_t)(sq.kb + j) * a.v_row + e];
+              const T* v = static_cast<const T*>(a.v) + (int64_t)w.head * a.v_head + c;
+              for (int j = p.first_hidden; j <= lim; ++j)
+                for (int e = 0; e < 8; ++e) {
+                  const float f = (float)v[(int64_t)(w.q.kb + j) * a.v_row + e];
                   if (!isfinite(f)) x[e] += f;
                 }
             }
-#pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              *reinterpret_cast<uint4*>(dst + c + e) =
-                  make_uint4(pack2<T>(x[e], x[e + 1]), pack2<T>(x[e + 2], x[e + 3]), pack2<T>(x[e + 4], x[e + 5]),
-                             pack2<T>(x[e + 6], x[e + 7]));
+            *reinterpret_cast<uint4*>(dst + c) = make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]),
+                                                            pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
           }
         }
       }
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive(work_empty + 8 * (nth % WORKS));
     }
   }
 
@@ -563,8 +698,7 @@ int launch_as(const PromptAttn& c, cudaStream_t s) {
   a.wait_ns = wait_limit_ns();
   // pairs of tiles: whole ones and at most one ragged per sequence
   const int64_t ctas = c.q_total / (2 * a.positions) + (c.S < c.q_total ? c.S : c.q_total);
-  if (ctas >= INT32_MAX) return Q4_ERR_SHAPE;
-  a.ctas = (int)ctas;
+  if (ctas >= INT32_MAX / c.kv_heads) return Q4_ERR_SHAPE;
   CUtensorMap mq, mk, mv;
   // without keys nothing is read from k and v: any valid map will do
   const bool keys = c.k_total > 0;
@@ -581,7 +715,7 @@ int launch_as(const PromptAttn& c, cudaStream_t s) {
       return Q4_ERR_CUDA;
     sized[dev].store(true);
   }
-  prompt_kernel<D, T><<<dim3((unsigned)ctas + 1, c.kv_heads), THREADS, Cfg<D>::SMEM, s>>>(a, mq, mk, mv);
+  prompt_kernel<D, T><<<(unsigned)(ctas * c.kv_heads), THREADS, Cfg<D>::SMEM, s>>>(a, mq, mk, mv);
   return cudaGetLastError() == cudaSuccess ? Q4_OK : Q4_ERR_CUDA;
 }
 

@@ -174,6 +174,31 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// ---- work of CTAs that have not been launched yet ----
+// Asks for one: 16 bytes at `dst`, counted on the barrier.
+__device__ __forceinline__ void take_cta(uint32_t dst, uint32_t bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   dst),
+               "r"(bar)
+               : "memory");
+}
+// The answer: whether one was left, and its blockIdx.x.  No further one may be asked for after a no.
+__device__ __forceinline__ bool taken_cta(uint32_t src, uint32_t* x) {
+  uint32_t ok, cx;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+      ".reg .b32 y, z;\n\tld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %1, 1, 0, p;\n\t"
+      "mov.u32 %0, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, _}, r;\n\t}"
+      : "=&r"(cx), "=&r"(ok)
+      : "r"(src)
+      : "memory");
+  *x = cx;
+  return ok != 0;
+}
+
 // ---- two fp32 values in one 64-bit register: one instruction for both ----
 using F2 = unsigned long long;
 __device__ __forceinline__ F2 f2(float a, float b) {
