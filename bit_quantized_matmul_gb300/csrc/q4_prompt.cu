@@ -15,30 +15,34 @@
 // blocks of 128; when it is done with them it takes over a pair of tiles that
 // another CTA of the launch was to do and has not begun (the longest come
 // first), so that the copies and first products of one pair run under the end
-// of the last one.  Roles (384 threads, three warpgroups):
-//   warps 0-3, 4-7  softmax of tile 0 / tile 1: a thread owns one row, so its
-//                   maximum and sum need no exchange.  S comes from tensor
-//                   memory, the weights go back over it as 16-bit values (the A
-//                   operand of the second product), and the accumulator O
-//                   stays in tensor memory.  O is rescaled only when a row's
-//                   maximum has grown by more than 2^8 since the last time:
-//                   the factor is kept in the sum as well, so the result is
-//                   the same softmax.
-//   warp 8          copies Q, and K and V through a ring of blocks, by TMA
-//                   tensor maps with the 128-byte swizzle
-//   warp 9          issues the products: S of one tile while the other tile's
-//                   softmax runs
-//   warp 10         finds the work
-// The launch gives each thread 168 registers; the softmax warpgroups take 208
-// and leave the third 88 (2 * 208 + 88 = 3 * 168), so a row of scores stays in
-// registers.  Weights are handed over in two halves, so the second product
-// starts while the second half is computed.
+// of the last one.  Roles (640 threads, five warpgroups):
+//   warps 0-15  softmax: warpgroups 0 and 1 have the two halves of tile 0's key
+//               columns, 2 and 3 those of tile 1; a thread owns half a row.  S
+//               comes from tensor memory, the weights go back over it as 16-bit
+//               values (the A operand of the second product), and the
+//               accumulator O stays in tensor memory.  The scores are taken
+//               relative to a reference, the row's maximum of some earlier
+//               block; only when a score passes it by more than 2^8 do the
+//               halves exchange their maxima and rescale O (the sum keeps the
+//               factor, so the result is the same softmax).  One barrier with a
+//               vote per block tells both halves.
+//   warp 16     copies Q, and K and V through a ring of blocks, by TMA tensor
+//               maps with the 128-byte swizzle
+//   warp 17     issues the products: S of one tile while the other tile's
+//               softmax runs; the second product of a half of the keys starts
+//               when its weights are there
+//   warp 18     finds the work
+//   warp 19     looks after masked places in V (below)
+// The launch gives each thread 96 registers; the softmax warpgroups take 104
+// and leave the fifth 64 (4 * 104 + 64 = 5 * 96).
+// With one thread a row (two softmax warpgroups), a block took 1.4 times as
+// long: the chain from scores to weights is a single warp's latency.
 // The products of a CTA run in order, so when S of block i + 1 is there, the
 // accumulation of block i is done and O may be rescaled without a wait.
 //
 // Masked places.  Scores past a row's limit are replaced, not added to.  A
 // weight of 0 times a NaN of V would still be NaN, so in blocks where some row
-// has such a limit warp 8 clears what V holds past the sequence, and sets
+// has such a limit warp 19 clears what V holds past the sequence, and sets
 // aside infinities and NaN of rows that only some of the tile's rows see (they
 // are added back at the end to the rows that do see them).
 #include <cuda.h>
@@ -56,9 +60,10 @@ namespace {
 
 constexpr int BM = 128;                 // packed rows per tile
 constexpr int BN = 128;                 // keys per block
-constexpr int TMA_WARP = 8, MMA_WARP = 9, WORK_WARP = 10;
+constexpr int SOFTMAX_WARPS = 16;
+constexpr int TMA_WARP = 16, MMA_WARP = 17, WORK_WARP = 18, FIX_WARP = 19;
 constexpr int WORKS = 2;                // the pair under way and the next one
-constexpr int THREADS = 384;
+constexpr int THREADS = 640;
 constexpr int TMEM_COLS = 512;
 constexpr float NEG_INF = -INFINITY;
 constexpr float RESCALE = 8.0f;         // log2 of the growth that triggers a rescale
@@ -218,6 +223,21 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+// Barrier of a tile's 256 softmax threads; with a vote: whether any says yes.
+__device__ __forceinline__ void tile_sync(int t) { asm volatile("bar.sync %0, 256;" ::"r"(1 + t) : "memory"); }
+__device__ __forceinline__ bool tile_vote(int t, bool yes) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "bar.red.or.pred q, %1, 256, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(1 + t), "r"((uint32_t)yes)
+      : "memory");
+  return any != 0;
+}
+
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   if constexpr (std::is_same<T, __half>::value) {
@@ -229,11 +249,13 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   }
 }
 
-// Whether a pair of 16-bit values holds an infinity or a NaN.
+// Whether eight 16-bit values hold an infinity or a NaN: an exponent of all
+// ones carries into the sign's place when one is added.
 template <typename T>
-__device__ __forceinline__ bool nonfinite2(uint32_t w) {
-  constexpr uint32_t E = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
-  return (w & E) == E || ((w >> 16) & E) == E;
+__device__ __forceinline__ bool nonfinite8(const uint4& v) {
+  constexpr uint32_t E = std::is_same<T, __half>::value ? 0x7C007C00u : 0x7F807F80u;
+  constexpr uint32_t ONE = std::is_same<T, __half>::value ? 0x04000400u : 0x00800080u;
+  return ((((v.x & E) + ONE) | ((v.y & E) + ONE) | ((v.z & E) + ONE) | ((v.w & E) + ONE)) & 0x80008000u) != 0;
 }
 
 // A pair with infinities and NaN replaced by 0.
@@ -256,6 +278,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   __shared__ Work work[WORKS];
   __shared__ __align__(16) uint4 taken;
   __shared__ int s_err, s_nonfinite[WORKS];
+  __shared__ float s_max[2][2][BM], s_sum[2][2][BM];  // [tile][half][row]: what the halves exchange
   __shared__ uint32_t s_tmem;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = a.group, P = a.positions;
@@ -264,7 +287,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint8_t* smem_p = smem_raw + (smem - smem_u32(smem_raw));
   const uint32_t q_smem = smem, ring = smem + 2 * C::TILE, bars = smem + C::BAR_OFF;
   const uint32_t q_full = bars, q_empty = q_full + 8, drain = q_empty + 8, answer = drain + 8;
-  const uint32_t full = answer + 8, empty = full + 8 * NST, fixed = empty + 8 * NST;
+  const uint32_t full = answer + 8, empty = full + 8 * NST, hidden = empty + 8 * NST, fixed = hidden + 8 * NST;
   const uint32_t s_full = fixed + 8 * NST, p_full = s_full + 16, o_full = p_full + 32, o_empty = o_full + 16;
   const uint32_t work_full = o_empty + 16, work_empty = work_full + 8 * WORKS;
   volatile int* err = &s_err;
@@ -276,6 +299,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int i = 0; i < NST; ++i) {
       mbar_init(full + 8 * i, 1);
       mbar_init(empty + 8 * i, 1);
+      mbar_init(hidden + 8 * i, 1);
       mbar_init(fixed + 8 * i, 1);
     }
     for (int t = 0; t < 2; ++t) {
@@ -283,11 +307,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(p_full + 16 * t, 4);
       mbar_init(p_full + 16 * t + 8, 4);
       mbar_init(o_full + 8 * t, 1);
-      mbar_init(o_empty + 8 * t, 4);
+      mbar_init(o_empty + 8 * t, 8);
     }
     for (int i = 0; i < WORKS; ++i) {
       mbar_init(work_full + 8 * i, 1);
-      mbar_init(work_empty + 8 * i, 10);  // the copies', the products' and eight softmax warps
+      mbar_init(work_empty + 8 * i, SOFTMAX_WARPS + 3);  // and the copies', the products' and V's warps
       s_nonfinite[i] = 0;
     }
     s_err = 0;
@@ -308,7 +332,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   };
 
   if (warp >= TMA_WARP) {
-    fewer_registers<88>();
+    fewer_registers<64>();
     if (warp == WORK_WARP) {
       // ---------------- work ----------------
       Finder f;
@@ -388,35 +412,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int c = 0; c < C::CHUNKS; ++c)
                   tensor_load(ring + st * C::TILE + c * C::CHUNK, kv ? (const void*)&map_v : (const void*)&map_k,
                               64 * c, w.head, sq.kb + i * BN, full + 8 * st);
+                if (kv && i >= p.zone) mbar_arrive(hidden + 8 * st);  // tells V's warp, which only waits for these
               }
             }
             ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0) != 0;
             if (ok) ++n;
-          }
-          if (ok && i >= p.zone) {  // make V safe to multiply with weights of 0
-            const int st = (n - 1) % NST;
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(full + 8 * st, ((n - 1) / NST) & 1, err, a.wait_ns));
-            if (!ok) break;
-            const int r0 = max(0, p.first_hidden - i * BN), end = min(BN, sq.klen - i * BN);
-            uint8_t* vb = smem_p + (ring - smem) + st * C::TILE;
-            bool found = false;
-            for (int it = lane; it < (BN - r0) * C::CHUNKS * 8; it += 32) {
-              const int row = r0 + it / (C::CHUNKS * 8), e = it % (C::CHUNKS * 8);
-              uint4* x = reinterpret_cast<uint4*>(vb + (e >> 3) * C::CHUNK + row * 128 + ((e & 7) ^ (row & 7)) * 16);
-              if (row >= end) {
-                *x = make_uint4(0u, 0u, 0u, 0u);
-              } else {
-                const uint4 v = *x;
-                if (nonfinite2<T>(v.x) || nonfinite2<T>(v.y) || nonfinite2<T>(v.z) || nonfinite2<T>(v.w)) {
-                  found = true;
-                  *x = make_uint4(finite2<T>(v.x), finite2<T>(v.y), finite2<T>(v.z), finite2<T>(v.w));
-                }
-              }
-            }
-            if (found) atomicExch(&s_nonfinite[nth % WORKS], 1);
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive(fixed + 8 * st);
           }
         }
         __syncwarp();
@@ -425,6 +425,55 @@ __global__ void __launch_bounds__(THREADS, 1)
       // the copies in flight land before the CTA ends, also when another role has given up
       if (nq > 0) mbar_wait_warp(q_full, (nq - 1) & 1, a.wait_ns);
       for (int v = max(0, n - NST); v < n; ++v) mbar_wait_warp(full + 8 * (v % NST), (v / NST) & 1, a.wait_ns);
+    } else if (warp == FIX_WARP) {
+      // ---------------- V in masked places: safe to multiply with weights of 0 ----------------
+      int n = 0;
+      uint32_t seen_once = 0;  // parity of each stage's `hidden`
+      bool ok = true;
+      Work w;
+      for (int nth = 0; ok; ++nth) {
+        if (!__all_sync(0xFFFFFFFFu, next_work(nth, &w))) break;
+        const Plan p(a, w);
+        for (int i = p.zone; i < p.nblocks; ++i) {
+          const int v = n + 2 * i + 1, st = v % NST;
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(hidden + 8 * st, (seen_once >> st) & 1, err, a.wait_ns) &&
+                                           mbar_wait(full + 8 * st, (v / NST) & 1, err, a.wait_ns));
+          seen_once ^= 1u << st;
+          if (!ok) break;
+          const int r0 = max(0, p.first_hidden - i * BN), end = min(BN, w.q.klen - i * BN);
+          uint8_t* vb = smem_p + (ring - smem) + st * C::TILE;
+          constexpr int VPR = C::CHUNKS * 8;  // 16-byte vectors per row
+          auto at = [&](int row, int e) {
+            return reinterpret_cast<uint4*>(vb + (e >> 3) * C::CHUNK + row * 128 + ((e & 7) ^ (row & 7)) * 16);
+          };
+          const int e = lane % VPR;
+          bool found = false;
+          for (int row = r0 + lane / VPR; row < end; row += 4 * (32 / VPR)) {
+            uint4 x[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int ru = row + u * (32 / VPR);
+              x[u] = ru < end ? *at(ru, e) : make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              if (nonfinite8<T>(x[u])) {
+                found = true;
+                *at(row + u * (32 / VPR), e) =
+                    make_uint4(finite2<T>(x[u].x), finite2<T>(x[u].y), finite2<T>(x[u].z), finite2<T>(x[u].w));
+              }
+            }
+          }
+          for (int row = max(r0, end) + lane / VPR; row < BN; row += 32 / VPR) *at(row, e) = make_uint4(0u, 0u, 0u, 0u);
+          if (found) atomicExch(&s_nonfinite[nth % WORKS], 1);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(fixed + 8 * st);
+        }
+        n += 2 * p.nblocks;
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(work_empty + 8 * (nth % WORKS));
+      }
     } else if (warp == MMA_WARP) {
       // ---------------- products ----------------
       if (lane == 0) {
@@ -479,7 +528,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tc_fence_after();
 #pragma unroll
                 for (int k = h * BN / 32; k < (h + 1) * BN / 32; ++k)
-                  mma_ts(tmem + C::O_COL + t * D, tmem + t * BN + k * 8,
+                  mma_ts(tmem + C::O_COL + t * D, tmem + t * BN + h * (BN / 2) + (k - h * BN / 32) * 8,
                          desc_sw128(ring + sv * C::TILE + k * 2048, C::CHUNK, 1024), ID_O, i > 0 || k > 0);
               }
               if (!ok) continue;
@@ -503,19 +552,24 @@ __global__ void __launch_bounds__(THREADS, 1)
       __syncwarp();
     }
   } else {
-    more_registers<208>();
+    more_registers<104>();
     // ---------------- softmax ----------------
-    const int t = warp >> 2;
+    // A thread that gives up stays in the loops and takes part in the tile's
+    // barriers; the vote at the next pair's beginning ends both halves together.
+    constexpr int HN = BN / 2, HD = D / 2;  // columns of S and of O that a thread has
+    const int t = warp >> 3, h = (warp >> 2) & 1;
     const int r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_addr = tmem + lanes + t * BN, o_addr = tmem + lanes + C::O_COL + t * D;
+    const uint32_t s_addr = tmem + lanes + t * BN + h * HN;
+    const uint32_t o_addr = tmem + lanes + C::O_COL + t * D + h * HD;
     const int row_pos = r / G, row_head = r - row_pos * G;
     const int first_pos = ((warp & 3) * 32) / G;  // of the warp's rows, which are in position order
     int ns = 0, no = 0;                           // scores and outputs so far
     bool ok = true;
     Work w;
-    for (int nth = 0; ok; ++nth) {
-      if (!__all_sync(0xFFFFFFFFu, next_work(nth, &w))) break;
+    for (int nth = 0;; ++nth) {
+      ok = ok && next_work(nth, &w);
+      if (tile_vote(t, !ok)) break;
       const Plan p(a, w);
       const int blocks = t ? p.blocks[1] : p.blocks[0];
       const int pos = w.pos0 + t * P + row_pos;
@@ -525,104 +579,120 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int clear = p.limit(a, w, min(w.pos0 + t * P + first_pos, w.q.qlen - 1));
       float m = NEG_INF, l = 0.0f;  // in units of log2, scaled
       for (int i = 0; i < blocks; ++i, ++ns) {
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(s_full + 8 * t, ns & 1, err, a.wait_ns));
-        if (!ok) break;
-        tc_fence_after();
-        uint32_t s[128];
-        tmem_ld32<0>(s_addr, s);
-        tmem_ld32<32>(s_addr + 32, s);
-        tmem_ld32<64>(s_addr + 64, s);
-        tmem_ld32<96>(s_addr + 96, s);
-        tmem_wait_ld();
-        if ((i + 1) * BN - 1 > clear) {
-          const int seen = lim - i * BN;  // columns up to here
+        ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(s_full + 8 * t, ns & 1, err, a.wait_ns));
+        const int c0 = i * BN + h * HN, seen = lim - c0;  // columns up to `seen` count
+        const bool masked = c0 + HN - 1 > clear;
+        // 32 scores, again from tensor memory for the weights: registers for all 64 would spill
+        auto scores = [&](int c, uint32_t (&s)[32]) {
+          tmem_ld32<0>(s_addr + c, s);
+          tmem_wait_ld();
+          if (masked) {
 #pragma unroll
-          for (int c = 0; c < BN; ++c) s[c] = c <= seen ? s[c] : __float_as_uint(NEG_INF);
+            for (int e = 0; e < 32; ++e) s[e] = c + e <= seen ? s[e] : __float_as_uint(NEG_INF);
+          }
+        };
+        float mn = NEG_INF;
+        if (ok) {
+          tc_fence_after();
+          float top[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
+#pragma unroll
+          for (int c = 0; c < HN; c += 32) {
+            uint32_t s[32];
+            scores(c, s);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2)
+              top[(e >> 1) & 3] = max3(top[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+          }
+          mn = max3(fmaxf(top[0], top[1]), top[2], top[3]) * a.scale_log2;  // positive: checked on the host
         }
-        float top[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
-#pragma unroll
-        for (int c = 0; c < BN; c += 2)
-          top[(c >> 1) & 3] = max3(top[(c >> 1) & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-        float mn = max3(fmaxf(top[0], top[1]), top[2], top[3]);
-        mn *= a.scale_log2;  // positive: checked on the host
-        if (i == 0) {
-          m = mn;
-        } else if (__any_sync(0xFFFFFFFFu, mn > m + RESCALE)) {
-          const float nm = fmaxf(m, mn);
+        if (tile_vote(t, i == 0 || mn > m + RESCALE)) {
+          s_max[t][h][r] = mn;
+          tile_sync(t);
+          const float nm = max3(m, mn, s_max[t][1 - h][r]);
           const float f = m == NEG_INF ? 0.0f : ex2(m - nm);
           m = nm;
-          l *= f;
+          if (i > 0) {
+            l *= f;
+            if (ok) {
 #pragma unroll
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tmem_ld32<0>(o_addr + c, o);
-            tmem_wait_ld();
+              for (int c = 0; c < HD; c += 16) {
+                uint32_t o[16];
+                tmem_ld16(o_addr + c, o);
+                tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st32<0>(o_addr + c, o);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st16(o_addr + c, o);
+              }
+              tmem_wait_st();
+              tc_fence_before();
+            }
+            tile_sync(t);  // a half's weights go to all of O: both halves of it are rescaled before
           }
         }
-        const float mm = m == NEG_INF ? 0.0f : m;
-        const F2 sc2 = f2(a.scale_log2, a.scale_log2), mm2 = f2(-mm, -mm);
-        F2 sum[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};
+        if (ok) {
+          const float mm = m == NEG_INF ? 0.0f : m;
+          const F2 sc2 = f2(a.scale_log2, a.scale_log2), mm2 = f2(-mm, -mm);
+          F2 sum[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+          for (int c = 0; c < HN; c += 32) {
+            uint32_t s[32], q[16];
+            scores(c, s);
 #pragma unroll
-          for (int c = h * BN / 2; c < (h + 1) * BN / 2; c += 2) {
-            const float2 x = unf2(fma2(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, mm2));
-            const float p0 = ex2(x.x), p1 = ex2(x.y);
-            sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], f2(p0, p1));
-            s[c / 2] = pack2<T>(p0, p1);
+            for (int e = 0; e < 32; e += 2) {
+              const float2 x = unf2(fma2(f2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sc2, mm2));
+              const float p0 = ex2(x.x), p1 = ex2(x.y);
+              sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], f2(p0, p1));
+              q[e / 2] = pack2<T>(p0, p1);
+            }
+            tmem_st16(s_addr + c / 2, q);  // over scores that this thread has read
           }
-          if (h == 0) tmem_st32<0>(s_addr, s);
-          else tmem_st32<32>(s_addr + 32, s);
+          const float2 l2 = unf2(add2(sum[0], sum[1]));
+          l += l2.x + l2.y;
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(p_full + 16 * t + 8 * h);
         }
-        const float2 l2 = unf2(add2(sum[0], sum[1]));
-        l += l2.x + l2.y;
       }
       // ---- O / l to memory ----
-      T* dst = static_cast<T*>(a.out) + ((int64_t)(w.q.qb + pos) * a.q_heads + w.head * G + row_head) * D;
+      T* dst = static_cast<T*>(a.out) + ((int64_t)(w.q.qb + pos) * a.q_heads + w.head * G + row_head) * D + h * HD;
       if (blocks == 0) {
         if (live)
-          for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(dst + c) = make_uint4(0u, 0u, 0u, 0u);
-      } else if (ok) {
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(o_full + 8 * t, no & 1, err, a.wait_ns));
-        if (!ok) break;
+          for (int c = 0; c < HD; c += 8) *reinterpret_cast<uint4*>(dst + c) = make_uint4(0u, 0u, 0u, 0u);
+      } else {
+        s_sum[t][h][r] = l;
+        tile_sync(t);
+        l += s_sum[t][1 - h][r];
+        ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(o_full + 8 * t, no & 1, err, a.wait_ns));
         ++no;
-        tc_fence_after();
-        uint32_t o[D];
-        tmem_ld32<0>(o_addr, o);
-        tmem_ld32<32>(o_addr + 32, o);
-        if constexpr (D == 128) {
-          tmem_ld32<64>(o_addr + 64, o);
-          tmem_ld32<96>(o_addr + 96, o);
-        }
-        tmem_wait_ld();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(o_empty + 8 * t);
-        const float inv = 1.0f / l;
-        const bool extra = s_nonfinite[nth % WORKS] != 0;
-        if (live) {
+        if (ok) {
+          tc_fence_after();
+          uint32_t o[HD];
+          tmem_ld32<0>(o_addr, o);
+          if constexpr (D == 128) tmem_ld32<32>(o_addr + 32, o);
+          tmem_wait_ld();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(o_empty + 8 * t);
+          const float inv = 1.0f / l;
+          const bool extra = s_nonfinite[nth % WORKS] != 0;
+          if (live) {
 #pragma unroll
-          for (int c = 0; c < D; c += 8) {
-            float x[8];
+            for (int c = 0; c < HD; c += 8) {
+              float x[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = lim < 0 ? 0.0f : __uint_as_float(o[c + e]) * inv;
-            if (extra) {  // what was set aside: keys that this row sees
-              const T* v = static_cast<const T*>(a.v) + (int64_t)w.head * a.v_head + c;
-              for (int j = p.first_hidden; j <= lim; ++j)
-                for (int e = 0; e < 8; ++e) {
-                  const float f = (float)v[(int64_t)(w.q.kb + j) * a.v_row + e];
-                  if (!isfinite(f)) x[e] += f;
-                }
+              for (int e = 0; e < 8; ++e) x[e] = lim < 0 ? 0.0f : __uint_as_float(o[c + e]) * inv;
+              if (extra) {  // what was set aside: keys that this row sees
+                const T* v = static_cast<const T*>(a.v) + (int64_t)w.head * a.v_head + h * HD + c;
+                for (int j = p.first_hidden; j <= lim; ++j)
+                  for (int e = 0; e < 8; ++e) {
+                    const float f = (float)v[(int64_t)(w.q.kb + j) * a.v_row + e];
+                    if (!isfinite(f)) x[e] += f;
+                  }
+              }
+              *reinterpret_cast<uint4*>(dst + c) = make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]),
+                                                              pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
             }
-            *reinterpret_cast<uint4*>(dst + c) = make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]),
-                                                            pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
           }
         }
       }
