@@ -481,14 +481,25 @@ __global__ void __launch_bounds__(THREADS, 1)
         int n = 0, nq = 0;
         int np[2] = {0, 0}, no[2] = {0, 0};  // weights taken and outputs begun, per tile
         uint32_t fixed_once = 0;             // parity of each stage's `fixed`
+        // Descriptors are bases plus constants (the address field counts 16 bytes, and no
+        // address carries out of it): put together anew for each product they took
+        // longer to make than the product takes.
+        const uint64_t q_desc = desc_sw128(q_smem, 16, 1024), k_desc = desc_sw128(ring, 16, 1024);
+        const uint64_t v_desc = desc_sw128(ring, C::CHUNK, 1024);
+        constexpr uint32_t TILE16 = C::TILE / 16, CHUNK16 = C::CHUNK / 16;
         auto qk = [&](int t, int st) {  // S_t = Q_t K^T
+          const uint64_t q = q_desc + t * TILE16, kd = k_desc + st * TILE16;
+          const uint32_t d = tmem + t * BN;
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (uint32_t)((k >> 2) * C::CHUNK + (k & 3) * 32);
-            mma_ss(tmem + t * BN, desc_sw128(q_smem + t * C::TILE + off, 16, 1024),
-                   desc_sw128(ring + st * C::TILE + off, 16, 1024), ID_S, k > 0);
-          }
+          for (int k = 0; k < D / 16; ++k)
+            mma_ss(d, q + ((k >> 2) * CHUNK16 + (k & 3) * 2), kd + ((k >> 2) * CHUNK16 + (k & 3) * 2), ID_S, k > 0);
           mma_commit(s_full + 8 * t);
+        };
+        auto pv = [&](int t, int st, int h, bool first) {  // O_t += P_t V, a half of the keys
+          const uint64_t v = v_desc + (st * TILE16 + h * (BN / 2) * 8);
+          const uint32_t d = tmem + C::O_COL + t * D, a = tmem + t * BN + h * (BN / 2);
+#pragma unroll
+          for (int k = 0; k < BN / 32; ++k) mma_ts(d, a + k * 8, v + k * 128, ID_O, !first || k > 0);
         };
         bool ok = true;
         Work w;
@@ -526,10 +537,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 ok = mbar_wait(p_full + 16 * t + 8 * h, np[t] & 1, err, a.wait_ns);
                 if (!ok) break;
                 tc_fence_after();
-#pragma unroll
-                for (int k = h * BN / 32; k < (h + 1) * BN / 32; ++k)
-                  mma_ts(tmem + C::O_COL + t * D, tmem + t * BN + h * (BN / 2) + (k - h * BN / 32) * 8,
-                         desc_sw128(ring + sv * C::TILE + k * 2048, C::CHUNK, 1024), ID_O, i > 0 || k > 0);
+                pv(t, sv, h, i == 0 && h == 0);
               }
               if (!ok) continue;
               ++np[t];
