@@ -26,18 +26,18 @@
 //               halves exchange their maxima and rescale O (the sum keeps the
 //               factor, so the result is the same softmax).  One barrier with a
 //               vote per block tells both halves.
-//   warp 16     copies Q, and K and V through a ring of blocks, by TMA tensor
-//               maps with the 128-byte swizzle
-//   warp 17     issues the products: S of one tile while the other tile's
-//               softmax runs; the second product of a half of the keys starts
-//               when its weights are there
-//   warp 18     finds the work
+//   warp 16     finds the work and copies Q, and K and V through a ring of
+//               blocks, by TMA tensor maps with the 128-byte swizzle
+//   warps 17,18 issue the products of tile 0 / tile 1, S of one tile while the
+//               other tile's softmax runs; the second product of a half of the
+//               keys starts when its weights are there.  (One warp for both
+//               tiles lost a quarter of the time to its waits and commits.)
 //   warp 19     looks after masked places in V (below)
 // The launch gives each thread 96 registers; the softmax warpgroups take 104
 // and leave the fifth 64 (4 * 104 + 64 = 5 * 96).
 // With one thread a row (two softmax warpgroups), a block took 1.4 times as
 // long: the chain from scores to weights is a single warp's latency.
-// The products of a CTA run in order, so when S of block i + 1 is there, the
+// The products of a tile run in order, so when S of block i + 1 is there, the
 // accumulation of block i is done and O may be rescaled without a wait.
 //
 // Masked places.  Scores past a row's limit are replaced, not added to.  A
@@ -61,8 +61,8 @@ namespace {
 constexpr int BM = 128;                 // packed rows per tile
 constexpr int BN = 128;                 // keys per block
 constexpr int SOFTMAX_WARPS = 16;
-constexpr int TMA_WARP = 16, MMA_WARP = 17, WORK_WARP = 18, FIX_WARP = 19;
-constexpr int WORKS = 2;                // the pair under way and the next one
+constexpr int TMA_WARP = 16, MMA_WARP = 17, FIX_WARP = 19;  // and MMA_WARP + 1
+constexpr int WORKS = 2;                // the pair that is copied and the one before
 constexpr int THREADS = 640;
 constexpr int TMEM_COLS = 512;
 constexpr float NEG_INF = -INFINITY;
@@ -280,7 +280,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   __shared__ int s_err, s_nonfinite[WORKS];
   __shared__ float s_max[2][2][BM], s_sum[2][2][BM];  // [tile][half][row]: what the halves exchange
   __shared__ uint32_t s_tmem;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // one value for the warp, as far as the compiler can see
   const int G = a.group, P = a.positions;
 
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -289,16 +290,16 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t q_full = bars, q_empty = q_full + 8, drain = q_empty + 8, answer = drain + 8;
   const uint32_t full = answer + 8, empty = full + 8 * NST, hidden = empty + 8 * NST, fixed = hidden + 8 * NST;
   const uint32_t s_full = fixed + 8 * NST, p_full = s_full + 16, o_full = p_full + 32, o_empty = o_full + 16;
-  const uint32_t work_full = o_empty + 16, work_empty = work_full + 8 * WORKS;
+  const uint32_t turn = o_empty + 16, work_full = turn + 16, work_empty = work_full + 8 * WORKS;
   volatile int* err = &s_err;
   if (tid == 0) {
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
-    mbar_init(drain, 1);
+    mbar_init(q_empty, 2);
+    mbar_init(drain, 2);
     mbar_init(answer, 1);
     for (int i = 0; i < NST; ++i) {
       mbar_init(full + 8 * i, 1);
-      mbar_init(empty + 8 * i, 1);
+      mbar_init(empty + 8 * i, 2);
       mbar_init(hidden + 8 * i, 1);
       mbar_init(fixed + 8 * i, 1);
     }
@@ -308,12 +309,14 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(p_full + 16 * t + 8, 4);
       mbar_init(o_full + 8 * t, 1);
       mbar_init(o_empty + 8 * t, 8);
+      mbar_init(turn + 8 * t, 1);
     }
     for (int i = 0; i < WORKS; ++i) {
       mbar_init(work_full + 8 * i, 1);
-      mbar_init(work_empty + 8 * i, SOFTMAX_WARPS + 3);  // and the copies', the products' and V's warps
+      mbar_init(work_empty + 8 * i, SOFTMAX_WARPS + 3);  // and the products' and V's warps
       s_nonfinite[i] = 0;
     }
+    mbar_arrive(turn);  // tile 0 begins
     s_err = 0;
     mbar_init_fence();
   }
@@ -331,38 +334,81 @@ __global__ void __launch_bounds__(THREADS, 1)
     return w->ok != 0;
   };
 
+  // One pair's copies, by one warp: n blocks and nq Q pairs so far.
+  auto copy_pair = [&](const Work& w, int& n, int& nq, bool& ok) {
+    const Plan p(a, w);
+    const Seq sq = w.q;
+    if (p.nblocks > 0) {
+      if (lane == 0) {
+        if (nq > 0) ok = mbar_wait(q_empty, (nq - 1) & 1, err, a.wait_ns);
+        if (ok) {
+          uint32_t bytes = 0;
+          for (int t = 0; t < 2; ++t)
+            if (p.blocks[t]) bytes += (uint32_t)(C::CHUNKS * P * G * 128);
+          mbar_expect_tx(q_full, bytes);
+          for (int t = 0; t < 2; ++t)
+            if (p.blocks[t])
+              for (int c = 0; c < C::CHUNKS; ++c)
+                tensor_load(q_smem + t * C::TILE + c * C::CHUNK, &map_q, 64 * c, w.head * G,
+                            sq.qb + w.pos0 + t * P, q_full);
+        }
+      }
+      ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0) != 0;
+      if (ok) ++nq;
+    }
+    for (int i = 0; i < p.nblocks && ok; ++i) {
+      for (int kv = 0; kv < 2 && ok; ++kv) {
+        const int st = n % NST;
+        if (lane == 0) {
+          if (n >= NST) ok = mbar_wait(empty + 8 * st, ((n / NST) - 1) & 1, err, a.wait_ns);
+          if (ok) {
+            mbar_expect_tx(full + 8 * st, C::TILE);
+            for (int c = 0; c < C::CHUNKS; ++c)
+              tensor_load(ring + st * C::TILE + c * C::CHUNK, kv ? (const void*)&map_v : (const void*)&map_k,
+                          64 * c, w.head, sq.kb + i * BN, full + 8 * st);
+            if (kv && i >= p.zone) mbar_arrive(hidden + 8 * st);  // tells V's warp, which only waits for these
+          }
+        }
+        ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0) != 0;
+        if (ok) ++n;
+      }
+    }
+  };
+
   if (warp >= TMA_WARP) {
     fewer_registers<64>();
-    if (warp == WORK_WARP) {
-      // ---------------- work ----------------
+    if (warp == TMA_WARP) {
+      // ---------------- work and copies ----------------
       Finder f;
       f.begin(a, lane);
+      int n = 0, nq = 0;  // blocks and Q pairs so far
+      int nth = 0;        // pairs so far
+      bool ok = true, more = true;
       uint32_t index = blockIdx.x;
-      bool more = true;
-      int nth = 0;
-      for (int asked = 0; more; ++asked) {
+      for (int asked = 0; ok && more; ++asked) {
+        if (lane == 0) {  // the answer is wanted when this pair's copies are under way
+          mbar_expect_tx(answer, 16);
+          take_cta(smem_u32(&taken), answer);
+        }
+        __syncwarp();
         Work w;
-        if (f.find(a, (int)(index / a.kv_heads), lane, &w)) {
-          if (lane == 0) {
-            w.head = (int)(index % a.kv_heads);
+        const bool found = f.find(a, (int)(index / a.kv_heads), lane, &w);
+        w.head = (int)(index % a.kv_heads);
+        if (f.gaps) clear_rows<D, T>(a, (int64_t)index * 32 + lane, (int64_t)gridDim.x * 32);
+        if (found) {
+          if (nth >= WORKS) {  // every role is done with the pair that had the slot
+            const int v = nth - WORKS;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(work_empty + 8 * (v % WORKS), (v / WORKS) & 1, err, a.wait_ns));
+          }
+          if (ok && lane == 0) {
             work[nth % WORKS] = w;
             s_nonfinite[nth % WORKS] = 0;
             mbar_arrive(work_full + 8 * (nth % WORKS));
           }
           __syncwarp();
+          if (ok) copy_pair(w, n, nq, ok);
           ++nth;
         }
-        if (f.gaps) clear_rows<D, T>(a, (int64_t)index * 32 + lane, (int64_t)gridDim.x * 32);
-        // one pair is under way and one waits: take another only when the first is done
-        if (nth >= WORKS) {
-          const int v = nth - WORKS;
-          if (!__all_sync(0xFFFFFFFFu, mbar_wait(work_empty + 8 * (v % WORKS), (v / WORKS) & 1, err, a.wait_ns))) break;
-        }
-        if (lane == 0) {
-          mbar_expect_tx(answer, 16);
-          take_cta(smem_u32(&taken), answer);
-        }
-        __syncwarp();
         if (!mbar_wait_warp(answer, asked & 1, a.wait_ns)) {
           *err = 1;
           break;
@@ -371,56 +417,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
       }
-      if (!more && lane == 0) {  // its slot is free: waited for above, or never used
-        work[nth % WORKS].ok = 0;
-        mbar_arrive(work_full + 8 * (nth % WORKS));
-      }
-    } else if (warp == TMA_WARP) {
-      // ---------------- copies ----------------
-      int n = 0, nq = 0;        // blocks and Q pairs so far
-      bool ok = true;
-      Work w;
-      for (int nth = 0; ok; ++nth) {
-        if (!__all_sync(0xFFFFFFFFu, next_work(nth, &w))) break;
-        const Plan p(a, w);
-        const Seq sq = w.q;
-        if (p.nblocks > 0) {
-          if (lane == 0) {
-            if (nq > 0) ok = mbar_wait(q_empty, (nq - 1) & 1, err, a.wait_ns);
-            if (ok) {
-              uint32_t bytes = 0;
-              for (int t = 0; t < 2; ++t)
-                if (p.blocks[t]) bytes += (uint32_t)(C::CHUNKS * P * G * 128);
-              mbar_expect_tx(q_full, bytes);
-              for (int t = 0; t < 2; ++t)
-                if (p.blocks[t])
-                  for (int c = 0; c < C::CHUNKS; ++c)
-                    tensor_load(q_smem + t * C::TILE + c * C::CHUNK, &map_q, 64 * c, w.head * G,
-                                sq.qb + w.pos0 + t * P, q_full);
-            }
-          }
-          ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0) != 0;
-          if (ok) ++nq;
+      if (ok && !more) {
+        if (nth >= WORKS) {
+          const int v = nth - WORKS;
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(work_empty + 8 * (v % WORKS), (v / WORKS) & 1, err, a.wait_ns));
         }
-        for (int i = 0; i < p.nblocks && ok; ++i) {
-          for (int kv = 0; kv < 2 && ok; ++kv) {
-            const int st = n % NST;
-            if (lane == 0) {
-              if (n >= NST) ok = mbar_wait(empty + 8 * st, ((n / NST) - 1) & 1, err, a.wait_ns);
-              if (ok) {
-                mbar_expect_tx(full + 8 * st, C::TILE);
-                for (int c = 0; c < C::CHUNKS; ++c)
-                  tensor_load(ring + st * C::TILE + c * C::CHUNK, kv ? (const void*)&map_v : (const void*)&map_k,
-                              64 * c, w.head, sq.kb + i * BN, full + 8 * st);
-                if (kv && i >= p.zone) mbar_arrive(hidden + 8 * st);  // tells V's warp, which only waits for these
-              }
-            }
-            ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0) != 0;
-            if (ok) ++n;
-          }
+        if (ok && lane == 0) {
+          work[nth % WORKS].ok = 0;
+          mbar_arrive(work_full + 8 * (nth % WORKS));
         }
-        __syncwarp();
-        if (ok && lane == 0) mbar_arrive(work_empty + 8 * (nth % WORKS));
       }
       // the copies in flight land before the CTA ends, also when another role has given up
       if (nq > 0) mbar_wait_warp(q_full, (nq - 1) & 1, a.wait_ns);
@@ -474,85 +479,117 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(work_empty + 8 * (nth % WORKS));
       }
-    } else if (warp == MMA_WARP) {
-      // ---------------- products ----------------
-      if (lane == 0) {
-        constexpr uint32_t ID_S = idesc_f16(BF16, BN, false), ID_O = idesc_f16(BF16, D, true);
-        int n = 0, nq = 0;
-        int np[2] = {0, 0}, no[2] = {0, 0};  // weights taken and outputs begun, per tile
-        uint32_t fixed_once = 0;             // parity of each stage's `fixed`
-        // Descriptors are bases plus constants (the address field counts 16 bytes, and no
-        // address carries out of it): put together anew for each product they took
-        // longer to make than the product takes.
-        const uint64_t q_desc = desc_sw128(q_smem, 16, 1024), k_desc = desc_sw128(ring, 16, 1024);
-        const uint64_t v_desc = desc_sw128(ring, C::CHUNK, 1024);
-        constexpr uint32_t TILE16 = C::TILE / 16, CHUNK16 = C::CHUNK / 16;
-        auto qk = [&](int t, int st) {  // S_t = Q_t K^T
-          const uint64_t q = q_desc + t * TILE16, kd = k_desc + st * TILE16;
-          const uint32_t d = tmem + t * BN;
+    } else {
+      // ---------------- products of a tile ----------------
+      // The whole warp runs the loop and one lane issues: what a product is told is
+      // then the same for the warp, and the compiler makes it in uniform registers.
+      // Descriptors are bases plus constants (the address field counts 16 bytes, and
+      // no address carries out of it).  A product takes 64 cycles; put together anew
+      // for each, in one lane's registers, its operands took up to 110.
+      const int t = warp - MMA_WARP;
+      constexpr uint32_t ID_S = idesc_f16(BF16, BN, false), ID_O = idesc_f16(BF16, D, true);
+      constexpr uint32_t TILE16 = C::TILE / 16, CHUNK16 = C::CHUNK / 16;
+      const uint64_t q_desc = desc_sw128(q_smem, 16, 1024) + t * TILE16;
+      const uint64_t k_desc = desc_sw128(ring, 16, 1024), v_desc = desc_sw128(ring, C::CHUNK, 1024);
+      const uint32_t s_col = tmem + t * BN, o_col = tmem + C::O_COL + t * D;
+      const bool one = lane == 0;
+      int n = 0, nq = 0, np = 0, no = 0, nt = 0;  // blocks, Q pairs, weights taken, outputs begun and turns so far
+      uint32_t fixed_once = 0;                    // parity of each stage's `fixed`
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, err, a.wait_ns)) != 0;
+      };
+      auto loaded = [&](int v) { return wait(full + 8 * (v % NST), (v / NST) & 1); };
+      auto give = [&](uint32_t bar) {
+        if (one) mbar_arrive(bar);
+      };
+      // the tiles take turns: left alone they fall into step, and both wait for
+      // products and then both for weights
+      auto my_turn = [&]() { return wait(turn + 8 * t, nt++ & 1); };
+      auto qk = [&](int st) {  // S_t = Q_t K^T
+        const uint64_t kd = k_desc + st * TILE16;
+        if (one) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            mma_ss(d, q + ((k >> 2) * CHUNK16 + (k & 3) * 2), kd + ((k >> 2) * CHUNK16 + (k & 3) * 2), ID_S, k > 0);
+            mma_ss(s_col, q_desc + ((k >> 2) * CHUNK16 + (k & 3) * 2), kd + ((k >> 2) * CHUNK16 + (k & 3) * 2), ID_S,
+                   k > 0);
           mma_commit(s_full + 8 * t);
-        };
-        auto pv = [&](int t, int st, int h, bool first) {  // O_t += P_t V, a half of the keys
-          const uint64_t v = v_desc + (st * TILE16 + h * (BN / 2) * 8);
-          const uint32_t d = tmem + C::O_COL + t * D, a = tmem + t * BN + h * (BN / 2);
-#pragma unroll
-          for (int k = 0; k < BN / 32; ++k) mma_ts(d, a + k * 8, v + k * 128, ID_O, !first || k > 0);
-        };
-        bool ok = true;
-        Work w;
-        for (int nth = 0; ok && next_work(nth, &w); ++nth) {
-          const Plan p(a, w);
-          if (p.nblocks > 0) {
-            ok = mbar_wait(q_full, nq & 1, err, a.wait_ns) &&
-                 mbar_wait(full + 8 * (n % NST), (n / NST) & 1, err, a.wait_ns);
-            if (!ok) break;
-            ++nq;
-            tc_fence_after();
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-              if (p.blocks[t]) qk(t, n % NST);
-            mma_commit(empty + 8 * (n % NST));
-            if (p.nblocks == 1) mma_commit(q_empty);
-          }
-          for (int i = 0; i < p.nblocks && ok; ++i, n += 2) {
-            const int sv = (n + 1) % NST, sk = (n + 2) % NST;
-            ok = mbar_wait(full + 8 * sv, ((n + 1) / NST) & 1, err, a.wait_ns);
-            if (ok && i >= p.zone) {
-              ok = mbar_wait(fixed + 8 * sv, (fixed_once >> sv) & 1, err, a.wait_ns);
-              fixed_once ^= 1u << sv;
-            }
-            if (ok && i + 1 < p.nblocks) ok = mbar_wait(full + 8 * sk, ((n + 2) / NST) & 1, err, a.wait_ns);
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              if (!ok || i >= p.blocks[t]) continue;
-              if (i == 0) {  // the last output of this tile has been read
-                if (no[t] > 0) ok = mbar_wait(o_empty + 8 * t, (no[t] - 1) & 1, err, a.wait_ns);
-                ++no[t];
-              }
-#pragma unroll
-              for (int h = 0; h < 2 && ok; ++h) {  // O_t += P_t V, a half of the keys at a time
-                ok = mbar_wait(p_full + 16 * t + 8 * h, np[t] & 1, err, a.wait_ns);
-                if (!ok) break;
-                tc_fence_after();
-                pv(t, sv, h, i == 0 && h == 0);
-              }
-              if (!ok) continue;
-              ++np[t];
-              if (i + 1 < p.blocks[t]) qk(t, sk);
-              else mma_commit(o_full + 8 * t);
-            }
-            if (ok) {
-              mma_commit(empty + 8 * sv);
-              if (i + 1 < p.nblocks) mma_commit(empty + 8 * sk);
-              if (i + 2 == p.nblocks) mma_commit(q_empty);  // the pair's last scores
-            }
-          }
-          if (ok) mbar_arrive(work_empty + 8 * (nth % WORKS));
+          mma_commit(empty + 8 * st);
         }
-        // every product issued is done before tensor memory is freed
+      };
+      auto pv = [&](int st, int h, bool first) {  // O_t += P_t V, a half of the keys
+        const uint64_t v = v_desc + (st * TILE16 + h * (BN / 2) * 8);
+        const uint32_t p = s_col + h * (BN / 2), more = first ? 0 : 1;
+        if (one) {
+          mma_ts(o_col, p, v, ID_O, more);
+#pragma unroll
+          for (int k = 1; k < BN / 32; ++k) mma_ts(o_col, p + k * 8, v + k * 128, ID_O, 1);
+        }
+      };
+      bool ok = true;
+      Work w;
+      for (int nth = 0;; ++nth) {
+        if (!__all_sync(0xFFFFFFFFu, ok && next_work(nth, &w))) break;
+        w.pos0 = __shfl_sync(0xFFFFFFFFu, w.pos0, 0);
+        w.q.qlen = __shfl_sync(0xFFFFFFFFu, w.q.qlen, 0);
+        w.q.klen = __shfl_sync(0xFFFFFFFFu, w.q.klen, 0);
+        const Plan p(a, w);
+        const int blocks = t ? p.blocks[1] : p.blocks[0];
+        if (p.nblocks > 0) {
+          ok = wait(q_full, nq & 1) && loaded(n);
+          if (!ok) break;
+          ++nq;
+          tc_fence_after();
+          if (blocks > 0) qk(n % NST);
+          else give(empty + 8 * (n % NST));
+          if (blocks <= 1 && one) mma_commit(q_empty);
+        }
+        // blocks that only the other tile has are waited for and given back
+        for (int i = 0; i < p.nblocks; ++i, n += 2) {
+          const int sv = (n + 1) % NST, sk = (n + 2) % NST;
+          ok = loaded(n + 1) && (i + 1 >= p.nblocks || loaded(n + 2));
+          if (ok && i >= p.zone) {
+            ok = wait(fixed + 8 * sv, (fixed_once >> sv) & 1);
+            fixed_once ^= 1u << sv;
+          }
+          if (!ok) break;
+          if (i >= blocks) {
+            ok = my_turn();
+            if (!ok) break;
+            give(turn + 8 * (1 - t));
+            give(empty + 8 * sv);
+            if (i + 1 < p.nblocks) give(empty + 8 * sk);
+            continue;
+          }
+          if (i == 0) {  // the last output of this tile has been read
+            if (no > 0) ok = wait(o_empty + 8 * t, (no - 1) & 1);
+            ++no;
+          }
+          ok = ok && wait(p_full + 16 * t, np & 1) && my_turn();
+          if (!ok) break;
+          tc_fence_after();
+          pv(sv, 0, i == 0);
+          ok = wait(p_full + 16 * t + 8, np & 1);
+          if (!ok) break;
+          tc_fence_after();
+          pv(sv, 1, false);
+          ++np;
+          if (i + 1 < blocks) {
+            qk(sk);
+            if (i + 2 == blocks && one) mma_commit(q_empty);  // the tile's last scores
+          } else {
+            if (one) mma_commit(o_full + 8 * t);
+            if (i + 1 < p.nblocks) give(empty + 8 * sk);
+          }
+          if (one) {
+            mbar_arrive(turn + 8 * (1 - t));
+            mma_commit(empty + 8 * sv);
+          }
+        }
+        if (!ok) break;
+        give(work_empty + 8 * (nth % WORKS));
+      }
+      // every product issued is done before tensor memory is freed
+      if (one) {
         mma_commit(drain);
         const unsigned long long t0 = globaltimer();
         while (!mbar_try(drain, 0) && globaltimer() - t0 < a.wait_ns) {}
