@@ -86,6 +86,7 @@ struct Args {
   int64_t q_total, k_total;
   int q_heads, kv_heads, group, positions;  // positions per tile
   int S, causal;
+  int wide;  // out is 32-byte aligned
   float scale_log2;
   const int32_t *q_offsets, *k_offsets;
   unsigned* status;
@@ -256,6 +257,19 @@ __device__ __forceinline__ bool nonfinite8(const uint4& v) {
   constexpr uint32_t E = std::is_same<T, __half>::value ? 0x7C007C00u : 0x7F807F80u;
   constexpr uint32_t ONE = std::is_same<T, __half>::value ? 0x04000400u : 0x00800080u;
   return ((((v.x & E) + ONE) | ((v.y & E) + ONE) | ((v.z & E) + ONE) | ((v.w & E) + ONE)) & 0x80008000u) != 0;
+}
+
+// Sixteen 16-bit values.  A thread's rows are not its neighbours', so a store
+// costs as many cycles as it has lanes; 32 bytes at once halve their number.
+__device__ __forceinline__ void store16(void* p, const uint32_t (&v)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
 }
 
 // A pair with infinities and NaN replaced by 0.
@@ -723,20 +737,22 @@ __global__ void __launch_bounds__(THREADS, 1)
           const bool extra = s_nonfinite[nth % WORKS] != 0;
           if (live) {
 #pragma unroll
-            for (int c = 0; c < HD; c += 8) {
-              float x[8];
+            for (int c = 0; c < HD; c += 16) {
+              float x[16];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) x[e] = lim < 0 ? 0.0f : __uint_as_float(o[c + e]) * inv;
+              for (int e = 0; e < 16; ++e) x[e] = lim < 0 ? 0.0f : __uint_as_float(o[c + e]) * inv;
               if (extra) {  // what was set aside: keys that this row sees
                 const T* v = static_cast<const T*>(a.v) + (int64_t)w.head * a.v_head + h * HD + c;
                 for (int j = p.first_hidden; j <= lim; ++j)
-                  for (int e = 0; e < 8; ++e) {
+                  for (int e = 0; e < 16; ++e) {
                     const float f = (float)v[(int64_t)(w.q.kb + j) * a.v_row + e];
                     if (!isfinite(f)) x[e] += f;
                   }
               }
-              *reinterpret_cast<uint4*>(dst + c) = make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]),
-                                                              pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
+              uint32_t y[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) y[e] = pack2<T>(x[2 * e], x[2 * e + 1]);
+              store16(dst + c, y, a.wide);
             }
           }
         }
@@ -806,6 +822,7 @@ int launch_as(const PromptAttn& c, cudaStream_t s) {
   a.positions = BM / a.group;
   a.S = c.S;
   a.causal = c.causal;
+  a.wide = (reinterpret_cast<uintptr_t>(c.out) & 31u) == 0;
   a.scale_log2 = c.scale * 1.44269504088896340736f;
   a.q_offsets = c.q_offsets;
   a.k_offsets = c.k_offsets;

@@ -189,6 +189,16 @@ def test_rows_of_no_sequence_are_zero(q4):
     assert not out[20:].any() and out[:20].any(-1).all()
 
 
+def test_output_aligned_to_16_bytes_only(q4):
+    q, k, v = (_normal(92 + i, (70, h, 128), torch.bfloat16).cuda() for i, h in enumerate((4, 2, 2)))
+    off = _i32([0, 70])
+    want = q4.q4_prompt_attention(q, k, v, off)
+    room = torch.zeros(70 * 4 * 128 + 8, dtype=torch.bfloat16, device="cuda")
+    out = room[8:].view(70, 4, 128)
+    assert out.data_ptr() % 32 == 16
+    assert torch.equal(q4.q4_prompt_attention(q, k, v, off, out=out), want)
+
+
 def test_many_short_sequences(q4):
     lens = [1 + (7 * i) % 5 for i in range(700)]
     _run(q4, 95, lens, lens, 1, 4, 64, torch.bfloat16)
