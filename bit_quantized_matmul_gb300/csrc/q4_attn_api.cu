@@ -42,7 +42,7 @@ int check_cache(int64_t slots, int64_t heads, int64_t head_dim, int64_t capacity
 
 int check_step(const int32_t* offsets, const int32_t* slot, const int32_t* pos, int64_t S, int64_t total,
                int64_t heads) {
-  if (S < 0 || S >= INT32_MAX || total < 0 || total >= INT32_MAX || total > INT32_MAX / heads)
+  if (S < 0 || S >= INT32_MAX || total < 0 || total > INT32_MAX / 2 || total > INT32_MAX / heads)
     return Q4_ERR_INVALID_ARG;
   if (total > 0 && S > 0 && (!offsets || !slot || !pos)) return Q4_ERR_INVALID_ARG;
   return Q4_OK;

@@ -6,14 +6,18 @@
 // q4_quantize, so the cache costs 4.5 bits a value where the 16-bit cache of
 // q4_kv_append costs 16.  Read: the rows back as (q - 8) * d.
 //
-// Both are bound by memory: a thread owns one 32-bit word of codes (eight
-// values), so a row is D/8 neighbouring lanes, its loads are 16 or 32 bytes a
-// lane and its codes one 32- or 64-byte run; a block's largest magnitude is
-// found with two shuffles among the four lanes that hold it.
+// Both are bound by memory, and for a decode step by the latency of a few loads
+// one after another.  A warp takes K or V of one packed row, all heads: it finds
+// the row's request once (32 offsets a load) while the row's first values are on
+// their way; a lane owns one 32-bit word of codes (eight values) at a time, so
+// its loads or stores of values are 16 or 32 bytes, and a block's largest
+// magnitude is found with two shuffles among the four lanes that hold it.
 #include "q4_kvq.cuh"
 
 namespace q4 {
 namespace {
+
+constexpr int ROW_THREADS = 128;
 
 template <typename T>
 struct AppendArgs {
@@ -26,73 +30,93 @@ struct AppendArgs {
   unsigned* status;
 };
 
+// Quantizes the eight values of word j of a block (the quad of lanes has the
+// block): its codes, and the block's scale.  status: what was wrong with it.
+__device__ __forceinline__ uint32_t quantize_word(const float (&v)[8], int j, int lane, uint16_t* scale,
+                                                  unsigned* status) {
+  // the first value of largest magnitude (lowest index among equals), and
+  // whether all are finite
+  float m = v[0];
+  bool finite = isfinite(v[0]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    finite = finite && isfinite(v[i]);
+    if (fabsf(v[i]) > fabsf(m)) m = v[i];
+  }
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    const float om = __shfl_xor_sync(0xFFFFFFFFu, m, o);
+    const bool take = (j & o) ? fabsf(om) >= fabsf(m) : fabsf(om) > fabsf(m);  // the lower lane's on equality
+    m = take ? om : m;
+  }
+  const unsigned odd = __ballot_sync(0xFFFFFFFFu, !finite) >> (lane & 28) & 0xFu;
+  const float d = __fdiv_rn(m, -8.0f);
+  const uint16_t d16 = __half_as_ushort(__float2half_rn(d));
+  if (odd || (d16 & 0x7C00u) == 0x7C00u) {
+    // a block that binary16 cannot scale reads back as NaN, as the values themselves would
+    *status = odd ? STATUS_KV_NONFINITE : STATUS_KV_SCALE;
+    *scale = 0x7FFFu;
+    return 0x99999999u;
+  }
+  uint32_t codes = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    int qi = 8;
+    if (d != 0.0f) {
+      qi = (int)roundf(__fdiv_rn(v[i], d)) + 8;  // roundf: half away from zero
+      qi = qi < 0 ? 0 : (qi > 15 ? 15 : qi);
+    }
+    codes |= (uint32_t)qi << (4 * i);
+  }
+  *scale = d16;
+  return codes;
+}
+
 template <int D, typename T>
-__global__ void __launch_bounds__(256) kvq_append_kernel(const AppendArgs<T> a) {
+__global__ void __launch_bounds__(ROW_THREADS) kvq_append_kernel(const AppendArgs<T> a) {
   using L = Kvq<D>;
-  constexpr int LPR = D / 8;  // lanes per row
-  const int64_t rows = a.total * a.heads;
-  const int kv = blockIdx.y;
-  const int w = threadIdx.x % LPR;  // word of the row: block w / 4, word w % 4 of the block
-  const int b = w >> 2, j = w & 3;
-  // whole rows per step, so the four lanes of a block always run together
-  for (int64_t r = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / LPR; r < rows;
-       r += (int64_t)gridDim.x * blockDim.x / LPR) {
-    const int64_t t = r / a.heads, h = r - t * a.heads;
-    const int s = kvq_find_request(a.offsets, a.S, t);
+  constexpr int LPR = D / 8, ROWS = 32 / LPR;  // lanes per row, heads that a warp takes at once
+  const int lane = threadIdx.x & 31;
+  const int w = lane % LPR, b = w >> 2, j = w & 3;
+  const int units = 2 * (int)a.total;  // (row, K or V); below 2^31: checked on the host
+  for (int u = blockIdx.x * (ROW_THREADS / 32) + (threadIdx.x >> 5); u < units; u += gridDim.x * (ROW_THREADS / 32)) {
+    const int kv = u & 1, t = u >> 1;
+    const int64_t s_head = kv ? a.s_head[1] : a.s_head[0];
+    const T* src = kv ? a.src[1] + t * a.s_token[1] : a.src[0] + t * a.s_token[0];
+    src += w * 8;
+    int h = lane / LPR;
+    float v[8] = {};
+    if (h < a.heads) kvq_load8(src + h * s_head, v);
+    const int s = kvq_find_request(a.offsets, a.S, t, lane);
     const KvqRequest q = kvq_request(a.offsets, a.slot, a.pos, s);
     if (t < q.b || t >= q.e) continue;  // a packed row that belongs to no request
     if (!q.ok(a.total, a.slots, a.capacity)) {
-      if (kv == 0 && w == 0 && h == 0) atomicOr(a.status, STATUS_KV_RANGE);
+      if (lane == 0) atomicOr(a.status, STATUS_KV_RANGE);
       continue;  // the whole request is left unwritten
     }
-    float v[8];
-    kvq_load8(a.src[kv] + t * a.s_token[kv] + h * a.s_head[kv] + w * 8, v);
-    // the first value of largest magnitude (lowest index among equals), and
-    // whether all are finite: NaN and infinity have the largest exponent
-    float m = v[0];
-    bool finite = isfinite(v[0]);
-#pragma unroll
-    for (int i = 1; i < 8; ++i) {
-      finite = finite && isfinite(v[i]);
-      if (fabsf(v[i]) > fabsf(m)) m = v[i];
-    }
-    const unsigned quad = 0xFu << (threadIdx.x & 28);  // the block's four lanes
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      const float om = __shfl_xor_sync(quad, m, o);
-      const bool take = (j & o) ? fabsf(om) >= fabsf(m) : fabsf(om) > fabsf(m);  // the lower lane's on equality
-      m = take ? om : m;
-    }
-    finite = __all_sync(quad, finite);
-    const float d = __fdiv_rn(m, -8.0f);
-    uint16_t d16 = __half_as_ushort(__float2half_rn(d));
-    uint32_t codes = 0;
-    if (!finite || (d16 & 0x7C00u) == 0x7C00u) {
-      // a block that binary16 cannot scale reads back as NaN, as the values themselves would
-      if (j == 0) atomicOr(a.status, finite ? STATUS_KV_SCALE : STATUS_KV_NONFINITE);
-      d16 = 0x7FFFu;
-      codes = 0x99999999u;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        int qi = 8;
-        if (d != 0.0f) {
-          qi = (int)roundf(__fdiv_rn(v[i], d)) + 8;  // roundf: half away from zero
-          qi = qi < 0 ? 0 : (qi > 15 ? 15 : qi);
+    const int p = (int)(q.pos + (t - q.b)), row = p % L::POS;
+    uint8_t* tile = a.cache + q.slot * a.heads * a.plane_bytes + (int64_t)(p / L::POS) * L::BYTES;
+    for (int h0 = 0; h0 < a.heads; h0 += ROWS) {
+      float next[8] = {};
+      if (h + ROWS < a.heads) kvq_load8(src + (h + ROWS) * s_head, next);
+      uint16_t d16;
+      unsigned bad = 0;
+      const uint32_t codes = quantize_word(v, j, lane, &d16, &bad);
+      if (h < a.heads) {
+        if (bad && j == 0) atomicOr(a.status, bad);
+        uint8_t* dst = tile + h * a.plane_bytes;
+        if (kv == 0) {
+          *reinterpret_cast<uint32_t*>(dst + kvq_k_word<D>(row, b, j)) = codes;
+        } else {
+          *reinterpret_cast<uint16_t*>(dst + kvq_v_half<D>(row, b, 2 * j)) = (uint16_t)codes;
+          *reinterpret_cast<uint16_t*>(dst + kvq_v_half<D>(row, b, 2 * j + 1)) = (uint16_t)(codes >> 16);
         }
-        codes |= (uint32_t)qi << (4 * i);
+        if (j == 0) *reinterpret_cast<uint16_t*>(dst + kvq_scale<D>(kv, row, b)) = d16;
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = next[i];
+      h += ROWS;
     }
-    const int64_t p = q.pos + (t - q.b);
-    const int row = (int)(p % L::POS);
-    uint8_t* tile = a.cache + (q.slot * a.heads + h) * a.plane_bytes + p / L::POS * L::BYTES;
-    if (kv == 0) {
-      *reinterpret_cast<uint32_t*>(tile + kvq_k_word<D>(row, b, j)) = codes;
-    } else {
-      *reinterpret_cast<uint16_t*>(tile + kvq_v_half<D>(row, b, 2 * j)) = (uint16_t)codes;
-      *reinterpret_cast<uint16_t*>(tile + kvq_v_half<D>(row, b, 2 * j + 1)) = (uint16_t)(codes >> 16);
-    }
-    if (j == 0) *reinterpret_cast<uint16_t*>(tile + kvq_scale<D>(kv, row, b)) = d16;
   }
 }
 
@@ -107,47 +131,57 @@ struct ReadArgs {
 };
 
 template <int D, typename T>
-__global__ void __launch_bounds__(256) kvq_read_kernel(const ReadArgs<T> a) {
+__global__ void __launch_bounds__(ROW_THREADS) kvq_read_kernel(const ReadArgs<T> a) {
   using L = Kvq<D>;
-  constexpr int LPR = D / 8;
-  const int64_t rows = a.total * a.heads;
-  const int kv = blockIdx.y;
-  const int w = threadIdx.x % LPR;
-  const int b = w >> 2, j = w & 3;
-  for (int64_t r = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / LPR; r < rows;
-       r += (int64_t)gridDim.x * blockDim.x / LPR) {
-    const int64_t t = r / a.heads, h = r - t * a.heads;
-    const int s = kvq_find_request(a.offsets, a.S, t);
+  constexpr int LPR = D / 8, ROWS = 32 / LPR;
+  const int lane = threadIdx.x & 31;
+  const int w = lane % LPR, b = w >> 2, j = w & 3;
+  const int units = 2 * (int)a.total;
+  // K and V of neighbouring rows go to the warps of a CTA: V's rows share their memory sectors
+  for (int u = blockIdx.x * (ROW_THREADS / 32) + (threadIdx.x >> 5); u < units; u += gridDim.x * (ROW_THREADS / 32)) {
+    const int kv = u & 1, t = u >> 1;
+    const int s = kvq_find_request(a.offsets, a.S, t, lane);
     const KvqRequest q = kvq_request(a.offsets, a.slot, a.pos, s);
-    float v[8] = {};
-    if (t >= q.b && t < q.e) {
-      if (!q.ok(a.total, a.slots, a.capacity)) {
-        if (kv == 0 && w == 0 && h == 0) atomicOr(a.status, STATUS_KV_RANGE);
-      } else {
-        const int64_t p = q.pos + (t - q.b);
-        const int row = (int)(p % L::POS);
-        const uint8_t* tile = a.cache + (q.slot * a.heads + h) * a.plane_bytes + p / L::POS * L::BYTES;
+    T* dst = (kv ? a.dst[1] : a.dst[0]) + (int64_t)t * a.heads * D + w * 8;
+    bool held = t >= q.b && t < q.e;
+    if (held && !q.ok(a.total, a.slots, a.capacity)) {
+      if (lane == 0) atomicOr(a.status, STATUS_KV_RANGE);
+      held = false;
+    }
+    const int p = held ? (int)(q.pos + (t - q.b)) : 0, row = p % L::POS;
+    const uint8_t* tile = a.cache + (held ? q.slot * a.heads * a.plane_bytes + (int64_t)(p / L::POS) * L::BYTES : 0);
+#pragma unroll 2
+    for (int h = lane / LPR; h < a.heads; h += ROWS) {
+      float v[8] = {};
+      if (held) {
+        const uint8_t* src = tile + h * a.plane_bytes;
         uint32_t codes;
         if (kv == 0) {
-          codes = *reinterpret_cast<const uint32_t*>(tile + kvq_k_word<D>(row, b, j));
+          codes = __ldg(reinterpret_cast<const uint32_t*>(src + kvq_k_word<D>(row, b, j)));
         } else {
-          codes = *reinterpret_cast<const uint16_t*>(tile + kvq_v_half<D>(row, b, 2 * j)) |
-                  (uint32_t)*reinterpret_cast<const uint16_t*>(tile + kvq_v_half<D>(row, b, 2 * j + 1)) << 16;
+          codes = __ldg(reinterpret_cast<const uint16_t*>(src + kvq_v_half<D>(row, b, 2 * j))) |
+                  (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(src + kvq_v_half<D>(row, b, 2 * j + 1))) << 16;
         }
-        const float d =
-            __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t*>(tile + kvq_scale<D>(kv, row, b))));
+        const float d = __half2float(
+            __ushort_as_half(__ldg(reinterpret_cast<const uint16_t*>(src + kvq_scale<D>(kv, row, b)))));
+        uint32_t r[4];
+        kvq_unpack_centred(codes, r);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = (float)((int)((codes >> (4 * i)) & 15u) - 8) * d;
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r[i]));
+          v[i] = f.x * d;
+          v[i + 4] = f.y * d;
+        }
       }
+      kvq_store8(dst + h * D, v);
     }
-    kvq_store8(a.dst[kv] + r * D + w * 8, v);
   }
 }
 
-// Blocks along x for `rows` rows of D values in each of the two planes.
-unsigned row_blocks(int64_t rows, int D, int num_sms) {
-  const int64_t per = 256 / (D / 8);
-  const int64_t need = (rows + per - 1) / per, most = (int64_t)num_sms * 8;
+// CTAs for K and V of `total` rows, a warp each.
+unsigned row_blocks(int64_t total, int num_sms) {
+  constexpr int PER = ROW_THREADS / 32;
+  const int64_t need = (2 * total + PER - 1) / PER, most = (int64_t)num_sms * (2048 / ROW_THREADS);
   return (unsigned)(need < most ? need : most);
 }
 
@@ -172,9 +206,9 @@ int append_as(const KvqStep& c, const void* k_new, const void* v_new, const int6
   a.pos = c.pos;
   a.S = c.S;
   a.status = c.status;
-  const dim3 grid(row_blocks(c.total * c.heads, c.head_dim, c.num_sms), 2);
-  if (c.head_dim == 128) kvq_append_kernel<128, T><<<grid, 256, 0, s>>>(a);
-  else kvq_append_kernel<64, T><<<grid, 256, 0, s>>>(a);
+  const unsigned grid = row_blocks(c.total, c.num_sms);
+  if (c.head_dim == 128) kvq_append_kernel<128, T><<<grid, ROW_THREADS, 0, s>>>(a);
+  else kvq_append_kernel<64, T><<<grid, ROW_THREADS, 0, s>>>(a);
   return cudaGetLastError() == cudaSuccess ? Q4_OK : Q4_ERR_CUDA;
 }
 
@@ -194,9 +228,9 @@ int read_as(const KvqStep& c, const uint8_t* cache, void* k_out, void* v_out, cu
   a.pos = c.pos;
   a.S = c.S;
   a.status = c.status;
-  const dim3 grid(row_blocks(c.total * c.heads, c.head_dim, c.num_sms), 2);
-  if (c.head_dim == 128) kvq_read_kernel<128, T><<<grid, 256, 0, s>>>(a);
-  else kvq_read_kernel<64, T><<<grid, 256, 0, s>>>(a);
+  const unsigned grid = row_blocks(c.total, c.num_sms);
+  if (c.head_dim == 128) kvq_read_kernel<128, T><<<grid, ROW_THREADS, 0, s>>>(a);
+  else kvq_read_kernel<64, T><<<grid, ROW_THREADS, 0, s>>>(a);
   return cudaGetLastError() == cudaSuccess ? Q4_OK : Q4_ERR_CUDA;
 }
 

@@ -66,14 +66,19 @@ __device__ __forceinline__ int kvq_scale(int kv, int r, int b) {
   return (kv ? Kvq<D>::VS_OFF : Kvq<D>::KS_OFF) + (((r >> 1) * Kvq<D>::NB + b) * 2 + (r & 1)) * 2;
 }
 
-// The request whose packed rows contain row t: the last s with offsets[s] <= t
-// (offsets are expected to be non-decreasing; callers check the result).
-__device__ __forceinline__ int kvq_find_request(const int32_t* __restrict__ offsets, int S, int64_t t) {
-  int lo = 0, hi = S;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if ((int64_t)__ldg(offsets + mid) <= t) lo = mid;
-    else hi = mid;
+// The request whose packed rows contain row t, found by a whole warp: the last s
+// with offsets[s] <= t (offsets are expected to be non-decreasing; callers check
+// the result).  32 offsets a round: a search by halves would wait for memory
+// log2(S) times.
+__device__ __forceinline__ int kvq_find_request(const int32_t* __restrict__ offsets, int S, int64_t t, int lane) {
+  int lo = 0, n = S;  // the answer lies in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = lo + lane * step;
+    const bool below = lane * step < n && (int64_t)__ldg(offsets + at) <= t;
+    const unsigned hit = __ballot_sync(0xFFFFFFFFu, below) | 1u;
+    const int k = 31 - __clz(hit);
+    lo += k * step;
+    n = min(step, n - k * step);
   }
   return lo;
 }
@@ -91,6 +96,21 @@ __device__ __forceinline__ KvqRequest kvq_request(const int32_t* __restrict__ of
                                                   const int32_t* __restrict__ slot,
                                                   const int32_t* __restrict__ pos, int s) {
   return {__ldg(offsets + s), __ldg(offsets + s + 1), __ldg(slot + s), __ldg(pos + s)};
+}
+
+// The operand registers of a word of codes: exact binary16 pairs q - 8 of
+// nibbles (0, 4), (1, 5), (2, 6) and (3, 7), as 1024 + q less 1032, or
+// (1024 + 16 q) / 16 less 72.
+__device__ __forceinline__ void kvq_unpack_centred(uint32_t w, uint32_t (&r)[4]) {
+  const __half2 k1032 = __float2half2_rn(-1032.0f), k72 = __float2half2_rn(-72.0f), k16 = __float2half2_rn(0.0625f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t v = i < 2 ? w : w >> 8;
+    const uint32_t x = (v & ((i & 1) ? 0x00F000F0u : 0x000F000Fu)) | 0x64006400u;
+    const __half2 h = *reinterpret_cast<const __half2*>(&x);
+    const __half2 y = (i & 1) ? __hfma2(h, k16, k72) : __hadd2(h, k1032);
+    r[i] = *reinterpret_cast<const uint32_t*>(&y);
+  }
 }
 
 // Eight consecutive elements as fp32 (16-byte aligned).

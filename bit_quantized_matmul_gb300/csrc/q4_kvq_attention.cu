@@ -50,6 +50,8 @@ constexpr int THREADS = 32 * WARPS;
 constexpr int ROWS = 8;               // virtual rows of an item
 constexpr int CTAS_PER_SM = 3;
 constexpr int STAGES = 3;             // tiles in flight per warp
+constexpr int MASS_STAGES = 4;        // K halves in flight per warp of the weights' launch
+constexpr int MASS_CTAS_PER_SM = 4;
 constexpr int ITEM_UNITS = 2;         // what beginning an item costs, in tiles: its queries, its sums' end
 constexpr float NEG_INF = -INFINITY;
 constexpr float SLACK = 5.0f;         // log2 of how far a weight may pass 1 before the sums are rescaled
@@ -108,20 +110,6 @@ __device__ __forceinline__ void unpack(uint32_t w, uint32_t (&r)[4]) {
   r[1] = w & 0x00F000F0u;
   r[2] = (w >> 8) & 0x000F000Fu;
   r[3] = (w >> 8) & 0x00F000F0u;
-}
-
-// The same as exact binary16 pairs q - 8: 1024 + q less 1032, or (1024 + 16 q) / 16 less 72.
-__device__ __forceinline__ void unpack_centred(uint32_t w, uint32_t (&r)[4]) {
-  const __half2 k1032 = __float2half2_rn(-1032.0f), k72 = __float2half2_rn(-72.0f),
-                k16 = __float2half2_rn(0.0625f);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t v = i < 2 ? w : w >> 8;
-    const uint32_t x = (v & ((i & 1) ? 0x00F000F0u : 0x000F000Fu)) | 0x64006400u;
-    const __half2 h = *reinterpret_cast<const __half2*>(&x);
-    const __half2 y = (i & 1) ? __hfma2(h, k16, k72) : __hadd2(h, k1032);
-    r[i] = *reinterpret_cast<const uint32_t*>(&y);
-  }
 }
 
 // ---------------------------------------------------------------- work ranges
@@ -531,8 +519,8 @@ __device__ __forceinline__ void take_tile(const uint8_t* tile, int p0, const Que
         split(x, hi[u], lo[u]);
       }
       uint32_t r0[4], r1[4];
-      unpack_centred(vw[0][b], r0);
-      unpack_centred(vw[1][b], r1);
+      kvq_unpack_centred(vw[0][b], r0);
+      kvq_unpack_centred(vw[1][b], r1);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {  // values 4g + 2i and 4g + 2i + 1 of the block as rows g and g + 8
         const uint32_t av[4] = {r0[2 * i], r0[2 * i + 1], r1[2 * i], r1[2 * i + 1]};
@@ -678,37 +666,31 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kvq_attention_kernel(con
 template <int D, typename T>
 __global__ void __launch_bounds__(THREADS) kvq_join_kernel(const Args<T> a) {
   constexpr int PER = D / 32;
-  __shared__ float s_sum[WARPS], s_top[WARPS];
+  __shared__ float2 s_ml[WARPS];
   __shared__ float s_acc[WARPS][D];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int t = blockIdx.x, hq = blockIdx.y;
-  const int hq_all = a.heads * a.group;
-  const int64_t at = (int64_t)t * hq_all + hq;
-  const int s = kvq_find_request(a.offsets, a.S, t);
+  const int64_t at = (int64_t)t * (a.heads * a.group) + hq;
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int s = kvq_find_request(a.offsets, a.S, t, lane);
   const Request r = load_request(a, s, true);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (r.tiles == 0 || t < r.b || t >= r.b + r.n) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int d = tid; d < D; d += THREADS) a.out[at * D + d] = (T)0.0f;
     if (a.lse && tid == 0) a.lse[at] = NEG_INF;
     return;
   }
-  const Shares share(a.unit_start[a.S], a.workers);
   const int head = hq / a.group;
   const int vr = (t - r.b) * a.group + (hq - head * a.group);
   const int item = head * (r.items / a.heads) + vr / ROWS, row = vr % ROWS;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Shares share(a.unit_start[a.S], a.workers);
   const int64_t u0 = a.unit_start[s] + (int64_t)item * r.span() + ITEM_UNITS;  // the first tile
   const int wa = share.of(u0), wb = share.of(u0 + r.tiles - 1);
   if (wa == wb) return;  // written by the main launch
-  float top = NEG_INF;
-  for (int w = wa + tid; w <= wb; w += THREADS)
-    top = fmaxf(top, a.partial_ml[(int64_t)(2 * w + (w == wa)) * ROWS + row].x);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-  if (lane == 0) s_top[warp] = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < WARPS; ++w) top = fmaxf(top, s_top[w]);
-  float sum = 0.0f, acc[PER] = {};
+  // each warp joins every fourth part as it comes, then the warps' sums are joined
+  float top = NEG_INF, sum = 0.0f, acc[PER] = {};
+  auto scale_of = [](float m, float top) { return m == NEG_INF ? 0.0f : ex2(m - top); };
 #pragma unroll 4
   for (int w = wa + warp; w <= wb; w += WARPS) {
     const int64_t p = (int64_t)(2 * w + (w == wa)) * ROWS + row;
@@ -721,25 +703,28 @@ __global__ void __launch_bounds__(THREADS) kvq_join_kernel(const Args<T> a) {
       const float2 x = *reinterpret_cast<const float2*>(a.partial + p * D + lane * 2);
       v[0] = x.x; v[1] = x.y;
     }
-    const float f = ml.x == NEG_INF ? 0.0f : ex2(ml.x - top);
-    sum = fmaf(ml.y, f, sum);
+    const float nt = fmaxf(top, ml.x), f0 = scale_of(top, nt), f1 = scale_of(ml.x, nt);
+    top = nt;
+    sum = sum * f0 + ml.y * f1;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) acc[i] = fmaf(v[i], f, acc[i]);
+    for (int i = 0; i < PER; ++i) acc[i] = acc[i] * f0 + v[i] * f1;
   }
-  if (lane == 0) s_sum[warp] = sum;
+  if (lane == 0) s_ml[warp] = make_float2(top, sum);
 #pragma unroll
   for (int i = 0; i < PER; ++i) s_acc[warp][lane * PER + i] = acc[i];
   __syncthreads();
+  top = NEG_INF;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) top = fmaxf(top, s_ml[w].x);
   sum = 0.0f;
+  float x = 0.0f;
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) sum += s_sum[w];
-  const float inv = 1.0f / sum;
-  if (tid < D) {
-    float v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) v += s_acc[w][tid];
-    a.out[at * D + tid] = (T)(v * inv);
+  for (int w = 0; w < WARPS; ++w) {
+    const float f = scale_of(s_ml[w].x, top);
+    sum = fmaf(s_ml[w].y, f, sum);
+    if (tid < D) x = fmaf(s_acc[w][tid], f, x);
   }
+  if (tid < D) a.out[at * D + tid] = (T)(x / sum);
   if (a.lse && tid == 0) a.lse[at] = top + log2f(sum);
 }
 
@@ -747,52 +732,97 @@ __global__ void __launch_bounds__(THREADS) kvq_join_kernel(const Args<T> a) {
 // mass[slot, head, p] += sum over the request's rows and the group's heads of
 // exp2(s - lse); a position that this step appended starts from 0.  Reads the
 // K half of the cache again: keeping the scores instead would write and read
-// as many bytes for a group of seven heads.  Every position belongs to one
-// thread, so the sums have a fixed order.
+// as many bytes for a group of seven heads.  The eight rows' weights of a tile
+// are summed over lanes and dealt out in seven shuffles, a position to each
+// lane; every position belongs to one lane, so the sums have a fixed order.
 template <int D, typename T>
 __global__ void __launch_bounds__(THREADS) kvq_mass_kernel(const Args<T> a) {
   using L = Kvq<D>;
+  constexpr int HALF = L::V_OFF;  // bytes of a tile's K half
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint4 frags[WARPS][QUERY_BYTES<D> / 16];
-  const int lane = threadIdx.x & 31;
+  __shared__ uint64_t bars[WARPS][MASS_STAGES];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, tq = lane & 3;
+  const uint8_t* ring = smem + warp * MASS_STAGES * HALF;
+  const uint32_t ring_u32 = smem_u32(ring), bar_u32 = smem_u32(bars[warp]);
+  if (lane < MASS_STAGES) mbar_init(bar_u32 + 8 * lane, 1);
+  mbar_init_fence();
+  __syncwarp();
   const Range range = plan_range(a, false, nullptr);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the lane's position of a tile after the sums are dealt out: 8u + 2 tq + c
+  const int mine = ((g >> 1) & 3) * 8 + 2 * tq + (g & 1);
+  unsigned issued = 0, taken = 0;
+  bool waited = false;
   Walk<T> it;
   for (it.begin(a, range, false); it.t0 < it.t1; it.next(a, false)) {
     const Request& r = it.r;
     const int head = it.item;
     const uint8_t* plane = a.cache + ((int64_t)r.slot * a.heads + head) * a.plane_bytes;
     float* mass = a.mass + ((int64_t)r.slot * a.heads + head) * a.capacity;
-    const int rows = r.n * a.group;
+    const int rows = r.n * a.group, end = r.pos + r.n;
     for (int row0 = 0; row0 < rows; row0 += ROWS) {
+      int next = it.t0;
+      auto issue = [&]() {
+        if (next >= it.t1) return;
+        if (lane == 0) {
+          const unsigned st = issued % MASS_STAGES;
+          mbar_expect_tx(bar_u32 + 8 * st, HALF);
+          bulk_load(ring_u32 + st * HALF, plane + (int64_t)next * L::BYTES, HALF, bar_u32 + 8 * st);
+        }
+        ++issued;
+        ++next;
+      };
+      for (int i = 0; i < MASS_STAGES; ++i) issue();
       Query<D> q;
-      load_query<D, T>(q, frags[threadIdx.x >> 5], a, r, head, row0, lane);
+      load_query<D, T>(q, frags[warp], a, r, head, row0, lane);
+      if (!waited) {  // what follows needs the rows' sums
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        waited = true;
+      }
       const int vr = row0 + g;
       const bool live = vr < rows;
       const int j = live ? vr / a.group : 0;
-      const float lse = live ? a.lse[(int64_t)(r.b + j) * (a.heads * a.group) + head * a.group + vr - j * a.group] : 0.0f;
-      const int64_t last = live ? r.pos + j : -1;
+      const float lse =
+          live ? a.lse[(int64_t)(r.b + j) * (a.heads * a.group) + head * a.group + vr - j * a.group] : 0.0f;
+      const int last = live ? r.pos + j : -1;
       for (int t = it.t0; t < it.t1; ++t) {
+        const int pm = t * L::POS + mine;
+        const float old = pm < end && (row0 > 0 || pm < r.pos) ? mass[pm] : 0.0f;
+        const unsigned st = taken % MASS_STAGES;
+        if (!mbar_wait_warp(bar_u32 + 8 * st, (taken / MASS_STAGES) & 1, a.wait_ns)) {
+          if (lane == 0) atomicOr(a.status, STATUS_TIMEOUT);
+          for (; taken < issued; ++taken)
+            mbar_wait_warp(bar_u32 + 8 * (taken % MASS_STAGES), (taken / MASS_STAGES) & 1, a.wait_ns);
+          return;
+        }
+        ++taken;
         float sc[L::POS / 8][2];
-        scores<D>(plane + (int64_t)t * L::BYTES, q, g, tq, sc);
+        scores<D>(ring + st * HALF, q, g, tq, sc);
+        __syncwarp();
+        issue();
+        float w[8];
 #pragma unroll
-        for (int u = 0; u < L::POS / 8; ++u) {
-          const int64_t p = (int64_t)t * L::POS + 8 * u + 2 * tq;
-          float w[2] = {p <= last ? ex2(sc[u][0] - lse) : 0.0f, p + 1 <= last ? ex2(sc[u][1] - lse) : 0.0f};
+        for (int e = 0; e < 8; ++e) {
+          const int p = t * L::POS + 8 * (e >> 1) + 2 * tq + (e & 1);
+          w[e] = p <= last ? ex2(sc[e >> 1][e & 1] - lse) : 0.0f;
+        }
+        // bits 2, 1, 0 of a value's index go to bits 2, 1, 0 of the lane's g
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            w[c] += __shfl_xor_sync(0xFFFFFFFFu, w[c], 4);
-            w[c] += __shfl_xor_sync(0xFFFFFFFFu, w[c], 8);
-            w[c] += __shfl_xor_sync(0xFFFFFFFFu, w[c], 16);
-            if (g == 0 && p + c < r.pos + r.n) {
-              const float old = (row0 == 0 && p + c >= r.pos) ? 0.0f : mass[p + c];
-              mass[p + c] = old + w[c];
-            }
+        for (int k = 4; k > 0; k >>= 1) {
+          const bool high = g & k;
+#pragma unroll
+          for (int e = 0; e < k; ++e) {
+            const float give = high ? w[e] : w[e + k];
+            const float got = __shfl_xor_sync(0xFFFFFFFFu, give, 4 * k);
+            w[e] = (high ? w[e + k] : w[e]) + got;
           }
         }
+        if (pm < end) mass[pm] = old + w[0];
       }
     }
   }
+  if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // the launch ends after the ones before
 }
 
 template <int D, typename T>
@@ -824,12 +854,15 @@ int launch_as(const KvqStep& c, const uint8_t* cache, const void* q, const int64
   a.lse = mass ? ws.lse : nullptr;
   a.mass = mass;
   constexpr int SMEM = WARPS * (STAGES * Kvq<D>::BYTES + QUERY_BYTES<D>);
-  static std::atomic<bool> sized[64];  // per device: the kernel's shared memory limit is set
+  constexpr int MASS_SMEM = WARPS * MASS_STAGES * Kvq<D>::V_OFF;
+  static std::atomic<bool> sized[64];  // per device: the kernels' shared memory limits are set
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return Q4_ERR_CUDA;
   if (!sized[dev].load()) {
     if (cudaFuncSetAttribute(kvq_attention_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) !=
-        cudaSuccess)
+            cudaSuccess ||
+        cudaFuncSetAttribute(kvq_mass_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, MASS_SMEM) !=
+            cudaSuccess)
       return Q4_ERR_CUDA;
     sized[dev].store(true);
   }
@@ -846,8 +879,8 @@ int launch_as(const KvqStep& c, const uint8_t* cache, const void* q, const int64
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, kvq_join_kernel<D, T>, a) != cudaSuccess) return Q4_ERR_CUDA;
   if (mass) {
-    cfg.gridDim = dim3(c.num_sms * 4);
-    cfg.numAttrs = 0;
+    cfg.gridDim = dim3(c.num_sms * MASS_CTAS_PER_SM);
+    cfg.dynamicSmemBytes = MASS_SMEM;
     if (cudaLaunchKernelEx(&cfg, kvq_mass_kernel<D, T>, a) != cudaSuccess) return Q4_ERR_CUDA;
   }
   return Q4_OK;
