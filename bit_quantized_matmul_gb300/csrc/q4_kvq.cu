@@ -178,10 +178,100 @@ __global__ void __launch_bounds__(ROW_THREADS) kvq_read_kernel(const ReadArgs<T>
   }
 }
 
-// CTAs for K and V of `total` rows, a warp each.
-unsigned row_blocks(int64_t total, int num_sms) {
+// The same for steps of long runs of rows: a warp takes the rows of one head
+// that lie in eight neighbouring positions (aligned), so it reads K's and V's
+// codes of all of them as 512 consecutive bytes each (D = 128) and finds the
+// request once.  Rows 8c .. 8c + 7 of the step are one CTA warp's; they lie in
+// two such groups at most unless a request ends among them.
+template <int D, typename T>
+__global__ void __launch_bounds__(ROW_THREADS) kvq_read_groups_kernel(const ReadArgs<T> a) {
+  using L = Kvq<D>;
+  constexpr int NB = L::NB;
+  const int lane = threadIdx.x & 31;
+  const int g = lane >> 2, tq = lane & 3;
+  const int chunks = (int)((a.total + 7) / 8), units = chunks * (int)a.heads;
+  for (int u = blockIdx.x * (ROW_THREADS / 32) + (threadIdx.x >> 5); u < units; u += gridDim.x * (ROW_THREADS / 32)) {
+    const int h = u % (int)a.heads, c = u / (int)a.heads;
+    const int t_end = (int)min(a.total, (int64_t)8 * c + 8);
+    for (int t = 8 * c; t < t_end;) {
+      const int s = kvq_find_request(a.offsets, a.S, t, lane);
+      const KvqRequest q = kvq_request(a.offsets, a.slot, a.pos, s);
+      bool held = t >= q.b && t < q.e;
+      // rows up to the request's end, or (outside of one) up to the next one's beginning
+      int stop = t_end;
+      if (held) stop = (int)min((int64_t)stop, q.e);
+      else if (t < q.b) stop = (int)min((int64_t)stop, q.b);
+      else if (s + 1 < a.S) stop = (int)min((int64_t)stop, max((int64_t)__ldg(a.offsets + s + 1), (int64_t)t + 1));
+      if (held && !q.ok(a.total, a.slots, a.capacity)) {
+        if (lane == 0) atomicOr(a.status, STATUS_KV_RANGE);
+        held = false;
+      }
+      const int p = held ? (int)(q.pos + (t - q.b)) : 0;
+      const int first = p & 7;  // the group's rows are positions p - first ..
+      if (held) stop = min(stop, t + 8 - first);
+      const int count = stop - t;
+      // lane (g, tq): K words j = tq of row g; V words of group g of the pair 2 tq, 2 tq + 1
+      uint32_t kw[NB], vw[NB], ks[NB], vs[NB];
+      if (held) {
+        const uint8_t* tile = a.cache + (q.slot * a.heads + h) * a.plane_bytes + (int64_t)(p / L::POS) * L::BYTES;
+        const int r0 = (p % L::POS) & ~7;
+        const uint32_t* k = reinterpret_cast<const uint32_t*>(tile + r0 * L::ROW) + lane * NB;
+        const uint32_t* v = reinterpret_cast<const uint32_t*>(tile + L::V_OFF + r0 * L::ROW) + lane * NB;
+        const uint32_t* kd = reinterpret_cast<const uint32_t*>(tile + kvq_scale<D>(0, r0 + (g & 6), 0));
+        const uint32_t* vd = reinterpret_cast<const uint32_t*>(tile + kvq_scale<D>(1, r0 + 2 * tq, 0));
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          kw[b] = __ldg(k + b);
+          vw[b] = __ldg(v + b);
+          ks[b] = __ldg(kd + b);
+          vs[b] = __ldg(vd + b);
+        }
+      } else {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          kw[b] = vw[b] = 0x88888888u;
+          ks[b] = vs[b] = 0;
+        }
+      }
+      // row r of the group is packed row t + r - first
+      auto in = [&](int r) { return r >= first && r < first + count; };
+      const int64_t width = a.heads * D;
+      T* kd = a.dst[0] + (int64_t)(t + g - first) * width + h * D + 8 * tq;
+      T* vd = a.dst[1] + (int64_t)(t + 2 * tq - first) * width + h * D + 4 * g;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const float2 dk = __half22float2(*reinterpret_cast<const __half2*>(&ks[b]));
+        const float2 dv = __half22float2(*reinterpret_cast<const __half2*>(&vs[b]));
+        const float d = (g & 1) ? dk.y : dk.x;
+        uint32_t r[4];
+        float x[8], even[4], odd[4];
+        kvq_unpack_centred(kw[b], r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r[i]));
+          x[i] = f.x * d;
+          x[i + 4] = f.y * d;
+        }
+        if (in(g)) kvq_store8(kd + 32 * b, x);
+        kvq_unpack_centred(vw[b], r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r[i]));
+          even[i] = f.x * dv.x;
+          odd[i] = f.y * dv.y;
+        }
+        if (in(2 * tq)) kvq_store4(vd + 32 * b, even);
+        if (in(2 * tq + 1)) kvq_store4(vd + width + 32 * b, odd);
+      }
+      t = stop;
+    }
+  }
+}
+
+// CTAs for so many warps' work.
+unsigned row_blocks(int64_t warps, int num_sms) {
   constexpr int PER = ROW_THREADS / 32;
-  const int64_t need = (2 * total + PER - 1) / PER, most = (int64_t)num_sms * (2048 / ROW_THREADS);
+  const int64_t need = (warps + PER - 1) / PER, most = (int64_t)num_sms * (2048 / ROW_THREADS);
   return (unsigned)(need < most ? need : most);
 }
 
@@ -206,7 +296,7 @@ int append_as(const KvqStep& c, const void* k_new, const void* v_new, const int6
   a.pos = c.pos;
   a.S = c.S;
   a.status = c.status;
-  const unsigned grid = row_blocks(c.total, c.num_sms);
+  const unsigned grid = row_blocks(2 * c.total, c.num_sms);
   if (c.head_dim == 128) kvq_append_kernel<128, T><<<grid, ROW_THREADS, 0, s>>>(a);
   else kvq_append_kernel<64, T><<<grid, ROW_THREADS, 0, s>>>(a);
   return cudaGetLastError() == cudaSuccess ? Q4_OK : Q4_ERR_CUDA;
@@ -228,9 +318,18 @@ int read_as(const KvqStep& c, const uint8_t* cache, void* k_out, void* v_out, cu
   a.pos = c.pos;
   a.S = c.S;
   a.status = c.status;
-  const unsigned grid = row_blocks(c.total, c.num_sms);
-  if (c.head_dim == 128) kvq_read_kernel<128, T><<<grid, ROW_THREADS, 0, s>>>(a);
-  else kvq_read_kernel<64, T><<<grid, ROW_THREADS, 0, s>>>(a);
+  // Groups pay where most rows have neighbours in their request: 65,536 rows of
+  // 32 requests, 4 heads, took 27.5 us against 54 row by row, and a decode step's
+  // single rows would wait for eight requests one after another.
+  if (c.total >= 8 * (int64_t)c.S) {
+    const unsigned grid = row_blocks((c.total + 7) / 8 * c.heads, c.num_sms);
+    if (c.head_dim == 128) kvq_read_groups_kernel<128, T><<<grid, ROW_THREADS, 0, s>>>(a);
+    else kvq_read_groups_kernel<64, T><<<grid, ROW_THREADS, 0, s>>>(a);
+  } else {
+    const unsigned grid = row_blocks(2 * c.total, c.num_sms);
+    if (c.head_dim == 128) kvq_read_kernel<128, T><<<grid, ROW_THREADS, 0, s>>>(a);
+    else kvq_read_kernel<64, T><<<grid, ROW_THREADS, 0, s>>>(a);
+  }
   return cudaGetLastError() == cudaSuccess ? Q4_OK : Q4_ERR_CUDA;
 }
 

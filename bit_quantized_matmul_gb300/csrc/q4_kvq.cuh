@@ -163,4 +163,15 @@ __device__ __forceinline__ void kvq_store8(__nv_bfloat16* p, const float (&v)[8]
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Four consecutive elements from fp32, rounded once (8-byte aligned, 16 for fp32).
+template <typename T>
+__device__ __forceinline__ void kvq_store4(T* p, const float (&v)[4]) {
+  if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+    const T h[4] = {(T)v[0], (T)v[1], (T)v[2], (T)v[3]};
+    *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(h);
+  }
+}
+
 }  // namespace q4

@@ -50,6 +50,7 @@ constexpr int THREADS = 32 * WARPS;
 constexpr int ROWS = 8;               // virtual rows of an item
 constexpr int CTAS_PER_SM = 3;
 constexpr int STAGES = 3;             // tiles in flight per warp
+constexpr int JOIN_WARPS = 8;
 constexpr int MASS_STAGES = 4;        // K halves in flight per warp of the weights' launch
 constexpr int MASS_CTAS_PER_SM = 4;
 constexpr int ITEM_UNITS = 2;         // what beginning an item costs, in tiles: its queries, its sums' end
@@ -533,16 +534,6 @@ __device__ __forceinline__ void take_tile(const uint8_t* tile, int p0, const Que
 
 // ---------------------------------------------------------------- main kernel
 template <int D, typename T>
-__device__ __forceinline__ void store4(T* p, const float (&v)[4]) {
-  if constexpr (sizeof(T) == 4) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  } else {
-    T h[4] = {(T)v[0], (T)v[1], (T)v[2], (T)v[3]};
-    *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(h);
-  }
-}
-
-template <int D, typename T>
 __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kvq_attention_kernel(const Args<T> a) {
   using L = Kvq<D>;
   constexpr int NB = L::NB;
@@ -652,8 +643,8 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kvq_attention_kernel(con
       for (int b = 0; b < NB; ++b) {
         const float v[4] = {sums.o[b][0][k] * fr, sums.o[b][0][2 + k] * fr, sums.o[b][1][k] * fr,
                             sums.o[b][1][2 + k] * fr};
-        if (!whole) store4<D>(a.partial + (slot + row) * D + 32 * b + 4 * g, v);
-        else if (row0 + row < rows) store4<D>(a.out + at * D + 32 * b + 4 * g, v);
+        if (!whole) kvq_store4(a.partial + (slot + row) * D + 32 * b + 4 * g, v);
+        else if (row0 + row < rows) kvq_store4(a.out + at * D + 32 * b + 4 * g, v);
       }
     }
     out.next(a, true);
@@ -661,70 +652,99 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kvq_attention_kernel(con
 }
 
 // ---------------------------------------------------------------- join
-// One CTA per (packed row, query head): joins the partial sums of an item cut
-// between workers; rows of no request, or of one that is out of range, get zeros.
-template <int D, typename T>
-__global__ void __launch_bounds__(THREADS) kvq_join_kernel(const Args<T> a) {
-  constexpr int PER = D / 32;
-  __shared__ float2 s_ml[WARPS];
-  __shared__ float s_acc[WARPS][D];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int t = blockIdx.x, hq = blockIdx.y;
-  const int64_t at = (int64_t)t * (a.heads * a.group) + hq;
+// Joins the partial sums of items cut between workers; rows of no request, or of
+// one that is out of range, get zeros.  PER_ROW warps take a (packed row, query
+// head): one where an item has few parts, the whole CTA where it has many.
+template <int D, typename T, int PER_ROW>
+__global__ void __launch_bounds__(32 * JOIN_WARPS) kvq_join_kernel(const Args<T> a) {
+  constexpr int PER = D / 32, AT_ONCE = 8;
+  __shared__ float2 s_ml[JOIN_WARPS];
+  __shared__ float s_acc[JOIN_WARPS][D];
+  const int lane = threadIdx.x & 31;
+  const int warp = PER_ROW == 1 ? 0 : threadIdx.x >> 5, tid = warp * 32 + lane;  // within the row's warps
+  const int q_heads = a.heads * a.group;
+  const int at = PER_ROW == 1 ? blockIdx.x * JOIN_WARPS + (threadIdx.x >> 5) : blockIdx.x;
+  const int t = at / q_heads, hq = at - t * q_heads;
   asm volatile("griddepcontrol.launch_dependents;");
   const int s = kvq_find_request(a.offsets, a.S, t, lane);
   const Request r = load_request(a, s, true);
+  T* out = a.out + (int64_t)at * D;
   if (r.tiles == 0 || t < r.b || t >= r.b + r.n) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int d = tid; d < D; d += THREADS) a.out[at * D + d] = (T)0.0f;
-    if (a.lse && tid == 0) a.lse[at] = NEG_INF;
+    if (t < a.total) {
+      for (int d = tid; d < D; d += 32 * PER_ROW) out[d] = (T)0.0f;
+      if (a.lse && tid == 0) a.lse[at] = NEG_INF;
+    }
     return;
   }
   const int head = hq / a.group;
   const int vr = (t - r.b) * a.group + (hq - head * a.group);
   const int item = head * (r.items / a.heads) + vr / ROWS, row = vr % ROWS;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Shares share(a.unit_start[a.S], a.workers);
-  const int64_t u0 = a.unit_start[s] + (int64_t)item * r.span() + ITEM_UNITS;  // the first tile
+  const int64_t all = a.unit_start[a.S], u_item = a.unit_start[s];
+  const Shares share(all, a.workers);
+  const int64_t u0 = u_item + (int64_t)item * r.span() + ITEM_UNITS;  // the first tile
   const int wa = share.of(u0), wb = share.of(u0 + r.tiles - 1);
   if (wa == wb) return;  // written by the main launch
-  // each warp joins every fourth part as it comes, then the warps' sums are joined
+  // eight parts on their way at once per warp
   float top = NEG_INF, sum = 0.0f, acc[PER] = {};
   auto scale_of = [](float m, float top) { return m == NEG_INF ? 0.0f : ex2(m - top); };
-#pragma unroll 4
-  for (int w = wa + warp; w <= wb; w += WARPS) {
-    const int64_t p = (int64_t)(2 * w + (w == wa)) * ROWS + row;
-    const float2 ml = a.partial_ml[p];
-    float v[PER];
-    if constexpr (PER == 4) {
-      const float4 x = *reinterpret_cast<const float4*>(a.partial + p * D + lane * 4);
-      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-    } else {
-      const float2 x = *reinterpret_cast<const float2*>(a.partial + p * D + lane * 2);
-      v[0] = x.x; v[1] = x.y;
-    }
-    const float nt = fmaxf(top, ml.x), f0 = scale_of(top, nt), f1 = scale_of(ml.x, nt);
-    top = nt;
-    sum = sum * f0 + ml.y * f1;
+  for (int w0 = wa + warp; w0 <= wb; w0 += PER_ROW * AT_ONCE) {
+    float2 ml[AT_ONCE];
+    float v[AT_ONCE][PER];
+    float nt = top;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) acc[i] = acc[i] * f0 + v[i] * f1;
+    for (int k = 0; k < AT_ONCE; ++k) {
+      const int w = w0 + k * PER_ROW;
+      ml[k] = make_float2(NEG_INF, 0.0f);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) v[k][i] = 0.0f;
+      if (w <= wb) {
+        const int64_t p = (int64_t)(2 * w + (w == wa)) * ROWS + row;
+        ml[k] = a.partial_ml[p];
+        if constexpr (PER == 4) *reinterpret_cast<float4*>(v[k]) = *reinterpret_cast<const float4*>(a.partial + p * D + lane * 4);
+        else *reinterpret_cast<float2*>(v[k]) = *reinterpret_cast<const float2*>(a.partial + p * D + lane * 2);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < AT_ONCE; ++k) nt = fmaxf(nt, ml[k].x);
+    const float f0 = scale_of(top, nt);
+    top = nt;
+    sum *= f0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) acc[i] *= f0;
+#pragma unroll
+    for (int k = 0; k < AT_ONCE; ++k) {
+      const float f = scale_of(ml[k].x, nt);
+      sum = fmaf(ml[k].y, f, sum);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) acc[i] = fmaf(v[k][i], f, acc[i]);
+    }
+  }
+  if (PER_ROW == 1) {
+    const float inv = 1.0f / sum;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) out[lane * PER + i] = (T)(acc[i] * inv);
+    if (a.lse && lane == 0) a.lse[at] = top + log2f(sum);
+    return;
   }
   if (lane == 0) s_ml[warp] = make_float2(top, sum);
 #pragma unroll
   for (int i = 0; i < PER; ++i) s_acc[warp][lane * PER + i] = acc[i];
   __syncthreads();
+  if (tid >= D) return;
   top = NEG_INF;
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) top = fmaxf(top, s_ml[w].x);
+  for (int w = 0; w < JOIN_WARPS; ++w) top = fmaxf(top, s_ml[w].x);
   sum = 0.0f;
   float x = 0.0f;
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) {
+  for (int w = 0; w < JOIN_WARPS; ++w) {
     const float f = scale_of(s_ml[w].x, top);
     sum = fmaf(s_ml[w].y, f, sum);
-    if (tid < D) x = fmaf(s_acc[w][tid], f, x);
+    x = fmaf(s_acc[w][tid], f, x);
   }
-  if (tid < D) a.out[at * D + tid] = (T)(x / sum);
+  out[tid] = (T)(x / sum);
   if (a.lse && tid == 0) a.lse[at] = top + log2f(sum);
 }
 
@@ -872,14 +892,23 @@ int launch_as(const KvqStep& c, const uint8_t* cache, const void* q, const int64
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)c.total, (unsigned)q_heads);
-  cfg.blockDim = dim3(THREADS);
+  // Parts an item has on average: a warp joins up to 16 in two rounds of loads.
+  // 64 ragged requests (7 parts) took 42.4 us in all with a CTA a row, 36.4 with a
+  // warp; 8 requests at 32k (57 parts) 53.1 with a warp, 44.7 with a CTA.
+  const int64_t rows = c.total * q_heads;
+  const int64_t items = c.total * c.heads * ((a.group + ROWS - 1) / ROWS);
+  const bool few = items * 16 >= a.workers;
+  cfg.gridDim = dim3((unsigned)(few ? (rows + JOIN_WARPS - 1) / JOIN_WARPS : rows));
+  cfg.blockDim = dim3(32 * JOIN_WARPS);
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kvq_join_kernel<D, T>, a) != cudaSuccess) return Q4_ERR_CUDA;
+  if ((few ? cudaLaunchKernelEx(&cfg, kvq_join_kernel<D, T, 1>, a)
+           : cudaLaunchKernelEx(&cfg, kvq_join_kernel<D, T, JOIN_WARPS>, a)) != cudaSuccess)
+    return Q4_ERR_CUDA;
   if (mass) {
     cfg.gridDim = dim3(c.num_sms * MASS_CTAS_PER_SM);
+    cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = MASS_SMEM;
     if (cudaLaunchKernelEx(&cfg, kvq_mass_kernel<D, T>, a) != cudaSuccess) return Q4_ERR_CUDA;
   }

@@ -5,20 +5,24 @@
 // keep - recent of largest weight (the lowest position among equals); their
 // order is kept.  Select: a radix select over the weights' order-preserving
 // 32-bit keys (four passes of 8 bits) gives the smallest weight that stays and
-// how many positions of exactly that weight do; one more pass in position
-// order numbers the positions that stay.  Move: row i of the result is row
-// kept[i] >= i, so a copy within one slot runs chunk by chunk, each chunk read
-// whole before it is written; a copy to another slot has no order.
-//
-// Both are short: select reads 4 bytes a position from the caches a few times,
-// move reads and writes the kept rows once.
+// how many positions of exactly that weight do; then each warp counts what
+// stays in a run of positions, and with the runs before it known numbers them.
+// The weights are read once, into shared memory (caches of up to 48,000
+// positions; longer ones are read again by each pass): the passes are then
+// bound by their barriers, not by six trips to memory.
+// Move: row i of the result is row kept[i] >= i, so a copy within one slot runs
+// chunk by chunk, each chunk read whole before it is written; a copy to another
+// slot has no order.
+#include <atomic>
+
 #include "q4_kvq.cuh"
 
 namespace q4 {
 namespace {
 
-constexpr int SEL_THREADS = 512;
+constexpr int SEL_THREADS = 1024;
 constexpr int SEL_WARPS = SEL_THREADS / 32;
+constexpr int64_t SEL_SHARED_MOST = 48000;  // positions whose weights fit shared memory
 constexpr int MOVE_THREADS = 256;
 constexpr int MOVE_VEC = 4;  // pieces per thread and step
 
@@ -45,9 +49,12 @@ __device__ __forceinline__ uint32_t order_key(float f) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// SHARED: the weights are kept in shared memory.
+template <bool SHARED>
 __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const KvqEvict a) {
+  extern __shared__ float s_mass[];
   __shared__ unsigned hist[256];
-  __shared__ unsigned warp_sum[2][SEL_WARPS];
+  __shared__ int2 runs[SEL_WARPS];  // per warp's run: positions that stay for sure, and of exactly the smallest weight
   __shared__ uint32_t s_prefix;
   __shared__ unsigned s_want;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -71,6 +78,11 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const KvqEvic
   float* mass_out = a.mass + ((int64_t)a.dst[s] * a.heads + h) * a.capacity;
   if (tid == 0 && h == 0) a.new_len[s] = out_n;
   for (int i = out_n + tid; i < a.keep; i += SEL_THREADS) kept[i] = -1;
+  if (SHARED) {
+#pragma unroll 4
+    for (int p = tid; p < n; p += SEL_THREADS) s_mass[p] = mass[p];
+  }
+  auto weight = [&](int p) { return SHARED ? s_mass[p] : mass[p]; };
 
   // the key of rank `want` from the top, 8 bits at a time
   uint32_t prefix = 0;
@@ -79,9 +91,14 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const KvqEvic
     for (int shift = 24; shift >= 0; shift -= 8) {
       if (tid < 256) hist[tid] = 0;
       __syncthreads();
-      for (int p = tid; p < first; p += SEL_THREADS) {
-        const uint32_t k = order_key(mass[p]);
-        if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+      for (int p0 = warp * 32; p0 < first; p0 += SEL_THREADS) {
+        const int p = p0 + lane;
+        const uint32_t k = p < first ? order_key(weight(p)) : 0u;
+        const bool in = p < first && (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8)));
+        // one addition per value and warp: weights crowd into a few bins
+        const uint32_t bin = in ? (k >> shift) & 255u : 256u;
+        const unsigned same = __match_any_sync(0xFFFFFFFFu, bin);
+        if (in && lane == __ffs(same) - 1) atomicAdd(&hist[bin], __popc(same));
       }
       __syncthreads();
       if (warp == 0) {  // lane i sums the bins 8i .. 8i+7; the first lane from the top that reaches `left` looks closer
@@ -111,45 +128,51 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const KvqEvic
       prefix = s_prefix;
       left = s_want;
     }
+  } else {
+    __syncthreads();
   }
   const bool all_stay = want >= first, none_stays = want <= 0;
 
-  // number the positions that stay, in position order
-  int done = 0;           // written so far
-  unsigned ties = 0;      // positions of exactly the smallest weight met so far
-  for (int p0 = 0; p0 < n; p0 += SEL_THREADS) {
-    const int p = p0 + tid;
-    const bool in = p < n;
-    const float w = in ? mass[p] : 0.0f;
-    const uint32_t k = order_key(w);
-    const bool competes = in && p < first;
-    const bool tie = competes && !all_stay && !none_stays && k == prefix;
-    bool stay = in && (p >= first || all_stay || (!none_stays && k > prefix));
-    const unsigned tb = __ballot_sync(0xFFFFFFFFu, tie);
-    if (lane == 0) warp_sum[0][warp] = __popc(tb);
-    __syncthreads();
-    unsigned before = ties, all_ties = 0;
-    for (int i = 0; i < SEL_WARPS; ++i) {
-      if (i < warp) before += warp_sum[0][i];
-      all_ties += warp_sum[0][i];
-    }
+  // each warp has a run of positions, 32 at a time
+  const int run = (n + SEL_THREADS - 1) / SEL_THREADS * 32, p0 = warp * run, p1 = min(n, p0 + run);
+  auto look = [&](int p, unsigned* sure, unsigned* tie) {
+    const bool in = p < p1;
+    const uint32_t k = in && p < first ? order_key(weight(p)) : 0u;
+    *sure = __ballot_sync(0xFFFFFFFFu, in && (p >= first || all_stay || (!none_stays && k > prefix)));
+    *tie = __ballot_sync(0xFFFFFFFFu, in && p < first && !all_stay && !none_stays && k == prefix);
+  };
+  int2 mine = make_int2(0, 0);
+  for (int p = p0; p < p1; p += 32) {
+    unsigned sure, tie;
+    look(p + lane, &sure, &tie);
+    mine.x += __popc(sure);
+    mine.y += __popc(tie);
+  }
+  if (lane == 0) runs[warp] = mine;
+  __syncthreads();
+  int2 before = make_int2(0, 0);
+  for (int w = 0; w < warp; ++w) {
+    before.x += runs[w].x;
+    before.y += runs[w].y;
+  }
+  // of the first x positions, the sure ones stay and min(ties, left) of the others
+  for (int p = p0; p < p1; p += 32) {
+    unsigned sure, tie;
+    look(p + lane, &sure, &tie);
     const unsigned below = (1u << lane) - 1u;
-    if (tie) stay = before + __popc(tb & below) < left;
-    ties += all_ties;
-    const unsigned sb = __ballot_sync(0xFFFFFFFFu, stay);
-    if (lane == 0) warp_sum[1][warp] = __popc(sb);
-    __syncthreads();  // every thread has read its weight, and the weights written below lie at or before them
-    int at = done, all = 0;
-    for (int i = 0; i < SEL_WARPS; ++i) {
-      if (i < warp) at += warp_sum[1][i];
-      all += warp_sum[1][i];
-    }
-    if (stay) {
-      at += __popc(sb & below);
-      kept[at] = p;
-      mass_out[at] = w;
-    }
-    done += all;
+    const unsigned ties = before.y + __popc(tie & below);
+    if ((sure >> lane & 1u) || ((tie >> lane & 1u) && ties < left))
+      kept[before.x + __popc(sure & below) + min(ties, left)] = p + lane;
+    before.x += __popc(sure);
+    before.y += __popc(tie);
+  }
+  __syncthreads();
+  // the weights: kept[i] >= i, so a step's are read before the places of any later one's are written
+  for (int i0 = 0; i0 < out_n; i0 += SEL_THREADS) {
+    const int i = i0 + tid;
+    const float w = i < out_n ? weight(kept[i]) : 0.0f;
+    if (!SHARED) __syncthreads();
+    if (i < out_n) mass_out[i] = w;
   }
 }
 
@@ -250,7 +273,20 @@ __global__ void __launch_bounds__(MOVE_THREADS) evict_move_kernel(const KvqEvict
 
 int launch_kvq_evict(const KvqEvict& c, cudaStream_t s) {
   const int64_t planes = (int64_t)c.S * c.heads;
-  evict_select_kernel<<<(unsigned)planes, SEL_THREADS, 0, s>>>(c);
+  if (c.capacity <= SEL_SHARED_MOST) {
+    static std::atomic<bool> sized[64];  // per device: the kernel's shared memory limit is set
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return Q4_ERR_CUDA;
+    if (!sized[dev].load()) {
+      if (cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)(SEL_SHARED_MOST * sizeof(float))) != cudaSuccess)
+        return Q4_ERR_CUDA;
+      sized[dev].store(true);
+    }
+    evict_select_kernel<true><<<(unsigned)planes, SEL_THREADS, (size_t)c.capacity * sizeof(float), s>>>(c);
+  } else {
+    evict_select_kernel<false><<<(unsigned)planes, SEL_THREADS, 0, s>>>(c);
+  }
   if (cudaGetLastError() != cudaSuccess) return Q4_ERR_CUDA;
   const int64_t items = (int64_t)((c.keep + 1) / 2) * (2 * (c.head_dim / 32) + 10);
   const int64_t steps = (items + MOVE_THREADS * MOVE_VEC - 1) / (MOVE_THREADS * MOVE_VEC);
