@@ -11,8 +11,9 @@
 // positions; longer ones are read again by each pass): the passes are then
 // bound by their barriers, not by six trips to memory.
 // Move: row i of the result is row kept[i] >= i, so a copy within one slot runs
-// chunk by chunk, each chunk read whole before it is written; a copy to another
-// slot has no order.
+// step by step, each step read whole before it is written: a cluster of eight
+// CTAs does that with its barrier between the two.  A copy to another slot has
+// no order, and more clusters share it.
 #include <atomic>
 
 #include "q4_kvq.cuh"
@@ -24,7 +25,8 @@ constexpr int SEL_THREADS = 1024;
 constexpr int SEL_WARPS = SEL_THREADS / 32;
 constexpr int64_t SEL_SHARED_MOST = 48000;  // positions whose weights fit shared memory
 constexpr int MOVE_THREADS = 256;
-constexpr int MOVE_VEC = 4;  // pieces per thread and step
+constexpr int MOVE_VEC = 2;      // pieces per thread and step
+constexpr int MOVE_CLUSTER = 8;
 
 // A request whose slots, length and neighbours allow it.
 __device__ bool evict_ok(const KvqEvict& a, int s) {
@@ -95,6 +97,7 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const KvqEvic
         const int p = p0 + lane;
         const uint32_t k = p < first ? order_key(weight(p)) : 0u;
         const bool in = p < first && (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8)));
+        if (!__any_sync(0xFFFFFFFFu, in)) continue;
         // one addition per value and warp: weights crowd into a few bins
         const uint32_t bin = in ? (k >> shift) & 255u : 256u;
         const unsigned same = __match_any_sync(0xFFFFFFFFu, bin);
@@ -231,21 +234,24 @@ struct PairPieces {
 };
 
 template <int D>
-__global__ void __launch_bounds__(MOVE_THREADS) evict_move_kernel(const KvqEvict a, int64_t plane_bytes) {
+__global__ void __cluster_dims__(MOVE_CLUSTER, 1, 1) __launch_bounds__(MOVE_THREADS)
+    evict_move_kernel(const KvqEvict a, int64_t plane_bytes) {
   using R = PairPieces<D>;
   const int s = blockIdx.y / (int)a.heads, h = blockIdx.y % (int)a.heads;
   const int n = a.new_len[s];
   if (n <= 0) return;
   const int64_t src_slot = a.src[s], dst_slot = a.dst[s];
   const bool in_place = src_slot == dst_slot;
-  if (in_place && (blockIdx.x != 0 || n == a.len[s])) return;
+  // (whole clusters leave)
+  if (in_place && (blockIdx.x >= MOVE_CLUSTER || n == a.len[s])) return;
   uint8_t* src = a.cache + (src_slot * a.heads + h) * plane_bytes;
   uint8_t* dst = a.cache + (dst_slot * a.heads + h) * plane_bytes;
   const int32_t* kept = a.kept + (int64_t)blockIdx.y * a.keep;
   const int items = (n + 1) / 2 * R::PIECES;  // below 2^31: checked on the host
   constexpr int STEP = MOVE_THREADS * MOVE_VEC;
-  const int first = in_place ? 0 : blockIdx.x * STEP, stride = in_place ? STEP : gridDim.x * STEP;
-  for (int i0 = first; i0 < items; i0 += stride) {
+  const int stride = (in_place ? MOVE_CLUSTER : gridDim.x) * STEP;
+  for (int step = 0; step < items; step += stride) {
+    const int i0 = step + blockIdx.x * STEP;
     typename R::Piece v[MOVE_VEC];
 #pragma unroll
     for (int u = 0; u < MOVE_VEC; ++u) {
@@ -257,7 +263,8 @@ __global__ void __launch_bounds__(MOVE_THREADS) evict_move_kernel(const KvqEvict
         v[u] = R::read(src, p0, p1, e);
       }
     }
-    if (in_place) __syncthreads();  // the step is read before it is written; later steps read from further on
+    if (in_place)  // the step is read before it is written; later steps read from further on
+      asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 #pragma unroll
     for (int u = 0; u < MOVE_VEC; ++u) {
       const int it = i0 + u * MOVE_THREADS + threadIdx.x;
@@ -290,8 +297,9 @@ int launch_kvq_evict(const KvqEvict& c, cudaStream_t s) {
   if (cudaGetLastError() != cudaSuccess) return Q4_ERR_CUDA;
   const int64_t items = (int64_t)((c.keep + 1) / 2) * (2 * (c.head_dim / 32) + 10);
   const int64_t steps = (items + MOVE_THREADS * MOVE_VEC - 1) / (MOVE_THREADS * MOVE_VEC);
-  int64_t gx = ((int64_t)c.num_sms * 8 + planes - 1) / planes;
+  int64_t gx = ((int64_t)c.num_sms * 32 + planes - 1) / planes;
   if (gx > steps) gx = steps;
+  gx = (gx + MOVE_CLUSTER - 1) / MOVE_CLUSTER * MOVE_CLUSTER;
   const dim3 grid((unsigned)gx, (unsigned)planes);
   const int64_t pb = kvq_plane_bytes(c.head_dim, c.capacity);
   if (c.head_dim == 128) evict_move_kernel<128><<<grid, MOVE_THREADS, 0, s>>>(c, pb);
