@@ -397,16 +397,23 @@ _f32, _i32 = torch.float32, torch.int32
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _call(fn, what: str, device: torch.device, stream, *args):
-    """fn(*args, stream) with `device` current; raises on a status that is not Q4_OK."""
-    if torch.cuda.current_device() != device.index:
-        with torch.cuda.device(device):
-            return _call(fn, what, device, stream, *args)
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _enter(device_index: int, stream):
+    """The raw stream of a call on that device, which has to be current."""
     if stream is None and _raw_stream is not None:
-        stream = _raw_stream(device.index)
+        return _raw_stream(device_index)
+    return _stream(stream)
+
+
+def _call(fn, what: str, index: int, stream, *args):
+    """fn(*args, stream) with CUDA device `index` current; raises on a status that is not Q4_OK."""
+    if _get_device() == index:
+        status = fn(*args, _enter(index, stream))
     else:
-        stream = _stream(stream)
-    status = fn(*args, stream)
+        with torch.cuda.device(index):
+            status = fn(*args, _enter(index, stream))
     if status != Q4_OK:
         raise Q4Error(status, what)
 
@@ -418,23 +425,23 @@ def _dtype_code(dtype, name: str) -> int:
     return code
 
 
-def _rows3(t: torch.Tensor, name: str, heads: int, head_dim: int, dtype, device):
-    """(rows, the two outer strides) of a [rows, heads, head_dim] view with contiguous head_dim."""
+def _rows3(t: torch.Tensor, name: str, heads: int, head_dim: int, dtype, index: int):
+    """(rows, the two outer strides) of a [rows, heads, head_dim] view with contiguous head_dim on device `index`."""
     shape = t.shape
     if len(shape) != 3 or shape[1] != heads or shape[2] != head_dim:
         raise ValueError("%s must be a [rows, %d, %d] view" % (name, heads, head_dim))
     s0, s1, s2 = t.stride()
     if s2 != 1 and t.numel():
         raise ValueError("%s must have contiguous rows of head_dim values" % name)
-    if t.dtype != dtype or t.device != device:
-        raise ValueError("%s must be %s on %s" % (name, dtype, device))
+    if t.dtype is not dtype or t.get_device() != index:
+        raise ValueError("%s must be %s on CUDA device %d" % (name, dtype, index))
     return shape[0], _I64x2(s0, s1)
 
 
-def _ints(device, t: torch.Tensor, name: str) -> int:
-    """Length of a contiguous int32 tensor on `device`."""
-    if t.dtype != _i32 or t.device != device or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous int32 tensor on %s" % (name, device))
+def _ints(index: int, t: torch.Tensor, name: str) -> int:
+    """Length of a contiguous int32 tensor on device `index`."""
+    if t.dtype is not _i32 or t.get_device() != index or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 tensor on CUDA device %d" % (name, index))
     return t.numel()
 
 
@@ -461,7 +468,7 @@ class Q4KVCache:
         self.data = torch.zeros(n.value, dtype=torch.uint8, device=device)
         self.device = self.data.device
         self._dims = (self.slots, self.heads, self.head_dim, self.capacity)
-        self._ptr = self.data.data_ptr()
+        self._ptr, self._index = self.data.data_ptr(), self.data.get_device()
 
     @property
     def nbytes(self) -> int:
@@ -473,9 +480,9 @@ class Q4KVCache:
 
 
 def _step(cache: Q4KVCache, offsets, slot, pos) -> int:
-    device = cache.device
-    S = _ints(device, slot, "slot")
-    if _ints(device, offsets, "offsets") != S + 1 or _ints(device, pos, "pos") != S:
+    index = cache._index
+    S = _ints(index, slot, "slot")
+    if _ints(index, offsets, "offsets") != S + 1 or _ints(index, pos, "pos") != S:
         raise ValueError("offsets must have S + 1 entries and pos S")
     return S
 
@@ -495,14 +502,14 @@ def q4_kvq_append(cache: Q4KVCache, k_new: torch.Tensor, v_new: torch.Tensor, of
     step becomes position pos[s] + j of slot[s].
     """
     S = _step(cache, offsets, slot, pos)
-    dtype, device = k_new.dtype, cache.device
+    dtype, index = k_new.dtype, cache._index
     code = _dtype_code(dtype, "k_new")
     slots, heads, d, cap = cache._dims
-    total, ks = _rows3(k_new, "k_new", heads, d, dtype, device)
-    total_v, vs = _rows3(v_new, "v_new", heads, d, dtype, device)
+    total, ks = _rows3(k_new, "k_new", heads, d, dtype, index)
+    total_v, vs = _rows3(v_new, "v_new", heads, d, dtype, index)
     if total_v != total:
         raise ValueError("k_new and v_new differ in rows")
-    _call(_lib.q4_kvq_append, "q4_kvq_append", device, stream, cache._ptr, k_new.data_ptr(), v_new.data_ptr(), code,
+    _call(_lib.q4_kvq_append, "q4_kvq_append", index, stream, cache._ptr, k_new.data_ptr(), v_new.data_ptr(), code,
           slots, heads, d, cap, ks, vs, offsets.data_ptr(), slot.data_ptr(), pos.data_ptr(), S, total)
 
 
@@ -516,7 +523,7 @@ def q4_kvq_read(cache: Q4KVCache, offsets: torch.Tensor, slot: torch.Tensor, pos
     shape = (int(total), heads, d)
     k = _out3(k, shape, dtype, device, "k")
     v = _out3(v, shape, dtype, device, "v")
-    _call(_lib.q4_kvq_read, "q4_kvq_read", device, stream, cache._ptr, k.data_ptr(), v.data_ptr(), code, slots, heads,
+    _call(_lib.q4_kvq_read, "q4_kvq_read", cache._index, stream, cache._ptr, k.data_ptr(), v.data_ptr(), code, slots, heads,
           d, cap, offsets.data_ptr(), slot.data_ptr(), pos.data_ptr(), S, shape[0])
     return k, v
 
@@ -537,9 +544,9 @@ def q4_kvq_attention(cache: Q4KVCache, q: torch.Tensor, offsets: torch.Tensor, s
     hq = q.shape[1] if q.dim() == 3 else 0
     if hq == 0 or hq % heads:
         raise ValueError("q must be [total, q_heads, head_dim] with q_heads a multiple of %d" % heads)
-    total, qs = _rows3(q, "q", hq, d, dtype, device)
+    total, qs = _rows3(q, "q", hq, d, dtype, cache._index)
     out = _out3(out, (total, hq, d), dtype, device, "out")
-    _call(_lib.q4_kvq_attention, "q4_kvq_attention", device, stream, cache._ptr, q.data_ptr(), out.data_ptr(),
+    _call(_lib.q4_kvq_attention, "q4_kvq_attention", cache._index, stream, cache._ptr, q.data_ptr(), out.data_ptr(),
           None if mass is None else _mass(cache, mass), code, slots, heads, hq, d, cap, qs,
           d ** -0.5 if scale is None else scale, offsets.data_ptr(), slot.data_ptr(), pos.data_ptr(), S, total)
     return out
@@ -553,15 +560,15 @@ def q4_kvq_evict(cache: Q4KVCache, mass: torch.Tensor, src: torch.Tensor, dst: t
     positions and the others of largest mass, `keep` in all, moved in order
     to the front of slot dst[s] (the same slot: in place), mass alike.
     """
-    device, keep = cache.device, int(keep)
-    S = _ints(device, src, "src")
-    if _ints(device, dst, "dst") != S or _ints(device, length, "length") != S:
+    device, index, keep = cache.device, cache._index, int(keep)
+    S = _ints(index, src, "src")
+    if _ints(index, dst, "dst") != S or _ints(index, length, "length") != S:
         raise ValueError("src, dst and length differ in length")
     mass_ptr = _mass(cache, mass)
     slots, heads, d, cap = cache._dims
     new_length = torch.empty((S,), dtype=_i32, device=device)
     kept = torch.empty((S, heads, max(keep, 0)), dtype=_i32, device=device)
-    _call(_lib.q4_kvq_evict, "q4_kvq_evict", device, stream, cache._ptr, mass_ptr, slots, heads, d, cap,
+    _call(_lib.q4_kvq_evict, "q4_kvq_evict", index, stream, cache._ptr, mass_ptr, slots, heads, d, cap,
           src.data_ptr(), dst.data_ptr(), length.data_ptr(), S, keep, int(recent), new_length.data_ptr(),
           kept.data_ptr())
     return new_length, kept
@@ -583,17 +590,17 @@ def q4_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_off
         raise ValueError("q must be a float16 or bfloat16 CUDA tensor")
     if k_offsets is None:
         k_offsets = q_offsets
-    hq, hk, d = q.shape[1], k.shape[1], q.shape[2]
-    tq, qs = _rows3(q, "q", hq, d, dtype, device)
-    tk, ks = _rows3(k, "k", hk, d, dtype, device)
-    tv, vs = _rows3(v, "v", hk, d, dtype, device)
+    index, hq, hk, d = q.get_device(), q.shape[1], k.shape[1], q.shape[2]
+    tq, qs = _rows3(q, "q", hq, d, dtype, index)
+    tk, ks = _rows3(k, "k", hk, d, dtype, index)
+    tv, vs = _rows3(v, "v", hk, d, dtype, index)
     if tv != tk:
         raise ValueError("k and v differ in rows")
-    S = _ints(device, q_offsets, "q_offsets") - 1
-    if _ints(device, k_offsets, "k_offsets") != S + 1:
+    S = _ints(index, q_offsets, "q_offsets") - 1
+    if _ints(index, k_offsets, "k_offsets") != S + 1:
         raise ValueError("q_offsets and k_offsets differ in length")
     out = _out3(out, (tq, hq, d), dtype, device, "out")
-    _call(_lib.q4_prompt_attention, "q4_prompt_attention", device, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+    _call(_lib.q4_prompt_attention, "q4_prompt_attention", index, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
           out.data_ptr(), _DTYPES[dtype], hq, hk, d, qs, ks, vs, d ** -0.5 if scale is None else scale,
           1 if causal else 0, q_offsets.data_ptr(), k_offsets.data_ptr(), S, tq, tk)
     return out

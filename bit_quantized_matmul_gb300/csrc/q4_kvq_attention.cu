@@ -38,6 +38,7 @@
 // the plan no warp waits for another.  Items cut between warps leave
 // (reference score, sum, o) in scratch and a second launch joins them.
 #include <atomic>
+#include <type_traits>
 
 #include "q4_kvq.cuh"
 #include "q4_ptx.cuh"
@@ -69,6 +70,7 @@ struct Args {
   const int32_t *offsets, *slot, *pos;
   unsigned* status;
   unsigned long long wait_ns;
+  int stall;                // test setting: no copy is issued, so every wait runs out
   float* partial;           // [2 * workers][ROWS][D]
   float2* partial_ml;       // [2 * workers][ROWS] (reference score, sum)
   int64_t* unit_start;      // [S + 1]
@@ -431,10 +433,16 @@ struct Sums {
   }
 };
 
+// Whether the weights get a lo term: results in bfloat16 round off more than
+// binary16 weights do (2^-9 against 2^-12).  8 requests at 32k: 40.5 us without,
+// 44.7 with.
+template <typename T>
+constexpr bool WEIGHT_LO = !std::is_same<T, __nv_bfloat16>::value;
+
 // Takes the positions p0 .. p0 + 31 of a tile.  MASKED: some row does not see
 // them all; row g sees those up to `last`, and what lies at `end` and after
 // may be anything.
-template <int D, bool MASKED>
+template <int D, bool MASKED, bool LO>
 __device__ __forceinline__ void take_tile(const uint8_t* tile, int p0, const Query<D>& q, Sums<D>& a, int g, int tq,
                                           int last, int end) {
   using L = Kvq<D>;
@@ -507,7 +515,7 @@ __device__ __forceinline__ void take_tile(const uint8_t* tile, int p0, const Que
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       // weights times the block's V scales, as hi and lo terms: B operand with keys along k
-      uint32_t hi[2], lo[2];
+      uint32_t hi[2], lo[2] = {0, 0};
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         F2 x = mul2(p[u], half2_f2(vd[u][b]));
@@ -517,7 +525,12 @@ __device__ __forceinline__ void take_tile(const uint8_t* tile, int p0, const Que
           if (sc[2 * k + u][1] == NEG_INF) y.y = 0.0f;
           x = f2(y.x, y.y);
         }
-        split(x, hi[u], lo[u]);
+        if constexpr (LO) {
+          split(x, hi[u], lo[u]);
+        } else {
+          const float2 y = unf2(x);
+          hi[u] = pack(y.x, y.y);
+        }
       }
       uint32_t r0[4], r1[4];
       kvq_unpack_centred(vw[0][b], r0);
@@ -526,7 +539,7 @@ __device__ __forceinline__ void take_tile(const uint8_t* tile, int p0, const Que
       for (int i = 0; i < 2; ++i) {  // values 4g + 2i and 4g + 2i + 1 of the block as rows g and g + 8
         const uint32_t av[4] = {r0[2 * i], r0[2 * i + 1], r1[2 * i], r1[2 * i + 1]};
         mma(a.o[b][i], av, hi[0], hi[1], a.o[b][i]);
-        mma(a.o[b][i], av, lo[0], lo[1], a.o[b][i]);
+        if constexpr (LO) mma(a.o[b][i], av, lo[0], lo[1], a.o[b][i]);
       }
     }
   }
@@ -572,7 +585,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kvq_attention_kernel(con
       if (in.t0 >= in.t1) return;
       enter();
     }
-    if (lane == 0) {
+    if (lane == 0 && !a.stall) {
       const unsigned st = issued % STAGES;
       mbar_expect_tx(bar_u32 + 8 * st, L::BYTES);
       bulk_load(ring_u32 + st * L::BYTES, in_ptr, L::BYTES, bar_u32 + 8 * st);
@@ -608,8 +621,8 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kvq_attention_kernel(con
       }
       ++taken;
       const uint8_t* tile = ring + st * L::BYTES;
-      if ((t + 1) * L::POS <= clear) take_tile<D, false>(tile, t * L::POS, q, sums, g, tq, last, end);
-      else take_tile<D, true>(tile, t * L::POS, q, sums, g, tq, last, end);
+      if ((t + 1) * L::POS <= clear) take_tile<D, false, WEIGHT_LO<T>>(tile, t * L::POS, q, sums, g, tq, last, end);
+      else take_tile<D, true, WEIGHT_LO<T>>(tile, t * L::POS, q, sums, g, tq, last, end);
       __syncwarp();  // every lane has read the stage before it is written again
       issue();
     }
@@ -785,7 +798,7 @@ __global__ void __launch_bounds__(THREADS) kvq_mass_kernel(const Args<T> a) {
       int next = it.t0;
       auto issue = [&]() {
         if (next >= it.t1) return;
-        if (lane == 0) {
+        if (lane == 0 && !a.stall) {
           const unsigned st = issued % MASS_STAGES;
           mbar_expect_tx(bar_u32 + 8 * st, HALF);
           bulk_load(ring_u32 + st * HALF, plane + (int64_t)next * L::BYTES, HALF, bar_u32 + 8 * st);
@@ -867,6 +880,7 @@ int launch_as(const KvqStep& c, const uint8_t* cache, const void* q, const int64
   a.pos = c.pos;
   a.status = c.status;
   a.wait_ns = wait_limit_ns();
+  a.stall = stall_for_test();
   a.workers = c.num_sms * CTAS_PER_SM * WARPS;
   a.partial = ws.partial;
   a.partial_ml = ws.partial_ml;

@@ -91,6 +91,7 @@ struct Args {
   const int32_t *q_offsets, *k_offsets;
   unsigned* status;
   unsigned long long wait_ns;
+  int stall;  // test setting: no copy is issued, so every wait for one runs out
 };
 
 struct Seq {
@@ -355,7 +356,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (p.nblocks > 0) {
       if (lane == 0) {
         if (nq > 0) ok = mbar_wait(q_empty, (nq - 1) & 1, err, a.wait_ns);
-        if (ok) {
+        if (ok && !a.stall) {
           uint32_t bytes = 0;
           for (int t = 0; t < 2; ++t)
             if (p.blocks[t]) bytes += (uint32_t)(C::CHUNKS * P * G * 128);
@@ -375,7 +376,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int st = n % NST;
         if (lane == 0) {
           if (n >= NST) ok = mbar_wait(empty + 8 * st, ((n / NST) - 1) & 1, err, a.wait_ns);
-          if (ok) {
+          if (ok && !a.stall) {
             mbar_expect_tx(full + 8 * st, C::TILE);
             for (int c = 0; c < C::CHUNKS; ++c)
               tensor_load(ring + st * C::TILE + c * C::CHUNK, kv ? (const void*)&map_v : (const void*)&map_k,
@@ -828,6 +829,7 @@ int launch_as(const PromptAttn& c, cudaStream_t s) {
   a.k_offsets = c.k_offsets;
   a.status = c.status;
   a.wait_ns = wait_limit_ns();
+  a.stall = stall_for_test();
   // pairs of tiles: whole ones and at most one ragged per sequence
   const int64_t ctas = c.q_total / (2 * a.positions) + (c.S < c.q_total ? c.S : c.q_total);
   if (ctas >= INT32_MAX / c.kv_heads) return Q4_ERR_SHAPE;

@@ -336,7 +336,8 @@ Q4_API int q4_kv_append(void* k_cache, void* v_cache, const void* k_new, const v
  *             [offsets[s], offsets[s+1]) of the step's `total` rows.
  *   slot,pos  device, int32 [S]: request s's slot and the position of its first
  *             row in the cache; row offsets[s] + j is position pos[s] + j.
- * Host-checked for all of them: sizes >= 1, total * heads below 2^31, pointers
+ * A slot is in one request of a call at most.  Host-checked for all of them:
+ * sizes >= 1, total * heads below 2^31, S >= 1 where there are rows, pointers
  * given (INVALID_ARG); head_dim 64 or 128 (SHAPE); base addresses and
  * strides multiples of 16 bytes (ALIGN).  On the device a request whose slot
  * is outside [0, slots), or whose rows pass capacity or total, is left out (its
@@ -432,7 +433,8 @@ Q4_API int q4_kvq_evict(void* cache, float* mass, int64_t slots, int64_t heads, 
  * rounded to dtype before the product with v; sums are held in fp32.  What
  * lies outside a sequence's rows, NaN included, does not reach its results.
  * head_dim 64 or 128, at most 128 query heads per key/value head (SHAPE);
- * addresses and strides multiples of 16 bytes (ALIGN).  A sequence whose
+ * addresses and strides multiples of 16 bytes (ALIGN), strides that are taken
+ * below 2^39 elements (INVALID_ARG).  A sequence whose
  * offsets are out of range gets zeros and q4_device_status reports
  * Q4_ERR_INVALID_ARG.  Needs sm_103 (UNSUPPORTED). */
 Q4_API int q4_prompt_attention(const void* q, const void* k, const void* v, void* out, int dtype,
@@ -483,7 +485,8 @@ Q4_API int64_t q4mm_get_group_m_threshold(void);
  *   q4mm_set_stall_for_test when on, later launches withhold their first
  *                           hand-off (the converter warps hand over no chunk,
  *                           the CTAs of a K split store no partial sum, the
- *                           tensor-core producer issues no copy), so that the
+ *                           tensor-core producer and the attention kernels
+ *                           issue no copy), so that the
  *                           waiting side waits for something nothing sets and
  *                           its bound runs out.  Outputs are then unspecified.
  * Launches with no wait (one K split with the activations converted up front)

@@ -1,0 +1,140 @@
+"""Pins of the cache and attention oracle (CPU), and the host-side checks of the
+calls it stands for."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import oracle
+import synthetic
+from oracle import attention as ref
+
+
+def test_encode_is_the_canonical_block_taken_apart():
+    x = synthetic.normal(5, (3, 2, 64))
+    codes, scales = ref.encode(x)
+    blocks = oracle.quantize(x.reshape(-1, 64))
+    assert np.array_equal(oracle.dequantize(blocks).astype(np.float64).reshape(x.shape), ref.decode(codes, scales))
+    # hand-derived: -8 is the first value of largest magnitude, so d = 1 and codes are value + 8
+    hand = np.zeros((1, 32), np.float32)
+    hand[0, :4] = [-8, 3, -2.5, 8]
+    codes, scales = ref.encode(hand)
+    assert scales[0, 0] == 1.0 and codes[0, :5].tolist() == [0, 11, 5, 15, 8]
+
+
+def test_attention_of_one_key_is_its_value():
+    q, k, v = (synthetic.normal(i, (1, h, 32)) for i, h in ((1, 4), (2, 2), (3, 2)))
+    o, mass = ref.attention(q, k.astype(np.float64), v.astype(np.float64), 0, 0.2)
+    assert np.allclose(o[0], np.repeat(v[0], 2, 0)) and np.allclose(mass, [[2.0], [2.0]])
+
+
+def test_equal_scores_average_the_values():
+    q = np.zeros((2, 1, 32))
+    v = synthetic.normal(4, (5, 1, 32)).astype(np.float64)
+    o, mass = ref.attention(q, v, v, 3, 1.0)
+    assert np.allclose(o[0, 0], v[:4, 0].mean(0)) and np.allclose(o[1, 0], v[:, 0].mean(0))
+    assert np.allclose(mass, [[0.45, 0.45, 0.45, 0.45, 0.2]])
+    p = ref.prompt(q, v, v, 1.0)
+    assert np.allclose(p, o)
+    assert not ref.prompt(np.zeros((7, 1, 32)), v, v, 1.0)[:2].any()  # two rows more than keys
+
+
+def test_evict_keeps_the_latest_and_the_heaviest():
+    w = np.array([0, 5, 1, 1, 0, 1, 9, 0], np.float32)
+    assert ref.evict(w, 4, 1).tolist() == [1, 2, 6, 7]       # ties: 2 before 3 and 5
+    assert ref.evict(w, 8, 3).tolist() == list(range(8))
+    assert ref.evict(np.array([np.nan, -np.inf, -1, 0], np.float32), 2, 0).tolist() == [2, 3]
+    assert ref.evict(np.array([np.nan, -np.inf, np.nan, 0], np.float32), 2, 0).tolist() == [1, 3]
+
+
+@pytest.fixture(scope="module")
+def q4():
+    import __graft_entry__
+
+    __graft_entry__.build()
+    import bit_quantized_matmul_gb300 as q4
+
+    return q4
+
+
+A = 4096  # an aligned stand-in address: these calls return before any CUDA call
+I2 = ctypes.c_int64 * 2
+
+
+def test_cache_bytes_and_dimensions(q4):
+    lib = q4.raw_library()
+    n = ctypes.c_size_t(0)
+    assert lib.q4_kvq_cache_bytes(3, 2, 128, 33, ctypes.byref(n)) == q4.Q4_OK
+    assert n.value == 3 * 2 * 2 * 32 * (128 + 16)  # two tiles of 32 positions, 4.5 bits a value, K and V
+    assert lib.q4_kvq_cache_bytes(1, 1, 64, 1, ctypes.byref(n)) == q4.Q4_OK and n.value == 32 * 72
+    for dims, status in (((0, 1, 64, 1), q4.Q4_ERR_INVALID_ARG), ((1, 1, 32, 1), q4.Q4_ERR_SHAPE),
+                         ((1, 1, 64, 1 << 31), q4.Q4_ERR_INVALID_ARG),
+                         ((1 << 30, 1 << 30, 64, 1), q4.Q4_ERR_INVALID_ARG)):
+        assert lib.q4_kvq_cache_bytes(*dims, ctypes.byref(n)) == status
+    assert lib.q4_kvq_cache_bytes(1, 1, 64, 1, None) == q4.Q4_ERR_INVALID_ARG
+
+
+def test_append_and_read_arguments_checked_on_host(q4):
+    lib = q4.raw_library()
+
+    def append(p=A, dtype=0, d=64, st=(128, 64), off=A, S=1, total=1, heads=2):
+        s = I2(*st) if st else None
+        return lib.q4_kvq_append(A, p, p, dtype, 2, heads, d, 16, s, s, off, off, off, S, total, None)
+
+    assert append(S=0) == q4.Q4_OK and append(total=0) == q4.Q4_OK
+    for bad in (dict(p=None), dict(dtype=3), dict(dtype=-1), dict(st=None), dict(st=(-1, 64)), dict(off=None),
+                dict(S=-1), dict(total=-1), dict(heads=0), dict(total=1 << 30, heads=4)):
+        assert append(**bad) == q4.Q4_ERR_INVALID_ARG, bad
+    assert append(d=96) == q4.Q4_ERR_SHAPE
+    assert append(p=A + 4) == q4.Q4_ERR_ALIGN
+    assert append(st=(130, 64), total=2) == q4.Q4_ERR_ALIGN
+
+    def read(out=A, dtype=0, S=1, total=1):
+        return lib.q4_kvq_read(A, out, out, dtype, 2, 2, 64, 16, A, A, A, S, total, None)
+
+    assert read(total=0) == q4.Q4_OK
+    assert read(out=None) == q4.Q4_ERR_INVALID_ARG and read(dtype=7) == q4.Q4_ERR_INVALID_ARG
+    assert read(S=0) == q4.Q4_ERR_INVALID_ARG
+    assert read(out=A + 8) == q4.Q4_ERR_ALIGN
+
+
+def test_attention_arguments_checked_on_host(q4):
+    lib = q4.raw_library()
+
+    def attend(q=A, out=A, dtype=0, heads=2, hq=14, d=64, st=(896, 64), scale=0.125, S=1, total=1):
+        return lib.q4_kvq_attention(A, q, out, None, dtype, 2, heads, hq, d, 16, I2(*st), scale, A, A, A, S, total, None)
+
+    assert attend(total=0) == q4.Q4_OK
+    for bad in (dict(q=None), dict(out=None), dict(dtype=3), dict(hq=13), dict(hq=0), dict(scale=0.0),
+                dict(scale=-1.0), dict(scale=float("inf")), dict(scale=float("nan")), dict(scale=3e38), dict(S=0)):
+        assert attend(**bad) == q4.Q4_ERR_INVALID_ARG, bad
+    assert attend(d=80) == q4.Q4_ERR_SHAPE and attend(heads=1, hq=65536) == q4.Q4_ERR_SHAPE
+    assert attend(out=A + 4) == q4.Q4_ERR_ALIGN and attend(st=(896, 66)) == q4.Q4_ERR_ALIGN
+
+
+def test_eviction_arguments_checked_on_host(q4):
+    lib = q4.raw_library()
+
+    def evict(mass=A, S=1, keep=4, recent=1, kept=A, heads=2):
+        return lib.q4_kvq_evict(A, mass, 2, heads, 64, 16, A, A, A, S, keep, recent, A, kept, None)
+
+    assert evict(S=0) == q4.Q4_OK
+    for bad in (dict(mass=None), dict(S=-1), dict(keep=0), dict(keep=17), dict(recent=5), dict(recent=-1),
+                dict(kept=None)):
+        assert evict(**bad) == q4.Q4_ERR_INVALID_ARG, bad
+    assert evict(S=40000) == q4.Q4_ERR_SHAPE
+
+
+def test_prompt_arguments_checked_on_host(q4):
+    lib = q4.raw_library()
+
+    def prompt(q=A, k=A, out=A, dtype=1, hq=14, hk=2, d=64, st=(1152, 64), scale=0.125, off=A, S=1, tq=4, tk=4):
+        s = I2(*st)
+        return lib.q4_prompt_attention(q, k, k, out, dtype, hq, hk, d, s, s, s, scale, 1, off, off, S, tq, tk, None)
+
+    assert prompt(tq=0) == q4.Q4_OK
+    for bad in (dict(q=None), dict(k=None), dict(out=None), dict(dtype=0), dict(hq=13), dict(hk=0), dict(scale=-0.1),
+                dict(off=None), dict(S=0), dict(S=-1), dict(tq=-1), dict(tk=1 << 31)):
+        assert prompt(**bad) == q4.Q4_ERR_INVALID_ARG, bad
+    assert prompt(d=96) == q4.Q4_ERR_SHAPE and prompt(hq=129, hk=1) == q4.Q4_ERR_SHAPE
+    assert prompt(q=A + 8) == q4.Q4_ERR_ALIGN and prompt(st=(1150, 64)) == q4.Q4_ERR_ALIGN

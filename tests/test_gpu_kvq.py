@@ -333,6 +333,28 @@ def test_offsets_past_32_bits(q4):
     del cache
 
 
+@pytest.mark.parametrize("mass", [False, True])
+def test_waits_run_out_and_the_next_call_is_right(q4, mass):
+    # copies withheld: every wait gives up after its bound, and nothing of it is left behind
+    heads, hq, d = 2, 14, 64
+    cache, _ = _filled(q4, 760, [300, 20], heads, d, 320)
+    q = _normal(761, (2, hq, d), torch.float32).cuda()
+    args = (cache, q, _i32(0, 1, 2), _i32(0, 1), _i32(299, 19))
+    m = cache.new_mass() if mass else None
+    want = q4.q4_kvq_attention(*args)
+    torch.cuda.synchronize()
+    q4.q4mm_set_wait_limit_ns(1000000)
+    q4.q4mm_set_stall_for_test(True)
+    try:
+        q4.q4_kvq_attention(*args, mass=m)
+        assert q4.q4_device_status() == q4.Q4_ERR_TIMEOUT
+    finally:
+        q4.q4mm_set_stall_for_test(False)
+        q4.q4mm_set_wait_limit_ns(0)
+    assert torch.equal(q4.q4_kvq_attention(*args), want)
+    assert q4.q4_device_status() == q4.Q4_OK
+
+
 # ---------------------------------------------------------------- eviction
 
 def _evict_case(q4, seed, lens, heads, d, cap, keep, recent, in_place, mass_of=None):
@@ -371,6 +393,11 @@ def _evict_case(q4, seed, lens, heads, d, cap, keep, recent, in_place, mass_of=N
 @pytest.mark.parametrize("keep,recent", [(1, 0), (1, 1), (7, 3), (64, 64), (100, 16), (700, 33)])
 def test_evict(q4, in_place, heads, d, keep, recent):
     _evict_case(q4, 800 + keep, [0, 1, 6, 64, 100, 101, 733, 1025], heads, d, 1030, keep, recent, in_place)
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+def test_evict_of_a_cache_too_long_for_shared_memory(q4, in_place):
+    _evict_case(q4, 840, [49000, 48000], 1, 64, 49001, 5000, 100, in_place)
 
 
 def test_evict_ties_negative_and_nan_weights(q4):

@@ -199,6 +199,36 @@ def test_output_aligned_to_16_bytes_only(q4):
     assert torch.equal(q4.q4_prompt_attention(q, k, v, off, out=out), want)
 
 
+def test_one_row_and_no_keys(q4):
+    _run(q4, 93, [1], [1], 2, 14, 64, torch.float16)
+    _run(q4, 94, [3], [0], 1, 4, 128, torch.bfloat16)
+
+
+def test_keys_shared_by_stride_zero(q4):
+    # an expanded view: every head of k and v is one head's rows
+    q, k, v = (_normal(96 + i, (140, h, 64), torch.bfloat16).cuda() for i, h in enumerate((4, 1, 1)))
+    off = _i32([0, 140])
+    want = q4.q4_prompt_attention(q, k.repeat(1, 2, 1), v.repeat(1, 2, 1), off)
+    assert torch.equal(q4.q4_prompt_attention(q, k.expand(-1, 2, -1), v.expand(-1, 2, -1), off), want)
+
+
+def test_waits_run_out_and_the_next_call_is_right(q4):
+    q, k, v = (_normal(98 + i, (700, h, 128), torch.bfloat16).cuda() for i, h in enumerate((8, 2, 2)))
+    off = _i32([0, 200, 700])
+    want = q4.q4_prompt_attention(q, k, v, off)
+    torch.cuda.synchronize()
+    q4.q4mm_set_wait_limit_ns(1000000)
+    q4.q4mm_set_stall_for_test(True)
+    try:
+        q4.q4_prompt_attention(q, k, v, off)
+        assert q4.q4_device_status() == q4.Q4_ERR_TIMEOUT
+    finally:
+        q4.q4mm_set_stall_for_test(False)
+        q4.q4mm_set_wait_limit_ns(0)
+    assert torch.equal(q4.q4_prompt_attention(q, k, v, off), want)
+    assert q4.q4_device_status() == q4.Q4_OK
+
+
 def test_many_short_sequences(q4):
     lens = [1 + (7 * i) % 5 for i in range(700)]
     _run(q4, 95, lens, lens, 1, 4, 64, torch.bfloat16)
