@@ -594,8 +594,10 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kvq_attention_kernel(con
     --in_left;
     in_ptr += L::BYTES;
   };
-#pragma unroll 1
-  for (int i = 0; i < STAGES; ++i) issue();
+  // One tile each before the rest: asked for all at once, the first tiles come
+  // in among the others', and every warp begins late.
+  issue();
+  int primed = 1;
 
   while (out.t0 < out.t1) {
     const Request& r = out.r;
@@ -604,6 +606,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kvq_attention_kernel(con
     Query<D> q;
     load_query<D, T>(q, reinterpret_cast<uint4*>(smem + WARPS * STAGES * L::BYTES + warp * QUERY_BYTES<D>), a, r, head,
                      row0, lane);
+    for (; primed < STAGES; ++primed) issue();
     Sums<D> sums;
     sums.clear();
     const int last = r.pos + (row0 + g) / a.group;  // the row's last visible position
