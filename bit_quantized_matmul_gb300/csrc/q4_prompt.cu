@@ -42,7 +42,7 @@
 //
 // Masked places.  Scores past a row's limit are replaced, not added to.  A
 // weight of 0 times a NaN of V would still be NaN, so in blocks where some row
-// has such a limit warp 19 clears what V holds past the sequence, and sets
+// has such a limit warp 19 clears the rows of V that no row sees, and sets
 // aside infinities and NaN of rows that only some of the tile's rows see (they
 // are added back at the end to the rows that do see them).
 #include <cuda.h>
@@ -181,6 +181,7 @@ struct Plan {
   int blocks[2];     // key blocks of each tile
   int nblocks;       // of the pair
   int first_hidden;  // the first key that some row does not see, klen when all are seen
+  int seen_end;      // keys from here on are seen by no row
   int zone;          // blocks from here on hold such keys, or end past the sequence
   int shift;
   __device__ __forceinline__ int limit(const Args& a, const Work& w, int pos) const {
@@ -195,6 +196,7 @@ struct Plan {
       blocks[t] = p0 < w.q.qlen && last >= 0 ? last / BN + 1 : 0;
     }
     nblocks = max(blocks[0], blocks[1]);
+    seen_end = min(limit(a, w, min(w.pos0 + 2 * a.positions, w.q.qlen) - 1) + 1, w.q.klen);
     first_hidden = max(0, min(limit(a, w, w.pos0) + 1, w.q.klen));
     zone = first_hidden / BN;  // past the last block when nothing is hidden
   }
@@ -460,7 +462,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                                            mbar_wait(full + 8 * st, (v / NST) & 1, err, a.wait_ns));
           seen_once ^= 1u << st;
           if (!ok) break;
-          const int r0 = max(0, p.first_hidden - i * BN), end = min(BN, w.q.klen - i * BN);
+          // rows [r0, end) some rows see, those after it none
+          const int r0 = max(0, p.first_hidden - i * BN), end = min(BN, p.seen_end - i * BN);
           uint8_t* vb = smem_p + (ring - smem) + st * C::TILE;
           constexpr int VPR = C::CHUNKS * 8;  // 16-byte vectors per row
           auto at = [&](int row, int e) {
