@@ -25,11 +25,13 @@
 //
 // Output.  Weights differ by many binades within a row, so here hi is x
 // rounded to binary16 and the codes are made q - 8 exactly (one more
-// instruction a register, none for the offset).  V's scales are folded into
-// the weights of their block; the weights' power-of-two scale follows the
-// largest V scale met so far as their exponent follows the largest score, so
-// that they fit binary16.  Values lie along m and virtual rows along n, and hi
-// and lo go into one accumulator.
+// instruction a register, none for the offset).  V's scales are folded into the
+// weights of their block, x = w d: with w = wh + wl split once for all blocks,
+// hi = wh d rounded, and lo = (wh d - hi) + wl d, whose first part a fused
+// multiply-add gives exactly: three instructions for two weights.  Weights are
+// scaled by a power of two (2^9, less where V's scales pass 1), so that they and
+// x fit binary16 and lo keeps its bits.  Values lie along m and virtual rows
+// along n, and hi and lo go into one accumulator.
 //
 // Work.  A unit is one cache tile (32 positions) of one item (request, head,
 // eight virtual rows).  The launch's warps take equal, contiguous ranges of
@@ -99,12 +101,15 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
 }
 
 // hi and lo terms of two values
-__device__ __forceinline__ void split(F2 x, uint32_t& hi, uint32_t& lo) {
+__device__ __forceinline__ void split(F2 x, __half2& hi, __half2& lo) {
   const float2 v = unf2(x);
-  hi = pack(v.x, v.y);
-  const float2 l = unf2(fma2(half2_f2(hi), f2(-1.0f, -1.0f), x));
-  lo = pack(l.x, l.y);
+  hi = __floats2half2_rn(v.x, v.y);
+  const float2 h = __half22float2(hi);
+  const float2 l = unf2(fma2(f2(h.x, h.y), f2(-1.0f, -1.0f), x));
+  lo = __floats2half2_rn(l.x, l.y);
 }
+__device__ __forceinline__ uint32_t bits(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+__device__ __forceinline__ __half2 half2_of(uint32_t w) { return *reinterpret_cast<const __half2*>(&w); }
 
 // The operand registers of a word of codes: nibbles (0, 4), 16 * (1, 5),
 // (2, 6) and 16 * (3, 7) as binary16 pairs scaled by 2^-24.
@@ -408,15 +413,17 @@ __device__ __forceinline__ void scores(const uint8_t* tile, const Query<D>& q, i
 }
 
 // ---------------------------------------------------------------- sums
+constexpr uint32_t ONE_BITS = 0x3C00u;  // 1 in binary16
+
 // A warp's running sums over the positions it has taken.  Weights are
 // 2^(score - m + up), where m is at most SLACK below the largest score and up is
-// such that weight times V scale is at most 2^14 (2^15 for scales above 2^15).
+// 9, or such that weight times V scale is at most 2^14 (2^15 for scales above 2^15).
 template <int D>
 struct Sums {
   float o[Kvq<D>::NB][2][4];  // [block][values 4g + 2i, + 1][rows 2 tq, 2 tq + 1, twice]
   F2 l;                       // row g
   float m, off;               // row g: the reference score, and m - up (0 while m is -inf)
-  uint32_t dtop;              // the largest V scale so far, as a power of two, in both halves
+  uint32_t dtop;              // the largest V scale so far, as a power of two from 1 on, in both halves
   int up;
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -428,8 +435,8 @@ struct Sums {
     l = f2(0.0f, 0.0f);
     m = NEG_INF;
     off = 0.0f;
-    dtop = 0;
-    up = 0;
+    dtop = ONE_BITS << 16 | ONE_BITS;
+    up = 9;
   }
 };
 
@@ -481,7 +488,7 @@ __device__ __forceinline__ void take_tile(const uint8_t* tile, int p0, const Que
     uint32_t h = max(dmw & 0xFFFFu, dmw >> 16);  // magnitudes order as integers
     h = max(h, __shfl_xor_sync(0xFFFFFFFFu, h, 1));
     h = max(h, __shfl_xor_sync(0xFFFFFFFFu, h, 2));
-    h = min((max(h, 1u << 10) + 0x3FFu) & 0x7C00u, 0x7800u);  // up to a power of two, 2^-14 .. 2^15
+    h = min((h + 0x3FFu) & 0x7C00u, 0x7800u);  // up to a power of two, 1 .. 2^15
     a.dtop = h | h << 16;
     a.up = 9 + 15 - (int)(h >> 10);
     const float no = mn == NEG_INF ? 0.0f : mn - (float)a.up;
@@ -502,13 +509,18 @@ __device__ __forceinline__ void take_tile(const uint8_t* tile, int p0, const Que
   }
 #pragma unroll
   for (int k = 0; k < N / 2; ++k) {  // sixteen keys a product: eight positions 2k, eight positions 2k + 1
-    F2 p[2];
-    uint32_t vd[2][NB], vw[2][NB];
+    __half2 wh[2], wl[2];
+    uint32_t vd[2][NB], vw[2][NB], keep[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int e = 2 * k + u;
-      p[u] = f2(ex2(sc[e][0] - a.off), ex2(sc[e][1] - a.off));
-      a.l = add2(a.l, p[u]);
+      const float w0 = ex2(sc[e][0] - a.off), w1 = ex2(sc[e][1] - a.off);
+      const F2 w = f2(w0, w1);
+      a.l = add2(a.l, w);
+      if constexpr (LO) split(w, wh[u], wl[u]);
+      else wh[u] = __floats2half2_rn(w0, w1);
+      // a weight of 0 keeps a NaN scale out
+      if constexpr (MASKED) keep[u] = (sc[e][0] == NEG_INF ? 0u : 0x0000FFFFu) | (sc[e][1] == NEG_INF ? 0u : 0xFFFF0000u);
       v_scales(e, vd[u]);
       load_words<NB>(tile + L::V_OFF + 8 * e * L::ROW + (4 * g + tq) * 4 * NB, vw[u]);
     }
@@ -518,18 +530,13 @@ __device__ __forceinline__ void take_tile(const uint8_t* tile, int p0, const Que
       uint32_t hi[2], lo[2] = {0, 0};
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        F2 x = mul2(p[u], half2_f2(vd[u][b]));
-        if constexpr (MASKED) {  // a weight of 0 keeps a NaN scale out
-          float2 y = unf2(x);
-          if (sc[2 * k + u][0] == NEG_INF) y.x = 0.0f;
-          if (sc[2 * k + u][1] == NEG_INF) y.y = 0.0f;
-          x = f2(y.x, y.y);
-        }
-        if constexpr (LO) {
-          split(x, hi[u], lo[u]);
-        } else {
-          const float2 y = unf2(x);
-          hi[u] = pack(y.x, y.y);
+        const __half2 d = half2_of(vd[u][b]);
+        const __half2 h = __hmul2(wh[u], d);
+        hi[u] = bits(h);
+        if constexpr (LO) lo[u] = bits(__hfma2(wl[u], d, __hfma2(wh[u], d, __hneg2(h))));
+        if constexpr (MASKED) {
+          hi[u] &= keep[u];
+          lo[u] &= keep[u];
         }
       }
       uint32_t r0[4], r1[4];
