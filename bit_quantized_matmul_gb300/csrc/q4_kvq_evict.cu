@@ -13,7 +13,14 @@
 // Move: row i of the result is row kept[i] >= i, so a copy within one slot runs
 // step by step, each step read whole before it is written: a cluster of eight
 // CTAs does that with its barrier between the two.  A copy to another slot has
-// no order, and more clusters share it.
+// no order, and more clusters share it.  A pair of V rows shares its sectors, so
+// rows that stay alone bring their neighbours along: of 5,000 positions of
+// which 2,048 stay the copy reads nearly all of V.  128 heads of that take
+// 26 us cold (75 MB of kept rows read and written: 2.9 TB/s), bound by those
+// sectors and by the latency of one gathered step after another.  Four pieces
+// per thread and step instead of two leave that as it is, and a short eviction
+// (2 x 1,500 positions to 513, in place) goes from 15 to 16.5 us; eight take
+// 14 us more.
 #include <atomic>
 
 #include "q4_kvq.cuh"
@@ -93,15 +100,10 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const KvqEvic
     for (int shift = 24; shift >= 0; shift -= 8) {
       if (tid < 256) hist[tid] = 0;
       __syncthreads();
-      for (int p0 = warp * 32; p0 < first; p0 += SEL_THREADS) {
-        const int p = p0 + lane;
-        const uint32_t k = p < first ? order_key(weight(p)) : 0u;
-        const bool in = p < first && (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8)));
-        if (!__any_sync(0xFFFFFFFFu, in)) continue;
-        // one addition per value and warp: weights crowd into a few bins
-        const uint32_t bin = in ? (k >> shift) & 255u : 256u;
-        const unsigned same = __match_any_sync(0xFFFFFFFFu, bin);
-        if (in && lane == __ffs(same) - 1) atomicAdd(&hist[bin], __popc(same));
+#pragma unroll 4
+      for (int p = tid; p < first; p += SEL_THREADS) {
+        const uint32_t k = order_key(weight(p));
+        if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255u], 1u);
       }
       __syncthreads();
       if (warp == 0) {  // lane i sums the bins 8i .. 8i+7; the first lane from the top that reaches `left` looks closer
