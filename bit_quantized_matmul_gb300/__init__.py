@@ -468,7 +468,7 @@ class Q4KVCache:
         self.data = torch.zeros(n.value, dtype=torch.uint8, device=device)
         self.device = self.data.device
         self._dims = (self.slots, self.heads, self.head_dim, self.capacity)
-        self._ptr, self._index = self.data.data_ptr(), self.data.get_device()
+        self._index = self.data.get_device()
 
     @property
     def nbytes(self) -> int:
@@ -509,7 +509,7 @@ def q4_kvq_append(cache: Q4KVCache, k_new: torch.Tensor, v_new: torch.Tensor, of
     total_v, vs = _rows3(v_new, "v_new", heads, d, dtype, index)
     if total_v != total:
         raise ValueError("k_new and v_new differ in rows")
-    _call(_lib.q4_kvq_append, "q4_kvq_append", index, stream, cache._ptr, k_new.data_ptr(), v_new.data_ptr(), code,
+    _call(_lib.q4_kvq_append, "q4_kvq_append", index, stream, cache.data.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), code,
           slots, heads, d, cap, ks, vs, offsets.data_ptr(), slot.data_ptr(), pos.data_ptr(), S, total)
 
 
@@ -523,7 +523,7 @@ def q4_kvq_read(cache: Q4KVCache, offsets: torch.Tensor, slot: torch.Tensor, pos
     shape = (int(total), heads, d)
     k = _out3(k, shape, dtype, device, "k")
     v = _out3(v, shape, dtype, device, "v")
-    _call(_lib.q4_kvq_read, "q4_kvq_read", cache._index, stream, cache._ptr, k.data_ptr(), v.data_ptr(), code, slots, heads,
+    _call(_lib.q4_kvq_read, "q4_kvq_read", cache._index, stream, cache.data.data_ptr(), k.data_ptr(), v.data_ptr(), code, slots, heads,
           d, cap, offsets.data_ptr(), slot.data_ptr(), pos.data_ptr(), S, shape[0])
     return k, v
 
@@ -546,7 +546,7 @@ def q4_kvq_attention(cache: Q4KVCache, q: torch.Tensor, offsets: torch.Tensor, s
         raise ValueError("q must be [total, q_heads, head_dim] with q_heads a multiple of %d" % heads)
     total, qs = _rows3(q, "q", hq, d, dtype, cache._index)
     out = _out3(out, (total, hq, d), dtype, device, "out")
-    _call(_lib.q4_kvq_attention, "q4_kvq_attention", cache._index, stream, cache._ptr, q.data_ptr(), out.data_ptr(),
+    _call(_lib.q4_kvq_attention, "q4_kvq_attention", cache._index, stream, cache.data.data_ptr(), q.data_ptr(), out.data_ptr(),
           None if mass is None else _mass(cache, mass), code, slots, heads, hq, d, cap, qs,
           d ** -0.5 if scale is None else scale, offsets.data_ptr(), slot.data_ptr(), pos.data_ptr(), S, total)
     return out
@@ -568,7 +568,7 @@ def q4_kvq_evict(cache: Q4KVCache, mass: torch.Tensor, src: torch.Tensor, dst: t
     slots, heads, d, cap = cache._dims
     new_length = torch.empty((S,), dtype=_i32, device=device)
     kept = torch.empty((S, heads, max(keep, 0)), dtype=_i32, device=device)
-    _call(_lib.q4_kvq_evict, "q4_kvq_evict", index, stream, cache._ptr, mass_ptr, slots, heads, d, cap,
+    _call(_lib.q4_kvq_evict, "q4_kvq_evict", index, stream, cache.data.data_ptr(), mass_ptr, slots, heads, d, cap,
           src.data_ptr(), dst.data_ptr(), length.data_ptr(), S, keep, int(recent), new_length.data_ptr(),
           kept.data_ptr())
     return new_length, kept

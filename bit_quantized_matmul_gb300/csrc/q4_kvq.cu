@@ -6,8 +6,11 @@
 // q4_quantize, so the cache costs 4.5 bits a value where the 16-bit cache of
 // q4_kv_append costs 16.  Read: the rows back as (q - 8) * d.
 //
-// Both are bound by memory, and for a decode step by the latency of a few loads
-// one after another.  A warp takes K or V of one packed row, all heads: it finds
+// A decode step is bound by the latency of a few loads one after another: 64 rows
+// of 4 x 128 fp32 values appended and read back take 5.9 us together (two
+// launches).  Long appends are bound by instruction issue (about 250 per warp
+// and 256 values, the request's lookup included): 4,569 rows of bf16, 9.4 MB in
+// and 2.6 MB out, 11.8 us with the read back; dividing every value took 14.6.  A warp takes K or V of one packed row, all heads: it finds
 // the row's request once (32 offsets a load) while the row's first values are on
 // their way; a lane owns one 32-bit word of codes (eight values) at a time, so
 // its loads or stores of values are 16 or 32 bytes, and a block's largest
@@ -32,6 +35,8 @@ struct AppendArgs {
 
 // Quantizes the eight values of word j of a block (the quad of lanes has the
 // block): its codes, and the block's scale.  status: what was wrong with it.
+// WIDE: the values have more than 16 bits.
+template <bool WIDE>
 __device__ __forceinline__ uint32_t quantize_word(const float (&v)[8], int j, int lane, uint16_t* scale,
                                                   unsigned* status) {
   // the first value of largest magnitude (lowest index among equals), and
@@ -50,7 +55,7 @@ __device__ __forceinline__ uint32_t quantize_word(const float (&v)[8], int j, in
     m = take ? om : m;
   }
   const unsigned odd = __ballot_sync(0xFFFFFFFFu, !finite) >> (lane & 28) & 0xFu;
-  const float d = __fdiv_rn(m, -8.0f);
+  const float d = m * -0.125f;
   const uint16_t d16 = __half_as_ushort(__float2half_rn(d));
   if (odd || (d16 & 0x7C00u) == 0x7C00u) {
     // a block that binary16 cannot scale reads back as NaN, as the values themselves would
@@ -58,16 +63,38 @@ __device__ __forceinline__ uint32_t quantize_word(const float (&v)[8], int j, in
     *scale = 0x7FFFu;
     return 0x99999999u;
   }
-  uint32_t codes = 0;
+  if (d16 << 1 == 0) {  // a scale of 0 makes every value 0 whatever its code
+    *scale = 0;
+    return 0x88888888u;
+  }
+  // x / d to the nearest integer, halves away from zero.  |x / d| is about 8 at
+  // most, and y = x * (1 / d) has a relative error below 2^-22.
+  // Values of 16 bits: x / d is a half exactly, or off it by 2^-15.1 of itself or more
+  // (x - h d is a whole number of units of d's last place, of which h d has
+  // 17 * 2^11 at most).  So y a little larger, by 2^-18, is never near a half.
+  // Values of 32 bits: the few y near a half, 2^-17, divide.
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));  // within 2^-23; |d| is 2^-25 or more
+  if (!WIDE) r *= 1.0f + 0x1p-18f;
+  constexpr float BASE = 0x1.8p23f;  // BASE + y holds y's integer in its low bits
+  float t[8];
+  bool clear = true;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    int qi = 8;
-    if (d != 0.0f) {
-      qi = (int)roundf(__fdiv_rn(v[i], d)) + 8;  // roundf: half away from zero
-      qi = qi < 0 ? 0 : (qi > 15 ? 15 : qi);
-    }
-    codes |= (uint32_t)qi << (4 * i);
+    const float y = v[i] * r;
+    t[i] = y + BASE;
+    if (WIDE) clear = clear && fabsf(y - (t[i] - BASE)) < 0.5f - 0x1p-17f;
   }
+  if (WIDE && !clear) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (!(fabsf(v[i] * r - (t[i] - BASE)) < 0.5f - 0x1p-17f))
+        t[i] = roundf(__fdiv_rn(v[i], d)) + BASE;  // roundf: half away from zero
+  }
+  uint32_t codes = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    codes |= (uint32_t)min(max(__float_as_int(t[i]) - (0x4B400000 - 8), 0), 15) << (4 * i);
   *scale = d16;
   return codes;
 }
@@ -101,7 +128,7 @@ __global__ void __launch_bounds__(ROW_THREADS) kvq_append_kernel(const AppendArg
       if (h + ROWS < a.heads) kvq_load8(src + (h + ROWS) * s_head, next);
       uint16_t d16;
       unsigned bad = 0;
-      const uint32_t codes = quantize_word(v, j, lane, &d16, &bad);
+      const uint32_t codes = quantize_word<sizeof(T) == 4>(v, j, lane, &d16, &bad);
       if (h < a.heads) {
         if (bad && j == 0) atomicOr(a.status, bad);
         uint8_t* dst = tile + h * a.plane_bytes;
@@ -182,7 +209,9 @@ __global__ void __launch_bounds__(ROW_THREADS) kvq_read_kernel(const ReadArgs<T>
 // that lie in eight neighbouring positions (aligned), so it reads K's and V's
 // codes of all of them as 512 consecutive bytes each (D = 128) and finds the
 // request once.  Rows 8c .. 8c + 7 of the step are one CTA warp's; they lie in
-// two such groups at most unless a request ends among them.
+// two such groups at most unless a request ends among them.  65,536 rows of
+// 4 heads (32 requests, bf16) take 28 us, 38 MB of cache in and 134 MB of values
+// out: 6.1 TB/s, bound by memory.
 template <int D, typename T>
 __global__ void __launch_bounds__(ROW_THREADS) kvq_read_groups_kernel(const ReadArgs<T> a) {
   using L = Kvq<D>;
@@ -318,9 +347,9 @@ int read_as(const KvqStep& c, const uint8_t* cache, void* k_out, void* v_out, cu
   a.pos = c.pos;
   a.S = c.S;
   a.status = c.status;
-  // Groups pay where most rows have neighbours in their request: 65,536 rows of
-  // 32 requests, 4 heads, took 27.5 us against 54 row by row, and a decode step's
-  // single rows would wait for eight requests one after another.
+  // Groups pay where most rows have neighbours in their request (28 us against 51
+  // for 32 x 2,048 rows); a decode step's single rows would wait for eight requests
+  // one after another (9 us against 3 for 64).
   if (c.total >= 8 * (int64_t)c.S) {
     const unsigned grid = row_blocks((c.total + 7) / 8 * c.heads, c.num_sms);
     if (c.head_dim == 128) kvq_read_groups_kernel<128, T><<<grid, ROW_THREADS, 0, s>>>(a);

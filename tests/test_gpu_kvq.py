@@ -87,6 +87,31 @@ def test_append_and_read_match_the_block_rule(q4, dtype, heads, d):
             assert torch.equal(got.cpu(), want)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_halves_and_their_neighbours_round_as_the_quotient_does(q4, dtype):
+    """Values on half codes, next to them in the type, and scales from the smallest to the largest."""
+    rows, heads, d = 400, 2, 128
+    g = torch.Generator().manual_seed(15)
+    top = torch.randn((rows, heads, d // 32, 1), generator=g)
+    top = (top * 2.0 ** torch.randint(-24, 15, top.shape, generator=g)).to(dtype).float()
+    x = (top / -8) * torch.randint(-16, 17, (rows, heads, d // 32, 32), generator=g) / 2
+    x = x.to(dtype)
+    step = torch.randint(-2, 3, x.shape, generator=g)
+    ints = x.view(torch.int32 if dtype == torch.float32 else torch.int16)
+    near_zero = (ints & (2 ** 31 - 1 if dtype == torch.float32 else 2 ** 15 - 1)) < 4  # a step may pass zero there
+    x = torch.where(near_zero, x, (ints + step.to(ints.dtype)).view(dtype)).float()
+    x = torch.where(x.abs() > top.abs(), top, x)
+    x[..., :1] = top
+    x = x.reshape(rows, heads, d).to(dtype)
+    cache = q4.Q4KVCache(1, heads, d, rows)
+    args = (_i32(0, rows), _i32(0), _i32(0))
+    q4.q4_kvq_append(cache, x.cuda(), x.flip(0).cuda(), *args)
+    k, v = q4.q4_kvq_read(cache, *args, rows)
+    assert q4.q4_device_status() == q4.Q4_OK
+    want = torch.from_numpy(ref.held(x.float().numpy())).float()
+    assert torch.equal(k.cpu(), want) and torch.equal(v.cpu(), want.flip(0))
+
+
 def test_append_leaves_other_rows_alone(q4):
     heads, d, cap = 2, 64, 37
     cache, rows = _filled(q4, 21, [cap, cap], heads, d, cap)
