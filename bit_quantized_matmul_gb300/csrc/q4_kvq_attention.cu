@@ -39,6 +39,16 @@
 // host needs none of them), each through its own ring of bulk copies; after
 // the plan no warp waits for another.  Items cut between warps leave
 // (reference score, sum, o) in scratch and a second launch joins them.
+//
+// Measured (28/4 heads of 128; both launches in a graph): 64 fp32 rows over
+// 176,432 positions 35.2 us (103 MB: 2.9 TB/s), 8 bf16 rows over 254,706
+// 38.1 us (147 MB: 3.9 TB/s).  The copies alone take 23 and 31 us.  What is left is
+// the arithmetic of 4-bit operands on warp-wide products: 384 warp instructions
+// for 16 positions (fp32 rows), with which issue slots are 52% busy, the ALU 41%, the
+// products 33%; three CTAs per SM (168 registers) hide no more of their latency, and
+// four (128 registers) were slower.  44 draft rows of 16 requests (five row groups a head, each unpacks
+// the cache for itself) take 22.3 us, one row over 2,049 positions of 2 heads of 64
+// 8.0 us, all of it launches and the latency of one short chain.
 #include <atomic>
 #include <type_traits>
 
@@ -441,8 +451,8 @@ struct Sums {
 };
 
 // Whether the weights get a lo term: results in bfloat16 round off more than
-// binary16 weights do (2^-9 against 2^-12).  8 requests at 32k: 40.5 us without,
-// 44.7 with.
+// binary16 weights do (2^-9 against 2^-12).  8 requests at 32k: 38.1 us without,
+// 42.4 with.
 template <typename T>
 constexpr bool WEIGHT_LO = !std::is_same<T, __nv_bfloat16>::value;
 
@@ -677,7 +687,9 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kvq_attention_kernel(con
 // ---------------------------------------------------------------- join
 // Joins the partial sums of items cut between workers; rows of no request, or of
 // one that is out of range, get zeros.  PER_ROW warps take a (packed row, query
-// head): one where an item has few parts, the whole CTA where it has many.
+// head): one where an item has few parts, the whole CTA where it has many.  Bound by
+// the latency of a few dependent loads, most of it under the main launch's end: 64
+// rows of 28 heads take 8.5 us cold and alone, and add 3 us to the main launch.
 template <int D, typename T, int PER_ROW>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) kvq_join_kernel(const Args<T> a) {
   constexpr int PER = D / 32, AT_ONCE = 8;
@@ -778,6 +790,8 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kvq_join_kernel(const Args<T>
 // as many bytes for a group of seven heads.  The eight rows' weights of a tile
 // are summed over lanes and dealt out in seven shuffles, a position to each
 // lane; every position belongs to one lane, so the sums have a fixed order.
+// 32 requests of 103,047 positions (4 heads of 128): 16.5 us cold, 30 MB of K;
+// it starts when the join is done and is bound as the main launch is.
 template <int D, typename T>
 __global__ void __launch_bounds__(THREADS) kvq_mass_kernel(const Args<T> a) {
   using L = Kvq<D>;
@@ -917,8 +931,9 @@ int launch_as(const KvqStep& c, const uint8_t* cache, const void* q, const int64
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   // Parts an item has on average: a warp joins up to 16 in two rounds of loads.
-  // 64 ragged requests (7 parts) took 42.4 us in all with a CTA a row, 36.4 with a
-  // warp; 8 requests at 32k (57 parts) 53.1 with a warp, 44.7 with a CTA.
+  // 64 ragged requests (7 parts) take 41.4 us in all with a CTA a row, 35.2 with a
+  // warp; 8 requests at 32k (57 parts) 46.1 with a warp, 38.2 with a CTA; one
+  // of 2,049 12.0 and 8.1.
   const int64_t rows = c.total * q_heads;
   const int64_t items = c.total * c.heads * ((a.group + ROWS - 1) / ROWS);
   const bool few = items * 16 >= a.workers;

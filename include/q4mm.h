@@ -388,8 +388,9 @@ Q4_API int q4_kvq_read(const void* cache, void* k_out, void* v_out, int dtype, i
  *         most one request of the call.
  * Products carry fp32 accuracy for fp32 queries; sums are held in fp32.  The
  * lengths are read on the device only: a launch of a fixed number of CTAs
- * divides them evenly, and the result does not depend on anything but the
- * arguments.  Uses the library's scratch (grown on the first call of a larger
+ * divides them evenly.  The same call gives the same bits; where a request is
+ * divided, and with it the last bits of its rows, depends on the lengths of the
+ * call's other requests.  Uses the library's scratch (grown on the first call of a larger
  * S, or of larger total * q_heads with mass): order calls on one stream. */
 Q4_API int q4_kvq_attention(const void* cache, const void* q, void* out, float* mass, int dtype,
                             int64_t slots, int64_t heads, int64_t q_heads, int64_t head_dim,
