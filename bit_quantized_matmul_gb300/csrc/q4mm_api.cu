@@ -201,14 +201,16 @@ int workspace_get(int device, size_t partial_bytes, size_t xop_bytes, Workspace*
                   size_t xpre_bytes, size_t attn_bytes) {
   DeviceScratch& ds = g_dev[device];
   if (attn_bytes > ds.ws.attn_bytes) {
+    // An outgrown area stays: a captured decode step may hold its address, and steps
+    // grow with the number of requests.  Each area is 1.5 times the last or more, so all of
+    // them together stay below three times the one in use.
     size_t want = attn_bytes + attn_bytes / 2;
-    if (ds.ws.attn) cudaFree(ds.ws.attn);
-    ds.ws.attn = nullptr;
-    ds.ws.attn_bytes = 0;
-    if (cudaMalloc(&ds.ws.attn, want) != cudaSuccess) {
+    uint8_t* area = nullptr;
+    if (cudaMalloc(&area, want) != cudaSuccess) {
       cudaGetLastError();
       return Q4_ERR_NOMEM;
     }
+    ds.ws.attn = area;
     ds.ws.attn_bytes = want;
   }
   if (xpre_bytes > ds.ws.xpre_bytes) {

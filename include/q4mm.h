@@ -390,8 +390,10 @@ Q4_API int q4_kvq_read(const void* cache, void* k_out, void* v_out, int dtype, i
  * lengths are read on the device only: a launch of a fixed number of CTAs
  * divides them evenly.  The same call gives the same bits; where a request is
  * divided, and with it the last bits of its rows, depends on the lengths of the
- * call's other requests.  Uses the library's scratch (grown on the first call of a larger
- * S, or of larger total * q_heads with mass): order calls on one stream. */
+ * call's other requests.  Uses the library's scratch: order calls on one stream.
+ * The first call, and one of a much larger S (or total * q_heads, with mass),
+ * allocates some; what it outgrows stays allocated, so graphs captured
+ * before remain valid. */
 Q4_API int q4_kvq_attention(const void* cache, const void* q, void* out, float* mass, int dtype,
                             int64_t slots, int64_t heads, int64_t q_heads, int64_t head_dim,
                             int64_t capacity, const int64_t* q_strides, float scale,

@@ -333,6 +333,36 @@ def test_attention_in_a_cuda_graph(q4):
         assert torch.equal(out, q4.q4_kvq_attention(cache, q, offsets, slot, _i32(p)))
 
 
+def test_a_captured_step_outlives_the_growth_of_the_scratch(q4):
+    cache, _ = _filled(q4, 171, [700, 33], 2, 128, 704)
+    q = _normal(173, (2, 8, 128), torch.float32).cuda()
+    step = (_starts([1, 1]), _i32(0, 1), _i32(699, 32))
+    out = torch.empty_like(q)
+    want = q4.q4_kvq_attention(cache, q, *step)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        q4.q4_kvq_attention(cache, q, *step, out=out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q4.q4_kvq_attention(cache, q, *step, out=out)
+    # 131,072 rows of 32 heads with weights: 17 MB of row sums
+    wide = q4.Q4KVCache(4096, 1, 64, 32)
+    wide.data.zero_()
+    rows = torch.zeros((4096 * 32, 32, 64), dtype=torch.bfloat16, device="cuda")
+    n = torch.arange(4097, dtype=torch.int32, device="cuda")
+    mass = wide.new_mass()
+    q4.q4_kvq_attention(wide, rows, n * 32, n[:-1].contiguous(), torch.zeros_like(n[:-1]), mass=mass)
+    total = mass.double().sum((1, 2)).cpu()
+    assert torch.allclose(total, torch.full_like(total, 32.0 * 32.0), rtol=1e-5, atol=0)
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    assert q4.q4_device_status() == q4.Q4_OK
+
+
 def test_offsets_past_32_bits(q4):
     # one plane of the cache starts beyond 2^32 bytes
     heads, hq, d = 1, 4, 128
