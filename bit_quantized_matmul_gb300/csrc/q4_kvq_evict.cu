@@ -7,21 +7,19 @@
 // 32-bit keys (four passes of 8 bits) gives the smallest weight that stays and
 // how many positions of exactly that weight do; then each warp counts what
 // stays in a run of positions, and with the runs before it known numbers them.
-// The weights are read once, into shared memory (caches of up to 48,000
+// The weights are read once, as keys into shared memory (caches of up to 48,000
 // positions; longer ones are read again by each pass): the passes are then
 // bound by their barriers, not by six trips to memory.
 // Move: row i of the result is row kept[i] >= i, so a copy within one slot runs
 // step by step, each step read whole before it is written: a cluster of eight
 // CTAs does that with its barrier between the two.  A copy to another slot has
-// no order, and more clusters share it.  A pair of V rows shares its sectors, so
-// rows that stay alone bring their neighbours along: of 5,000 positions of
-// which 2,048 stay the copy reads nearly all of V.  128 heads of that take
-// 26 us cold (75 MB of kept rows read and written: 2.9 TB/s), bound by those
-// sectors and by the latency of one gathered step after another.  Four pieces
-// per thread and step instead of two leave that as it is, and a short eviction
-// (2 x 1,500 positions to 513, in place) goes from 15 to 16.5 us; eight take
-// 14 us more.
+// no order, and more clusters share it.  V's rows lie four to a sector, so rows
+// that stay bring others along: of 5,000 positions of which 2,048 stay the copy
+// reads nearly all of V.  128 heads of that take 22 us cold, 91 MB read and 38 MB
+// written (5.9 TB/s).  A thread takes one piece a step: two or four at once
+// were slower (71 and 76 us for copy, eviction and read together, against 68).
 #include <atomic>
+#include <type_traits>
 
 #include "q4_kvq.cuh"
 
@@ -32,7 +30,6 @@ constexpr int SEL_THREADS = 1024;
 constexpr int SEL_WARPS = SEL_THREADS / 32;
 constexpr int64_t SEL_SHARED_MOST = 48000;  // positions whose weights fit shared memory
 constexpr int MOVE_THREADS = 256;
-constexpr int MOVE_VEC = 2;      // pieces per thread and step
 constexpr int MOVE_CLUSTER = 8;
 
 // A request whose slots, length and neighbours allow it.
@@ -58,10 +55,14 @@ __device__ __forceinline__ uint32_t order_key(float f) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// SHARED: the weights are kept in shared memory.
+__device__ __forceinline__ float key_weight(uint32_t k) {
+  return k == 0u ? NAN : __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
+}
+
+// SHARED: the weights' keys are kept in shared memory.
 template <bool SHARED>
 __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const KvqEvict a) {
-  extern __shared__ float s_mass[];
+  extern __shared__ uint32_t s_key[];
   __shared__ unsigned hist[256];
   __shared__ int2 runs[SEL_WARPS];  // per warp's run: positions that stay for sure, and of exactly the smallest weight
   __shared__ uint32_t s_prefix;
@@ -89,9 +90,9 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const KvqEvic
   for (int i = out_n + tid; i < a.keep; i += SEL_THREADS) kept[i] = -1;
   if (SHARED) {
 #pragma unroll 4
-    for (int p = tid; p < n; p += SEL_THREADS) s_mass[p] = mass[p];
+    for (int p = tid; p < n; p += SEL_THREADS) s_key[p] = order_key(mass[p]);
   }
-  auto weight = [&](int p) { return SHARED ? s_mass[p] : mass[p]; };
+  auto key = [&](int p) { return SHARED ? s_key[p] : order_key(mass[p]); };
 
   // the key of rank `want` from the top, 8 bits at a time
   uint32_t prefix = 0;
@@ -102,7 +103,7 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const KvqEvic
       __syncthreads();
 #pragma unroll 4
       for (int p = tid; p < first; p += SEL_THREADS) {
-        const uint32_t k = order_key(weight(p));
+        const uint32_t k = key(p);
         if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255u], 1u);
       }
       __syncthreads();
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const KvqEvic
   const int run = (n + SEL_THREADS - 1) / SEL_THREADS * 32, p0 = warp * run, p1 = min(n, p0 + run);
   auto look = [&](int p, unsigned* sure, unsigned* tie) {
     const bool in = p < p1;
-    const uint32_t k = in && p < first ? order_key(weight(p)) : 0u;
+    const uint32_t k = in && p < first ? key(p) : 0u;
     *sure = __ballot_sync(0xFFFFFFFFu, in && (p >= first || all_stay || (!none_stays && k > prefix)));
     *tie = __ballot_sync(0xFFFFFFFFu, in && p < first && !all_stay && !none_stays && k == prefix);
   };
@@ -155,11 +156,9 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const KvqEvic
   }
   if (lane == 0) runs[warp] = mine;
   __syncthreads();
-  int2 before = make_int2(0, 0);
-  for (int w = 0; w < warp; ++w) {
-    before.x += runs[w].x;
-    before.y += runs[w].y;
-  }
+  const int2 other = lane < warp ? runs[lane] : make_int2(0, 0);
+  int2 before = make_int2((int)__reduce_add_sync(0xFFFFFFFFu, (unsigned)other.x),
+                          (int)__reduce_add_sync(0xFFFFFFFFu, (unsigned)other.y));
   // of the first x positions, the sure ones stay and min(ties, left) of the others
   for (int p = p0; p < p1; p += 32) {
     unsigned sure, tie;
@@ -175,63 +174,37 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const KvqEvic
   // the weights: kept[i] >= i, so a step's are read before the places of any later one's are written
   for (int i0 = 0; i0 < out_n; i0 += SEL_THREADS) {
     const int i = i0 + tid;
-    const float w = i < out_n ? weight(kept[i]) : 0.0f;
+    const float w = i >= out_n ? 0.0f : SHARED ? key_weight(s_key[kept[i]]) : mass[kept[i]];
     if (!SHARED) __syncthreads();
     if (i < out_n) mass_out[i] = w;
   }
 }
 
-// A pair of result rows as pieces: 16-byte vectors of K codes (of either row),
-// the V word groups (both rows interleaved) and the scale words of K and V
-// (likewise).
+// A pair of result rows as pieces of a lane's load: four of K codes (of each of
+// the two rows), eight V word groups (both rows interleaved) and the scale words of K
+// and V (likewise).  Two loads make any piece; K's are two stores.
 template <int D>
 struct PairPieces {
   using L = Kvq<D>;
-  static constexpr int NB = L::NB;
-  static constexpr int CV = D / 32;          // K code vectors per row
-  static constexpr int PIECES = 2 * CV + 8 + 2;
-  struct Piece {
-    uint32_t w[4];
-  };
-  __device__ static uint8_t* tile(uint8_t* plane, int64_t p) { return plane + p / L::POS * L::BYTES; }
-  __device__ static uint4* k_vec(uint8_t* plane, int64_t p, int e) {
-    return reinterpret_cast<uint4*>(tile(plane, p) + (int)(p % L::POS) * L::ROW + e * 16);
+  static constexpr unsigned W = 4 * L::NB, K = 4, PIECES = K + 8 + 2;
+  using Vec = std::conditional_t<D == 128, uint4, uint2>;
+  static_assert(K * W == L::ROW && sizeof(Vec) == W, "a K row is four pieces");
+  // byte of piece e of position p in a plane
+  __device__ static int64_t at(unsigned p, unsigned e) {
+    const unsigned r = p % L::POS;
+    const int in = e < K ? r * L::ROW + e * W : e < K + 8 ? kvq_v_group<D>(r, e - K) : kvq_scale<D>(e - K - 8, r & ~1u, 0);
+    return (int64_t)(p / L::POS) * L::BYTES + in;
   }
-  // NB words of positions p and p ^ 1: V's group e, or the scales of K (8) or V (9)
-  __device__ static uint32_t* words(uint8_t* plane, int64_t p, int e) {
-    const int r = (int)(p % L::POS);
-    return reinterpret_cast<uint32_t*>(tile(plane, p) +
-                                       (e < 8 ? kvq_v_group<D>(r, e) : kvq_scale<D>(e - 8, r & ~1, 0)));
-  }
-  __device__ static Piece load(const uint32_t* p) {
-    Piece v;
-    if constexpr (NB == 4) *reinterpret_cast<uint4*>(v.w) = *reinterpret_cast<const uint4*>(p);
-    else *reinterpret_cast<uint2*>(v.w) = *reinterpret_cast<const uint2*>(p);
-    return v;
-  }
-  // piece e of the pair whose rows are positions p0 and p1 of `src`
-  __device__ static Piece read(uint8_t* src, int64_t p0, int64_t p1, int e) {
-    Piece v;
-    if (e < 2 * CV) {
-      *reinterpret_cast<uint4*>(v.w) = *k_vec(src, e < CV ? p0 : p1, e % CV);
-      return v;
-    }
-    v = load(words(src, p0, e - 2 * CV));
-    const Piece b = load(words(src, p1, e - 2 * CV));
-    // the half of each word that the position owns
+  // a and b with the half of each word that positions p0 and p1 own
+  __device__ static Vec merge(Vec a, Vec b, unsigned p0, unsigned p1) {
     const unsigned sel = ((p0 & 1) ? 0x32u : 0x10u) | ((p1 & 1) ? 0x7600u : 0x5400u);
-#pragma unroll
-    for (int i = 0; i < NB; ++i) v.w[i] = __byte_perm(v.w[i], b.w[i], sel);
-    return v;
-  }
-  __device__ static void write(uint8_t* dst, int64_t p, int e, const Piece& v) {  // p even
-    if (e < 2 * CV) {
-      *k_vec(dst, p + (e < CV ? 0 : 1), e % CV) = *reinterpret_cast<const uint4*>(v.w);
-      return;
+    a.x = __byte_perm(a.x, b.x, sel);
+    a.y = __byte_perm(a.y, b.y, sel);
+    if constexpr (D == 128) {
+      a.z = __byte_perm(a.z, b.z, sel);
+      a.w = __byte_perm(a.w, b.w, sel);
     }
-    uint32_t* q = words(dst, p, e - 2 * CV);
-    if constexpr (NB == 4) *reinterpret_cast<uint4*>(q) = *reinterpret_cast<const uint4*>(v.w);
-    else *reinterpret_cast<uint2*>(q) = *reinterpret_cast<const uint2*>(v.w);
+    return a;
   }
 };
 
@@ -240,40 +213,36 @@ __global__ void __cluster_dims__(MOVE_CLUSTER, 1, 1) __launch_bounds__(MOVE_THRE
     evict_move_kernel(const KvqEvict a, int64_t plane_bytes) {
   using R = PairPieces<D>;
   const int s = blockIdx.y / (int)a.heads, h = blockIdx.y % (int)a.heads;
-  const int n = a.new_len[s];
-  if (n <= 0) return;
+  const int n_out = a.new_len[s];
+  if (n_out <= 0) return;
+  const unsigned n = n_out;
   const int64_t src_slot = a.src[s], dst_slot = a.dst[s];
   const bool in_place = src_slot == dst_slot;
   // (whole clusters leave)
-  if (in_place && (blockIdx.x >= MOVE_CLUSTER || n == a.len[s])) return;
+  if (in_place && (blockIdx.x >= MOVE_CLUSTER || n_out == a.len[s])) return;
   uint8_t* src = a.cache + (src_slot * a.heads + h) * plane_bytes;
   uint8_t* dst = a.cache + (dst_slot * a.heads + h) * plane_bytes;
   const int32_t* kept = a.kept + (int64_t)blockIdx.y * a.keep;
-  const int items = (n + 1) / 2 * R::PIECES;  // below 2^31: checked on the host
-  constexpr int STEP = MOVE_THREADS * MOVE_VEC;
-  const int stride = (in_place ? MOVE_CLUSTER : gridDim.x) * STEP;
-  for (int step = 0; step < items; step += stride) {
-    const int i0 = step + blockIdx.x * STEP;
-    typename R::Piece v[MOVE_VEC];
-#pragma unroll
-    for (int u = 0; u < MOVE_VEC; ++u) {
-      const int it = i0 + u * MOVE_THREADS + threadIdx.x;
-      if (it < items) {
-        const int pair = it / R::PIECES, e = it - pair * R::PIECES;
-        const int p0 = kept[2 * pair];
-        const int p1 = 2 * pair + 1 < n ? kept[2 * pair + 1] : p0;  // a last odd row: its neighbour is never used
-        v[u] = R::read(src, p0, p1, e);
-      }
+  const unsigned items = (n + 1) / 2 * R::PIECES;  // below 2^31: checked on the host
+  const unsigned stride = (in_place ? MOVE_CLUSTER : gridDim.x) * MOVE_THREADS;
+  // (the barrier is for all threads of the cluster: the loop runs by whole steps)
+  for (unsigned step = 0; step < items; step += stride) {
+    const unsigned it = step + blockIdx.x * MOVE_THREADS + threadIdx.x;
+    const unsigned pair = it / R::PIECES, e = it % R::PIECES;
+    typename R::Vec v0, v1;
+    unsigned p0, p1;
+    if (it < items) {
+      p0 = kept[2 * pair];
+      p1 = 2 * pair + 1 < n ? kept[2 * pair + 1] : p0;  // a last odd row: its neighbour is never used
+      v0 = *reinterpret_cast<const typename R::Vec*>(src + R::at(p0, e));
+      v1 = *reinterpret_cast<const typename R::Vec*>(src + R::at(p1, e));
     }
     if (in_place)  // the step is read before it is written; later steps read from further on
       asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-#pragma unroll
-    for (int u = 0; u < MOVE_VEC; ++u) {
-      const int it = i0 + u * MOVE_THREADS + threadIdx.x;
-      if (it < items) {
-        const int pair = it / R::PIECES;
-        R::write(dst, 2 * (int64_t)pair, it - pair * R::PIECES, v[u]);
-      }
+    if (it < items) {
+      auto* out = reinterpret_cast<typename R::Vec*>(dst + R::at(2 * pair, e));
+      *out = e < R::K ? v0 : R::merge(v0, v1, p0, p1);
+      if (e < R::K) out[R::K] = v1;  // the next row's
     }
   }
 }
@@ -297,8 +266,8 @@ int launch_kvq_evict(const KvqEvict& c, cudaStream_t s) {
     evict_select_kernel<false><<<(unsigned)planes, SEL_THREADS, 0, s>>>(c);
   }
   if (cudaGetLastError() != cudaSuccess) return Q4_ERR_CUDA;
-  const int64_t items = (int64_t)((c.keep + 1) / 2) * (2 * (c.head_dim / 32) + 10);
-  const int64_t steps = (items + MOVE_THREADS * MOVE_VEC - 1) / (MOVE_THREADS * MOVE_VEC);
+  const int64_t items = (int64_t)((c.keep + 1) / 2) * PairPieces<128>::PIECES;
+  const int64_t steps = (items + MOVE_THREADS - 1) / MOVE_THREADS;
   int64_t gx = ((int64_t)c.num_sms * 32 + planes - 1) / planes;
   if (gx > steps) gx = steps;
   gx = (gx + MOVE_CLUSTER - 1) / MOVE_CLUSTER * MOVE_CLUSTER;
