@@ -69,6 +69,7 @@ __global__ void __launch_bounds__(SEL_THREADS) evict_select_kernel(const KvqEvic
   __shared__ unsigned s_want;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int s = blockIdx.x / (int)a.heads, h = blockIdx.x % (int)a.heads;
+  asm volatile("griddepcontrol.launch_dependents;");
   const bool ok = evict_ok(a, s);
   const bool apart = evict_apart(a, s);
   int32_t* kept = a.kept + (int64_t)blockIdx.x * a.keep;
@@ -212,6 +213,7 @@ template <int D>
 __global__ void __cluster_dims__(MOVE_CLUSTER, 1, 1) __launch_bounds__(MOVE_THREADS)
     evict_move_kernel(const KvqEvict a, int64_t plane_bytes) {
   using R = PairPieces<D>;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the select launch has ended
   const int s = blockIdx.y / (int)a.heads, h = blockIdx.y % (int)a.heads;
   const int n_out = a.new_len[s];
   if (n_out <= 0) return;
@@ -273,9 +275,19 @@ int launch_kvq_evict(const KvqEvict& c, cudaStream_t s) {
   gx = (gx + MOVE_CLUSTER - 1) / MOVE_CLUSTER * MOVE_CLUSTER;
   const dim3 grid((unsigned)gx, (unsigned)planes);
   const int64_t pb = kvq_plane_bytes(c.head_dim, c.capacity);
-  if (c.head_dim == 128) evict_move_kernel<128><<<grid, MOVE_THREADS, 0, s>>>(c, pb);
-  else evict_move_kernel<64><<<grid, MOVE_THREADS, 0, s>>>(c, pb);
-  return cudaGetLastError() == cudaSuccess ? Q4_OK : Q4_ERR_CUDA;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(MOVE_THREADS);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return (c.head_dim == 128 ? cudaLaunchKernelEx(&cfg, evict_move_kernel<128>, c, pb)
+                            : cudaLaunchKernelEx(&cfg, evict_move_kernel<64>, c, pb)) == cudaSuccess
+             ? Q4_OK
+             : Q4_ERR_CUDA;
 }
 
 }  // namespace q4
