@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(ROW_THREADS) kvq_append_kernel(const AppendArg
   constexpr int LPR = D / 8, ROWS = 32 / LPR;  // lanes per row, heads that a warp takes at once
   const int lane = threadIdx.x & 31;
   const int w = lane % LPR, b = w >> 2, j = w & 3;
+  asm volatile("griddepcontrol.launch_dependents;");
   const int units = 2 * (int)a.total;  // (row, K or V); below 2^31: checked on the host
   for (int u = blockIdx.x * (ROW_THREADS / 32) + (threadIdx.x >> 5); u < units; u += gridDim.x * (ROW_THREADS / 32)) {
     const int kv = u & 1, t = u >> 1;
