@@ -158,6 +158,14 @@ struct ReadArgs {
   unsigned* status;
 };
 
+// The reads' launch begins under the end of the one before, whose kernel may have
+// had the cache's older lines in the L1: codes and scales are loaded past it.
+__device__ __forceinline__ void load2(const uint32_t* p, uint32_t* w) {
+  const uint2 v = __ldcg(reinterpret_cast<const uint2*>(p));
+  w[0] = v.x;
+  w[1] = v.y;
+}
+
 template <int D, typename T>
 __global__ void __launch_bounds__(ROW_THREADS) kvq_read_kernel(const ReadArgs<T> a) {
   using L = Kvq<D>;
@@ -165,6 +173,7 @@ __global__ void __launch_bounds__(ROW_THREADS) kvq_read_kernel(const ReadArgs<T>
   const int lane = threadIdx.x & 31;
   const int w = lane % LPR, b = w >> 2, j = w & 3;
   const int units = 2 * (int)a.total;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   // K and V of neighbouring rows go to the warps of a CTA: V's rows share their memory sectors
   for (int u = blockIdx.x * (ROW_THREADS / 32) + (threadIdx.x >> 5); u < units; u += gridDim.x * (ROW_THREADS / 32)) {
     const int kv = u & 1, t = u >> 1;
@@ -185,13 +194,13 @@ __global__ void __launch_bounds__(ROW_THREADS) kvq_read_kernel(const ReadArgs<T>
         const uint8_t* src = tile + h * a.plane_bytes;
         uint32_t codes;
         if (kv == 0) {
-          codes = __ldg(reinterpret_cast<const uint32_t*>(src + kvq_k_word<D>(row, b, j)));
+          codes = __ldcg(reinterpret_cast<const uint32_t*>(src + kvq_k_word<D>(row, b, j)));
         } else {
-          codes = __ldg(reinterpret_cast<const uint16_t*>(src + kvq_v_half<D>(row, b, 2 * j))) |
-                  (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(src + kvq_v_half<D>(row, b, 2 * j + 1))) << 16;
+          codes = __ldcg(reinterpret_cast<const uint16_t*>(src + kvq_v_half<D>(row, b, 2 * j))) |
+                  (uint32_t)__ldcg(reinterpret_cast<const uint16_t*>(src + kvq_v_half<D>(row, b, 2 * j + 1))) << 16;
         }
         const float d = __half2float(
-            __ushort_as_half(__ldg(reinterpret_cast<const uint16_t*>(src + kvq_scale<D>(kv, row, b)))));
+            __ushort_as_half(__ldcg(reinterpret_cast<const uint16_t*>(src + kvq_scale<D>(kv, row, b)))));
         uint32_t r[4];
         kvq_unpack_centred(codes, r);
 #pragma unroll
@@ -220,6 +229,7 @@ __global__ void __launch_bounds__(ROW_THREADS) kvq_read_groups_kernel(const Read
   const int lane = threadIdx.x & 31;
   const int g = lane >> 2, tq = lane & 3;
   const int chunks = (int)((a.total + 7) / 8), units = chunks * (int)a.heads;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   for (int u = blockIdx.x * (ROW_THREADS / 32) + (threadIdx.x >> 5); u < units; u += gridDim.x * (ROW_THREADS / 32)) {
     const int h = u % (int)a.heads, c = u / (int)a.heads;
     const int t_end = (int)min(a.total, (int64_t)8 * c + 8);
@@ -250,11 +260,11 @@ __global__ void __launch_bounds__(ROW_THREADS) kvq_read_groups_kernel(const Read
         const uint32_t* kd = reinterpret_cast<const uint32_t*>(tile + kvq_scale<D>(0, r0 + (g & 6), 0));
         const uint32_t* vd = reinterpret_cast<const uint32_t*>(tile + kvq_scale<D>(1, r0 + 2 * tq, 0));
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          kw[b] = __ldg(k + b);
-          vw[b] = __ldg(v + b);
-          ks[b] = __ldg(kd + b);
-          vs[b] = __ldg(vd + b);
+        for (int b = 0; b < NB; b += 2) {
+          load2(k + b, kw + b);
+          load2(v + b, vw + b);
+          load2(kd + b, ks + b);
+          load2(vd + b, vs + b);
         }
       } else {
 #pragma unroll
@@ -351,16 +361,19 @@ int read_as(const KvqStep& c, const uint8_t* cache, void* k_out, void* v_out, cu
   // Groups pay where most rows have neighbours in their request (28 us against 51
   // for 32 x 2,048 rows); a decode step's single rows would wait for eight requests
   // one after another (9 us against 3 for 64).
-  if (c.total >= 8 * (int64_t)c.S) {
-    const unsigned grid = row_blocks((c.total + 7) / 8 * c.heads, c.num_sms);
-    if (c.head_dim == 128) kvq_read_groups_kernel<128, T><<<grid, ROW_THREADS, 0, s>>>(a);
-    else kvq_read_groups_kernel<64, T><<<grid, ROW_THREADS, 0, s>>>(a);
-  } else {
-    const unsigned grid = row_blocks(2 * c.total, c.num_sms);
-    if (c.head_dim == 128) kvq_read_kernel<128, T><<<grid, ROW_THREADS, 0, s>>>(a);
-    else kvq_read_kernel<64, T><<<grid, ROW_THREADS, 0, s>>>(a);
-  }
-  return cudaGetLastError() == cudaSuccess ? Q4_OK : Q4_ERR_CUDA;
+  const bool groups = c.total >= 8 * (int64_t)c.S;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(row_blocks(groups ? (c.total + 7) / 8 * c.heads : 2 * c.total, c.num_sms));
+  cfg.blockDim = dim3(ROW_THREADS);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const auto kernel = c.head_dim == 128 ? (groups ? kvq_read_groups_kernel<128, T> : kvq_read_kernel<128, T>)
+                                        : (groups ? kvq_read_groups_kernel<64, T> : kvq_read_kernel<64, T>);
+  return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? Q4_OK : Q4_ERR_CUDA;
 }
 
 }  // namespace
