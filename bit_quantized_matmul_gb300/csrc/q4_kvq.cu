@@ -7,14 +7,15 @@
 // q4_kv_append costs 16.  Read: the rows back as (q - 8) * d.
 //
 // A decode step is bound by the latency of a few loads one after another: 64 rows
-// of 4 x 128 fp32 values appended and read back take 5.9 us together (two
+// of 4 x 128 fp32 values appended and read back take 5.6 us together (two
 // launches).  Long appends are bound by instruction issue (about 250 per warp
 // and 256 values, the request's lookup included): 4,569 rows of bf16, 9.4 MB in
-// and 2.6 MB out, 11.8 us with the read back; dividing every value took 14.6.  A warp takes K or V of one packed row, all heads: it finds
-// the row's request once (32 offsets a load) while the row's first values are on
-// their way; a lane owns one 32-bit word of codes (eight values) at a time, so
-// its loads or stores of values are 16 or 32 bytes, and a block's largest
-// magnitude is found with two shuffles among the four lanes that hold it.
+// and 2.6 MB out, 13.2 us with the read back, of which the append is 10.5;
+// dividing every value cost it 12.1.  A warp takes K or V of one packed row, all
+// heads: it finds the row's request once (32 offsets a load) while the row's first
+// values are on their way; a lane owns one 32-bit word of codes (eight values) at
+// a time, so its loads or stores of values are 16 or 32 bytes, and a block's
+// largest magnitude is found with two shuffles among the four lanes that hold it.
 #include "q4_kvq.cuh"
 
 namespace q4 {
@@ -220,8 +221,8 @@ __global__ void __launch_bounds__(ROW_THREADS) kvq_read_kernel(const ReadArgs<T>
 // codes of all of them as 512 consecutive bytes each (D = 128) and finds the
 // request once.  Rows 8c .. 8c + 7 of the step are one CTA warp's; they lie in
 // two such groups at most unless a request ends among them.  65,536 rows of
-// 4 heads (32 requests, bf16) take 28 us, 38 MB of cache in and 134 MB of values
-// out: 6.1 TB/s, bound by memory.
+// 4 heads (32 requests, bf16) take 27.5 us, 38 MB of cache in and 134 MB of values
+// out: 6.2 TB/s, bound by memory.
 template <int D, typename T>
 __global__ void __launch_bounds__(ROW_THREADS) kvq_read_groups_kernel(const ReadArgs<T> a) {
   using L = Kvq<D>;

@@ -44,15 +44,16 @@
 // in the first launch is worth 2 us of every call that follows another (64 ragged
 // requests called in turn 38.8 us without, 36.8 with).
 //
-// Measured (28/4 heads of 128; both launches in a graph): 64 fp32 rows over
-// 176,432 positions 35.2 us (103 MB: 2.9 TB/s), 8 bf16 rows over 254,706
-// 38.1 us (147 MB: 3.9 TB/s).  The copies alone take 23 and 31 us.  What is left is
-// the arithmetic of 4-bit operands on warp-wide products: 384 warp instructions
-// for 16 positions (fp32 rows), with which issue slots are 52% busy, the ALU 41%, the
-// products 33%; three CTAs per SM (168 registers) hide no more of their latency, and
-// four (128 registers) were slower.  44 draft rows of 16 requests (five row groups a head, each unpacks
-// the cache for itself) take 22.3 us, one row over 2,049 positions of 2 heads of 64
-// 8.0 us, all of it launches and the latency of one short chain.
+// Measured (28/4 heads of 128; both launches in a graph, inputs past the L2): 64
+// fp32 rows over 176,432 positions 36.5 us (103 MB: 2.8 TB/s), 8 bf16 rows over
+// 254,706 39.1 us (147 MB: 3.8 TB/s).  The copies alone take 23 and 31 us.  What is
+// left is the arithmetic of 4-bit operands on warp-wide products: 384 warp
+// instructions for 16 positions (fp32 rows), with which issue slots are 52% busy, the
+// ALU 41%, the products 34%; three CTAs per SM (168 registers) hide no more of
+// their latency, and four (128 registers) were slower.  44 draft rows of 16
+// requests (five row groups a head, each unpacks the cache for itself) take 22.5 us,
+// one row over 2,049 positions of 2 heads of 64 7.9 us, all of it launches and the
+// latency of one short chain.
 #include <atomic>
 #include <type_traits>
 
@@ -455,8 +456,8 @@ struct Sums {
 };
 
 // Whether the weights get a lo term: results in bfloat16 round off more than
-// binary16 weights do (2^-9 against 2^-12).  8 requests at 32k: 38.1 us without,
-// 42.4 with.
+// binary16 weights do (2^-9 against 2^-12).  8 requests at 32k, in one graph over the
+// same inputs: 38.1 us without, 42.4 with.
 template <typename T>
 constexpr bool WEIGHT_LO = !std::is_same<T, __nv_bfloat16>::value;
 
