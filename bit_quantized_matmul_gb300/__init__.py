@@ -8,6 +8,7 @@ is missing, importing this package raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch  # device memory and streams; loads the CUDA runtime first
@@ -400,20 +401,13 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _enter(device_index: int, stream):
-    """The raw stream of a call on that device, which has to be current."""
-    if stream is None and _raw_stream is not None:
-        return _raw_stream(device_index)
-    return _stream(stream)
-
-
 def _call(fn, what: str, index: int, stream, *args):
     """fn(*args, stream) with CUDA device `index` current; raises on a status that is not Q4_OK."""
-    if _get_device() == index:
-        status = fn(*args, _enter(index, stream))
+    if stream is None and _get_device() == index and _raw_stream is not None:
+        status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
-            status = fn(*args, _enter(index, stream))
+            status = fn(*args, _stream(stream))
     if status != Q4_OK:
         raise Q4Error(status, what)
 
@@ -423,6 +417,11 @@ def _dtype_code(dtype, name: str) -> int:
     if code is None:
         raise ValueError("%s must be float32, float16 or bfloat16" % name)
     return code
+
+
+@functools.lru_cache(maxsize=1024)
+def _strides(s0: int, s1: int):
+    return _I64x2(s0, s1)  # read by the library only
 
 
 def _rows3(t: torch.Tensor, name: str, heads: int, head_dim: int, dtype, index: int):
@@ -435,7 +434,7 @@ def _rows3(t: torch.Tensor, name: str, heads: int, head_dim: int, dtype, index: 
         raise ValueError("%s must have contiguous rows of head_dim values" % name)
     if t.dtype is not dtype or t.get_device() != index:
         raise ValueError("%s must be %s on CUDA device %d" % (name, dtype, index))
-    return shape[0], _I64x2(s0, s1)
+    return shape[0], _strides(s0, s1)
 
 
 def _ints(index: int, t: torch.Tensor, name: str) -> int:

@@ -481,6 +481,53 @@ def test_evict_then_attend(q4):
     _check(o, q.double().numpy(), k, v, 89, d ** -0.5, torch.float32, "thinned")
 
 
+@pytest.mark.parametrize("heads,hq,d", [(4, 28, 128), (2, 14, 64), (8, 8, 64)])
+def test_calls_in_a_row_see_what_the_last_one_wrote(q4, heads, hq, d):
+    """Launches begin under the end of the one before: with a wait for the GPU after every call the results are the same."""
+    S, cap, keep, steps = 6, 96, 40, 24
+    k = _normal(181, (steps, S, heads, d), torch.float32).cuda()
+    v = _normal(182, (steps, S, heads, d), torch.float32).cuda()
+    q = _normal(183, (S, hq, d), torch.float32).cuda()
+    offsets, slot, zero = _starts([1] * S), _i32(*range(S)), _i32(*[0] * S)
+    lens = [70, 41, 66, 90, 40, 55]
+
+    def run(between):
+        cache, _ = _filled(q4, 185, lens, heads, d, cap)
+        mass = cache.new_mass()
+        pos = list(lens)
+        out = []
+        between()
+        for t in range(steps):
+            at = _i32(*pos)
+            q4.q4_kvq_append(cache, k[t], v[t], offsets, slot, at)
+            between()
+            # the next query is the last output: nothing comes between the calls
+            o = q4.q4_kvq_attention(cache, out[-1] if out else q, offsets, slot, at, mass=mass)
+            between()
+            o = q4.q4_kvq_attention(cache, o, offsets, slot, at, mass=mass)
+            between()
+            out.append(o)
+            pos = [p + 1 for p in pos]
+            if max(pos) > 80:
+                n, _ = q4.q4_kvq_evict(cache, mass, slot, slot, _i32(*pos), keep, 8)
+                between()
+                pos = [min(p, keep) for p in pos]
+                rows = q4.q4_kvq_read(cache, _starts(pos), slot, zero, sum(pos))
+                between()
+                out.extend(rows)
+                assert n.tolist() == pos
+                out.append(torch.ones((S, hq, d), device="cuda"))  # the next step's query
+        out.append(mass)
+        torch.cuda.synchronize()
+        return [x.cpu() for x in out]
+
+    apart = run(torch.cuda.synchronize)
+    for _ in range(3):
+        for x, y in zip(run(lambda: None), apart):
+            assert torch.equal(x, y)
+    assert q4.q4_device_status() == q4.Q4_OK
+
+
 def test_evict_refuses_slots_that_meet(q4):
     heads, d, cap = 1, 64, 40
     cache, _ = _filled(q4, 880, [40, 40, 40], heads, d, cap, slots=5)
