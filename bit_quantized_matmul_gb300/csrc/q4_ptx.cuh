@@ -139,20 +139,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[N]) {
       : "memory");
 }
 
-template <int O, int N>
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[N]) {
-  static_assert(O + 32 <= N, "range");
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-      "r"(v[O + 0]), "r"(v[O + 1]), "r"(v[O + 2]), "r"(v[O + 3]), "r"(v[O + 4]), "r"(v[O + 5]), "r"(v[O + 6]),
-      "r"(v[O + 7]), "r"(v[O + 8]), "r"(v[O + 9]), "r"(v[O + 10]), "r"(v[O + 11]), "r"(v[O + 12]), "r"(v[O + 13]),
-      "r"(v[O + 14]), "r"(v[O + 15]), "r"(v[O + 16]), "r"(v[O + 17]), "r"(v[O + 18]), "r"(v[O + 19]),
-      "r"(v[O + 20]), "r"(v[O + 21]), "r"(v[O + 22]), "r"(v[O + 23]), "r"(v[O + 24]), "r"(v[O + 25]),
-      "r"(v[O + 26]), "r"(v[O + 27]), "r"(v[O + 28]), "r"(v[O + 29]), "r"(v[O + 30]), "r"(v[O + 31])
-      : "memory");
-}
-
 // 16 consecutive columns
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
   asm volatile(
