@@ -31,7 +31,10 @@
 // multiply-add gives exactly: three instructions for two weights.  Weights are
 // scaled by a power of two (2^9, less where V's scales pass 1), so that they and
 // x fit binary16 and lo keeps its bits.  Values lie along m and virtual rows
-// along n, and hi and lo go into one accumulator.
+// along n, and hi and lo go into one accumulator.  Rows of 16 bits get the lo terms
+// too: without them sums that nearly cancel keep errors of 2^-12 of their terms,
+// more than their own rounding (8 bf16 requests at 32k would take 38.1 us instead of
+// 42.4, in one graph over the same inputs).
 //
 // Work.  A unit is one cache tile (32 positions) of one item (request, head,
 // eight virtual rows).  The launch's warps take equal, contiguous ranges of
@@ -46,7 +49,7 @@
 //
 // Measured (28/4 heads of 128; both launches in a graph, inputs past the L2): 64
 // fp32 rows over 176,432 positions 36.5 us (103 MB: 2.8 TB/s), 8 bf16 rows over
-// 254,706 39.1 us (147 MB: 3.8 TB/s).  The copies alone take 23 and 31 us.  What is
+// 254,706 44.0 us (147 MB: 3.3 TB/s).  The copies alone take 23 and 31 us.  What is
 // left is the arithmetic of 4-bit operands on warp-wide products: 384 warp
 // instructions for 16 positions (fp32 rows), with which issue slots are 52% busy, the
 // ALU 41%, the products 34%; three CTAs per SM (168 registers) hide no more of
@@ -55,7 +58,6 @@
 // one row over 2,049 positions of 2 heads of 64 7.9 us, all of it launches and the
 // latency of one short chain.
 #include <atomic>
-#include <type_traits>
 
 #include "q4_kvq.cuh"
 #include "q4_ptx.cuh"
@@ -455,16 +457,10 @@ struct Sums {
   }
 };
 
-// Whether the weights get a lo term: results in bfloat16 round off more than
-// binary16 weights do (2^-9 against 2^-12).  8 requests at 32k, in one graph over the
-// same inputs: 38.1 us without, 42.4 with.
-template <typename T>
-constexpr bool WEIGHT_LO = !std::is_same<T, __nv_bfloat16>::value;
-
 // Takes the positions p0 .. p0 + 31 of a tile.  MASKED: some row does not see
 // them all; row g sees those up to `last`, and what lies at `end` and after
 // may be anything.
-template <int D, bool MASKED, bool LO>
+template <int D, bool MASKED>
 __device__ __forceinline__ void take_tile(const uint8_t* tile, int p0, const Query<D>& q, Sums<D>& a, int g, int tq,
                                           int last, int end) {
   using L = Kvq<D>;
@@ -532,8 +528,7 @@ __device__ __forceinline__ void take_tile(const uint8_t* tile, int p0, const Que
       const float w0 = ex2(sc[e][0] - a.off), w1 = ex2(sc[e][1] - a.off);
       const F2 w = f2(w0, w1);
       a.l = add2(a.l, w);
-      if constexpr (LO) split(w, wh[u], wl[u]);
-      else wh[u] = __floats2half2_rn(w0, w1);
+      split(w, wh[u], wl[u]);
       // a weight of 0 keeps a NaN scale out
       if constexpr (MASKED) keep[u] = (sc[e][0] == NEG_INF ? 0u : 0x0000FFFFu) | (sc[e][1] == NEG_INF ? 0u : 0xFFFF0000u);
       v_scales(e, vd[u]);
@@ -542,13 +537,13 @@ __device__ __forceinline__ void take_tile(const uint8_t* tile, int p0, const Que
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       // weights times the block's V scales, as hi and lo terms: B operand with keys along k
-      uint32_t hi[2], lo[2] = {0, 0};
+      uint32_t hi[2], lo[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const __half2 d = half2_of(vd[u][b]);
         const __half2 h = __hmul2(wh[u], d);
         hi[u] = bits(h);
-        if constexpr (LO) lo[u] = bits(__hfma2(wl[u], d, __hfma2(wh[u], d, __hneg2(h))));
+        lo[u] = bits(__hfma2(wl[u], d, __hfma2(wh[u], d, __hneg2(h))));
         if constexpr (MASKED) {
           hi[u] &= keep[u];
           lo[u] &= keep[u];
@@ -561,7 +556,7 @@ __device__ __forceinline__ void take_tile(const uint8_t* tile, int p0, const Que
       for (int i = 0; i < 2; ++i) {  // values 4g + 2i and 4g + 2i + 1 of the block as rows g and g + 8
         const uint32_t av[4] = {r0[2 * i], r0[2 * i + 1], r1[2 * i], r1[2 * i + 1]};
         mma(a.o[b][i], av, hi[0], hi[1], a.o[b][i]);
-        if constexpr (LO) mma(a.o[b][i], av, lo[0], lo[1], a.o[b][i]);
+        mma(a.o[b][i], av, lo[0], lo[1], a.o[b][i]);
       }
     }
   }
@@ -647,8 +642,8 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kvq_attention_kernel(con
       }
       ++taken;
       const uint8_t* tile = ring + st * L::BYTES;
-      if ((t + 1) * L::POS <= clear) take_tile<D, false, WEIGHT_LO<T>>(tile, t * L::POS, q, sums, g, tq, last, end);
-      else take_tile<D, true, WEIGHT_LO<T>>(tile, t * L::POS, q, sums, g, tq, last, end);
+      if ((t + 1) * L::POS <= clear) take_tile<D, false>(tile, t * L::POS, q, sums, g, tq, last, end);
+      else take_tile<D, true>(tile, t * L::POS, q, sums, g, tq, last, end);
       __syncwarp();  // every lane has read the stage before it is written again
       issue();
     }
@@ -943,7 +938,7 @@ int launch_as(const KvqStep& c, const uint8_t* cache, const void* q, const int64
   if (cudaLaunchKernelEx(&cfg, kvq_attention_kernel<D, T>, a) != cudaSuccess) return Q4_ERR_CUDA;
   // Parts an item has on average: a warp joins up to 16 in two rounds of loads.
   // 64 ragged requests (7 parts) take 41.4 us in all with a CTA a row, 35.2 with a
-  // warp; 8 requests at 32k (57 parts) 46.1 with a warp, 38.2 with a CTA; one
+  // warp; 8 requests at 32k (57 parts) 8 us less with a CTA than with a warp; one
   // of 2,049 12.0 and 8.1.
   const int64_t rows = c.total * q_heads;
   const int64_t items = c.total * c.heads * ((a.group + ROWS - 1) / ROWS);

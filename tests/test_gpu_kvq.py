@@ -257,6 +257,22 @@ def test_attention_query_ranges(q4, sigma, scale):
     _attend(q4, 500, [150, 33], [1, 2], 2, 14, 128, torch.float32, sigma=sigma, scale=scale)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n", [2, 8, 70])
+def test_attention_sums_that_nearly_cancel(q4, dtype, n):
+    # every other value row is the last one's negative and weights are nearly equal: what
+    # remains is small, and the output type's own rounding of it hides nothing
+    heads, hq, d = 2, 14, 128
+    k = _normal(600, (n, heads, d), dtype)
+    v = _normal(601, (n, heads, d), dtype)
+    v[1::2] = -v[::2]
+    q = _normal(602, (1, hq, d), dtype, 1e-3)
+    cache = q4.Q4KVCache(1, heads, d, n)
+    q4.q4_kvq_append(cache, k.cuda(), v.cuda(), _i32(0, n), _i32(0), _i32(0))
+    o = q4.q4_kvq_attention(cache, q.cuda(), _i32(0, 1), _i32(0), _i32(n - 1)).cpu().double().numpy()
+    _check(o, q.double().numpy(), k.float().numpy(), v.float().numpy(), n - 1, d ** -0.5, dtype, "%d keys" % n)
+
+
 @pytest.mark.parametrize("heads,hq,d,news", [(4, 28, 128, [1, 1, 1]), (2, 14, 64, [1, 3, 4]), (1, 16, 64, [2, 0, 1])])
 def test_attention_mass(q4, heads, hq, d, news):
     _attend(q4, 600, [70, 0, 515], news, heads, hq, d, torch.float32, mass=True)
