@@ -42,7 +42,11 @@
 // host needs none of them), each through its own ring of bulk copies; after
 // the plan no warp waits for another.  Items cut between warps leave
 // (reference score, sum, o) in scratch and a second launch joins them.  Each
-// launch begins under the end of the one before and waits for it on the device; what an
+// launch begins under the end of the one before and waits for it on the device.  A launch
+// that lets others begin before its own wait is done would let them begin while a kernel
+// two places back still runs, and their waits are for the launch before them only: so the
+// first launch lets the join begin after its wait, and what the join and the weights'
+// launch read before theirs is older than the call.  What an
 // earlier launch wrote is loaded past the L1, which may hold an older line.  The wait
 // in the first launch is worth 2 us of every call that follows another (64 ragged
 // requests called in turn 38.8 us without, 36.8 with).
@@ -576,8 +580,11 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kvq_attention_kernel(con
   if (lane < STAGES) mbar_init(bar_u32 + 8 * lane, 1);
   mbar_init_fence();
   __syncwarp();
-  asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");  // this launch begins under the end of the one before
+  // Only now may the join begin, and behind it the weights' launch: what they read
+  // before their own waits (the step's description, queries, the cache) was written by
+  // launches that ended before this line.
+  asm volatile("griddepcontrol.launch_dependents;");
   const int worker = warp * gridDim.x + blockIdx.x;
 
   // the issue cursor runs ahead of the consuming one by up to STAGES tiles

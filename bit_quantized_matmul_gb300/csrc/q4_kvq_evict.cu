@@ -213,8 +213,8 @@ template <int D>
 __global__ void __cluster_dims__(MOVE_CLUSTER, 1, 1) __launch_bounds__(MOVE_THREADS)
     evict_move_kernel(const KvqEvict a, int64_t plane_bytes) {
   using R = PairPieces<D>;
-  asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the select launch has ended
+  asm volatile("griddepcontrol.launch_dependents;");  // not before: a later launch waits for this one only
   const int s = blockIdx.y / (int)a.heads, h = blockIdx.y % (int)a.heads;
   const int n_out = a.new_len[s];
   if (n_out <= 0) return;

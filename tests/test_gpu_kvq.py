@@ -605,3 +605,62 @@ def test_binding_refuses_what_does_not_fit(q4):
     q4.q4_kvq_append(cache, x[:0], x[:0], _i32(0), _i32(), _i32())
     assert q4.q4_kvq_attention(cache, x[:0], _i32(0, 0), s, p).shape == (0, 2, 64)
     assert q4.q4_device_status() == q4.Q4_OK
+
+
+# ---------------------------------------------------------------- launches that begin early
+
+@pytest.mark.parametrize("heads,hq,d", [(4, 28, 128), (2, 14, 64), (8, 8, 64)])
+@pytest.mark.parametrize("lens,news", [([700, 300, 5, 64], [1, 1, 1, 1]), ([1500, 900], [400, 33]), ([9000], [1])])
+def test_a_captured_chain_waits_for_what_it_reads(q4, heads, hq, d, lens, news):
+    """Evictions, appends and weighing calls back to back in one CUDA graph, with nothing of the host's pace
+    between them, against the same calls with a wait for the GPU after each: bit for bit, many times."""
+    S, keep, keep2 = len(lens), 256, 200
+    mid = [min(n, keep) for n in lens]                        # rows after the first eviction
+    end = [min(n + r, keep2) for n, r in zip(mid, news)]      # and after the second
+    cap = max(max(lens), max(m + r for m, r in zip(mid, news)))
+    cache, _ = _filled(q4, 190, lens, heads, d, cap)
+    full = cache.data.clone()
+    mass0 = torch.from_numpy(np.abs(synthetic.normal(192, (S, heads, cap)))).cuda()
+    mass = mass0.clone()
+    total = sum(news)
+    k, v = (_normal(193 + i, (total, heads, d), torch.bfloat16).cuda() for i in range(2))
+    q = _normal(195, (total, hq, d), torch.float32).cuda()
+    one = _normal(196, (S, hq, d), torch.float32).cuda()
+    slot, zero, lens_d, mid_d = _i32(*range(S)), _i32(*[0] * S), _i32(*lens), _i32(*mid)
+    grown_d, last_d = _i32(*[m + r for m, r in zip(mid, news)]), _i32(*[e - 1 for e in end])
+    rows, single, held = _starts(news), _starts([1] * S), _starts(end)
+
+    def chain(between):
+        cache.data.copy_(full)
+        mass.copy_(mass0)
+        between()
+        n1, kept1 = q4.q4_kvq_evict(cache, mass, slot, slot, lens_d, keep, 16)
+        between()
+        # the lengths that the eviction wrote are the positions of the next calls
+        q4.q4_kvq_append(cache, k, v, rows, slot, n1)
+        between()
+        m1 = q4.q4_kvq_attention(cache, q, rows, slot, n1, mass=mass)
+        between()
+        o = q4.q4_kvq_attention(cache, m1, rows, slot, n1)
+        between()
+        p = q4.q4_kvq_attention(cache, o, rows, slot, mid_d, mass=mass)
+        between()
+        n2, kept2 = q4.q4_kvq_evict(cache, mass, slot, slot, grown_d, keep2, 8)
+        between()
+        w = q4.q4_kvq_attention(cache, one, single, slot, last_d, mass=mass)
+        between()
+        kk, vv = q4.q4_kvq_read(cache, held, slot, zero, sum(end))
+        between()
+        return [n1, kept1, m1, o, p, n2, kept2, w, kk, vv]
+
+    want = [x.clone() for x in chain(torch.cuda.synchronize)] + [mass.clone()]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = chain(lambda: None) + [mass]
+    for _ in range(60):
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, (x, y) in enumerate(zip(outs, want)):
+            assert torch.equal(x, y), i
+    assert q4.q4_device_status() == q4.Q4_OK
