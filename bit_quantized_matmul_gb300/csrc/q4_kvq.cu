@@ -115,9 +115,9 @@ __global__ void __launch_bounds__(ROW_THREADS) kvq_append_kernel(const AppendArg
     src += w * 8;
     int h = lane / LPR;
     float v[8] = {};
-    if (h < a.heads) kvq_load8(src + h * s_head, v);
-    const int s = kvq_find_request(a.offsets, a.S, t, lane);
-    const KvqRequest q = kvq_request(a.offsets, a.slot, a.pos, s);
+    if (h < a.heads) kvq_load8<false>(src + h * s_head, v);
+    const int s = kvq_find_request<false>(a.offsets, a.S, t, lane);
+    const KvqRequest q = kvq_request<false>(a.offsets, a.slot, a.pos, s);
     if (t < q.b || t >= q.e) continue;  // a packed row that belongs to no request
     if (!q.ok(a.total, a.slots, a.capacity)) {
       if (lane == 0) atomicOr(a.status, STATUS_KV_RANGE);
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(ROW_THREADS) kvq_append_kernel(const AppendArg
     uint8_t* tile = a.cache + q.slot * a.heads * a.plane_bytes + (int64_t)(p / L::POS) * L::BYTES;
     for (int h0 = 0; h0 < a.heads; h0 += ROWS) {
       float next[8] = {};
-      if (h + ROWS < a.heads) kvq_load8(src + (h + ROWS) * s_head, next);
+      if (h + ROWS < a.heads) kvq_load8<false>(src + (h + ROWS) * s_head, next);
       uint16_t d16;
       unsigned bad = 0;
       const uint32_t codes = quantize_word<sizeof(T) == 4>(v, j, lane, &d16, &bad);
@@ -178,8 +178,8 @@ __global__ void __launch_bounds__(ROW_THREADS) kvq_read_kernel(const ReadArgs<T>
   // K and V of neighbouring rows go to the warps of a CTA: V's rows share their memory sectors
   for (int u = blockIdx.x * (ROW_THREADS / 32) + (threadIdx.x >> 5); u < units; u += gridDim.x * (ROW_THREADS / 32)) {
     const int kv = u & 1, t = u >> 1;
-    const int s = kvq_find_request(a.offsets, a.S, t, lane);
-    const KvqRequest q = kvq_request(a.offsets, a.slot, a.pos, s);
+    const int s = kvq_find_request<true>(a.offsets, a.S, t, lane);
+    const KvqRequest q = kvq_request<true>(a.offsets, a.slot, a.pos, s);
     T* dst = (kv ? a.dst[1] : a.dst[0]) + (int64_t)t * a.heads * D + w * 8;
     bool held = t >= q.b && t < q.e;
     if (held && !q.ok(a.total, a.slots, a.capacity)) {
@@ -235,14 +235,14 @@ __global__ void __launch_bounds__(ROW_THREADS) kvq_read_groups_kernel(const Read
     const int h = u % (int)a.heads, c = u / (int)a.heads;
     const int t_end = (int)min(a.total, (int64_t)8 * c + 8);
     for (int t = 8 * c; t < t_end;) {
-      const int s = kvq_find_request(a.offsets, a.S, t, lane);
-      const KvqRequest q = kvq_request(a.offsets, a.slot, a.pos, s);
+      const int s = kvq_find_request<true>(a.offsets, a.S, t, lane);
+      const KvqRequest q = kvq_request<true>(a.offsets, a.slot, a.pos, s);
       bool held = t >= q.b && t < q.e;
       // rows up to the request's end, or (outside of one) up to the next one's beginning
       int stop = t_end;
       if (held) stop = (int)min((int64_t)stop, q.e);
       else if (t < q.b) stop = (int)min((int64_t)stop, q.b);
-      else if (s + 1 < a.S) stop = (int)min((int64_t)stop, max((int64_t)__ldg(a.offsets + s + 1), (int64_t)t + 1));
+      else if (s + 1 < a.S) stop = (int)min((int64_t)stop, max((int64_t)kvq_ld<true>(a.offsets + s + 1), (int64_t)t + 1));
       if (held && !q.ok(a.total, a.slots, a.capacity)) {
         if (lane == 0) atomicOr(a.status, STATUS_KV_RANGE);
         held = false;

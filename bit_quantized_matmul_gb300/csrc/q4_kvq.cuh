@@ -66,15 +66,38 @@ __device__ __forceinline__ int kvq_scale(int kv, int r, int b) {
   return (kv ? Kvq<D>::VS_OFF : Kvq<D>::KS_OFF) + (((r >> 1) * Kvq<D>::NB + b) * 2 + (r & 1)) * 2;
 }
 
+// Loads of what a call is given.  EARLY: the kernel is launched early, so an earlier
+// launch may be writing the address while the kernel lives.  It waits before it reads, and
+// the wait makes those writes visible to ordinary loads, but not to the read-only path:
+// so the step's description, which every warp reads again, comes by a load that
+// the compiler cannot turn into one of those (from the L2 each time, eight positions
+// a warp read for 32 requests would take 25 us longer), rows that are read once from the L2.
+template <bool EARLY>
+__device__ __forceinline__ int32_t kvq_ld(const int32_t* p) {
+  if constexpr (EARLY) {
+    int32_t v;
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+  } else {
+    return __ldg(p);
+  }
+}
+template <bool EARLY, typename V>
+__device__ __forceinline__ V kvq_ld_row(const V* p) {
+  if constexpr (EARLY) return __ldcg(p);
+  else return __ldg(p);
+}
+
 // The request whose packed rows contain row t, found by a whole warp: the last s
 // with offsets[s] <= t (offsets are expected to be non-decreasing; callers check
 // the result).  32 offsets a round: a search by halves would wait for memory
 // log2(S) times.
-__device__ __forceinline__ int kvq_find_request(const int32_t* __restrict__ offsets, int S, int64_t t, int lane) {
+template <bool EARLY>
+__device__ __forceinline__ int kvq_find_request(const int32_t* offsets, int S, int64_t t, int lane) {
   int lo = 0, n = S;  // the answer lies in [lo, lo + n)
   while (n > 1) {
     const int step = (n + 31) / 32, at = lo + lane * step;
-    const bool below = lane * step < n && (int64_t)__ldg(offsets + at) <= t;
+    const bool below = lane * step < n && (int64_t)kvq_ld<EARLY>(offsets + at) <= t;
     const unsigned hit = __ballot_sync(0xFFFFFFFFu, below) | 1u;
     const int k = 31 - __clz(hit);
     lo += k * step;
@@ -92,10 +115,10 @@ struct KvqRequest {
   }
 };
 
-__device__ __forceinline__ KvqRequest kvq_request(const int32_t* __restrict__ offsets,
-                                                  const int32_t* __restrict__ slot,
-                                                  const int32_t* __restrict__ pos, int s) {
-  return {__ldg(offsets + s), __ldg(offsets + s + 1), __ldg(slot + s), __ldg(pos + s)};
+template <bool EARLY>
+__device__ __forceinline__ KvqRequest kvq_request(const int32_t* offsets, const int32_t* slot, const int32_t* pos,
+                                                  int s) {
+  return {kvq_ld<EARLY>(offsets + s), kvq_ld<EARLY>(offsets + s + 1), kvq_ld<EARLY>(slot + s), kvq_ld<EARLY>(pos + s)};
 }
 
 // The operand registers of a word of codes: exact binary16 pairs q - 8 of
@@ -114,13 +137,16 @@ __device__ __forceinline__ void kvq_unpack_centred(uint32_t w, uint32_t (&r)[4])
 }
 
 // Eight consecutive elements as fp32 (16-byte aligned).
+template <bool EARLY>
 __device__ __forceinline__ void kvq_load8(const float* p, float (&v)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  const float4 a = kvq_ld_row<EARLY>(reinterpret_cast<const float4*>(p));
+  const float4 b = kvq_ld_row<EARLY>(reinterpret_cast<const float4*>(p) + 1);
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
+template <bool EARLY>
 __device__ __forceinline__ void kvq_load8(const __half* p, float (&v)[8]) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint4 a = kvq_ld_row<EARLY>(reinterpret_cast<const uint4*>(p));
   const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -129,8 +155,9 @@ __device__ __forceinline__ void kvq_load8(const __half* p, float (&v)[8]) {
     v[2 * i + 1] = f.y;
   }
 }
+template <bool EARLY>
 __device__ __forceinline__ void kvq_load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint4 a = kvq_ld_row<EARLY>(reinterpret_cast<const uint4*>(p));
   const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {

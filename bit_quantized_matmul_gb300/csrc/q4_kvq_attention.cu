@@ -46,9 +46,9 @@
 // that lets others begin before its own wait is done would let them begin while a kernel
 // two places back still runs, and their waits are for the launch before them only: so the
 // first launch lets the join begin after its wait, and what the join and the weights'
-// launch read before theirs is older than the call.  What an
-// earlier launch wrote is loaded past the L1, which may hold an older line.  The wait
-// in the first launch is worth 2 us of every call that follows another (64 ragged
+// launch read before theirs is older than the call.  Nothing comes by the read-only
+// path, which is for memory that no kernel writes meanwhile.  The early beginning
+// of the first launch is worth 2 us of every call that follows another (64 ragged
 // requests called in turn 38.8 us without, 36.8 with).
 //
 // Measured (28/4 heads of 128; both launches in a graph, inputs past the L2): 64
@@ -152,7 +152,7 @@ struct Request {
 
 template <typename T>
 __device__ __forceinline__ Request load_request(const Args<T>& a, int s, bool by_rows, bool* bad = nullptr) {
-  const KvqRequest q = kvq_request(a.offsets, a.slot, a.pos, s);
+  const KvqRequest q = kvq_request<true>(a.offsets, a.slot, a.pos, s);
   Request r{(int)q.b, (int)q.pos, (int)q.slot, 0, 0, 0};
   if (!q.ok(a.total, a.slots, a.capacity)) {
     if (bad) *bad = q.e > q.b;
@@ -327,7 +327,7 @@ __device__ __forceinline__ void load_query(Query<D>& f, uint4* frag, const Args<
     const T* p = a.q + (int64_t)(r.b + j) * a.q_token + (int64_t)(head * a.group + hg) * a.q_head + 8 * tq;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      kvq_load8(p + 32 * b, x[b]);
+      kvq_load8<true>(p + 32 * b, x[b]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         x[b][i] *= a.scale_log2;
@@ -709,7 +709,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kvq_join_kernel(const Args<T>
   const int at = PER_ROW == 1 ? blockIdx.x * JOIN_WARPS + (threadIdx.x >> 5) : blockIdx.x;
   const int t = at / q_heads, hq = at - t * q_heads;
   asm volatile("griddepcontrol.launch_dependents;");
-  const int s = kvq_find_request(a.offsets, a.S, t, lane);
+  const int s = kvq_find_request<true>(a.offsets, a.S, t, lane);
   const Request r = load_request(a, s, true);
   T* out = a.out + (int64_t)at * D;
   if (r.tiles == 0 || t < r.b || t >= r.b + r.n) {

@@ -216,13 +216,13 @@ __global__ void __cluster_dims__(MOVE_CLUSTER, 1, 1) __launch_bounds__(MOVE_THRE
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the select launch has ended
   asm volatile("griddepcontrol.launch_dependents;");  // not before: a later launch waits for this one only
   const int s = blockIdx.y / (int)a.heads, h = blockIdx.y % (int)a.heads;
-  const int n_out = a.new_len[s];
+  const int n_out = kvq_ld<true>(a.new_len + s);
   if (n_out <= 0) return;
   const unsigned n = n_out;
-  const int64_t src_slot = a.src[s], dst_slot = a.dst[s];
+  const int64_t src_slot = kvq_ld<true>(a.src + s), dst_slot = kvq_ld<true>(a.dst + s);
   const bool in_place = src_slot == dst_slot;
   // (whole clusters leave)
-  if (in_place && (blockIdx.x >= MOVE_CLUSTER || n_out == a.len[s])) return;
+  if (in_place && (blockIdx.x >= MOVE_CLUSTER || n_out == kvq_ld<true>(a.len + s))) return;
   uint8_t* src = a.cache + (src_slot * a.heads + h) * plane_bytes;
   uint8_t* dst = a.cache + (dst_slot * a.heads + h) * plane_bytes;
   const int32_t* kept = a.kept + (int64_t)blockIdx.y * a.keep;
@@ -235,8 +235,8 @@ __global__ void __cluster_dims__(MOVE_CLUSTER, 1, 1) __launch_bounds__(MOVE_THRE
     typename R::Vec v0, v1;
     unsigned p0, p1;
     if (it < items) {
-      p0 = kept[2 * pair];
-      p1 = 2 * pair + 1 < n ? kept[2 * pair + 1] : p0;  // a last odd row: its neighbour is never used
+      p0 = kvq_ld<true>(kept + 2 * pair);
+      p1 = 2 * pair + 1 < n ? kvq_ld<true>(kept + 2 * pair + 1) : p0;  // a last odd row: its neighbour is never used
       v0 = *reinterpret_cast<const typename R::Vec*>(src + R::at(p0, e));
       v1 = *reinterpret_cast<const typename R::Vec*>(src + R::at(p1, e));
     }

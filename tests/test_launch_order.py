@@ -59,3 +59,30 @@ def test_the_join_and_the_weights_wait_on_every_path():
     # the joined rows return from inside a branch that has a wait of its own
     assert KERNELS["kvq_join_kernel"].count(WAIT) == 2
     assert KERNELS["kvq_mass_kernel"].count(WAIT) == 2
+
+
+# The read-only path (__ldg, and what the compiler may make of a plain load) is for memory that
+# nobody writes while the kernel lives; a launch that begins early lives beside its predecessors.
+EARLY = ["kvq_read_kernel", "kvq_read_groups_kernel", "kvq_attention_kernel", "kvq_join_kernel", "kvq_mass_kernel",
+         "evict_move_kernel"]
+
+
+def source(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+def test_launches_that_begin_early_read_past_the_read_only_path():
+    for name in EARLY:
+        assert "__ldg" not in KERNELS[name], name
+        assert "kvq_find_request(" not in KERNELS[name] and "kvq_request(" not in KERNELS[name], name
+    assert "__ldg" not in source("q4_kvq_attention.cu")
+    # the shared helpers take the kind of load as an argument, and these kernels ask for an ordinary one
+    helpers = source("q4_kvq_attention.cu") + "".join(KERNELS[n] for n in EARLY)
+    asked = re.findall(r"kvq_(?:find_request|request|load8)<(\w+)>", helpers)
+    assert asked and set(asked) == {"true"}
+    assert not re.search(r"kvq_(find_request|request|load8)\(", helpers)
+
+
+def test_the_move_reads_what_the_select_wrote_by_loads_that_stay_ordinary():
+    assert not re.search(r"= a\.(new_len|src|dst|len|kept)\[|\bkept\[|== a\.len\[", KERNELS["evict_move_kernel"])
