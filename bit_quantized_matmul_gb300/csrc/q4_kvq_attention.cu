@@ -28,9 +28,12 @@
 // instruction a register, none for the offset).  V's scales are folded into the
 // weights of their block, x = w d: with w = wh + wl split once for all blocks,
 // hi = wh d rounded, and lo = (wh d - hi) + wl d, whose first part a fused
-// multiply-add gives exactly: three instructions for two weights.  Weights are
-// scaled by a power of two (2^9, less where V's scales pass 1), so that they and
-// x fit binary16 and lo keeps its bits.  Values lie along m and virtual rows
+// multiply-add gives exactly: three instructions for two weights.  Weights and
+// V's scales are taken times powers of two (the weights 2^9, the scales so that the largest
+// so far is about 1), so that they and x fit binary16 and lo keeps its bits; a scale's costs one
+// more instruction for two (no time: 36.5 us either way for 64 ragged requests).
+// Lo ends at 2^-24 all the same: next to a key of weight 1 the others are held to 2^-29 of V's
+// largest scale each, so of a weight 2^-b about 33 - b bits count.  Values lie along m and virtual rows
 // along n, and hi and lo go into one accumulator.  Rows of 16 bits get the lo terms
 // too: without them sums that nearly cancel keep errors of 2^-12 of their terms,
 // more than their own rounding (8 bf16 requests at 32k would take 38.1 us instead of
@@ -434,18 +437,22 @@ __device__ __forceinline__ void scores(const uint8_t* tile, const Query<D>& q, i
 }
 
 // ---------------------------------------------------------------- sums
-constexpr uint32_t ONE_BITS = 0x3C00u;  // 1 in binary16
+constexpr uint32_t HALF_ONE = 0x3C00u;   // 1 in binary16
+constexpr uint32_t HALF_TOP = 0x7800u;   // 2^15
+constexpr uint32_t HALF_LOW = 0x0400u;   // 2^-14, its smallest normal number
 
 // A warp's running sums over the positions it has taken.  Weights are
-// 2^(score - m + up), where m is at most SLACK below the largest score and up is
-// 9, or such that weight times V scale is at most 2^14 (2^15 for scales above 2^15).
+// w = 2^(score - m + up), where m is at most SLACK below the largest score, and meet V's
+// scales times a power of two: with T the largest scale so far as a power of two,
+// kept within 2^-14 .. 2^15, up is 9 and the scales are taken by 1 / T where T <= 1,
+// else up is 9 - log2 T and they are taken as they are.  A weight times a scale is then
+// at most 2^14 (2^15 for scales above 2^15), and o holds 2^9 / T times its sum either way.
 template <int D>
 struct Sums {
   float o[Kvq<D>::NB][2][4];  // [block][values 4g + 2i, + 1][rows 2 tq, 2 tq + 1, twice]
   F2 l;                       // row g
   float m, off;               // row g: the reference score, and m - up (0 while m is -inf)
-  uint32_t dtop;              // the largest V scale so far, as a power of two from 1 on, in both halves
-  int up;
+  uint32_t dtop;              // T in both halves
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int b = 0; b < Kvq<D>::NB; ++b)
@@ -456,8 +463,13 @@ struct Sums {
     l = f2(0.0f, 0.0f);
     m = NEG_INF;
     off = 0.0f;
-    dtop = ONE_BITS << 16 | ONE_BITS;
-    up = 9;
+    dtop = HALF_LOW << 16 | HALF_LOW;
+  }
+  __device__ __forceinline__ int top_exponent() const { return (int)(dtop >> 26) - 15; }  // log2 T
+  __device__ __forceinline__ int up() const { return 9 - max(top_exponent(), 0); }
+  // what the scales are multiplied with, in both halves: 1 / T, at least 1
+  __device__ __forceinline__ __half2 lift() const {
+    return __hmax2(half2_of((HALF_TOP << 16 | HALF_TOP) - dtop), half2_of(HALF_ONE << 16 | HALF_ONE));
   }
 };
 
@@ -503,15 +515,17 @@ __device__ __forceinline__ void take_tile(const uint8_t* tile, int p0, const Que
     uint32_t h = max(dmw & 0xFFFFu, dmw >> 16);  // magnitudes order as integers
     h = max(h, __shfl_xor_sync(0xFFFFFFFFu, h, 1));
     h = max(h, __shfl_xor_sync(0xFFFFFFFFu, h, 2));
-    h = min((h + 0x3FFu) & 0x7C00u, 0x7800u);  // up to a power of two, 1 .. 2^15
+    h = max(min((h + 0x3FFu) & 0x7C00u, HALF_TOP), HALF_LOW);  // up to a power of two
+    const int up = a.up(), top_e = a.top_exponent();
     a.dtop = h | h << 16;
-    a.up = 9 + 15 - (int)(h >> 10);
-    const float no = mn == NEG_INF ? 0.0f : mn - (float)a.up;
+    const float no = mn == NEG_INF ? 0.0f : mn - (float)a.up();
     const float f = a.m == NEG_INF ? 1.0f : ex2(a.off - no);  // nothing summed yet while m is -inf
     a.m = mn;
     a.off = no;
     a.l = mul2(a.l, f2(f, f));
-    const float f0 = __shfl_sync(0xFFFFFFFFu, f, 8 * tq), f1 = __shfl_sync(0xFFFFFFFFu, f, 8 * tq + 4);
+    // o's own factor has the change of the scales' lift
+    const float fo = f * pow2((top_e + up) - (a.top_exponent() + a.up()));
+    const float f0 = __shfl_sync(0xFFFFFFFFu, fo, 8 * tq), f1 = __shfl_sync(0xFFFFFFFFu, fo, 8 * tq + 4);
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -522,6 +536,7 @@ __device__ __forceinline__ void take_tile(const uint8_t* tile, int p0, const Que
         a.o[b][i][3] *= f1;
       }
   }
+  const __half2 lift = a.lift();
 #pragma unroll
   for (int k = 0; k < N / 2; ++k) {  // sixteen keys a product: eight positions 2k, eight positions 2k + 1
     __half2 wh[2], wl[2];
@@ -544,7 +559,7 @@ __device__ __forceinline__ void take_tile(const uint8_t* tile, int p0, const Que
       uint32_t hi[2], lo[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const __half2 d = half2_of(vd[u][b]);
+        const __half2 d = __hmul2(half2_of(vd[u][b]), lift);  // exact
         const __half2 h = __hmul2(wh[u], d);
         hi[u] = bits(h);
         lo[u] = bits(__hfma2(wl[u], d, __hfma2(wh[u], d, __hneg2(h))));
@@ -660,12 +675,12 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kvq_attention_kernel(con
     float l = lp.x + lp.y;
     l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
     l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
-    const float down = pow2(-sums.up);
+    const float down = pow2(-sums.up()), down_o = pow2(sums.top_exponent() - 9);
     const bool whole = out.t0 == 0 && out.t1 == r.tiles;
     const int rows = r.n * a.group;
     // the row of this lane's l is g, those of its values 2 tq and 2 tq + 1
     const int64_t slot = ((int64_t)2 * worker + (out.t0 == 0 ? 1 : 0)) * ROWS;
-    const float f = whole ? 1.0f / l : down;
+    const float f = whole ? pow2(sums.top_exponent() + sums.up() - 9) / l : down_o;
     if (whole) {
       if (a.lse && tq == 0 && row0 + g < rows) {
         const int j = (row0 + g) / a.group;

@@ -386,7 +386,9 @@ Q4_API int q4_kvq_read(const void* cache, void* k_out, void* v_out, int dtype, i
  *         request and head).  Positions pos[s] .. of this step start from 0, so
  *         only a prompt's positions have to be set before.  Each slot in at
  *         most one request of the call.
- * Products carry fp32 accuracy for fp32 queries; sums are held in fp32.  The
+ * Products carry fp32 accuracy for fp32 queries; sums are held in fp32.  What a
+ * key adds is held to 2^-29 of the largest scale among its head's V blocks (of 2^-14 at
+ * least), however small its weight next to the row's largest.  The
  * lengths are read on the device only: a launch of a fixed number of CTAs
  * divides them evenly.  The same call gives the same bits; where a request is
  * divided, and with it the last bits of its rows, depends on the lengths of the

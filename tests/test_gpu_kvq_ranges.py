@@ -1,0 +1,123 @@
+"""Attention over the 4-bit cache where V or the weights span many binades, against float64.
+
+Bound.  As in test_gpu_kvq.py, with one term more: a weight times V's scale is
+held in two binary16 terms, whose last place is 2^-24 however small they are.
+Relative to a weight of 1 (the row's largest is no less) the weight is taken by 2^9 and the
+scale by 1 / T, T the largest scale of the request's head so far as a power of two
+(2^-14 at least); three roundings of half a place, codes of 8 at most:
+
+    8 * 3 * 2^-25 * 2^-9 * T <= 2^-29 T  per key,
+
+with T <= 2 max |scale|.  So, per value,
+
+    |o - o64| <= (4 max ds + 2^-18 + (n / 16 + 64) 2^-22) * sum_p w_p 16 |s_v| + n 2^-29 T + u |o64|."""
+import numpy as np
+import pytest
+import torch
+
+import synthetic
+from oracle import attention as ref
+
+pytestmark = pytest.mark.gpu
+
+UNIT = {torch.float32: 2.0 ** -24, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
+
+
+@pytest.fixture(scope="module")
+def q4():
+    import __graft_entry__
+
+    __graft_entry__.build()
+    import bit_quantized_matmul_gb300 as q4
+
+    return q4
+
+
+def _i32(*v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def _check(o, q, k, v, dtype, what):
+    """One row o, q [hq, d] over all of k, v [n, heads, d]; every value."""
+    n, heads, d = k.shape
+    hq = q.shape[0]
+    ck, sk = ref.encode(k)
+    cv, sv = ref.encode(v)
+    k64, v64 = ref.decode(ck, sk), ref.decode(cv, sv)
+    wide_k = 16 * np.repeat(np.abs(sk.astype(np.float64)), 32, -1)
+    wide_v = 16 * np.repeat(np.abs(sv.astype(np.float64)), 32, -1)
+    scale, worst = d ** -0.5, 0.0
+    for x in range(hq):
+        h = x // (hq // heads)
+        s = scale * (k64[:, h] @ q[x])
+        w = np.exp(s - s.max())
+        w /= w.sum()
+        want = w @ v64[:, h]
+        ds = 2.0 ** -18 * scale * (wide_k[:, h] @ np.abs(q[x])).max()
+        top = max(2 * np.abs(sv[:, h].astype(np.float64)).max(), 2.0 ** -14)
+        bound = (4 * ds + 2.0 ** -18 + (n / 16 + 64) * 2.0 ** -22) * (w @ wide_v[:, h])
+        bound = bound + n * 2.0 ** -29 * top + UNIT[dtype] * np.abs(want) + 2.0 ** -25 * (dtype == torch.float16)
+        err = np.abs(o[x] - want)
+        assert np.all(err <= bound), "%s, head %d: %.3g of the bound" % (what, x, (err / bound).max())
+        worst = max(worst, float((err / bound).max()))
+    return worst
+
+
+def _attend_all(q4, q, k, v, dtype, what, requests=1):
+    """Requests that all cache the rows k, v [n, heads, d] and ask with q [1, hq, d] on the last of them."""
+    n, heads, d = k.shape
+    cache = q4.Q4KVCache(requests, heads, d, n)
+    q, k, v = (torch.from_numpy(np.ascontiguousarray(x, np.float32)).to(dtype) for x in (q, k, v))
+    slots = _i32(*range(requests))
+    rows = _i32(*[n * i for i in range(requests + 1)])
+    q4.q4_kvq_append(cache, k.cuda().repeat(requests, 1, 1), v.cuda().repeat(requests, 1, 1), rows, slots,
+                     _i32(*[0] * requests))
+    o = q4.q4_kvq_attention(cache, q.cuda().repeat(requests, 1, 1), _i32(*range(requests + 1)), slots,
+                            _i32(*[n - 1] * requests)).cpu().double().numpy()
+    assert q4.q4_device_status() == q4.Q4_OK
+    q, k, v = q.double().numpy()[0], k.float().numpy(), v.float().numpy()
+    return max(_check(o[r], q, k, v, dtype, what) for r in {0, requests - 1})
+
+
+HEADS = [(4, 28, 128), (2, 14, 64)]
+
+
+@pytest.mark.parametrize("sigma", [1e-6, 1e-5, 1e-3, 3000.0])
+@pytest.mark.parametrize("heads,hq,d", HEADS)
+@pytest.mark.parametrize("n", [1, 9, 40, 700])
+def test_small_and_large_values(q4, sigma, heads, hq, d, n):
+    q, k = synthetic.normal(900, (1, hq, d)), synthetic.normal(901, (n, heads, d))
+    _attend_all(q4, q, k, synthetic.normal(902, (n, heads, d), sigma=sigma), torch.float32, "sigma %g" % sigma)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("heads,hq,d", HEADS)
+@pytest.mark.parametrize("bits", [6, 12, 16, 20])
+@pytest.mark.parametrize("n,sigma", [(40, 1.0), (40, 2.0 ** -8), (700, 2.0 ** -8), (5000, 1.0)])
+def test_one_heavy_key_without_a_value(q4, dtype, heads, hq, d, bits, n, sigma):
+    # all that counts lies `bits` binades below the row's largest weight
+    q = np.repeat(synthetic.normal(910, (1, heads, d)), hq // heads, 1) + synthetic.normal(911, (1, hq, d), sigma=0.05)
+    k, v = synthetic.normal(912, (n, heads, d), sigma=0.2), synthetic.normal(913, (n, heads, d), sigma=sigma)
+    at = n // 3
+    k[at] = bits * np.log(2.0) / np.sqrt(d) * q[0].reshape(heads, hq // heads, d)[:, 0]
+    v[at] = 0.0
+    _attend_all(q4, q, k, v, dtype, "%d binades" % bits)
+
+
+@pytest.mark.parametrize("heads,hq,d", HEADS)
+@pytest.mark.parametrize("falling", [False, True])
+def test_values_that_grow_or_shrink_along_the_cache(q4, heads, hq, d, falling):
+    # the scales' power of two changes again and again within one warp's tiles
+    n = 6000
+    q, k, v = (synthetic.normal(920 + i, s) for i, s in enumerate([(1, hq, d), (n, heads, d), (n, heads, d)]))
+    v = v * np.float32(2.0) ** np.linspace(-20, 12, n, dtype=np.float32)[:, None, None]
+    _attend_all(q4, q, k, v[::-1] if falling else v, torch.float32, "growing")
+
+
+@pytest.mark.parametrize("falling", [False, True])
+def test_several_tiles_of_changing_scales_a_warp(q4, falling):
+    # 12,032 tiles: more than the launch has warps, so each takes a run of them
+    heads, hq, d, n = 8, 8, 64, 3000
+    q, k, v = (synthetic.normal(930 + i, s) for i, s in enumerate([(1, hq, d), (n, heads, d), (n, heads, d)]))
+    v = v * np.float32(2.0) ** np.linspace(-18, 6, n, dtype=np.float32)[:, None, None]
+    _attend_all(q4, q, k, v[::-1] if falling else v, torch.float32, "runs", requests=16)
