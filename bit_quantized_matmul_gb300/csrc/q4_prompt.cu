@@ -72,7 +72,15 @@ constexpr int WORKS = 2;                // the pair that is copied and the one b
 constexpr int THREADS = 640;
 constexpr int TMEM_COLS = 512;
 constexpr float NEG_INF = -INFINITY;
-constexpr float RESCALE = 8.0f;         // log2 of the growth that triggers a rescale
+constexpr float GROW = 8.0f;            // log2 of how far a score may pass the reference before the sums are rescaled
+
+// log2 of what the weights, rounded to T for the second product, are taken by.  bfloat16 has
+// exponents enough.  binary16 ends at 2^-24 and the sum does not: lifted to just below its
+// largest numbers, a weight of 2^-b of the reference's keeps all its bits for b <= 21 and is off by
+// 2^-32 at most below that.  Four binades more, with GROW = 4, would cost 5 to 9% where scores
+// are sharp (four times the spread), as sums are rescaled more often; the lift itself costs nothing.
+template <typename T>
+constexpr float LIFT = std::is_same<T, __nv_bfloat16>::value ? 0.0f : 7.0f;
 
 template <int D>
 struct Cfg {
@@ -646,7 +654,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int lim = live ? p.limit(a, w, pos) : -1;
       // keys up to here are seen by every live row of the warp
       const int clear = p.limit(a, w, min(w.pos0 + t * P + first_pos, w.q.qlen - 1));
-      float m = NEG_INF, l = 0.0f;  // in units of log2, scaled
+      float m = NEG_INF, l = 0.0f;  // in units of log2, scaled; m less LIFT
       for (int i = 0; i < blocks; ++i, ++ns) {
         ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(s_full + 8 * t, ns & 1, err, a.wait_ns));
         const int c0 = i * BN + h * HN, seen = lim - c0;  // columns up to `seen` count
@@ -674,10 +682,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           mn = max3(fmaxf(top[0], top[1]), top[2], top[3]) * a.scale_log2;  // positive: checked on the host
         }
-        if (tile_vote(t, i == 0 || mn > m + RESCALE)) {
+        if (tile_vote(t, i == 0 || mn > m + (LIFT<T> + GROW))) {
           s_max[t][h][r] = mn;
           tile_sync(t);
-          const float nm = max3(m, mn, s_max[t][1 - h][r]);
+          const float nm = fmaxf(m, fmaxf(mn, s_max[t][1 - h][r]) - LIFT<T>);
           const float f = m == NEG_INF ? 0.0f : ex2(m - nm);
           m = nm;
           if (i > 0) {

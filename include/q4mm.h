@@ -435,7 +435,8 @@ Q4_API int q4_kvq_evict(void* cache, float* mass, int64_t slots, int64_t heads, 
  *   causal     nonzero: row i of a sequence sees its keys j <= i + klen - qlen
  *              (the rows are the sequence's last); else all of its keys.
  * Rows that see no key, and rows of no sequence, get zeros.  Weights are
- * rounded to dtype before the product with v; sums are held in fp32.  What
+ * rounded to dtype before the product with v (F16: a key's weight below 2^-21 of the row's
+ * largest to 2^-32 of that); sums are held in fp32.  What
  * lies outside a sequence's rows, NaN included, does not reach its results.
  * head_dim 64 or 128, at most 128 query heads per key/value head (SHAPE);
  * addresses and strides multiples of 16 bytes (ALIGN), strides that are taken
