@@ -82,6 +82,14 @@ constexpr float GROW = 8.0f;            // log2 of how far a score may pass the 
 template <typename T>
 constexpr float LIFT = std::is_same<T, __nv_bfloat16>::value ? 0.0f : 7.0f;
 
+// References of this size (in units of log2) and above have steps that a weight would show:
+// a score's product with the scale less its own rounding is not 0 (past 2^24 it may be 2 to
+// any power).  Such a row is "far": its reference is a score, which is taken off the others, in
+// tensor memory, before the product.  All of a far row's blocks call for another
+// reference, so that this is done where sums are rescaled and costs the others nothing; a
+// subtraction or a choice in the weights' own loop would cost every block 2 to 3%.
+constexpr float FAR = 0x1p12f;
+
 template <int D>
 struct Cfg {
   static constexpr int CHUNKS = D / 64;                 // 128-byte column chunks of a row
@@ -654,7 +662,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int lim = live ? p.limit(a, w, pos) : -1;
       // keys up to here are seen by every live row of the warp
       const int clear = p.limit(a, w, min(w.pos0 + t * P + first_pos, w.q.qlen - 1));
-      float m = NEG_INF, l = 0.0f;  // in units of log2, scaled; m less LIFT
+      // The reference, in units of log2, scaled and less LIFT (-LIFT in far rows, 0 before the first score); the
+      // scaled score that calls for another (-inf: any does); a far row's reference.
+      float m = 0.0f, most = NEG_INF, l = 0.0f, far_ref = NEG_INF;
       for (int i = 0; i < blocks; ++i, ++ns) {
         ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(s_full + 8 * t, ns & 1, err, a.wait_ns));
         const int c0 = i * BN + h * HN, seen = lim - c0;  // columns up to `seen` count
@@ -680,14 +690,28 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int e = 0; e < 32; e += 2)
               top[(e >> 1) & 3] = max3(top[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
           }
-          mn = max3(fmaxf(top[0], top[1]), top[2], top[3]) * a.scale_log2;  // positive: checked on the host
+          mn = live ? max3(fmaxf(top[0], top[1]), top[2], top[3]) : NEG_INF;  // Q's rows past the tile hold anything
         }
-        if (tile_vote(t, i == 0 || mn > m + (LIFT<T> + GROW))) {
+        if (tile_vote(t, i == 0 || mn * a.scale_log2 > most)) {  // a positive scale: checked on the host
           s_max[t][h][r] = mn;
           tile_sync(t);
-          const float nm = fmaxf(m, fmaxf(mn, s_max[t][1 - h][r]) - LIFT<T>);
-          const float f = m == NEG_INF ? 0.0f : ex2(m - nm);
-          m = nm;
+          const float score = fmaxf(mn, s_max[t][1 - h][r]), top = score * a.scale_log2;
+          const bool was_far = far_ref != NEG_INF, none = most == NEG_INF && !was_far;
+          const bool far =
+              was_far || (fabsf(top) >= FAR && score != NEG_INF && (none || top - LIFT<T> > m));
+          float f;
+          if (far) {
+            const float ref = fmaxf(far_ref, score);
+            f = was_far ? ex2((far_ref - ref) * a.scale_log2) : none ? 0.0f : ex2(m + LIFT<T> - top);
+            far_ref = ref;
+            m = -LIFT<T>;
+            most = NEG_INF;
+          } else {
+            const float nm = none ? top - LIFT<T> : fmaxf(m, top - LIFT<T>);
+            f = none ? 0.0f : ex2(m - nm);
+            m = nm == NEG_INF ? 0.0f : nm;
+            most = nm + (LIFT<T> + GROW);
+          }
           if (i > 0) {
             l *= f;
             if (ok) {
@@ -705,10 +729,22 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             tile_sync(t);  // a half's weights go to all of O: both halves of it are rescaled before
           }
+          if (__any_sync(0xFFFFFFFFu, far) && ok) {
+            const float off = far ? far_ref : 0.0f;
+#pragma unroll 1
+            for (int c = 0; c < HN; c += 16) {
+              uint32_t s[16];
+              tmem_ld16(s_addr + c, s);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) - off);
+              tmem_st16(s_addr + c, s);
+            }
+            tmem_wait_st();
+          }
         }
         if (ok) {
-          const float mm = m == NEG_INF ? 0.0f : m;
-          const F2 sc2 = f2(a.scale_log2, a.scale_log2), mm2 = f2(-mm, -mm);
+          const F2 sc2 = f2(a.scale_log2, a.scale_log2), mm2 = f2(-m, -m);
           F2 sum[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};
 #pragma unroll
           for (int c = 0; c < HN; c += 32) {
