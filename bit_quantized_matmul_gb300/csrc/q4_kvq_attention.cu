@@ -83,6 +83,9 @@ constexpr int MASS_CTAS_PER_SM = 4;
 constexpr int ITEM_UNITS = 2;         // what beginning an item costs, in tiles: its queries, its sums' end
 constexpr float NEG_INF = -INFINITY;
 constexpr float SLACK = 5.0f;         // log2 of how far a weight may pass 1 before the sums are rescaled
+// References of this size (in units of log2) and above have steps that a power of two added to them
+// would be lost in: their rows' weights are taken as they are, and the reference has no slack.
+constexpr float FAR = 0x1p16f;
 
 template <typename T>
 struct Args {
@@ -101,7 +104,7 @@ struct Args {
   float2* partial_ml;       // [2 * workers][ROWS] (reference score, sum)
   int64_t* unit_start;      // [S + 1]
   int workers;              // warps of the main launch
-  float* lse;               // [total, q_heads] log2 of the sum of exponentials, or null
+  float2* lse;              // [total, q_heads] a row's reference and the log2 of its sum of exponentials, or null
   float* mass;              // [slots, heads, capacity], or null
 };
 
@@ -451,7 +454,8 @@ template <int D>
 struct Sums {
   float o[Kvq<D>::NB][2][4];  // [block][values 4g + 2i, + 1][rows 2 tq, 2 tq + 1, twice]
   F2 l;                       // row g
-  float m, off;               // row g: the reference score, and m - up (0 while m is -inf)
+  float m, off;               // row g: the reference score, and m - up (m in far rows, 0 while m is -inf)
+  float most;                 // row g: the score that calls for another reference
   uint32_t dtop;              // T in both halves
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -461,12 +465,15 @@ struct Sums {
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[b][i][k] = 0.0f;
     l = f2(0.0f, 0.0f);
-    m = NEG_INF;
+    m = most = NEG_INF;
     off = 0.0f;
     dtop = HALF_LOW << 16 | HALF_LOW;
   }
   __device__ __forceinline__ int top_exponent() const { return (int)(dtop >> 26) - 15; }  // log2 T
   __device__ __forceinline__ int up() const { return 9 - max(top_exponent(), 0); }
+  // row g's own
+  __device__ __forceinline__ bool far() const { return fabsf(m) >= FAR; }
+  __device__ __forceinline__ int row_up() const { return far() ? 0 : up(); }
   // what the scales are multiplied with, in both halves: 1 / T, at least 1
   __device__ __forceinline__ __half2 lift() const {
     return __hmax2(half2_of((HALF_TOP << 16 | HALF_TOP) - dtop), half2_of(HALF_ONE << 16 | HALF_ONE));
@@ -509,7 +516,7 @@ __device__ __forceinline__ void take_tile(const uint8_t* tile, int p0, const Que
     for (int b = 0; b < NB; ++b) dm = __hmax2(dm, __habs2(*reinterpret_cast<const __half2*>(&vd[b])));
   }
   const uint32_t dmw = *reinterpret_cast<const uint32_t*>(&dm);
-  if (__any_sync(0xFFFFFFFFu, top > a.m + SLACK || dmw != a.dtop)) {
+  if (__any_sync(0xFFFFFFFFu, top > a.most || dmw != a.dtop)) {
     float mn = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
     mn = fmaxf(a.m, fmaxf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, 2)));
     uint32_t h = max(dmw & 0xFFFFu, dmw >> 16);  // magnitudes order as integers
@@ -518,10 +525,12 @@ __device__ __forceinline__ void take_tile(const uint8_t* tile, int p0, const Que
     h = max(min((h + 0x3FFu) & 0x7C00u, HALF_TOP), HALF_LOW);  // up to a power of two
     const int up = a.up(), top_e = a.top_exponent();
     a.dtop = h | h << 16;
-    const float no = mn == NEG_INF ? 0.0f : mn - (float)a.up();
-    const float f = a.m == NEG_INF ? 1.0f : ex2(a.off - no);  // nothing summed yet while m is -inf
+    const bool none = a.m == NEG_INF;
     a.m = mn;
+    const float no = mn == NEG_INF ? 0.0f : a.far() ? mn : mn - (float)a.up();
+    const float f = none ? 1.0f : ex2(a.off - no);  // nothing summed yet while m is -inf
     a.off = no;
+    a.most = a.far() ? mn : mn + SLACK;
     a.l = mul2(a.l, f2(f, f));
     // o's own factor has the change of the scales' lift
     const float fo = f * pow2((top_e + up) - (a.top_exponent() + a.up()));
@@ -675,16 +684,18 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) kvq_attention_kernel(con
     float l = lp.x + lp.y;
     l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
     l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
-    const float down = pow2(-sums.up()), down_o = pow2(sums.top_exponent() - 9);
+    const float down = pow2(-sums.row_up());                             // l's factor, and that of the scales in o
+    const float down_scales = pow2(sums.top_exponent() + sums.up() - 9);
     const bool whole = out.t0 == 0 && out.t1 == r.tiles;
     const int rows = r.n * a.group;
     // the row of this lane's l is g, those of its values 2 tq and 2 tq + 1
     const int64_t slot = ((int64_t)2 * worker + (out.t0 == 0 ? 1 : 0)) * ROWS;
-    const float f = whole ? pow2(sums.top_exponent() + sums.up() - 9) / l : down_o;
+    const float f = whole ? down_scales / l : down * down_scales;
     if (whole) {
       if (a.lse && tq == 0 && row0 + g < rows) {
         const int j = (row0 + g) / a.group;
-        a.lse[(int64_t)(r.b + j) * (a.heads * a.group) + head * a.group + row0 + g - j * a.group] = sums.off + log2f(l);
+        a.lse[(int64_t)(r.b + j) * (a.heads * a.group) + head * a.group + row0 + g - j * a.group] =
+            make_float2(sums.off, log2f(l));
       }
     } else if (tq == 0) {
       a.partial_ml[slot + g] = make_float2(sums.m, l * down);
@@ -731,7 +742,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kvq_join_kernel(const Args<T>
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (t < a.total) {
       for (int d = tid; d < D; d += 32 * PER_ROW) out[d] = (T)0.0f;
-      if (a.lse && tid == 0) a.lse[at] = NEG_INF;
+      if (a.lse && tid == 0) a.lse[at] = make_float2(NEG_INF, 0.0f);
     }
     return;
   }
@@ -783,7 +794,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kvq_join_kernel(const Args<T>
     const float inv = 1.0f / sum;
 #pragma unroll
     for (int i = 0; i < PER; ++i) out[lane * PER + i] = (T)(acc[i] * inv);
-    if (a.lse && lane == 0) a.lse[at] = top + log2f(sum);
+    if (a.lse && lane == 0) a.lse[at] = make_float2(top, log2f(sum));
     return;
   }
   if (lane == 0) s_ml[warp] = make_float2(top, sum);
@@ -803,12 +814,12 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kvq_join_kernel(const Args<T>
     x = fmaf(s_acc[w][tid], f, x);
   }
   out[tid] = (T)(x / sum);
-  if (a.lse && tid == 0) a.lse[at] = top + log2f(sum);
+  if (a.lse && tid == 0) a.lse[at] = make_float2(top, log2f(sum));
 }
 
 // ---------------------------------------------------------------- weights
 // mass[slot, head, p] += sum over the request's rows and the group's heads of
-// exp2(s - lse); a position that this step appended starts from 0.  Reads the
+// exp2(s - m - log2 l), m a row's reference and l its sum; a position that this step appended starts from 0.  Reads the
 // K half of the cache again: keeping the scores instead would write and read
 // as many bytes for a group of seven heads.  The eight rows' weights of a tile
 // are summed over lanes and dealt out in seven shuffles, a position to each
@@ -863,8 +874,8 @@ __global__ void __launch_bounds__(THREADS) kvq_mass_kernel(const Args<T> a) {
       const int vr = row0 + g;
       const bool live = vr < rows;
       const int j = live ? vr / a.group : 0;
-      const float lse =
-          live ? __ldcg(a.lse + (int64_t)(r.b + j) * (a.heads * a.group) + head * a.group + vr - j * a.group) : 0.0f;
+      const int64_t row = (int64_t)(r.b + j) * (a.heads * a.group) + head * a.group + vr - j * a.group;
+      const float2 lse = live ? __ldcg(a.lse + row) : make_float2(0.0f, 0.0f);
       const int last = live ? r.pos + j : -1;
       for (int t = it.t0; t < it.t1; ++t) {
         const int pm = t * L::POS + mine;
@@ -885,7 +896,7 @@ __global__ void __launch_bounds__(THREADS) kvq_mass_kernel(const Args<T> a) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int p = t * L::POS + 8 * (e >> 1) + 2 * tq + (e & 1);
-          w[e] = p <= last ? ex2(sc[e >> 1][e & 1] - lse) : 0.0f;
+          w[e] = p <= last ? ex2(sc[e >> 1][e & 1] - lse.x - lse.y) : 0.0f;
         }
         // bits 2, 1, 0 of a value's index go to bits 2, 1, 0 of the lane's g
 #pragma unroll
@@ -1000,12 +1011,12 @@ size_t kvq_attn_scratch_bytes(int64_t S, int64_t total, int q_heads, bool mass, 
   };
   const size_t segs = (size_t)2 * num_sms * CTAS_PER_SM * WARPS * ROWS;
   const size_t p = take(segs * 128 * sizeof(float)), ml = take(segs * sizeof(float2));
-  const size_t us = take((size_t)(S + 1) * sizeof(int64_t)), ls = take(mass ? (size_t)total * q_heads * 4 : 0);
+  const size_t us = take((size_t)(S + 1) * sizeof(int64_t)), ls = take(mass ? (size_t)total * q_heads * sizeof(float2) : 0);
   if (out) {
     out->partial = reinterpret_cast<float*>(base + p);
     out->partial_ml = reinterpret_cast<float2*>(base + ml);
     out->unit_start = reinterpret_cast<int64_t*>(base + us);
-    out->lse = reinterpret_cast<float*>(base + ls);
+    out->lse = reinterpret_cast<float2*>(base + ls);
   }
   return at;
 }

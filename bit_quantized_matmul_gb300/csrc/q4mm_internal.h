@@ -182,7 +182,7 @@ struct KvqAttnScratch {
   float* partial;
   float2* partial_ml;
   int64_t* unit_start;
-  float* lse;
+  float2* lse;
 };
 // Bytes of the attention scratch of a call; with `out`, its parts at `base`.
 size_t kvq_attn_scratch_bytes(int64_t S, int64_t total, int q_heads, bool mass, int num_sms, KvqAttnScratch* out,

@@ -121,3 +121,33 @@ def test_several_tiles_of_changing_scales_a_warp(q4, falling):
     q, k, v = (synthetic.normal(930 + i, s) for i, s in enumerate([(1, hq, d), (n, heads, d), (n, heads, d)]))
     v = v * np.float32(2.0) ** np.linspace(-18, 6, n, dtype=np.float32)[:, None, None]
     _attend_all(q4, q, k, v[::-1] if falling else v, torch.float32, "runs", requests=16)
+
+
+@pytest.mark.parametrize("heads,hq,d", HEADS)
+@pytest.mark.parametrize("n,order", [(30, "mixed"), (254, "rising"), (254, "falling"), (3000, "mixed"), (3000, "rising")])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_scores_far_from_zero(q4, heads, hq, d, n, order, sign):
+    # One exact product each: 8 significant bits of the key, powers of two up to 2^60 of the query, so that scores go
+    # from a few to far past 2^24.  A score is off by 2^-23 of itself, which shows in weights only while neighbours
+    # are less than 40 apart, so up to scores of about 2^13: by 2^-10, and the weight beside it by as much.
+    rng = np.random.default_rng(5)
+    of = (128 + np.arange(n) % 128) * 2.0 ** (np.arange(n) * 4 // n)
+    of = {"rising": of, "falling": of[::-1], "mixed": rng.permutation(of)}[order]
+    powers = 2.0 ** np.round(np.linspace(-2, 60, hq))
+    q, k, v = np.zeros((1, hq, d)), np.zeros((n, heads, d)), synthetic.normal(940, (n, heads, d))
+    q[0, :, 0], k[:, :, 0] = sign * powers, of[:, None] / 128
+    k, v = k.astype(np.float32), np.asarray(v, np.float32)
+    cache = q4.Q4KVCache(1, heads, d, n)
+    q4.q4_kvq_append(cache, torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), _i32(0, n), _i32(0), _i32(0))
+    mass = cache.new_mass()
+    args = (cache, torch.from_numpy(q).float().cuda(), _i32(0, 1), _i32(0), _i32(n - 1))
+    o = q4.q4_kvq_attention(*args, scale=1.0, mass=mass)
+    assert torch.equal(o, q4.q4_kvq_attention(*args, scale=1.0))
+    assert q4.q4_device_status() == q4.Q4_OK
+    want, weights = ref.attention(q, ref.held(k), ref.held(v), n - 1, 1.0)
+    assert np.array_equal(ref.held(k), k)
+    wide = 16 * np.abs(ref.encode(v)[1].astype(np.float64)).max()
+    assert np.abs(o.cpu().double().numpy() - want).max() <= 2.0 ** -9 * wide
+    got = mass[0].cpu().numpy()
+    assert np.abs(got - weights).max() <= 2.0 ** -9 * hq / heads
+    assert np.allclose(got.sum(-1), hq / heads, rtol=1e-3)
