@@ -64,7 +64,7 @@ __device__ __forceinline__ uint32_t quantize_word(const float (&v)[8], int j, in
     *scale = 0x7FFFu;
     return 0x99999999u;
   }
-  if (d16 << 1 == 0) {  // a scale of 0 makes every value 0 whatever its code
+  if ((d16 & 0x7FFFu) == 0) {  // a scale of 0 (or -0) makes every value 0 whatever its code
     *scale = 0;
     return 0x88888888u;
   }

@@ -151,3 +151,28 @@ def test_scores_far_from_zero(q4, heads, hq, d, n, order, sign):
     got = mass[0].cpu().numpy()
     assert np.abs(got - weights).max() <= 2.0 ** -9 * hq / heads
     assert np.allclose(got.sum(-1), hq / heads, rtol=1e-3)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("d", [64, 128])
+def test_blocks_without_a_scale_hold_positive_zeros(q4, dtype, d):
+    # all zero, and values whose scale rounds to 0 in binary16 from either side: code 8 with scale 0, so 0 and not -0
+    x = torch.zeros((40, 2, d), dtype=torch.float32)
+    x[1], x[2] = 1e-8, -1e-8                          # scales -+1.25e-9
+    x[3, :, ::2], x[4, :, 1::2] = 2e-7, -2e-7         # half of 2^-24 is 2.98e-8: 2.5e-8 rounds to 0
+    if dtype != torch.float16:
+        x[5], x[6] = 1e-40, -1e-40                    # no normal number
+    x[7] = -0.0
+    x = x.to(dtype)
+    cache = q4.Q4KVCache(1, 2, d, 40)
+    cache.data.fill_(255)
+    args = (_i32(0, 40), _i32(0), _i32(0))
+    q4.q4_kvq_append(cache, x.cuda(), x.cuda(), *args)
+    for got in q4.q4_kvq_read(cache, *args, 40):
+        assert not got.any() and not torch.signbit(got).any()
+    assert q4.q4_device_status() == q4.Q4_OK
+    # the codes as well: the first tile (32 positions) holds nothing but code 8 and scale 0
+    tile = cache.data[:32 * (d + d // 8)].cpu()
+    half = 32 * (d // 2 + d // 16)
+    for part in (tile[:half], tile[half:]):
+        assert (part[:16 * d] == 0x88).all() and not part[16 * d:].any()
