@@ -534,7 +534,8 @@ def q4_kvq_attention(cache: Q4KVCache, q: torch.Tensor, offsets: torch.Tensor, s
 
     Row j of request s sees positions 0 .. pos[s] + j of its slot (append the
     step's rows first).  scale defaults to 1 / sqrt(head_dim).  mass, fp32
-    [slots, heads, capacity], collects the weight that each position got.
+    [slots, heads, capacity], collects the weight that each position got.  out
+    may be q itself (contiguous) where no mass is asked for, and overlaps nothing else.
     """
     S = _step(cache, offsets, slot, pos)
     dtype, device = q.dtype, cache.device
@@ -580,7 +581,8 @@ def q4_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_off
     (float16 or bfloat16), sequence s being rows offsets[s] .. offsets[s + 1].
 
     Causal rows are the last of their sequence's keys; k_offsets defaults to
-    q_offsets and scale to 1 / sqrt(D).
+    q_offsets and scale to 1 / sqrt(D).  out may be q itself (contiguous), and
+    overlaps nothing else.
     """
     if q.dim() != 3 or k.dim() != 3 or k.shape[1] == 0 or q.shape[1] == 0 or q.shape[1] % k.shape[1]:
         raise ValueError("q must be [rows, q_heads, D] with q_heads a multiple of k's heads")

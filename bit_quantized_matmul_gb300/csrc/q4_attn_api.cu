@@ -28,6 +28,32 @@ bool strides_aligned(const int64_t* st, int eb, int64_t rows, int64_t heads) {
   return (rows == 1 || st[0] * eb % 16 == 0) && (heads == 1 || st[1] * eb % 16 == 0);
 }
 
+// Whether n bytes at p and m bytes at q have one in common.
+bool meet(const void* p, int64_t n, const void* q, int64_t m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return n > 0 && m > 0 && (a <= b ? b - a < (uintptr_t)n : a - b < (uintptr_t)m);
+}
+
+// Rows x heads x D values at p: a row of them is taken as one piece, its heads' gaps included.
+struct Rows {
+  const void* p;
+  int64_t row, piece, rows;  // bytes from row to row and of a row
+  Rows(const void* p, const int64_t* st, int64_t rows, int64_t heads, int64_t d, int eb)
+      : p(p), row(rows > 1 ? st[0] * eb : 0), piece(((heads > 1 ? (heads - 1) * st[1] : 0) + d) * eb), rows(rows) {}
+  bool meets(const void* out, int64_t bytes) const {
+    const char* base = static_cast<const char*>(p);
+    if (row == 0) return rows > 0 && meet(base, piece, out, bytes);
+    // the first row that ends after `out` begins
+    const int64_t before = static_cast<const char*>(out) - base - piece;
+    const int64_t t = before < 0 ? 0 : before / row + 1;
+    return t < rows && meet(base + t * row, piece, out, bytes);
+  }
+  // the very rows, packed
+  bool same(const void* out, int64_t heads, int64_t d, int eb) const {
+    return p == out && piece == heads * d * eb && (rows == 1 || row == piece);
+  }
+};
+
 // A positive factor that stays finite in units of log2.
 bool scale_ok(float scale) { return scale > 0.0f && std::isfinite(scale * 1.4427f); }
 
@@ -96,6 +122,8 @@ int q4_kvq_read(const void* cache, void* k_out, void* v_out, int dtype, int64_t 
   if (total == 0) return Q4_OK;
   if (!cache || !k_out || !v_out || S == 0) return Q4_ERR_INVALID_ARG;
   if (!aligned16(cache) || !aligned16(k_out) || !aligned16(v_out)) return Q4_ERR_ALIGN;
+  const int64_t bytes = total * heads * head_dim * elem_bytes(dtype);
+  if (meet(k_out, bytes, v_out, bytes)) return Q4_ERR_INVALID_ARG;
   ScratchLock l;
   st = scratch_acquire(0, &l);
   if (st) return st;
@@ -117,6 +145,11 @@ int q4_kvq_attention(const void* cache, const void* q, void* out, float* mass, i
   if (total == 0) return Q4_OK;
   if (!cache || !q || !out || S == 0) return Q4_ERR_INVALID_ARG;
   if (!aligned16(cache) || !aligned16(q) || !aligned16(out) || !strides_aligned(q_strides, eb, total, q_heads)) return Q4_ERR_ALIGN;
+  // a row's queries are read before it is written, but the weights read them again
+  const Rows queries(q, q_strides, total, q_heads, head_dim, eb);
+  const int64_t out_bytes = total * q_heads * head_dim * eb;
+  if (queries.meets(out, out_bytes) && (mass || !queries.same(out, q_heads, head_dim, eb))) return Q4_ERR_INVALID_ARG;
+  if (mass && meet(mass, slots * heads * capacity * 4, out, out_bytes)) return Q4_ERR_INVALID_ARG;
   ScratchLock l;
   st = scratch_acquire(0, &l);
   if (st) return st;
@@ -145,6 +178,9 @@ int q4_kvq_evict(void* cache, float* mass, int64_t slots, int64_t heads, int64_t
   // a grid dimension, and the 32-bit item index of one plane's copy
   if (S * heads > 65535 || keep > INT32_MAX / 16) return Q4_ERR_SHAPE;
   if (!aligned16(cache)) return Q4_ERR_ALIGN;
+  for (const int32_t* in : {src, dst, len})  // read by every CTA, whichever writes first
+    if (meet(in, S * 4, new_len, S * 4) || meet(in, S * 4, kept, S * heads * keep * 4)) return Q4_ERR_INVALID_ARG;
+  if (meet(new_len, S * 4, kept, S * heads * keep * 4)) return Q4_ERR_INVALID_ARG;
   ScratchLock l;
   st = scratch_acquire(0, &l);
   if (st) return st;
@@ -171,6 +207,13 @@ int q4_prompt_attention(const void* q, const void* k, const void* v, void* out, 
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !strides_aligned(q_strides, 2, q_total, q_heads) ||
       !strides_aligned(k_strides, 2, k_total, kv_heads) || !strides_aligned(v_strides, 2, k_total, kv_heads))
     return Q4_ERR_ALIGN;
+  // a tile's queries are read before its rows are written, keys and values by other tiles too
+  const Rows queries(q, q_strides, q_total, q_heads, head_dim, 2);
+  const int64_t out_bytes = q_total * q_heads * head_dim * 2;
+  if ((queries.meets(out, out_bytes) && !queries.same(out, q_heads, head_dim, 2)) ||
+      Rows(k, k_strides, k_total, kv_heads, head_dim, 2).meets(out, out_bytes) ||
+      Rows(v, v_strides, k_total, kv_heads, head_dim, 2).meets(out, out_bytes))
+    return Q4_ERR_INVALID_ARG;
   ScratchLock l;
   const int st = scratch_acquire(0, &l);
   if (st) return st;

@@ -339,7 +339,9 @@ Q4_API int q4_kv_append(void* k_cache, void* v_cache, const void* k_new, const v
  * A slot is in one request of a call at most.  Host-checked for all of them:
  * sizes >= 1, total * heads below 2^31, S >= 1 where there are rows, pointers
  * given (INVALID_ARG); head_dim 64 or 128 (SHAPE); base addresses and
- * strides multiples of 16 bytes (ALIGN).  On the device a request whose slot
+ * strides multiples of 16 bytes (ALIGN).  What a call writes overlaps nothing else
+ * that it is given (INVALID_ARG for the rows and int32 arrays of a call), but for
+ * an attention's out that is q itself, packed, where no mass is asked for.  On the device a request whose slot
  * is outside [0, slots), or whose rows pass capacity or total, is left out (its
  * rows are not written; rows that a call puts out for it are zero) and
  * q4_device_status then reports Q4_ERR_INVALID_ARG. */
@@ -440,7 +442,8 @@ Q4_API int q4_kvq_evict(void* cache, float* mass, int64_t slots, int64_t heads, 
  * lies outside a sequence's rows, NaN included, does not reach its results.
  * head_dim 64 or 128, at most 128 query heads per key/value head (SHAPE);
  * addresses and strides multiples of 16 bytes (ALIGN), strides that are taken
- * below 2^39 elements (INVALID_ARG).  A sequence whose
+ * below 2^39 elements (INVALID_ARG).  out may be q itself, packed, and overlaps
+ * nothing else (INVALID_ARG).  A sequence whose
  * offsets are out of range gets zeros and q4_device_status reports
  * Q4_ERR_INVALID_ARG.  Needs sm_103 (UNSUPPORTED). */
 Q4_API int q4_prompt_attention(const void* q, const void* k, const void* v, void* out, int dtype,

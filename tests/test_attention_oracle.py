@@ -4,6 +4,7 @@ import ctypes
 
 import numpy as np
 import pytest
+import torch
 
 import oracle
 import synthetic
@@ -138,3 +139,62 @@ def test_prompt_arguments_checked_on_host(q4):
         assert prompt(**bad) == q4.Q4_ERR_INVALID_ARG, bad
     assert prompt(d=96) == q4.Q4_ERR_SHAPE and prompt(hq=129, hk=1) == q4.Q4_ERR_SHAPE
     assert prompt(q=A + 8) == q4.Q4_ERR_ALIGN and prompt(st=(1150, 64)) == q4.Q4_ERR_ALIGN
+
+
+# ---------------------------------------------------------------- outputs over inputs
+
+def _accepted(status, q4):
+    # past the arguments' checks a call looks for a device: made only where there is none
+    return status not in (q4.Q4_ERR_INVALID_ARG, q4.Q4_ERR_SHAPE, q4.Q4_ERR_ALIGN)
+
+
+def test_outputs_over_inputs_are_refused_on_host(q4):
+    lib = q4.raw_library()
+    no_device = not torch.cuda.is_available()
+    row = 14 * 64 * 4  # bytes of a packed fp32 row
+
+    def attend(q, out, st=(896, 64), mass=None, total=3):
+        return lib.q4_kvq_attention(A << 20, q, out, mass, 0, 2, 2, 14, 64, 16, I2(*st), 0.125, A, A, A, 3, total, None)
+
+    B = A << 8
+    for bad in (dict(q=B, out=B + 16), dict(q=B, out=B - 16), dict(q=B, out=B + 3 * row - 16),
+                dict(q=B, out=B - 3 * row + 16), dict(q=B, out=B, mass=A << 30), dict(q=B, out=B, st=(1024, 64)),
+                dict(q=B, out=B, st=(896, 128)), dict(q=B, out=B + 8 * row, st=(4 * 896, 64)),
+                dict(q=B, out=B << 4, mass=(B << 4) + row),
+                dict(q=B, out=B + 16, st=(0, 64))):
+        assert attend(**bad) == q4.Q4_ERR_INVALID_ARG, bad
+    if no_device:
+        for good in (dict(q=B, out=B), dict(q=B, out=B + 3 * row), dict(q=B, out=B - 3 * row),
+                     dict(q=B, out=B + 9 * row, st=(4 * 896, 64)), dict(q=B, out=B + row, st=(8 * 896, 64)),
+                     dict(q=B, out=B + row, st=(0, 64)), dict(q=B, out=B << 4, mass=A << 30)):
+            assert _accepted(attend(**good), q4), good
+
+    def prompt(q, k, v, out, st=(1152, 64), tq=4, tk=9):
+        s = I2(*st)
+        return lib.q4_prompt_attention(q, k, v, out, 1, 14, 2, 64, s, s, s, 0.125, 1, A, A, 1, tq, tk, None)
+
+    far, row = A << 20, 14 * 64 * 2
+    for bad in (dict(q=B, k=far, v=far, out=B), dict(q=far, k=B, v=far, out=B), dict(q=far, k=far, v=B, out=B),
+                dict(q=far, k=B, v=far, out=B + 8 * 1152 * 2 + 16), dict(q=far, k=far, v=B, out=B - 4 * row + 16)):
+        assert prompt(**bad) == q4.Q4_ERR_INVALID_ARG, bad
+    assert prompt(q=B, k=far, v=far, out=B + 16, st=(896, 64)) == q4.Q4_ERR_INVALID_ARG
+    if no_device:
+        assert _accepted(prompt(q=B, k=far, v=far, out=B, st=(896, 64)), q4)
+        assert _accepted(prompt(q=far, k=B, v=far, out=B + 8 * 1152 * 2 + 256), q4)
+        assert _accepted(prompt(q=far, k=0, v=0, out=far * 2, tk=0), q4)
+
+    def read(k, v):
+        return lib.q4_kvq_read(far, k, v, 0, 2, 2, 64, 16, A, A, A, 1, 5, None)
+
+    for bad in ((B, B), (B, B + 5 * 2 * 64 * 4 - 16), (B + 16, B)):
+        assert read(*bad) == q4.Q4_ERR_INVALID_ARG, bad
+    if no_device:
+        assert _accepted(read(B, B + 5 * 2 * 64 * 4), q4)
+
+    def evict(length, new_len, kept, src=B, dst=B):
+        return lib.q4_kvq_evict(far, far * 2, 4, 2, 64, 16, src, dst, length, 3, 5, 1, new_len, kept, None)
+
+    for bad in ((B, B, A), (B, B + 8, A), (A, B * 2, B - 4), (A, B * 2, B - 3 * 2 * 5 * 4 + 4), (A, A * 2, A * 2 + 8)):
+        assert evict(*bad) == q4.Q4_ERR_INVALID_ARG, bad
+    if no_device:
+        assert _accepted(evict(B, A, A + 12), q4) and _accepted(evict(B, B - 12, B + 12), q4)

@@ -176,3 +176,27 @@ def test_blocks_without_a_scale_hold_positive_zeros(q4, dtype, d):
     half = 32 * (d // 2 + d // 16)
     for part in (tile[:half], tile[half:]):
         assert (part[:16 * d] == 0x88).all() and not part[16 * d:].any()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("heads,hq,d", HEADS)
+def test_output_in_place_of_the_queries(q4, dtype, heads, hq, d):
+    lens, news = [3000, 5, 700], [1, 3, 5]
+    cache = q4.Q4KVCache(3, heads, d, 3008)
+    k, v = (torch.from_numpy(synthetic.normal(950 + i, (sum(lens), heads, d))).cuda() for i in range(2))
+    at = np.cumsum([0] + lens).tolist()
+    q4.q4_kvq_append(cache, k, v, _i32(*at), _i32(0, 1, 2), _i32(0, 0, 0))
+    q = torch.from_numpy(synthetic.normal(952, (9, hq, d))).to(dtype).cuda()
+    step = (_i32(0, 1, 4, 9), _i32(0, 1, 2), _i32(*[n - r for n, r in zip(lens, news)]))
+    want = q4.q4_kvq_attention(cache, q, *step)
+    room = q.clone()
+    assert q4.q4_kvq_attention(cache, room, *step, out=room) is room
+    assert torch.equal(room, want)
+    room = q.clone()
+    for call in (lambda: q4.q4_kvq_attention(cache, room, *step, out=room, mass=cache.new_mass()),
+                 lambda: q4.q4_kvq_read(cache, *step, 9, k=k[:9], v=k[:9])):
+        with pytest.raises(q4.Q4Error) as e:
+            call()
+        assert e.value.status == q4.Q4_ERR_INVALID_ARG
+    assert torch.equal(room, q)
+    assert q4.q4_device_status() == q4.Q4_OK

@@ -158,3 +158,20 @@ def test_rows_of_small_and_large_scores_in_one_tile(q4, dtype, d, causal):
     err = np.abs(o - w @ v)
     assert np.all(err <= bound), "%.3g of the bound at %s" % ((err / bound).max(),
                                                               np.unravel_index(np.argmax(err / bound), err.shape))
+
+
+@pytest.mark.parametrize("heads,hq,d", [(4, 28, 128), (2, 14, 64), (8, 8, 64)])
+def test_output_in_place_of_the_queries(q4, heads, hq, d):
+    n = 700
+    q, k, v = (torch.from_numpy(synthetic.normal(990 + i, (n, h, d))).bfloat16().cuda()
+               for i, h in enumerate((hq, heads, heads)))
+    off = _i32(0, 1, 130, 400, n)
+    want = q4.q4_prompt_attention(q, k, v, off)
+    room = q.clone()
+    assert torch.equal(q4.q4_prompt_attention(room, k, v, off, out=room), want)
+    if heads == hq:
+        for call in (lambda: q4.q4_prompt_attention(q, k, v, off, out=k), lambda: q4.q4_prompt_attention(q, k, v, off, out=v)):
+            with pytest.raises(q4.Q4Error) as e:
+                call()
+            assert e.value.status == q4.Q4_ERR_INVALID_ARG
+    assert q4.q4_device_status() == q4.Q4_OK
