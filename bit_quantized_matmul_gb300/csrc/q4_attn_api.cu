@@ -12,6 +12,9 @@ using namespace q4;
 namespace {
 
 constexpr int64_t LIM = (int64_t)1 << 31;
+// Row, position and request counts end here: kernels step past their end by up to a
+// grid's worth (152 x 16 CTAs of 4 warps at most) in 32 bits.
+constexpr int64_t MOST = LIM - (1 << 17);
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -58,7 +61,7 @@ struct Rows {
 bool scale_ok(float scale) { return scale > 0.0f && std::isfinite(scale * 1.4427f); }
 
 int check_cache(int64_t slots, int64_t heads, int64_t head_dim, int64_t capacity) {
-  if (slots < 1 || heads < 1 || capacity < 1 || slots >= LIM || heads >= LIM || capacity >= LIM - 64)
+  if (slots < 1 || heads < 1 || capacity < 1 || slots >= LIM || heads >= LIM || capacity > MOST)
     return Q4_ERR_INVALID_ARG;
   if (head_dim != 64 && head_dim != 128) return Q4_ERR_SHAPE;
   // bytes and plane indexes stay far below 2^63
@@ -68,7 +71,7 @@ int check_cache(int64_t slots, int64_t heads, int64_t head_dim, int64_t capacity
 
 int check_step(const int32_t* offsets, const int32_t* slot, const int32_t* pos, int64_t S, int64_t total,
                int64_t heads) {
-  if (S < 0 || S >= INT32_MAX || total < 0 || total > INT32_MAX / 2 || total > INT32_MAX / heads)
+  if (S < 0 || S > MOST || total < 0 || total > MOST / 2 || total > MOST / heads)
     return Q4_ERR_INVALID_ARG;
   if (total > 0 && S > 0 && (!offsets || !slot || !pos)) return Q4_ERR_INVALID_ARG;
   return Q4_OK;
@@ -141,7 +144,7 @@ int q4_kvq_attention(const void* cache, const void* q, void* out, float* mass, i
   const int eb = elem_bytes(dtype);
   if (!eb || !strides_ok(q_strides) || q_heads < 1 || q_heads % heads || !scale_ok(scale))
     return Q4_ERR_INVALID_ARG;
-  if (q_heads > 65535 || total > INT32_MAX / q_heads) return Q4_ERR_SHAPE;  // a grid dimension; 32-bit row counts
+  if (q_heads > 65535 || total > MOST / q_heads) return Q4_ERR_SHAPE;  // a grid dimension; 32-bit row counts
   if (total == 0) return Q4_OK;
   if (!cache || !q || !out || S == 0) return Q4_ERR_INVALID_ARG;
   if (!aligned16(cache) || !aligned16(q) || !aligned16(out) || !strides_aligned(q_strides, eb, total, q_heads)) return Q4_ERR_ALIGN;
@@ -171,7 +174,7 @@ int q4_kvq_evict(void* cache, float* mass, int64_t slots, int64_t heads, int64_t
                  int32_t* new_len, int32_t* kept, cudaStream_t stream) {
   int st = check_cache(slots, heads, head_dim, capacity);
   if (st) return st;
-  if (S < 0 || S >= INT32_MAX || keep < 1 || keep > capacity || recent < 0 || recent > keep)
+  if (S < 0 || S > MOST || keep < 1 || keep > capacity || recent < 0 || recent > keep)
     return Q4_ERR_INVALID_ARG;
   if (S == 0) return Q4_OK;
   if (!cache || !mass || !src || !dst || !len || !new_len || !kept) return Q4_ERR_INVALID_ARG;
@@ -195,12 +198,12 @@ int q4_prompt_attention(const void* q, const void* k, const void* v, void* out, 
                         const int32_t* k_offsets, int64_t S, int64_t q_total, int64_t k_total, cudaStream_t stream) {
   if (dtype != Q4_DTYPE_F16 && dtype != Q4_DTYPE_BF16) return Q4_ERR_INVALID_ARG;
   if (!strides_ok(q_strides) || !strides_ok(k_strides) || !strides_ok(v_strides) || !scale_ok(scale) ||
-      q_heads < 1 || kv_heads < 1 || q_heads % kv_heads || S < 0 || S >= INT32_MAX || q_total < 0 ||
-      q_total >= INT32_MAX || k_total < 0 || k_total >= INT32_MAX)
+      q_heads < 1 || kv_heads < 1 || q_heads % kv_heads || S < 0 || S > MOST || q_total < 0 || q_total > MOST ||
+      k_total < 0 || k_total > MOST)
     return Q4_ERR_INVALID_ARG;
   // one tile of 128 rows takes all query heads of a key/value head; 32-bit output row index
   if ((head_dim != 64 && head_dim != 128) || q_heads / kv_heads > 128 || q_heads >= 65536 ||
-      q_total > INT32_MAX / q_heads)
+      q_total > MOST / q_heads)
     return Q4_ERR_SHAPE;
   if (q_total == 0) return Q4_OK;
   if (!q || !out || S == 0 || !q_offsets || !k_offsets || (k_total > 0 && (!k || !v))) return Q4_ERR_INVALID_ARG;

@@ -337,8 +337,8 @@ Q4_API int q4_kv_append(void* k_cache, void* v_cache, const void* k_new, const v
  *   slot,pos  device, int32 [S]: request s's slot and the position of its first
  *             row in the cache; row offsets[s] + j is position pos[s] + j.
  * A slot is in one request of a call at most.  Host-checked for all of them:
- * sizes >= 1, total * heads below 2^31, S >= 1 where there are rows, pointers
- * given (INVALID_ARG); head_dim 64 or 128 (SHAPE); base addresses and
+ * sizes >= 1, capacity, S, 2 * total and total * heads up to 2^31 - 2^17, S >= 1
+ * where there are rows, pointers given (INVALID_ARG); head_dim 64 or 128 (SHAPE); base addresses and
  * strides multiples of 16 bytes (ALIGN).  What a call writes overlaps nothing else
  * that it is given (INVALID_ARG for the rows and int32 arrays of a call), but for
  * an attention's out that is q itself, packed, where no mass is asked for.  On the device a request whose slot

@@ -198,3 +198,41 @@ def test_outputs_over_inputs_are_refused_on_host(q4):
         assert evict(*bad) == q4.Q4_ERR_INVALID_ARG, bad
     if no_device:
         assert _accepted(evict(B, A, A + 12), q4) and _accepted(evict(B, B - 12, B + 12), q4)
+
+
+def test_sizes_that_32_bit_indexes_would_pass_are_refused_on_host(q4):
+    """A loop over rows or positions steps past its end by up to a grid's warps; just below 2^31 that would turn
+    negative: an append of 2^30 - 1 rows would never end."""
+    lib = q4.raw_library()
+    most = 2 ** 31 - 2 ** 17
+    n = ctypes.c_size_t(0)
+    assert lib.q4_kvq_cache_bytes(1, 1, 64, most, ctypes.byref(n)) == q4.Q4_OK
+    for capacity in (most + 1, 2 ** 31 - 1000, 2 ** 31 - 65):
+        assert lib.q4_kvq_cache_bytes(1, 1, 64, capacity, ctypes.byref(n)) == q4.Q4_ERR_INVALID_ARG
+
+    def append(S, total, heads):
+        return lib.q4_kvq_append(A, A, A, 1, 2, heads, 64, 16, I2(0, 64), I2(0, 64), A, A, A, S, total, None)
+
+    def read(S, total, heads):
+        return lib.q4_kvq_read(A, A << 8, A << 60, 1, 2, heads, 64, 16, A, A, A, S, total, None)
+
+    for call in (append, read):
+        for S, total, heads in ((1, 2 ** 30 - 1, 1), (1, most // 2 + 1, 1), (1, most // 3 + 1, 3), (most + 1, 1, 1)):
+            assert call(S, total, heads) == q4.Q4_ERR_INVALID_ARG, (S, total, heads)
+
+    def attend(total, hq, heads=1, S=1):
+        return lib.q4_kvq_attention(A, A, A << 8, None, 1, 2, heads, hq, 64, 16, I2(0, 64), 0.125, A, A, A, S, total,
+                                    None)
+
+    assert attend(2 ** 30 - 1, 2) == q4.Q4_ERR_INVALID_ARG
+    assert attend((2 ** 31 - 1) // 28, 28) == q4.Q4_ERR_SHAPE and attend(most // 28 + 1, 28) == q4.Q4_ERR_SHAPE
+    assert attend(1, 28, S=most + 1) == q4.Q4_ERR_INVALID_ARG
+
+    def prompt(S=1, tq=4, tk=4, hq=1):
+        s = I2(0, 64)
+        return lib.q4_prompt_attention(A, A, A, A << 8, 1, hq, 1, 64, s, s, s, 0.125, 1, A, A, S, tq, tk, None)
+
+    for bad in (dict(S=most + 1), dict(tq=most + 1), dict(tk=most + 1)):
+        assert prompt(**bad) == q4.Q4_ERR_INVALID_ARG, bad
+    assert prompt(tq=most // 7 + 1, hq=7) == q4.Q4_ERR_SHAPE
+    assert lib.q4_kvq_evict(A, A, 2, 1, 64, 16, A, A, A, most + 1, 4, 1, A, A, None) == q4.Q4_ERR_INVALID_ARG
