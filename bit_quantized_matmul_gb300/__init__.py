@@ -536,6 +536,8 @@ def q4_kvq_attention(cache: Q4KVCache, q: torch.Tensor, offsets: torch.Tensor, s
     step's rows first).  scale defaults to 1 / sqrt(head_dim).  mass, fp32
     [slots, heads, capacity], collects the weight that each position got.  out
     may be q itself (contiguous) where no mass is asked for, and overlaps nothing else.
+    Uses the library's scratch, which the device's streams share: order calls on
+    one stream.  The first call, or one of many more requests, allocates some.
     """
     S = _step(cache, offsets, slot, pos)
     dtype, device = q.dtype, cache.device

@@ -338,13 +338,14 @@ Q4_API int q4_kv_append(void* k_cache, void* v_cache, const void* k_new, const v
  *             row in the cache; row offsets[s] + j is position pos[s] + j.
  * A slot is in one request of a call at most.  Host-checked for all of them:
  * sizes >= 1, capacity, S, 2 * total and total * heads up to 2^31 - 2^17, S >= 1
- * where there are rows, pointers given (INVALID_ARG); head_dim 64 or 128 (SHAPE); base addresses and
- * strides multiples of 16 bytes (ALIGN).  What a call writes overlaps nothing else
- * that it is given (INVALID_ARG for the rows and int32 arrays of a call), but for
- * an attention's out that is q itself, packed, where no mass is asked for.  On the device a request whose slot
- * is outside [0, slots), or whose rows pass capacity or total, is left out (its
- * rows are not written; rows that a call puts out for it are zero) and
- * q4_device_status then reports Q4_ERR_INVALID_ARG. */
+ * where there are rows, pointers given (INVALID_ARG); head_dim 64 or 128
+ * (SHAPE); base addresses and strides multiples of 16 bytes (ALIGN).  What a
+ * call writes overlaps nothing else that it is given (INVALID_ARG for its rows
+ * and int32 arrays), but for an attention's out that is q itself, packed, where
+ * no mass is asked for.  On the device a request whose slot is outside
+ * [0, slots), or whose rows pass capacity or total, is left out (its rows are
+ * not written; rows that a call puts out for it are zero) and q4_device_status
+ * then reports Q4_ERR_INVALID_ARG. */
 
 /* Element types of rows that are passed in or out. */
 #define Q4_DTYPE_F32 0
@@ -389,8 +390,8 @@ Q4_API int q4_kvq_read(const void* cache, void* k_out, void* v_out, int dtype, i
  *         only a prompt's positions have to be set before.  Each slot in at
  *         most one request of the call.
  * Products carry fp32 accuracy for fp32 queries; sums are held in fp32.  What a
- * key adds is held to 2^-29 of the largest scale among its head's V blocks (of 2^-14 at
- * least), however small its weight next to the row's largest.  The
+ * key adds is held to 2^-29 of the largest scale among its head's V blocks (of
+ * 2^-14 at least), however small its weight next to the row's largest.  The
  * lengths are read on the device only: a launch of a fixed number of CTAs
  * divides them evenly.  The same call gives the same bits; where a request is
  * divided, and with it the last bits of its rows, depends on the lengths of the
@@ -437,9 +438,9 @@ Q4_API int q4_kvq_evict(void* cache, float* mass, int64_t slots, int64_t heads, 
  *   causal     nonzero: row i of a sequence sees its keys j <= i + klen - qlen
  *              (the rows are the sequence's last); else all of its keys.
  * Rows that see no key, and rows of no sequence, get zeros.  Weights are
- * rounded to dtype before the product with v (F16: a key's weight below 2^-21 of the row's
- * largest to 2^-32 of that); sums are held in fp32.  What
- * lies outside a sequence's rows, NaN included, does not reach its results.
+ * rounded to dtype before the product with v (F16: a weight below 2^-21 of the
+ * row's largest to 2^-32 of that); sums are held in fp32.  What lies outside a
+ * sequence's rows, NaN included, does not reach its results.
  * head_dim 64 or 128, at most 128 query heads per key/value head (SHAPE);
  * addresses and strides multiples of 16 bytes (ALIGN), strides that are taken
  * below 2^39 elements (INVALID_ARG).  out may be q itself, packed, and overlaps
