@@ -28,40 +28,43 @@
 // instruction a register, none for the offset).  V's scales are folded into the
 // weights of their block, x = w d: with w = wh + wl split once for all blocks,
 // hi = wh d rounded, and lo = (wh d - hi) + wl d, whose first part a fused
-// multiply-add gives exactly: three instructions for two weights.  Weights and
-// V's scales are taken times powers of two (the weights 2^9, the scales so that the largest
-// so far is about 1), so that they and x fit binary16 and lo keeps its bits; a scale's costs one
-// more instruction for two (no time: 36.5 us either way for 64 ragged requests).
-// Lo ends at 2^-24 all the same: next to a key of weight 1 the others are held to 2^-29 of V's
-// largest scale each, so of a weight 2^-b about 33 - b bits count.  Values lie along m and virtual rows
-// along n, and hi and lo go into one accumulator.  Rows of 16 bits get the lo terms
-// too: without them sums that nearly cancel keep errors of 2^-12 of their terms,
-// more than their own rounding (8 bf16 requests at 32k would take 38.1 us instead of
-// 42.4, in one graph over the same inputs).
+// multiply-add gives exactly: three instructions for two weights.  Weights and V's
+// scales are taken times powers of two (the weights 2^9, the scales so that the
+// largest so far is about 1), so that they and x fit binary16 and lo keeps its
+// bits.  A scale's costs one more instruction for two: 64 ragged requests called in
+// turn take 38.0 us with it, 37.0 without, 8 at 32k 43.3 and 43.1.  Lo ends at 2^-24
+// all the same: next to a key of weight 1 the others are held to 2^-29 of V's largest
+// scale each, so of a weight 2^-b about 33 - b bits count.  Values lie along m and
+// virtual rows along n, and hi and lo go into one accumulator.  Rows of 16 bits get
+// the lo terms too: without them sums that nearly cancel keep errors of 2^-12 of their
+// terms, more than their own rounding (8 bf16 requests at 32k would take 38.1 us
+// instead of 42.4, in one graph over the same inputs).
 //
 // Work.  A unit is one cache tile (32 positions) of one item (request, head,
 // eight virtual rows).  The launch's warps take equal, contiguous ranges of
 // units whatever the lengths are (each CTA sums the lengths itself, so the
 // host needs none of them), each through its own ring of bulk copies; after
 // the plan no warp waits for another.  Items cut between warps leave
-// (reference score, sum, o) in scratch and a second launch joins them.  Each
-// launch begins under the end of the one before and waits for it on the device.  A launch
-// that lets others begin before its own wait is done would let them begin while a kernel
-// two places back still runs, and their waits are for the launch before them only: so the
-// first launch lets the join begin after its wait, and what the join and the weights'
-// launch read before theirs is older than the call.  Nothing comes by the read-only
-// path, which is for memory that no kernel writes meanwhile.  The early beginning
-// of the first launch is worth 2 us of every call that follows another (64 ragged
-// requests called in turn 38.8 us without, 36.8 with).
+// (reference score, sum, o) in scratch and a second launch joins them.
+//
+// Launches.  Each begins under the end of the one before and waits for it on the device.
+// One that let others begin before its own wait was done would let them begin while
+// a kernel two places back still ran, and their waits are for the launch before them
+// only: so the first launch lets the join begin after its wait, and what the join and the
+// weights' launch read before theirs is older than the call.  Nothing comes by the
+// read-only path, which is for memory that no kernel writes meanwhile.  The early
+// beginning of the first launch is worth 0.8 us of a call that follows another
+// (64 ragged requests called in turn 38.9 us without, 38.1 with; 32 with weights,
+// behind the copy of theirs, 53.2 and 50.2).
 //
 // Measured (28/4 heads of 128; both launches in a graph, inputs past the L2): 64
-// fp32 rows over 176,432 positions 36.5 us (103 MB: 2.8 TB/s), 8 bf16 rows over
-// 254,706 44.0 us (147 MB: 3.3 TB/s).  The copies alone take 23 and 31 us.  What is
-// left is the arithmetic of 4-bit operands on warp-wide products: 384 warp
+// fp32 rows over 176,432 positions 37.4 us (103 MB: 2.8 TB/s), 8 bf16 rows over
+// 254,706 44.2 us (147 MB: 3.3 TB/s).  The copies alone take 23 and 31 us.  What is
+// left is the arithmetic of 4-bit operands on warp-wide products: 395 warp
 // instructions for 16 positions (fp32 rows), with which issue slots are 52% busy, the
-// ALU 41%, the products 34%; three CTAs per SM (168 registers) hide no more of
+// ALU 41%, the products 33%; three CTAs per SM (168 registers) hide no more of
 // their latency, and four (128 registers) were slower.  44 draft rows of 16
-// requests (five row groups a head, each unpacks the cache for itself) take 22.5 us,
+// requests (five row groups a head, each unpacks the cache for itself) take 23.6 us,
 // one row over 2,049 positions of 2 heads of 64 7.9 us, all of it launches and the
 // latency of one short chain.
 #include <atomic>
@@ -734,6 +737,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kvq_join_kernel(const Args<T>
   const int q_heads = a.heads * a.group;
   const int at = PER_ROW == 1 ? blockIdx.x * JOIN_WARPS + (threadIdx.x >> 5) : blockIdx.x;
   const int t = at / q_heads, hq = at - t * q_heads;
+  // the weights' launch may begin: what it reads before its wait, the main launch does not write
   asm volatile("griddepcontrol.launch_dependents;");
   const int s = kvq_find_request<true>(a.offsets, a.S, t, lane);
   const Request r = load_request(a, s, true);
@@ -824,7 +828,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kvq_join_kernel(const Args<T>
 // as many bytes for a group of seven heads.  The eight rows' weights of a tile
 // are summed over lanes and dealt out in seven shuffles, a position to each
 // lane; every position belongs to one lane, so the sums have a fixed order.
-// 32 requests of 103,047 positions (4 heads of 128): 16.5 us cold, 30 MB of K;
+// 32 requests of 103,047 positions (4 heads of 128): 17 us cold, 30 MB of K;
 // it starts when the join is done and is bound as the main launch is.
 template <int D, typename T>
 __global__ void __launch_bounds__(THREADS) kvq_mass_kernel(const Args<T> a) {

@@ -37,9 +37,12 @@
 // The products of a tile run in order, so when S of block i + 1 is there, the
 // accumulation of block i is done and O may be rescaled without a wait.
 //
-// Measured (28/4 heads of 128): a bf16 prompt of 16,384 rows takes 1.22 ms,
-// 1,584 TFLOP/s; one of 4,096 rows 1,163 TFLOP/s (tensor pipe 57% busy, issue slots
-// 43%, exponentials 29%); nine fp16 prompts of 15,374 rows 197 us, 1,042 TFLOP/s.
+// Measured (28/4 heads of 128, in a graph): a bf16 prompt of 16,384 rows takes 1.19 ms,
+// 1,617 TFLOP/s, over the same inputs again, 1.21 to 1.29 ms over others in turn and
+// 1.29 when it is called without a pause (1,490: the clock gives way); one of 4,096
+// rows 102 us, 1,180 TFLOP/s (tensor pipe 59% busy, issue slots 43%, exponentials 30%);
+// nine fp16 prompts of 15,374 rows 197 us, 1,042 TFLOP/s.  Scores of four times the
+// spread, whose sums are rescaled more often, cost 5 to 9% more.
 // What is lost there is the ends: a pair's first scores and its last output
 // have no other product beside them, about 1.5 us a pair.  Issuing a product
 // from one lane's registers instead of the warp's uniform ones cost a fifth
