@@ -57,6 +57,7 @@ EXPORTS = (
     "q4_kv_append",
     "q4_kvq_cache_bytes", "q4_kvq_append", "q4_kvq_read", "q4_kvq_attention", "q4_kvq_evict",
     "q4_prompt_attention",
+    "q4_paged_reserve", "q4_paged_append", "q4_paged_attention",
 )
 
 if not os.path.exists(LIB_PATH):
@@ -93,6 +94,10 @@ _sig = {
     "q4_kvq_evict": [_p, _p] + [_i64] * 4 + [_p] * 3 + [_i64] * 3 + [_p] * 3,
     "q4_prompt_attention": [_p] * 4 + [_int] + [_i64] * 3 + [_p] * 3 + [ctypes.c_float, _int, _p, _p] + [_i64] * 3 +
                            [_p],
+    "q4_paged_reserve": [_p] * 4 + [_i64] * 4 + [_p] * 3 + [_i64, _i64] + [_p] * 3,
+    "q4_paged_append": [_p, _p, _int, _p, _p, _int] + [_i64] * 4 + [_p] * 3 + [_i64, _p],
+    "q4_paged_attention": [_p] * 4 + [_int] + [_i64] * 5 + [_p, ctypes.c_float, _p, _i64, _i64] + [_p] * 3 +
+                          [_i64, _i64, _p],
     "q4mm_select_path": [_p, _i64, _u32],
     "q4mm_plan_info": [_p, _i64, _u32, ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int),
                        ctypes.POINTER(ctypes.c_int)],
@@ -452,6 +457,14 @@ def _out3(t, shape, dtype, device, name: str) -> torch.Tensor:
     return t
 
 
+def _out1(t, n: int, index: int, device, name: str) -> torch.Tensor:
+    if t is None:
+        return torch.empty((n,), dtype=_i32, device=device)
+    if _ints(index, t, name) != n:
+        raise ValueError("%s must have %d entries" % (name, n))
+    return t
+
+
 class Q4KVCache:
     """A 4-bit KV cache of one decoder layer: slots x heads x capacity positions of head_dim values.
 
@@ -606,6 +619,112 @@ def q4_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_off
     _call(_lib.q4_prompt_attention, "q4_prompt_attention", index, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(),
           out.data_ptr(), _DTYPES[dtype], hq, hk, d, qs, ks, vs, d ** -0.5 if scale is None else scale,
           1 if causal else 0, q_offsets.data_ptr(), k_offsets.data_ptr(), S, tq, tk)
+    return out
+
+
+class Q4PageTable:
+    """Block tables of `slots` requests, up to `width` pages each, over a pool of `pages` pages of `page_size` positions.
+
+    One int32 buffer (``state``) holds it all: ``free_count`` [1], ``free`` [pages], ``held`` [slots] and ``table``
+    [slots, width] are views of it, so copying it back takes a step back.  At first every page is free.
+    """
+
+    def __init__(self, slots: int, width: int, pages: int, page_size: int, device=None):
+        self.slots, self.width, self.pages, self.page_size = int(slots), int(width), int(pages), int(page_size)
+        if min(self.slots, self.width, self.pages) < 1 or self.page_size not in (16, 32, 64, 128):
+            raise ValueError("slots, width and pages must be positive and page_size 16, 32, 64 or 128")
+        n = 1 + self.pages
+        device = torch.device("cuda" if device is None else device)
+        self.state = torch.full((n + self.slots * (self.width + 1),), -1, dtype=_i32, device=device)
+        self.free_count, self.free = self.state[:1], self.state[1:n]
+        self.held = self.state[n:n + self.slots]
+        self.table = self.state[n + self.slots:].view(self.slots, self.width)
+        self.free_count.fill_(self.pages)
+        self.free.copy_(torch.arange(self.pages - 1, -1, -1, dtype=_i32))  # page 0 is given out first
+        self.held.zero_()
+        self.device = self.state.device
+        self._index = self.state.get_device()
+        base = self.state.data_ptr()
+        self._pointers = (base + 4 * (n + self.slots), base + 4 * n, base + 4, base)  # table, held, free, free_count
+
+
+class Q4PagedCache:
+    """K and V of one decoder layer in pages: ``k`` and ``v`` [pages, heads, page_size, head_dim] of a 16-bit type."""
+
+    def __init__(self, pages: int, heads: int, head_dim: int, page_size: int, dtype=torch.bfloat16, device=None):
+        self.pages, self.heads, self.head_dim, self.page_size = int(pages), int(heads), int(head_dim), int(page_size)
+        if dtype not in (torch.float16, torch.bfloat16):
+            raise ValueError("dtype must be float16 or bfloat16")
+        device = torch.device("cuda" if device is None else device)
+        self.dtype = dtype
+        self._data = torch.zeros((2, self.pages, self.heads, self.page_size, self.head_dim), dtype=dtype, device=device)
+        self.k, self.v = self._data[0], self._data[1]
+        self.device = self._data.device
+        self._dims = (self.pages, self.heads, self.head_dim, self.page_size)
+        self._index = self._data.get_device()
+        self._pointers = (self.k.data_ptr(), self.v.data_ptr())
+
+    @property
+    def nbytes(self) -> int:
+        return self._data.numel() * 2
+
+
+def q4_paged_reserve(tables: Q4PageTable, offsets: torch.Tensor, slot: torch.Tensor, pos: torch.Tensor, total: int,
+                     slot_map: torch.Tensor | None = None, new_length: torch.Tensor | None = None, stream=None):
+    """Pages for a step's requests: (slot_map int32 [total], new_length int32 [S]).
+
+    Afterwards slot[s] holds the pages of pos[s] plus its packed rows offsets[s] .. offsets[s + 1]: it
+    is given what it lacks, and surplus ones return to the pool (a request that ended: pos 0, no rows).
+    slot_map has each row's place for ``q4_paged_append``, -1 where a request is refused; new_length
+    is then -1 too, and ``q4_device_status`` says why (no pages left: Q4_ERR_NOMEM).
+    """
+    S = _step(tables, offsets, slot, pos)
+    total, index = int(total), tables._index
+    slot_map = _out1(slot_map, total, index, tables.device, "slot_map")
+    new_length = _out1(new_length, S, index, tables.device, "new_length")
+    _call(_lib.q4_paged_reserve, "q4_paged_reserve", index, stream, *tables._pointers, tables.slots, tables.width,
+          tables.pages, tables.page_size, offsets.data_ptr(), slot.data_ptr(), pos.data_ptr(), S, total,
+          slot_map.data_ptr(), new_length.data_ptr())
+    return slot_map, new_length
+
+
+def q4_paged_append(cache: Q4PagedCache, k_new: torch.Tensor, v_new: torch.Tensor, slot_map: torch.Tensor, stream=None):
+    """The step's new K/V rows ([total, heads, head_dim] views of the cache's type, or float32, then
+    rounded) into the pages: row t to place slot_map[t] (int32 [total], -1: not cached)."""
+    dtype, index = k_new.dtype, cache._index
+    code = _dtype_code(dtype, "k_new")
+    pages, heads, d, page = cache._dims
+    total, ks = _rows3(k_new, "k_new", heads, d, dtype, index)
+    total_v, vs = _rows3(v_new, "v_new", heads, d, dtype, index)
+    if total_v != total or _ints(index, slot_map, "slot_map") != total:
+        raise ValueError("k_new, v_new and slot_map differ in rows")
+    _call(_lib.q4_paged_append, "q4_paged_append", index, stream, *cache._pointers, _DTYPES[cache.dtype],
+          k_new.data_ptr(), v_new.data_ptr(), code, pages, heads, d, page, ks, vs, slot_map.data_ptr(), total)
+
+
+def q4_paged_attention(cache: Q4PagedCache, tables: Q4PageTable, q: torch.Tensor, offsets: torch.Tensor,
+                       slot: torch.Tensor, pos: torch.Tensor, scale: float | None = None,
+                       out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of the step's query rows over the pages, [total, q_heads, head_dim] of the cache's type.
+
+    Row j of request s sees positions 0 .. pos[s] + j of its slot (append the step's rows first):
+    single tokens, drafts and chunks of prompts in one call.  scale defaults to 1 / sqrt(head_dim).
+    out may be q itself (contiguous), and overlaps nothing else.  Uses the library's
+    scratch, which the device's streams share: order calls on one stream.  The first call allocates some.
+    """
+    S = _step(cache, offsets, slot, pos)
+    pages, heads, d, page = cache._dims
+    if tables._index != cache._index or tables.page_size != page or tables.pages != pages:
+        raise ValueError("tables and cache differ in pages, page_size or device")
+    hq = q.shape[1] if q.dim() == 3 else 0
+    if hq == 0 or hq % heads:
+        raise ValueError("q must be [total, q_heads, head_dim] with q_heads a multiple of %d" % heads)
+    total, qs = _rows3(q, "q", hq, d, cache.dtype, cache._index)
+    out = _out3(out, (total, hq, d), cache.dtype, cache.device, "out")
+    _call(_lib.q4_paged_attention, "q4_paged_attention", cache._index, stream, *cache._pointers, q.data_ptr(),
+          out.data_ptr(), _DTYPES[cache.dtype], pages, heads, hq, d, page, qs, d ** -0.5 if scale is None else scale,
+          tables._pointers[0], tables.slots, tables.width, offsets.data_ptr(), slot.data_ptr(), pos.data_ptr(), S,
+          total)
     return out
 
 

@@ -1,0 +1,980 @@
+// q4_paged_attention.cu — attention of a step's rows over a paged 16-bit cache,
+// on the tensor cores.
+//
+//   o[j] = sum_{p <= pos + j} softmax_p(scale q_j . k_p) v_p,
+//   position p in row p % P of page table[slot][p / P], per request and head.
+#include "q4_tiles.cuh"
+#include "q4mm_internal.h"
+
+namespace q4 {
+namespace {
+
+constexpr int SOFTMAX_WARPS = 16;
+constexpr int COPY_WARP = 16, MMA_WARP = 17, FIX_WARP = 19;  // and MMA_WARP + 1
+constexpr int WORKS = 2;                                     // the piece that is copied and the one before
+constexpr int THREADS = 640;
+constexpr int TMEM_COLS = 512;
+constexpr int END_UNITS = 1;  // what an item costs beside its blocks, in blocks
+
+template <int D>
+struct Cfg {
+  static constexpr int CHUNKS = D / 64;              // 128-byte column chunks of a row
+  static constexpr int TILE = BM * D * 2;            // one Q tile, K block or V block
+  static constexpr int Q_CHUNK = BM * 128;           // Q: chunk by chunk
+  static constexpr int GROUP = CHUNKS * 1024;        // K, V: eight keys, chunk by chunk
+  static constexpr int STAGES = D == 128 ? 4 : 8;    // K, V blocks in the ring (even: K and V alternate)
+  static constexpr int BAR_OFF = (2 + STAGES) * TILE;
+  static constexpr int SMEM = BAR_OFF + 512 + 1024;  // + alignment slack
+  static constexpr int O_COL = 2 * BN;               // S0, S1, then O0, O1
+};
+
+struct Args {
+  const void* v_pages;
+  void* out;
+  int64_t total, slots, width;
+  int pages, heads, q_heads, group, positions, shift;  // positions per tile; a page is 1 << shift positions
+  int S;
+  int wide;  // out is 32-byte aligned
+  float scale_log2;
+  const int32_t *table, *offsets, *slot, *pos;
+  PagedAttnScratch ws;
+  unsigned* status;
+  unsigned long long wait_ns;
+  int stall;  // test setting: no copy is issued, so every wait for one runs out
+};
+
+struct Request {
+  int qb, rows, past, slot;
+};
+
+__device__ __forceinline__ bool load_request(const Args& a, int s, Request* r) {
+  const int b = a.offsets[s], e = a.offsets[s + 1];
+  *r = Request{b, e - b, a.pos[s], a.slot[s]};
+  const bool ok = b >= 0 && e >= b && e <= a.total && r->slot >= 0 && r->slot < a.slots && r->past >= 0 &&
+                  (int64_t)r->past + r->rows <= a.width << a.shift;
+  return ok;
+}
+
+// The key blocks of full pairs 0 .. n - 1 of a request: pair i sees up to position
+// past + (i + 1) 2 P - 1, which repeats with the period of 64 pairs (P blocks).
+__host__ __device__ __forceinline__ int64_t full_blocks(int past, int positions, int n) {
+  const int step = 2 * positions, q = n / 64, r = n % 64;
+  int64_t part = 0, period = 0;
+  const int upto = q ? 64 : r;
+  for (int i = 0; i < upto; ++i) {
+    const int64_t nb = ((int64_t)past + (int64_t)(i + 1) * step - 1) / BN + 1;
+    period += nb;
+    if (i < r) part += nb;
+  }
+  return part + (q ? q * period + (int64_t)positions * 64 * ((int64_t)q * (q - 1) / 2) + (int64_t)r * q * positions : 0);
+}
+// Units of one head of a request: its blocks, and what its items cost beside them.
+__host__ __device__ __forceinline__ int64_t head_units(int past, int rows, int positions) {
+  const int step = 2 * positions, n = rows / step;
+  int64_t u = full_blocks(past, positions, n) + (int64_t)n * END_UNITS;
+  if (rows % step) u += ((int64_t)past + rows - 1) / BN + 1 + END_UNITS;
+  return u;
+}
+// The first unit of share c of n.
+__host__ __device__ __forceinline__ int64_t share_begin(int64_t all, int c, int n) { return all * c / n; }
+// The share that has a unit.
+__host__ __device__ __forceinline__ int share_of(int64_t all, int64_t unit, int n) {
+  int c = (int)((double)unit * n / (double)all);
+  c = c < 0 ? 0 : c > n - 1 ? n - 1 : c;
+  while (c > 0 && share_begin(all, c, n) > unit) --c;
+  while (c < n - 1 && share_begin(all, c + 1, n) <= unit) ++c;
+  return c;
+}
+
+// A share's piece of an item: blocks [b0, b1) of a pair of tiles of one head.
+struct Piece {
+  int ok;    // 0: there is no more
+  int head, pos0;  // first row of tile 0 in the request
+  Request r;
+  int b0, b1;
+  int part;  // where its sums go: -1: the whole item, straight to the output
+};
+
+// What the roles derive from a piece.
+struct Plan {
+  int mine[2];       // the piece's blocks that each tile sees
+  int nblocks;       // of the piece
+  int first_hidden;  // the first position that some row of the pair does not see
+  int seen_end;      // positions from here on are seen by no row of it
+  int zone;          // blocks from here on hold such positions
+  __device__ __forceinline__ Plan(const Args& a, const Piece& w) {
+    nblocks = w.b1 - w.b0;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int p0 = w.pos0 + t * a.positions;
+      const int blocks = p0 < w.r.rows ? (w.r.past + min(p0 + a.positions, w.r.rows) - 1) / BN + 1 : 0;
+      mine[t] = max(0, min(blocks, w.b1) - w.b0);
+    }
+    seen_end = w.r.past + min(w.pos0 + 2 * a.positions, w.r.rows);
+    first_hidden = w.r.past + w.pos0 + 1;
+    zone = first_hidden / BN;
+  }
+};
+
+__device__ __forceinline__ int64_t scan64(int64_t v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    if (lane >= o) v += x;
+  }
+  return v;
+}
+
+// Rows that belong to no request, or to one that is out of range, are zero: the
+// share of one of `threads` threads.
+template <int D>
+__device__ void clear_rows(const Args& a, bool bad, int64_t thread, int64_t threads) {
+  const int64_t row = (int64_t)a.q_heads * D / 8;  // 16-byte vectors of a packed row
+  auto clear = [&](int64_t r0, int64_t r1) {
+    uint4* p = static_cast<uint4*>(a.out);
+    r0 = r0 < 0 ? 0 : r0;
+    r1 = r1 > a.total ? a.total : r1;
+    for (int64_t i = r0 * row + thread; i < r1 * row; i += threads) p[i] = make_uint4(0u, 0u, 0u, 0u);
+  };
+  clear(0, a.offsets[0]);
+  clear(a.offsets[a.S], a.total);
+  for (int s = 0; bad && s < a.S; ++s) {
+    Request r;
+    if (!load_request(a, s, &r)) clear(r.qb, (int64_t)r.qb + r.rows);
+  }
+}
+
+// Goes through the pieces of a CTA's share, run by one warp.
+struct Walk {
+  Request r;          // lane l: request base + l
+  int base;
+  int s, head, pair;  // the item it stands at
+  int64_t skip;       // units of it that belong to shares before
+  int64_t left;       // units of the share
+  __device__ __forceinline__ void load(const Args& a, int lane) {
+    r = Request{0, 0, 0, 0};
+    if (base + lane < a.S && !load_request(a, base + lane, &r)) r.rows = 0;
+  }
+  // at unit `rem` of request s0
+  __device__ __forceinline__ void begin(const Args& a, int s0, int64_t rem, int64_t units, int lane) {
+    base = s = s0;
+    left = units;
+    load(a, lane);
+    const int past = __shfl_sync(0xFFFFFFFFu, r.past, 0), rows = __shfl_sync(0xFFFFFFFFu, r.rows, 0);
+    const int64_t each = head_units(past, rows, a.positions);
+    head = each ? (int)(rem / each) : 0;
+    rem -= head * each;
+    const int step = 2 * a.positions, pairs = (rows + step - 1) / step;
+    // 32 pairs at a time
+    pair = 0;
+    for (int i = 0; i < pairs; i += 32) {
+      const int p = i + lane;
+      const int64_t u = p < pairs ? ((int64_t)past + min((p + 1) * (int64_t)step, (int64_t)rows) - 1) / BN + 1 + END_UNITS
+                                  : 0;
+      const int64_t upto = scan64(u, lane);
+      const unsigned hit = __ballot_sync(0xFFFFFFFFu, rem < upto);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        pair = i + l;
+        rem -= __shfl_sync(0xFFFFFFFFu, upto - u, l);
+        break;
+      }
+      rem -= __shfl_sync(0xFFFFFFFFu, upto, 31);
+    }
+    skip = rem;
+  }
+  // The next piece, the same for every lane; false when there is none.
+  __device__ __forceinline__ bool next(const Args& a, int cta, int lane, Piece* w) {
+    const int step = 2 * a.positions;
+    while (left > 0) {
+      if (s - base >= 32) {
+        base = s;
+        load(a, lane);
+      }
+      const int l = s - base;
+      w->r.qb = __shfl_sync(0xFFFFFFFFu, r.qb, l);
+      w->r.rows = __shfl_sync(0xFFFFFFFFu, r.rows, l);
+      w->r.past = __shfl_sync(0xFFFFFFFFu, r.past, l);
+      w->r.slot = __shfl_sync(0xFFFFFFFFu, r.slot, l);
+      if ((int64_t)pair * step >= w->r.rows) {  // a request without rows
+        ++s;
+        head = pair = 0;
+        continue;
+      }
+      w->ok = 1;
+      w->head = head;
+      w->pos0 = pair * step;
+      const int nb = (int)(((int64_t)w->r.past + min((int64_t)w->pos0 + step, (int64_t)w->r.rows) - 1) / BN + 1);
+      const int64_t upto = min((int64_t)nb + END_UNITS, skip + left);
+      w->b0 = (int)max((int64_t)0, skip - END_UNITS);
+      w->b1 = (int)max((int64_t)0, upto - END_UNITS);
+      w->part = w->b0 == 0 && w->b1 == nb ? -1 : 2 * cta + (w->b0 > 0 ? 0 : 1);
+      left -= upto - skip;
+      skip = 0;
+      if ((int64_t)w->pos0 + step < w->r.rows) {
+        ++pair;
+      } else {
+        pair = 0;
+        if (++head == a.heads) {
+          head = 0;
+          ++s;
+        }
+      }
+      if (w->b1 > w->b0) return true;
+    }
+    return false;
+  }
+};
+
+template <int D, typename T>
+__global__ void __launch_bounds__(THREADS, 1)
+    paged_kernel(const Args a, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                 const __grid_constant__ CUtensorMap map_v) {
+  using C = Cfg<D>;
+  constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
+  constexpr int NST = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Piece work[WORKS];
+  __shared__ int s_err, s_bad, s_first, s_nonfinite[WORKS];
+  __shared__ int64_t s_rem, s_scan[THREADS / 32];
+  __shared__ float s_max[2][2][BM], s_sum[2][2][BM];  // [tile][half][row]: what the halves exchange
+  __shared__ uint32_t s_tmem;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // one value for the warp, as far as the compiler can see
+  const int G = a.group, P = a.positions;
+
+  const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* smem_p = smem_raw + (smem - smem_u32(smem_raw));
+  const uint32_t q_smem = smem, ring = smem + 2 * C::TILE, bars = smem + C::BAR_OFF;
+  const uint32_t q_full = bars, q_empty = q_full + 8, drain = q_empty + 8;
+  const uint32_t full = drain + 8, empty = full + 8 * NST, hidden = empty + 8 * NST, fixed = hidden + 8 * NST;
+  const uint32_t s_full = fixed + 8 * NST, p_full = s_full + 16, o_full = p_full + 32, o_empty = o_full + 16;
+  const uint32_t turn = o_empty + 16, work_full = turn + 16, work_empty = work_full + 8 * WORKS;
+  volatile int* err = &s_err;
+  if (tid == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 2);
+    mbar_init(drain, 2);
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, 2);
+      mbar_init(hidden + 8 * i, 1);
+      mbar_init(fixed + 8 * i, 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(s_full + 8 * t, 1);
+      mbar_init(p_full + 16 * t, 4);
+      mbar_init(p_full + 16 * t + 8, 4);
+      mbar_init(o_full + 8 * t, 1);
+      mbar_init(o_empty + 8 * t, 8);
+      mbar_init(turn + 8 * t, 1);
+    }
+    for (int i = 0; i < WORKS; ++i) {
+      mbar_init(work_full + 8 * i, 1);
+      mbar_init(work_empty + 8 * i, SOFTMAX_WARPS + 3);  // and the products' and V's warps
+      s_nonfinite[i] = 0;
+    }
+    mbar_arrive(turn);  // tile 0 begins
+    s_err = 0;
+    s_bad = 0;
+    mbar_init_fence();
+  }
+  if (warp == MMA_WARP) tmem_alloc(smem_u32(&s_tmem), TMEM_COLS);
+
+  // ---- the CTA's share of the units, by all threads: each has a run of requests ----
+  const int per = (a.S + THREADS - 1) / THREADS, s_begin = min(a.S, tid * per), s_end = min(a.S, s_begin + per);
+  int64_t units = 0;
+  bool bad = false;
+  for (int s = s_begin; s < s_end; ++s) {
+    Request r;
+    if (load_request(a, s, &r)) units += a.heads * head_units(r.past, r.rows, P);
+    else bad = true;
+  }
+  const int64_t upto = scan64(units, lane);
+  if (lane == 31) s_scan[warp] = upto;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (bad) s_bad = 1;
+  int64_t before = upto - units, all = 0;
+  for (int i = 0; i < THREADS / 32; ++i) {
+    if (i < warp) before += s_scan[i];
+    all += s_scan[i];
+  }
+  const int shares = (int)min((int64_t)gridDim.x, all);
+  const bool idle = (int)blockIdx.x >= shares;
+  const int64_t u0 = idle ? 0 : share_begin(all, blockIdx.x, shares);
+  const int64_t u1 = idle ? 0 : share_begin(all, blockIdx.x + 1, shares);
+  if (!idle && u0 >= before && u0 < before + units) {
+    int64_t rem = u0 - before;
+    int s = s_begin;
+    for (; s < s_end; ++s) {
+      Request r;
+      const int64_t u = load_request(a, s, &r) ? a.heads * head_units(r.past, r.rows, P) : 0;
+      if (rem < u) break;
+      rem -= u;
+    }
+    s_first = s;
+    s_rem = rem;
+  }
+  __syncthreads();
+  if (s_bad || a.offsets[0] > 0 || a.offsets[a.S] < a.total)
+    clear_rows<D>(a, s_bad != 0, (int64_t)blockIdx.x * THREADS + tid, (int64_t)gridDim.x * THREADS);
+  if (tid == 0) {
+    if (s_bad && blockIdx.x == 0) atomicOr(a.status, STATUS_KV_RANGE);
+    a.ws.joins[blockIdx.x].pieces = 0;
+  }
+  __syncthreads();
+
+  const uint32_t tmem = s_tmem;
+  // The roles go through the same pieces in the same order, each with its own
+  // count of what it has waited for.  The next piece, false when there is none.
+  auto next_work = [&](int nth, Piece* w) {
+    const bool ok = mbar_wait(work_full + 8 * (nth % WORKS), (nth / WORKS) & 1, err, a.wait_ns);
+    if (!ok) return false;
+    *w = work[nth % WORKS];
+    return w->ok != 0;
+  };
+
+  if (warp >= COPY_WARP) {
+    fewer_registers<64>();
+    if (warp == COPY_WARP) {
+      // ---------------- work and copies ----------------
+      Walk walk;
+      walk.left = 0;
+      if (!idle) walk.begin(a, s_first, s_rem, u1 - u0, lane);
+      int n = 0, nq = 0;  // blocks and Q pairs so far
+      int nth = 0;        // pieces so far
+      bool ok = true, wild = false;
+      Piece w;
+      while (ok && walk.next(a, blockIdx.x, lane, &w)) {
+        if (nth >= WORKS) {  // every role is done with the piece that had the slot
+          const int v = nth - WORKS;
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(work_empty + 8 * (v % WORKS), (v / WORKS) & 1, err, a.wait_ns));
+        }
+        if (!ok) break;
+        const Plan p(a, w);
+        if (lane == 0) {
+          work[nth % WORKS] = w;
+          s_nonfinite[nth % WORKS] = 0;
+          mbar_arrive(work_full + 8 * (nth % WORKS));
+          // the item's last piece: says where the others are
+          const int nb = (p.seen_end - 1) / BN + 1;
+          if (w.part >= 0 && w.b1 == nb) {
+            // this share's first block is the item's block b0, so block 0 lies b0 units before
+            const int c0 = share_of(all, u0 - w.b0, shares);
+            a.ws.joins[blockIdx.x] =
+                PagedJoin{(int)blockIdx.x - c0 + 1, w.r.qb + w.pos0, min(2 * P, w.r.rows - w.pos0), w.head};
+          }
+        }
+        ++nth;
+        // the pages' numbers: lane l has page first + l, and the one 32 later
+        const int per_block = BN >> a.shift, last_page = (p.seen_end - 1) >> a.shift;
+        const int32_t* table = a.table + (int64_t)w.r.slot * a.width;
+        auto number = [&](int page) { return page <= last_page ? table[page] : 0; };
+        int first = (w.b0 * per_block) & ~31;
+        int id = number(first + lane), id_next = number(first + 32 + lane);
+        if (lane == 0) {
+          if (nq > 0) ok = mbar_wait(q_empty, (nq - 1) & 1, err, a.wait_ns);
+          if (ok && !a.stall) {
+            uint32_t bytes = 0;
+            for (int t = 0; t < 2; ++t)
+              if (p.mine[t]) bytes += (uint32_t)(C::CHUNKS * P * G * 128);
+            mbar_expect_tx(q_full, bytes);
+            for (int t = 0; t < 2; ++t)
+              if (p.mine[t])
+                for (int c = 0; c < C::CHUNKS; ++c)
+                  tensor_load(q_smem + t * C::TILE + c * C::Q_CHUNK, &map_q, 64 * c, w.head * G,
+                              w.r.qb + w.pos0 + t * P, q_full);
+          }
+        }
+        ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0) != 0;
+        if (ok) ++nq;
+        const uint32_t page_bytes = (uint32_t)(D * 2) << a.shift;
+        const int page_groups = 1 << (a.shift - 3);
+        for (int i = w.b0; i < w.b1 && ok; ++i) {
+          const int pg = i * per_block, here = min(per_block, last_page - pg + 1);
+          if (pg >= first + 32) {
+            first += 32;
+            id = id_next;
+            id_next = number(first + 32 + lane);
+          }
+          int mine = __shfl_sync(0xFFFFFFFFu, id, (pg - first + lane) & 31);
+          if (lane < here && (mine < 0 || mine >= a.pages)) {
+            wild = true;
+            mine = a.pages;  // past the end: the copy fills in zeros
+          }
+          const int at = (mine * a.heads + w.head) * page_groups;
+          for (int kv = 0; kv < 2 && ok; ++kv) {
+            const int st = n % NST;
+            if (lane == 0) {
+              if (n >= NST) ok = mbar_wait(empty + 8 * st, ((n / NST) - 1) & 1, err, a.wait_ns);
+              if (ok && !a.stall) {
+                mbar_expect_tx(full + 8 * st, (uint32_t)here * page_bytes);
+                if (kv && i >= p.zone) mbar_arrive(hidden + 8 * st);  // tells V's warp, which only waits for these
+              }
+            }
+            ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0) != 0;
+            if (ok && !a.stall && lane < here)
+              tensor_load4(ring + st * C::TILE + lane * page_bytes, kv ? (const void*)&map_v : (const void*)&map_k, 0,
+                           0, 0, at, full + 8 * st);
+            __syncwarp();
+            if (ok) ++n;
+          }
+        }
+      }
+      if (ok) {
+        if (nth >= WORKS) {
+          const int v = nth - WORKS;
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(work_empty + 8 * (v % WORKS), (v / WORKS) & 1, err, a.wait_ns));
+        }
+        if (ok && lane == 0) {
+          work[nth % WORKS].ok = 0;
+          mbar_arrive(work_full + 8 * (nth % WORKS));
+        }
+      }
+      if (__any_sync(0xFFFFFFFFu, wild) && lane == 0) atomicOr(a.status, STATUS_KV_RANGE);
+      // the copies in flight land before the CTA ends, also when another role has given up
+      if (nq > 0) mbar_wait_warp(q_full, (nq - 1) & 1, a.wait_ns);
+      for (int v = max(0, n - NST); v < n; ++v) mbar_wait_warp(full + 8 * (v % NST), (v / NST) & 1, a.wait_ns);
+    } else if (warp == FIX_WARP) {
+      // ---------------- V in masked places: safe to multiply with weights of 0 ----------------
+      int n = 0;
+      uint32_t seen_once = 0;  // parity of each stage's `hidden`
+      bool ok = true;
+      Piece w;
+      for (int nth = 0; ok; ++nth) {
+        if (!__all_sync(0xFFFFFFFFu, next_work(nth, &w))) break;
+        const Plan p(a, w);
+        for (int i = max(p.zone, w.b0); i < w.b1; ++i) {
+          const int v = n + 2 * (i - w.b0) + 1, st = v % NST;
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(hidden + 8 * st, (seen_once >> st) & 1, err, a.wait_ns) &&
+                                           mbar_wait(full + 8 * st, (v / NST) & 1, err, a.wait_ns));
+          seen_once ^= 1u << st;
+          if (!ok) break;
+          // rows [r0, end) some rows see, those after it none; products take keys by 16
+          const int r0 = max(0, p.first_hidden - i * BN), end = min(BN, p.seen_end - i * BN);
+          const int stop = (end + 15) & ~15;
+          uint8_t* vb = smem_p + (ring - smem) + st * C::TILE;
+          constexpr int VPR = C::CHUNKS * 8;  // 16-byte vectors per row
+          auto at = [&](int row, int e) {
+            return reinterpret_cast<uint4*>(vb + (row >> 3) * C::GROUP + (e >> 3) * 1024 + (row & 7) * 128 +
+                                            ((e & 7) ^ (row & 7)) * 16);
+          };
+          const int e = lane % VPR;
+          bool found = false;
+          for (int row = r0 + lane / VPR; row < end; row += 4 * (32 / VPR)) {
+            uint4 x[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int ru = row + u * (32 / VPR);
+              x[u] = ru < end ? *at(ru, e) : make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              if (nonfinite8<T>(x[u])) {
+                found = true;
+                *at(row + u * (32 / VPR), e) =
+                    make_uint4(finite2<T>(x[u].x), finite2<T>(x[u].y), finite2<T>(x[u].z), finite2<T>(x[u].w));
+              }
+            }
+          }
+          for (int row = max(r0, end) + lane / VPR; row < stop; row += 32 / VPR) *at(row, e) = make_uint4(0u, 0u, 0u, 0u);
+          if (found) atomicExch(&s_nonfinite[nth % WORKS], 1);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(fixed + 8 * st);
+        }
+        n += 2 * p.nblocks;
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(work_empty + 8 * (nth % WORKS));
+      }
+    } else {
+      // ---------------- products of a tile ----------------
+      // The whole warp runs the loop and one lane issues, so that what a product is
+      // told is made in uniform registers.
+      const int t = warp - MMA_WARP;
+      constexpr uint32_t ID_S = idesc_f16(BF16, BN, false), ID_O = idesc_f16(BF16, D, true);
+      constexpr uint32_t TILE16 = C::TILE / 16, Q_CHUNK16 = C::Q_CHUNK / 16, GROUP16 = C::GROUP / 16;
+      const uint64_t q_desc = desc_sw128(q_smem, 16, 1024) + t * TILE16;
+      const uint64_t k_desc = desc_sw128(ring, 16, C::GROUP), v_desc = desc_sw128(ring, 1024, C::GROUP);
+      const uint32_t s_col = tmem + t * BN, o_col = tmem + C::O_COL + t * D;
+      const bool one = lane == 0;
+      int n = 0, nq = 0, np = 0, no = 0, nt = 0;  // blocks, Q pairs, weights taken, outputs begun and turns so far
+      uint32_t fixed_once = 0;                    // parity of each stage's `fixed`
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, err, a.wait_ns)) != 0;
+      };
+      auto loaded = [&](int v) { return wait(full + 8 * (v % NST), (v / NST) & 1); };
+      auto give = [&](uint32_t bar) {
+        if (one) mbar_arrive(bar);
+      };
+      // the tiles take turns: left alone they fall into step, and both wait for
+      // products and then both for weights
+      auto my_turn = [&]() { return wait(turn + 8 * t, nt++ & 1); };
+      auto qk = [&](int st) {  // S_t = Q_t K^T
+        const uint64_t kd = k_desc + st * TILE16;
+        if (one) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            mma_ss(s_col, q_desc + ((k >> 2) * Q_CHUNK16 + (k & 3) * 2), kd + ((k >> 2) * 64 + (k & 3) * 2), ID_S,
+                   k > 0);
+          mma_commit(s_full + 8 * t);
+          mma_commit(empty + 8 * st);
+        }
+      };
+      auto pv = [&](int st, int h, int steps, bool first) {  // O_t += P_t V, `steps` times 16 keys of a half
+        const uint64_t v = v_desc + (st * TILE16 + h * (BN / 2 / 8) * GROUP16);
+        const uint32_t p = s_col + h * (BN / 2), more = first ? 0 : 1;
+        if (one) {
+          mma_ts(o_col, p, v, ID_O, more);
+#pragma unroll
+          for (int k = 1; k < BN / 32; ++k)
+            if (k < steps) mma_ts(o_col, p + k * 8, v + k * 2 * GROUP16, ID_O, 1);
+        }
+      };
+      bool ok = true;
+      Piece w;
+      for (int nth = 0;; ++nth) {
+        if (!__all_sync(0xFFFFFFFFu, ok && next_work(nth, &w))) break;
+        w.pos0 = __shfl_sync(0xFFFFFFFFu, w.pos0, 0);
+        w.r.rows = __shfl_sync(0xFFFFFFFFu, w.r.rows, 0);
+        w.r.past = __shfl_sync(0xFFFFFFFFu, w.r.past, 0);
+        w.b0 = __shfl_sync(0xFFFFFFFFu, w.b0, 0);
+        w.b1 = __shfl_sync(0xFFFFFFFFu, w.b1, 0);
+        const Plan p(a, w);
+        const int blocks = t ? p.mine[1] : p.mine[0];
+        ok = wait(q_full, nq & 1) && loaded(n);
+        if (!ok) break;
+        ++nq;
+        tc_fence_after();
+        if (blocks > 0) qk(n % NST);
+        else give(empty + 8 * (n % NST));
+        if (blocks <= 1 && one) mma_commit(q_empty);
+        // blocks that only the other tile has are waited for and given back
+        for (int i = 0; i < p.nblocks; ++i, n += 2) {
+          const int sv = (n + 1) % NST, sk = (n + 2) % NST;
+          ok = loaded(n + 1) && (i + 1 >= p.nblocks || loaded(n + 2));
+          if (ok && w.b0 + i >= p.zone) {
+            ok = wait(fixed + 8 * sv, (fixed_once >> sv) & 1);
+            fixed_once ^= 1u << sv;
+          }
+          if (!ok) break;
+          if (i >= blocks) {
+            ok = my_turn();
+            if (!ok) break;
+            give(turn + 8 * (1 - t));
+            give(empty + 8 * sv);
+            if (i + 1 < p.nblocks) give(empty + 8 * sk);
+            continue;
+          }
+          if (i == 0) {  // the last output of this tile has been read
+            if (no > 0) ok = wait(o_empty + 8 * t, (no - 1) & 1);
+            ++no;
+          }
+          ok = ok && wait(p_full + 16 * t, np & 1) && my_turn();
+          if (!ok) break;
+          tc_fence_after();
+          // keys past the last that is seen are left out, 16 at a time
+          const int steps = min(BN / 16, (p.seen_end - (w.b0 + i) * BN + 15) / 16);
+          pv(sv, 0, steps, i == 0);
+          ok = wait(p_full + 16 * t + 8, np & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (steps > BN / 32) pv(sv, 1, steps - BN / 32, false);
+          ++np;
+          if (i + 1 < blocks) {
+            qk(sk);
+            if (i + 2 == blocks && one) mma_commit(q_empty);  // the tile's last scores
+          } else {
+            if (one) mma_commit(o_full + 8 * t);
+            if (i + 1 < p.nblocks) give(empty + 8 * sk);
+          }
+          if (one) {
+            mbar_arrive(turn + 8 * (1 - t));
+            mma_commit(empty + 8 * sv);
+          }
+        }
+        if (!ok) break;
+        give(work_empty + 8 * (nth % WORKS));
+      }
+      // every product issued is done before tensor memory is freed
+      if (one) {
+        mma_commit(drain);
+        const unsigned long long t0 = globaltimer();
+        while (!mbar_try(drain, 0) && globaltimer() - t0 < a.wait_ns) {}
+      }
+      __syncwarp();
+    }
+  } else {
+    more_registers<104>();
+    // ---------------- softmax ----------------
+    // A thread that gives up stays in the loops and takes part in the tile's
+    // barriers; the vote at the next piece's beginning ends both halves together.
+    constexpr int HN = BN / 2, HD = D / 2;  // columns of S and of O that a thread has
+    const int t = warp >> 3, h = (warp >> 2) & 1;
+    const int r = tid & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_addr = tmem + lanes + t * BN + h * HN;
+    const uint32_t o_addr = tmem + lanes + C::O_COL + t * D + h * HD;
+    const int row_pos = r / G, row_head = r - row_pos * G;
+    const int first_pos = ((warp & 3) * 32) / G;  // of the warp's rows, which are in position order
+    int ns = 0, no = 0;                           // scores and outputs so far
+    bool ok = true;
+    Piece w;
+    for (int nth = 0;; ++nth) {
+      ok = ok && next_work(nth, &w);
+      if (tile_vote(t, !ok)) break;
+      const Plan p(a, w);
+      const int blocks = t ? p.mine[1] : p.mine[0];
+      const int pos = w.pos0 + t * P + row_pos;
+      const bool live = r < P * G && pos < w.r.rows;
+      const bool any_live = __any_sync(0xFFFFFFFFu, live);  // the other warps' rows are padding
+      const int lim = live ? w.r.past + pos : -1;
+      // positions up to here are seen by every live row of the warp
+      const int clear = w.r.past + min(w.pos0 + t * P + first_pos, w.r.rows - 1);
+      // The reference, in units of log2, scaled and less LIFT (-LIFT in far rows, 0 before the first score); the
+      // scaled score that calls for another (-inf: any does); a far row's reference.
+      float m = 0.0f, most = NEG_INF, l = 0.0f, far_ref = NEG_INF;
+      for (int i = 0; i < blocks; ++i, ++ns) {
+        ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(s_full + 8 * t, ns & 1, err, a.wait_ns));
+        const int c0 = (w.b0 + i) * BN + h * HN, seen = lim - c0;  // columns up to `seen` count
+        const bool masked = c0 + HN - 1 > clear;
+        const bool use = ok && any_live;
+        // 32 scores, again from tensor memory for the weights: registers for all 64 would spill
+        auto scores = [&](int c, uint32_t (&s)[32]) {
+          tmem_ld32<0>(s_addr + c, s);
+          tmem_wait_ld();
+          if (masked) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[e] = c + e <= seen ? s[e] : __float_as_uint(NEG_INF);
+          }
+        };
+        float mn = NEG_INF;
+        if (use) {
+          tc_fence_after();
+          float top[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
+#pragma unroll
+          for (int c = 0; c < HN; c += 32) {
+            uint32_t s[32];
+            scores(c, s);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2)
+              top[(e >> 1) & 3] = max3(top[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+          }
+          mn = live ? max3(fmaxf(top[0], top[1]), top[2], top[3]) : NEG_INF;  // Q's rows past the tile hold anything
+        }
+        if (tile_vote(t, i == 0 || mn * a.scale_log2 > most)) {  // a positive scale: checked on the host
+          s_max[t][h][r] = mn;
+          tile_sync(t);
+          const float score = fmaxf(mn, s_max[t][1 - h][r]), top = score * a.scale_log2;
+          const bool was_far = far_ref != NEG_INF, none = most == NEG_INF && !was_far;
+          const bool far =
+              was_far || (fabsf(top) >= FAR && score != NEG_INF && (none || top - LIFT<T> > m));
+          float f;
+          if (far) {
+            const float ref = fmaxf(far_ref, score);
+            f = was_far ? ex2((far_ref - ref) * a.scale_log2) : none ? 0.0f : ex2(m + LIFT<T> - top);
+            far_ref = ref;
+            m = -LIFT<T>;
+            most = NEG_INF;
+          } else {
+            const float nm = none ? top - LIFT<T> : fmaxf(m, top - LIFT<T>);
+            f = none ? 0.0f : ex2(m - nm);
+            m = nm == NEG_INF ? 0.0f : nm;
+            most = nm + (LIFT<T> + GROW);
+          }
+          if (i > 0) {
+            l *= f;
+            if (use) {
+#pragma unroll
+              for (int c = 0; c < HD; c += 16) {
+                uint32_t o[16];
+                tmem_ld16(o_addr + c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st16(o_addr + c, o);
+              }
+              tmem_wait_st();
+              tc_fence_before();
+            }
+            tile_sync(t);  // a half's weights go to all of O: both halves of it are rescaled before
+          }
+          if (__any_sync(0xFFFFFFFFu, far) && use) {
+            const float off = far ? far_ref : 0.0f;
+#pragma unroll 1
+            for (int c = 0; c < HN; c += 16) {
+              uint32_t s[16];
+              tmem_ld16(s_addr + c, s);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) - off);
+              tmem_st16(s_addr + c, s);
+            }
+            tmem_wait_st();
+          }
+        }
+        if (use) {
+          const F2 sc2 = f2(a.scale_log2, a.scale_log2), mm2 = f2(-m, -m);
+          F2 sum[2] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f)};
+#pragma unroll
+          for (int c = 0; c < HN; c += 32) {
+            uint32_t s[32], q[16];
+            scores(c, s);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float2 x = unf2(fma2(f2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), sc2, mm2));
+              const float p0 = ex2(x.x), p1 = ex2(x.y);
+              sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], f2(p0, p1));
+              q[e / 2] = pack2<T>(p0, p1);
+            }
+            tmem_st16(s_addr + c / 2, q);  // over scores that this thread has read
+          }
+          const float2 l2 = unf2(add2(sum[0], sum[1]));
+          l += l2.x + l2.y;
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(p_full + 16 * t + 8 * h);
+      }
+      // ---- O / l to memory, or O and l to scratch ----
+      const bool whole = w.part < 0;
+      float4* ml = a.ws.ml + ((int64_t)(whole ? 0 : w.part) * 2 + t) * BM + r;
+      if (blocks == 0) {
+        if (!whole && live && h == 0) *ml = make_float4(0.0f, NEG_INF, NEG_INF, 0.0f);
+      } else {
+        s_sum[t][h][r] = l;
+        tile_sync(t);
+        l += s_sum[t][1 - h][r];
+        ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(o_full + 8 * t, no & 1, err, a.wait_ns));
+        ++no;
+        if (ok) {
+          tc_fence_after();
+          uint32_t o[HD];
+          tmem_ld32<0>(o_addr, o);
+          if constexpr (D == 128) tmem_ld32<32>(o_addr + 32, o);
+          tmem_wait_ld();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(o_empty + 8 * t);
+          const float inv = whole ? 1.0f / l : 1.0f;
+          const bool extra = s_nonfinite[nth % WORKS] != 0;
+          if (live) {
+            T* dst = static_cast<T*>(a.out) + ((int64_t)(w.r.qb + pos) * a.q_heads + w.head * G + row_head) * D + h * HD;
+            float* part = a.ws.partial + (((int64_t)(whole ? 0 : w.part) * 2 + t) * BM + r) * D + h * HD;
+            if (!whole && h == 0)
+              *ml = make_float4(l, far_ref != NEG_INF ? far_ref * a.scale_log2 : most == NEG_INF ? NEG_INF : m + LIFT<T>,
+                                far_ref, 0.0f);
+#pragma unroll
+            for (int c = 0; c < HD; c += 16) {
+              float x[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(o[c + e]) * inv;
+              if (extra) {  // what was set aside: positions of this piece that the row sees
+                const int j1 = min(lim, w.b1 * BN - 1);
+                for (int j = max(p.first_hidden, w.b0 * BN); j <= j1; ++j) {
+                  const int id = a.table[(int64_t)w.r.slot * a.width + (j >> a.shift)];
+                  if (id < 0 || id >= a.pages) continue;
+                  const T* v = static_cast<const T*>(a.v_pages) +
+                               ((((int64_t)id * a.heads + w.head) << a.shift) + (j & ((1 << a.shift) - 1))) * D + h * HD + c;
+                  for (int e = 0; e < 16; ++e) {
+                    const float f = (float)v[e];
+                    if (!isfinite(f)) x[e] += f;
+                  }
+                }
+              }
+              if (whole) {
+                uint32_t y[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = pack2<T>(x[2 * e], x[2 * e + 1]);
+                store16(dst + c, y, a.wide);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 16; e += 8) {
+                  uint32_t y[8];
+#pragma unroll
+                  for (int f = 0; f < 8; ++f) y[f] = __float_as_uint(x[e + f]);
+                  store16(part + c + e, y, true);
+                }
+              }
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive(work_empty + 8 * (nth % WORKS));
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == MMA_WARP) tmem_dealloc(tmem, TMEM_COLS);
+  if (tid == 0 && s_err) atomicOr(a.status, STATUS_TIMEOUT);
+}
+
+// ---- the pieces of items that were cut, joined ----
+//   out = sum_i f_i O_i / sum_i f_i l_i,  f_i = 2^(reference_i - largest reference)
+// One warp a row; a row's references lie in its lanes, 32 pieces at a time.
+constexpr int JOIN_WARPS = 8;
+
+template <int D, typename T>
+__global__ void __launch_bounds__(32 * JOIN_WARPS) paged_join_kernel(const Args a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 d = __ldcg(reinterpret_cast<const int4*>(a.ws.joins + blockIdx.x));
+  const PagedJoin j{d.x, d.y, d.z, d.w};
+  const int lane = threadIdx.x & 31, G = a.group, P = a.positions;
+  const int rows = j.pieces ? j.rows * G : 0, c0 = (int)blockIdx.x - j.pieces + 1;
+  constexpr int V = D / 32;  // values of a lane
+  for (int i = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5); i < rows; i += gridDim.y * JOIN_WARPS) {
+    // row i of the item: position i / G, in tile 0 or 1
+    const int pos = i / G, t = pos >= P ? 1 : 0, r = (pos - t * P) * G + i % G;
+    auto place = [&](int k) {  // of piece k: the first of an item is its share's last
+      return ((int64_t)(2 * (c0 + k) + (k == 0 ? 1 : 0)) * 2 + t) * BM + r;
+    };
+    float top = NEG_INF, top_far = NEG_INF;
+    for (int k = lane; k < j.pieces; k += 32) {
+      const float4 x = __ldcg(a.ws.ml + place(k));
+      if (x.x != 0.0f) {
+        top = fmaxf(top, x.y);
+        top_far = fmaxf(top_far, x.z);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+      top_far = fmaxf(top_far, __shfl_xor_sync(0xFFFFFFFFu, top_far, o));
+    }
+    float l = 0.0f, o[V] = {};
+    for (int k0 = 0; k0 < j.pieces; k0 += 32) {
+      float f = 0.0f, lk = 0.0f;
+      if (k0 + lane < j.pieces) {
+        const float4 x = __ldcg(a.ws.ml + place(k0 + lane));
+        lk = x.x;
+        // far rows have scores, whose differences keep their bits.  Never 0, so that infinities and NaN stay.
+        f = lk == 0.0f ? 0.0f
+                       : fmaxf(ex2(x.z != NEG_INF && top_far * a.scale_log2 == top ? (x.z - top_far) * a.scale_log2
+                                                                                  : x.y - top),
+                               0x1p-126f);
+      }
+      const int n = min(32, j.pieces - k0);
+      for (int k = 0; k < n; ++k) {
+        const float fk = __shfl_sync(0xFFFFFFFFu, f, k), lkk = __shfl_sync(0xFFFFFFFFu, lk, k);
+        if (fk == 0.0f) continue;
+        l += fk * lkk;
+        const float* p = a.ws.partial + place(k0 + k) * D + lane * V;
+        if constexpr (V == 4) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(p));
+          o[0] += fk * x.x;
+          o[1] += fk * x.y;
+          o[2] += fk * x.z;
+          o[3] += fk * x.w;
+        } else {
+          const float2 x = __ldcg(reinterpret_cast<const float2*>(p));
+          o[0] += fk * x.x;
+          o[1] += fk * x.y;
+        }
+      }
+    }
+    const float inv = 1.0f / l;
+    T* dst = static_cast<T*>(a.out) + ((int64_t)(j.row + pos) * a.q_heads + j.head * G + i % G) * D + lane * V;
+    if constexpr (V == 4)
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv));
+    else
+      *reinterpret_cast<uint32_t*>(dst) = pack2<T>(o[0] * inv, o[1] * inv);
+  }
+}
+
+// ---------------------------------------------------------------- host
+
+// Map of the pages of K or V: eight rows, chunks of a row, groups of eight rows; a box is a page of one head.
+bool make_pages_map(CUtensorMap* map, bool bf16, const void* p, int64_t groups, int D, int page) {
+  const EncodeFn encode = encode_fn();
+  if (!encode) return false;
+  const cuuint64_t dims[4] = {64, 8, (cuuint64_t)(D / 64), (cuuint64_t)groups};
+  const cuuint64_t strides[3] = {(cuuint64_t)D * 2, 128, (cuuint64_t)D * 16};
+  const cuuint32_t box[4] = {64, 8, (cuuint32_t)(D / 64), (cuuint32_t)(page / 8)};
+  const cuuint32_t elem[4] = {1, 1, 1, 1};
+  return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                const_cast<void*>(p), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, typename T>
+int launch_as(const PagedAttn& c, cudaStream_t s) {
+  constexpr bool BF16 = std::is_same<T, __nv_bfloat16>::value;
+  Args a;
+  a.v_pages = c.v_pages;
+  a.out = c.out;
+  a.total = c.total;
+  a.slots = c.slots;
+  a.width = c.width;
+  a.pages = (int)c.pages;
+  a.heads = c.heads;
+  a.q_heads = c.q_heads;
+  a.group = c.q_heads / c.heads;
+  a.positions = BM / a.group;
+  a.shift = c.shift;
+  a.S = c.S;
+  a.wide = (reinterpret_cast<uintptr_t>(c.out) & 31u) == 0;
+  a.scale_log2 = c.scale * 1.44269504088896340736f;
+  a.table = c.table;
+  a.offsets = c.offsets;
+  a.slot = c.slot;
+  a.pos = c.pos;
+  a.ws = c.ws;
+  a.status = c.status;
+  a.wait_ns = wait_limit_ns();
+  a.stall = stall_for_test();
+  CUtensorMap mq, mk, mv;
+  const int64_t groups = (c.pages * c.heads) << (c.shift - 3);
+  if (!make_rows_map(&mq, BF16, c.q, c.total, c.q_heads, D, c.q_strides, a.group, a.positions) ||
+      !make_pages_map(&mk, BF16, c.k_pages, groups, D, 1 << c.shift) ||
+      !make_pages_map(&mv, BF16, c.v_pages, groups, D, 1 << c.shift))
+    return Q4_ERR_INVALID_ARG;
+  static std::atomic<bool> sized[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return Q4_ERR_CUDA;
+  if (!sized[dev].load()) {
+    if (cudaFuncSetAttribute(paged_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM) !=
+        cudaSuccess)
+      return Q4_ERR_CUDA;
+    sized[dev].store(true);
+  }
+  paged_kernel<D, T><<<(unsigned)c.num_sms, THREADS, Cfg<D>::SMEM, s>>>(a, mq, mk, mv);
+  if (cudaGetLastError() != cudaSuccess) return Q4_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)c.num_sms, 8);
+  cfg.blockDim = dim3(32 * JOIN_WARPS);
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, T>, a) == cudaSuccess ? Q4_OK : Q4_ERR_CUDA;
+}
+
+}  // namespace
+
+size_t paged_attn_scratch_bytes(int64_t head_dim, int num_sms, PagedAttnScratch* out, uint8_t* base) {
+  const size_t rows = (size_t)num_sms * 2 * 2 * BM;  // two pieces a share, two tiles each
+  const size_t partial = rows * head_dim * sizeof(float), ml = rows * sizeof(float4);
+  if (out) {
+    out->partial = reinterpret_cast<float*>(base);
+    out->ml = reinterpret_cast<float4*>(base + partial);
+    out->joins = reinterpret_cast<PagedJoin*>(base + partial + ml);
+  }
+  return partial + ml + (size_t)num_sms * sizeof(PagedJoin);
+}
+
+int launch_paged_attention(const PagedAttn& c, cudaStream_t s) {
+  if (c.dtype == Q4_DTYPE_F16)
+    return c.head_dim == 128 ? launch_as<128, __half>(c, s) : launch_as<64, __half>(c, s);
+  return c.head_dim == 128 ? launch_as<128, __nv_bfloat16>(c, s) : launch_as<64, __nv_bfloat16>(c, s);
+}
+
+}  // namespace q4

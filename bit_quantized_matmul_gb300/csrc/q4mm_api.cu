@@ -788,8 +788,10 @@ int q4_device_status(void) {
   if (st) return st;
   v |= na;
   if (v & STATUS_TIMEOUT) return Q4_ERR_TIMEOUT;
-  if (v & ~(STATUS_KV_NONFINITE | STATUS_KV_SCALE)) return Q4_ERR_INVALID_ARG;
-  if (v) return (v & STATUS_KV_NONFINITE) ? Q4_ERR_NONFINITE : Q4_ERR_RANGE;
+  if (v & ~(STATUS_KV_NONFINITE | STATUS_KV_SCALE | STATUS_PAGES)) return Q4_ERR_INVALID_ARG;
+  if (v & STATUS_KV_NONFINITE) return Q4_ERR_NONFINITE;
+  if (v & STATUS_KV_SCALE) return Q4_ERR_RANGE;
+  if (v) return Q4_ERR_NOMEM;
   return Q4_OK;
 }
 

@@ -89,6 +89,8 @@ constexpr unsigned STATUS_KV_RANGE = 4u;  // a cache or prompt request was out o
 constexpr unsigned STATUS_KV_NONFINITE = 8u;  // q4_kvq_append met a NaN or an infinity (stored as NaN)
 constexpr unsigned STATUS_KV_SCALE = 16u;     // a block's scale passed binary16 (stored as NaN)
 
+constexpr unsigned STATUS_PAGES = 32u;        // q4_paged_reserve ran out of pages
+
 // Returns Q4_OK and fills *ws with at least the requested capacities.
 int workspace_get(int device, size_t partial_bytes, size_t xop_bytes, Workspace* ws, size_t gu_bytes = 0,
                   size_t xpre_bytes = 0, size_t attn_bytes = 0);
@@ -214,6 +216,56 @@ struct PromptAttn {
   int num_sms;
 };
 int launch_prompt_attention(const PromptAttn& c, cudaStream_t s);
+
+// ---- paged 16-bit KV cache ----
+constexpr int PAGED_REQUESTS = 8192;  // requests and slots of one reserve call: they lie in shared memory
+constexpr int PAGED_SLOTS = 65536;
+struct PagedReserve {
+  int32_t *table, *held, *free_list, *free_count;
+  int64_t slots, width, pages, total;
+  int shift, S;  // a page is 1 << shift positions
+  const int32_t *offsets, *slot, *pos;
+  int32_t *slot_map, *new_len;
+  unsigned* status;
+};
+int launch_paged_reserve(const PagedReserve& c, cudaStream_t s);
+struct PagedAppend {
+  void *k_pages, *v_pages;
+  const void *k_new, *v_new;
+  int cache_dtype, dtype;
+  int64_t pages, heads, total;
+  int head_dim, shift;
+  int64_t k_strides[2], v_strides[2];  // row, head; in elements
+  const int32_t* slot_map;
+  unsigned* status;
+  int num_sms;
+};
+int launch_paged_append(const PagedAppend& c, cudaStream_t s);
+// An item whose last piece a CTA had: how many CTAs up to and with it had one, its rows.
+struct alignas(16) PagedJoin {
+  int pieces, row, rows, head;
+};
+struct PagedAttnScratch {
+  float* partial;   // [pieces][2 tiles][128 rows][head_dim]
+  float4* ml;       // [pieces][2][128]: sum, reference (log2), a far row's reference
+  PagedJoin* joins;
+};
+// Bytes of the attention scratch (the same for every call of a head_dim); with `out`, its parts at `base`.
+size_t paged_attn_scratch_bytes(int64_t head_dim, int num_sms, PagedAttnScratch* out, uint8_t* base);
+struct PagedAttn {
+  const void *k_pages, *v_pages, *q;
+  void* out;
+  int dtype;
+  int64_t pages, slots, width, total;
+  int heads, q_heads, head_dim, shift, S;
+  int64_t q_strides[2];
+  float scale;
+  const int32_t *table, *offsets, *slot, *pos;
+  PagedAttnScratch ws;
+  unsigned* status;
+  int num_sms;
+};
+int launch_paged_attention(const PagedAttn& c, cudaStream_t s);
 
 // The scratch of the current device, locked: other calls' launches wait until
 // it goes out of scope, so the pointers stay valid while this call launches.

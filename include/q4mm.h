@@ -79,7 +79,7 @@ extern "C" {
 #define Q4_ERR_RANGE 5        /* a block scale does not fit binary16 (|d| >= 65520) */
 #define Q4_ERR_CUDA 6         /* a CUDA runtime error (launch failure, sticky fault) */
 #define Q4_ERR_TIMEOUT 7      /* a bounded device-side wait ran out */
-#define Q4_ERR_NOMEM 8        /* device allocation failed */
+#define Q4_ERR_NOMEM 8        /* device allocation failed; or q4_paged_reserve ran out of pages */
 #define Q4_ERR_UNSUPPORTED 9  /* the device is not sm_103 / requested path unavailable */
 
 /* ---- flags for the _ex entry points ---- */
@@ -453,6 +453,95 @@ Q4_API int q4_prompt_attention(const void* q, const void* k, const void* v, void
                                const int64_t* v_strides, float scale, int causal,
                                const int32_t* q_offsets, const int32_t* k_offsets, int64_t S,
                                int64_t q_total, int64_t k_total, cudaStream_t stream);
+
+/* ---- paged 16-bit KV cache --------------------------------------------------
+ *
+ * K and V rows in fp16 or bf16, in pages of page_size positions (16, 32, 64 or
+ * 128) that requests are given as they grow.  A layer's cache is two device
+ * buffers, K and V, [pages][heads][page_size][head_dim] each, contiguous,
+ * caller-owned, 16-byte aligned; head_dim 64 or 128.  Position p of a slot lies in
+ * row p % page_size of page table[slot][p / page_size].  One block table serves
+ * all layers.  Nothing has to be initialised: rows that no position of a
+ * request has reached may hold anything, NaN included.
+ *
+ * offsets, slot, pos describe the step's packed rows as for the 4-bit cache
+ * (device, int32, offsets non-decreasing); S >= 1 where there are rows.  What a
+ * call writes overlaps nothing else that it is given (INVALID_ARG), but for an
+ * attention's out that is q itself, packed.  Another page_size or head_dim: SHAPE.
+ * pages, width in positions, S and 2 * total up to 2^31 - 2^17, and so is
+ * (pages + 1) * heads * page_size / 8 (INVALID_ARG). */
+
+/* Block tables and slot map of a step, from the requests' lengths, on the GPU.
+ * After it slot[s] has ceil((pos[s] + rows of s) / page_size) pages: surplus ones (of
+ * requests that ended, pos = 0 without rows, or were cut back) return to the
+ * free list, and a request that grows past its last page is given others.
+ *   table       device, int32 [slots, width]: each slot's pages, in order; entries
+ *               of pages that went back become -1.
+ *   held        device, int32 [slots]: the pages that each slot has (0 at first).
+ *   free_list   device, int32 [pages]: the pages that nobody has are its first
+ *               *free_count entries (at first all of 0 .. pages - 1, in any order).
+ *   free_count  device, int32 [1].
+ *   slot_map    device, int32 [total] out, fully overwritten: page * page_size +
+ *               row in the page of each packed row; -1 for rows of no request
+ *               and of refused ones.
+ *   new_len     device, int32 [S] out: pos + rows, or -1 for a refused request.
+ * All surplus pages return first, in the requests' order, each request's by
+ * position, to the end of the list; then the requests take theirs from the end, in order.
+ * From the first request on for which pages run out, requests that need
+ * some are refused.  So the same call on the same state gives the same tables.
+ * Refused, with nothing of theirs changed: such requests (q4_device_status then
+ * reports NOMEM), and (INVALID_ARG) requests whose slot is out of range or in two
+ * requests of the call, whose positions pass width * page_size, or that begin
+ * past the pages their slot has; all of them where offsets decrease or pass total, or
+ * the pool holds more pages than there are.
+ * S at most 8192, slots at most 65536 (SHAPE).  Asynchronous on stream. */
+Q4_API int q4_paged_reserve(int32_t* table, int32_t* held, int32_t* free_list, int32_t* free_count,
+                            int64_t slots, int64_t width, int64_t pages, int64_t page_size,
+                            const int32_t* offsets, const int32_t* slot, const int32_t* pos, int64_t S,
+                            int64_t total, int32_t* slot_map, int32_t* new_len, cudaStream_t stream);
+
+/* The step's new K and V rows into the pages: row t to place slot_map[t] (as
+ * q4_paged_reserve puts it out; -1: not cached).
+ *   cache_dtype   F16 or BF16.
+ *   k_new, v_new  device, of dtype: cache_dtype, or F32, rounded to nearest; element
+ *                 (t, h, d) at t*strides[0] + h*strides[1] + d (host arrays of 2
+ *                 strides, in elements).
+ * No place is in slot_map twice.  A place out of range is not written, and
+ * q4_device_status reports INVALID_ARG.  total = 0: a no-op.  Asynchronous on
+ * stream. */
+Q4_API int q4_paged_append(void* k_pages, void* v_pages, int cache_dtype, const void* k_new, const void* v_new,
+                           int dtype, int64_t pages, int64_t heads, int64_t head_dim, int64_t page_size,
+                           const int64_t* k_strides, const int64_t* v_strides, const int32_t* slot_map,
+                           int64_t total, cudaStream_t stream);
+
+/* Attention of the step's query rows over the pages (its own rows already
+ * appended), on the tensor cores: row j of request s sees positions 0 .. pos[s] + j
+ * of its slot,
+ *   out[t, hq] = sum_p softmax_p(scale * q[t, hq] . K[p]) V[p]
+ * with key/value head hq / (q_heads / heads); scale is positive.  One call takes single
+ * tokens, drafts and chunks of prompts together.
+ *   q      device, dtype (F16 or BF16, the cache's), strides as in append;
+ *          q_heads a multiple of heads, at most 128 for each (SHAPE).
+ *   out    device, dtype [total, q_heads, head_dim], fully overwritten; rows of
+ *          no request get zeros.
+ *   table  device, int32 [slots, width].
+ * Weights are rounded to dtype before the product with V (F16: a weight below 2^-21
+ * of the row's largest to 2^-32 of that); sums are held in fp32.  Rows of K and V
+ * that a row does not see, NaN included, do not reach its results.
+ * The lengths are read on the device only: a launch of a fixed number of CTAs
+ * divides the work evenly, and a request is divided between them where
+ * that falls, so the last bits of its rows depend on the call's other
+ * requests; the same call gives the same bits.  A request that is out of range (its
+ * slot, its rows, or positions past width * page_size) gets zeros, a page
+ * number out of range reads as zeros, and q4_device_status then reports
+ * INVALID_ARG.  Uses the library's scratch: order calls on one stream.  The first
+ * call of a head_dim may allocate some (about 62 MB at 128).  Needs sm_103
+ * (UNSUPPORTED). */
+Q4_API int q4_paged_attention(const void* k_pages, const void* v_pages, const void* q, void* out, int dtype,
+                              int64_t pages, int64_t heads, int64_t q_heads, int64_t head_dim, int64_t page_size,
+                              const int64_t* q_strides, float scale, const int32_t* table, int64_t slots,
+                              int64_t width, const int32_t* offsets, const int32_t* slot, const int32_t* pos,
+                              int64_t S, int64_t total, cudaStream_t stream);
 
 /* The kernel path (Q4MM_PATH_*) a call with these arguments would take, or a
  * negative status. */
