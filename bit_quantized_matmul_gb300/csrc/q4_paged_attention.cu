@@ -11,9 +11,11 @@ namespace {
 
 constexpr int SOFTMAX_WARPS = 16;
 constexpr int COPY_WARP = 16, MMA_WARP = 17, FIX_WARP = 19;  // and MMA_WARP + 1
+constexpr int LIGHT_WARPS = 8;  // warps 0-7
 constexpr int WORKS = 2;                                     // the piece that is copied and the one before
 constexpr int THREADS = 640;
 constexpr int TMEM_COLS = 512;
+constexpr int LIGHT = 8;      // rows (positions times heads of a group) of a request that needs no tiles
 constexpr int END_UNITS = 1;  // what an item costs beside its blocks, in blocks
 
 template <int D>
@@ -24,7 +26,7 @@ struct Cfg {
   static constexpr int GROUP = CHUNKS * 1024;        // K, V: eight keys, chunk by chunk
   static constexpr int STAGES = D == 128 ? 4 : 8;    // K, V blocks in the ring (even: K and V alternate)
   static constexpr int BAR_OFF = (2 + STAGES) * TILE;
-  static constexpr int SMEM = BAR_OFF + 512 + 1024;  // + alignment slack
+  static constexpr int SMEM = BAR_OFF + 768 + 1024;  // + alignment slack
   static constexpr int O_COL = 2 * BN;               // S0, S1, then O0, O1
 };
 
@@ -92,11 +94,13 @@ struct Piece {
   int head, pos0;  // first row of tile 0 in the request
   Request r;
   int b0, b1;
+  int n;     // blocks (K and V) of the pieces before it
   int part;  // where its sums go: -1: the whole item, straight to the output
 };
 
 // What the roles derive from a piece.
 struct Plan {
+  bool light;        // few rows: no tiles
   int mine[2];       // the piece's blocks that each tile sees
   int nblocks;       // of the piece
   int first_hidden;  // the first position that some row of the pair does not see
@@ -110,6 +114,8 @@ struct Plan {
       const int blocks = p0 < w.r.rows ? (w.r.past + min(p0 + a.positions, w.r.rows) - 1) / BN + 1 : 0;
       mine[t] = max(0, min(blocks, w.b1) - w.b0);
     }
+    light = w.r.rows * a.group <= LIGHT;
+    if (light) mine[0] = mine[1] = 0;
     seen_end = w.r.past + min(w.pos0 + 2 * a.positions, w.r.rows);
     first_hidden = w.r.past + w.pos0 + 1;
     zone = first_hidden / BN;
@@ -226,6 +232,54 @@ struct Walk {
   }
 };
 
+// The largest reference (log2) of sums that are joined, a sum being (l, reference, a
+// far row's score); sums of nothing have l = 0.  Far rows have scores, whose differences keep
+// their bits.  A factor is never 0, so that infinities and NaN stay.
+struct Reference {
+  float ref = NEG_INF, far = NEG_INF;
+  __device__ __forceinline__ void take(float l, float r, float f) {
+    if (l != 0.0f) {
+      ref = fmaxf(ref, r);
+      far = fmaxf(far, f);
+    }
+  }
+  __device__ __forceinline__ bool is_far(float scale_log2) const { return far * scale_log2 == ref; }
+  __device__ __forceinline__ float factor(float l, float r, float f, float scale_log2) const {
+    if (l == 0.0f) return 0.0f;
+    return fmaxf(ex2(f != NEG_INF && is_far(scale_log2) ? (f - far) * scale_log2 : r - ref), 0x1p-126f);
+  }
+};
+
+// ---- small products, for light rows ----
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+template <typename T>
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (std::is_same<T, __half>::value)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
 template <int D, typename T>
 __global__ void __launch_bounds__(THREADS, 1)
     paged_kernel(const Args a, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -250,6 +304,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t full = drain + 8, empty = full + 8 * NST, hidden = empty + 8 * NST, fixed = hidden + 8 * NST;
   const uint32_t s_full = fixed + 8 * NST, p_full = s_full + 16, o_full = p_full + 32, o_empty = o_full + 16;
   const uint32_t turn = o_empty + 16, work_full = turn + 16, work_empty = work_full + 8 * WORKS;
+  const uint32_t used = work_empty + 8 * WORKS, q_used = used + 8 * NST;
   volatile int* err = &s_err;
   if (tid == 0) {
     mbar_init(q_full, 1);
@@ -260,6 +315,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(empty + 8 * i, 2);
       mbar_init(hidden + 8 * i, 1);
       mbar_init(fixed + 8 * i, 1);
+      mbar_init(used + 8 * i, LIGHT_WARPS);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(s_full + 8 * t, 1);
@@ -274,6 +330,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(work_empty + 8 * i, SOFTMAX_WARPS + 3);  // and the products' and V's warps
       s_nonfinite[i] = 0;
     }
+    mbar_init(q_used, LIGHT_WARPS);
     mbar_arrive(turn);  // tile 0 begins
     s_err = 0;
     s_bad = 0;
@@ -354,6 +411,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         if (!ok) break;
         const Plan p(a, w);
+        w.n = n;
         if (lane == 0) {
           work[nth % WORKS] = w;
           s_nonfinite[nth % WORKS] = 0;
@@ -379,10 +437,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (ok && !a.stall) {
             uint32_t bytes = 0;
             for (int t = 0; t < 2; ++t)
-              if (p.mine[t]) bytes += (uint32_t)(C::CHUNKS * P * G * 128);
+              if (p.mine[t] || (p.light && t == 0)) bytes += (uint32_t)(C::CHUNKS * P * G * 128);
             mbar_expect_tx(q_full, bytes);
             for (int t = 0; t < 2; ++t)
-              if (p.mine[t])
+              if (p.mine[t] || (p.light && t == 0))
                 for (int c = 0; c < C::CHUNKS; ++c)
                   tensor_load(q_smem + t * C::TILE + c * C::Q_CHUNK, &map_q, 64 * c, w.head * G,
                               w.r.qb + w.pos0 + t * P, q_full);
@@ -439,22 +497,42 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int v = max(0, n - NST); v < n; ++v) mbar_wait_warp(full + 8 * (v % NST), (v / NST) & 1, a.wait_ns);
     } else if (warp == FIX_WARP) {
       // ---------------- V in masked places: safe to multiply with weights of 0 ----------------
-      int n = 0;
-      uint32_t seen_once = 0;  // parity of each stage's `hidden`
-      bool ok = true;
+      uint32_t seen_once = 0, used_once = 0;  // parities of each stage's `hidden` and `used`
+      int nl = 0;                             // light pieces so far
+      bool ok = true, tiles_before = false;
       Piece w;
       for (int nth = 0; ok; ++nth) {
         if (!__all_sync(0xFFFFFFFFu, next_work(nth, &w))) break;
         const Plan p(a, w);
-        for (int i = max(p.zone, w.b0); i < w.b1; ++i) {
+        const int n = w.n;
+        if (p.light && tiles_before)  // as for the light rows' warps
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(work_empty + 8 * ((nth - 1) % WORKS), ((nth - 1) / WORKS) & 1, err,
+                                                 a.wait_ns));
+        tiles_before = !p.light;
+        // of light rows, gives back what their warps have read
+        auto give_back = [&](int v) {
+          const int st = v % NST;
+          ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(full + 8 * st, (v / NST) & 1, err, a.wait_ns) &&
+                                           mbar_wait(used + 8 * st, (used_once >> st) & 1, err, a.wait_ns));
+          used_once ^= 1u << st;
+          if (ok && lane == 0) mbar_arrive_n(empty + 8 * st, 2);
+        };
+        for (int i = p.light ? w.b0 : max(p.zone, w.b0); ok && i < w.b1; ++i) {
           const int v = n + 2 * (i - w.b0) + 1, st = v % NST;
+          if (p.light) {
+            give_back(v - 1);
+            if (i < p.zone) {
+              give_back(v);
+              continue;
+            }
+          }
+          if (!ok) break;
           ok = __all_sync(0xFFFFFFFFu, mbar_wait(hidden + 8 * st, (seen_once >> st) & 1, err, a.wait_ns) &&
                                            mbar_wait(full + 8 * st, (v / NST) & 1, err, a.wait_ns));
           seen_once ^= 1u << st;
           if (!ok) break;
-          // rows [r0, end) some rows see, those after it none; products take keys by 16
+          // rows [r0, end) some rows see, those after it none
           const int r0 = max(0, p.first_hidden - i * BN), end = min(BN, p.seen_end - i * BN);
-          const int stop = (end + 15) & ~15;
           uint8_t* vb = smem_p + (ring - smem) + st * C::TILE;
           constexpr int VPR = C::CHUNKS * 8;  // 16-byte vectors per row
           auto at = [&](int row, int e) {
@@ -479,13 +557,19 @@ __global__ void __launch_bounds__(THREADS, 1)
               }
             }
           }
+          // (light rows' warps take keys by 16, products whole blocks)
+          const int stop = p.light ? (end + 15) & ~15 : BN;
           for (int row = max(r0, end) + lane / VPR; row < stop; row += 32 / VPR) *at(row, e) = make_uint4(0u, 0u, 0u, 0u);
           if (found) atomicExch(&s_nonfinite[nth % WORKS], 1);
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) mbar_arrive(fixed + 8 * st);
+          if (p.light) give_back(v);
         }
-        n += 2 * p.nblocks;
+        if (ok && p.light) {
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(q_used, nl++ & 1, err, a.wait_ns));
+          if (ok && lane == 0) mbar_arrive_n(q_empty, 2);
+        }
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(work_empty + 8 * (nth % WORKS));
       }
@@ -500,8 +584,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint64_t k_desc = desc_sw128(ring, 16, C::GROUP), v_desc = desc_sw128(ring, 1024, C::GROUP);
       const uint32_t s_col = tmem + t * BN, o_col = tmem + C::O_COL + t * D;
       const bool one = lane == 0;
-      int n = 0, nq = 0, np = 0, no = 0, nt = 0;  // blocks, Q pairs, weights taken, outputs begun and turns so far
+      int np = 0, no = 0, nt = 0;                 // weights taken, outputs begun and turns so far
       uint32_t fixed_once = 0;                    // parity of each stage's `fixed`
+      bool light_before = false;                  // the piece before had no tiles
       auto wait = [&](uint32_t bar, uint32_t parity) {
         return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, err, a.wait_ns)) != 0;
       };
@@ -523,14 +608,13 @@ __global__ void __launch_bounds__(THREADS, 1)
           mma_commit(empty + 8 * st);
         }
       };
-      auto pv = [&](int st, int h, int steps, bool first) {  // O_t += P_t V, `steps` times 16 keys of a half
+      auto pv = [&](int st, int h, bool first) {  // O_t += P_t V, a half of the keys
         const uint64_t v = v_desc + (st * TILE16 + h * (BN / 2 / 8) * GROUP16);
         const uint32_t p = s_col + h * (BN / 2), more = first ? 0 : 1;
         if (one) {
           mma_ts(o_col, p, v, ID_O, more);
 #pragma unroll
-          for (int k = 1; k < BN / 32; ++k)
-            if (k < steps) mma_ts(o_col, p + k * 8, v + k * 2 * GROUP16, ID_O, 1);
+          for (int k = 1; k < BN / 32; ++k) mma_ts(o_col, p + k * 8, v + k * 2 * GROUP16, ID_O, 1);
         }
       };
       bool ok = true;
@@ -542,11 +626,21 @@ __global__ void __launch_bounds__(THREADS, 1)
         w.r.past = __shfl_sync(0xFFFFFFFFu, w.r.past, 0);
         w.b0 = __shfl_sync(0xFFFFFFFFu, w.b0, 0);
         w.b1 = __shfl_sync(0xFFFFFFFFu, w.b1, 0);
+        int n = __shfl_sync(0xFFFFFFFFu, w.n, 0);  // blocks so far
         const Plan p(a, w);
         const int blocks = t ? p.mine[1] : p.mine[0];
-        ok = wait(q_full, nq & 1) && loaded(n);
+        if (p.light) {
+          for (int i = max(p.zone, w.b0); i < w.b1; ++i) fixed_once ^= 1u << ((n + 2 * (i - w.b0) + 1) % NST);
+          give(work_empty + 8 * (nth % WORKS));
+          light_before = true;
+          continue;
+        }
+        if (light_before) {  // its copies have all been taken up: no barrier is two phases from where this warp believes it
+          ok = wait(work_empty + 8 * ((nth - 1) % WORKS), ((nth - 1) / WORKS) & 1);
+          light_before = false;
+        }
+        ok = ok && wait(q_full, nth & 1) && loaded(n);
         if (!ok) break;
-        ++nq;
         tc_fence_after();
         if (blocks > 0) qk(n % NST);
         else give(empty + 8 * (n % NST));
@@ -575,13 +669,11 @@ __global__ void __launch_bounds__(THREADS, 1)
           ok = ok && wait(p_full + 16 * t, np & 1) && my_turn();
           if (!ok) break;
           tc_fence_after();
-          // keys past the last that is seen are left out, 16 at a time
-          const int steps = min(BN / 16, (p.seen_end - (w.b0 + i) * BN + 15) / 16);
-          pv(sv, 0, steps, i == 0);
+          pv(sv, 0, i == 0);
           ok = wait(p_full + 16 * t + 8, np & 1);
           if (!ok) break;
           tc_fence_after();
-          if (steps > BN / 32) pv(sv, 1, steps - BN / 32, false);
+          pv(sv, 1, false);
           ++np;
           if (i + 1 < blocks) {
             qk(sk);
@@ -621,33 +713,231 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int first_pos = ((warp & 3) * 32) / G;  // of the warp's rows, which are in position order
     int ns = 0, no = 0;                           // scores and outputs so far
     bool ok = true;
-    Piece w;
-    for (int nth = 0;; ++nth) {
-      ok = ok && next_work(nth, &w);
-      if (tile_vote(t, !ok)) break;
+    // What the loop over a piece's blocks needs of it, and no more: registers for the whole of it would spill.
+    struct View {
+      int blocks;        // that the tile sees
+      int seen, clear;   // the last column of its first block that the row sees; that all of the warp's live rows see
+      bool live, any_live;
+    };
+    auto view = [&](const Piece& w) {
       const Plan p(a, w);
-      const int blocks = t ? p.mine[1] : p.mine[0];
-      const int pos = w.pos0 + t * P + row_pos;
-      const bool live = r < P * G && pos < w.r.rows;
-      const bool any_live = __any_sync(0xFFFFFFFFu, live);  // the other warps' rows are padding
-      const int lim = live ? w.r.past + pos : -1;
-      // positions up to here are seen by every live row of the warp
-      const int clear = w.r.past + min(w.pos0 + t * P + first_pos, w.r.rows - 1);
+      const int tile_pos = w.pos0 + t * P, c0 = w.b0 * BN + h * HN;
+      View v;
+      v.blocks = t ? p.mine[1] : p.mine[0];
+      v.live = r < P * G && tile_pos + row_pos < w.r.rows;
+      v.any_live = __any_sync(0xFFFFFFFFu, v.live);  // the other warps' rows are padding
+      v.seen = (v.live ? w.r.past + tile_pos + row_pos : -1) - c0;
+      v.clear = w.r.past + min(tile_pos + first_pos, w.r.rows - 1) - c0;
+      return v;
+    };
+    // What was set aside of V: positions of a piece that the row sees, N columns from col.
+    auto set_aside = [&](const Piece& w, int first_hidden, int lim, int col, float* x, int N) {
+      const int j1 = min(lim, w.b1 * BN - 1);
+      for (int j = max(first_hidden, w.b0 * BN); j <= j1; ++j) {
+        const int id = a.table[(int64_t)w.r.slot * a.width + (j >> a.shift)];
+        if (id < 0 || id >= a.pages) continue;
+        const T* v = static_cast<const T*>(a.v_pages) +
+                     ((((int64_t)id * a.heads + w.head) << a.shift) + (j & ((1 << a.shift) - 1))) * D + col;
+        for (int e = 0; e < N; ++e) {
+          const float f = (float)v[e];
+          if (!isfinite(f)) x[e] += f;
+        }
+      }
+    };
+    // Light rows (at most eight), on warps 0-7.  Each has 16 keys of every block, and sums of its own over
+    // them: S = K Q^T and O = V^T P^T in 16 x 8 products, keys and then values along their 16 rows.
+    uint32_t fixed_once = 0;  // parity of each stage's `fixed`
+    auto light_piece = [&](const Piece& w, const Plan& p, int nth) {
+      const int g = lane >> 2, tq = lane & 3;
+      ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(q_full, nth & 1, err, a.wait_ns));
+      uint32_t q[D / 32][4];  // fragments of Q, 32 values each
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        const int vec = 4 * k + (lane >> 3);
+        ldsm4(q_smem + (vec >> 3) * C::Q_CHUNK + (lane & 7) * 128 + (((vec & 7) ^ (lane & 7)) << 4), q[k]);
+      }
+      // rows 2 tq and 2 tq + 1: last position seen, reference (a score), the lane's share of the sum
+      const int live_rows = w.r.rows * G;
+      const int lim0 = 2 * tq < live_rows ? w.r.past + 2 * tq / G : -1;
+      const int lim1 = 2 * tq + 1 < live_rows ? w.r.past + (2 * tq + 1) / G : -1;
+      float ref0 = NEG_INF, ref1 = NEG_INF, l0 = 0.0f, l1 = 0.0f, o[D / 16][4] = {};
+      const uint32_t k_at = (2 * warp + ((lane >> 3) & 1)) * C::GROUP + (lane & 7) * 128;
+      const uint32_t v_at = (2 * warp + (lane >> 4)) * C::GROUP + (lane & 7) * 128;
+      int n = w.n;
+      for (int i = w.b0; i < w.b1; ++i, n += 2) {
+        const int sk = n % NST, sv = (n + 1) % NST, key = i * BN + warp * 16 + g;
+        const bool some = i * BN + warp * 16 < p.seen_end;  // of the warp's keys
+        ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(full + 8 * sk, (n / NST) & 1, err, a.wait_ns));
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (ok && some) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const int vec = 2 * k + (lane >> 4);
+            uint32_t x[4];
+            ldsm4(ring + sk * C::TILE + k_at + (vec >> 3) * 1024 + (((vec & 7) ^ (lane & 7)) << 4), x);
+            mma16<T>(s, x, q[k / 2][(k & 1) * 2], q[k / 2][(k & 1) * 2 + 1]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(used + 8 * sk);
+        uint32_t p0 = 0, p1 = 0;
+        if (ok && some) {
+          if (key > lim0) s[0] = NEG_INF;
+          if (key > lim1) s[1] = NEG_INF;
+          if (key + 8 > lim0) s[2] = NEG_INF;
+          if (key + 8 > lim1) s[3] = NEG_INF;
+          float m0 = fmaxf(s[0], s[2]), m1 = fmaxf(s[1], s[3]);
+#pragma unroll
+          for (int d = 4; d < 32; d *= 2) {
+            m0 = fmaxf(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, d));
+            m1 = fmaxf(m1, __shfl_xor_sync(0xFFFFFFFFu, m1, d));
+          }
+          // a first score, or one that passes the reference by more than 2^GROW
+          const bool more0 = m0 > ref0 && !((m0 - ref0) * a.scale_log2 <= GROW);
+          const bool more1 = m1 > ref1 && !((m1 - ref1) * a.scale_log2 <= GROW);
+          if (__any_sync(0xFFFFFFFFu, more0 || more1)) {
+            const float f0 = more0 ? ex2((ref0 - m0) * a.scale_log2) : 1.0f;
+            const float f1 = more1 ? ex2((ref1 - m1) * a.scale_log2) : 1.0f;
+            ref0 = more0 ? m0 : ref0;
+            ref1 = more1 ? m1 : ref1;
+            l0 *= f0;
+            l1 *= f1;
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+              o[d][0] *= f0;
+              o[d][1] *= f1;
+              o[d][2] *= f0;
+              o[d][3] *= f1;
+            }
+          }
+          // differences of scores keep their bits, however far from zero the scores are
+          const float r0 = ref0 == NEG_INF ? 0.0f : ref0, r1 = ref1 == NEG_INF ? 0.0f : ref1;
+          const float w0 = ex2(fmaf(s[0] - r0, a.scale_log2, LIFT<T>)), w1 = ex2(fmaf(s[1] - r1, a.scale_log2, LIFT<T>));
+          const float w2 = ex2(fmaf(s[2] - r0, a.scale_log2, LIFT<T>)), w3 = ex2(fmaf(s[3] - r1, a.scale_log2, LIFT<T>));
+          l0 += w0 + w2;
+          l1 += w1 + w3;
+          p0 = transpose8(pack2<T>(w0, w1));
+          p1 = transpose8(pack2<T>(w2, w3));
+        }
+        ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(full + 8 * sv, ((n + 1) / NST) & 1, err, a.wait_ns));
+        if (i >= p.zone) {
+          ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(fixed + 8 * sv, (fixed_once >> sv) & 1, err, a.wait_ns));
+          fixed_once ^= 1u << sv;
+        }
+        if (ok && some) {
+#pragma unroll
+          for (int d = 0; d < D / 16; ++d) {
+            const int vec = 2 * d + ((lane >> 3) & 1);
+            uint32_t x[4];
+            ldsm4_t(ring + sv * C::TILE + v_at + (vec >> 3) * 1024 + (((vec & 7) ^ (lane & 7)) << 4), x);
+            mma16<T>(o[d], x, p0, p1);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(used + 8 * sv);
+      }
+      // the warps' sums, joined through Q's place
+#pragma unroll
+      for (int d = 4; d < 32; d *= 2) {
+        l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, d);
+        l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, d);
+      }
+      tile_sync(0);
+      float* const sums = reinterpret_cast<float*>(smem_p);  // [warp][8 rows][D], columns turned so that banks differ
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d) {
+        float* row = sums + (warp * 8 + 2 * tq) * D;
+        row[(d * 16 + g) ^ (tq * 8)] = o[d][0];
+        row[D + ((d * 16 + g) ^ (tq * 8))] = o[d][1];
+        row[(d * 16 + g + 8) ^ (tq * 8)] = o[d][2];
+        row[D + ((d * 16 + g + 8) ^ (tq * 8))] = o[d][3];
+      }
+      if (g == 0) {
+        s_max[0][0][warp * 8 + 2 * tq] = ref0;
+        s_max[0][0][warp * 8 + 2 * tq + 1] = ref1;
+        s_sum[0][0][warp * 8 + 2 * tq] = l0;
+        s_sum[0][0][warp * 8 + 2 * tq + 1] = l1;
+      }
+      tile_sync(0);
+      const int row = tid / (D / 4), col = tid % (D / 4) * 4;
+      if (ok && row < live_rows) {
+        Reference top;
+#pragma unroll
+        for (int i = 0; i < LIGHT_WARPS; ++i) {
+          const float ref = s_max[0][0][i * 8 + row];
+          top.take(s_sum[0][0][i * 8 + row], ref * a.scale_log2, ref);
+        }
+        float l = 0.0f, x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < LIGHT_WARPS; ++i) {
+          const float ref = s_max[0][0][i * 8 + row], li = s_sum[0][0][i * 8 + row];
+          const float f = top.factor(li, ref * a.scale_log2, ref, a.scale_log2);
+          if (f == 0.0f) continue;
+          l += f * li;
+          const float4 y = *reinterpret_cast<const float4*>(sums + (i * 8 + row) * D + (col ^ (((row >> 1) & 3) * 8)));
+          x[0] += f * y.x;
+          x[1] += f * y.y;
+          x[2] += f * y.z;
+          x[3] += f * y.w;
+        }
+        const bool whole = w.part < 0;
+        const float inv = whole ? 1.0f / l : 1.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] *= inv;
+        const int pos = row / G;
+        if (s_nonfinite[nth % WORKS]) set_aside(w, p.first_hidden, w.r.past + pos, col, x, 4);
+        if (whole) {
+          T* dst = static_cast<T*>(a.out) + ((int64_t)(w.r.qb + pos) * a.q_heads + w.head * G + row % G) * D + col;
+          *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]));
+        } else {
+          const int64_t place = (int64_t)w.part * 2 * BM + row;
+          *reinterpret_cast<float4*>(a.ws.partial + place * D + col) = make_float4(x[0], x[1], x[2], x[3]);
+          if (col == 0) a.ws.ml[place] = make_float4(l, top.ref, top.far, 0.0f);
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_used);
+    };
+    bool tiles_before = false;  // the piece before had tiles
+    for (int nth = 0;; ++nth) {
+      View u;
+      {
+        Piece w;
+        ok = ok && next_work(nth, &w);
+        if (tile_vote(t, !ok)) break;
+        const Plan p(a, w);
+        if (p.light) {
+          if (t == 0) {
+            // Its copies have all been taken up: no barrier is two phases from where these warps believe it to be.
+            if (tiles_before)
+              ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(work_empty + 8 * ((nth - 1) % WORKS), ((nth - 1) / WORKS) & 1,
+                                                           err, a.wait_ns));
+            light_piece(w, p, nth);
+          }
+          tiles_before = false;
+          __syncwarp();
+          if (ok && lane == 0) mbar_arrive(work_empty + 8 * (nth % WORKS));
+          continue;
+        }
+        tiles_before = true;
+        for (int i = max(p.zone, w.b0); i < w.b1; ++i) fixed_once ^= 1u << ((w.n + 2 * (i - w.b0) + 1) % NST);
+        u = view(w);
+      }
+      const bool live = u.live;
       // The reference, in units of log2, scaled and less LIFT (-LIFT in far rows, 0 before the first score); the
       // scaled score that calls for another (-inf: any does); a far row's reference.
       float m = 0.0f, most = NEG_INF, l = 0.0f, far_ref = NEG_INF;
-      for (int i = 0; i < blocks; ++i, ++ns) {
+      for (int i = 0; i < u.blocks; ++i, ++ns, u.seen -= BN, u.clear -= BN) {
         ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(s_full + 8 * t, ns & 1, err, a.wait_ns));
-        const int c0 = (w.b0 + i) * BN + h * HN, seen = lim - c0;  // columns up to `seen` count
-        const bool masked = c0 + HN - 1 > clear;
-        const bool use = ok && any_live;
+        const bool masked = HN - 1 > u.clear, use = ok && u.any_live;
         // 32 scores, again from tensor memory for the weights: registers for all 64 would spill
         auto scores = [&](int c, uint32_t (&s)[32]) {
           tmem_ld32<0>(s_addr + c, s);
           tmem_wait_ld();
           if (masked) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) s[e] = c + e <= seen ? s[e] : __float_as_uint(NEG_INF);
+            for (int e = 0; e < 32; ++e) s[e] = c + e <= u.seen ? s[e] : __float_as_uint(NEG_INF);
           }
         };
         float mn = NEG_INF;
@@ -739,11 +1029,36 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(p_full + 16 * t + 8 * h);
       }
-      // ---- O / l to memory, or O and l to scratch ----
+      // ---- O / l to memory, or O, l and their reference to scratch ----
+      const Piece w = work[nth % WORKS];
+      const Plan p(a, w);
+      const int blocks = t ? p.mine[1] : p.mine[0];
+      const int pos = w.pos0 + t * P + row_pos, lim = w.r.past + pos;
       const bool whole = w.part < 0;
-      float4* ml = a.ws.ml + ((int64_t)(whole ? 0 : w.part) * 2 + t) * BM + r;
+      const int64_t place = ((int64_t)(whole ? 0 : w.part) * 2 + t) * BM + r;
+      T* const dst = static_cast<T*>(a.out) + ((int64_t)(w.r.qb + pos) * a.q_heads + w.head * G + row_head) * D;
+      float* const part = a.ws.partial + place * D;
+      auto put = [&](int col, float (&x)[16], bool extra) {  // 16 columns of the row
+        if (extra) set_aside(w, p.first_hidden, lim, col, x, 16);
+        if (whole) {
+          uint32_t y[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = pack2<T>(x[2 * e], x[2 * e + 1]);
+          store16(dst + col, y, a.wide);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; e += 8) {
+            uint32_t y[8];
+#pragma unroll
+            for (int f = 0; f < 8; ++f) y[f] = __float_as_uint(x[e + f]);
+            store16(part + col + e, y, true);
+          }
+        }
+      };
+      const float ref =
+          far_ref != NEG_INF ? far_ref * a.scale_log2 : most == NEG_INF ? NEG_INF : m + LIFT<T>;
       if (blocks == 0) {
-        if (!whole && live && h == 0) *ml = make_float4(0.0f, NEG_INF, NEG_INF, 0.0f);
+        if (!whole && live && h == 0) a.ws.ml[place] = make_float4(0.0f, NEG_INF, NEG_INF, 0.0f);
       } else {
         s_sum[t][h][r] = l;
         tile_sync(t);
@@ -752,52 +1067,26 @@ __global__ void __launch_bounds__(THREADS, 1)
         ++no;
         if (ok) {
           tc_fence_after();
-          uint32_t o[HD];
-          tmem_ld32<0>(o_addr, o);
-          if constexpr (D == 128) tmem_ld32<32>(o_addr + 32, o);
-          tmem_wait_ld();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(o_empty + 8 * t);
           const float inv = whole ? 1.0f / l : 1.0f;
           const bool extra = s_nonfinite[nth % WORKS] != 0;
-          if (live) {
-            T* dst = static_cast<T*>(a.out) + ((int64_t)(w.r.qb + pos) * a.q_heads + w.head * G + row_head) * D + h * HD;
-            float* part = a.ws.partial + (((int64_t)(whole ? 0 : w.part) * 2 + t) * BM + r) * D + h * HD;
-            if (!whole && h == 0)
-              *ml = make_float4(l, far_ref != NEG_INF ? far_ref * a.scale_log2 : most == NEG_INF ? NEG_INF : m + LIFT<T>,
-                                far_ref, 0.0f);
+          if (live && !whole && h == 0) a.ws.ml[place] = make_float4(l, ref, far_ref, 0.0f);
+#pragma unroll 1
+          for (int c = 0; c < HD; c += 32) {
+            uint32_t o[32];
+            tmem_ld32<0>(o_addr + c, o);
+            tmem_wait_ld();
+            if (c + 32 == HD) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(o_empty + 8 * t);
+            }
+            if (live) {
 #pragma unroll
-            for (int c = 0; c < HD; c += 16) {
-              float x[16];
+              for (int d = 0; d < 32; d += 16) {
+                float x[16];
 #pragma unroll
-              for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(o[c + e]) * inv;
-              if (extra) {  // what was set aside: positions of this piece that the row sees
-                const int j1 = min(lim, w.b1 * BN - 1);
-                for (int j = max(p.first_hidden, w.b0 * BN); j <= j1; ++j) {
-                  const int id = a.table[(int64_t)w.r.slot * a.width + (j >> a.shift)];
-                  if (id < 0 || id >= a.pages) continue;
-                  const T* v = static_cast<const T*>(a.v_pages) +
-                               ((((int64_t)id * a.heads + w.head) << a.shift) + (j & ((1 << a.shift) - 1))) * D + h * HD + c;
-                  for (int e = 0; e < 16; ++e) {
-                    const float f = (float)v[e];
-                    if (!isfinite(f)) x[e] += f;
-                  }
-                }
-              }
-              if (whole) {
-                uint32_t y[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = pack2<T>(x[2 * e], x[2 * e + 1]);
-                store16(dst + c, y, a.wide);
-              } else {
-#pragma unroll
-                for (int e = 0; e < 16; e += 8) {
-                  uint32_t y[8];
-#pragma unroll
-                  for (int f = 0; f < 8; ++f) y[f] = __float_as_uint(x[e + f]);
-                  store16(part + c + e, y, true);
-                }
+                for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(o[d + e]) * inv;
+                put(h * HD + c + d, x, extra);
               }
             }
           }
@@ -834,18 +1123,15 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) paged_join_kernel(const Args 
     auto place = [&](int k) {  // of piece k: the first of an item is its share's last
       return ((int64_t)(2 * (c0 + k) + (k == 0 ? 1 : 0)) * 2 + t) * BM + r;
     };
-    float top = NEG_INF, top_far = NEG_INF;
+    Reference top;
     for (int k = lane; k < j.pieces; k += 32) {
       const float4 x = __ldcg(a.ws.ml + place(k));
-      if (x.x != 0.0f) {
-        top = fmaxf(top, x.y);
-        top_far = fmaxf(top_far, x.z);
-      }
+      top.take(x.x, x.y, x.z);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
-      top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-      top_far = fmaxf(top_far, __shfl_xor_sync(0xFFFFFFFFu, top_far, o));
+      top.ref = fmaxf(top.ref, __shfl_xor_sync(0xFFFFFFFFu, top.ref, o));
+      top.far = fmaxf(top.far, __shfl_xor_sync(0xFFFFFFFFu, top.far, o));
     }
     float l = 0.0f, o[V] = {};
     for (int k0 = 0; k0 < j.pieces; k0 += 32) {
@@ -853,11 +1139,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) paged_join_kernel(const Args 
       if (k0 + lane < j.pieces) {
         const float4 x = __ldcg(a.ws.ml + place(k0 + lane));
         lk = x.x;
-        // far rows have scores, whose differences keep their bits.  Never 0, so that infinities and NaN stay.
-        f = lk == 0.0f ? 0.0f
-                       : fmaxf(ex2(x.z != NEG_INF && top_far * a.scale_log2 == top ? (x.z - top_far) * a.scale_log2
-                                                                                  : x.y - top),
-                               0x1p-126f);
+        f = top.factor(lk, x.y, x.z, a.scale_log2);
       }
       const int n = min(32, j.pieces - k0);
       for (int k = 0; k < n; ++k) {
