@@ -12,11 +12,20 @@ namespace {
 constexpr int SOFTMAX_WARPS = 16;
 constexpr int COPY_WARP = 16, MMA_WARP = 17, FIX_WARP = 19;  // and MMA_WARP + 1
 constexpr int LIGHT_WARPS = 8;  // warps 0-7
-constexpr int WORKS = 2;                                     // the piece that is copied and the one before
+constexpr int WORKS = 4;                                     // pieces that the roles may be at
 constexpr int THREADS = 640;
 constexpr int TMEM_COLS = 512;
 constexpr int LIGHT = 8;      // rows (positions times heads of a group) of a request that needs no tiles
-constexpr int END_UNITS = 1;  // what an item costs beside its blocks, in blocks
+constexpr int WARP_REQUESTS = 128;  // requests up to which one warp finds a CTA's share
+
+// What a block of keys costs, and an item beside its blocks, in units of about a third of a
+// microsecond: of light rows, of one tile (a chain of products and softmax) and of two.
+#ifndef PAGED_COSTS
+#define PAGED_COSTS 4, 6, 5, 4, 8, 6
+#endif
+constexpr int COSTS[6] = {PAGED_COSTS};
+constexpr int BLOCK_LIGHT = COSTS[0], BLOCK_ONE = COSTS[1], BLOCK_TWO = COSTS[2], END_LIGHT = COSTS[3], END_TILES = COSTS[4];
+constexpr int SHARE_MIN = COSTS[5];  // units; at least a block's, so that a share inside an item has a piece of it
 
 template <int D>
 struct Cfg {
@@ -49,9 +58,17 @@ struct Request {
   int qb, rows, past, slot;
 };
 
+// The launch begins under the end of the one before, which may have written what the
+// call describes: after the wait by a load that the compiler cannot take for a read-only one.
+__device__ __forceinline__ int32_t ld_int(const int32_t* p) {
+  int32_t v;
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
 __device__ __forceinline__ bool load_request(const Args& a, int s, Request* r) {
-  const int b = a.offsets[s], e = a.offsets[s + 1];
-  *r = Request{b, e - b, a.pos[s], a.slot[s]};
+  const int b = ld_int(a.offsets + s), e = ld_int(a.offsets + s + 1);
+  *r = Request{b, e - b, ld_int(a.pos + s), ld_int(a.slot + s)};
   const bool ok = b >= 0 && e >= b && e <= a.total && r->slot >= 0 && r->slot < a.slots && r->past >= 0 &&
                   (int64_t)r->past + r->rows <= a.width << a.shift;
   return ok;
@@ -61,32 +78,58 @@ __device__ __forceinline__ bool load_request(const Args& a, int s, Request* r) {
 // past + (i + 1) 2 P - 1, which repeats with the period of 64 pairs (P blocks).
 __host__ __device__ __forceinline__ int64_t full_blocks(int past, int positions, int n) {
   const int step = 2 * positions, q = n / 64, r = n % 64;
-  int64_t part = 0, period = 0;
+  int part = 0, period = 0, last = past - 1;
   const int upto = q ? 64 : r;
+#pragma unroll 4
   for (int i = 0; i < upto; ++i) {
-    const int64_t nb = ((int64_t)past + (int64_t)(i + 1) * step - 1) / BN + 1;
-    period += nb;
-    if (i < r) part += nb;
+    last += step;
+    period += last / BN + 1;
+    if (i + 1 == r) part = period;
   }
-  return part + (q ? q * period + (int64_t)positions * 64 * ((int64_t)q * (q - 1) / 2) + (int64_t)r * q * positions : 0);
+  if (!q) return part;
+  return part + (int64_t)q * period + (int64_t)positions * 64 * ((int64_t)q * (q - 1) / 2) + (int64_t)r * q * positions;
 }
-// Units of one head of a request: its blocks, and what its items cost beside them.
-__host__ __device__ __forceinline__ int64_t head_units(int past, int rows, int positions) {
+// Units of a block of a request, and of an item beside its blocks.
+__host__ __device__ __forceinline__ int block_units(int rows, int positions, int group) {
+  return rows * group <= LIGHT ? BLOCK_LIGHT : rows <= positions ? BLOCK_ONE : BLOCK_TWO;
+}
+__host__ __device__ __forceinline__ int end_units(int rows, int group) {
+  return rows * group <= LIGHT ? END_LIGHT : END_TILES;
+}
+// Units of one head of a request.
+__host__ __device__ __forceinline__ int64_t head_units(int past, int rows, int positions, int group) {
   const int step = 2 * positions, n = rows / step;
-  int64_t u = full_blocks(past, positions, n) + (int64_t)n * END_UNITS;
-  if (rows % step) u += ((int64_t)past + rows - 1) / BN + 1 + END_UNITS;
-  return u;
+  int64_t blocks = n ? full_blocks(past, positions, n) : 0;
+  if (rows % step) blocks += (past + rows - 1) / BN + 1;
+  return blocks * block_units(rows, positions, group) + (int64_t)((rows + step - 1) / step) * end_units(rows, group);
 }
-// The first unit of share c of n.
-__host__ __device__ __forceinline__ int64_t share_begin(int64_t all, int c, int n) { return all * c / n; }
-// The share that has a unit.
-__host__ __device__ __forceinline__ int share_of(int64_t all, int64_t unit, int n) {
-  int c = (int)((double)unit * n / (double)all);
-  c = c < 0 ? 0 : c > n - 1 ? n - 1 : c;
-  while (c > 0 && share_begin(all, c, n) > unit) --c;
-  while (c < n - 1 && share_begin(all, c + 1, n) <= unit) ++c;
-  return c;
-}
+
+// All units in n equal shares.
+struct Shares {
+  int64_t all, each;
+  int n, rest;
+  __host__ __device__ __forceinline__ Shares(int64_t all, int ctas) : all(all) {
+    n = all / SHARE_MIN < ctas ? (int)(all / SHARE_MIN) : ctas;
+    if (n < 1) n = 1;
+    if (all < (int64_t)1 << 31) {
+      each = (unsigned)all / (unsigned)n;
+      rest = (int)((unsigned)all % (unsigned)n);
+    } else {
+      each = all / n;
+      rest = (int)(all % n);
+    }
+  }
+  // the first unit of share c
+  __host__ __device__ __forceinline__ int64_t begin(int c) const { return each * c + (unsigned)(rest * c) / (unsigned)n; }
+  // the share that has a unit
+  __host__ __device__ __forceinline__ int of(int64_t unit) const {
+    int c = (int)((float)unit / (float)all * (float)n);
+    c = c < 0 ? 0 : c > n - 1 ? n - 1 : c;
+    while (c > 0 && begin(c) > unit) --c;
+    while (c < n - 1 && begin(c + 1) <= unit) ++c;
+    return c;
+  }
+};
 
 // A share's piece of an item: blocks [b0, b1) of a pair of tiles of one head.
 struct Piece {
@@ -96,6 +139,8 @@ struct Piece {
   int b0, b1;
   int n;     // blocks (K and V) of the pieces before it
   int part;  // where its sums go: -1: the whole item, straight to the output
+  bool last; // the item's last
+  int64_t first;  // the unit of the item's block 0
 };
 
 // What the roles derive from a piece.
@@ -142,8 +187,8 @@ __device__ void clear_rows(const Args& a, bool bad, int64_t thread, int64_t thre
     r1 = r1 > a.total ? a.total : r1;
     for (int64_t i = r0 * row + thread; i < r1 * row; i += threads) p[i] = make_uint4(0u, 0u, 0u, 0u);
   };
-  clear(0, a.offsets[0]);
-  clear(a.offsets[a.S], a.total);
+  clear(0, ld_int(a.offsets));
+  clear(ld_int(a.offsets + a.S), a.total);
   for (int s = 0; bad && s < a.S; ++s) {
     Request r;
     if (!load_request(a, s, &r)) clear(r.qb, (int64_t)r.qb + r.rows);
@@ -156,27 +201,30 @@ struct Walk {
   int base;
   int s, head, pair;  // the item it stands at
   int64_t skip;       // units of it that belong to shares before
-  int64_t left;       // units of the share
+  int64_t left, at;   // units of the share that are left; the unit it stands at
   __device__ __forceinline__ void load(const Args& a, int lane) {
     r = Request{0, 0, 0, 0};
     if (base + lane < a.S && !load_request(a, base + lane, &r)) r.rows = 0;
   }
-  // at unit `rem` of request s0
-  __device__ __forceinline__ void begin(const Args& a, int s0, int64_t rem, int64_t units, int lane) {
+  // at unit `rem` of request s0, which is unit u0 of all
+  __device__ __forceinline__ void begin(const Args& a, int s0, int64_t rem, int64_t u0, int64_t u1, int lane) {
     base = s = s0;
-    left = units;
+    at = u0;
+    left = u1 - u0;
     load(a, lane);
     const int past = __shfl_sync(0xFFFFFFFFu, r.past, 0), rows = __shfl_sync(0xFFFFFFFFu, r.rows, 0);
-    const int64_t each = head_units(past, rows, a.positions);
-    head = each ? (int)(rem / each) : 0;
+    const int64_t each = head_units(past, rows, a.positions, a.group);
+    head = rem < (int64_t)1 << 31 && each < (int64_t)1 << 31 ? (int)((unsigned)rem / (unsigned)max((int)each, 1))
+                                                             : (int)(rem / each);
     rem -= head * each;
     const int step = 2 * a.positions, pairs = (rows + step - 1) / step;
+    const int block = block_units(rows, a.positions, a.group), end = end_units(rows, a.group);
     // 32 pairs at a time
     pair = 0;
-    for (int i = 0; i < pairs; i += 32) {
+    for (int i = 0; pairs > 1 && i < pairs; i += 32) {
       const int p = i + lane;
-      const int64_t u = p < pairs ? ((int64_t)past + min((p + 1) * (int64_t)step, (int64_t)rows) - 1) / BN + 1 + END_UNITS
-                                  : 0;
+      const int64_t u =
+          p < pairs ? (int64_t)((past + (int)min((p + 1) * (int64_t)step, (int64_t)rows) - 1) / BN + 1) * block + end : 0;
       const int64_t upto = scan64(u, lane);
       const unsigned hit = __ballot_sync(0xFFFFFFFFu, rem < upto);
       if (hit) {
@@ -210,11 +258,19 @@ struct Walk {
       w->ok = 1;
       w->head = head;
       w->pos0 = pair * step;
-      const int nb = (int)(((int64_t)w->r.past + min((int64_t)w->pos0 + step, (int64_t)w->r.rows) - 1) / BN + 1);
-      const int64_t upto = min((int64_t)nb + END_UNITS, skip + left);
-      w->b0 = (int)max((int64_t)0, skip - END_UNITS);
-      w->b1 = (int)max((int64_t)0, upto - END_UNITS);
+      const int nb = (w->r.past + (int)min((int64_t)w->pos0 + step, (int64_t)w->r.rows) - 1) / BN + 1;
+      const int block = block_units(w->r.rows, a.positions, a.group), end = end_units(w->r.rows, a.group);
+      const int64_t upto = min((int64_t)nb * block + end, skip + left);
+      // a block is the share's that has its first unit
+      auto blocks_before = [&](int64_t unit) {
+        return unit <= end ? 0 : (int)(((unsigned)min(unit - end, (int64_t)nb * block) + block - 1) / (unsigned)block);
+      };
+      w->b0 = blocks_before(skip);
+      w->b1 = blocks_before(upto);
       w->part = w->b0 == 0 && w->b1 == nb ? -1 : 2 * cta + (w->b0 > 0 ? 0 : 1);
+      w->first = at - skip + end;
+      w->last = w->b1 == nb;
+      at += upto - skip;
       left -= upto - skip;
       skip = 0;
       if ((int64_t)w->pos0 + step < w->r.rows) {
@@ -337,51 +393,73 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_init_fence();
   }
   if (warp == MMA_WARP) tmem_alloc(smem_u32(&s_tmem), TMEM_COLS);
-
-  // ---- the CTA's share of the units, by all threads: each has a run of requests ----
-  const int per = (a.S + THREADS - 1) / THREADS, s_begin = min(a.S, tid * per), s_end = min(a.S, s_begin + per);
-  int64_t units = 0;
-  bool bad = false;
-  for (int s = s_begin; s < s_end; ++s) {
-    Request r;
-    if (load_request(a, s, &r)) units += a.heads * head_units(r.past, r.rows, P);
-    else bad = true;
-  }
-  const int64_t upto = scan64(units, lane);
-  if (lane == 31) s_scan[warp] = upto;
+  if (warp == COPY_WARP && lane < 3) prefetch_map(lane == 0 ? &map_q : lane == 1 ? &map_k : &map_v);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (bad) s_bad = 1;
-  int64_t before = upto - units, all = 0;
-  for (int i = 0; i < THREADS / 32; ++i) {
-    if (i < warp) before += s_scan[i];
-    all += s_scan[i];
-  }
-  const int shares = (int)min((int64_t)gridDim.x, all);
-  const bool idle = (int)blockIdx.x >= shares;
-  const int64_t u0 = idle ? 0 : share_begin(all, blockIdx.x, shares);
-  const int64_t u1 = idle ? 0 : share_begin(all, blockIdx.x + 1, shares);
-  if (!idle && u0 >= before && u0 < before + units) {
-    int64_t rem = u0 - before;
-    int s = s_begin;
-    for (; s < s_end; ++s) {
+
+  // ---- the CTA's share of the units: each of `threads` threads has a run of requests ----
+  // Few requests are looked through by the warp that copies; the others need not wait for it.
+  const bool by_warp = a.S <= WARP_REQUESTS;
+  int s_first_ = 0;
+  int64_t rem = 0, all = 0;
+  if (!by_warp || warp == COPY_WARP) {
+    const int threads = by_warp ? 32 : THREADS, thread = by_warp ? lane : tid;
+    const int per = (a.S + threads - 1) / threads, s_begin = min(a.S, thread * per), s_end = min(a.S, s_begin + per);
+    auto units_of = [&](int s, bool* bad) -> int64_t {
       Request r;
-      const int64_t u = load_request(a, s, &r) ? a.heads * head_units(r.past, r.rows, P) : 0;
-      if (rem < u) break;
-      rem -= u;
+      if (load_request(a, s, &r)) return a.heads * head_units(r.past, r.rows, P, G);
+      *bad = true;
+      return 0;
+    };
+    int64_t units = 0;
+    bool bad = false;
+    for (int s = s_begin; s < s_end; ++s) units += units_of(s, &bad);
+    const int64_t upto = scan64(units, lane);
+    int64_t before = upto - units;
+    if (by_warp) {
+      all = __shfl_sync(0xFFFFFFFFu, upto, 31);
+    } else {
+      if (lane == 31) s_scan[warp] = upto;
+      if (bad) s_bad = 1;
+      __syncthreads();
+      for (int i = 0; i < THREADS / 32; ++i) {
+        if (i < warp) before += s_scan[i];
+        all += s_scan[i];
+      }
     }
-    s_first = s;
-    s_rem = rem;
+    const Shares shares(all, (int)gridDim.x);
+    const int64_t u0 = shares.begin(min((int)blockIdx.x, shares.n));
+    const bool mine = u0 >= before && u0 < before + units;
+    if (mine) {
+      rem = u0 - before;
+      s_first_ = s_begin;
+      for (int s = s_begin; s < s_end - 1; ++s) {
+        const int64_t u = units_of(s, &bad);
+        if (rem < u) break;
+        rem -= u;
+        ++s_first_;
+      }
+    }
+    if (by_warp) {
+      const int l = __ffs(__ballot_sync(0xFFFFFFFFu, mine)) - 1;
+      s_first_ = __shfl_sync(0xFFFFFFFFu, s_first_, l);
+      rem = __shfl_sync(0xFFFFFFFFu, rem, l);
+    } else {
+      if (mine) {
+        s_first = s_first_;
+        s_rem = rem;
+      }
+      __syncthreads();
+      if (s_bad || ld_int(a.offsets) > 0 || ld_int(a.offsets + a.S) < a.total)
+        clear_rows<D>(a, s_bad != 0, (int64_t)blockIdx.x * THREADS + tid, (int64_t)gridDim.x * THREADS);
+      if (tid == 0 && s_bad && blockIdx.x == 0) atomicOr(a.status, STATUS_KV_RANGE);
+      s_first_ = s_first;
+      rem = s_rem;
+    }
   }
-  __syncthreads();
-  if (s_bad || a.offsets[0] > 0 || a.offsets[a.S] < a.total)
-    clear_rows<D>(a, s_bad != 0, (int64_t)blockIdx.x * THREADS + tid, (int64_t)gridDim.x * THREADS);
-  if (tid == 0) {
-    if (s_bad && blockIdx.x == 0) atomicOr(a.status, STATUS_KV_RANGE);
-    a.ws.joins[blockIdx.x].pieces = 0;
-  }
-  __syncthreads();
 
   const uint32_t tmem = s_tmem;
   // The roles go through the same pieces in the same order, each with its own
@@ -397,14 +475,34 @@ __global__ void __launch_bounds__(THREADS, 1)
     fewer_registers<64>();
     if (warp == COPY_WARP) {
       // ---------------- work and copies ----------------
+      const Shares shares(all, (int)gridDim.x);
       Walk walk;
       walk.left = 0;
-      if (!idle) walk.begin(a, s_first, s_rem, u1 - u0, lane);
+      if ((int)blockIdx.x < shares.n && all > 0)
+        walk.begin(a, s_first_, rem, shares.begin(blockIdx.x), shares.begin(blockIdx.x + 1), lane);
+      PagedJoin join{0, 0, 0, 0};  // the item whose last piece this share has
+      int64_t join_first = 0;
       int n = 0, nq = 0;  // blocks and Q pairs so far
       int nth = 0;        // pieces so far
       bool ok = true, wild = false;
-      Piece w;
-      while (ok && walk.next(a, blockIdx.x, lane, &w)) {
+      // the numbers of a piece's pages: lane l has page first + l, and the one 32 later
+      struct Numbers {
+        int first, id, next;
+      };
+      const int per_block = BN >> a.shift;
+      auto number = [&](const Piece& w, int page) {
+        const int last_page = (w.r.past + min(w.pos0 + 2 * P, w.r.rows) - 1) >> a.shift;
+        return page <= last_page ? ld_int(a.table + (int64_t)w.r.slot * a.width + page) : 0;
+      };
+      auto numbers = [&](const Piece& w) {
+        const int first = (w.b0 * per_block) & ~31;
+        return Numbers{first, number(w, first + lane), number(w, first + 32 + lane)};
+      };
+      Piece w, then;
+      Numbers ids{0, 0, 0}, ids_then{0, 0, 0};
+      bool light_before = false, have = walk.next(a, blockIdx.x, lane, &w);
+      if (have) ids = numbers(w);
+      for (bool more = false; ok && have; have = more, w = then, ids = ids_then) {
         if (nth >= WORKS) {  // every role is done with the piece that had the slot
           const int v = nth - WORKS;
           ok = __all_sync(0xFFFFFFFFu, mbar_wait(work_empty + 8 * (v % WORKS), (v / WORKS) & 1, err, a.wait_ns));
@@ -416,22 +514,13 @@ __global__ void __launch_bounds__(THREADS, 1)
           work[nth % WORKS] = w;
           s_nonfinite[nth % WORKS] = 0;
           mbar_arrive(work_full + 8 * (nth % WORKS));
-          // the item's last piece: says where the others are
-          const int nb = (p.seen_end - 1) / BN + 1;
-          if (w.part >= 0 && w.b1 == nb) {
-            // this share's first block is the item's block b0, so block 0 lies b0 units before
-            const int c0 = share_of(all, u0 - w.b0, shares);
-            a.ws.joins[blockIdx.x] =
-                PagedJoin{(int)blockIdx.x - c0 + 1, w.r.qb + w.pos0, min(2 * P, w.r.rows - w.pos0), w.head};
-          }
         }
+        if (light_before && !p.light)  // the light rows' sums lie where tile 1's rows go
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(work_empty + 8 * ((nth - 1) % WORKS), ((nth - 1) / WORKS) & 1, err, a.wait_ns));
+        light_before = p.light;
         ++nth;
-        // the pages' numbers: lane l has page first + l, and the one 32 later
-        const int per_block = BN >> a.shift, last_page = (p.seen_end - 1) >> a.shift;
-        const int32_t* table = a.table + (int64_t)w.r.slot * a.width;
-        auto number = [&](int page) { return page <= last_page ? table[page] : 0; };
-        int first = (w.b0 * per_block) & ~31;
-        int id = number(first + lane), id_next = number(first + 32 + lane);
+        if (!ok) break;
+        const int last_page = (p.seen_end - 1) >> a.shift;
         if (lane == 0) {
           if (nq > 0) ok = mbar_wait(q_empty, (nq - 1) & 1, err, a.wait_ns);
           if (ok && !a.stall) {
@@ -450,14 +539,20 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (ok) ++nq;
         const uint32_t page_bytes = (uint32_t)(D * 2) << a.shift;
         const int page_groups = 1 << (a.shift - 3);
+        if (w.part >= 0 && w.last) join = PagedJoin{0, w.r.qb + w.pos0, min(2 * P, w.r.rows - w.pos0), w.head};
+        if (w.part >= 0 && w.last) join_first = w.first;
         for (int i = w.b0; i < w.b1 && ok; ++i) {
-          const int pg = i * per_block, here = min(per_block, last_page - pg + 1);
-          if (pg >= first + 32) {
-            first += 32;
-            id = id_next;
-            id_next = number(first + 32 + lane);
+          if (i == min(w.b0 + NST / 2, w.b1 - 1)) {  // the ring is full: the next piece, whose numbers are then on their way
+            more = walk.next(a, blockIdx.x, lane, &then);
+            if (more) ids_then = numbers(then);
           }
-          int mine = __shfl_sync(0xFFFFFFFFu, id, (pg - first + lane) & 31);
+          const int pg = i * per_block, here = min(per_block, last_page - pg + 1);
+          if (pg >= ids.first + 32) {
+            ids.first += 32;
+            ids.id = ids.next;
+            ids.next = number(w, ids.first + 32 + lane);
+          }
+          int mine = __shfl_sync(0xFFFFFFFFu, ids.id, (pg - ids.first + lane) & 31);
           if (lane < here && (mine < 0 || mine >= a.pages)) {
             wild = true;
             mine = a.pages;  // past the end: the copy fills in zeros
@@ -491,6 +586,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           mbar_arrive(work_full + 8 * (nth % WORKS));
         }
       }
+      if (lane == 0) {
+        if (join.rows) join.pieces = (int)blockIdx.x - shares.of(join_first) + 1;
+        a.ws.joins[blockIdx.x] = join;
+      }
       if (__any_sync(0xFFFFFFFFu, wild) && lane == 0) atomicOr(a.status, STATUS_KV_RANGE);
       // the copies in flight land before the CTA ends, also when another role has given up
       if (nq > 0) mbar_wait_warp(q_full, (nq - 1) & 1, a.wait_ns);
@@ -500,6 +599,17 @@ __global__ void __launch_bounds__(THREADS, 1)
       uint32_t seen_once = 0, used_once = 0;  // parities of each stage's `hidden` and `used`
       int nl = 0;                             // light pieces so far
       bool ok = true, tiles_before = false;
+      if (by_warp) {  // rows of no request
+        bool bad = false;
+        for (int s = lane; s < a.S; s += 32) {
+          Request r;
+          bad |= !load_request(a, s, &r);
+        }
+        bad = __any_sync(0xFFFFFFFFu, bad);
+        if (bad || ld_int(a.offsets) > 0 || ld_int(a.offsets + a.S) < a.total)
+          clear_rows<D>(a, bad, (int64_t)blockIdx.x * 32 + lane, (int64_t)gridDim.x * 32);
+        if (bad && lane == 0 && blockIdx.x == 0) atomicOr(a.status, STATUS_KV_RANGE);
+      }
       Piece w;
       for (int nth = 0; ok; ++nth) {
         if (!__all_sync(0xFFFFFFFFu, next_work(nth, &w))) break;
@@ -509,6 +619,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           ok = __all_sync(0xFFFFFFFFu, mbar_wait(work_empty + 8 * ((nth - 1) % WORKS), ((nth - 1) / WORKS) & 1, err,
                                                  a.wait_ns));
         tiles_before = !p.light;
+        if (ok && p.light) {
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(q_used, nl++ & 1, err, a.wait_ns));
+          if (ok && lane == 0) mbar_arrive_n(q_empty, 2);
+        }
         // of light rows, gives back what their warps have read
         auto give_back = [&](int v) {
           const int st = v % NST;
@@ -565,10 +679,6 @@ __global__ void __launch_bounds__(THREADS, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(fixed + 8 * st);
           if (p.light) give_back(v);
-        }
-        if (ok && p.light) {
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait(q_used, nl++ & 1, err, a.wait_ns));
-          if (ok && lane == 0) mbar_arrive_n(q_empty, 2);
         }
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(work_empty + 8 * (nth % WORKS));
@@ -734,7 +844,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     auto set_aside = [&](const Piece& w, int first_hidden, int lim, int col, float* x, int N) {
       const int j1 = min(lim, w.b1 * BN - 1);
       for (int j = max(first_hidden, w.b0 * BN); j <= j1; ++j) {
-        const int id = a.table[(int64_t)w.r.slot * a.width + (j >> a.shift)];
+        const int id = ld_int(a.table + (int64_t)w.r.slot * a.width + (j >> a.shift));
         if (id < 0 || id >= a.pages) continue;
         const T* v = static_cast<const T*>(a.v_pages) +
                      ((((int64_t)id * a.heads + w.head) << a.shift) + (j & ((1 << a.shift) - 1))) * D + col;
@@ -756,6 +866,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int vec = 4 * k + (lane >> 3);
         ldsm4(q_smem + (vec >> 3) * C::Q_CHUNK + (lane & 7) * 128 + (((vec & 7) ^ (lane & 7)) << 4), q[k]);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_used);
       // rows 2 tq and 2 tq + 1: last position seen, reference (a score), the lane's share of the sum
       const int live_rows = w.r.rows * G;
       const int lim0 = 2 * tq < live_rows ? w.r.past + 2 * tq / G : -1;
@@ -836,14 +948,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(used + 8 * sv);
       }
-      // the warps' sums, joined through Q's place
+      // the warps' sums, joined through the place of tile 1's rows
 #pragma unroll
       for (int d = 4; d < 32; d *= 2) {
         l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, d);
         l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, d);
       }
       tile_sync(0);
-      float* const sums = reinterpret_cast<float*>(smem_p);  // [warp][8 rows][D], columns turned so that banks differ
+      float* const sums = reinterpret_cast<float*>(smem_p + C::TILE);  // [warp][8 rows][D], columns turned so that banks differ
 #pragma unroll
       for (int d = 0; d < D / 16; ++d) {
         float* row = sums + (warp * 8 + 2 * tq) * D;
@@ -895,9 +1007,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (col == 0) a.ws.ml[place] = make_float4(l, top.ref, top.far, 0.0f);
         }
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_used);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // copies come there again
     };
     bool tiles_before = false;  // the piece before had tiles
     for (int nth = 0;; ++nth) {
@@ -1106,66 +1216,103 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 // ---- the pieces of items that were cut, joined ----
 //   out = sum_i f_i O_i / sum_i f_i l_i,  f_i = 2^(reference_i - largest reference)
-// One warp a row; a row's references lie in its lanes, 32 pieces at a time.
-constexpr int JOIN_WARPS = 8;
+// Two rows a warp at a time; a row's references lie in its lanes, 32 pieces at a
+// time.  Bound by latency: the first pieces' sums are loaded beside the references.
+constexpr int JOIN_WARPS = 8, JOIN_CTAS = 8;  // CTAs for each share
 
 template <int D, typename T>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) paged_join_kernel(const Args a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int4 d = __ldcg(reinterpret_cast<const int4*>(a.ws.joins + blockIdx.x));
   const PagedJoin j{d.x, d.y, d.z, d.w};
   const int lane = threadIdx.x & 31, G = a.group, P = a.positions;
   const int rows = j.pieces ? j.rows * G : 0, c0 = (int)blockIdx.x - j.pieces + 1;
-  constexpr int V = D / 32;  // values of a lane
-  for (int i = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5); i < rows; i += gridDim.y * JOIN_WARPS) {
+  constexpr int V = D / 32, ROWS = 2, EARLY = 4;  // values of a lane; rows of a warp; pieces loaded early
+  auto load = [&](float (&x)[V], int64_t place) {
+    const float* p = a.ws.partial + place * D + lane * V;
+    if constexpr (V == 4) {
+      const float4 y = __ldcg(reinterpret_cast<const float4*>(p));
+      x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
+    } else {
+      const float2 y = __ldcg(reinterpret_cast<const float2*>(p));
+      x[0] = y.x, x[1] = y.y;
+    }
+  };
+  for (int i0 = (blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5)) * ROWS; i0 < rows; i0 += JOIN_CTAS * JOIN_WARPS * ROWS) {
     // row i of the item: position i / G, in tile 0 or 1
-    const int pos = i / G, t = pos >= P ? 1 : 0, r = (pos - t * P) * G + i % G;
-    auto place = [&](int k) {  // of piece k: the first of an item is its share's last
-      return ((int64_t)(2 * (c0 + k) + (k == 0 ? 1 : 0)) * 2 + t) * BM + r;
-    };
-    Reference top;
-    for (int k = lane; k < j.pieces; k += 32) {
-      const float4 x = __ldcg(a.ws.ml + place(k));
-      top.take(x.x, x.y, x.z);
+    int64_t base[ROWS];
+    int pos[ROWS], head[ROWS];
+#pragma unroll
+    for (int u = 0; u < ROWS; ++u) {
+      const int i = min(i0 + u, rows - 1);
+      pos[u] = i / G;
+      head[u] = i - pos[u] * G;
+      const int t = pos[u] >= P ? 1 : 0;
+      base[u] = (int64_t)(4 * c0 + t) * BM + (pos[u] - t * P) * G + head[u];
+    }
+    auto place = [&](int u, int k) { return base[u] + (4 * k + (k == 0 ? 2 : 0)) * BM; };  // piece k: the first is its share's last
+    float4 ml[ROWS];
+    float early[ROWS][EARLY][V];
+#pragma unroll
+    for (int u = 0; u < ROWS; ++u) ml[u] = lane < j.pieces ? __ldcg(a.ws.ml + place(u, lane)) : make_float4(0, 0, 0, 0);
+#pragma unroll
+    for (int u = 0; u < ROWS; ++u)
+#pragma unroll
+      for (int k = 0; k < EARLY; ++k)
+        if (k < j.pieces) load(early[u][k], place(u, k));
+    Reference top[ROWS];
+#pragma unroll
+    for (int u = 0; u < ROWS; ++u) {
+      top[u].take(ml[u].x, ml[u].y, ml[u].z);
+      for (int k = lane + 32; k < j.pieces; k += 32) {
+        const float4 x = __ldcg(a.ws.ml + place(u, k));
+        top[u].take(x.x, x.y, x.z);
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        top[u].ref = fmaxf(top[u].ref, __shfl_xor_sync(0xFFFFFFFFu, top[u].ref, o));
+        top[u].far = fmaxf(top[u].far, __shfl_xor_sync(0xFFFFFFFFu, top[u].far, o));
+      }
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      top.ref = fmaxf(top.ref, __shfl_xor_sync(0xFFFFFFFFu, top.ref, o));
-      top.far = fmaxf(top.far, __shfl_xor_sync(0xFFFFFFFFu, top.far, o));
-    }
-    float l = 0.0f, o[V] = {};
-    for (int k0 = 0; k0 < j.pieces; k0 += 32) {
-      float f = 0.0f, lk = 0.0f;
-      if (k0 + lane < j.pieces) {
-        const float4 x = __ldcg(a.ws.ml + place(k0 + lane));
-        lk = x.x;
-        f = top.factor(lk, x.y, x.z, a.scale_log2);
-      }
-      const int n = min(32, j.pieces - k0);
-      for (int k = 0; k < n; ++k) {
-        const float fk = __shfl_sync(0xFFFFFFFFu, f, k), lkk = __shfl_sync(0xFFFFFFFFu, lk, k);
-        if (fk == 0.0f) continue;
-        l += fk * lkk;
-        const float* p = a.ws.partial + place(k0 + k) * D + lane * V;
-        if constexpr (V == 4) {
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(p));
-          o[0] += fk * x.x;
-          o[1] += fk * x.y;
-          o[2] += fk * x.z;
-          o[3] += fk * x.w;
-        } else {
-          const float2 x = __ldcg(reinterpret_cast<const float2*>(p));
-          o[0] += fk * x.x;
-          o[1] += fk * x.y;
+    for (int u = 0; u < ROWS; ++u) {
+      float l = 0.0f, o[V] = {};
+      auto add = [&](float f, float lk, const float (&x)[V]) {
+        l += f * lk;
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] += f == 0.0f ? 0.0f : f * x[e];  // pieces of nothing have not been written
+      };
+      for (int k0 = 0; k0 < j.pieces; k0 += 32) {
+        if (k0 > 0) ml[u] = k0 + lane < j.pieces ? __ldcg(a.ws.ml + place(u, k0 + lane)) : make_float4(0, 0, 0, 0);
+        const float lk = ml[u].x, f = top[u].factor(lk, ml[u].y, ml[u].z, a.scale_log2);
+        const int n = min(32, j.pieces - k0);
+        int k = 0;
+        if (k0 == 0) {
+#pragma unroll
+          for (int e = 0; e < EARLY; ++e) {
+            const float fk = __shfl_sync(0xFFFFFFFFu, f, e), lkk = __shfl_sync(0xFFFFFFFFu, lk, e);
+            if (e < n) add(fk, lkk, early[u][e]);
+          }
+          k = EARLY;
+        }
+#pragma unroll 4
+        for (; k < n; ++k) {
+          float x[V];
+          load(x, place(u, k0 + k));
+          add(__shfl_sync(0xFFFFFFFFu, f, k), __shfl_sync(0xFFFFFFFFu, lk, k), x);
         }
       }
+      if (i0 + u < rows) {
+        const float inv = 1.0f / l;
+        T* dst = static_cast<T*>(a.out) + ((int64_t)(j.row + pos[u]) * a.q_heads + j.head * G + head[u]) * D + lane * V;
+        if constexpr (V == 4)
+          *reinterpret_cast<uint2*>(dst) =
+              make_uint2(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv));
+        else
+          *reinterpret_cast<uint32_t*>(dst) = pack2<T>(o[0] * inv, o[1] * inv);
+      }
     }
-    const float inv = 1.0f / l;
-    T* dst = static_cast<T*>(a.out) + ((int64_t)(j.row + pos) * a.q_heads + j.head * G + i % G) * D + lane * V;
-    if constexpr (V == 4)
-      *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv));
-    else
-      *reinterpret_cast<uint32_t*>(dst) = pack2<T>(o[0] * inv, o[1] * inv);
   }
 }
 
@@ -1226,17 +1373,20 @@ int launch_as(const PagedAttn& c, cudaStream_t s) {
       return Q4_ERR_CUDA;
     sized[dev].store(true);
   }
-  paged_kernel<D, T><<<(unsigned)c.num_sms, THREADS, Cfg<D>::SMEM, s>>>(a, mq, mk, mv);
-  if (cudaGetLastError() != cudaSuccess) return Q4_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)c.num_sms, 8);
-  cfg.blockDim = dim3(32 * JOIN_WARPS);
+  cfg.gridDim = dim3((unsigned)c.num_sms);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = Cfg<D>::SMEM;
   cfg.stream = s;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, paged_kernel<D, T>, a, mq, mk, mv) != cudaSuccess) return Q4_ERR_CUDA;
+  cfg.gridDim = dim3((unsigned)c.num_sms, JOIN_CTAS);
+  cfg.blockDim = dim3(32 * JOIN_WARPS);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, T>, a) == cudaSuccess ? Q4_OK : Q4_ERR_CUDA;
 }
 

@@ -87,6 +87,9 @@ __device__ __forceinline__ void tensor_load(uint32_t dst, const void* map, int x
       : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const void* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
 // 4-d tile at (x, y, z, w); x alike
 __device__ __forceinline__ void tensor_load4(uint32_t dst, const void* map, int x, int y, int z, int w, uint32_t bar) {
   asm volatile(
