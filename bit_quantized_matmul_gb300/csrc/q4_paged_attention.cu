@@ -21,11 +21,12 @@ constexpr int WARP_REQUESTS = 128;  // requests up to which one warp finds a CTA
 // What a block of keys costs, and an item beside its blocks, in units of about a third of a
 // microsecond: of light rows, of one tile (a chain of products and softmax) and of two.
 #ifndef PAGED_COSTS
-#define PAGED_COSTS 4, 6, 5, 4, 8, 6
+#define PAGED_COSTS 4, 5, 6, 4, 8, 16, 6
 #endif
-constexpr int COSTS[6] = {PAGED_COSTS};
-constexpr int BLOCK_LIGHT = COSTS[0], BLOCK_ONE = COSTS[1], BLOCK_TWO = COSTS[2], END_LIGHT = COSTS[3], END_TILES = COSTS[4];
-constexpr int SHARE_MIN = COSTS[5];  // units; at least a block's, so that a share inside an item has a piece of it
+constexpr int COSTS[7] = {PAGED_COSTS};
+constexpr int BLOCK_LIGHT = COSTS[0], BLOCK_ONE = COSTS[1], BLOCK_TWO = COSTS[2], END_LIGHT = COSTS[3];
+constexpr int END_ONE = COSTS[4], END_TWO = COSTS[5];
+constexpr int SHARE_MIN = COSTS[6];  // units; at least a block's, so that a share inside an item has a piece of it
 
 template <int D>
 struct Cfg {
@@ -93,15 +94,15 @@ __host__ __device__ __forceinline__ int64_t full_blocks(int past, int positions,
 __host__ __device__ __forceinline__ int block_units(int rows, int positions, int group) {
   return rows * group <= LIGHT ? BLOCK_LIGHT : rows <= positions ? BLOCK_ONE : BLOCK_TWO;
 }
-__host__ __device__ __forceinline__ int end_units(int rows, int group) {
-  return rows * group <= LIGHT ? END_LIGHT : END_TILES;
+__host__ __device__ __forceinline__ int end_units(int rows, int positions, int group) {
+  return rows * group <= LIGHT ? END_LIGHT : rows <= positions ? END_ONE : END_TWO;
 }
 // Units of one head of a request.
 __host__ __device__ __forceinline__ int64_t head_units(int past, int rows, int positions, int group) {
   const int step = 2 * positions, n = rows / step;
   int64_t blocks = n ? full_blocks(past, positions, n) : 0;
   if (rows % step) blocks += (past + rows - 1) / BN + 1;
-  return blocks * block_units(rows, positions, group) + (int64_t)((rows + step - 1) / step) * end_units(rows, group);
+  return blocks * block_units(rows, positions, group) + (int64_t)((rows + step - 1) / step) * end_units(rows, positions, group);
 }
 
 // All units in n equal shares.
@@ -218,7 +219,7 @@ struct Walk {
                                                              : (int)(rem / each);
     rem -= head * each;
     const int step = 2 * a.positions, pairs = (rows + step - 1) / step;
-    const int block = block_units(rows, a.positions, a.group), end = end_units(rows, a.group);
+    const int block = block_units(rows, a.positions, a.group), end = end_units(rows, a.positions, a.group);
     // 32 pairs at a time
     pair = 0;
     for (int i = 0; pairs > 1 && i < pairs; i += 32) {
@@ -259,7 +260,7 @@ struct Walk {
       w->head = head;
       w->pos0 = pair * step;
       const int nb = (w->r.past + (int)min((int64_t)w->pos0 + step, (int64_t)w->r.rows) - 1) / BN + 1;
-      const int block = block_units(w->r.rows, a.positions, a.group), end = end_units(w->r.rows, a.group);
+      const int block = block_units(w->r.rows, a.positions, a.group), end = end_units(w->r.rows, a.positions, a.group);
       const int64_t upto = min((int64_t)nb * block + end, skip + left);
       // a block is the share's that has its first unit
       auto blocks_before = [&](int64_t unit) {
@@ -1228,7 +1229,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) paged_join_kernel(const Args 
   const PagedJoin j{d.x, d.y, d.z, d.w};
   const int lane = threadIdx.x & 31, G = a.group, P = a.positions;
   const int rows = j.pieces ? j.rows * G : 0, c0 = (int)blockIdx.x - j.pieces + 1;
-  constexpr int V = D / 32, ROWS = 2, EARLY = 4;  // values of a lane; rows of a warp; pieces loaded early
+  constexpr int V = D / 32, ROWS = 1, EARLY = 4;  // values of a lane; rows of a warp; pieces loaded early
   auto load = [&](float (&x)[V], int64_t place) {
     const float* p = a.ws.partial + place * D + lane * V;
     if constexpr (V == 4) {
