@@ -31,6 +31,7 @@ constexpr int THREADS = 1024;
 constexpr int WARPS = THREADS / 32;
 constexpr int CLUSTER = 8;
 constexpr int64_t ONE_CTA = 4096;  // rows and requests up to which one CTA is enough
+constexpr int FEW = 4;             // loads of a thread on their way at once
 
 __device__ __forceinline__ unsigned cluster_rank() {
   unsigned r;
@@ -170,9 +171,18 @@ __global__ void __launch_bounds__(THREADS) reserve_kernel(const Reserve a) {
       if (have < 0) continue;
       const int need = (int)(((int64_t)m.pos[s] + m.off[s + 1] - m.off[s] + page - 1) >> a.shift);
       int32_t* row = a.table + (int64_t)m.slot[s] * a.width;
-      for (int i = need + lane; i < have; i += 32) {
-        a.free_list[count + m.back[s] + i - need] = row[i];
-        row[i] = -1;
+      for (int i0 = need + lane; i0 < have; i0 += 32 * FEW) {
+        int id[FEW];
+#pragma unroll
+        for (int u = 0; u < FEW; ++u)
+          if (i0 + 32 * u < have) id[u] = row[i0 + 32 * u];
+#pragma unroll
+        for (int u = 0; u < FEW; ++u) {
+          const int i = i0 + 32 * u;
+          if (i >= have) break;
+          a.free_list[count + m.back[s] + i - need] = id[u];
+          row[i] = -1;
+        }
       }
     }
   }
@@ -207,27 +217,45 @@ __global__ void __launch_bounds__(THREADS) reserve_kernel(const Reserve a) {
 
   // ---- rows ----
   bool wild = false;
-  for (int64_t t = (int64_t)rank * THREADS + tid; t < a.total; t += (int64_t)ctas * THREADS) {
-    int lo = 0, n = a.S;  // the last request that begins at t or before it
-    while (n > 1) {
-      const int half = n >> 1;
-      if (m.off[lo + half] <= t) {
-        lo += half;
-        n -= half;
-      } else {
-        n = half;
+  const int64_t stride = (int64_t)ctas * THREADS;
+  for (int64_t t0 = (int64_t)rank * THREADS + tid; t0 < a.total; t0 += FEW * stride) {
+    int32_t* entry[FEW];  // where the row's page stands or is entered; null where the row has none
+    int id[FEW], at[FEW];
+    bool enters[FEW];
+#pragma unroll
+    for (int u = 0; u < FEW; ++u) {
+      const int64_t t = t0 + u * stride;
+      entry[u] = nullptr;
+      if (t >= a.total) continue;
+      int lo = 0, n = a.S;  // the last request that begins at t or before it
+      while (n > 1) {
+        const int half = n >> 1;
+        if (m.off[lo + half] <= t) {
+          lo += half;
+          n -= half;
+        } else {
+          n = half;
+        }
       }
-    }
-    int to = -1;
-    if (!none && t >= m.off[lo] && t < m.off[lo + 1] && wants(lo) >= 0) {
+      if (t < m.off[lo] || t >= m.off[lo + 1] || wants(lo) < 0) continue;
       const int have = m.have[lo], p = m.pos[lo] + (int)(t - m.off[lo]), i = p >> a.shift;
-      int32_t* entry = a.table + (int64_t)m.slot[lo] * a.width + i;
-      const int id = i < have ? *entry : __ldcg(a.free_list + (top - 1 - (m.more[lo] + i - have)));
-      if (i >= have && (p & (page - 1)) == 0) *entry = id;
-      if (id >= 0 && id < a.pages) to = (id << a.shift) + (p & (page - 1));
-      else wild = true;
+      at[u] = p & (page - 1);
+      entry[u] = a.table + (int64_t)m.slot[lo] * a.width + i;
+      enters[u] = i >= have && at[u] == 0;
+      id[u] = i < have ? *entry[u] : __ldcg(a.free_list + (top - 1 - (m.more[lo] + i - have)));
     }
-    a.slot_map[t] = to;
+#pragma unroll
+    for (int u = 0; u < FEW; ++u) {
+      const int64_t t = t0 + u * stride;
+      if (t >= a.total) break;
+      int to = -1;
+      if (entry[u]) {
+        if (enters[u]) *entry[u] = id[u];
+        if (id[u] >= 0 && id[u] < a.pages) to = (id[u] << a.shift) + at[u];
+        else wild = true;
+      }
+      a.slot_map[t] = to;
+    }
   }
   if (wild) atomicOr(a.status, STATUS_KV_RANGE);
 }
@@ -255,32 +283,32 @@ __device__ __forceinline__ uint32_t pair_of(float a, float b) {
   }
 }
 
-// Cached type T; F32: rows come in fp32 and are rounded.  grid.y: K, V.
+// Cached type T; F32: rows come in fp32 and are rounded.  A thread's piece is one of K
+// and the same one of V, so that two rows and the place are on their way at once.
 template <int D, typename T, bool F32>
 __global__ void __launch_bounds__(256) paged_append_kernel(const Append a) {
   constexpr int VPR = D / 8;  // 16-byte pieces of a cached row
-  const bool kv = blockIdx.y != 0;
-  const void* src = kv ? a.src[1] : a.src[0];
-  T* const pages = static_cast<T*>(kv ? a.pages[1] : a.pages[0]);
-  const int64_t row_st = kv ? a.row[1] : a.row[0], head_st = kv ? a.head[1] : a.head[0];
   const uint32_t per_row = (uint32_t)a.heads * VPR, items = (uint32_t)a.total * per_row;
-  for (uint32_t it = blockIdx.x * 256u + threadIdx.x; it < items; it += gridDim.x * 256u) {
-    const uint32_t t = it / per_row, hv = it - t * per_row, h = hv / VPR, v = hv % VPR;
-    const int to = __ldg(a.slot_map + t);
-    const int64_t from = t * row_st + h * head_st + v * 8;
-    uint4 x;
+  auto take = [&](const void* src, int64_t from) {
     if constexpr (F32) {
       const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(src) + from);
       const float4 f = __ldg(p), g = __ldg(p + 1);
-      x = make_uint4(pair_of<T>(f.x, f.y), pair_of<T>(f.z, f.w), pair_of<T>(g.x, g.y), pair_of<T>(g.z, g.w));
+      return make_uint4(pair_of<T>(f.x, f.y), pair_of<T>(f.z, f.w), pair_of<T>(g.x, g.y), pair_of<T>(g.z, g.w));
     } else {
-      x = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(src) + from));
+      return __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(src) + from));
     }
+  };
+  for (uint32_t it = blockIdx.x * 256u + threadIdx.x; it < items; it += gridDim.x * 256u) {
+    const uint32_t t = it / per_row, hv = it - t * per_row, h = hv / VPR, v = hv % VPR;
+    const int to = __ldg(a.slot_map + t);
+    const uint4 k = take(a.src[0], t * a.row[0] + h * a.head[0] + v * 8);
+    const uint4 x = take(a.src[1], t * a.row[1] + h * a.head[1] + v * 8);
     if (to >= 0 && to < a.places) {
       const int64_t page = to >> a.shift, at = to & ((1 << a.shift) - 1);
-      T* row = pages + (((page * a.heads + h) << a.shift) + at) * D;
-      reinterpret_cast<uint4*>(row)[v] = x;
-    } else if (to != -1 && hv == 0 && !kv) {
+      const int64_t place = ((((page * a.heads + h) << a.shift) + at) * D) / 8 + v;
+      static_cast<uint4*>(a.pages[0])[place] = k;
+      static_cast<uint4*>(a.pages[1])[place] = x;
+    } else if (to != -1 && hv == 0) {
       atomicOr(a.status, STATUS_KV_RANGE);
     }
   }
@@ -289,8 +317,8 @@ __global__ void __launch_bounds__(256) paged_append_kernel(const Append a) {
 template <int D, typename T>
 int append_as(const PagedAppend& c, const Append& a, cudaStream_t s) {
   const int64_t blocks = ((int64_t)a.total * a.heads * (D / 8) + 255) / 256;
-  const int64_t most = (int64_t)c.num_sms * 64;
-  const dim3 grid((unsigned)(blocks < most ? blocks : most), 2);
+  const int64_t most = (int64_t)c.num_sms * 8;
+  const unsigned grid = (unsigned)(blocks < most ? blocks : most);
   if (c.dtype == Q4_DTYPE_F32) paged_append_kernel<D, T, true><<<grid, 256, 0, s>>>(a);
   else paged_append_kernel<D, T, false><<<grid, 256, 0, s>>>(a);
   return cudaGetLastError() == cudaSuccess ? Q4_OK : Q4_ERR_CUDA;
@@ -312,6 +340,10 @@ int launch_paged_reserve(const PagedReserve& c, cudaStream_t s) {
     sized[dev].store(true);
   }
   const int ctas = c.total + c.S <= ONE_CTA ? 1 : CLUSTER;
+  if (ctas == 1) {  // a cluster of one by itself
+    reserve_kernel<<<1, THREADS, smem, s>>>(a);
+    return cudaGetLastError() == cudaSuccess ? Q4_OK : Q4_ERR_CUDA;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(THREADS);
