@@ -634,14 +634,14 @@ class Q4PageTable:
         if min(self.slots, self.width, self.pages) < 1 or self.page_size not in (16, 32, 64, 128):
             raise ValueError("slots, width and pages must be positive and page_size 16, 32, 64 or 128")
         n = 1 + self.pages
-        device = torch.device("cuda" if device is None else device)
-        self.state = torch.full((n + self.slots * (self.width + 1),), -1, dtype=_i32, device=device)
+        state = torch.full((n + self.slots * (self.width + 1),), -1, dtype=_i32)
+        state[0] = self.pages
+        state[1:n] = torch.arange(self.pages - 1, -1, -1, dtype=_i32)  # page 0 is given out first
+        state[n:n + self.slots] = 0
+        self.state = state.to(torch.device("cuda" if device is None else device))
         self.free_count, self.free = self.state[:1], self.state[1:n]
         self.held = self.state[n:n + self.slots]
         self.table = self.state[n + self.slots:].view(self.slots, self.width)
-        self.free_count.fill_(self.pages)
-        self.free.copy_(torch.arange(self.pages - 1, -1, -1, dtype=_i32))  # page 0 is given out first
-        self.held.zero_()
         self.device = self.state.device
         self._index = self.state.get_device()
         base = self.state.data_ptr()
@@ -649,7 +649,10 @@ class Q4PageTable:
 
 
 class Q4PagedCache:
-    """K and V of one decoder layer in pages: ``k`` and ``v`` [pages, heads, page_size, head_dim] of a 16-bit type."""
+    """K and V of one decoder layer in pages: ``k`` and ``v`` [pages, heads, page_size, head_dim] of a 16-bit type.
+
+    The buffers are not cleared: rows that nothing was appended to may hold anything.
+    """
 
     def __init__(self, pages: int, heads: int, head_dim: int, page_size: int, dtype=torch.bfloat16, device=None):
         self.pages, self.heads, self.head_dim, self.page_size = int(pages), int(heads), int(head_dim), int(page_size)
@@ -657,7 +660,7 @@ class Q4PagedCache:
             raise ValueError("dtype must be float16 or bfloat16")
         device = torch.device("cuda" if device is None else device)
         self.dtype = dtype
-        self._data = torch.zeros((2, self.pages, self.heads, self.page_size, self.head_dim), dtype=dtype, device=device)
+        self._data = torch.empty((2, self.pages, self.heads, self.page_size, self.head_dim), dtype=dtype, device=device)
         self.k, self.v = self._data[0], self._data[1]
         self.device = self._data.device
         self._dims = (self.pages, self.heads, self.head_dim, self.page_size)

@@ -20,13 +20,9 @@ constexpr int WARP_REQUESTS = 128;  // requests up to which one warp finds a CTA
 
 // What a block of keys costs, and an item beside its blocks, in units of about a third of a
 // microsecond: of light rows, of one tile (a chain of products and softmax) and of two.
-#ifndef PAGED_COSTS
-#define PAGED_COSTS 4, 5, 6, 4, 8, 16, 6
-#endif
-constexpr int COSTS[7] = {PAGED_COSTS};
-constexpr int BLOCK_LIGHT = COSTS[0], BLOCK_ONE = COSTS[1], BLOCK_TWO = COSTS[2], END_LIGHT = COSTS[3];
-constexpr int END_ONE = COSTS[4], END_TWO = COSTS[5];
-constexpr int SHARE_MIN = COSTS[6];  // units; at least a block's, so that a share inside an item has a piece of it
+constexpr int BLOCK_LIGHT = 4, BLOCK_ONE = 5, BLOCK_TWO = 6;
+constexpr int END_LIGHT = 4, END_ONE = 8, END_TWO = 16;
+constexpr int SHARE_MIN = 6;  // at least a block's units, so that a share inside an item has a piece of it
 
 template <int D>
 struct Cfg {

@@ -207,6 +207,7 @@ def test_appended_rows(q4, cache_dtype, dtype, heads, d, page, total):
 
 def test_places_out_of_range_are_not_written(q4):
     c = q4.Q4PagedCache(2, 1, 64, 16)
+    c.k.zero_()
     k = torch.ones((4, 1, 64), dtype=torch.bfloat16, device="cuda")
     q4.q4_paged_append(c, k, k, _i32([32, -2, 31, 2 ** 31 - 1]))
     assert q4.q4_device_status() == q4.Q4_ERR_INVALID_ARG
@@ -324,6 +325,26 @@ def test_many_requests(q4, heads, hq, d):
     rows = [rng.choice((0, 1, 1, 1, 2)) for _ in past]
     s = Step(q4, 30, past, rows, heads, hq, d, 32, torch.bfloat16, gap=1)
     s.check(s.run())
+
+
+@pytest.mark.parametrize("S", [1, 31, 32, 33, 64, 65, 127, 128, 129, 640, 641])
+def test_counts_of_requests(q4, S):
+    # up to 128 one warp looks through them, up to 640 each thread through one
+    rng = random.Random(S)
+    past = [rng.choice((0, 1, 15, rng.randint(0, 300))) for _ in range(S)]
+    rows = [rng.choice((1, 1, 0, 2, 9, 40)) if S < 200 else rng.choice((1, 0)) for _ in past]
+    rows[-1] = 3
+    s = Step(q4, 31, past, rows, 1, 2, 64, 16, torch.float16, gap=2)
+    s.check(s.run())
+
+
+@pytest.mark.parametrize("rows", [1, 7, 8, 9, 64, 126, 127, 128, 129, 255, 256, 257])
+@pytest.mark.parametrize("heads,hq", [(2, 2), (1, 8), (1, 7)])
+def test_rows_at_the_borders_of_tiles(q4, rows, heads, hq):
+    # light rows (rows x group up to 8), one tile, two tiles, two pairs; pasts that end at and beside a block
+    for past in (0, 127, 128, 700):
+        s = Step(q4, 32, [past, 5], [rows, 1], heads, hq, 64, 32, torch.bfloat16)
+        s.check(s.run())
 
 
 @pytest.mark.parametrize("hq,heads", [(128, 1), (64, 1), (40, 1), (33, 1), (130, 2)])
@@ -511,6 +532,63 @@ def test_pages_past_32_bits(q4):
     assert q4.q4_device_status() == q4.Q4_OK
     _check(out.cpu().double().numpy(), q.double().numpy(), k.double().numpy(), v.double().numpy(), n - 3, d ** -0.5,
            torch.bfloat16, "last pages")
+
+
+@pytest.mark.parametrize("past,rows", [([3000, 40], [1, 1]), ([500, 900], [300, 1]), ([300], [20])])
+def test_waits_that_run_out(q4, past, rows):
+    """No copy is issued, so every wait for one runs out: the status says so, and later calls are right."""
+    s = Step(q4, 150, past, rows, 2, 14, 64, 16, torch.bfloat16)
+    want = s.run().clone()
+    assert q4.q4_device_status() == q4.Q4_OK
+    q4.q4mm_set_wait_limit_ns(20_000_000)
+    q4.q4mm_set_stall_for_test(True)
+    try:
+        s.run()
+        status = q4.q4_device_status()
+    finally:
+        q4.q4mm_set_stall_for_test(False)
+        q4.q4mm_set_wait_limit_ns(0)
+    assert status == q4.Q4_ERR_TIMEOUT and q4.q4_device_status() == q4.Q4_OK
+    for _ in range(2):
+        assert torch.equal(s.run(), want)
+    s.check(want)
+
+
+def test_beside_the_other_attentions(q4):
+    """The calls that share the library's scratch, one after another on a stream and in a graph."""
+    heads, hq, d = 2, 14, 64
+    s = Step(q4, 160, [2500, 100], [1, 30], heads, hq, d, 16, torch.bfloat16)
+    kvq = q4.Q4KVCache(2, heads, d, 4000)
+    k, v = (_normal(161 + i, (3000, heads, d), torch.bfloat16).cuda() for i in range(2))
+    q4.q4_kvq_append(kvq, k, v, _i32([0, 3000]), _i32([1]), _i32([0]))
+    q1 = _normal(163, (1, hq, d), torch.bfloat16).cuda()
+    off, slot, pos = _i32([0, 1]), _i32([1]), _i32([2999])
+    prompt = _normal(164, (200, hq + 2 * heads, d), torch.bfloat16).cuda()
+    poff = _i32([0, 200])
+    q, soff, sslot, spos = s.q.cuda(), _i32(s.offsets), _i32(s.slot), _i32(s.past)
+
+    def calls():
+        a = q4.q4_paged_attention(s.cache, s.tables, q, soff, sslot, spos)
+        b = q4.q4_kvq_attention(kvq, q1, off, slot, pos)
+        c = q4.q4_paged_attention(s.cache, s.tables, q, soff, sslot, spos)
+        e = q4.q4_prompt_attention(prompt[:, :hq], prompt[:, hq:hq + heads], prompt[:, hq + heads:], poff)
+        return a, b, c, e, q4.q4_paged_attention(s.cache, s.tables, q, soff, sslot, spos)
+
+    alone = s.run().clone()
+    first = [x.clone() for x in calls()]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = calls()
+    for _ in range(10):
+        g.replay()
+        calls()
+        torch.cuda.synchronize()
+        for x, y in zip(outs, first):
+            assert torch.equal(x, y)
+    for i in (0, 2, 4):
+        assert torch.equal(first[i], alone)
+    assert q4.q4_device_status() == q4.Q4_OK
 
 
 # ---------------------------------------------------------------- together
