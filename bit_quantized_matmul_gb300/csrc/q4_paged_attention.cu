@@ -3,6 +3,53 @@
 //
 //   o[j] = sum_{p <= pos + j} softmax_p(scale q_j . k_p) v_p,
 //   position p in row p % P of page table[slot][p / P], per request and head.
+//
+// One launch takes single rows, drafts and chunks of prompts.  An item is a head
+// of a request and a pair of tiles of its rows, as in prompt attention: the G query
+// heads that share a key/value head are packed with the positions into the 128
+// rows of a tile, and blocks of 128 keys are fetched once for both tiles.  A request of at most
+// eight rows (positions times G) has one item a head and no tiles: see below.
+//
+// Shares.  The items' blocks stand in one line, request by request, and each of the launch's CTAs, one
+// an SM, takes an equal piece of it, weighed by what blocks and ends of items cost, so
+// that 64 decode rows and a chunk of 4,096 keep all SMs busy alike.  Each CTA finds
+// its share from the step's description by itself.  An item that is cut leaves unnormalised sums
+// and references in scratch (two pieces a CTA at most), and a second launch
+// joins them.
+//
+// Roles (640 threads, registers split as in prompt attention):
+//   warps 0-15  softmax of two tiles, two threads a row; warps 0-7 the light rows
+//   warp 16     walks the share, and copies Q, and K and V through a ring of blocks: a page of a
+//               head is one tensor-map copy (four dimensions: 64 values, eight rows, the chunks of 64
+//               values, the groups of eight rows), issued by a lane each, so that a block in pages of
+//               16 takes one instruction; the next piece's page numbers are on their way meanwhile
+//   warps 17,18 issue the products of tile 0 / tile 1
+//   warp 19     clears places of V that no row sees, sets aside infinities and NaN that
+//               some rows do not see, gives back what the light rows' warps have read
+// In shared memory a block of K or V is groups of eight keys, each chunk by chunk
+// under the 128-byte swizzle: what one copy leaves is what products and ldmatrix read.
+//
+// Light rows.  With eight rows at most the tiles' products would be padding, and their
+// chain of products and softmax, 1.4 us a block, as long as the copy.  So eight warps take 16 keys
+// of a block each: S = K Q^T and O = V^T P^T as 16 x 8 mma.sync products with
+// keys and then values along m, a running reference and sums of their own, joined in
+// shared memory at the end.  Their work hides behind the copies: without it the calls below take 1.5 us less.
+//
+// Bounds, measured in a graph (7B: 28/4 heads of 128): 8 requests of 30,001 to 32,768 positions, 91 us,
+// 5.7 TB/s; 64 of 33 to 6,000, 83 us, 5.2 TB/s (HBM; without start and join about 6.2); 2,048
+// rows over 14,001, 326 us, 1,353 TFLOP/s, 4,096 over 28,672, 1,157 us, 1,559 TFLOP/s (tensor cores: 1.56 us a block
+// of two tiles, 1,637 TFLOP/s; the join of items that were cut, 15 us; starts and ends of pairs, 15 us).
+// One row over 2,049 positions, 0.5B, takes 11.5 us: the start 5 (three dependent loads, code that is
+// not in the instruction cache), a block and its join in the CTA 3, the second launch 3.
+// Joining the pieces at the end of the first launch, by the CTA that is last, was slower (its code costs the
+// loops registers: 366 us instead of 326), as was one tile for light rows with its blocks in
+// turn on both tiles' warps (98 us instead of 91).  What a product is told has to be made in uniform
+// registers: with a place in the ring that the warp counted itself, in a loop with branches, the chunks
+// took 1,300 us; it now comes with the piece.
+//
+// Barriers of the ring.  A warp that waits for a phase by its parity must never be two
+// phases away from it.  So who does not take part in a piece's blocks (products in light ones, light rows' warps
+// in others) waits, before it does again, until every role is done with the piece before.
 #include "q4_tiles.cuh"
 #include "q4mm_internal.h"
 
@@ -11,11 +58,11 @@ namespace {
 
 constexpr int SOFTMAX_WARPS = 16;
 constexpr int COPY_WARP = 16, MMA_WARP = 17, FIX_WARP = 19;  // and MMA_WARP + 1
-constexpr int LIGHT_WARPS = 8;  // warps 0-7
+constexpr int LIGHT_WARPS = 8;                               // warps 0-7
 constexpr int WORKS = 4;                                     // pieces that the roles may be at
 constexpr int THREADS = 640;
 constexpr int TMEM_COLS = 512;
-constexpr int LIGHT = 8;      // rows (positions times heads of a group) of a request that needs no tiles
+constexpr int LIGHT = 8;            // rows (positions times heads of a group) of a request that needs no tiles
 constexpr int WARP_REQUESTS = 128;  // requests up to which one warp finds a CTA's share
 
 // What a block of keys costs, and an item beside its blocks, in units of about a third of a
@@ -66,9 +113,8 @@ __device__ __forceinline__ int32_t ld_int(const int32_t* p) {
 __device__ __forceinline__ bool load_request(const Args& a, int s, Request* r) {
   const int b = ld_int(a.offsets + s), e = ld_int(a.offsets + s + 1);
   *r = Request{b, e - b, ld_int(a.pos + s), ld_int(a.slot + s)};
-  const bool ok = b >= 0 && e >= b && e <= a.total && r->slot >= 0 && r->slot < a.slots && r->past >= 0 &&
-                  (int64_t)r->past + r->rows <= a.width << a.shift;
-  return ok;
+  return b >= 0 && e >= b && e <= a.total && r->slot >= 0 && r->slot < a.slots && r->past >= 0 &&
+         (int64_t)r->past + r->rows <= a.width << a.shift;
 }
 
 // The key blocks of full pairs 0 .. n - 1 of a request: pair i sees up to position
@@ -98,7 +144,8 @@ __host__ __device__ __forceinline__ int64_t head_units(int past, int rows, int p
   const int step = 2 * positions, n = rows / step;
   int64_t blocks = n ? full_blocks(past, positions, n) : 0;
   if (rows % step) blocks += (past + rows - 1) / BN + 1;
-  return blocks * block_units(rows, positions, group) + (int64_t)((rows + step - 1) / step) * end_units(rows, positions, group);
+  return blocks * block_units(rows, positions, group) +
+         (int64_t)((rows + step - 1) / step) * end_units(rows, positions, group);
 }
 
 // All units in n equal shares.
@@ -130,14 +177,14 @@ struct Shares {
 
 // A share's piece of an item: blocks [b0, b1) of a pair of tiles of one head.
 struct Piece {
-  int ok;    // 0: there is no more
+  int ok;          // 0: there is no more
   int head, pos0;  // first row of tile 0 in the request
   Request r;
   int b0, b1;
-  int n;     // blocks (K and V) of the pieces before it
-  int part;  // where its sums go: -1: the whole item, straight to the output
-  bool last; // the item's last
-  int64_t first;  // the unit of the item's block 0
+  int n;           // blocks (K and V) of the pieces before it
+  int part;        // where its sums go: -1: the whole item, straight to the output
+  bool last;       // the item's last
+  int64_t first;   // the unit of the item's block 0
 };
 
 // What the roles derive from a piece.
@@ -242,16 +289,20 @@ struct Walk {
         base = s;
         load(a, lane);
       }
+      if (base >= a.S) break;
+      if (head == 0 && pair == 0) {  // the next request that has rows
+        const unsigned rest = __ballot_sync(0xFFFFFFFFu, r.rows > 0) >> (s - base);
+        if (!rest) {
+          s = base + 32;
+          continue;
+        }
+        s += __ffs(rest) - 1;
+      }
       const int l = s - base;
       w->r.qb = __shfl_sync(0xFFFFFFFFu, r.qb, l);
       w->r.rows = __shfl_sync(0xFFFFFFFFu, r.rows, l);
       w->r.past = __shfl_sync(0xFFFFFFFFu, r.past, l);
       w->r.slot = __shfl_sync(0xFFFFFFFFu, r.slot, l);
-      if ((int64_t)pair * step >= w->r.rows) {  // a request without rows
-        ++s;
-        head = pair = 0;
-        continue;
-      }
       w->ok = 1;
       w->head = head;
       w->pos0 = pair * step;

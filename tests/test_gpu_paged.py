@@ -338,6 +338,17 @@ def test_counts_of_requests(q4, S):
     s.check(s.run())
 
 
+@pytest.mark.parametrize("S", [100, 5000])
+def test_requests_without_rows(q4, S):
+    # a padded step: most requests bring nothing, runs of them lie between the others and at both ends
+    rows = [0] * S
+    for i, n in ((3, 1), (35, 40), (36, 1), (S // 2, 5), (S - 20, 300), (S - 2, 1)):
+        rows[i] = n
+    past = [(i * 7) % 900 if n else 0 for i, n in enumerate(rows)]
+    s = Step(q4, 33, past, rows, 2, 14, 64, 16, torch.bfloat16, gap=1)
+    s.check(s.run())
+
+
 @pytest.mark.parametrize("rows", [1, 7, 8, 9, 64, 126, 127, 128, 129, 255, 256, 257])
 @pytest.mark.parametrize("heads,hq", [(2, 2), (1, 8), (1, 7)])
 def test_rows_at_the_borders_of_tiles(q4, rows, heads, hq):
