@@ -1263,9 +1263,11 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // ---- the pieces of items that were cut, joined ----
-//   out = sum_i f_i O_i / sum_i f_i l_i,  f_i = 2^(reference_i - largest reference)
-// Two rows a warp at a time; a row's references lie in its lanes, 32 pieces at a
-// time.  Bound by latency: the first pieces' sums are loaded beside the references.
+//   out = sum_k f_k O_k / sum_k f_k l_k,  f_k = 2^(reference_k - largest reference)
+// A warp a row, whose references lie in its lanes, 32 pieces at a time.  Bound by latency: the
+// first pieces' sums are loaded beside the references.  One row of 17 pieces takes 3 us, 76 items of
+// two tiles 15 (39 MB of sums; two or four rows a warp at once took 1 to 10 us more, as did
+// factors that every lane makes for itself, all for fewer warps on an SM).
 constexpr int JOIN_WARPS = 8, JOIN_CTAS = 8;  // CTAs for each share
 
 template <int D, typename T>
@@ -1276,91 +1278,71 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) paged_join_kernel(const Args 
   const PagedJoin j{d.x, d.y, d.z, d.w};
   const int lane = threadIdx.x & 31, G = a.group, P = a.positions;
   const int rows = j.pieces ? j.rows * G : 0, c0 = (int)blockIdx.x - j.pieces + 1;
-  constexpr int V = D / 32, ROWS = 1, EARLY = 4;  // values of a lane; rows of a warp; pieces loaded early
-  auto load = [&](float (&x)[V], int64_t place) {
-    const float* p = a.ws.partial + place * D + lane * V;
-    if constexpr (V == 4) {
-      const float4 y = __ldcg(reinterpret_cast<const float4*>(p));
-      x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
-    } else {
-      const float2 y = __ldcg(reinterpret_cast<const float2*>(p));
-      x[0] = y.x, x[1] = y.y;
-    }
-  };
-  for (int i0 = (blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5)) * ROWS; i0 < rows; i0 += JOIN_CTAS * JOIN_WARPS * ROWS) {
+  constexpr int V = D / 32, EARLY = 4;  // values of a lane; pieces loaded early
+  for (int i = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5); i < rows; i += JOIN_CTAS * JOIN_WARPS) {
     // row i of the item: position i / G, in tile 0 or 1
-    int64_t base[ROWS];
-    int pos[ROWS], head[ROWS];
-#pragma unroll
-    for (int u = 0; u < ROWS; ++u) {
-      const int i = min(i0 + u, rows - 1);
-      pos[u] = i / G;
-      head[u] = i - pos[u] * G;
-      const int t = pos[u] >= P ? 1 : 0;
-      base[u] = (int64_t)(4 * c0 + t) * BM + (pos[u] - t * P) * G + head[u];
-    }
-    auto place = [&](int u, int k) { return base[u] + (4 * k + (k == 0 ? 2 : 0)) * BM; };  // piece k: the first is its share's last
-    float4 ml[ROWS];
-    float early[ROWS][EARLY][V];
-#pragma unroll
-    for (int u = 0; u < ROWS; ++u) ml[u] = lane < j.pieces ? __ldcg(a.ws.ml + place(u, lane)) : make_float4(0, 0, 0, 0);
-#pragma unroll
-    for (int u = 0; u < ROWS; ++u)
-#pragma unroll
-      for (int k = 0; k < EARLY; ++k)
-        if (k < j.pieces) load(early[u][k], place(u, k));
-    Reference top[ROWS];
-#pragma unroll
-    for (int u = 0; u < ROWS; ++u) {
-      top[u].take(ml[u].x, ml[u].y, ml[u].z);
-      for (int k = lane + 32; k < j.pieces; k += 32) {
-        const float4 x = __ldcg(a.ws.ml + place(u, k));
-        top[u].take(x.x, x.y, x.z);
+    const int pos = i / G, head = i - pos * G, t = pos >= P ? 1 : 0;
+    const int64_t base = (int64_t)(4 * c0 + t) * BM + (pos - t * P) * G + head;
+    auto place = [&](int k) { return base + (4 * k + (k == 0 ? 2 : 0)) * BM; };  // piece k: the first is its share's last
+    auto load = [&](float (&x)[V], int k) {
+      const float* p = a.ws.partial + place(k) * D + lane * V;
+      if constexpr (V == 4) {
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(p));
+        x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
+      } else {
+        const float2 y = __ldcg(reinterpret_cast<const float2*>(p));
+        x[0] = y.x, x[1] = y.y;
       }
+    };
+    float l = 0.0f, o[V] = {};
+    auto add = [&](float f, float lk, const float (&x)[V]) {
+      l += f * lk;
 #pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        top[u].ref = fmaxf(top[u].ref, __shfl_xor_sync(0xFFFFFFFFu, top[u].ref, o));
-        top[u].far = fmaxf(top[u].far, __shfl_xor_sync(0xFFFFFFFFu, top[u].far, o));
-      }
+      for (int e = 0; e < V; ++e) o[e] += f == 0.0f ? 0.0f : f * x[e];  // pieces of nothing have not been written
+    };
+    auto references = [&](int k) { return k < j.pieces ? __ldcg(a.ws.ml + place(k)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f); };
+    float4 ml = references(lane);
+    float early[EARLY][V];
+#pragma unroll
+    for (int k = 0; k < EARLY; ++k)
+      if (k < j.pieces) load(early[k], k);
+    Reference top;
+    top.take(ml.x, ml.y, ml.z);
+    for (int k = lane + 32; k < j.pieces; k += 32) {
+      const float4 x = references(k);
+      top.take(x.x, x.y, x.z);
     }
 #pragma unroll
-    for (int u = 0; u < ROWS; ++u) {
-      float l = 0.0f, o[V] = {};
-      auto add = [&](float f, float lk, const float (&x)[V]) {
-        l += f * lk;
+    for (int n = 16; n; n >>= 1) {
+      top.ref = fmaxf(top.ref, __shfl_xor_sync(0xFFFFFFFFu, top.ref, n));
+      top.far = fmaxf(top.far, __shfl_xor_sync(0xFFFFFFFFu, top.far, n));
+    }
+    for (int k0 = 0; k0 < j.pieces; k0 += 32) {
+      if (k0 > 0) ml = references(k0 + lane);
+      const float lk = ml.x, f = top.factor(lk, ml.y, ml.z, a.scale_log2);
+      const int n = min(32, j.pieces - k0);
+      int k = 0;
+      if (k0 == 0) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) o[e] += f == 0.0f ? 0.0f : f * x[e];  // pieces of nothing have not been written
-      };
-      for (int k0 = 0; k0 < j.pieces; k0 += 32) {
-        if (k0 > 0) ml[u] = k0 + lane < j.pieces ? __ldcg(a.ws.ml + place(u, k0 + lane)) : make_float4(0, 0, 0, 0);
-        const float lk = ml[u].x, f = top[u].factor(lk, ml[u].y, ml[u].z, a.scale_log2);
-        const int n = min(32, j.pieces - k0);
-        int k = 0;
-        if (k0 == 0) {
-#pragma unroll
-          for (int e = 0; e < EARLY; ++e) {
-            const float fk = __shfl_sync(0xFFFFFFFFu, f, e), lkk = __shfl_sync(0xFFFFFFFFu, lk, e);
-            if (e < n) add(fk, lkk, early[u][e]);
-          }
-          k = EARLY;
+        for (int e = 0; e < EARLY; ++e) {
+          const float fk = __shfl_sync(0xFFFFFFFFu, f, e), lkk = __shfl_sync(0xFFFFFFFFu, lk, e);
+          if (e < n) add(fk, lkk, early[e]);
         }
+        k = EARLY;
+      }
 #pragma unroll 4
-        for (; k < n; ++k) {
-          float x[V];
-          load(x, place(u, k0 + k));
-          add(__shfl_sync(0xFFFFFFFFu, f, k), __shfl_sync(0xFFFFFFFFu, lk, k), x);
-        }
-      }
-      if (i0 + u < rows) {
-        const float inv = 1.0f / l;
-        T* dst = static_cast<T*>(a.out) + ((int64_t)(j.row + pos[u]) * a.q_heads + j.head * G + head[u]) * D + lane * V;
-        if constexpr (V == 4)
-          *reinterpret_cast<uint2*>(dst) =
-              make_uint2(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv));
-        else
-          *reinterpret_cast<uint32_t*>(dst) = pack2<T>(o[0] * inv, o[1] * inv);
+      for (; k < n; ++k) {
+        float x[V];
+        load(x, k0 + k);
+        add(__shfl_sync(0xFFFFFFFFu, f, k), __shfl_sync(0xFFFFFFFFu, lk, k), x);
       }
     }
+    const float inv = 1.0f / l;
+    T* dst = static_cast<T*>(a.out) + ((int64_t)(j.row + pos) * a.q_heads + j.head * G + head) * D + lane * V;
+    if constexpr (V == 4)
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv));
+    else
+      *reinterpret_cast<uint32_t*>(dst) = pack2<T>(o[0] * inv, o[1] * inv);
   }
 }
 

@@ -805,7 +805,7 @@ const char* q4_status_string(int status) {
     case Q4_ERR_RANGE: return "block scale out of binary16 range";
     case Q4_ERR_CUDA: return "CUDA runtime error";
     case Q4_ERR_TIMEOUT: return "device-side wait timed out";
-    case Q4_ERR_NOMEM: return "device allocation failed";
+    case Q4_ERR_NOMEM: return "device allocation failed, or no pages left";
     case Q4_ERR_UNSUPPORTED: return "unsupported device or path";
     default: return "unknown status";
   }
