@@ -494,6 +494,7 @@ Q4_API int q4_prompt_attention(const void* q, const void* k, const void* v, void
  * requests of the call, whose positions pass width * page_size, or that begin
  * past the pages their slot has; all of them where offsets decrease or pass total, or
  * the pool holds more pages than there are.
+ * A page number out of range in the table or the list gives -1 in slot_map (INVALID_ARG).
  * S at most 8192, slots at most 65536 (SHAPE).  Asynchronous on stream. */
 Q4_API int q4_paged_reserve(int32_t* table, int32_t* held, int32_t* free_list, int32_t* free_count,
                             int64_t slots, int64_t width, int64_t pages, int64_t page_size,
