@@ -602,6 +602,30 @@ def test_beside_the_other_attentions(q4):
     assert q4.q4_device_status() == q4.Q4_OK
 
 
+def test_the_binding_refuses(q4):
+    s = Step(q4, 170, [10, 3], [1, 2], 2, 4, 64, 16, torch.bfloat16)
+    q, off, slot, pos = s.q.cuda(), _i32(s.offsets), _i32(s.slot), _i32(s.past)
+    attend = q4.q4_paged_attention
+    other = q4.Q4PageTable(4, 3, s.cache.pages, 32)
+    for bad in (lambda: attend(s.cache, s.tables, q.half(), off, slot, pos),
+                lambda: attend(s.cache, s.tables, s.q, off, slot, pos),
+                lambda: attend(s.cache, other, q, off, slot, pos),
+                lambda: attend(s.cache, s.tables, q[:, :3], off, slot, pos),
+                lambda: attend(s.cache, s.tables, q, off[:2], slot, pos),
+                lambda: attend(s.cache, s.tables, q, off, slot.long(), pos),
+                lambda: attend(s.cache, s.tables, q.transpose(1, 2), off, slot, pos),
+                lambda: attend(s.cache, s.tables, q, off, slot, pos, out=torch.empty_like(q)[:1]),
+                lambda: q4.q4_paged_append(s.cache, q[:, :2], q[:, 2:], _i32([0, 1])),
+                lambda: q4.q4_paged_append(s.cache, q[:, :2].half(), q[:, 2:].half(), _i32([0, 1, 2])),
+                lambda: q4.q4_paged_append(s.cache, q[:, :2], q[:2, 2:], _i32([0, 1, 2])),
+                lambda: q4.q4_paged_reserve(s.tables, off, slot, pos[:1], 3),
+                lambda: q4.q4_paged_reserve(s.tables, off, slot, pos, 3, slot_map=_i32([0, 0]))):
+        with pytest.raises((ValueError, q4.Q4Error)):
+            bad()
+    assert q4.q4_device_status() == q4.Q4_OK
+    s.check(s.run())
+
+
 # ---------------------------------------------------------------- together
 
 @pytest.mark.parametrize("dtype", TYPES)
