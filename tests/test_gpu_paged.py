@@ -545,6 +545,59 @@ def test_pages_past_32_bits(q4):
            torch.bfloat16, "last pages")
 
 
+def test_a_long_chunk_that_fills_its_table(q4):
+    n, past, d, page = 40000, 960, 64, 64
+    total = n + past
+    cache = q4.Q4PagedCache(total // page, 1, d, page)
+    tables = q4.Q4PageTable(1, total // page, total // page, page)
+    slot_map, length = q4.q4_paged_reserve(tables, _i32([0, total]), _i32([0]), _i32([0]), total)
+    assert length.tolist() == [total] and torch.equal(slot_map, torch.arange(total, dtype=torch.int32, device="cuda"))
+    k, v, q = (_normal(180 + i, (m, h, d), torch.bfloat16) for i, (m, h) in enumerate(((total, 1), (total, 1), (n, 2))))
+    q4.q4_paged_append(cache, k.cuda(), v.cuda(), slot_map)
+    out = q4.q4_paged_attention(cache, tables, q.cuda(), _i32([0, n]), _i32([0]), _i32([past])).cpu().double().numpy()
+    assert q4.q4_device_status() == q4.Q4_OK
+    k, v, q = (x.double().numpy() for x in (k, v, q))
+    for i in (0, 1, 63, 64, 127, 128, 5000, 12345, 20031, 39999):
+        _check(out[i:i + 1], q[i:i + 1], k[:past + i + 1], v[:past + i + 1], past + i, d ** -0.5, torch.bfloat16, "row %d" % i)
+
+
+def test_a_whole_step_in_a_graph(q4):
+    """Pages, rows and attention of two decoding requests captured once; each replay is a step further."""
+    heads, hq, d, page, steps = 2, 14, 64, 16, 40
+    tables = q4.Q4PageTable(3, 8, 20, page)
+    cache = q4.Q4PagedCache(20, heads, d, page)
+    k, v, q = (_normal(190 + i, (steps + 1, 2, h, d), torch.bfloat16).cuda() for i, h in enumerate((heads, heads, hq)))
+    off, slot, pos = _i32([0, 1, 2]), _i32([2, 0]), _i32([0, 0])
+    now = [torch.empty_like(x[0]) for x in (k, v, q)]
+
+    def step():
+        slot_map, length = q4.q4_paged_reserve(tables, off, slot, pos, 2)
+        q4.q4_paged_append(cache, now[0], now[1], slot_map)
+        out = q4.q4_paged_attention(cache, tables, now[2], off, slot, pos)
+        pos.copy_(length)
+        return out
+
+    def feed(i):
+        for x, y in zip(now, (k, v, q)):
+            x.copy_(y[i])
+
+    feed(0)
+    first = step().clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step()
+    got = [first]
+    for i in range(1, steps + 1):
+        feed(i)
+        g.replay()
+        got.append(out.clone())
+    assert q4.q4_device_status() == q4.Q4_OK and pos.tolist() == [steps + 1] * 2
+    o = torch.stack(got).cpu().double().numpy()
+    kk, vv, qq = (x.cpu().double().numpy() for x in (k, v, q))
+    for r in range(2):
+        _check(o[:, r], qq[:, r], kk[:, r], vv[:, r], 0, d ** -0.5, torch.bfloat16, "request %d" % r)
+
+
 @pytest.mark.parametrize("past,rows", [([3000, 40], [1, 1]), ([500, 900], [300, 1]), ([300], [20])])
 def test_waits_that_run_out(q4, past, rows):
     """No copy is issued, so every wait for one runs out: the status says so, and later calls are right."""
