@@ -629,23 +629,23 @@ __global__ void __launch_bounds__(THREADS, 1)
                            kv ? (const void*)&map_v : (const void*)&map_k, 0, 0, 0, at, full + 8 * (st + kv));
             __syncwarp();
             if (ok) n += 2;
-            continue;
-          }
-          for (int kv = 0; kv < 2 && ok; ++kv) {
-            const int st = n % NST;
-            if (lane == 0) {
-              if (n >= NST) ok = mbar_wait(empty + 8 * st, ((n / NST) - 1) & 1, err, a.wait_ns);
-              if (ok && !a.stall) {
-                mbar_expect_tx(full + 8 * st, (uint32_t)here * page_bytes);
-                if (kv && i >= p.zone) mbar_arrive(hidden + 8 * st);  // tells V's warp, which only waits for these
+          } else {
+            for (int kv = 0; kv < 2 && ok; ++kv) {
+              const int st = n % NST;
+              if (lane == 0) {
+                if (n >= NST) ok = mbar_wait(empty + 8 * st, ((n / NST) - 1) & 1, err, a.wait_ns);
+                if (ok && !a.stall) {
+                  mbar_expect_tx(full + 8 * st, (uint32_t)here * page_bytes);
+                  if (kv && i >= p.zone) mbar_arrive(hidden + 8 * st);  // tells V's warp, which only waits for these
+                }
               }
+              ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0) != 0;
+              if (ok && !a.stall && lane < here)
+                tensor_load4(ring + st * C::TILE + lane * page_bytes, kv ? (const void*)&map_v : (const void*)&map_k, 0,
+                             0, 0, at, full + 8 * st);
+              __syncwarp();
+              if (ok) ++n;
             }
-            ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0) != 0;
-            if (ok && !a.stall && lane < here)
-              tensor_load4(ring + st * C::TILE + lane * page_bytes, kv ? (const void*)&map_v : (const void*)&map_k, 0,
-                           0, 0, at, full + 8 * st);
-            __syncwarp();
-            if (ok) ++n;
           }
         }
       }
