@@ -375,11 +375,13 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 template <typename T>
 __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if constexpr (std::is_same<T, __half>::value)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+                 "{%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+                 "{%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -451,7 +453,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   // ---- the CTA's share of the units: each of `threads` threads has a run of requests ----
   // Few requests are looked through by the warp that copies; the others need not wait for it.
   const bool by_warp = a.S <= WARP_REQUESTS;
-  int s_first_ = 0;
+  int first_s = 0;
   int64_t rem = 0, all = 0;
   if (!by_warp || warp == COPY_WARP) {
     const int threads = by_warp ? 32 : THREADS, thread = by_warp ? lane : tid;
@@ -483,28 +485,28 @@ __global__ void __launch_bounds__(THREADS, 1)
     const bool mine = u0 >= before && u0 < before + units;
     if (mine) {
       rem = u0 - before;
-      s_first_ = s_begin;
+      first_s = s_begin;
       for (int s = s_begin; s < s_end - 1; ++s) {
         const int64_t u = units_of(s, &bad);
         if (rem < u) break;
         rem -= u;
-        ++s_first_;
+        ++first_s;
       }
     }
     if (by_warp) {
       const int l = __ffs(__ballot_sync(0xFFFFFFFFu, mine)) - 1;
-      s_first_ = __shfl_sync(0xFFFFFFFFu, s_first_, l);
+      first_s = __shfl_sync(0xFFFFFFFFu, first_s, l);
       rem = __shfl_sync(0xFFFFFFFFu, rem, l);
     } else {
       if (mine) {
-        s_first = s_first_;
+        s_first = first_s;
         s_rem = rem;
       }
       __syncthreads();
       if (s_bad || ld_int(a.offsets) > 0 || ld_int(a.offsets + a.S) < a.total)
         clear_rows<D>(a, s_bad != 0, (int64_t)blockIdx.x * THREADS + tid, (int64_t)gridDim.x * THREADS);
       if (tid == 0 && s_bad && blockIdx.x == 0) atomicOr(a.status, STATUS_KV_RANGE);
-      s_first_ = s_first;
+      first_s = s_first;
       rem = s_rem;
     }
   }
@@ -527,7 +529,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       Walk walk;
       walk.left = 0;
       if ((int)blockIdx.x < shares.n && all > 0)
-        walk.begin(a, s_first_, rem, shares.begin(blockIdx.x), shares.begin(blockIdx.x + 1), lane);
+        walk.begin(a, first_s, rem, shares.begin(blockIdx.x), shares.begin(blockIdx.x + 1), lane);
       PagedJoin join{0, 0, 0, 0};  // the item whose last piece this share has
       int64_t join_first = 0;
       int n = 0, nq = 0;  // blocks and Q pairs so far
@@ -564,7 +566,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           mbar_arrive(work_full + 8 * (nth % WORKS));
         }
         if (light_before && !p.light)  // the light rows' sums lie where tile 1's rows go
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait(work_empty + 8 * ((nth - 1) % WORKS), ((nth - 1) / WORKS) & 1, err, a.wait_ns));
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(work_empty + 8 * ((nth - 1) % WORKS), ((nth - 1) / WORKS) & 1, err,
+                                                 a.wait_ns));
         light_before = p.light;
         ++nth;
         if (!ok) break;
@@ -1028,7 +1031,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, d);
       }
       tile_sync(0);
-      float* const sums = reinterpret_cast<float*>(smem_p + C::TILE);  // [warp][8 rows][D], columns turned so that banks differ
+      // [warp][8 rows][D], columns turned so that banks differ
+      float* const sums = reinterpret_cast<float*>(smem_p + C::TILE);
 #pragma unroll
       for (int d = 0; d < D / 16; ++d) {
         float* row = sums + (warp * 8 + 2 * tq) * D;
