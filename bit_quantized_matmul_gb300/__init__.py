@@ -712,6 +712,7 @@ def q4_paged_attention(cache: Q4PagedCache, tables: Q4PageTable, q: torch.Tensor
 
     Row j of request s sees positions 0 .. pos[s] + j of its slot (append the step's rows first):
     single tokens, drafts and chunks of prompts in one call.  scale defaults to 1 / sqrt(head_dim).
+    A request that ``q4_paged_reserve`` refused for want of pages gets zeros.
     out may be q itself (contiguous), and overlaps nothing else.  Uses the library's
     scratch, which the device's streams share: order calls on one stream.  The first call allocates some.
     """

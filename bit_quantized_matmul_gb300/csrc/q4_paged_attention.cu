@@ -175,6 +175,17 @@ struct Shares {
   }
 };
 
+// Beside a join's pieces: some piece of the share had a page number out of range.
+constexpr int JOIN_WILD = 1 << 30;
+
+// Where the table has the page of a request's last position.  It is -1 where reserve refused the request for want of
+// pages: tables begin as -1, and entries past what a slot holds stay so.  The copies take -1 as any number out
+// of range; such requests are looked for after them, since telling them apart any earlier costs the loops
+// registers (8 requests of 32k 94 us instead of 91, four chunks 167 instead of 160).
+__device__ __forceinline__ int64_t last_entry(const Args& a, const Request& r) {
+  return (int64_t)r.slot * a.width + ((r.past + r.rows - 1) >> a.shift);
+}
+
 // A share's piece of an item: blocks [b0, b1) of a pair of tiles of one head.
 struct Piece {
   int ok;          // 0: there is no more
@@ -395,6 +406,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   constexpr int NST = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Piece work[WORKS];
+  __shared__ PagedJoin s_join;  // the item whose last piece this share has
+  __shared__ int64_t s_join_first, s_join_last;
   __shared__ int s_err, s_bad, s_first, s_nonfinite[WORKS];
   __shared__ int64_t s_rem, s_scan[THREADS / 32];
   __shared__ float s_max[2][2][BM], s_sum[2][2][BM];  // [tile][half][row]: what the halves exchange
@@ -440,6 +453,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_arrive(turn);  // tile 0 begins
     s_err = 0;
     s_bad = 0;
+    s_join = PagedJoin{0, 0, 0, 0};
     mbar_init_fence();
   }
   if (warp == MMA_WARP) tmem_alloc(smem_u32(&s_tmem), TMEM_COLS);
@@ -530,8 +544,6 @@ __global__ void __launch_bounds__(THREADS, 1)
       walk.left = 0;
       if ((int)blockIdx.x < shares.n && all > 0)
         walk.begin(a, first_s, rem, shares.begin(blockIdx.x), shares.begin(blockIdx.x + 1), lane);
-      PagedJoin join{0, 0, 0, 0};  // the item whose last piece this share has
-      int64_t join_first = 0;
       int n = 0, nq = 0;  // blocks and Q pairs so far
       int nth = 0;        // pieces so far
       bool ok = true, wild = false;
@@ -590,8 +602,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (ok) ++nq;
         const uint32_t page_bytes = (uint32_t)(D * 2) << a.shift;
         const int page_groups = 1 << (a.shift - 3);
-        if (w.part >= 0 && w.last) join = PagedJoin{0, w.r.qb + w.pos0, min(2 * P, w.r.rows - w.pos0), w.head};
-        if (w.part >= 0 && w.last) join_first = w.first;
+        if (w.part >= 0 && w.last && lane == 0) {
+          s_join = PagedJoin{0, w.r.qb + w.pos0, min(2 * P, w.r.rows - w.pos0), w.head};
+          s_join_first = w.first;
+          s_join_last = last_entry(a, w.r);
+        }
         for (int i = w.b0; i < w.b1 && ok; ++i) {
           if (i == min(w.b0 + NST / 2, w.b1 - 1)) {  // the ring is full: the next piece, whose numbers are then on their way
             more = walk.next(a, blockIdx.x, lane, &then);
@@ -662,11 +677,14 @@ __global__ void __launch_bounds__(THREADS, 1)
           mbar_arrive(work_full + 8 * (nth % WORKS));
         }
       }
+      wild = __any_sync(0xFFFFFFFFu, wild);  // of what kind the second launch finds out
       if (lane == 0) {
-        if (join.rows) join.pieces = (int)blockIdx.x - shares.of(join_first) + 1;
+        PagedJoin join = s_join;
+        if (join.rows && ld_int(a.table + s_join_last) != -1)  // a refused request's rows are cleared
+          join.pieces = (int)blockIdx.x - shares.of(s_join_first) + 1;
+        if (wild) join.pieces |= JOIN_WILD;
         a.ws.joins[blockIdx.x] = join;
       }
-      if (__any_sync(0xFFFFFFFFu, wild) && lane == 0) atomicOr(a.status, STATUS_KV_RANGE);
       // the copies in flight land before the CTA ends, also when another role has given up
       if (nq > 0) mbar_wait_warp(q_full, (nq - 1) & 1, a.wait_ns);
       for (int v = max(0, n - NST); v < n; ++v) mbar_wait_warp(full + 8 * (v % NST), (v / NST) & 1, a.wait_ns);
@@ -1299,13 +1317,38 @@ __global__ void __launch_bounds__(THREADS, 1)
 // factors that every lane makes for itself, all for fewer warps on an SM).
 constexpr int JOIN_WARPS = 8, JOIN_CTAS = 8;  // CTAs for each share
 
+// For a share that met a page number out of range: the rows of requests that reserve refused become zeros, whatever the
+// first launch made of the pages that they have (the share that has a request's last position meets its -1),
+// and the status says what there was.  A warp a request; shares that come here together write the same.
+template <int D>
+__device__ __noinline__ void find_wild(const Args& a, int warp, int lane) {
+  const int64_t row = (int64_t)a.q_heads * D / 8;  // 16-byte vectors of a packed row
+  for (int s = warp; s < a.S; s += JOIN_CTAS * JOIN_WARPS) {
+    Request r;
+    if (!load_request(a, s, &r) || r.rows == 0) continue;
+    if (ld_int(a.table + last_entry(a, r)) == -1) {
+      uint4* p = static_cast<uint4*>(a.out) + r.qb * row;
+      for (int64_t i = lane; i < r.rows * row; i += 32) p[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (lane == 0) atomicOr(a.status, STATUS_PAGES);
+      continue;
+    }
+    bool wild = false;
+    for (int64_t i = (int64_t)r.slot * a.width + lane; i <= last_entry(a, r); i += 32) {
+      const int id = ld_int(a.table + i);
+      wild |= id < 0 || id >= a.pages;
+    }
+    if (__any_sync(0xFFFFFFFFu, wild) && lane == 0) atomicOr(a.status, STATUS_KV_RANGE);
+  }
+}
+
 template <int D, typename T>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) paged_join_kernel(const Args a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int4 d = __ldcg(reinterpret_cast<const int4*>(a.ws.joins + blockIdx.x));
-  const PagedJoin j{d.x, d.y, d.z, d.w};
+  const PagedJoin j{d.x & ~JOIN_WILD, d.y, d.z, d.w};
   const int lane = threadIdx.x & 31, G = a.group, P = a.positions;
+  if (d.x & JOIN_WILD) find_wild<D>(a, blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5), lane);
   const int rows = j.pieces ? j.rows * G : 0, c0 = (int)blockIdx.x - j.pieces + 1;
   constexpr int V = D / 32, EARLY = 4;  // values of a lane; pieces loaded early
   for (int i = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5); i < rows; i += JOIN_CTAS * JOIN_WARPS) {

@@ -475,8 +475,8 @@ Q4_API int q4_prompt_attention(const void* q, const void* k, const void* v, void
  * After it slot[s] has ceil((pos[s] + rows of s) / page_size) pages: surplus ones (of
  * requests that ended, pos = 0 without rows, or were cut back) return to the
  * free list, and a request that grows past its last page is given others.
- *   table       device, int32 [slots, width]: each slot's pages, in order; entries
- *               of pages that went back become -1.
+ *   table       device, int32 [slots, width], -1 at first: each slot's pages, in
+ *               order; entries of pages that went back become -1.
  *   held        device, int32 [slots]: the pages that each slot has (0 at first).
  *   free_list   device, int32 [pages]: the pages that nobody has are its first
  *               *free_count entries (at first all of 0 .. pages - 1, in any order).
@@ -535,9 +535,12 @@ Q4_API int q4_paged_append(void* k_pages, void* v_pages, int cache_dtype, const 
  * requests; the same call gives the same bits.  A request that is out of range (its
  * slot, its rows, or positions past width * page_size) gets zeros, a page
  * number out of range reads as zeros, and q4_device_status then reports
- * INVALID_ARG.  Uses the library's scratch: order calls on one stream.  The first
- * call of a head_dim may allocate some (about 62 MB at 128).  Needs sm_103
- * (UNSUPPORTED). */
+ * INVALID_ARG.  A request whose last position has page number -1, as
+ * q4_paged_reserve leaves it where pages ran out, gets zeros, and q4_device_status
+ * reports NOMEM: a step's calls need not wait to hear who was refused.  (A slot in two
+ * requests, which reserve refuses with INVALID_ARG, is read as the table stands.)
+ * Uses the library's scratch: order calls on one stream.  The first call of a
+ * head_dim may allocate some (about 62 MB at 128).  Needs sm_103 (UNSUPPORTED). */
 Q4_API int q4_paged_attention(const void* k_pages, const void* v_pages, const void* q, void* out, int dtype,
                               int64_t pages, int64_t heads, int64_t q_heads, int64_t head_dim, int64_t page_size,
                               const int64_t* q_strides, float scale, const int32_t* table, int64_t slots,
