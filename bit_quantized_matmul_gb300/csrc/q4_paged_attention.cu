@@ -112,7 +112,7 @@ __device__ __forceinline__ int32_t ld_int(const int32_t* p) {
 
 __device__ __forceinline__ bool load_request(const Args& a, int s, Request* r) {
   const int b = ld_int(a.offsets + s), e = ld_int(a.offsets + s + 1);
-  *r = Request{b, e - b, ld_int(a.pos + s), ld_int(a.slot + s)};
+  *r = Request{b, (int)((unsigned)e - (unsigned)b), ld_int(a.pos + s), ld_int(a.slot + s)};
   return b >= 0 && e >= b && e <= a.total && r->slot >= 0 && r->slot < a.slots && r->past >= 0 &&
          (int64_t)r->past + r->rows <= a.width << a.shift;
 }
@@ -246,7 +246,7 @@ __device__ void clear_rows(const Args& a, bool bad, int64_t thread, int64_t thre
   clear(ld_int(a.offsets + a.S), a.total);
   for (int s = 0; bad && s < a.S; ++s) {
     Request r;
-    if (!load_request(a, s, &r)) clear(r.qb, (int64_t)r.qb + r.rows);
+    if (!load_request(a, s, &r)) clear(r.qb, ld_int(a.offsets + s + 1));  // its count of rows may pass 32 bits
   }
 }
 
