@@ -656,6 +656,8 @@ class Q4PagedCache:
 
     def __init__(self, pages: int, heads: int, head_dim: int, page_size: int, dtype=torch.bfloat16, device=None):
         self.pages, self.heads, self.head_dim, self.page_size = int(pages), int(heads), int(head_dim), int(page_size)
+        if min(self.pages, self.heads) < 1 or self.head_dim not in (64, 128) or self.page_size not in (16, 32, 64, 128):
+            raise ValueError("pages and heads must be positive, head_dim 64 or 128 and page_size 16, 32, 64 or 128")
         if dtype not in (torch.float16, torch.bfloat16):
             raise ValueError("dtype must be float16 or bfloat16")
         device = torch.device("cuda" if device is None else device)
