@@ -716,7 +716,8 @@ def q4_paged_attention(cache: Q4PagedCache, tables: Q4PageTable, q: torch.Tensor
     single tokens, drafts and chunks of prompts in one call.  scale defaults to 1 / sqrt(head_dim).
     A request that ``q4_paged_reserve`` refused for want of pages gets zeros.
     out may be q itself (contiguous), and overlaps nothing else.  Uses the library's
-    scratch, which the device's streams share: order calls on one stream.  The first call allocates some.
+    scratch, which the device's streams share: order calls on one stream.  The first call allocates some, so it
+    cannot be one that is captured.
     """
     S = _step(cache, offsets, slot, pos)
     pages, heads, d, page = cache._dims

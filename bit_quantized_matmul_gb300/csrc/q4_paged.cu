@@ -9,8 +9,8 @@
 // so every page has its place without any order between the threads, and the
 // same step on the same state always gives the same tables.  A packed row finds its page
 // the same way, so the slot map does not wait for the tables; the row that begins a page enters it.
-// Bound by latency: a few dependent loads and three barriers.  One CTA for a decode
-// step (64 requests: 4 us in a graph); from 4,096 rows and requests on a cluster of eight, each of
+// Bound by latency: a few dependent loads and nine barriers of 1,024 threads, four more for every further
+// 1,024 requests (two a sum).  One CTA for a decode step (64 requests: 4 us in a graph); from 4,096 rows and requests on a cluster of eight, each of
 // which makes the sums for itself (they are cheap) and takes a share of the rows (512 requests with
 // 47,886 rows: 12 us; with one row or page of a thread on its way at a time 14).
 //

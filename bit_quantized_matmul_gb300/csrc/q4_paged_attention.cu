@@ -35,10 +35,18 @@
 // keys and then values along m, a running reference and sums of their own, joined in
 // shared memory at the end.  Their work hides behind the copies: without it the calls below take 1.5 us less.
 //
+// Weights are rounded to the cache's type for the product with V: tcgen05 takes both operands in one 16-bit type, and light
+// rows keep to it.  Sums of weights keep the unrounded ones.  A weight is off by 2^-8 (bf16) or 2^-11 of itself at most,
+// and the error of the whole result against 64 bits is 2.1e-3 instead of the 1.7e-3 that rounding the output alone
+// makes (64 rows, bf16; chunks 2.3e-3; fp16 2.9e-4 instead of 2.1e-4).  A second term for light rows' weights, of what
+// the rounding took, brings them to 1.7e-3 and takes 90 us instead of 84 (64 rows), 180 instead of 160 (four chunks
+// beside 60 rows).
+//
 // Bounds, measured in a graph (7B: 28/4 heads of 128): 8 requests of 30,001 to 32,768 positions, 91 us,
 // 5.7 TB/s; 64 of 33 to 6,000, 83 us, 5.2 TB/s (HBM; without start and join about 6.2); 2,048
-// rows over 14,001, 326 us, 1,353 TFLOP/s, 4,096 over 28,672, 1,157 us, 1,559 TFLOP/s (tensor cores: 1.56 us a block
-// of two tiles, 1,637 TFLOP/s; the join of items that were cut, 15 us; starts and ends of pairs, 15 us).
+// rows over 14,001, 326 us, 1,353 TFLOP/s, 4,096 over 28,672, 1,170 us, 1,542 TFLOP/s (tensor cores: 1.56 us a block
+// of two tiles, 1,637 TFLOP/s; the join of items that were cut, 15 us; starts and ends of pairs, 15 us).  The compiler still
+// spills 24 bytes a thread at heads of 128, 32 at 64.
 // One row over 2,049 positions, 0.5B, takes 11.5 us: the start 5 (three dependent loads, code that is
 // not in the instruction cache), a block and its join in the CTA 3, the second launch 3.
 // Joining the pieces at the end of the first launch, by the CTA that is last, was slower (its code costs the
@@ -65,8 +73,11 @@ constexpr int TMEM_COLS = 512;
 constexpr int LIGHT = 8;            // rows (positions times heads of a group) of a request that needs no tiles
 constexpr int WARP_REQUESTS = 128;  // requests up to which one warp finds a CTA's share
 
-// What a block of keys costs, and an item beside its blocks, in units of about a third of a
-// microsecond: of light rows, of one tile (a chain of products and softmax) and of two.
+// What a block of keys costs, and an item beside its blocks: of light rows, of one tile (a chain of products
+// and softmax) and of two.  Only their ratios count; they were chosen by trying them on calls of each kind and mixed
+// ones.  Clocks in the kernel have a block at 1.1 to 1.45 us (light rows; the more SMs copy at once, the longer), 1.3
+// and 1.6 us, an end at 1.7, 2.3 and about 8 us.  Where both kinds meet (four chunks beside 60 rows) CTAs with light
+// rows are done 13 us after those with tiles, of 150.
 constexpr int BLOCK_LIGHT = 4, BLOCK_ONE = 5, BLOCK_TWO = 6;
 constexpr int END_LIGHT = 4, END_ONE = 8, END_TWO = 16;
 constexpr int SHARE_MIN = 6;  // at least a block's units, so that a share inside an item has a piece of it
@@ -181,7 +192,7 @@ constexpr int JOIN_WILD = 1 << 30;
 // Where the table has the page of a request's last position.  It is -1 where reserve refused the request for want of
 // pages: tables begin as -1, and entries past what a slot holds stay so.  The copies take -1 as any number out
 // of range; such requests are looked for after them, since telling them apart any earlier costs the loops
-// registers (8 requests of 32k 94 us instead of 91, four chunks 167 instead of 160).
+// registers (8 requests of 32k 93 us instead of 91, four chunks 167 instead of 160).
 __device__ __forceinline__ int64_t last_entry(const Args& a, const Request& r) {
   return (int64_t)r.slot * a.width + ((r.past + r.rows - 1) >> a.shift);
 }
@@ -917,7 +928,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int first_pos = ((warp & 3) * 32) / G;  // of the warp's rows, which are in position order
     int ns = 0, no = 0;                           // scores and outputs so far
     bool ok = true;
-    // What the loop over a piece's blocks needs of it, and no more: registers for the whole of it would spill.
+    // What the loop over a piece's blocks needs of it, and no more: registers for the whole of it spill by more still.
     struct View {
       int blocks;        // that the tile sees
       int seen, clear;   // the last column of its first block that the row sees; that all of the warp's live rows see
@@ -1136,7 +1147,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int i = 0; i < u.blocks; ++i, ++ns, u.seen -= BN, u.clear -= BN) {
         ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(s_full + 8 * t, ns & 1, err, a.wait_ns));
         const bool masked = HN - 1 > u.clear, use = ok && u.any_live;
-        // 32 scores, again from tensor memory for the weights: registers for all 64 would spill
+        // 32 scores, again from tensor memory for the weights: there are no registers for all 64
         auto scores = [&](int c, uint32_t (&s)[32]) {
           tmem_ld32<0>(s_addr + c, s);
           tmem_wait_ld();

@@ -540,7 +540,8 @@ Q4_API int q4_paged_append(void* k_pages, void* v_pages, int cache_dtype, const 
  * reports NOMEM: a step's calls need not wait to hear who was refused.  (A slot in two
  * requests, which reserve refuses with INVALID_ARG, is read as the table stands.)
  * Uses the library's scratch: order calls on one stream.  The first call of a
- * head_dim may allocate some (about 62 MB at 128).  Needs sm_103 (UNSUPPORTED). */
+ * head_dim may allocate some (about 62 MB at 128), so it cannot be one that is
+ * captured.  Needs sm_103 (UNSUPPORTED). */
 Q4_API int q4_paged_attention(const void* k_pages, const void* v_pages, const void* q, void* out, int dtype,
                               int64_t pages, int64_t heads, int64_t q_heads, int64_t head_dim, int64_t page_size,
                               const int64_t* q_strides, float scale, const int32_t* table, int64_t slots,
