@@ -102,3 +102,60 @@ def test_a_pool_that_runs_out_step_by_step(q4):
         assert status == (q4.Q4_ERR_NOMEM if refused else q4.Q4_OK)
         seen.add(len(refused))
     assert 0 in seen and len(seen) > 2
+
+
+def test_a_refused_request_beside_a_page_number_out_of_range(q4):
+    page = 16
+    r = Requests(q4, 2, 14, 64, page, torch.bfloat16, 3, 12)
+    assert r.step([0, 1, 2], [4 * page, 3 * page, 4 * page + 3]) == ([], q4.Q4_OK)
+    k, v, q = (_normal(900 + i, (3, h, 64), torch.bfloat16) for i, h in enumerate((2, 2, 14)))
+    dev = (_i32([0, 1, 2, 3]), _i32([0, 1, 2]), _i32([4 * page, 3 * page, 4 * page + 3]))
+    r.tables.free_count.fill_(0)  # requests 0 and 1 want a page
+    slot_map, length = q4.q4_paged_reserve(r.tables, *dev, 3)
+    q4.q4_paged_append(r.cache, k.cuda(), v.cuda(), slot_map)
+    assert length.tolist() == [-1, -1, 4 * page + 4] and q4.q4_device_status() == q4.Q4_ERR_NOMEM
+    r.tables.table[2, 1] = 12
+    out = q4.q4_paged_attention(r.cache, r.tables, q.cuda(), *dev)
+    assert q4.q4_device_status() == q4.Q4_ERR_INVALID_ARG  # the graver of the two
+    assert not out[:2].any()
+    k, v = (torch.cat([x[2], y[2:]]) for x, y in ((r.k, k), (r.v, v)))
+    k[page:2 * page] = 0
+    v[page:2 * page] = 0
+    _check(out[2:].cpu().double().numpy(), q[2:].double().numpy(), k.double().numpy(), v.double().numpy(), 4 * page + 3,
+           64 ** -0.5, torch.bfloat16, "request 2")
+
+
+def test_a_pool_that_runs_out_in_a_graph(q4):
+    """A captured step replayed past the pool's end: who is refused keeps its place and gets zeros until a page is free."""
+    page, d = 16, 64
+    tables = q4.Q4PageTable(2, 4, 3, page)
+    cache = q4.Q4PagedCache(3, 2, d, page)
+    steps = 40
+    k, v, q = (_normal(950 + i, (steps, 2, h, d), torch.bfloat16).cuda() for i, h in enumerate((2, 2, 14)))
+    off, slot, pos = _i32([0, 1, 2]), _i32([0, 1]), _i32([0, 0])
+    now = [torch.empty_like(x[0]) for x in (k, v, q)]
+    q4.q4_paged_attention(cache, tables, now[2], _i32([0, 0, 0]), slot, pos)  # the first call allocates
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        slot_map, length = q4.q4_paged_reserve(tables, off, slot, pos, 2)
+        q4.q4_paged_append(cache, now[0], now[1], slot_map)
+        out = q4.q4_paged_attention(cache, tables, now[2], off, slot, pos)
+        pos.copy_(torch.where(length < 0, pos, length))
+    rows, got = [[], []], []
+    for i in range(steps):
+        for x, y in zip(now, (k, v, q)):
+            x.copy_(y[i])
+        g.replay()
+        torch.cuda.synchronize()
+        got.append(out.clone())
+        for s in range(2):
+            if not (i >= 32 or (s == 1 and i >= 16)):
+                rows[s].append(i)
+        assert pos.tolist() == [len(rows[0]), len(rows[1])]
+        assert q4.q4_device_status() == (q4.Q4_ERR_NOMEM if i >= 16 else q4.Q4_OK)
+    o = torch.stack(got).cpu().double().numpy()
+    kk, vv, qq = (x.cpu().double().numpy() for x in (k, v, q))
+    for s in range(2):
+        n = len(rows[s])
+        _check(o[:n, s], qq[:n, s], kk[:n, s], vv[:n, s], 0, d ** -0.5, torch.bfloat16, "slot %d" % s)
+        assert not o[n:, s].any()
