@@ -99,7 +99,7 @@ struct Seq {
 __device__ __forceinline__ bool load_seq(const Args& a, int s, Seq* q) {
   const int qb = __ldg(a.q_offsets + s), qe = __ldg(a.q_offsets + s + 1);
   const int kb = __ldg(a.k_offsets + s), ke = __ldg(a.k_offsets + s + 1);
-  *q = Seq{qb, qe - qb, kb, ke - kb};
+  *q = Seq{qb, (int)((unsigned)qe - (unsigned)qb), kb, (int)((unsigned)ke - (unsigned)kb)};
   return qb >= 0 && qe >= qb && qe <= a.q_total && kb >= 0 && ke >= kb && ke <= a.k_total;
 }
 
@@ -215,7 +215,7 @@ __device__ void clear_rows(const Args& a, int64_t thread, int64_t threads) {
   clear(a.q_offsets[a.S], a.q_total);
   for (int s = 0; s < a.S; ++s) {
     Seq q;
-    if (!load_seq(a, s, &q)) clear(q.qb, (int64_t)q.qb + q.qlen);
+    if (!load_seq(a, s, &q)) clear(q.qb, __ldg(a.q_offsets + s + 1));  // its count of rows may pass 32 bits
   }
 }
 
